@@ -108,7 +108,8 @@ def _quantize(x, rows, kind):
     m, k = x.shape[-2:]
     x = x.float()
     a = _amax(x, rows)
-    return (x * _spread(F8_MAX[kind] / a, rows, m, k)).to(F8[kind]), a / F8_MAX[kind]
+    factor = a.reciprocal() * F8_MAX[kind]
+    return (x * _spread(factor, rows, m, k)).to(F8[kind]), a * (1 / F8_MAX[kind])
 
 
 def _pitched(q):
@@ -297,9 +298,10 @@ def _codes64(x, rows, kind):
     full[:m, :k] = x
     tile = full.view(mb, rows, -1, 128).permute(0, 2, 1, 3)              # (row block, K block, rows, 128)
     top = torch.maximum(tile.abs().flatten(2).max(2).values, torch.tensor(TINY, device=x.device))
-    q = (tile * (lim / top)[..., None, None]).to(F8[kind]).double()
+    factor = (1 / top) * lim
+    q = (tile * factor[..., None, None]).to(F8[kind]).double()
     q = q.permute(0, 2, 1, 3).reshape(full.shape)[:m, :k]
-    return q, (top / lim).double()
+    return q, (top * (1 / lim)).double()
 
 
 def _scaled64(q, s):
