@@ -232,7 +232,7 @@ def run(state):
     if own:
         import dense_fp16_tensor_gemm_gb300 as gnt
         if c["op"] == "product":
-            return gnt.gemm_nt_block128(s["a"], s["sa"], s["b"], s["sb"], out_dtype=REAL[c["out"]])
+            return gnt.gemm_nt_block128_tensors(s["a"], s["sa"], s["b"], s["sb"], out_dtype=REAL[c["out"]])
         if c["op"] == "quantize":
             return gnt.quantize_block128(s["x"], F8[c["type"]], block_rows=c["rows"], transposed=c["both"])
         if c["op"] == "linear":
