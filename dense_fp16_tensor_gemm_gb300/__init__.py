@@ -59,8 +59,16 @@ class GemmError(RuntimeError):
         super().__init__("libgemm_nt: %s (%s)" % (error_string(status), self.status.name))
 
 
+class Scale128(ctypes.Structure):
+    """gemm_scale128_t: fp32 scales of one operand, one for each 128 elements of
+    K of every row (rows = 1) or of every 128 rows (rows = 128)."""
+    _fields_ = [("data", ctypes.c_void_p), ("rows", ctypes.c_int32), ("row_stride", ctypes.c_int64),
+                ("kb_stride", ctypes.c_int64), ("batch_stride", ctypes.c_int64)]
+
+
 # name -> (restype, argtypes); mirrors include/gemm_nt.h
 _i64, _vp, _u64 = ctypes.c_int64, ctypes.c_void_p, ctypes.c_uint64
+_sp = ctypes.POINTER(Scale128)
 _SIGNATURES = {
     "gemm_nt_f16_f32": (ctypes.c_int, [_vp, _vp, _vp] + [_i64] * 6 + [_vp]),
     "gemm_nt_f16_f32_batched": (ctypes.c_int, [_vp, _vp, _vp] + [_i64] * 10 + [_vp]),
@@ -74,6 +82,13 @@ _SIGNATURES = {
     "gemm_nt_mx": (ctypes.c_int, [_vp] * 5 + [ctypes.c_int, ctypes.c_int] + [_i64] * 10 + [ctypes.c_int, _vp]),
     "gemm_nt_mx_scale_bytes": (_i64, [_i64, _i64]),
     "gemm_nt_mx_pack_scales": (ctypes.c_int, [_vp, _i64, _i64, _vp, _i64, _i64, _i64, _vp]),
+    "gemm_nt_block128": (ctypes.c_int, [_vp, _sp, _vp, _sp, _vp, ctypes.c_int, ctypes.c_int] + [_i64] * 10
+                         + [ctypes.c_int, _vp]),
+    "gemm_nt_block128_quantize": (ctypes.c_int, [_vp, ctypes.c_int, _i64, _i64, _i64, _vp, _i64, _sp, _vp, _i64, _sp,
+                                                 ctypes.c_int, _vp]),
+    "gemm_nt_moe": (ctypes.c_int, [_vp, _i64, _vp, _i64, _vp, _i64, _i64, _sp, _vp, _i64, _i64, _sp, _vp, _i64,
+                                   ctypes.c_int, ctypes.c_int] + [_i64] * 5 + [ctypes.c_int, _vp, _i64, _vp]),
+    "gemm_nt_moe_workspace_bytes": (_i64, [_i64, _i64, _i64]),
     "gemm_nt_select_path": (ctypes.c_int, [_vp, _vp, _vp] + [_i64] * 10),
     "gemm_nt_check": (ctypes.c_int, [_vp]),
     "gemm_nt_error_string": (ctypes.c_char_p, [ctypes.c_int]),
@@ -154,6 +169,30 @@ def gemm_nt_mx_scale_bytes(rows, K):
 
 def gemm_nt_mx_pack_scales(plain, ld, stride, packed, rows, K, batch=1, stream=0):
     _check(load().gemm_nt_mx_pack_scales(plain, ld, stride, packed, rows, K, batch, stream))
+
+
+def gemm_nt_block128(A, SA, B, SB, Out, ab_type, out_type, M, N, K, lda, ldb, ldo, strideA, strideB, strideO, batch,
+                     path=0, stream=0):
+    """8-bit product with an fp32 scale per 128 elements of K; SA / SB are
+    Scale128 (or None when K is 0)."""
+    _check(load().gemm_nt_block128(A, SA, B, SB, Out, int(ab_type), int(out_type), M, N, K, lda, ldb, ldo, strideA,
+                                   strideB, strideO, batch, int(path), stream))
+
+
+def gemm_nt_block128_quantize(X, x_type, rows, cols, ldx, Q, ldq, SQ, QT, ldqt, ST, q_type, stream=0):
+    _check(load().gemm_nt_block128_quantize(X, int(x_type), rows, cols, ldx, Q, ldq, SQ, QT, ldqt, ST, int(q_type),
+                                            stream))
+
+
+def gemm_nt_moe(X, ldx, logits, ldl, W13, ldw13, strideW13, S13, W2, ldw2, strideW2, S2, Out, ldo, x_type, w_type,
+                tokens, experts, topk, hidden, inner, renormalize, workspace, workspace_bytes, stream=0):
+    _check(load().gemm_nt_moe(X, ldx, logits, ldl, W13, ldw13, strideW13, S13, W2, ldw2, strideW2, S2, Out, ldo,
+                              int(x_type), int(w_type), tokens, experts, topk, hidden, inner, int(renormalize),
+                              workspace, workspace_bytes, stream))
+
+
+def gemm_nt_moe_workspace_bytes(tokens, topk, inner):
+    return int(load().gemm_nt_moe_workspace_bytes(tokens, topk, inner))
 
 
 def gemm_nt_f16_f32_batched_no_alloc(A, B, Out, M, N, K, lda, ldb, ldo, strideA, strideB, strideO,
@@ -346,4 +385,190 @@ def gemm_nt_batched(A, B, out=None, path=Path.AUTO, stream=None, out_dtype=None)
     gemm_nt_batched_ex(A.data_ptr(), B.data_ptr(), out.data_ptr(), ab, ot, M, N, K,
                        _matrix_ld(A, "A"), _matrix_ld(B, "B"), _matrix_ld(out, "out"),
                        A.stride(0), B.stride(0), out.stride(0), batch, path, _stream_handle(stream))
+    return out
+
+
+# ---------------------------------------------------------------- one scale per block of 128
+def _type_code(dtype, allowed, what):
+    import torch
+    codes = {torch.float16: DType.F16, torch.bfloat16: DType.BF16, torch.float32: DType.F32,
+             torch.float8_e4m3fn: DType.E4M3, torch.float8_e5m2: DType.E5M2}
+    if dtype not in codes or codes[dtype] not in allowed:
+        raise TypeError("%s must be one of %s" % (what, ", ".join(a.name for a in allowed)))
+    return codes[dtype]
+
+
+def _keep(t, stream):
+    """A temporary that work on `stream` still reads: torch's allocator must not
+    hand its memory to another stream before that work is done."""
+    import torch
+    if stream is not None and t is not None:
+        handle = _stream_handle(stream)
+        if handle != torch.cuda.current_stream().cuda_stream:
+            t.record_stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(handle))
+    return t
+
+
+def _scale128(S, rows, K, name):
+    """A scale tensor (rows or ceil(rows/128), ceil(K/128)), optionally with a
+    leading batch dimension, as the C struct."""
+    import torch
+    if S.dtype != torch.float32:
+        raise TypeError("%s must be float32" % name)
+    kb = (K + 127) // 128
+    if S.dim() not in (2, 3) or S.shape[-1] != kb or S.shape[-2] not in (rows, (rows + 127) // 128):
+        raise ValueError("%s: (%d or %d, %d) scales for %d rows and K = %d"
+                         % (name, rows, (rows + 127) // 128, kb, rows, K))
+    return Scale128(S.data_ptr(), 1 if S.shape[-2] == rows else 128, S.stride(-2), S.stride(-1),
+                    S.stride(0) if S.dim() == 3 and S.shape[0] > 1 else 0)
+
+
+def gemm_nt_block128_tensors(A, SA, B, SB, out=None, path=Path.AUTO, stream=None, out_dtype=None):
+    """Out[i,j] = sum_c SA[i,c] SB[j,c] sum_{k in block c} A[i,k] B[j,k] for torch
+    CUDA tensors, c the blocks of 128 of K: A (M,K) and B (N,K) both
+    float8_e4m3fn or both float8_e5m2; SA and SB float32, one scale a row (M or
+    N, ceil(K/128)) or one for 128 rows (ceil(M/128) or ceil(N/128),
+    ceil(K/128)), any strides.  With a leading batch dimension on all four
+    (stride 0 shares an operand), a batch of products.  ``out``/``out_dtype`` as
+    in :func:`gemm_nt`, float32 by default.
+    """
+    import torch
+    if A.dim() not in (2, 3) or B.dim() != A.dim() or A.shape[-1] != B.shape[-1] or A.shape[:-2] != B.shape[:-2] \
+            or SA.dim() != A.dim() or SB.dim() != A.dim() or SA.shape[:-2] != A.shape[:-2] \
+            or SB.shape[:-2] != A.shape[:-2]:
+        raise ValueError("shapes: A (M,K), B (N,K) and their scales, or the same with a leading batch dimension")
+    if A.dtype != B.dtype:
+        raise TypeError("A and B must have the same type")
+    ab = _type_code(A.dtype, (DType.E4M3, DType.E5M2), "A and B")
+    dt = out.dtype if out is not None else (out_dtype or torch.float32)
+    ot = _type_code(dt, (DType.F32, DType.F16, DType.BF16), "out")
+    M, K = A.shape[-2:]
+    N = B.shape[-2]
+    shape = tuple(A.shape[:-2]) + (M, N)
+    if out is None:
+        out = torch.empty(shape, dtype=dt, device=A.device)
+    if tuple(out.shape) != shape:
+        raise ValueError("out must have shape (M,N), with A's batch dimension")
+    sa, sb = _scale128(SA, M, K, "SA"), _scale128(SB, N, K, "SB")
+    batched = A.dim() == 3
+    gemm_nt_block128(A.data_ptr(), sa, B.data_ptr(), sb, out.data_ptr(), ab, ot, M, N, K, _matrix_ld(A, "A"),
+                     _matrix_ld(B, "B"), _matrix_ld(out, "out"), A.stride(0) if batched else 0,
+                     B.stride(0) if batched else 0, out.stride(0) if batched else 0, A.shape[0] if batched else 1,
+                     path, _stream_handle(stream))
+    return out
+
+
+def quantize_block128(X, q_dtype=None, block_rows=1, transposed=False, stream=None):
+    """8-bit codes and fp32 scales of X (rows, cols; float32, float16 or
+    bfloat16), one scale for each 1 x 128 (``block_rows`` 1) or 128 x 128 (128)
+    block: a = max(max |x|, 2^-100), scale = a / F, code = x * (F / a) rounded to
+    ``q_dtype`` (float8_e4m3fn by default, or float8_e5m2), F its largest value.
+
+    Returns ``(Q, S)``, or with ``transposed`` ``(Q, S, QT, ST)`` from one read
+    of X: QT (cols, rows) is X transposed, quantised in blocks of its own rows.
+    Rows of the codes start on 16-byte boundaries; scales of single rows are
+    stored with the rows adjacent (strides (1, rows)).
+    """
+    import torch
+    if X.dim() != 2:
+        raise ValueError("X must be a matrix")
+    if block_rows not in (1, 128):
+        raise ValueError("block_rows must be 1 or 128")
+    q_dtype = q_dtype or torch.float8_e4m3fn
+    qt_code = _type_code(q_dtype, (DType.E4M3, DType.E5M2), "q_dtype")
+    xt = _type_code(X.dtype, (DType.F32, DType.F16, DType.BF16), "X")
+    ldx = _matrix_ld(X, "X")
+    rows, cols = X.shape
+
+    def outputs(r, c):
+        q = torch.empty((r, (c + 15) // 16 * 16), dtype=torch.uint8, device=X.device).view(q_dtype)[:, :c]
+        kb = (c + 127) // 128
+        if block_rows == 1:
+            s = torch.empty((kb, r), dtype=torch.float32, device=X.device).t()
+        else:
+            s = torch.empty(((r + 127) // 128, kb), dtype=torch.float32, device=X.device)
+        return q, s, max(q.stride(0), 1), Scale128(s.data_ptr(), block_rows, s.stride(0), s.stride(1), 0)
+
+    q, s, ldq, sq = outputs(rows, cols)
+    qt = st = stc = None
+    ldqt = 0
+    if transposed:
+        qt, st, ldqt, stc = outputs(cols, rows)
+    gemm_nt_block128_quantize(X.data_ptr(), xt, rows, cols, ldx, q.data_ptr(), ldq, sq,
+                              qt.data_ptr() if transposed else 0, ldqt, stc, qt_code, _stream_handle(stream))
+    return (q, s, qt, st) if transposed else (q, s)
+
+
+def linear_block128(X, W, SW, stream=None):
+    """Y = X @ W.T in 8 bits: X (tokens, in) float16 or bfloat16 is quantised by
+    rows; W (out, in) float8_e4m3fn with scales SW (ceil(out/128), ceil(in/128)),
+    as ``quantize_block128(weight, block_rows=128)`` leaves it.  Returns Y in X's
+    type and what :func:`linear_block128_backward` needs (X transposed, in 8
+    bits)."""
+    q, s, qt, st = quantize_block128(X, W.dtype, transposed=True, stream=stream)
+    y = gemm_nt_block128_tensors(q, s, W, SW, out_dtype=X.dtype, stream=stream)
+    _keep(q, stream), _keep(s, stream)
+    return y, (qt, st)
+
+
+def linear_block128_backward(dY, saved, WT, SWT, stream=None):
+    """Gradients of :func:`linear_block128`: dX = dY @ W in dY's type and dW =
+    dY.T @ X in float32, both products in 8 bits.  WT (in, out) and SWT are W's
+    codes and scales transposed (the ``transposed`` half of
+    ``quantize_block128(weight, block_rows=128, transposed=True)``)."""
+    qt_x, st_x = saved
+    q, s, qt, st = quantize_block128(dY, WT.dtype, transposed=True, stream=stream)
+    dx = gemm_nt_block128_tensors(q, s, WT, SWT, out_dtype=dY.dtype, stream=stream)
+    dw = gemm_nt_block128_tensors(qt, st, qt_x, st_x, stream=stream)
+    for t in (q, s, qt, st, qt_x, st_x):
+        _keep(t, stream)
+    return dx, dw
+
+
+def moe_few_tokens(X, logits, W13, W2, topk, S13=None, S2=None, renormalize=True, out=None, workspace=None,
+                   stream=None):
+    """A mixture-of-experts layer for up to 128 tokens (see gemm_nt_moe in
+    include/gemm_nt.h): X (tokens, hidden) float16 or bfloat16; ``logits``
+    (tokens, experts) float32, -inf for experts a token may not take; W13
+    (experts, 2*inner, hidden), gate rows first, and W2 (experts, hidden, inner)
+    in X's type, or float8_e4m3fn with float32 scales S13 and S2 (one for each
+    128 elements of a row, or for each 128 x 128 block).  ``renormalize``: the
+    weights of a token's ``topk`` experts are normalised over those alone,
+    otherwise over all of its experts.  ``workspace``, a uint8 tensor of
+    :func:`gemm_nt_moe_workspace_bytes` bytes, is allocated if not given.
+    """
+    import torch
+    if X.dim() != 2 or logits.dim() != 2 or W13.dim() != 3 or W2.dim() != 3:
+        raise ValueError("shapes: X (tokens, hidden), logits (tokens, experts), W13 (experts, 2*inner, hidden), "
+                         "W2 (experts, hidden, inner)")
+    tokens, hidden = X.shape
+    experts, inner = logits.shape[1], W2.shape[2]
+    if logits.shape[0] != tokens or tuple(W13.shape) != (experts, 2 * inner, hidden) or \
+            tuple(W2.shape) != (experts, hidden, inner):
+        raise ValueError("shapes: X (tokens, hidden), logits (tokens, experts), W13 (experts, 2*inner, hidden), "
+                         "W2 (experts, hidden, inner)")
+    xt = _type_code(X.dtype, (DType.F16, DType.BF16), "X")
+    if W13.dtype != W2.dtype:
+        raise TypeError("W13 and W2 must have the same type")
+    wt = _type_code(W13.dtype, (xt, DType.E4M3), "W13 and W2")
+    if logits.dtype != torch.float32:
+        raise TypeError("logits must be float32")
+    if (wt == DType.E4M3) != (S13 is not None) or (S13 is None) != (S2 is None):
+        raise ValueError("8-bit weights take S13 and S2, 16-bit weights none")
+    if out is None:
+        out = torch.empty((tokens, hidden), dtype=X.dtype, device=X.device)
+    if tuple(out.shape) != (tokens, hidden) or out.dtype != X.dtype:
+        raise ValueError("out must have X's shape and type")
+    s13 = s2 = None
+    if S13 is not None:
+        if S13.dim() != 3 or S2.dim() != 3 or S13.shape[0] != experts or S2.shape[0] != experts:
+            raise ValueError("S13 and S2 need a leading expert dimension")
+        s13, s2 = _scale128(S13, 2 * inner, hidden, "S13"), _scale128(S2, hidden, inner, "S2")
+    need = gemm_nt_moe_workspace_bytes(tokens, topk, inner) if topk > 0 else 0
+    if workspace is None:
+        workspace = _keep(torch.empty(max(need, 16), dtype=torch.uint8, device=X.device), stream)
+    gemm_nt_moe(X.data_ptr(), _matrix_ld(X, "X"), logits.data_ptr(), _matrix_ld(logits, "logits"), W13.data_ptr(),
+                _matrix_ld(W13, "W13"), W13.stride(0), s13, W2.data_ptr(), _matrix_ld(W2, "W2"), W2.stride(0), s2,
+                out.data_ptr(), _matrix_ld(out, "out"), xt, wt, tokens, experts, topk, hidden, inner, renormalize,
+                workspace.data_ptr(), workspace.numel(), _stream_handle(stream))
     return out

@@ -20,6 +20,7 @@
 #include <cudaTypedefs.h>
 
 #include "gemm_nt.h"
+#include "block128.h"
 #include "internal.h"
 
 namespace gnt {
@@ -98,6 +99,7 @@ gemm_status_t device_state(DeviceState** out)
                 if (e == cudaSuccess) e = tc05_configure(64, true);
                 if (e == cudaSuccess) e = tc05_small_configure();
                 if (e == cudaSuccess) e = tc05_pair_configure(&max_pairs);
+                if (e == cudaSuccess) e = moe_configure();
                 if (e != cudaSuccess)
                     return GEMM_ERR_LAUNCH;
                 d.status = static_cast<uint32_t*>(sym);
@@ -1044,6 +1046,21 @@ gemm_status_t from_host_pipelined(const void* A_host, const void* B_host, float*
 
 }  // namespace
 
+int device_info(DeviceInfo* out)
+{
+    DeviceState* d = nullptr;
+    const gemm_status_t st = device_state(&d);
+    if (st == GEMM_OK)
+        *out = DeviceInfo{d->num_sms, d->status, wait_limit(), g_fault.load()};
+    return st;
+}
+
+bool operand_map(CUtensorMap* map, const void* base, int64_t rows, int64_t K, int64_t ld, int64_t batch,
+                 int64_t stride, int box_rows, int* bmul, int dtype)
+{
+    return make_map(map, base, rows, K, ld, batch, stride, box_rows, bmul, dtype);
+}
+
 // The CTA-pair kernel with its split scratch taken from memory the caller of
 // this function owns (no allocation): arguments are checked before any CUDA
 // call, then `scratch` gives the current device's fixed scratch, and the work
@@ -1232,7 +1249,7 @@ const char* gemm_nt_error_string(gemm_status_t status)
     case GEMM_ERR_UNSUPPORTED_DEVICE: return "device is not compute capability 10.3 (sm_103a)";
     case GEMM_ERR_NOT_SUPPORTED: return "the requested kernel cannot take these arguments";
     case GEMM_ERR_SCRATCH_TOO_SMALL:
-        return "the call needs more scratch than the no-allocation entry point's fixed array holds";
+        return "the call needs more scratch than the no-allocation entry point's fixed array, or the given workspace, holds";
     }
     return "unknown status";
 }

@@ -1,0 +1,844 @@
+// moe.cu -- a mixture-of-experts layer for a few tokens, in two kernels.
+//
+//   up    h[t,j]  = silu(Wg x_t) * (Wu x_t)        for the experts e_j of token t
+//   down  Out[t]  = sum_j p_j W2[e_j] h[t,j]
+//
+// With few tokens both are bound by reading the chosen experts' weights once
+// (6 * hidden * inner bytes an expert in 16 bits), so the kernels are built
+// around keeping bytes in flight.  Weights go straight to the warps that use
+// them: each warp owns a ring in shared memory, filled with 16-byte cp.async by
+// the very lanes that read it back, so that no barrier stands between a load
+// and its use.  A warp item is 16 (or 32) weight rows by 64 elements of K; the
+// warps of a CTA split K.
+//
+// Products use mma.sync m16n8k8 in tf32, weights on the 16-row side and 8
+// tokens on the other.  Every fp16, bf16 and E4M3 value is a tf32 value, and
+// tf32 has fp32's range, so one path serves all types: x and the weights enter
+// exactly, and h, which stays in fp32, enters as the sum of two tf32 values
+// (22 significant bits; one alone would add the error of an fp16 rounding).  The order of K inside an item is
+// free as long as both operands share it: a lane takes 16 contiguous bytes of
+// a row, and its consecutive elements feed slots t and t + 4 of the MMA.
+//
+// Routing is recomputed by every CTA from the logits, a few thousand
+// instructions; that spares a kernel and a round trip through memory.
+#include "gemm_nt.h"
+#include "block128.h"
+#include "ptx.cuh"
+
+namespace gnt {
+
+namespace {
+
+constexpr int kWarps = 8, kThreads = 32 * kWarps;
+constexpr int kItem = 64;  // elements of K per warp item
+
+// ---------------------------------------------------------------- small PTX
+// 16 bytes global -> shared; bytes past `n` (0..16) of the source are zeros
+// and are not read.  .cg: past L1, for data read once; .ca: through L1.
+__device__ __forceinline__ void cp_async_cg(uint32_t dst, const void* src, int n)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ void cp_async_ca(uint32_t dst, const void* src, int n)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ void mma_tf32(float (&c)[4], float a0, float a1, float a2, float a3, float b0, float b1)
+{
+    asm volatile(
+        "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(__float_as_uint(a0)), "r"(__float_as_uint(a1)), "r"(__float_as_uint(a2)), "r"(__float_as_uint(a3)),
+          "r"(__float_as_uint(b0)), "r"(__float_as_uint(b1)));
+}
+
+// The tf32 value that is left of v when its low 13 bits are dropped.
+__device__ __forceinline__ float tf32_head(float v) { return __uint_as_float(__float_as_uint(v) & 0xffffe000u); }
+
+__device__ __forceinline__ float ld_cluster(uint32_t addr)
+{
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
+}
+
+// v - head, exact; nothing for an infinity, which its head holds whole.
+__device__ __forceinline__ float tf32_rest(float v, float head) { return fabsf(v) < INFINITY ? v - head : 0.f; }
+
+template <bool BF16>
+__device__ __forceinline__ void widen2(uint32_t w, float& a, float& b)
+{
+    if constexpr (BF16) {
+        a = __uint_as_float(w << 16);
+        b = __uint_as_float(w & 0xffff0000u);
+    } else {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
+        a = f.x, b = f.y;
+    }
+}
+
+// Two E4M3 bytes -> two floats.
+__device__ __forceinline__ void widen2_e4m3(uint32_t w, float& a, float& b)
+{
+    uint32_t h;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(w)));
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+    a = f.x, b = f.y;
+}
+
+// ---------------------------------------------------------------- routing
+// Per CTA, in shared memory.  A slot is token * topk + j.
+struct Route {
+    uint32_t* mask;    // [experts][words]: bit t of an expert's mask: token t takes it
+    float* p;          // [slots]
+    uint16_t* chosen;  // [slots] expert, 0xffff: none
+    uint16_t* list;    // [slots] slots by expert, then token
+    uint16_t* off;     // [experts] start of each expert's part of list
+    uint16_t* act;     // [active + 1] experts with tokens, ascending
+    uint16_t* aoff;    // [active + 1] their starts in list; the last entry closes it
+    uint8_t* bad;      // [tokens] the token's logits hold a NaN
+    int* nact;
+};
+
+__host__ __device__ inline int route_bytes(int tokens, int experts, int topk)
+{
+    const int words = (tokens + 31) / 32, slots = tokens * topk, act = experts < slots ? experts : slots;
+    const int b = 4 * (experts * words + slots + 1) + 2 * (2 * slots + experts + 2 * (act + 1)) + tokens;
+    return (b + 15) / 16 * 16;
+}
+
+__device__ __forceinline__ Route route_carve(uint8_t* s, const MoeParams& p)
+{
+    const int words = (p.tokens + 31) / 32, slots = p.tokens * p.topk;
+    const int act = p.experts < slots ? p.experts : slots;
+    Route r;
+    r.mask = reinterpret_cast<uint32_t*>(s);
+    r.p = reinterpret_cast<float*>(r.mask + p.experts * words);
+    r.nact = reinterpret_cast<int*>(r.p + slots);
+    r.chosen = reinterpret_cast<uint16_t*>(r.nact + 1);
+    r.list = r.chosen + slots;
+    r.off = r.list + slots;
+    r.act = r.off + p.experts;
+    r.aoff = r.act + act + 1;
+    r.bad = reinterpret_cast<uint8_t*>(r.aoff + act + 1);
+    return r;
+}
+
+// Unsigned keys in the order of the floats; 0 marks what cannot be taken (NaN,
+// or taken already), and a -inf is below kAbove.
+constexpr uint32_t kAbove = 0x00800000u;
+__device__ __forceinline__ uint32_t order_key(float v)
+{
+    const uint32_t u = __float_as_uint(v);
+    return v != v ? 0u : (u & 0x80000000u ? ~u : u | 0x80000000u);
+}
+__device__ __forceinline__ float key_value(uint32_t k)
+{
+    return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
+}
+
+// One warp, one token: topk rounds of a warp-wide maximum over keys held in
+// registers (VPL experts a lane), the lowest index among equals; lane j keeps
+// round j's result.
+template <int VPL>
+__device__ __forceinline__ void route_token(const MoeParams& p, const Route& r, int t, int lane)
+{
+    const float* l = p.logits + t * p.ldl;
+    const int words = (p.tokens + 31) / 32;
+    uint32_t key[VPL];
+    bool nan = false;  // + 0 below makes -0 and 0 the tie they are
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+        const int e = lane + 32 * i;
+        const float v = e < p.experts ? __fadd_rn(l[e], 0.f) : -INFINITY;
+        nan |= v != v;
+        key[i] = order_key(v);
+    }
+    nan = __any_sync(0xffffffffu, nan);
+    float all = 0.f;  // sum of exponentials over every expert (softmax before the choice)
+    uint32_t top = 0, mine = 0;
+    int at = -1;
+    for (int j = 0; j < p.topk; ++j) {
+        uint32_t best = 0;
+        int idx = 0;
+#pragma unroll
+        for (int i = 0; i < VPL; ++i)
+            if (key[i] > best) {
+                best = key[i];
+                idx = lane + 32 * i;
+            }
+        const uint32_t m = __reduce_max_sync(0xffffffffu, best);
+        if (m < kAbove)
+            break;
+        const int e = static_cast<int>(__reduce_min_sync(0xffffffffu, best == m ? static_cast<uint32_t>(idx) : ~0u));
+        if (j == 0) {
+            top = m;
+            if (!p.renorm) {
+#pragma unroll
+                for (int i = 0; i < VPL; ++i)
+                    if (key[i] >= kAbove)
+                        all += expf(key_value(key[i]) - key_value(m));
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < VPL; ++i)
+            if (e == lane + 32 * i)
+                key[i] = 0;
+        if (lane == j) {
+            mine = m;
+            at = e;
+        }
+    }
+    const float ev = at >= 0 ? expf(key_value(mine) - key_value(top)) : 0.f;
+    float sum = p.renorm ? ev : all;
+#pragma unroll
+    for (int s = 16; s > 0; s >>= 1)
+        sum += __shfl_xor_sync(0xffffffffu, sum, s);
+    if (lane < p.topk) {
+        r.chosen[t * p.topk + lane] = at >= 0 ? static_cast<uint16_t>(at) : uint16_t(0xffff);
+        r.p[t * p.topk + lane] = nan ? NAN : ev / sum;
+        if (at >= 0)
+            atomicOr(&r.mask[at * words + t / 32], 1u << (t & 31));
+    }
+    if (lane == 0)
+        r.bad[t] = nan;
+}
+
+__device__ __forceinline__ void route_all(const MoeParams& p, const Route& r)
+{
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int words = (p.tokens + 31) / 32, slots = p.tokens * p.topk;
+    for (int i = threadIdx.x; i < p.experts * words; i += kThreads)
+        r.mask[i] = 0;
+    __syncthreads();
+    for (int t = warp; t < p.tokens; t += kWarps) {
+        if (p.experts <= 64)
+            route_token<2>(p, r, t, lane);
+        else if (p.experts <= 256)
+            route_token<8>(p, r, t, lane);
+        else
+            route_token<32>(p, r, t, lane);
+    }
+    __syncthreads();
+    if (warp == 0) {
+        int total = 0, nact = 0;
+        for (int e0 = 0; e0 < p.experts; e0 += 32) {
+            const int e = e0 + lane;
+            int n = 0;
+            if (e < p.experts)
+                for (int w = 0; w < words; ++w)
+                    n += __popc(r.mask[e * words + w]);
+            int incl = n;
+#pragma unroll
+            for (int s = 1; s < 32; s *= 2) {
+                const int v = __shfl_up_sync(0xffffffffu, incl, s);
+                if (lane >= s)
+                    incl += v;
+            }
+            const uint32_t has = __ballot_sync(0xffffffffu, n > 0);
+            if (e < p.experts)
+                r.off[e] = static_cast<uint16_t>(total + incl - n);
+            if (n > 0) {
+                const int a = nact + __popc(has & ((1u << lane) - 1));
+                r.act[a] = static_cast<uint16_t>(e);
+                r.aoff[a] = static_cast<uint16_t>(total + incl - n);
+            }
+            nact += __popc(has);
+            total += __shfl_sync(0xffffffffu, incl, 31);
+        }
+        if (lane == 0) {
+            r.aoff[nact] = static_cast<uint16_t>(total);
+            *r.nact = nact;
+        }
+    }
+    __syncthreads();
+    for (int s = threadIdx.x; s < slots; s += kThreads) {
+        const int e = r.chosen[s], t = s / p.topk;
+        if (e != 0xffff) {
+            int pos = r.off[e] + __popc(r.mask[e * words + t / 32] & ((1u << (t & 31)) - 1));
+            for (int w = 0; w < t / 32; ++w)
+                pos += __popc(r.mask[e * words + w]);
+            r.list[pos] = static_cast<uint16_t>(s);
+        }
+    }
+    __syncthreads();
+}
+
+// ---------------------------------------------------------------- items
+// Shared-memory layout of one ring stage, in 512-byte lines (32 lanes x 16
+// bytes): first the weights, then the tokens' side.  A lane holds 16 elements
+// of K per row: two chunks of 8 (16-bit weights: k = 32*half + 8*t, t = lane %
+// 4), or one of 16 (8-bit: k = 16*t).
+template <bool W8, int MT, int NT, int BSIZE>
+struct Stage {
+    static constexpr int W_LINES = MT * 2 * (W8 ? 1 : 2);  // [mt][row half][chunk]
+    static constexpr int B_PER_TOKEN = BSIZE == 2 ? 2 : 4;  // 16 elements of 2 or 4 bytes
+    static constexpr int LINES = W_LINES + NT * B_PER_TOKEN;
+    static constexpr int BYTES = LINES * 512;
+};
+
+// First of the 8 elements of K that a lane's half `hf` covers within an item.
+template <bool W8>
+__device__ __forceinline__ int half_k(int t, int hf)
+{
+    return W8 ? 16 * t + 8 * hf : 32 * hf + 8 * t;
+}
+
+__device__ __forceinline__ int clamp16(int bytes) { return bytes < 0 ? 0 : (bytes > 16 ? 16 : bytes); }
+
+// A 16-byte chunk of a row that starts anywhere: byte by byte, zeros past n.
+__device__ __forceinline__ void copy_bytes(uint32_t dst, const uint8_t* src, int n)
+{
+    uint32_t w[4] = {0, 0, 0, 0};
+    for (int i = 0; i < n; ++i)
+        w[i >> 2] |= static_cast<uint32_t>(src[i]) << (8 * (i & 3));
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
+                 : "memory");
+}
+
+// One lane's weight chunks of one row for the item at k0: `row` points at the
+// row, or is null (zeros) for rows outside the matrix; `any` is a readable
+// address for those.
+template <bool W8>
+__device__ __forceinline__ void load_row(uint32_t dst, const uint8_t* row, const void* any, int k0, int K, int t, bool vec)
+{
+    constexpr int ES = W8 ? 1 : 2;
+#pragma unroll
+    for (int c = 0; c < (W8 ? 1 : 2); ++c) {
+        const int k = k0 + half_k<W8>(t, c);
+        const int n = row ? clamp16((K - k) * ES) : 0;
+        const uint8_t* src = n > 0 ? row + static_cast<int64_t>(k) * ES : static_cast<const uint8_t*>(any);
+        if (vec)
+            cp_async_cg(dst + c * 512, src, n);
+        else
+            copy_bytes(dst + c * 512, src, n);
+    }
+}
+
+// One lane's chunks of a token's row (BSIZE bytes an element).
+template <bool W8, int BSIZE>
+__device__ __forceinline__ void load_token(uint32_t dst, const uint8_t* row, const void* any, int k0, int K, int t,
+                                           bool vec)
+{
+#pragma unroll
+    for (int c = 0; c < 16 * BSIZE / 16; ++c) {  // 8 (BSIZE 2) or 4 (BSIZE 4) elements each
+        const int k = k0 + (BSIZE == 2 ? half_k<W8>(t, c) : half_k<W8>(t, c >> 1) + 4 * (c & 1));
+        const int n = row ? clamp16((K - k) * BSIZE) : 0;
+        const uint8_t* src = n > 0 ? row + static_cast<int64_t>(k) * BSIZE : static_cast<const uint8_t*>(any);
+        if (vec)
+            cp_async_ca(dst + c * 512, src, n);
+        else
+            copy_bytes(dst + c * 512, src, n);
+    }
+}
+
+__device__ __forceinline__ uint4 lds16(uint32_t a)
+{
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+    return v;
+}
+
+// 8 weights of a lane's half from the stage.
+template <bool BF16, bool W8>
+__device__ __forceinline__ void weights8(uint32_t line, int hf, float (&v)[8])
+{
+    if constexpr (W8) {
+        uint32_t a, b;
+        asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(a), "=r"(b) : "r"(line + 8 * hf) : "memory");
+        widen2_e4m3(a, v[0], v[1]);
+        widen2_e4m3(a >> 16, v[2], v[3]);
+        widen2_e4m3(b, v[4], v[5]);
+        widen2_e4m3(b >> 16, v[6], v[7]);
+    } else {
+        const uint4 w = lds16(line + 512 * hf);
+        widen2<BF16>(w.x, v[0], v[1]);
+        widen2<BF16>(w.y, v[2], v[3]);
+        widen2<BF16>(w.z, v[4], v[5]);
+        widen2<BF16>(w.w, v[6], v[7]);
+    }
+}
+
+template <bool BF16, int BSIZE>
+__device__ __forceinline__ void tokens8(uint32_t line, int hf, float (&v)[8])
+{
+    if constexpr (BSIZE == 2) {
+        const uint4 w = lds16(line + 512 * hf);
+        widen2<BF16>(w.x, v[0], v[1]);
+        widen2<BF16>(w.y, v[2], v[3]);
+        widen2<BF16>(w.z, v[4], v[5]);
+        widen2<BF16>(w.w, v[6], v[7]);
+    } else {
+        const uint4 a = lds16(line + 1024 * hf), b = lds16(line + 1024 * hf + 512);
+        v[0] = __uint_as_float(a.x), v[1] = __uint_as_float(a.y), v[2] = __uint_as_float(a.z), v[3] = __uint_as_float(a.w);
+        v[4] = __uint_as_float(b.x), v[5] = __uint_as_float(b.y), v[6] = __uint_as_float(b.z), v[7] = __uint_as_float(b.w);
+    }
+}
+
+// Multiplies one landed item into c: stage address `st` is the lane's own (line
+// + 16 * lane), nt token tiles of 8 are in use.
+template <bool BF16, bool W8, int MT, int NT, int BSIZE>
+__device__ __forceinline__ void multiply_item(uint32_t st, int nt, float (&c)[MT][NT][4])
+{
+    using S = Stage<W8, MT, NT, BSIZE>;
+    constexpr int PER_ROW = W8 ? 1 : 2;
+#pragma unroll
+    for (int hf = 0; hf < 2; ++hf) {
+        float lo[MT][8], hi[MT][8];
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+            weights8<BF16, W8>(st + (m * 2 * PER_ROW) * 512, hf, lo[m]);
+            weights8<BF16, W8>(st + (m * 2 * PER_ROW + PER_ROW) * 512, hf, hi[m]);
+        }
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            if (n < nt) {
+                float b[8];
+                tokens8<BF16, BSIZE>(st + (S::W_LINES + n * S::B_PER_TOKEN) * 512, hf, b);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float b0 = BSIZE == 4 ? tf32_head(b[2 * j]) : b[2 * j];
+                    const float b1 = BSIZE == 4 ? tf32_head(b[2 * j + 1]) : b[2 * j + 1];
+#pragma unroll
+                    for (int m = 0; m < MT; ++m) {
+                        mma_tf32(c[m][n], lo[m][2 * j], hi[m][2 * j], lo[m][2 * j + 1], hi[m][2 * j + 1], b0, b1);
+                        if (BSIZE == 4)  // fp32 tokens: what their heads leave
+                            mma_tf32(c[m][n], lo[m][2 * j], hi[m][2 * j], lo[m][2 * j + 1], hi[m][2 * j + 1],
+                                     tf32_rest(b[2 * j], b0), tf32_rest(b[2 * j + 1], b1));
+                    }
+                }
+            }
+        }
+    }
+}
+
+__device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; }
+
+// ---------------------------------------------------------------- up
+// A unit is 8 gate rows and the 8 up rows that go with them (one m16 tile: the
+// MMA's lower accumulator rows are the gates, the upper ones their ups), over
+// all of K, for up to 8*NT of the expert's tokens at a time.  CTAs take even
+// ranges of the units of all active experts; the 8 warps split K and meet once
+// per unit in shared memory.
+template <bool W8, int NT>
+struct UpCfg {
+    using S = Stage<W8, 1, NT, 2>;
+    // ring stages, and buffers for the warps' sums: what lets two CTAs share an SM
+    static constexpr int D = NT == 1 || W8 ? 4 : 3;
+    static constexpr int RBUF = NT == 1 ? 2 : 1;
+    static constexpr int RING = kWarps * D * S::BYTES;
+    static constexpr int FIXED = RING + RBUF * kWarps * NT * 4 * 32 * 4;
+};
+
+template <bool BF16, bool W8, int NT>
+__global__ void __launch_bounds__(kThreads, 2) moe_up_kernel(const MoeParams p)
+{
+    using C = UpCfg<W8, NT>;
+    using S = typename C::S;
+    constexpr int D = C::D;
+    extern __shared__ __align__(16) uint8_t smem[];
+    float* red = reinterpret_cast<float*>(smem + C::RING);
+    const Route r = route_carve(smem + C::FIXED, p);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+
+    pdl_wait();
+    // After the wait: the down kernel may start early and read the logits, which
+    // are then complete.
+    pdl_launch_dependents();
+    route_all(p, r);
+
+    const int tiles = ceil_div(p.inner, 8), nit = ceil_div(p.hidden, kItem);
+    const int64_t units = static_cast<int64_t>(*r.nact) * tiles;
+    const int u0 = static_cast<int>(units * blockIdx.x / gridDim.x);
+    const int u1 = static_cast<int>(units * (blockIdx.x + 1) / gridDim.x);
+    const int ks0 = nit * warp / kWarps, ks1 = nit * (warp + 1) / kWarps;
+    const uint32_t ring = smem_u32(smem) + warp * D * S::BYTES + lane * 16;
+    constexpr int ES = W8 ? 1 : 2;
+    const uint8_t* xb = static_cast<const uint8_t*>(p.x);
+    const uint8_t* wb = static_cast<const uint8_t*>(p.w13);
+
+    // Loader: the items (unit, token group, K item) of this warp in order.
+    int lu = u0, lg = 0, lk = ks0, lslot = 0;
+    bool fresh = true;
+    const uint8_t *wg = nullptr, *wu = nullptr;
+    const uint8_t* xr[NT];
+    int lgroups = 0;
+    auto load_next = [&] {
+        if (ks0 < ks1 && lu < u1) {
+            if (fresh) {
+                const int a = lu / tiles, i = (lu - a * tiles) * 8 + g;
+                const int n = r.aoff[a + 1] - r.aoff[a];
+                lgroups = ceil_div(n, 8 * NT);
+                const uint8_t* we = wb + static_cast<int64_t>(r.act[a]) * p.stride_w13 * ES;
+                wg = i < p.inner ? we + static_cast<int64_t>(i) * p.ldw13 * ES : nullptr;
+                wu = i < p.inner ? we + static_cast<int64_t>(p.inner + i) * p.ldw13 * ES : nullptr;
+#pragma unroll
+                for (int q = 0; q < NT; ++q) {
+                    const int j = lg * 8 * NT + q * 8 + g;
+                    xr[q] = j < n ? xb + static_cast<int64_t>(r.list[r.aoff[a] + j] / p.topk) * p.ldx * 2 : nullptr;
+                }
+                fresh = false;
+            }
+            const uint32_t st = ring + lslot * S::BYTES;
+            load_row<W8>(st, wg, wb, lk * kItem, p.hidden, t, p.vec_13);
+            load_row<W8>(st + (W8 ? 1 : 2) * 512, wu, wb, lk * kItem, p.hidden, t, p.vec_13);
+#pragma unroll
+            for (int q = 0; q < NT; ++q)
+                load_token<W8, 2>(st + (S::W_LINES + q * S::B_PER_TOKEN) * 512, xr[q], xb, lk * kItem, p.hidden, t,
+                                  p.vec_x);
+            if (++lk == ks1) {
+                lk = ks0;
+                fresh = true;
+                if (++lg == lgroups) {
+                    lg = 0;
+                    ++lu;
+                }
+            }
+        }
+        cp_async_commit();
+        lslot = lslot + 1 == D ? 0 : lslot + 1;
+    };
+#pragma unroll 1
+    for (int i = 0; i < D - 1; ++i)
+        load_next();
+
+    int slot = 0, parity = 0;
+#pragma unroll 1
+    for (int u = u0; u < u1; ++u) {
+        const int a = u / tiles, i0 = (u - a * tiles) * 8;
+        const int first = r.aoff[a], n = r.aoff[a + 1] - first, e = r.act[a];
+#pragma unroll 1
+        for (int g0 = 0; g0 < n; g0 += 8 * NT) {
+            const int nt = min(NT, ceil_div(n - g0, 8));
+            float c[1][NT][4] = {};
+#pragma unroll 1
+            for (int k = ks0; k < ks1; ++k) {
+                float sg = 0.f, su = 0.f;
+                if (W8) {
+                    const int i = min(i0 + g, p.inner - 1), kb = k * kItem / 128;
+                    sg = scale_at(p.s13, e, i, kb);
+                    su = scale_at(p.s13, e, p.inner + i, kb);
+                }
+                cp_async_wait<D - 2>();
+                if constexpr (W8) {
+                    float part[1][NT][4] = {};
+                    multiply_item<BF16, W8, 1, NT, 2>(ring + slot * S::BYTES, nt, part);
+#pragma unroll
+                    for (int q = 0; q < NT; ++q) {
+                        c[0][q][0] = fmaf(part[0][q][0], sg, c[0][q][0]);
+                        c[0][q][1] = fmaf(part[0][q][1], sg, c[0][q][1]);
+                        c[0][q][2] = fmaf(part[0][q][2], su, c[0][q][2]);
+                        c[0][q][3] = fmaf(part[0][q][3], su, c[0][q][3]);
+                    }
+                } else {
+                    multiply_item<BF16, W8, 1, NT, 2>(ring + slot * S::BYTES, nt, c);
+                }
+                slot = slot + 1 == D ? 0 : slot + 1;
+                load_next();
+            }
+            float* rd = red + parity * (kWarps * NT * 4 * 32);
+            if (C::RBUF == 2)
+                parity ^= 1;  // the other buffer is rewritten only after the next unit's barrier
+            else
+                __syncthreads();
+#pragma unroll
+            for (int q = 0; q < NT; ++q)
+#pragma unroll
+                for (int v = 0; v < 4; ++v)
+                    rd[((warp * NT + q) * 4 + v) * 32 + lane] = c[0][q][v];
+            __syncthreads();
+            for (int idx = threadIdx.x; idx < nt * 64; idx += kThreads) {
+                const int l = idx & 31, wh = (idx >> 5) & 1, q = idx >> 6;
+                float gate = 0.f, up = 0.f;
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w) {
+                    gate += rd[((w * NT + q) * 4 + wh) * 32 + l];
+                    up += rd[((w * NT + q) * 4 + 2 + wh) * 32 + l];
+                }
+                const int i = i0 + (l >> 2), j = g0 + q * 8 + 2 * (l & 3) + wh;
+                if (i < p.inner && j < n)
+                    p.h[r.list[first + j] * p.ldh + i] = gate / (1.f + expf(-gate)) * up;
+            }
+        }
+    }
+    cp_async_wait<0>();
+}
+
+// ---------------------------------------------------------------- down
+// A cluster of C CTAs owns 16*MT rows of Out; its 8*C warps take even ranges of
+// the items (active expert, K item).  A warp adds each expert's share, times
+// the tokens' weights, to sums of its own in shared memory, so that nothing
+// synchronises until the end, when the warps' and then the CTAs' sums are added
+// in a fixed order.
+template <bool W8, int NT, int MT>
+struct DownCfg {
+    using S = Stage<W8, MT, NT, 4>;
+    // ring stages: NT == 1 lets two CTAs share an SM; else the sums leave this much
+    static constexpr int D = NT == 1 ? (W8 ? 4 : 3) : (MT == 2 && W8 ? 3 : 2);
+    static constexpr int RING = kWarps * D * S::BYTES;
+};
+
+__host__ __device__ inline int down_sum_bytes(int tokens, int mt) { return kWarps * tokens * 16 * mt * 4; }
+
+template <bool BF16, bool W8, int NT, int MT>
+__global__ void __launch_bounds__(kThreads, MT == 1 && NT == 1 ? 2 : 1) moe_down_kernel(const MoeParams p, int cluster)
+{
+    using C = DownCfg<W8, NT, MT>;
+    using S = typename C::S;
+    constexpr int D = C::D, ROWS = 16 * MT;
+    extern __shared__ __align__(16) uint8_t smem[];
+    float* sums = reinterpret_cast<float*>(smem + C::RING);  // [warp][token][row]
+    const Route r = route_carve(smem + C::RING + down_sum_bytes(p.tokens, MT), p);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const int rank = static_cast<int>(blockIdx.x % cluster);
+    const int r0 = static_cast<int>(blockIdx.x / cluster) * ROWS;
+
+    const int nout = p.tokens * ROWS;
+    for (int i = threadIdx.x; i < kWarps * nout; i += kThreads)
+        sums[i] = 0.f;
+    route_all(p, r);  // the logits were complete before the up kernel let this one start
+    pdl_wait();       // h
+
+    const int nit = ceil_div(p.inner, kItem);
+    const int64_t items = static_cast<int64_t>(*r.nact) * nit;
+    const int part = rank * kWarps + warp, parts = cluster * kWarps;
+    const int q0 = static_cast<int>(items * part / parts), q1 = static_cast<int>(items * (part + 1) / parts);
+    const uint32_t ring = smem_u32(smem) + warp * D * S::BYTES + lane * 16;
+    constexpr int ES = W8 ? 1 : 2;
+    const uint8_t* wb = static_cast<const uint8_t*>(p.w2);
+    const uint8_t* hb = reinterpret_cast<const uint8_t*>(p.h);
+
+    // Loader: per expert of the range, per token group, its K items.
+    int lq = q0, lg = 0, lk = 0, lend = 0, lslot = 0, lgroups = 0;
+    bool fresh = true;
+    const uint8_t* wr[2 * MT];
+    const uint8_t* hr[NT];
+    auto load_next = [&] {
+        if (lq < q1) {
+            if (fresh) {
+                const int a = lq / nit, n = r.aoff[a + 1] - r.aoff[a];
+                lk = lq - a * nit;
+                lend = min(nit, lk + q1 - lq);
+                lgroups = ceil_div(n, 8 * NT);
+                const uint8_t* we = wb + static_cast<int64_t>(r.act[a]) * p.stride_w2 * ES;
+#pragma unroll
+                for (int m = 0; m < 2 * MT; ++m) {
+                    const int row = r0 + 8 * m + g;
+                    wr[m] = row < p.hidden ? we + static_cast<int64_t>(row) * p.ldw2 * ES : nullptr;
+                }
+#pragma unroll
+                for (int q = 0; q < NT; ++q) {
+                    const int j = lg * 8 * NT + q * 8 + g;
+                    hr[q] = j < n ? hb + static_cast<int64_t>(r.list[r.aoff[a] + j]) * p.ldh * 4 : nullptr;
+                }
+                fresh = false;
+            }
+            const uint32_t st = ring + lslot * S::BYTES;
+#pragma unroll
+            for (int m = 0; m < 2 * MT; ++m)
+                load_row<W8>(st + m * (W8 ? 1 : 2) * 512, wr[m], wb, lk * kItem, p.inner, t, p.vec_2);
+#pragma unroll
+            for (int q = 0; q < NT; ++q)
+                load_token<W8, 4>(st + (S::W_LINES + q * S::B_PER_TOKEN) * 512, hr[q], hb, lk * kItem, p.inner, t, true);
+            if (++lk == lend) {
+                fresh = true;
+                if (++lg == lgroups) {
+                    lg = 0;
+                    lq += lend - lq % nit;
+                }
+            }
+        }
+        cp_async_commit();
+        lslot = lslot + 1 == D ? 0 : lslot + 1;
+    };
+#pragma unroll 1
+    for (int i = 0; i < D - 1; ++i)
+        load_next();
+
+    float* mine = sums + warp * nout;
+    int slot = 0;
+#pragma unroll 1
+    for (int q = q0; q < q1;) {
+        const int a = q / nit, k0 = q - a * nit, k1 = min(nit, k0 + q1 - q);
+        const int first = r.aoff[a], n = r.aoff[a + 1] - first, e = r.act[a];
+#pragma unroll 1
+        for (int g0 = 0; g0 < n; g0 += 8 * NT) {
+            const int nt = min(NT, ceil_div(n - g0, 8));
+            float c[MT][NT][4] = {};
+#pragma unroll 1
+            for (int k = k0; k < k1; ++k) {
+                float s[2 * MT];
+                if (W8) {
+#pragma unroll
+                    for (int m = 0; m < 2 * MT; ++m)
+                        s[m] = scale_at(p.s2, e, min(r0 + 8 * m + g, p.hidden - 1), k * kItem / 128);
+                }
+                cp_async_wait<D - 2>();
+                if constexpr (W8) {
+                    float part8[MT][NT][4] = {};
+                    multiply_item<BF16, W8, MT, NT, 4>(ring + slot * S::BYTES, nt, part8);
+#pragma unroll
+                    for (int m = 0; m < MT; ++m)
+#pragma unroll
+                        for (int w = 0; w < NT; ++w)
+#pragma unroll
+                            for (int v = 0; v < 4; ++v)
+                                c[m][w][v] = fmaf(part8[m][w][v], s[2 * m + (v >> 1)], c[m][w][v]);
+                } else {
+                    multiply_item<BF16, W8, MT, NT, 4>(ring + slot * S::BYTES, nt, c);
+                }
+                slot = slot + 1 == D ? 0 : slot + 1;
+                load_next();
+            }
+#pragma unroll
+            for (int w = 0; w < NT; ++w)
+#pragma unroll
+                for (int v = 0; v < 2; ++v) {
+                    const int j = g0 + w * 8 + 2 * t + v;
+                    if (w < nt && j < n) {
+                        const int sl = r.list[first + j];
+                        const float pw = r.p[sl];
+                        float* d = mine + (sl / p.topk) * ROWS + g;
+#pragma unroll
+                        for (int m = 0; m < MT; ++m) {
+                            d[16 * m] = fmaf(pw, c[m][w][v], d[16 * m]);
+                            d[16 * m + 8] = fmaf(pw, c[m][w][2 + v], d[16 * m + 8]);
+                        }
+                    }
+                }
+            __syncwarp();
+        }
+        q += k1 - k0;
+    }
+    cp_async_wait<0>();
+    __syncthreads();
+    for (int i = threadIdx.x; i < nout; i += kThreads) {
+        float s = sums[i];
+#pragma unroll
+        for (int w = 1; w < kWarps; ++w)
+            s += sums[w * nout + i];
+        sums[i] = s;
+    }
+    cluster_sync();
+    const int o0 = static_cast<int>(static_cast<int64_t>(nout) * rank / cluster);
+    const int o1 = static_cast<int>(static_cast<int64_t>(nout) * (rank + 1) / cluster);
+    const uint32_t base = smem_u32(sums);
+    for (int i = o0 + threadIdx.x; i < o1; i += kThreads) {
+        float s = 0.f;
+        for (int q = 0; q < cluster; ++q)
+            s += ld_cluster(mapa_shared(base + 4 * i, q));
+        const int tok = i / ROWS, row = r0 + i % ROWS;
+        if (r.bad[tok])
+            s = NAN;
+        if (row < p.hidden) {
+            using O = OutStore<BF16 ? kOutBF16 : kOutF16>;
+            O::st1(static_cast<typename O::T*>(p.out) + tok * p.ldo + row, s);
+        }
+    }
+    cluster_sync();  // no CTA leaves while another may still read its sums
+}
+
+// ---------------------------------------------------------------- host
+constexpr int kMaxSmem = 232448;
+
+template <bool BF16, bool W8, int NT, int MT>
+cudaError_t configure_one()
+{
+    cudaError_t e = cudaFuncSetAttribute(moe_up_kernel<BF16, W8, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(moe_down_kernel<BF16, W8, NT, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
+    return e;
+}
+
+template <bool BF16, bool W8, int NT, int MT>
+cudaError_t launch_one(const MoeParams& p, int num_sms, cudaStream_t stream)
+{
+    const int rb = route_bytes(p.tokens, p.experts, p.topk);
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    const int64_t reach = p.experts < p.tokens * p.topk ? p.experts : p.tokens * p.topk;  // most experts in use
+    {
+        cudaLaunchConfig_t cfg = {};
+        const int64_t units = reach * ((p.inner + 7) / 8);
+        cfg.gridDim = dim3(static_cast<unsigned>(units < 2 * num_sms ? units : 2 * num_sms));
+        cfg.blockDim = dim3(kThreads);
+        cfg.dynamicSmemBytes = UpCfg<W8, NT>::FIXED + rb;
+        cfg.stream = stream;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        const cudaError_t e = cudaLaunchKernelEx(&cfg, moe_up_kernel<BF16, W8, NT>, p);
+        if (e != cudaSuccess)
+            return e;
+    }
+    // Clusters large enough for two CTAs (one, where a CTA takes most of an
+    // SM's shared memory) on every SM, as long as each warp keeps a few items.
+    const int tiles = (p.hidden + 16 * MT - 1) / (16 * MT);
+    const int64_t items = reach * ((p.inner + kItem - 1) / kItem);
+    const int want = num_sms * (MT == 1 && NT == 1 ? 2 : 1);
+    int c = 1;
+    while (c < 8 && tiles * c < want && items >= 2 * 2 * c * kWarps)
+        c *= 2;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(tiles * c));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = DownCfg<W8, NT, MT>::RING + down_sum_bytes(p.tokens, MT) + rb;
+    cfg.stream = stream;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = static_cast<unsigned>(c);
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, moe_down_kernel<BF16, W8, NT, MT>, p, c);
+}
+
+// Up to 8 tokens: one token tile, 16 rows a warp.  More: two token tiles, and 32
+// rows a warp in the down kernel, which halves how often h is read from L2, while
+// the sums of 32 rows fit beside the rings.
+template <bool BF16, bool W8>
+cudaError_t launch_typed(const MoeParams& p, int num_sms, cudaStream_t stream)
+{
+    if (p.tokens <= 8)
+        return launch_one<BF16, W8, 1, 1>(p, num_sms, stream);
+    if (p.tokens <= 64 && DownCfg<W8, 2, 2>::RING + down_sum_bytes(p.tokens, 2) +
+                                  route_bytes(p.tokens, p.experts, p.topk) <= kMaxSmem)
+        return launch_one<BF16, W8, 2, 2>(p, num_sms, stream);
+    return launch_one<BF16, W8, 2, 1>(p, num_sms, stream);
+}
+
+template <bool BF16, bool W8>
+cudaError_t configure_typed()
+{
+    cudaError_t e = configure_one<BF16, W8, 1, 1>();
+    if (e == cudaSuccess) e = configure_one<BF16, W8, 2, 2>();
+    if (e == cudaSuccess) e = configure_one<BF16, W8, 2, 1>();
+    return e;
+}
+
+}  // namespace
+
+cudaError_t moe_configure()
+{
+    cudaError_t e = configure_typed<false, false>();
+    if (e == cudaSuccess) e = configure_typed<false, true>();
+    if (e == cudaSuccess) e = configure_typed<true, false>();
+    if (e == cudaSuccess) e = configure_typed<true, true>();
+    return e;
+}
+
+cudaError_t moe_launch(const MoeParams& p, int num_sms, cudaStream_t stream)
+{
+    if (p.bf16)
+        return p.w8 ? launch_typed<true, true>(p, num_sms, stream) : launch_typed<true, false>(p, num_sms, stream);
+    return p.w8 ? launch_typed<false, true>(p, num_sms, stream) : launch_typed<false, false>(p, num_sms, stream);
+}
+
+}  // namespace gnt

@@ -74,7 +74,8 @@ typedef enum gemm_status {
     /* Codes 7 and 8 belong to entry points beyond the plain and batched products: */
     GEMM_ERR_NOT_SUPPORTED = 7,      /* the requested kernel cannot take these arguments */
     GEMM_ERR_SCRATCH_TOO_SMALL = 8   /* gemm_nt_f16_f32_batched_no_alloc: the call needs more
-                                        scratch than the library's fixed array holds */
+                                        scratch than the library's fixed array holds;
+                                        gemm_nt_moe: than the workspace given */
 } gemm_status_t;
 
 /* Element types of gemm_nt_batched_ex. */
@@ -283,6 +284,120 @@ int64_t gemm_nt_mx_scale_bytes(int64_t rows, int64_t K);
  */
 gemm_status_t gemm_nt_mx_pack_scales(const void *plain, int64_t ld, int64_t stride, void *packed,
                                      int64_t rows, int64_t K, int64_t batch, gemm_stream_t stream);
+
+/*
+ * Products with one fp32 scale for each block of 128 elements of K.
+ *
+ * A gemm_scale128_t describes the scales of one operand, a logical
+ * (rows_of_operand / rows, ceil(K/128)) fp32 matrix in device memory (4-byte
+ * aligned) with any strides, in elements: the scale of row r and K block c
+ * (elements [128c, 128c+128)) of batch b is
+ *   data[b*batch_stride + (r / rows)*row_stride + c*kb_stride].
+ * rows is 1 (a scale for each row: activations, gradients) or 128 (a scale for
+ * each 128 x 128 block: weights).  gemm_nt_block128_quantize leaves scales with
+ * rows == 1 K block by K block (row_stride 1), the order the kernels read
+ * without gathering.
+ */
+typedef struct gemm_scale128 {
+    const float *data;
+    int32_t rows;          /* 1 or 128 */
+    int64_t row_stride;    /* >= 0 */
+    int64_t kb_stride;     /* >= 0 */
+    int64_t batch_stride;  /* >= 0; 0: shared by every batch */
+} gemm_scale128_t;
+
+/*
+ * The 8-bit product with those scales:
+ *   Out[b,i,j] = sum_c sa[b,i,c] * sb[b,j,c] * sum_{k in block c} A[b,i,k] * B[b,j,k]
+ * A and B both E4M3 or both E5M2, K-major, the last K block as long as K leaves
+ * it.  The inner sums are exact products accumulated in fp32 by the tensor
+ * cores; they are scaled and summed over c in fp32 registers.  Out is fp32, or
+ * that sum rounded once to nearest even into fp16 or bf16.  sa and sb may hold
+ * any fp32 values; infinities and NaN follow IEEE arithmetic.
+ *
+ * path: GEMM_PATH_AUTO, GEMM_PATH_TC05_PAIR (256 x 256 tiles on CTA pairs),
+ * GEMM_PATH_SKINNY (128 rows of B by up to 128 rows of A per CTA, K split over
+ * a cluster when there are few tiles) or GEMM_PATH_MMASYNC (warp MMA, any
+ * layout).  The first two need 16-byte aligned A and B with lda, ldb and batch
+ * strides that are multiples of 16, else GEMM_ERR_NOT_SUPPORTED; AUTO takes the
+ * warp kernel then.  Other paths: GEMM_ERR_NOT_SUPPORTED.  Null scales with
+ * K > 0, rows other than 1 or 128, negative scale strides or other types:
+ * GEMM_ERR_INVALID_VALUE; Out overlapping an operand or its scales:
+ * GEMM_ERR_OVERLAP.  Other arguments and errors as gemm_nt_batched_ex; the
+ * result does not depend on the run (no atomics).
+ */
+gemm_status_t gemm_nt_block128(const void *A, const gemm_scale128_t *SA, const void *B, const gemm_scale128_t *SB,
+                               void *Out, gemm_dtype_t ab_type, gemm_dtype_t out_type,
+                               int64_t M, int64_t N, int64_t K,
+                               int64_t lda, int64_t ldb, int64_t ldo,
+                               int64_t strideA, int64_t strideB, int64_t strideO,
+                               int64_t batch, gemm_path_t path, gemm_stream_t stream);
+
+/*
+ * Quantises X (rows x cols, fp32, fp16 or bf16, row pitch ldx) into the
+ * operands gemm_nt_block128 reads.  For each block of 1 x 128 (SQ->rows == 1)
+ * or 128 x 128 (SQ->rows == 128) elements, with F the type's largest value (448
+ * for E4M3, 57344 for E5M2),
+ *   a = max(max |x|, 2^-100),  scale = a * (1/F),  q = round_to_nearest_even(x * (F * (1/a)))
+ * with every step rounded to fp32; a NaN in a block makes its scale NaN, an infinity makes
+ * the scale infinite and the infinite elements NaN.
+ *
+ * Q (rows x cols, pitch ldq bytes) and its scales SQ, or QT (cols x rows, pitch
+ * ldqt) and its scales ST, or both are written, in one pass over X: QT is X
+ * transposed, quantised in blocks of its own rows (128 rows of X each) -- the
+ * operand of the product that sums over X's rows, a weight gradient.  Null Q
+ * (then SQ is ignored) or null QT leaves that form out.  With both, SQ->rows
+ * and ST->rows agree; with 128 both hold the same values and scales.  The
+ * scales' data are written here although the struct's pointer is const.
+ * Scale matrices must not overlap themselves (row_stride and kb_stride that
+ * separate the elements).  Empty X: GEMM_OK, nothing launched.  Errors:
+ * GEMM_ERR_INVALID_VALUE as elsewhere; GEMM_ERR_OVERLAP when an output overlaps
+ * X or another output (the byte spans, counting pitches).
+ */
+gemm_status_t gemm_nt_block128_quantize(const void *X, gemm_dtype_t x_type, int64_t rows, int64_t cols, int64_t ldx,
+                                        void *Q, int64_t ldq, const gemm_scale128_t *SQ,
+                                        void *QT, int64_t ldqt, const gemm_scale128_t *ST,
+                                        gemm_dtype_t q_type, gemm_stream_t stream);
+
+/*
+ * A mixture-of-experts layer for a few tokens, in two kernels.  For token t
+ * with router logits l (fp32, `experts` of them, row pitch ldl):
+ *   e_0, e_1, ... = the `topk` largest logits, best first, ties to the lower
+ *                   index; an expert whose logit is -inf is never taken
+ *   p_j = exp(l[e_j] - l[e_0]) / sum, the sum over the chosen experts
+ *         (renormalize != 0) or over all of them (softmax first)
+ *   h_j = silu(Wg x) * (Wu x),  silu(v) = v / (1 + exp(-v)),
+ *         Wg = W13[e_j] rows [0, inner), Wu = W13[e_j] rows [inner, 2*inner)
+ *   Out[t] = sum_j p_j * W2[e_j] h_j
+ * A token whose logits are all -inf gets zeros.  A NaN among a token's logits
+ * makes its row NaN, as softmax does.
+ *
+ * X (tokens x hidden) and Out (tokens x hidden) have x_type fp16 or bf16; W13
+ * (experts x 2*inner x hidden) and W2 (experts x hidden x inner), row pitches
+ * ldw13 and ldw2, expert strides strideW13 and strideW2, are of x_type, or
+ * E4M3 with scales S13 and S2 (rows 1 or 128, batch_stride the expert stride;
+ * null for 16-bit weights).  Only the weights of experts that a token chose are
+ * read.  Products run on the warp MMA in tf32, which holds every 16- and 8-bit
+ * value exactly, with fp32 accumulation; h stays in fp32 (its products are taken
+ * in two tf32 parts), and Out is rounded once to x_type.  Sums over experts
+ * follow the expert index, so results do not depend on the run.
+ *
+ * tokens <= 128, experts <= 1024, topk <= min(32, experts): more is
+ * GEMM_ERR_NOT_SUPPORTED.  `workspace` (device memory, 16-byte aligned, the
+ * caller's, at least gemm_nt_moe_workspace_bytes(tokens, topk, inner) bytes) is
+ * overwritten; less is GEMM_ERR_SCRATCH_TOO_SMALL.  Any pitch and alignment is
+ * accepted; rows that start on 16-byte boundaries are read fastest.  tokens or
+ * hidden 0: nothing to do; inner 0: Out is zero.
+ */
+gemm_status_t gemm_nt_moe(const void *X, int64_t ldx, const float *logits, int64_t ldl,
+                          const void *W13, int64_t ldw13, int64_t strideW13, const gemm_scale128_t *S13,
+                          const void *W2, int64_t ldw2, int64_t strideW2, const gemm_scale128_t *S2,
+                          void *Out, int64_t ldo, gemm_dtype_t x_type, gemm_dtype_t w_type,
+                          int64_t tokens, int64_t experts, int64_t topk, int64_t hidden, int64_t inner,
+                          int renormalize, void *workspace, int64_t workspace_bytes, gemm_stream_t stream);
+
+/* Bytes of workspace gemm_nt_moe needs (-1 for negative arguments). */
+int64_t gemm_nt_moe_workspace_bytes(int64_t tokens, int64_t topk, int64_t inner);
 
 /*
  * Host-side pipeline for callers whose data lives in host memory: copies A and
