@@ -49,6 +49,7 @@ struct BlkParams {
 // What a launch needs to know about the current device.
 struct DeviceInfo {
     int num_sms;
+    int block_pairs;  // CTA pairs of block128_pair resident at once
     uint32_t* status;
     unsigned long long wait_limit;
     int fault;
@@ -61,6 +62,13 @@ bool operand_map(CUtensorMap* map, const void* base, int64_t rows, int64_t K, in
                  int64_t stride, int box_rows, int* bmul, int dtype);
 
 cudaError_t block128_any_launch(const BlkParams& p, cudaStream_t stream);
+
+// CTA pairs, 256 x 256 tiles.
+cudaError_t block128_pair_configure(int* max_pairs);  // one-time per device
+cudaError_t block128_pair_launch(const BlkParams& p, int max_pairs, cudaStream_t stream);
+// Single CTAs, 128 rows of B by up to 128 rows of A, K split over clusters.
+cudaError_t block128_swap_configure();  // one-time per device
+cudaError_t block128_swap_launch(const BlkParams& p, int num_sms, cudaStream_t stream);
 
 // Quantiser: block (1 x 128 or 128 x 128) scales of X, in X's order (q) and / or
 // transposed (qt).

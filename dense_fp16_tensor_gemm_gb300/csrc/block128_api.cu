@@ -63,6 +63,25 @@ int kernel_out(gemm_dtype_t t) { return t == GEMM_DTYPE_F16 ? kOutF16 : (t == GE
 
 bool f8(gemm_dtype_t t) { return t == GEMM_DTYPE_E4M3 || t == GEMM_DTYPE_E5M2; }
 
+// Whether tensor maps can describe A and B: 16-byte aligned bases, pitches and
+// batch strides of whole 16 bytes below 2^40, batches that step over matrices.
+bool maps_ok(const BlkParams& p)
+{
+    const auto ok = [&](const void* base, int64_t rows, int64_t ld, int64_t stride) {
+        return aligned(base, 16) && ld % 16 == 0 && ld < (int64_t(1) << 40) &&
+               (p.batch == 1 || stride == 0 ||
+                (stride % 16 == 0 && stride >= rows * ld && stride < (int64_t(1) << 40)));
+    };
+    return ok(p.A, p.M, p.lda, p.stride_a) && ok(p.B, p.N, p.ldb, p.stride_b);
+}
+
+gemm_path_t select(const BlkParams& p, const DeviceInfo& d, int64_t pair_tiles)
+{
+    if (p.K == 0 || !maps_ok(p) || 16 * pair_tiles > INT32_MAX)
+        return GEMM_PATH_MMASYNC;
+    return p.M > 128 && d.block_pairs > 0 && 2 * pair_tiles >= d.block_pairs ? GEMM_PATH_TC05_PAIR : GEMM_PATH_SKINNY;
+}
+
 gemm_status_t status_of(cudaError_t e) { return e == cudaSuccess ? GEMM_OK : GEMM_ERR_LAUNCH; }
 
 }  // namespace
@@ -115,8 +134,8 @@ gemm_status_t gemm_nt_block128(const void* A, const gemm_scale128_t* SA, const v
     p.K = static_cast<int>(K);
     p.batch = static_cast<int>(batch);
     p.num_kb = static_cast<int>(kblocks(K));
-    p.lda = lda;
-    p.ldb = ldb;
+    p.lda = M == 1 ? (K + 15) / 16 * 16 : lda;  // a single row's pitch is never stepped by
+    p.ldb = N == 1 ? (K + 15) / 16 * 16 : ldb;
     p.ldo = ldo;
     p.stride_a = strideA;
     p.stride_b = strideB;
@@ -128,12 +147,25 @@ gemm_status_t gemm_nt_block128(const void* A, const gemm_scale128_t* SA, const v
     p.status = d.status;
     p.wait_limit = d.wait_limit;
     p.fault = d.fault;
+    const int64_t pair_tiles = ((M + 255) / 256) * ((N + 255) / 256) * batch;
     if (path == GEMM_PATH_AUTO)
-        path = GEMM_PATH_MMASYNC;
-    switch (path) {
-    case GEMM_PATH_MMASYNC: return status_of(block128_any_launch(p, s));
-    default: return GEMM_ERR_NOT_SUPPORTED;
-    }
+        path = select(p, d, pair_tiles);
+    if (path == GEMM_PATH_MMASYNC)
+        return status_of(block128_any_launch(p, s));
+    if ((path != GEMM_PATH_TC05_PAIR && path != GEMM_PATH_SKINNY) || (K > 0 && !maps_ok(p)) ||
+        (path == GEMM_PATH_TC05_PAIR && d.block_pairs < 1) || 16 * pair_tiles > INT32_MAX)
+        return GEMM_ERR_NOT_SUPPORTED;
+    if (K == 0)  // nothing to multiply: zeros, which the warp kernel stores in any layout
+        return status_of(block128_any_launch(p, s));
+    // what Out's rows allow: 16-byte stores of 8 elements, or pairs
+    const auto rows_on = [&](int64_t n) {
+        return aligned(Out, static_cast<uintptr_t>(n * osize)) && ldo % n == 0 && (batch == 1 || strideO % n == 0);
+    };
+    p.vec = rows_on(8) ? 8 : (rows_on(2) ? 2 : 1);
+    p.idesc_bits = p.e5m2 ? (1u << 7) | (1u << 10) : 0;
+    if (path == GEMM_PATH_TC05_PAIR)
+        return status_of(block128_pair_launch(p, d.block_pairs, s));
+    return status_of(block128_swap_launch(p, d.num_sms, s));
 }
 
 gemm_status_t gemm_nt_block128_quantize(const void* X, gemm_dtype_t x_type, int64_t rows, int64_t cols, int64_t ldx,

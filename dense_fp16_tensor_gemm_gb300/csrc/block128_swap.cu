@@ -1,0 +1,437 @@
+// block128_swap.cu -- block-scaled 8-bit product on single CTAs (tcgen05), for
+// few rows of A or few tiles.
+//
+// The operands are swapped: 128 rows of B (weights) are the MMA's row side and
+// BN = 16, 32, 64 or 128 rows of A its column side, so a decode batch pays for
+// no padding beyond its next power of two.  Bound by reading B once: a K block
+// brings 16 KB of B a tile, 700 cycles at an SM's share of memory bandwidth,
+// against 64 cycles of MMA at BN = 32.  What matters is bytes in flight, hence a
+// ring of up to 200 KB, and enough CTAs: with fewer tiles than SMs a cluster of
+// up to 8 CTAs splits K of one tile and adds its sums through distributed
+// shared memory, in CTA order, so the result never depends on timing.
+//
+// As in the pair kernel each K block is a fresh accumulator (four of them in
+// Tensor Memory) that promotion warps scale and add to sums in registers; here
+// a thread holds one row of B (32x32b loads) and half of the columns, its row's
+// scale in a register and the columns' scales broadcast from shared memory.
+#include <algorithm>
+
+#include "block128_tc.cuh"
+
+namespace gnt {
+
+namespace {
+
+using namespace blk;
+using tc::BM;
+
+constexpr int kAcc = 4;         // accumulators in Tensor Memory
+constexpr int kScaleRing = 8;
+constexpr int kScaleBatch = 4;
+constexpr int kMaxCluster = 8;
+
+constexpr int max_int(int a, int b) { return a > b ? a : b; }
+constexpr int min_int(int a, int b) { return a < b ? a : b; }
+
+template <int BN>
+struct Cfg {
+    static constexpr int X_BYTES = BM * kRowBytes, Y_BYTES = BN * kRowBytes;
+    static constexpr int STAGE = X_BYTES + Y_BYTES;
+    static constexpr int SCALE_FLOATS = 128 + BN;
+    static constexpr int BAR_BYTES = 512;
+    static constexpr int REST = 1024 + kScaleRing * SCALE_FLOATS * 4 + BAR_BYTES;
+    static constexpr int STAGES = min_int(12, (232448 - REST) / STAGE);
+    static constexpr int SMEM = REST + STAGES * STAGE;
+    static constexpr int TMEM_COLS = max_int(32, kAcc * BN);
+    static constexpr int COLS = BN / 2;  // columns of a promotion thread
+    static_assert(BM * BN * 4 <= STAGES * STAGE, "a tile's sums fit in the ring");
+    static_assert((2 * STAGES + 2 * kAcc + 2 * kScaleRing + 1) * 8 + 8 <= BAR_BYTES, "barrier area");
+};
+
+__device__ __forceinline__ float ld_cluster(uint32_t addr)
+{
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
+}
+
+// Tiles: rows of B first, so that neighbours share A.
+__device__ __forceinline__ void decode(const BlkParams& p, int t, int bn, int& b, int& x0, int& y0)
+{
+    const int per = p.tiles_m * p.tiles_n;
+    b = t / per;
+    t -= b * per;
+    y0 = t / p.tiles_n * bn;
+    x0 = t % p.tiles_n * BM;
+}
+
+template <int BN>
+__global__ void __launch_bounds__(kThreads, 1)
+    block128_swap_kernel(const __grid_constant__ CUtensorMap tmx, const __grid_constant__ CUtensorMap tmy,
+                         const BlkParams p, int cluster)
+{
+    using C = Cfg<BN>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t* xs = smem;
+    uint8_t* ys = smem + C::STAGES * C::X_BYTES;
+    float* scales = reinterpret_cast<float*>(smem + C::STAGES * C::STAGE);
+    uint64_t* full = reinterpret_cast<uint64_t*>(scales + kScaleRing * C::SCALE_FLOATS);
+    uint64_t* empty = full + C::STAGES;
+    uint64_t* tfull = empty + C::STAGES;
+    uint64_t* tempty = tfull + kAcc;
+    uint64_t* sfull = tempty + kAcc;
+    uint64_t* sempty = sfull + kScaleRing;
+    uint64_t* drain = sempty + kScaleRing;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = static_cast<int>(blockIdx.x) % cluster;
+    const int first = static_cast<int>(blockIdx.x) / cluster, step = static_cast<int>(gridDim.x) / cluster;
+    const int kb0 = static_cast<int>(static_cast<int64_t>(p.num_kb) * rank / cluster);
+    const int kb1 = static_cast<int>(static_cast<int64_t>(p.num_kb) * (rank + 1) / cluster);
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < C::STAGES; ++s) {
+            mbar_init(smem_u32(&full[s]), 1);
+            mbar_init(smem_u32(&empty[s]), 1);
+        }
+        for (int b = 0; b < kAcc; ++b) {
+            mbar_init(smem_u32(&tfull[b]), 1);
+            mbar_init(smem_u32(&tempty[b]), kPromoWarps);
+        }
+        for (int r = 0; r < kScaleRing; ++r) {
+            mbar_init(smem_u32(&sfull[r]), 32);
+            mbar_init(smem_u32(&sempty[r]), kPromoWarps);
+        }
+        mbar_init(smem_u32(drain), 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+        tma_prefetch_map(&tmx);
+        tma_prefetch_map(&tmy);
+    }
+    if (warp == 1) {
+        tmem_alloc<C::TMEM_COLS>(smem_u32(tmem_slot));
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem_base = *tmem_slot;
+    pdl_launch_dependents();
+    pdl_wait();  // global memory only after the preceding grids are done
+
+    uint64_t acc[C::COLS / 2];  // promotion threads: pairs of columns
+#pragma unroll
+    for (int j = 0; j < C::COLS / 2; ++j)
+        acc[j] = 0;
+    const int q = warp & 3, ch = (warp - 4) >> 2;  // promotion: lane quadrant, column half
+
+    if (warp == 0) {
+        if (lane == 0) {
+            // -------------------------------------------------------- producer
+            int stage = 0;
+            uint32_t phase = 0, filled = 0, fill_parity = 0;
+            // B is read once, A by every tile row: keep A in L2 under the stream
+            const uint64_t pol_x = l2_policy_evict_first(), pol_y = l2_policy_evict_last();
+            bool ok = true, drop = p.fault == 1 && blockIdx.x == 0;
+            for (int t = first; ok && t < p.num_tiles; t += step) {
+                int b, x0, y0;
+                decode(p, t, BN, b, x0, y0);
+                for (int kb = kb0; kb < kb1; ++kb) {
+                    if (!wait_bounded(smem_u32(&empty[stage]), phase ^ 1, abort_flag, p.wait_limit)) {
+                        raise(p, abort_flag);
+                        ok = false;
+                        break;
+                    }
+                    if (!drop) {
+                        const uint32_t fb = smem_u32(&full[stage]);
+                        mbar_arrive_expect_tx(fb, C::STAGE);
+                        filled |= 1u << stage;
+                        fill_parity = (fill_parity & ~(1u << stage)) | (phase << stage);
+                        tma_load_3d_hint(smem_u32(xs + stage * C::X_BYTES), &tmx, fb, kb * kRowBytes, x0, b * p.b_bmul, pol_x);
+                        tma_load_3d_hint(smem_u32(ys + stage * C::Y_BYTES), &tmy, fb, kb * kRowBytes, y0, b * p.a_bmul, pol_y);
+                    }
+                    drop = false;
+                    if (++stage == C::STAGES) {
+                        stage = 0;
+                        phase ^= 1;
+                    }
+                }
+            }
+            for (int s = 0; s < C::STAGES; ++s)
+                if (filled & (1u << s))
+                    drain_wait(smem_u32(&full[s]), (fill_parity >> s) & 1u, p.wait_limit);
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            // -------------------------------------------------------- MMA issue
+            const uint32_t idesc = idesc_f16_f32(BM, BN) | p.idesc_bits;
+            const DescWords dx = desc_words(smem_u32(xs), false), dy = desc_words(smem_u32(ys), false);
+            int stage = 0, buf = 0;
+            uint32_t phase = 0, tphase = 0;
+            bool ok = true, skip_release = p.fault == 2 && blockIdx.x == 0;
+            for (int t = first; ok && t < p.num_tiles; t += step) {
+                for (int kb = kb0; kb < kb1; ++kb) {
+                    if (!wait_bounded(smem_u32(&tempty[buf]), tphase ^ 1, abort_flag, p.wait_limit) ||
+                        !wait_bounded(smem_u32(&full[stage]), phase, abort_flag, p.wait_limit)) {
+                        raise(p, abort_flag);
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t d = tmem_base + static_cast<uint32_t>(buf * BN);
+                    const uint32_t xlo = dx.lo + stage * (C::X_BYTES >> 4), ylo = dy.lo + stage * (C::Y_BYTES >> 4);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        tc_mma_w<true>(d, xlo + k * dx.kstep, dx.hi, ylo + k * dy.kstep, dy.hi, idesc, k > 0);
+                    if (!skip_release)
+                        tc_commit(smem_u32(&empty[stage]));
+                    skip_release = false;
+                    tc_commit(smem_u32(&tfull[buf]));
+                    if (++stage == C::STAGES) {
+                        stage = 0;
+                        phase ^= 1;
+                    }
+                    if (++buf == kAcc) {
+                        buf = 0;
+                        tphase ^= 1;
+                    }
+                }
+            }
+            // no MMA may still be running when Tensor Memory is released
+            tc_commit(smem_u32(drain));
+            drain_wait(smem_u32(drain), 0, p.wait_limit);
+        }
+    } else if (warp == 2) {
+        // ------------------------------------------------------------ scales: 128 rows of B, BN rows of A
+        constexpr int NY = (BN + 31) / 32;
+        int slot = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        for (int t = first; ok && t < p.num_tiles; t += step) {
+            int b, x0, y0;
+            decode(p, t, BN, b, x0, y0);
+            for (int k0 = kb0; ok && k0 < kb1; k0 += kScaleBatch) {
+                float vx[kScaleBatch][4], vy[kScaleBatch][NY];
+#pragma unroll
+                for (int i = 0; i < kScaleBatch; ++i) {
+                    const int kb = min(k0 + i, kb1 - 1);
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        vx[i][r] = scale_at(p.sb, b, min(x0 + 32 * r + lane, p.N - 1), kb);
+#pragma unroll
+                    for (int r = 0; r < NY; ++r)
+                        vy[i][r] = scale_at(p.sa, b, min(y0 + 32 * r + lane, p.M - 1), kb);
+                }
+#pragma unroll
+                for (int i = 0; i < kScaleBatch; ++i) {
+                    if (ok && k0 + i < kb1) {
+                        if (!wait_bounded(smem_u32(&sempty[slot]), phase ^ 1, abort_flag, p.wait_limit)) {
+                            raise(p, abort_flag);
+                            ok = false;
+                        } else {
+                            float* s = scales + slot * C::SCALE_FLOATS;
+#pragma unroll
+                            for (int r = 0; r < 4; ++r)
+                                s[32 * r + lane] = vx[i][r];
+#pragma unroll
+                            for (int r = 0; r < NY; ++r)
+                                if (32 * r + lane < BN)
+                                    s[128 + 32 * r + lane] = vy[i][r];
+                            mbar_arrive(smem_u32(&sfull[slot]));
+                            if (++slot == kScaleRing) {
+                                slot = 0;
+                                phase ^= 1;
+                            }
+                        }
+                    }
+                }
+            }
+        }
+    } else if (warp >= 4) {
+        // ------------------------------------------------------------ promotion
+        int slot = 0, buf = 0;
+        uint32_t sphase = 0, tphase = 0;
+        bool ok = true;
+        for (int t = first; ok && t < p.num_tiles; t += step) {
+            for (int kb = kb0; kb < kb1; ++kb) {
+                if (!wait_bounded(smem_u32(&sfull[slot]), sphase, abort_flag, p.wait_limit) ||
+                    !wait_bounded(smem_u32(&tfull[buf]), tphase, abort_flag, p.wait_limit)) {
+                    raise(p, abort_flag);
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const float* s = scales + slot * C::SCALE_FLOATS;
+                const float fx = s[32 * q + lane];
+                const uint64_t sx = pack2(fx, fx);
+                const uint32_t ta = tmem_base + static_cast<uint32_t>(buf * BN + C::COLS * ch) +
+                                    (static_cast<uint32_t>(32 * q) << 16);
+                uint32_t x[C::COLS];
+#pragma unroll
+                for (int c = 0; c < C::COLS; c += 8)
+                    tmem_ld32x8(ta + c, x + c);
+#pragma unroll
+                for (int c = 0; c < C::COLS; c += 8)
+                    tmem_wait8(x + c);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(smem_u32(&tempty[buf]));
+                const ulonglong2* sy = reinterpret_cast<const ulonglong2*>(s + 128 + C::COLS * ch);
+#pragma unroll
+                for (int j = 0; j < C::COLS / 4; ++j) {
+                    const ulonglong2 w = sy[j];
+                    acc[2 * j] = fma2(mul2(pack2u(x[4 * j], x[4 * j + 1]), w.x), sx, acc[2 * j]);
+                    acc[2 * j + 1] = fma2(mul2(pack2u(x[4 * j + 2], x[4 * j + 3]), w.y), sx, acc[2 * j + 1]);
+                }
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(smem_u32(&sempty[slot]));
+                if (++slot == kScaleRing) {
+                    slot = 0;
+                    sphase ^= 1;
+                }
+                if (++buf == kAcc) {
+                    buf = 0;
+                    tphase ^= 1;
+                }
+            }
+            if (!ok || cluster > 1)
+                break;  // a cluster has one tile, finished below
+            int b, x0, y0;
+            decode(p, t, BN, b, x0, y0);
+            const int x = x0 + 32 * q + lane, y = y0 + C::COLS * ch;
+            const auto store = [&](auto ot) {
+                using S = OutStore<decltype(ot)::value>;
+                typename S::T* d = static_cast<typename S::T*>(p.out) + b * p.stride_o + static_cast<int64_t>(y) * p.ldo + x;
+#pragma unroll
+                for (int j = 0; j < C::COLS; j += 2) {
+                    float v0, v1;
+                    unpack2(acc[j / 2], v0, v1);
+                    acc[j / 2] = 0;
+                    if (x < p.N) {
+                        if (y + j < p.M)
+                            S::st1(d, v0);
+                        if (y + j + 1 < p.M)
+                            S::st1(d + p.ldo, v1);
+                    }
+                    d += 2 * p.ldo;
+                }
+            };
+            if (p.out_type == kOutF16)
+                store(std::integral_constant<int, kOutF16>());
+            else if (p.out_type == kOutBF16)
+                store(std::integral_constant<int, kOutBF16>());
+            else
+                store(std::integral_constant<int, kOutF32>());
+        }
+        if (cluster > 1) {
+            // Every MMA has read its operands (the last accumulator is here), so the
+            // ring can take the sums: column j of the tile at [j][row].
+            float* d = reinterpret_cast<float*>(smem) + C::COLS * ch * BM + 32 * q + lane;
+#pragma unroll
+            for (int j = 0; j < C::COLS; j += 2) {
+                float v0, v1;
+                unpack2(acc[j / 2], v0, v1);
+                d[j * BM] = v0;
+                d[(j + 1) * BM] = v1;
+            }
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (cluster > 1) {
+        cluster_sync();
+        int b, x0, y0;
+        decode(p, first, BN, b, x0, y0);
+        const int n = min(BN, p.M - y0) * BM;
+        const int lo = static_cast<int>(static_cast<int64_t>(n) * rank / cluster);
+        const int hi = static_cast<int>(static_cast<int64_t>(n) * (rank + 1) / cluster);
+        const uint32_t base = smem_u32(smem);
+        for (int i = lo + static_cast<int>(threadIdx.x); i < hi; i += kThreads) {
+            float s = 0.f;
+            for (int r = 0; r < cluster; ++r)
+                s += ld_cluster(mapa_shared(base + 4 * i, r));
+            const int x = x0 + i % BM, y = y0 + i / BM;
+            if (x < p.N) {
+                const int64_t o = b * p.stride_o + static_cast<int64_t>(y) * p.ldo + x;
+                if (p.out_type == kOutF16)
+                    OutStore<kOutF16>::st1(static_cast<uint16_t*>(p.out) + o, s);
+                else if (p.out_type == kOutBF16)
+                    OutStore<kOutBF16>::st1(static_cast<uint16_t*>(p.out) + o, s);
+                else
+                    OutStore<kOutF32>::st1(static_cast<float*>(p.out) + o, s);
+            }
+        }
+        cluster_sync();  // no CTA leaves while another may still read its sums
+    }
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc<C::TMEM_COLS>(tmem_base);
+    }
+}
+
+template <int BN>
+cudaError_t launch(BlkParams p, int num_sms, cudaStream_t stream)
+{
+    CUtensorMap tmx, tmy;
+    const int type = p.e5m2 ? 4 : 3;  // gemm_dtype_t
+    if (!operand_map(&tmx, p.B, p.N, p.K, p.ldb, p.batch, p.stride_b, BM, &p.b_bmul, type) ||
+        !operand_map(&tmy, p.A, p.M, p.K, p.lda, p.batch, p.stride_a, BN, &p.a_bmul, type))
+        return cudaErrorInvalidValue;
+    p.tiles_m = (p.M + BN - 1) / BN;
+    p.tiles_n = (p.N + BM - 1) / BM;
+    p.num_tiles = p.tiles_m * p.tiles_n * p.batch;
+    // split K while whole clusters still fit the GPU and a CTA keeps 4 K blocks
+    int c = 1;
+    while (c < kMaxCluster && p.num_tiles * 2 * c <= num_sms && p.num_kb >= 8 * c)
+        c *= 2;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(c > 1 ? p.num_tiles * c : std::min(p.num_tiles, num_sms)));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = Cfg<BN>::SMEM;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = static_cast<unsigned>(c);
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, block128_swap_kernel<BN>, tmx, tmy, p, c);
+}
+
+template <int BN>
+cudaError_t configure()
+{
+    return cudaFuncSetAttribute(block128_swap_kernel<BN>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<BN>::SMEM);
+}
+
+}  // namespace
+
+cudaError_t block128_swap_configure()
+{
+    cudaError_t e = configure<16>();
+    if (e == cudaSuccess) e = configure<32>();
+    if (e == cudaSuccess) e = configure<64>();
+    if (e == cudaSuccess) e = configure<128>();
+    return e;
+}
+
+cudaError_t block128_swap_launch(const BlkParams& p, int num_sms, cudaStream_t stream)
+{
+    if (p.M <= 16)
+        return launch<16>(p, num_sms, stream);
+    if (p.M <= 32)
+        return launch<32>(p, num_sms, stream);
+    if (p.M <= 64)
+        return launch<64>(p, num_sms, stream);
+    return launch<128>(p, num_sms, stream);
+}
+
+}  // namespace gnt

@@ -43,6 +43,7 @@ struct DeviceState {
     bool supported = false;
     int num_sms = 0;
     int max_pairs = 0;  // CTA pairs of the pair kernel resident at once
+    int block_pairs = 0;  // and of the block-scaled one
     uint32_t* status = nullptr;
     // host-buffer pipeline: copy streams and events, created by the first call
     // that succeeds in creating them
@@ -90,7 +91,7 @@ gemm_status_t device_state(DeviceState** out)
             const bool supported = major == 10 && minor == 3;
             if (supported) {
                 void* sym = nullptr;
-                int max_pairs = 0;
+                int max_pairs = 0, block_pairs = 0;
                 e = cudaGetSymbolAddress(&sym, g_status_word);
                 if (e == cudaSuccess) e = cudaMemset(sym, 0, sizeof(uint32_t));
                 if (e == cudaSuccess) e = tc05_configure(64, false);
@@ -99,11 +100,14 @@ gemm_status_t device_state(DeviceState** out)
                 if (e == cudaSuccess) e = tc05_configure(64, true);
                 if (e == cudaSuccess) e = tc05_small_configure();
                 if (e == cudaSuccess) e = tc05_pair_configure(&max_pairs);
+                if (e == cudaSuccess) e = block128_pair_configure(&block_pairs);
+                if (e == cudaSuccess) e = block128_swap_configure();
                 if (e == cudaSuccess) e = moe_configure();
                 if (e != cudaSuccess)
                     return GEMM_ERR_LAUNCH;
                 d.status = static_cast<uint32_t*>(sym);
                 d.max_pairs = max_pairs;
+                d.block_pairs = block_pairs;
             }
             d.num_sms = sms;
             d.supported = supported;
@@ -1051,7 +1055,7 @@ int device_info(DeviceInfo* out)
     DeviceState* d = nullptr;
     const gemm_status_t st = device_state(&d);
     if (st == GEMM_OK)
-        *out = DeviceInfo{d->num_sms, d->status, wait_limit(), g_fault.load()};
+        *out = DeviceInfo{d->num_sms, d->block_pairs, d->status, wait_limit(), g_fault.load()};
     return st;
 }
 

@@ -15,7 +15,7 @@ import dense_fp16_tensor_gemm_gb300 as gnt
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
 
-PATHS = [gnt.Path.AUTO, gnt.Path.MMASYNC]
+PATHS = [gnt.Path.AUTO, gnt.Path.MMASYNC, gnt.Path.SKINNY, gnt.Path.TC05_PAIR]
 HALF_ULP = {torch.float32: 2.0 ** -24, torch.float16: 2.0 ** -11, torch.bfloat16: 2.0 ** -8}
 SMALLEST = {torch.float32: 2.0 ** -149, torch.float16: 2.0 ** -24, torch.bfloat16: 2.0 ** -133}
 
