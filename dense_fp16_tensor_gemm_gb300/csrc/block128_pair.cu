@@ -8,19 +8,22 @@
 // Memory, and "promotion" warps take it out, scale it and add it to sums they
 // hold in registers.  A pair owns a 256 x 256 tile; per block the MMAs take 512
 // cycles (four 256x256x32 instructions at 8192 multiply-adds an SM and cycle),
-// in which each SM's 8 promotion warps must read 128 x 256 values from Tensor
-// Memory and do one (or, with scales per row of B, two) packed fp32 operations
-// for every two of them: 128 or 256 issue cycles of the 512 a scheduler has.
-// Two accumulators of 256 columns fill Tensor Memory and let block c + 1's MMAs
-// run while block c is promoted.
+// as does shared memory (64 KB in and out at 128 bytes a cycle), and each SM's
+// promotion warps read 128 x 256 values from Tensor Memory and do one packed fp32
+// operation for every two of them (300 cycles; two, where B has a scale for
+// every row).  Two accumulators of 256 columns fill Tensor Memory; what bounds
+// the kernel is the round trip of one: MMA, commit to both CTAs, loads and
+// arithmetic, release to the leader.  Measured per block (4864 x 4096 x 8192):
+// 519 ns, 300 ns with the loads and the arithmetic left out; halves of 128
+// columns, which shorten the trip, take 582 (A is read twice and shared memory
+// fills up); 16 warps with 64 sums each 760.
 //
-// Roles per CTA (384 threads): warp 0 TMA producer; warp 1 Tensor Memory and,
-// in the leader, MMA issue; warp 2 brings the scales into a ring of their own
-// (plain loads: any strides); warps 4-11 promotion, 128 sums per thread, which
-// take over registers from warps 0-3.  Warps 4-11 read Tensor Memory in the
-// 16x256b shape: a quad of lanes holds 8 consecutive columns of a row, so a
-// thread needs 4 row scales and, for scales per row of B, 32 column scales
-// instead of 128, and Out leaves in row segments.
+// Roles per CTA (384 threads): warp 0 TMA producer; warps 1 and 3 in the leader
+// MMA issue; warp 2 brings the scales into a ring of their own (any strides);
+// warps 4-11 promotion, 128 sums per thread, which take over registers from
+// warps 0-3.  A thread holds 128 columns of one row (32x32b loads), so a block
+// takes two scales from shared memory, or 1 + 128; Out passes through a small
+// staging area to leave in row segments.
 // Synchronisation:
 //   full[s], empty[s]    operand ring, as in the unscaled pair kernel
 //   tfull[b], tempty[b]  accumulators: leader's commit to both CTAs / one
@@ -39,14 +42,20 @@ using namespace blk;
 using tc::BM;
 
 constexpr int kTile = 256;                  // rows and columns of a pair's tile
-constexpr int kStages = 6;
+constexpr int kThreads = 384;
+constexpr int kPromoWarps = 8;
+constexpr int kCols = 128;                  // columns of a promotion thread
+constexpr int kPiece = 32;                  // columns of one accumulator load
+constexpr int kAcc = 2;                     // accumulators in Tensor Memory, one per K block parity
+constexpr int kStages = 5;
 constexpr int kOpBytes = BM * kRowBytes;    // one CTA's half of A, and of B
-constexpr int kScaleRing = 8;
-constexpr int kScaleFloats = 128 + 256;     // rows' scales, columns' scales (or rows' times each column block's)
-constexpr int kScaleBatch = 4;              // K blocks whose scale loads are in flight together
+constexpr int kScaleRing = 4;               // slots of kScaleGroup K blocks
+constexpr int kScaleGroup = 4;
+constexpr int kScaleFloats = 128 + 256;     // rows' scales, then columns' (or the two column blocks')
+constexpr int kStageWords = 32 * 16;        // a promotion warp's staging area: 32 rows of 64 bytes
 constexpr int kTmemCols = 512;
 constexpr int kBarBytes = 512;
-constexpr int kSmem = 1024 + kStages * 2 * kOpBytes + kScaleRing * kScaleFloats * 4 + kBarBytes;
+constexpr int kSmem = 1024 + kStages * 2 * kOpBytes + kScaleRing * kScaleGroup * kScaleFloats * 4 + kPromoWarps * kStageWords * 4 + kBarBytes;
 static_assert(kSmem <= 232448, "shared memory budget");
 
 // Tile t of this pair's walk -> batch and tile origin; tiles go down groups of
@@ -62,85 +71,110 @@ __device__ __forceinline__ void decode(const BlkParams& p, int t, int& b, int& m
     n0 = r / gm * kTile;
 }
 
-// 4 x 4 words across a quad of lanes: lane i ends with word i of lanes 0..3.
-__device__ __forceinline__ void quad_transpose(uint32_t (&v)[4], int lane)
+// K blocks of all of a pair's tiles.
+__device__ __forceinline__ int blocks_of(const BlkParams& p, int pair, int pairs)
 {
-    const bool odd = lane & 1, high = lane & 2;
-    const uint32_t a = __shfl_xor_sync(0xffffffffu, odd ? v[0] : v[1], 1);
-    const uint32_t b = __shfl_xor_sync(0xffffffffu, odd ? v[2] : v[3], 1);
-    if (odd) {
-        v[0] = a;
-        v[2] = b;
-    } else {
-        v[1] = a;
-        v[3] = b;
-    }
-    const uint32_t c = __shfl_xor_sync(0xffffffffu, high ? v[0] : v[2], 2);
-    const uint32_t d = __shfl_xor_sync(0xffffffffu, high ? v[1] : v[3], 2);
-    if (high) {
-        v[0] = c;
-        v[1] = d;
-    } else {
-        v[2] = c;
-        v[3] = d;
-    }
+    return (p.num_tiles - pair + pairs - 1) / pairs * p.num_kb;
 }
 
-// Stores a promotion warp's 32 rows x 128 columns: acc[c][h][half][j] holds
-// columns 32c + 8j + 2(lane % 4) + {0, 1} of row 16h + 8*half + lane / 4.
+// Stores a promotion warp's 32 rows x 128 columns, a row per thread, through its
+// staging area: 64 bytes of every row at a time, in 16-byte slots XOR-swizzled
+// by row so that neither side has bank conflicts, leave as whole row segments.
 template <int OT>
-__device__ __forceinline__ void store_tile(const BlkParams& p, const uint64_t (&acc)[4][2][2][4], int b, int row0,
-                                           int col0, int lane)
+__device__ __forceinline__ void store_tile(const BlkParams& p, const uint64_t (&acc)[kCols / 2], uint32_t* stage, int b,
+                                           int row0, int col0, int lane)
 {
     using S = OutStore<OT>;
+    constexpr int PER_WORD = OT == kOutF32 ? 1 : 2, SEG = 16 * PER_WORD;  // elements of a word, of a segment
     typename S::T* out = static_cast<typename S::T*>(p.out) + b * p.stride_o;
+    const bool wide = p.vec >= 4 * PER_WORD;  // rows on 16-byte boundaries
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
+    for (int c = 0; c < kCols; c += SEG) {
+        uint32_t w[16];
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            const int row = row0 + 16 * h + 8 * half + (lane >> 2);
-            typename S::T* d = out + static_cast<int64_t>(row) * p.ldo;
+        for (int i = 0; i < 16; ++i) {
+            if constexpr (OT == kOutF32) {
+                float f[2];
+                unpack2(acc[(c + i) / 2], f[0], f[1]);
+                w[i] = __float_as_uint(f[i & 1]);
+            } else {
+                float f0, f1;
+                unpack2(acc[c / 2 + i], f0, f1);
+                w[i] = S::pack(f0, f1);
+            }
+        }
+        uint4* s4 = reinterpret_cast<uint4*>(stage);
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                float v[8];
+        for (int j = 0; j < 4; ++j)
+            s4[lane * 4 + (j ^ ((lane >> 1) & 3))] = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+        __syncwarp();
+        const int cs = col0 + c;
+        if (wide && cs + SEG <= p.N) {
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    unpack2(acc[c][h][half][j], v[2 * j], v[2 * j + 1]);
-                if constexpr (OT != kOutF32) {
-                    if (p.vec == 8) {  // 16-byte stores: each lane takes 8 consecutive columns
-                        uint32_t w[4];
-#pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            w[j] = S::pack(v[2 * j], v[2 * j + 1]);
-                        quad_transpose(w, lane);
-                        const int col = col0 + 32 * c + 8 * (lane & 3);
-                        if (row < p.M && col + 8 <= p.N) {
-                            __stcs(reinterpret_cast<uint4*>(d + col), make_uint4(w[0], w[1], w[2], w[3]));
-                        } else if (row < p.M) {
-#pragma unroll
-                            for (int e = 0; e < 8; ++e)
-                                if (col + e < p.N)
-                                    d[col + e] = static_cast<uint16_t>(w[e >> 1] >> (16 * (e & 1)));
-                        }
-                        continue;
-                    }
-                }
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int col = col0 + 32 * c + 8 * j + 2 * (lane & 3);
-                    if (row < p.M) {
-                        if (p.vec >= 2 && col + 2 <= p.N) {
-                            S::st2(d + col, v[2 * j], v[2 * j + 1]);
-                        } else {
-                            if (col < p.N)
-                                S::st1(d + col, v[2 * j]);
-                            if (col + 1 < p.N)
-                                S::st1(d + col + 1, v[2 * j + 1]);
-                        }
+            for (int i = 0; i < 4; ++i) {
+                const int r = 8 * i + (lane >> 2), j = lane & 3;
+                if (row0 + r < p.M)
+                    __stcs(reinterpret_cast<uint4*>(out + static_cast<int64_t>(row0 + r) * p.ldo + cs) + j,
+                           s4[r * 4 + (j ^ ((r >> 1) & 3))]);
+            }
+        } else {
+            const int word = lane & 15, col = cs + word * PER_WORD;
+#pragma unroll 8
+            for (int i = 0; i < 16; ++i) {
+                const int r = 2 * i + (lane >> 4);
+                const uint32_t v = stage[r * 16 + (((word >> 2) ^ ((r >> 1) & 3)) << 2) + (word & 3)];
+                if (row0 + r < p.M && col < p.N) {
+                    typename S::T* d = out + static_cast<int64_t>(row0 + r) * p.ldo + col;
+                    if constexpr (OT == kOutF32) {
+                        __stcs(d, __uint_as_float(v));
+                    } else if (p.vec >= 2 && col + 1 < p.N) {
+                        __stcs(reinterpret_cast<uint32_t*>(d), v);
+                    } else {
+                        d[0] = static_cast<uint16_t>(v);
+                        if (col + 1 < p.N)
+                            d[1] = static_cast<uint16_t>(v >> 16);
                     }
                 }
             }
         }
+        __syncwarp();
+    }
+}
+
+// The scale warp: for every K block of the pair's tiles, this CTA's 128 row scales
+// of A and the tile's 256 (BROW) or 2 of B into the scale ring, by asynchronous
+// copies that signal the slot's barrier, so that a ring's worth is in flight.
+// Rows outside Out multiply zeros and are not stored; they take the last row's
+// scale.
+template <bool BROW>
+__device__ __forceinline__ void load_scales(const BlkParams& p, int rank, float* scales, uint64_t* sfull, uint64_t* sempty,
+                                            volatile int* abort_flag, int pair, int pairs)
+{
+    const uint32_t ring = smem_u32(scales);
+    int n = 0;  // K blocks so far
+    for (int t = pair; t < p.num_tiles; t += pairs) {
+        int b, m0, n0;
+        decode(p, t, b, m0, n0);
+        ScaleRun<4> a(p.sa, b, m0 + rank * BM, p.M);
+        ScaleRun<BROW ? 8 : 1> w(p.sb, b, n0, p.N, BROW ? 1 : 128);
+#pragma unroll 1
+        for (int kb = 0; kb < p.num_kb; ++kb, ++n) {
+            const int slot = n / kScaleGroup % kScaleRing;
+            if (n % kScaleGroup == 0 &&
+                !wait_bounded(smem_u32(&sempty[slot]), (n / (kScaleGroup * kScaleRing) & 1) ^ 1, abort_flag, p.wait_limit)) {
+                raise(p, abort_flag);
+                return;
+            }
+            const uint32_t s = ring + n % (kScaleGroup * kScaleRing) * (kScaleFloats * 4);
+            a.copy(s);
+            w.copy(s + 128 * 4);
+            if (n % kScaleGroup == kScaleGroup - 1)
+                cp_async_arrive(smem_u32(&sfull[slot]));
+        }
+    }
+    if (n % kScaleGroup != 0)  // the last group, short
+        cp_async_arrive(smem_u32(&sfull[n / kScaleGroup % kScaleRing]));
+    cp_async_wait_all();
 }
 
 // BROW: a scale for each row of B (each column of the tile), else one for each
@@ -155,18 +189,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint8_t* as = smem;
     uint8_t* bs = smem + kStages * kOpBytes;
     float* scales = reinterpret_cast<float*>(smem + 2 * kStages * kOpBytes);
-    uint64_t* full = reinterpret_cast<uint64_t*>(scales + kScaleRing * kScaleFloats);
+    uint32_t* staging = reinterpret_cast<uint32_t*>(scales + kScaleRing * kScaleGroup * kScaleFloats);
+    uint64_t* tfull = reinterpret_cast<uint64_t*>(staging + kPromoWarps * kStageWords);
+    uint64_t* tempty = tfull + kAcc;
+    uint64_t* full = tempty + kAcc;
     uint64_t* empty = full + kStages;
-    uint64_t* tfull = empty + kStages;
-    uint64_t* tempty = tfull + 2;
-    uint64_t* sfull = tempty + 2;
+    uint64_t* sfull = empty + kStages;
     uint64_t* sempty = sfull + kScaleRing;
     uint64_t* drain = sempty + kScaleRing;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 2);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-    static_assert((2 * kStages + 4 + 2 * kScaleRing + 1) * 8 + 8 <= kBarBytes, "barrier area");
+    static_assert((2 * kStages + 2 * kAcc + 2 * kScaleRing + 2) * 8 + 8 <= kBarBytes, "barrier area");
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const uint32_t rank = cluster_ctarank();
     const bool leader = rank == 0;
     const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
@@ -176,7 +211,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(smem_u32(&full[s]), 1);
             mbar_init(smem_u32(&empty[s]), 1);
         }
-        for (int b = 0; b < 2; ++b) {
+        for (int b = 0; b < kAcc; ++b) {
             mbar_init(smem_u32(&tfull[b]), 1);
             mbar_init(smem_u32(&tempty[b]), 2 * kPromoWarps);
         }
@@ -184,7 +219,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(smem_u32(&sfull[r]), 32);
             mbar_init(smem_u32(&sempty[r]), kPromoWarps);
         }
-        mbar_init(smem_u32(drain), 1);
+        mbar_init(smem_u32(&drain[0]), 1);
+        mbar_init(smem_u32(&drain[1]), 1);
         *abort_flag = 0;
         fence_mbar_init();
         tma_prefetch_map(&tma);
@@ -202,7 +238,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     pdl_wait();  // global memory only after the preceding grids are done
 
     if (warp < 4) {
-        regs_utility();
+        regs_give<72>();
         if (warp == 0 && lane == 0) {
             // -------------------------------------------------------- producer (both CTAs)
             int stage = 0;
@@ -212,6 +248,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 int b, m0, n0;
                 decode(p, t, b, m0, n0);
                 const int xa = m0 + static_cast<int>(rank) * BM, xb = n0 + static_cast<int>(rank) * BM;
+#pragma unroll 1
                 for (int kb = 0; kb < p.num_kb; ++kb) {
                     if (!wait_bounded(smem_u32(&empty[stage]), phase ^ 1, abort_flag, p.wait_limit)) {
                         raise(p, abort_flag);
@@ -236,194 +273,148 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             // every load of the pair lands before either CTA leaves
+#pragma unroll 1
             for (int s = 0; s < kStages; ++s)
                 if (filled & (1u << s))
                     drain_wait(smem_u32(&full[s]), (fill_parity >> s) & 1u, p.wait_limit);
-        } else if (warp == 1 && lane == 0 && leader) {
+        } else if ((warp == 1 || warp == 3) && leader) {
             // -------------------------------------------------------- MMA issue (leader)
+            // Warps 1 and 3 take the even and odd K blocks (counted over the pair's
+            // tiles).  What a block costs its warp beside the MMAs (waits, commits,
+            // loop) is longer than the 128 cycles that the tensor core's queue covers,
+            // so each warp pays it while the other's MMAs run.  The whole warp runs the
+            // loop, lanes polling different barriers at once and operands in uniform
+            // registers; one lane issues.
+            const int par = warp >> 1;
             const uint32_t idesc = idesc_f16_f32(kTile, kTile) | p.idesc_bits;
             const DescWords da = desc_words(smem_u32(as), false), db = desc_words(smem_u32(bs), false);
-            int stage = 0, buf = 0;
+            const uint32_t d = tmem_base + static_cast<uint32_t>(par * kTile);
+            const uint32_t te = smem_u32(&tempty[par]), tf = smem_u32(&tfull[par]);
+            int stage = par;
             uint32_t phase = 0, tphase = 0;
-            bool ok = true, skip_release = p.fault == 2 && blockIdx.x == 0;
-            for (int t = pair; ok && t < p.num_tiles; t += pairs) {
-                for (int kb = 0; kb < p.num_kb; ++kb) {
-                    if (!wait_bounded(smem_u32(&tempty[buf]), tphase ^ 1, abort_flag, p.wait_limit) ||
-                        !wait_bounded(smem_u32(&full[stage]), phase, abort_flag, p.wait_limit)) {
-                        raise(p, abort_flag);
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    const uint32_t d = tmem_base + static_cast<uint32_t>(buf * kTile);
-                    const uint32_t alo = da.lo + stage * (kOpBytes >> 4), blo = db.lo + stage * (kOpBytes >> 4);
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        tc_mma_pair_w<true>(d, alo + k * da.kstep, da.hi, blo + k * db.kstep, db.hi, idesc, k > 0);
-                    if (!skip_release)
-                        tc_commit_pair_mc(smem_u32(&empty[stage]), 0x3);
-                    skip_release = false;
-                    tc_commit_pair_mc(smem_u32(&tfull[buf]), 0x3);
-                    if (++stage == kStages) {
-                        stage = 0;
-                        phase ^= 1;
-                    }
-                    buf ^= 1;
-                    tphase ^= buf == 0;
-                }
-            }
-            // no MMA may still be running when Tensor Memory is released
-            tc_commit_pair(smem_u32(drain));
-            drain_wait(smem_u32(drain), 0, p.wait_limit);
-        } else if (warp == 2) {
-            // -------------------------------------------------------- scales (each CTA its rows)
-            // Rows and columns outside Out multiply zeros and are not stored;
-            // they take the last row's scale.  The loads of kScaleBatch K blocks
-            // are in flight together.
-            constexpr int NB = BROW ? 8 : 2;
-            int slot = 0;
-            uint32_t phase = 0;
-            bool ok = true;
-            for (int t = pair; ok && t < p.num_tiles; t += pairs) {
-                int b, m0, n0;
-                decode(p, t, b, m0, n0);
-                m0 += static_cast<int>(rank) * BM;
-                for (int kb0 = 0; ok && kb0 < p.num_kb; kb0 += kScaleBatch) {
-                    float va[kScaleBatch][4], vb[kScaleBatch][NB];
-#pragma unroll
-                    for (int i = 0; i < kScaleBatch; ++i) {
-                        const int kb = min(kb0 + i, p.num_kb - 1);
-#pragma unroll
-                        for (int r = 0; r < 4; ++r)
-                            va[i][r] = scale_at(p.sa, b, min(m0 + 32 * r + lane, p.M - 1), kb);
-#pragma unroll
-                        for (int r = 0; r < NB; ++r)
-                            vb[i][r] = scale_at(p.sb, b, min(BROW ? n0 + 32 * r + lane : n0 + 128 * r, p.N - 1), kb);
-                    }
-#pragma unroll
-                    for (int i = 0; i < kScaleBatch; ++i) {
-                        if (ok && kb0 + i < p.num_kb) {
-                            if (!wait_bounded(smem_u32(&sempty[slot]), phase ^ 1, abort_flag, p.wait_limit)) {
-                                raise(p, abort_flag);
-                                ok = false;
-                            } else {
-                                float* s = scales + slot * kScaleFloats;
-#pragma unroll
-                                for (int r = 0; r < 4; ++r) {
-                                    if (BROW) {
-                                        s[32 * r + lane] = va[i][r];
-                                    } else {
-                                        s[128 + 32 * r + lane] = va[i][r] * vb[i][0];
-                                        s[256 + 32 * r + lane] = va[i][r] * vb[i][1];
-                                    }
-                                }
-                                if (BROW) {
-#pragma unroll
-                                    for (int r = 0; r < NB; ++r)
-                                        s[128 + 32 * r + lane] = vb[i][r];
-                                }
-                                mbar_arrive(smem_u32(&sfull[slot]));
-                                if (++slot == kScaleRing) {
-                                    slot = 0;
-                                    phase ^= 1;
-                                }
-                            }
-                        }
-                    }
-                }
-            }
-        }
-    } else {
-        // ------------------------------------------------------------ promotion (both CTAs)
-        regs_promotion();
-        const int q = warp & 3, ch = (warp - 4) >> 2;  // lane quadrant, column half
-        int slot = 0, buf = 0;
-        uint32_t sphase = 0, tphase = 0;
-        bool ok = true;
-        for (int t = pair; ok && t < p.num_tiles; t += pairs) {
-            uint64_t acc[4][2][2][4];
-#pragma unroll
-            for (int c = 0; c < 4; ++c)
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-#pragma unroll
-                    for (int v = 0; v < 2; ++v)
-#pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            acc[c][h][v][j] = 0;
-            for (int kb = 0; kb < p.num_kb; ++kb) {
-                if (!wait_bounded(smem_u32(&sfull[slot]), sphase, abort_flag, p.wait_limit)) {
+            bool skip_release = p.fault == 2 && blockIdx.x == 0 && par == 0;
+            const bool chosen = elect_one();
+#pragma unroll 1
+            for (int n = blocks_of(p, pair, pairs) - par; n > 0; n -= 2) {
+                const uint32_t fa = smem_u32(&full[stage]), ea = smem_u32(&empty[stage]);
+                const uint32_t alo = da.lo + static_cast<uint32_t>(stage * (kOpBytes >> 4));
+                const uint32_t blo = db.lo + static_cast<uint32_t>(stage * (kOpBytes >> 4));
+                // even lanes: the accumulator is free; odd lanes: the operands are here
+                if (!wait_lanes(lane & 1 ? fa : te, lane & 1 ? phase : tphase ^ 1, abort_flag, p.wait_limit)) {
                     raise(p, abort_flag);
-                    ok = false;
-                    break;
-                }
-                const float* s = scales + slot * kScaleFloats;
-                uint64_t sr[2][2];  // the thread's 4 rows' scales, twice each
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-#pragma unroll
-                    for (int v = 0; v < 2; ++v) {
-                        const float f = s[(BROW ? 0 : 128 + 128 * ch) + 32 * q + 16 * h + 8 * v + (lane >> 2)];
-                        sr[h][v] = pack2(f, f);
-                    }
-                const uint64_t* sc = reinterpret_cast<const uint64_t*>(s + 128 + 128 * ch) + (lane & 3);
-                if (!wait_bounded(smem_u32(&tfull[buf]), tphase, abort_flag, p.wait_limit)) {
-                    raise(p, abort_flag);
-                    ok = false;
                     break;
                 }
                 tc_fence_after();
-                const uint32_t ta = tmem_base + static_cast<uint32_t>(buf * kTile + 128 * ch) +
-                                    (static_cast<uint32_t>(32 * q) << 16);
-                // the next 16 x 32 chunk's load runs under the arithmetic of this one
-                uint32_t x[2][16];
-                tmem_ld16x256_x4(ta, x[0]);
+                if (chosen) {
 #pragma unroll
-                for (int u = 0; u < 8; ++u) {
-                    const int c = u >> 1, h = u & 1;
-                    tmem_wait(x[u & 1]);
-                    if (u < 7) {
-                        tmem_ld16x256_x4(ta + 32 * ((u + 1) >> 1) + (((u + 1) & 1) ? 16u << 16 : 0u), x[(u + 1) & 1]);
-                    } else {
-                        // the accumulator is in registers: free it for block kb + 2
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0)
-                            mbar_arrive_cluster(mapa_shared(smem_u32(&tempty[buf]), 0));
-                    }
+                    for (int k = 0; k < 4; ++k)
+                        tc_mma_pair_w<true>(d, alo + k * da.kstep, da.hi, blo + k * db.kstep, db.hi, idesc, k > 0);
+                    tc_commit_pair_mc(tf, 0x3);
+                    if (!skip_release)
+                        tc_commit_pair_mc(ea, 0x3);
+                }
+                __syncwarp();
+                skip_release = false;
+                tphase ^= 1;
+                stage += 2;
+                if (stage >= kStages) {
+                    stage -= kStages;
+                    phase ^= 1;
+                }
+            }
+            // no MMA may still be running when Tensor Memory is released
+            if (chosen) {
+                tc_commit_pair(smem_u32(&drain[par]));
+                drain_wait(smem_u32(&drain[par]), 0, p.wait_limit);
+            }
+        } else if (warp == 2) {
+            load_scales<BROW>(p, static_cast<int>(rank), scales, sfull, sempty, abort_flag, pair, pairs);
+        }
+    } else {
+        // ------------------------------------------------------------ promotion (both CTAs)
+        regs_take<216>();
+        // Lane quadrant q, columns [128cq, 128cq + 128): pieces of 32 columns in two
+        // register buffers, a piece's load under the arithmetic of the piece before.
+        const int q = warp & 3, cq = (warp - 4) >> 2;
+        const uint32_t tmem_warp = tmem_base + static_cast<uint32_t>(128 * cq) + (static_cast<uint32_t>(32 * q) << 16);
+        const uint32_t my_scales = smem_u32(scales) + (32 * q + lane) * 4;
+        const uint32_t col_scales = smem_u32(scales) + (128 + (BROW ? 128 * cq : cq)) * 4;
+        const uint32_t tf0 = smem_u32(tfull), sf0 = smem_u32(sfull);
+        const uint32_t te0 = mapa_shared(smem_u32(tempty), 0);
+        const int blocks = blocks_of(p, pair, pairs);
+        int n = 0;  // K blocks so far: ring positions and phases follow from it
+        bool ok = true;
+        while (ok && n < blocks) {
+            uint64_t acc[kCols / 2];
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const uint64_t cs = BROW ? sc[16 * c + 4 * j] : 0;
+            for (int j = 0; j < kCols / 2; ++j)
+                acc[j] = 0;
+            int left = p.num_kb;
+#pragma unroll 1
+            do {
+                if (n % kScaleGroup == 0)
+                    ok &= wait_bounded(sf0 + n / kScaleGroup % kScaleRing * 8, n / (kScaleGroup * kScaleRing) & 1, abort_flag,
+                                       p.wait_limit);
+                const uint32_t so = n % (kScaleGroup * kScaleRing) * (kScaleFloats * 4);
+                const float fa = lds_f32(my_scales + so), fb = BROW ? 1.f : lds_f32(col_scales + so);
+                ok &= wait_bounded(tf0 + (n & 1) * 8, n >> 1 & 1, abort_flag, p.wait_limit);
+                tc_fence_after();
+                const uint32_t ta = tmem_warp + (n & 1) * kTile;
+                uint64_t sr = 0;
 #pragma unroll
-                        for (int v = 0; v < 2; ++v) {
-                            uint64_t part = pack2u(x[u & 1][4 * j + 2 * v], x[u & 1][4 * j + 2 * v + 1]);
-                            if (BROW)
-                                part = mul2(part, cs);
-                            acc[c][h][v][j] = fma2(part, sr[h][v], acc[c][h][v][j]);
+                for (int g = 0; g < kCols / kPiece; g += 2) {
+                    uint32_t x[2][kPiece];
+                    tmem_ld(ta + kPiece * g, x[0]);
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        uint32_t(&z)[kPiece] = x[c];
+                        tmem_wait(z);
+                        if (c == 0) {
+                            tmem_ld(ta + kPiece * (g + 1), x[1]);
+                        } else if (g + 2 == kCols / kPiece) {
+                            // the accumulator is in registers: free it for block n + 2
+                            tc_fence_before();
+                            if (lane == 0)
+                                mbar_arrive_cluster(te0 + (n & 1) * 8);
+                        }
+                        if (g == 0 && c == 0) {
+                            const float f = BROW ? fa : fa * fb;
+                            sr = pack2(f, f);
+                        }
+#pragma unroll
+                        for (int j = 0; j < kPiece / 4; ++j) {
+                            uint64_t p0 = pack2u(z[4 * j], z[4 * j + 1]), p1 = pack2u(z[4 * j + 2], z[4 * j + 3]);
+                            if (BROW) {
+                                const ulonglong2 w = lds_f32x4(col_scales + so + (kPiece * (g + c) + 4 * j) * 4);
+                                p0 = mul2(p0, w.x);
+                                p1 = mul2(p1, w.y);
+                            }
+                            uint64_t* d = acc + kPiece / 2 * (g + c) + 2 * j;
+                            d[0] = fma2(p0, sr, d[0]);
+                            d[1] = fma2(p1, sr, d[1]);
                         }
                     }
                 }
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive(smem_u32(&sempty[slot]));
-                if (++slot == kScaleRing) {
-                    slot = 0;
-                    sphase ^= 1;
+                if (n % kScaleGroup == kScaleGroup - 1) {
+                    __syncwarp();
+                    mbar_arrive_if(smem_u32(&sempty[n / kScaleGroup % kScaleRing]), lane == 0);
                 }
-                buf ^= 1;
-                tphase ^= buf == 0;
-            }
-            if (!ok)
+                ++n;
+            } while (--left > 0 && ok);
+            if (!ok) {
+                raise(p, abort_flag);
                 break;
+            }
             int b, m0, n0;
-            decode(p, t, b, m0, n0);
-            const int row0 = m0 + static_cast<int>(rank) * BM + 32 * q, col0 = n0 + 128 * ch;
+            decode(p, pair + (n / p.num_kb - 1) * pairs, b, m0, n0);
+            const int row0 = m0 + static_cast<int>(rank) * BM + 32 * q, col0 = n0 + 128 * cq;
+            uint32_t* stage_buf = staging + (warp - 4) * kStageWords;
             if (p.out_type == kOutF16)
-                store_tile<kOutF16>(p, acc, b, row0, col0, lane);
+                store_tile<kOutF16>(p, acc, stage_buf, b, row0, col0, lane);
             else if (p.out_type == kOutBF16)
-                store_tile<kOutBF16>(p, acc, b, row0, col0, lane);
+                store_tile<kOutBF16>(p, acc, stage_buf, b, row0, col0, lane);
             else
-                store_tile<kOutF32>(p, acc, b, row0, col0, lane);
+                store_tile<kOutF32>(p, acc, stage_buf, b, row0, col0, lane);
         }
     }
 

@@ -25,6 +25,8 @@ namespace {
 using namespace blk;
 using tc::BM;
 
+constexpr int kThreads = 384;   // warps 0-3: producer, MMA, scales, idle; warps 4-11: promotion
+constexpr int kPromoWarps = 8;
 constexpr int kAcc = 4;         // accumulators in Tensor Memory
 constexpr int kScaleRing = 8;
 constexpr int kScaleBatch = 4;

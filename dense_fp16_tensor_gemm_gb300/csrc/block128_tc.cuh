@@ -9,8 +9,6 @@
 namespace gnt {
 namespace blk {
 
-constexpr int kThreads = 384;     // warps 0-3: producer, MMA, scales, idle; warps 4-11: promotion
-constexpr int kPromoWarps = 8;
 constexpr int kRowBytes = 128;    // one K block of an operand row
 
 // Two fp32 operations in one instruction (each rounded to nearest even).
@@ -43,28 +41,80 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b)
     return r;
 }
 
-// tcgen05.ld 16x256b.x4 as tmem_ld16x256_x4_wait, without the wait: r may be
-// used only after tmem_wait(r).
-__device__ __forceinline__ void tmem_ld16x256_x4(uint32_t taddr, uint32_t (&r)[16])
+// 32 lanes x 16 columns with the wait, as tmem_ld32_wait; and that one under the same name.
+__device__ __forceinline__ void tmem_load_wait(uint32_t taddr, uint32_t (&r)[16])
 {
     asm volatile(
-        "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
-        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
         : "r"(taddr)
         : "memory");
 }
+__device__ __forceinline__ void tmem_load_wait(uint32_t taddr, uint32_t (&r)[32]) { tmem_ld32_wait(taddr, r); }
 
-// Waits for this thread's Tensor Memory loads; names the registers so that no
-// use of them is scheduled before it.
+// The load alone: r may be used only after tmem_wait(r), which waits for all of this
+// thread's loads and names the registers so that no use of them is scheduled before it.
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[16])
+{
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
+        : "memory");
+}
 __device__ __forceinline__ void tmem_wait(uint32_t (&r)[16])
 {
     asm volatile("tcgen05.wait::ld.sync.aligned;"
-                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
-                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
-                 :
-                 : "memory");
+        : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+          "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+        :
+        : "memory");
+}
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[32])
+{
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_wait(uint32_t (&r)[32])
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+        : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+          "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
+          "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
+          "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+        :
+        : "memory");
+}
+
+// Shared-memory loads by 32-bit address.
+__device__ __forceinline__ float lds_f32(uint32_t a)
+{
+    float v;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ ulonglong2 lds_f32x4(uint32_t a)
+{
+    ulonglong2 v;
+    asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(v.x), "=l"(v.y) : "r"(a) : "memory");
+    return v;
+}
+
+// mbar_arrive of the lanes whose predicate holds, without a branch.
+__device__ __forceinline__ void mbar_arrive_if(uint32_t bar, bool pred)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %1, 0;\n\t@p mbarrier.arrive.shared::cta.b64 _, [%0];\n\t}" ::"r"(bar),
+        "r"(static_cast<uint32_t>(pred))
+        : "memory");
 }
 
 // 32 lanes x 8 columns: thread i of the warp receives TMEM lane (lane field) + i.
@@ -83,11 +133,18 @@ __device__ __forceinline__ void tmem_wait8(uint32_t* r)
                  : "memory");
 }
 
-// Register hand-over: the kernels launch 384 threads with 168 registers each;
-// the utility warpgroup keeps 104 and the two promotion warpgroups take 200:
-// 104 + 2 * 200 = 504 = 3 * 168.
-__device__ __forceinline__ void regs_utility() { asm volatile("setmaxnreg.dec.sync.aligned.u32 104;"); }
-__device__ __forceinline__ void regs_promotion() { asm volatile("setmaxnreg.inc.sync.aligned.u32 200;"); }
+// Register hand-over between the warpgroups of a CTA: what the takers gain must
+// come from what the givers return of the registers the CTA was launched with.
+template <int N>
+__device__ __forceinline__ void regs_give()
+{
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_take()
+{
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
 
 __device__ __forceinline__ void raise(const BlkParams& p, volatile int* abort_flag)
 {
@@ -100,13 +157,117 @@ __device__ __forceinline__ void raise(const BlkParams& p, volatile int* abort_fl
 __device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity, const volatile int* abort_flag,
                                              unsigned long long limit)
 {
-    if (mbar_try_wait(bar, parity))
+    if (__builtin_expect(mbar_try_wait(bar, parity), 1))
         return true;
     const long long t0 = clock64();
     while (!mbar_try_wait_sleep(bar, parity, 1000000u))
         if (*abort_flag || static_cast<unsigned long long>(clock64() - t0) > limit)
             return false;
     return true;
+}
+
+// A whole warp waits, each lane on a barrier and phase of its own; true once all
+// have completed.
+__device__ __forceinline__ bool wait_lanes(uint32_t bar, uint32_t parity, const volatile int* abort_flag,
+                                           unsigned long long limit)
+{
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity)))
+        return true;
+    const long long t0 = clock64();
+    while (!__all_sync(0xffffffffu, mbar_try_wait_sleep(bar, parity, 1000000u)))
+        if (__any_sync(0xffffffffu, *abort_flag || static_cast<unsigned long long>(clock64() - t0) > limit))
+            return false;
+    return true;
+}
+
+// One lane of a converged warp, the same at every call.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.b32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0;
+}
+
+// ---------------------------------------------------------------- scales
+__device__ __forceinline__ void cp_async4(uint32_t dst, const float* src)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async16(uint32_t dst, const float* src)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+// One of the barrier's expected arrivals, made when this thread's copies so far have landed.
+__device__ __forceinline__ void cp_async_arrive(uint32_t bar)
+{
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
+// The scales of 32*R rows from `first` (or, step 128, of one in 128 rows in the
+// first lanes), copied K block by K block by one warp.  Where the rows' scales
+// are adjacent and on 16-byte boundaries (as the quantiser leaves them when the
+// number of rows is a multiple of 4), 128 rows take one instruction, else four.
+template <int R>
+struct ScaleRun {
+    const float* src[R];
+    int64_t step;
+    bool wide;
+    uint32_t off;
+
+    __device__ __forceinline__ ScaleRun(const ScaleView& v, int b, int first, int rows, int every = 1)
+    {
+        const int lane = threadIdx.x & 31;
+        const float* base = v.data + b * v.bs;
+        step = v.ks;
+        wide = R % 4 == 0 && every == 1 && v.shift == 0 && v.rs == 1 && v.ks % 4 == 0 && first + 32 * R <= rows &&
+               (reinterpret_cast<uintptr_t>(base + first) & 15) == 0;
+        off = static_cast<uint32_t>(wide ? 16 * lane : 4 * lane);
+        if (wide) {
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+                src[r] = base + first + 128 * r + 4 * lane;  // only the first R / 4 are used
+        } else {
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                const int row = min(first + (every == 1 ? 32 * r + lane : every * (lane & 1)), rows - 1);
+                src[r] = base + static_cast<int64_t>(row >> v.shift) * v.rs;
+            }
+        }
+    }
+
+    // The next K block's scales to shared address `dst`.
+    __device__ __forceinline__ void copy(uint32_t dst)
+    {
+        dst += off;
+        if (wide) {
+#pragma unroll
+            for (int r = 0; r < R / 4; ++r) {
+                cp_async16(dst + 512 * r, src[r]);
+                src[r] += step;
+            }
+        } else {
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                cp_async4(dst + 128 * r, src[r]);
+                src[r] += step;
+            }
+        }
+    }
+};
+
+// True if the phase with the given parity has completed; never suspends.
+__device__ __forceinline__ bool mbar_test_wait(uint32_t bar, uint32_t parity)
+{
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.b32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
 }
 
 // Waits (with the limit) without giving up early: for drains before exit.
