@@ -389,38 +389,63 @@ def gemm_nt_batched(A, B, out=None, path=Path.AUTO, stream=None, out_dtype=None)
 
 
 # ---------------------------------------------------------------- one scale per block of 128
-def _type_code(dtype, allowed, what):
-    import torch
-    codes = {torch.float16: DType.F16, torch.bfloat16: DType.BF16, torch.float32: DType.F32,
-             torch.float8_e4m3fn: DType.E4M3, torch.float8_e5m2: DType.E5M2}
-    if dtype not in codes or codes[dtype] not in allowed:
-        raise TypeError("%s must be one of %s" % (what, ", ".join(a.name for a in allowed)))
-    return codes[dtype]
+# These calls serve single tokens, where the host's time per call counts: types
+# are looked up once, the stream handle is read without building a Stream object,
+# and an output is one allocation.
+_torch = None
+_CODES = {}     # torch dtype -> gemm_dtype_t value
+_IN_F8 = _OUT = _X16 = ()
 
 
-def _keep(t, stream):
-    """A temporary that work on `stream` still reads: torch's allocator must not
-    hand its memory to another stream before that work is done."""
+def _init_torch():
+    global _torch, _IN_F8, _OUT, _X16
     import torch
-    if stream is not None and t is not None:
-        handle = _stream_handle(stream)
-        if handle != torch.cuda.current_stream().cuda_stream:
-            t.record_stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(handle))
-    return t
+    _CODES.update({torch.float16: 0, torch.bfloat16: 1, torch.float32: 2, torch.float8_e4m3fn: 3,
+                   torch.float8_e5m2: 4})
+    _IN_F8 = (torch.float8_e4m3fn, torch.float8_e5m2)
+    _OUT = (torch.float32, torch.float16, torch.bfloat16)
+    _X16 = (torch.float16, torch.bfloat16)
+    _torch = torch
+    return torch
+
+
+def _one_of(dtype, allowed, what):
+    if dtype not in allowed:
+        raise TypeError("%s must be one of %s" % (what, ", ".join(str(a).replace("torch.", "") for a in allowed)))
+    return _CODES[dtype]
+
+
+def _stream_of(stream, device):
+    """The handle of `stream`, or of torch's current stream on the device."""
+    if stream is None and device.type == "cuda":
+        return _torch._C._cuda_getCurrentRawStream(device.index)
+    return _stream_handle(stream)
+
+
+def _keep(tensors, stream):
+    """Temporaries that work on `stream` still reads: torch's allocator must not
+    hand their memory to another stream before that work is done."""
+    if stream is None:
+        return
+    handle = _stream_handle(stream)
+    if handle != _torch.cuda.current_stream().cuda_stream:
+        s = stream if isinstance(stream, _torch.cuda.Stream) else _torch.cuda.ExternalStream(handle)
+        for t in tensors:
+            t.record_stream(s)
 
 
 def _scale128(S, rows, K, name):
     """A scale tensor (rows or ceil(rows/128), ceil(K/128)), optionally with a
     leading batch dimension, as the C struct."""
-    import torch
-    if S.dtype != torch.float32:
+    if S.dtype != _torch.float32:
         raise TypeError("%s must be float32" % name)
-    kb = (K + 127) // 128
-    if S.dim() not in (2, 3) or S.shape[-1] != kb or S.shape[-2] not in (rows, (rows + 127) // 128):
+    shape, strides = S.shape, S.stride()
+    n, kb = shape[-2], (K + 127) // 128
+    if len(shape) not in (2, 3) or shape[-1] != kb or n not in (rows, (rows + 127) // 128):
         raise ValueError("%s: (%d or %d, %d) scales for %d rows and K = %d"
                          % (name, rows, (rows + 127) // 128, kb, rows, K))
-    return Scale128(S.data_ptr(), 1 if S.shape[-2] == rows else 128, S.stride(-2), S.stride(-1),
-                    S.stride(0) if S.dim() == 3 and S.shape[0] > 1 else 0)
+    return Scale128(S.data_ptr(), 1 if n == rows else 128, strides[-2], strides[-1],
+                    strides[0] if len(shape) == 3 and shape[0] > 1 else 0)
 
 
 def gemm_nt_block128_tensors(A, SA, B, SB, out=None, path=Path.AUTO, stream=None, out_dtype=None):
@@ -432,71 +457,77 @@ def gemm_nt_block128_tensors(A, SA, B, SB, out=None, path=Path.AUTO, stream=None
     (stride 0 shares an operand), a batch of products.  ``out``/``out_dtype`` as
     in :func:`gemm_nt`, float32 by default.
     """
-    import torch
-    if A.dim() not in (2, 3) or B.dim() != A.dim() or A.shape[-1] != B.shape[-1] or A.shape[:-2] != B.shape[:-2] \
-            or SA.dim() != A.dim() or SB.dim() != A.dim() or SA.shape[:-2] != A.shape[:-2] \
-            or SB.shape[:-2] != A.shape[:-2]:
+    torch = _torch or _init_torch()
+    ash, bsh = A.shape, B.shape
+    batched = len(ash) == 3
+    if not (batched or len(ash) == 2) or len(bsh) != len(ash) or ash[-1] != bsh[-1] or SA.dim() != len(ash) \
+            or SB.dim() != len(ash) or batched and not ash[0] == bsh[0] == SA.shape[0] == SB.shape[0]:
         raise ValueError("shapes: A (M,K), B (N,K) and their scales, or the same with a leading batch dimension")
     if A.dtype != B.dtype:
         raise TypeError("A and B must have the same type")
-    ab = _type_code(A.dtype, (DType.E4M3, DType.E5M2), "A and B")
+    ab = _one_of(A.dtype, _IN_F8, "A and B")
     dt = out.dtype if out is not None else (out_dtype or torch.float32)
-    ot = _type_code(dt, (DType.F32, DType.F16, DType.BF16), "out")
-    M, K = A.shape[-2:]
-    N = B.shape[-2]
-    shape = tuple(A.shape[:-2]) + (M, N)
+    ot = _one_of(dt, _OUT, "out")
+    M, K = ash[-2:]
+    N = bsh[-2]
+    shape = (ash[0], M, N) if batched else (M, N)
     if out is None:
         out = torch.empty(shape, dtype=dt, device=A.device)
-    if tuple(out.shape) != shape:
+    elif tuple(out.shape) != shape:
         raise ValueError("out must have shape (M,N), with A's batch dimension")
-    sa, sb = _scale128(SA, M, K, "SA"), _scale128(SB, N, K, "SB")
-    batched = A.dim() == 3
-    gemm_nt_block128(A.data_ptr(), sa, B.data_ptr(), sb, out.data_ptr(), ab, ot, M, N, K, _matrix_ld(A, "A"),
-                     _matrix_ld(B, "B"), _matrix_ld(out, "out"), A.stride(0) if batched else 0,
-                     B.stride(0) if batched else 0, out.stride(0) if batched else 0, A.shape[0] if batched else 1,
-                     path, _stream_handle(stream))
+    gemm_nt_block128(A.data_ptr(), _scale128(SA, M, K, "SA"), B.data_ptr(), _scale128(SB, N, K, "SB"), out.data_ptr(),
+                     ab, ot, M, N, K, _matrix_ld(A, "A"), _matrix_ld(B, "B"), _matrix_ld(out, "out"),
+                     A.stride(0) if batched else 0, B.stride(0) if batched else 0, out.stride(0) if batched else 0,
+                     ash[0] if batched else 1, path, _stream_of(stream, A.device))
     return out
+
+
+def _quantized(rows, cols, q_dtype, block_rows, device):
+    """Empty codes and scales for a (rows, cols) matrix, the codes' pitch, and
+    the scales as the C struct.  Rows of codes, and columns of single rows'
+    scales, start on 16-byte boundaries, as the products read them fastest."""
+    pitch, kb = (cols + 15) // 16 * 16, (cols + 127) // 128
+    q = _torch.empty_strided((rows, cols), (pitch, 1), dtype=q_dtype, device=device)
+    if block_rows == 1:
+        n, strides = rows, (1, (rows + 3) // 4 * 4)
+    else:
+        n, strides = (rows + 127) // 128, (kb, 1)
+    s = _torch.empty_strided((n, kb), strides, dtype=_torch.float32, device=device)
+    return q, s, pitch, Scale128(s.data_ptr(), block_rows, strides[0], strides[1], 0)
 
 
 def quantize_block128(X, q_dtype=None, block_rows=1, transposed=False, stream=None):
     """8-bit codes and fp32 scales of X (rows, cols; float32, float16 or
     bfloat16), one scale for each 1 x 128 (``block_rows`` 1) or 128 x 128 (128)
-    block: a = max(max |x|, 2^-100), scale = a / F, code = x * (F / a) rounded to
-    ``q_dtype`` (float8_e4m3fn by default, or float8_e5m2), F its largest value.
+    block: a = max(max |x|, 2^-100), scale = a * (1/F), code = x * (F * (1/a))
+    rounded to ``q_dtype`` (float8_e4m3fn by default, or float8_e5m2), F its
+    largest value.
 
     Returns ``(Q, S)``, or with ``transposed`` ``(Q, S, QT, ST)`` from one read
     of X: QT (cols, rows) is X transposed, quantised in blocks of its own rows.
     Rows of the codes start on 16-byte boundaries; scales of single rows are
-    stored with the rows adjacent (strides (1, rows)).
+    stored with the rows adjacent.
     """
-    import torch
+    torch = _torch or _init_torch()
     if X.dim() != 2:
         raise ValueError("X must be a matrix")
     if block_rows not in (1, 128):
         raise ValueError("block_rows must be 1 or 128")
     q_dtype = q_dtype or torch.float8_e4m3fn
-    qt_code = _type_code(q_dtype, (DType.E4M3, DType.E5M2), "q_dtype")
-    xt = _type_code(X.dtype, (DType.F32, DType.F16, DType.BF16), "X")
+    code = _one_of(q_dtype, _IN_F8, "q_dtype")
+    xt = _one_of(X.dtype, _OUT, "X")
     ldx = _matrix_ld(X, "X")
     rows, cols = X.shape
-
-    def outputs(r, c):
-        q = torch.empty((r, (c + 15) // 16 * 16), dtype=torch.uint8, device=X.device).view(q_dtype)[:, :c]
-        kb = (c + 127) // 128
-        if block_rows == 1:
-            s = torch.empty((kb, r), dtype=torch.float32, device=X.device).t()
-        else:
-            s = torch.empty(((r + 127) // 128, kb), dtype=torch.float32, device=X.device)
-        return q, s, max(q.stride(0), 1), Scale128(s.data_ptr(), block_rows, s.stride(0), s.stride(1), 0)
-
-    q, s, ldq, sq = outputs(rows, cols)
-    qt = st = stc = None
-    ldqt = 0
-    if transposed:
-        qt, st, ldqt, stc = outputs(cols, rows)
-    gemm_nt_block128_quantize(X.data_ptr(), xt, rows, cols, ldx, q.data_ptr(), ldq, sq,
-                              qt.data_ptr() if transposed else 0, ldqt, stc, qt_code, _stream_handle(stream))
-    return (q, s, qt, st) if transposed else (q, s)
+    device = X.device
+    q, s, ldq, sq = _quantized(rows, cols, q_dtype, block_rows, device)
+    if not transposed:
+        gemm_nt_block128_quantize(X.data_ptr(), xt, rows, cols, ldx, q.data_ptr(), ldq, sq, 0, 0, None, code,
+                                  _stream_of(stream, device))
+        return q, s
+    qt, st, ldqt, sqt = _quantized(cols, rows, q_dtype, block_rows, device)
+    gemm_nt_block128_quantize(X.data_ptr(), xt, rows, cols, ldx, q.data_ptr(), ldq, sq, qt.data_ptr(), ldqt, sqt, code,
+                              _stream_of(stream, device))
+    return q, s, qt, st
 
 
 def linear_block128(X, W, SW, stream=None):
@@ -507,7 +538,7 @@ def linear_block128(X, W, SW, stream=None):
     bits)."""
     q, s, qt, st = quantize_block128(X, W.dtype, transposed=True, stream=stream)
     y = gemm_nt_block128_tensors(q, s, W, SW, out_dtype=X.dtype, stream=stream)
-    _keep(q, stream), _keep(s, stream)
+    _keep((q, s), stream)
     return y, (qt, st)
 
 
@@ -520,9 +551,12 @@ def linear_block128_backward(dY, saved, WT, SWT, stream=None):
     q, s, qt, st = quantize_block128(dY, WT.dtype, transposed=True, stream=stream)
     dx = gemm_nt_block128_tensors(q, s, WT, SWT, out_dtype=dY.dtype, stream=stream)
     dw = gemm_nt_block128_tensors(qt, st, qt_x, st_x, stream=stream)
-    for t in (q, s, qt, st, qt_x, st_x):
-        _keep(t, stream)
+    _keep((q, s, qt, st, qt_x, st_x), stream)
     return dx, dw
+
+
+_MOE_SHAPES = ("shapes: X (tokens, hidden), logits (tokens, experts), W13 (experts, 2*inner, hidden), "
+               "W2 (experts, hidden, inner)")
 
 
 def moe_few_tokens(X, logits, W13, W2, topk, S13=None, S2=None, renormalize=True, out=None, workspace=None,
@@ -537,38 +571,36 @@ def moe_few_tokens(X, logits, W13, W2, topk, S13=None, S2=None, renormalize=True
     otherwise over all of its experts.  ``workspace``, a uint8 tensor of
     :func:`gemm_nt_moe_workspace_bytes` bytes, is allocated if not given.
     """
-    import torch
+    torch = _torch or _init_torch()
     if X.dim() != 2 or logits.dim() != 2 or W13.dim() != 3 or W2.dim() != 3:
-        raise ValueError("shapes: X (tokens, hidden), logits (tokens, experts), W13 (experts, 2*inner, hidden), "
-                         "W2 (experts, hidden, inner)")
+        raise ValueError(_MOE_SHAPES)
     tokens, hidden = X.shape
     experts, inner = logits.shape[1], W2.shape[2]
-    if logits.shape[0] != tokens or tuple(W13.shape) != (experts, 2 * inner, hidden) or \
-            tuple(W2.shape) != (experts, hidden, inner):
-        raise ValueError("shapes: X (tokens, hidden), logits (tokens, experts), W13 (experts, 2*inner, hidden), "
-                         "W2 (experts, hidden, inner)")
-    xt = _type_code(X.dtype, (DType.F16, DType.BF16), "X")
+    if logits.shape[0] != tokens or W13.shape != (experts, 2 * inner, hidden) or W2.shape != (experts, hidden, inner):
+        raise ValueError(_MOE_SHAPES)
+    xt = _one_of(X.dtype, _X16, "X")
     if W13.dtype != W2.dtype:
         raise TypeError("W13 and W2 must have the same type")
-    wt = _type_code(W13.dtype, (xt, DType.E4M3), "W13 and W2")
+    wt = _one_of(W13.dtype, (X.dtype, torch.float8_e4m3fn), "W13 and W2")
     if logits.dtype != torch.float32:
         raise TypeError("logits must be float32")
-    if (wt == DType.E4M3) != (S13 is not None) or (S13 is None) != (S2 is None):
+    if (wt == 3) != (S13 is not None) or (S13 is None) != (S2 is None):
         raise ValueError("8-bit weights take S13 and S2, 16-bit weights none")
     if out is None:
         out = torch.empty((tokens, hidden), dtype=X.dtype, device=X.device)
-    if tuple(out.shape) != (tokens, hidden) or out.dtype != X.dtype:
+    elif tuple(out.shape) != (tokens, hidden) or out.dtype != X.dtype:
         raise ValueError("out must have X's shape and type")
     s13 = s2 = None
     if S13 is not None:
         if S13.dim() != 3 or S2.dim() != 3 or S13.shape[0] != experts or S2.shape[0] != experts:
             raise ValueError("S13 and S2 need a leading expert dimension")
         s13, s2 = _scale128(S13, 2 * inner, hidden, "S13"), _scale128(S2, hidden, inner, "S2")
-    need = gemm_nt_moe_workspace_bytes(tokens, topk, inner) if topk > 0 else 0
     if workspace is None:
-        workspace = _keep(torch.empty(max(need, 16), dtype=torch.uint8, device=X.device), stream)
+        need = gemm_nt_moe_workspace_bytes(tokens, topk, inner) if topk > 0 else 0
+        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=X.device)
+        _keep((workspace,), stream)
     gemm_nt_moe(X.data_ptr(), _matrix_ld(X, "X"), logits.data_ptr(), _matrix_ld(logits, "logits"), W13.data_ptr(),
                 _matrix_ld(W13, "W13"), W13.stride(0), s13, W2.data_ptr(), _matrix_ld(W2, "W2"), W2.stride(0), s2,
                 out.data_ptr(), _matrix_ld(out, "out"), xt, wt, tokens, experts, topk, hidden, inner, renormalize,
-                workspace.data_ptr(), workspace.numel(), _stream_handle(stream))
+                workspace.data_ptr(), workspace.numel(), _stream_of(stream, X.device))
     return out

@@ -12,10 +12,17 @@
 // they leave as whole rows of 128 bytes.  R = 8 (a 128 x 128 tile) when a
 // column or tile maximum is needed, else 2: four times the CTAs when few rows
 // are quantised for the next product.
+//
+// 16-bit inputs stay packed, two to a register, and their maxima are taken on
+// pairs (exact: a maximum rounds nothing); the registers saved make room for
+// half as many CTAs again, which is what keeps enough bytes in flight.  A block's factor
+// is computed by one lane and passed on: an fp32 reciprocal costs as much as
+// quantising 8 elements.
 #include <cuda_fp8.h>
 
 #include "gemm_nt.h"
 #include "block128.h"
+#include "ptx.cuh"
 
 namespace gnt {
 
@@ -29,41 +36,6 @@ __device__ __forceinline__ float max_nan(float a, float b)
     float r;
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
     return r;
-}
-
-template <int XT>
-__device__ __forceinline__ float load1(const void* x, int64_t i)
-{
-    if constexpr (XT == GEMM_DTYPE_F32)
-        return static_cast<const float*>(x)[i];
-    else if constexpr (XT == GEMM_DTYPE_F16)
-        return __half2float(static_cast<const __half*>(x)[i]);
-    else
-        return __bfloat162float(static_cast<const __nv_bfloat16*>(x)[i]);
-}
-
-// 8 consecutive elements from a 16-byte aligned place.
-template <int XT>
-__device__ __forceinline__ void load8(const void* x, int64_t i, float (&v)[8])
-{
-    if constexpr (XT == GEMM_DTYPE_F32) {
-        const float4* g = reinterpret_cast<const float4*>(static_cast<const float*>(x) + i);
-        const float4 a = __ldcs(g), b = __ldcs(g + 1);
-        v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-    } else {
-        const uint4 w = __ldcs(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(x) + i));
-        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            if constexpr (XT == GEMM_DTYPE_F16) {
-                const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&u[j]));
-                v[2 * j] = f.x, v[2 * j + 1] = f.y;
-            } else {
-                v[2 * j] = __uint_as_float(u[j] << 16);
-                v[2 * j + 1] = __uint_as_float(u[j] & 0xffff0000u);
-            }
-        }
-    }
 }
 
 template <bool E5M2>
@@ -80,124 +52,243 @@ __device__ __forceinline__ void store_bytes(uint8_t* d, const uint32_t* w, int n
         d[i] = static_cast<uint8_t>(w[i >> 2] >> (8 * (i & 3)));
 }
 
+// max of two pairs of 16-bit floats, keeping NaN; the arguments are magnitudes.
+template <int XT>
+__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b)
+{
+    uint32_t r;
+    if constexpr (XT == GEMM_DTYPE_F16)
+        asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    else
+        asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+template <int XT>
+__device__ __forceinline__ float2 widen(uint32_t w)
+{
+    if constexpr (XT == GEMM_DTYPE_F16)
+        return __half22float2(*reinterpret_cast<const __half2*>(&w));
+    else
+        return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+
+// A thread's R rows x 8 columns: fp32 values as they are, 16-bit ones packed.
+template <int XT, int R>
+struct Tile {
+    static constexpr bool WIDE = XT == GEMM_DTYPE_F32;
+    static constexpr int W = WIDE ? 8 : 4;  // words of a row
+    uint32_t v[R][W];
+
+    __device__ __forceinline__ void load(const QuantParams& p, int64_t row, int64_t col, int ncol)
+    {
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+#pragma unroll
+            for (int j = 0; j < W; ++j)
+                v[i][j] = 0;
+            if (row + i < p.rows) {
+                const int64_t at = (row + i) * p.ldx + col;
+                if (p.vec_x && ncol == 8) {
+                    const uint4* g = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p.x) + at * (WIDE ? 4 : 2));
+#pragma unroll
+                    for (int j = 0; j < W / 4; ++j) {
+                        const uint4 w = __ldcs(g + j);
+                        v[i][4 * j] = w.x, v[i][4 * j + 1] = w.y, v[i][4 * j + 2] = w.z, v[i][4 * j + 3] = w.w;
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        if (j < ncol) {
+                            if constexpr (WIDE)
+                                v[i][j] = static_cast<const uint32_t*>(p.x)[at + j];
+                            else
+                                v[i][j / 2] |= static_cast<uint32_t>(static_cast<const uint16_t*>(p.x)[at + j]) << (16 * (j & 1));
+                        }
+                }
+            }
+        }
+    }
+
+    __device__ __forceinline__ float get(int i, int j) const
+    {
+        if constexpr (WIDE) {
+            return __uint_as_float(v[i][j]);
+        } else {
+            const float2 f = widen<XT>(v[i][j / 2]);
+            return j & 1 ? f.y : f.x;
+        }
+    }
+
+    // Largest magnitude of each row over the 16 lanes that hold it.
+    __device__ __forceinline__ void row_max(float (&a)[R]) const
+    {
+        if constexpr (WIDE) {
+#pragma unroll
+            for (int i = 0; i < R; ++i) {
+                a[i] = 0.f;
+#pragma unroll
+                for (int j = 0; j < W; ++j)
+                    a[i] = max_nan(a[i], fabsf(__uint_as_float(v[i][j])));
+#pragma unroll
+                for (int s = 1; s < 16; s *= 2)
+                    a[i] = max_nan(a[i], __shfl_xor_sync(0xffffffffu, a[i], s));
+            }
+        } else {
+            constexpr uint32_t M = 0x7fff7fffu;
+#pragma unroll
+            for (int i = 0; i < R; i += 2) {  // two rows' maxima in one word
+                const uint32_t m0 = max2<XT>(max2<XT>(v[i][0] & M, v[i][1] & M), max2<XT>(v[i][2] & M, v[i][3] & M));
+                const uint32_t m1 =
+                    max2<XT>(max2<XT>(v[i + 1][0] & M, v[i + 1][1] & M), max2<XT>(v[i + 1][2] & M, v[i + 1][3] & M));
+                uint32_t m = max2<XT>(__byte_perm(m0, m1, 0x5410), __byte_perm(m0, m1, 0x7632));
+#pragma unroll
+                for (int s = 1; s < 16; s *= 2)
+                    m = max2<XT>(m, __shfl_xor_sync(0xffffffffu, m, s));
+                const float2 f = widen<XT>(m);
+                a[i] = f.x;
+                a[i + 1] = f.y;
+            }
+        }
+    }
+
+    // Largest magnitude of each column over the warp's rows, as stored: a word a
+    // column (fp32) or two columns.
+    __device__ __forceinline__ void col_max(uint32_t (&a)[W]) const
+    {
+#pragma unroll
+        for (int j = 0; j < W; ++j) {
+            if constexpr (WIDE) {
+                float m = 0.f;
+#pragma unroll
+                for (int i = 0; i < R; ++i)
+                    m = max_nan(m, fabsf(__uint_as_float(v[i][j])));
+                a[j] = __float_as_uint(max_nan(m, __shfl_xor_sync(0xffffffffu, m, 16)));
+            } else {
+                uint32_t m = 0;
+#pragma unroll
+                for (int i = 0; i < R; ++i)
+                    m = max2<XT>(m, v[i][j] & 0x7fff7fffu);
+                a[j] = max2<XT>(m, __shfl_xor_sync(0xffffffffu, m, 16));
+            }
+        }
+    }
+};
+
 // R: rows per thread (the CTA holds 16 R rows x 128 columns).  TILE: one scale
 // for the whole 128 x 128 tile.  Q / T: which orders are written.
 template <int XT, bool E5M2, int R, bool TILE, bool Q, bool T>
-__global__ void __launch_bounds__(256) quantize_kernel(const QuantParams p)
+__global__ void __launch_bounds__(256, XT == GEMM_DTYPE_F32 ? 2 : (R == 8 ? 3 : 4)) quantize_kernel(const QuantParams p)
 {
     static_assert(R == 8 || (!TILE && !T), "column and tile maxima need all 128 rows");
     constexpr float F = E5M2 ? 57344.f : 448.f;
     constexpr float kInvF = 1.f / F;
     constexpr int kPitchT = 128 + 16;
+    using D = Tile<XT, R>;
+    constexpr int CW = 16 * D::W;  // words of a warp's column maxima
     __shared__ __align__(16) uint8_t tq[T ? 128 * kPitchT : 16];
-    __shared__ float cmax[T || TILE ? 8 : 1][128];
-    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4, warp = threadIdx.x >> 5;
+    __shared__ uint32_t cmax[T || TILE ? 8 : 1][T || TILE ? CW : 1];
+    __shared__ __align__(16) float cfac[T || TILE ? 128 : 4];  // columns' factors (TILE: their maxima)
+    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t col0 = static_cast<int64_t>(blockIdx.x) * 128;
     const int64_t col = col0 + tx * 8;
     const int ncol = col < p.cols ? static_cast<int>(min(static_cast<int64_t>(8), p.cols - col)) : 0;
+    pdl_wait();
+    pdl_launch_dependents();
     for (int64_t row0 = static_cast<int64_t>(blockIdx.y) * (16 * R); row0 < p.rows;
          row0 += static_cast<int64_t>(gridDim.y) * (16 * R)) {
         const int64_t row = row0 + ty * R;
-        float v[R][8];
-#pragma unroll
-        for (int i = 0; i < R; ++i) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                v[i][j] = 0.f;
-            if (row + i < p.rows) {
-                if (p.vec_x && ncol == 8) {
-                    load8<XT>(p.x, (row + i) * p.ldx + col, v[i]);
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        if (j < ncol)
-                            v[i][j] = load1<XT>(p.x, (row + i) * p.ldx + col + j);
-                }
-            }
-        }
-        float ra[R];  // largest of each row's 128 columns, in every lane that holds the row
-        if (Q && !TILE) {
-#pragma unroll
-            for (int i = 0; i < R; ++i) {
-                float a = kFloor;
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    a = max_nan(a, fabsf(v[i][j]));
-                ra[i] = a;
-            }
-#pragma unroll
-            for (int s = 1; s < 16; s *= 2)
-#pragma unroll
-                for (int i = 0; i < R; ++i)
-                    ra[i] = max_nan(ra[i], __shfl_xor_sync(0xffffffffu, ra[i], s));
-        }
-        float ca[8];  // largest of each of the thread's 8 columns (TILE: all the same)
+        D d;
+        d.load(p, row, col, ncol);
         if (T || TILE) {
+            uint32_t m[D::W];
+            d.col_max(m);
+            if (lane < 16) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                float a = kFloor;
-#pragma unroll
-                for (int i = 0; i < R; ++i)
-                    a = max_nan(a, fabsf(v[i][j]));
-                ca[j] = max_nan(a, __shfl_xor_sync(0xffffffffu, a, 16));
-            }
-            if ((threadIdx.x & 16) == 0) {
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    cmax[warp][tx * 8 + j] = ca[j];
+                for (int j = 0; j < D::W; ++j)
+                    cmax[warp][tx * D::W + j] = m[j];
             }
             __syncthreads();
+            if (threadIdx.x < CW) {  // a word's columns: their maxima, factors and scales
+                uint32_t w = cmax[0][threadIdx.x];
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
+                for (int k = 1; k < 8; ++k) {
+                    const uint32_t u = cmax[k][threadIdx.x];
+                    if constexpr (D::WIDE)
+                        w = __float_as_uint(max_nan(__uint_as_float(w), __uint_as_float(u)));
+                    else
+                        w = max2<XT>(w, u);
+                }
+                float a[2];
+                if constexpr (D::WIDE) {
+                    a[0] = __uint_as_float(w);
+                } else {
+                    const float2 f = widen<XT>(w);
+                    a[0] = f.x, a[1] = f.y;
+                }
 #pragma unroll
-                for (int w = 0; w < 8; ++w)
-                    ca[j] = max_nan(ca[j], cmax[w][tx * 8 + j]);
-            if (TILE) {
-                float a = ca[0];
+                for (int e = 0; e < 128 / CW; ++e) {
+                    const int c = threadIdx.x * (128 / CW) + e;
+                    const float m1 = max_nan(a[e], kFloor);
+                    cfac[c] = TILE ? m1 : F * (1.f / m1);
+                    if (T && !TILE && col0 + c < p.cols)
+                        p.st[(col0 + c) * p.st_rs + row0 / 128 * p.st_ks] = m1 * kInvF;
+                }
+            }
+            __syncthreads();
+        }
+        float tile_factor = 0.f;
+        if (TILE) {
+            float a = max_nan(max_nan(cfac[lane], cfac[lane + 32]), max_nan(cfac[lane + 64], cfac[lane + 96]));
 #pragma unroll
-                for (int j = 1; j < 8; ++j)
-                    a = max_nan(a, ca[j]);
-#pragma unroll
-                for (int s = 1; s < 16; s *= 2)
-                    a = max_nan(a, __shfl_xor_sync(0xffffffffu, a, s));
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    ca[j] = a;
+            for (int s = 1; s < 32; s *= 2)
+                a = max_nan(a, __shfl_xor_sync(0xffffffffu, a, s));
+            tile_factor = F * (1.f / a);
+            if (threadIdx.x == 0) {
+                if (Q)
+                    p.sq[row0 / 128 * p.sq_rs + blockIdx.x * p.sq_ks] = a * kInvF;
+                if (T)
+                    p.st[blockIdx.x * p.st_rs + row0 / 128 * p.st_ks] = a * kInvF;
             }
         }
         if (Q) {
-            float r = TILE ? F * (1.f / ca[0]) : 0.f;
+            float mine = tile_factor;
+            if (!TILE) {
+                float a[R];
+                d.row_max(a);
+                float m = a[0];  // lane tx looks after row tx % R
+#pragma unroll
+                for (int i = 1; i < R; ++i)
+                    m = tx % R == i ? a[i] : m;
+                m = max_nan(m, kFloor);
+                mine = F * (1.f / m);
+                if (tx < R && row + tx < p.rows)
+                    p.sq[(row + tx) * p.sq_rs + blockIdx.x * p.sq_ks] = m * kInvF;
+            }
 #pragma unroll
             for (int i = 0; i < R; ++i) {
-                if (!TILE)
-                    r = F * (1.f / ra[i]);
-                const uint32_t w[2] = {pack4<E5M2>(v[i][0] * r, v[i][1] * r, v[i][2] * r, v[i][3] * r),
-                                       pack4<E5M2>(v[i][4] * r, v[i][5] * r, v[i][6] * r, v[i][7] * r)};
+                const float r = TILE ? tile_factor : __shfl_sync(0xffffffffu, mine, (lane & 16) + i);
+                const uint32_t w[2] = {
+                    pack4<E5M2>(d.get(i, 0) * r, d.get(i, 1) * r, d.get(i, 2) * r, d.get(i, 3) * r),
+                    pack4<E5M2>(d.get(i, 4) * r, d.get(i, 5) * r, d.get(i, 6) * r, d.get(i, 7) * r)};
                 if (row + i < p.rows && ncol > 0) {
-                    uint8_t* d = p.q + (row + i) * p.ldq + col;
+                    uint8_t* o = p.q + (row + i) * p.ldq + col;
                     if (p.vec_q && ncol == 8)
-                        *reinterpret_cast<uint2*>(d) = make_uint2(w[0], w[1]);
+                        *reinterpret_cast<uint2*>(o) = make_uint2(w[0], w[1]);
                     else
-                        store_bytes(d, w, ncol);
+                        store_bytes(o, w, ncol);
                 }
-                if (!TILE && tx == 0 && row + i < p.rows)
-                    p.sq[(row + i) * p.sq_rs + blockIdx.x * p.sq_ks] = ra[i] * kInvF;
             }
-            if (TILE && threadIdx.x == 0)
-                p.sq[row0 / 128 * p.sq_rs + blockIdx.x * p.sq_ks] = ca[0] * kInvF;
         }
         if (T) {
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const float r = F * (1.f / ca[j]);
-                const uint2 w = make_uint2(pack4<E5M2>(v[0][j] * r, v[1 % R][j] * r, v[2 % R][j] * r, v[3 % R][j] * r),
-                                           pack4<E5M2>(v[4 % R][j] * r, v[5 % R][j] * r, v[6 % R][j] * r, v[7 % R][j] * r));
+                const float r = TILE ? tile_factor : cfac[tx * 8 + j];
+                const uint2 w = make_uint2(
+                    pack4<E5M2>(d.get(0, j) * r, d.get(1 % R, j) * r, d.get(2 % R, j) * r, d.get(3 % R, j) * r),
+                    pack4<E5M2>(d.get(4 % R, j) * r, d.get(5 % R, j) * r, d.get(6 % R, j) * r, d.get(7 % R, j) * r));
                 *reinterpret_cast<uint2*>(tq + (tx * 8 + j) * kPitchT + ty * 8) = w;
-                if (!TILE && ty == 0 && j < ncol)
-                    p.st[(col + j) * p.st_rs + row0 / 128 * p.st_ks] = ca[j] * kInvF;
             }
-            if (TILE && threadIdx.x == 0)
-                p.st[blockIdx.x * p.st_rs + row0 / 128 * p.st_ks] = ca[0] * kInvF;
             __syncthreads();
             const int nrow = static_cast<int>(min(static_cast<int64_t>(128), p.rows - row0));
 #pragma unroll
@@ -205,19 +296,34 @@ __global__ void __launch_bounds__(256) quantize_kernel(const QuantParams p)
                 const int c = (threadIdx.x >> 3) + 32 * e, r = (threadIdx.x & 7) * 16;
                 if (col0 + c < p.cols && r < nrow) {
                     const uint4 w = *reinterpret_cast<const uint4*>(tq + c * kPitchT + r);
-                    uint8_t* d = p.qt + (col0 + c) * p.ldqt + row0 + r;
+                    uint8_t* o = p.qt + (col0 + c) * p.ldqt + row0 + r;
                     if (p.vec_qt && r + 16 <= nrow) {
-                        *reinterpret_cast<uint4*>(d) = w;
+                        *reinterpret_cast<uint4*>(o) = w;
                     } else {
                         const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-                        store_bytes(d, u, min(16, nrow - r));
+                        store_bytes(o, u, min(16, nrow - r));
                     }
                 }
             }
         }
         if (T || TILE)
-            __syncthreads();  // cmax and tq are rewritten by the next rows
+            __syncthreads();  // cmax, cfac and tq are rewritten by the next rows
     }
+}
+
+template <auto KERNEL>
+cudaError_t start(const QuantParams& p, dim3 grid, cudaStream_t stream)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(256);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, KERNEL, p);
 }
 
 template <int XT, bool E5M2>
@@ -229,20 +335,14 @@ cudaError_t launch(const QuantParams& p, bool tile, cudaStream_t stream)
     const dim3 grid(static_cast<unsigned>((p.cols + 127) / 128), static_cast<unsigned>(gy < 65535 ? gy : 65535));
     if (tile) {
         if (q && t)
-            quantize_kernel<XT, E5M2, 8, true, true, true><<<grid, 256, 0, stream>>>(p);
-        else if (q)
-            quantize_kernel<XT, E5M2, 8, true, true, false><<<grid, 256, 0, stream>>>(p);
-        else
-            quantize_kernel<XT, E5M2, 8, true, false, true><<<grid, 256, 0, stream>>>(p);
-    } else {
-        if (q && t)
-            quantize_kernel<XT, E5M2, 8, false, true, true><<<grid, 256, 0, stream>>>(p);
-        else if (q)
-            quantize_kernel<XT, E5M2, 2, false, true, false><<<grid, 256, 0, stream>>>(p);
-        else
-            quantize_kernel<XT, E5M2, 8, false, false, true><<<grid, 256, 0, stream>>>(p);
+            return start<quantize_kernel<XT, E5M2, 8, true, true, true>>(p, grid, stream);
+        return q ? start<quantize_kernel<XT, E5M2, 8, true, true, false>>(p, grid, stream)
+                 : start<quantize_kernel<XT, E5M2, 8, true, false, true>>(p, grid, stream);
     }
-    return cudaGetLastError();
+    if (q && t)
+        return start<quantize_kernel<XT, E5M2, 8, false, true, true>>(p, grid, stream);
+    return q ? start<quantize_kernel<XT, E5M2, 2, false, true, false>>(p, grid, stream)
+             : start<quantize_kernel<XT, E5M2, 8, false, false, true>>(p, grid, stream);
 }
 
 }  // namespace
