@@ -11,13 +11,20 @@
 // and its use.  A warp item is 16 (or 32) weight rows by 64 elements of K; the
 // warps of a CTA split K.
 //
-// Products use mma.sync m16n8k8 in tf32, weights on the 16-row side and 8
-// tokens on the other.  Every fp16, bf16 and E4M3 value is a tf32 value, and
-// tf32 has fp32's range, so one path serves all types: x and the weights enter
-// exactly, and h, which stays in fp32, enters as the sum of two tf32 values
-// (22 significant bits; one alone would add the error of an fp16 rounding).  The order of K inside an item is
-// free as long as both operands share it: a lane takes 16 contiguous bytes of
-// a row, and its consecutive elements feed slots t and t + 4 of the MMA.
+// Products use mma.sync with fp32 accumulation, weights on the 16-row side and 8
+// tokens on the other.  The up kernel multiplies x as it is, m16n8k16 in x's
+// type, with weights of that type or E4M3 ones widened to it (exact).  h is fp32;
+// for bf16 and E4M3 weights it is stored as the sum of two bf16 values (16
+// significant bits, fp32's range) and multiplied as two bf16 operands.  fp16
+// weights do not fit bf16 and fp16 does not hold h's range, so there the down
+// kernel multiplies in tf32 (m16n8k8), which holds every fp16 value, h in two
+// parts again.  The order of K inside an item is free as long as both operands
+// share it: a lane takes 16 contiguous bytes of a row, and its consecutive
+// elements feed the slots of the MMA that are its own.
+//
+// With 64 tokens the issue slots bound the kernels, not memory (an item of E4M3
+// weights cost 409 instructions a warp when everything was widened to tf32), so
+// an item's loads and loop are kept to running pointers and immediate offsets.
 //
 // Routing is recomputed by every CTA from the logits, a few thousand
 // instructions; that spares a kernel and a round trip through memory.
@@ -60,6 +67,25 @@ __device__ __forceinline__ void mma_tf32(float (&c)[4], float a0, float a1, floa
           "r"(__float_as_uint(b0)), "r"(__float_as_uint(b1)));
 }
 
+// m16n8k16 in fp16 or bf16: a and b as packed pairs.
+template <bool BF16>
+__device__ __forceinline__ void mma_16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                       uint32_t b1)
+{
+    if constexpr (BF16)
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+            "{%0, %1, %2, %3};"
+            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    else
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+            "{%0, %1, %2, %3};"
+            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
 // The tf32 value that is left of v when its low 13 bits are dropped.
 __device__ __forceinline__ float tf32_head(float v) { return __uint_as_float(__float_as_uint(v) & 0xffffe000u); }
 
@@ -73,25 +99,18 @@ __device__ __forceinline__ float ld_cluster(uint32_t addr)
 // v - head, exact; nothing for an infinity, which its head holds whole.
 __device__ __forceinline__ float tf32_rest(float v, float head) { return fabsf(v) < INFINITY ? v - head : 0.f; }
 
+// Two E4M3 bytes -> a pair of fp16 or bf16 values (exact; NaN stays NaN).
 template <bool BF16>
-__device__ __forceinline__ void widen2(uint32_t w, float& a, float& b)
-{
-    if constexpr (BF16) {
-        a = __uint_as_float(w << 16);
-        b = __uint_as_float(w & 0xffff0000u);
-    } else {
-        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
-        a = f.x, b = f.y;
-    }
-}
-
-// Two E4M3 bytes -> two floats.
-__device__ __forceinline__ void widen2_e4m3(uint32_t w, float& a, float& b)
+__device__ __forceinline__ uint32_t widen_e4m3(uint32_t w)
 {
     uint32_t h;
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(w)));
-    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
-    a = f.x, b = f.y;
+    if constexpr (BF16) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+        const __nv_bfloat162 b = __floats2bfloat162_rn(f.x, f.y);
+        h = *reinterpret_cast<const uint32_t*>(&b);
+    }
+    return h;
 }
 
 // ---------------------------------------------------------------- routing
@@ -276,18 +295,20 @@ __device__ __forceinline__ void route_all(const MoeParams& p, const Route& r)
 // Shared-memory layout of one ring stage, in 512-byte lines (32 lanes x 16
 // bytes): first the weights, then the tokens' side.  A lane holds 16 elements
 // of K per row: two chunks of 8 (16-bit weights: k = 32*half + 8*t, t = lane %
-// 4), or one of 16 (8-bit: k = 16*t).
-template <bool W8, int MT, int NT, int BSIZE>
+// 4), or one of 16 (8-bit: k = 16*t).  TB: bytes of a token's element, 2 (x) or
+// 4 (h: 8 fp32 values, or 8 bf16 heads and then their 8 rests).
+template <bool W8, int MT, int NT, int TB>
 struct Stage {
-    static constexpr int W_LINES = MT * 2 * (W8 ? 1 : 2);  // [mt][row half][chunk]
-    static constexpr int B_PER_TOKEN = BSIZE == 2 ? 2 : 4;  // 16 elements of 2 or 4 bytes
+    static constexpr int PER_ROW = W8 ? 1 : 2;
+    static constexpr int W_LINES = MT * 2 * PER_ROW;  // [mt][row half][chunk]
+    static constexpr int B_PER_TOKEN = TB;            // 16 elements
     static constexpr int LINES = W_LINES + NT * B_PER_TOKEN;
     static constexpr int BYTES = LINES * 512;
 };
 
 // First of the 8 elements of K that a lane's half `hf` covers within an item.
 template <bool W8>
-__device__ __forceinline__ int half_k(int t, int hf)
+__host__ __device__ constexpr int half_k(int t, int hf)
 {
     return W8 ? 16 * t + 8 * hf : 32 * hf + 8 * t;
 }
@@ -295,7 +316,7 @@ __device__ __forceinline__ int half_k(int t, int hf)
 __device__ __forceinline__ int clamp16(int bytes) { return bytes < 0 ? 0 : (bytes > 16 ? 16 : bytes); }
 
 // A 16-byte chunk of a row that starts anywhere: byte by byte, zeros past n.
-__device__ __forceinline__ void copy_bytes(uint32_t dst, const uint8_t* src, int n)
+__device__ __noinline__ void copy_bytes(uint32_t dst, const uint8_t* src, int n)
 {
     uint32_t w[4] = {0, 0, 0, 0};
     for (int i = 0; i < n; ++i)
@@ -304,39 +325,32 @@ __device__ __forceinline__ void copy_bytes(uint32_t dst, const uint8_t* src, int
                  : "memory");
 }
 
-// One lane's weight chunks of one row for the item at k0: `row` points at the
-// row, or is null (zeros) for rows outside the matrix; `any` is a readable
-// address for those.
-template <bool W8>
-__device__ __forceinline__ void load_row(uint32_t dst, const uint8_t* row, const void* any, int k0, int K, int t, bool vec)
+// One lane's N chunks of one row of an item, chunk c from byte (c / PAIR) * STEP +
+// (c % PAIR) * 16 of src to line c.  `bytes` is 16, or 0 for a row that gives
+// zeros (src is then any readable row).  `inside`: the whole item lies within the
+// row; else ends[c / PAIR] bytes from there are the row's.
+template <int N, int PAIR, int STEP, bool STREAM>
+__device__ __forceinline__ void load_chunks(uint32_t dst, const uint8_t* src, int bytes, bool inside, int end0, int end1,
+                                            bool vec)
 {
-    constexpr int ES = W8 ? 1 : 2;
+    if (vec && inside) {
 #pragma unroll
-    for (int c = 0; c < (W8 ? 1 : 2); ++c) {
-        const int k = k0 + half_k<W8>(t, c);
-        const int n = row ? clamp16((K - k) * ES) : 0;
-        const uint8_t* src = n > 0 ? row + static_cast<int64_t>(k) * ES : static_cast<const uint8_t*>(any);
-        if (vec)
-            cp_async_cg(dst + c * 512, src, n);
-        else
-            copy_bytes(dst + c * 512, src, n);
-    }
-}
-
-// One lane's chunks of a token's row (BSIZE bytes an element).
-template <bool W8, int BSIZE>
-__device__ __forceinline__ void load_token(uint32_t dst, const uint8_t* row, const void* any, int k0, int K, int t,
-                                           bool vec)
-{
+        for (int c = 0; c < N; ++c) {
+            if (STREAM)
+                cp_async_cg(dst + c * 512, src + c / PAIR * STEP + c % PAIR * 16, bytes);
+            else
+                cp_async_ca(dst + c * 512, src + c / PAIR * STEP + c % PAIR * 16, bytes);
+        }
+    } else {
 #pragma unroll
-    for (int c = 0; c < 16 * BSIZE / 16; ++c) {  // 8 (BSIZE 2) or 4 (BSIZE 4) elements each
-        const int k = k0 + (BSIZE == 2 ? half_k<W8>(t, c) : half_k<W8>(t, c >> 1) + 4 * (c & 1));
-        const int n = row ? clamp16((K - k) * BSIZE) : 0;
-        const uint8_t* src = n > 0 ? row + static_cast<int64_t>(k) * BSIZE : static_cast<const uint8_t*>(any);
-        if (vec)
-            cp_async_ca(dst + c * 512, src, n);
-        else
-            copy_bytes(dst + c * 512, src, n);
+        for (int c = 0; c < N; ++c) {
+            const int n = bytes ? clamp16((c / PAIR ? end1 : end0) - c % PAIR * 16) : 0;
+            const uint8_t* from = src + (n ? c / PAIR * STEP + c % PAIR * 16 : 0);
+            if (vec)
+                cp_async_ca(dst + c * 512, from, n);
+            else
+                copy_bytes(dst + c * 512, from, n);
+        }
     }
 }
 
@@ -347,72 +361,72 @@ __device__ __forceinline__ uint4 lds16(uint32_t a)
     return v;
 }
 
-// 8 weights of a lane's half from the stage.
+// The 8 weights of a lane's half, as 4 packed pairs of the MMA's type.
 template <bool BF16, bool W8>
-__device__ __forceinline__ void weights8(uint32_t line, int hf, float (&v)[8])
+__device__ __forceinline__ void weights8(uint32_t line, int hf, uint32_t (&v)[4])
 {
     if constexpr (W8) {
         uint32_t a, b;
         asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(a), "=r"(b) : "r"(line + 8 * hf) : "memory");
-        widen2_e4m3(a, v[0], v[1]);
-        widen2_e4m3(a >> 16, v[2], v[3]);
-        widen2_e4m3(b, v[4], v[5]);
-        widen2_e4m3(b >> 16, v[6], v[7]);
+        v[0] = widen_e4m3<BF16>(a);
+        v[1] = widen_e4m3<BF16>(a >> 16);
+        v[2] = widen_e4m3<BF16>(b);
+        v[3] = widen_e4m3<BF16>(b >> 16);
     } else {
         const uint4 w = lds16(line + 512 * hf);
-        widen2<BF16>(w.x, v[0], v[1]);
-        widen2<BF16>(w.y, v[2], v[3]);
-        widen2<BF16>(w.z, v[4], v[5]);
-        widen2<BF16>(w.w, v[6], v[7]);
+        v[0] = w.x, v[1] = w.y, v[2] = w.z, v[3] = w.w;
     }
 }
 
-template <bool BF16, int BSIZE>
-__device__ __forceinline__ void tokens8(uint32_t line, int hf, float (&v)[8])
-{
-    if constexpr (BSIZE == 2) {
-        const uint4 w = lds16(line + 512 * hf);
-        widen2<BF16>(w.x, v[0], v[1]);
-        widen2<BF16>(w.y, v[2], v[3]);
-        widen2<BF16>(w.z, v[4], v[5]);
-        widen2<BF16>(w.w, v[6], v[7]);
-    } else {
-        const uint4 a = lds16(line + 1024 * hf), b = lds16(line + 1024 * hf + 512);
-        v[0] = __uint_as_float(a.x), v[1] = __uint_as_float(a.y), v[2] = __uint_as_float(a.z), v[3] = __uint_as_float(a.w);
-        v[4] = __uint_as_float(b.x), v[5] = __uint_as_float(b.y), v[6] = __uint_as_float(b.z), v[7] = __uint_as_float(b.w);
-    }
-}
+__device__ __forceinline__ float2 halves(uint32_t w) { return __half22float2(*reinterpret_cast<const __half2*>(&w)); }
 
-// Multiplies one landed item into c: stage address `st` is the lane's own (line
-// + 16 * lane), nt token tiles of 8 are in use.
-template <bool BF16, bool W8, int MT, int NT, int BSIZE>
+// How an item is multiplied: x as it is; h as bf16 heads and rests; h as fp32 on
+// tf32 (fp16 weights).
+enum { kPlain, kSplit, kTf32 };
+
+// Multiplies one landed item into c: `st` is the lane's own stage address (+ 16 *
+// lane), nt token tiles of 8 are in use.
+template <int HOW, bool BF16, bool W8, int MT, int NT>
 __device__ __forceinline__ void multiply_item(uint32_t st, int nt, float (&c)[MT][NT][4])
 {
-    using S = Stage<W8, MT, NT, BSIZE>;
-    constexpr int PER_ROW = W8 ? 1 : 2;
+    using S = Stage<W8, MT, NT, HOW == kPlain ? 2 : 4>;
 #pragma unroll
     for (int hf = 0; hf < 2; ++hf) {
-        float lo[MT][8], hi[MT][8];
+        uint32_t lo[MT][4], hi[MT][4];
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
-            weights8<BF16, W8>(st + (m * 2 * PER_ROW) * 512, hf, lo[m]);
-            weights8<BF16, W8>(st + (m * 2 * PER_ROW + PER_ROW) * 512, hf, hi[m]);
+            weights8<BF16, W8>(st + m * 2 * S::PER_ROW * 512, hf, lo[m]);
+            weights8<BF16, W8>(st + (m * 2 + 1) * S::PER_ROW * 512, hf, hi[m]);
         }
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             if (n < nt) {
-                float b[8];
-                tokens8<BF16, BSIZE>(st + (S::W_LINES + n * S::B_PER_TOKEN) * 512, hf, b);
+                const uint32_t line = st + (S::W_LINES + n * S::B_PER_TOKEN) * 512;
+                if constexpr (HOW == kTf32) {
+                    const uint4 x = lds16(line + 1024 * hf), y = lds16(line + 1024 * hf + 512);
+                    const float b[8] = {__uint_as_float(x.x), __uint_as_float(x.y), __uint_as_float(x.z),
+                                        __uint_as_float(x.w), __uint_as_float(y.x), __uint_as_float(y.y),
+                                        __uint_as_float(y.z), __uint_as_float(y.w)};
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float b0 = BSIZE == 4 ? tf32_head(b[2 * j]) : b[2 * j];
-                    const float b1 = BSIZE == 4 ? tf32_head(b[2 * j + 1]) : b[2 * j + 1];
+                    for (int j = 0; j < 4; ++j) {
+                        const float b0 = tf32_head(b[2 * j]), b1 = tf32_head(b[2 * j + 1]);
+                        const float d0 = tf32_rest(b[2 * j], b0), d1 = tf32_rest(b[2 * j + 1], b1);
 #pragma unroll
-                    for (int m = 0; m < MT; ++m) {
-                        mma_tf32(c[m][n], lo[m][2 * j], hi[m][2 * j], lo[m][2 * j + 1], hi[m][2 * j + 1], b0, b1);
-                        if (BSIZE == 4)  // fp32 tokens: what their heads leave
-                            mma_tf32(c[m][n], lo[m][2 * j], hi[m][2 * j], lo[m][2 * j + 1], hi[m][2 * j + 1],
-                                     tf32_rest(b[2 * j], b0), tf32_rest(b[2 * j + 1], b1));
+                        for (int m = 0; m < MT; ++m) {
+                            const float2 l = halves(lo[m][j]), h = halves(hi[m][j]);
+                            mma_tf32(c[m][n], l.x, h.x, l.y, h.y, b0, b1);
+                            mma_tf32(c[m][n], l.x, h.x, l.y, h.y, d0, d1);
+                        }
+                    }
+                } else {
+#pragma unroll
+                    for (int part = 0; part < (HOW == kSplit ? 2 : 1); ++part) {
+                        const uint4 w = lds16(line + (HOW == kSplit ? 1024 * hf + 512 * part : 512 * hf));
+#pragma unroll
+                        for (int m = 0; m < MT; ++m) {
+                            mma_16<BF16>(c[m][n], lo[m][0], hi[m][0], lo[m][1], hi[m][1], w.x, w.y);
+                            mma_16<BF16>(c[m][n], lo[m][2], hi[m][2], lo[m][3], hi[m][3], w.z, w.w);
+                        }
                     }
                 }
             }
@@ -465,38 +479,51 @@ __global__ void __launch_bounds__(kThreads, 2) moe_up_kernel(const MoeParams p)
     const uint8_t* xb = static_cast<const uint8_t*>(p.x);
     const uint8_t* wb = static_cast<const uint8_t*>(p.w13);
 
-    // Loader: the items (unit, token group, K item) of this warp in order.
-    int lu = u0, lg = 0, lk = ks0, lslot = 0;
-    bool fresh = true;
-    const uint8_t *wg = nullptr, *wu = nullptr;
+    // Loader: the items (unit, token group, K item) of this warp in order, by
+    // pointers to the lane's own bytes.  Rows outside the matrix, and tokens past
+    // the group, read nothing of row 0.
+    int lu = u0, lg = 0, lk = ks0, lslot = 0, lgroups = 0, wbytes = 0;
+    const uint8_t *wg = wb, *wu = wb;
     const uint8_t* xr[NT];
-    int lgroups = 0;
+    uint32_t xbytes = 0;  // bit q: token of tile q
     auto load_next = [&] {
         if (ks0 < ks1 && lu < u1) {
-            if (fresh) {
+            if (lk == ks0) {
                 const int a = lu / tiles, i = (lu - a * tiles) * 8 + g;
                 const int n = r.aoff[a + 1] - r.aoff[a];
                 lgroups = ceil_div(n, 8 * NT);
-                const uint8_t* we = wb + static_cast<int64_t>(r.act[a]) * p.stride_w13 * ES;
-                wg = i < p.inner ? we + static_cast<int64_t>(i) * p.ldw13 * ES : nullptr;
-                wu = i < p.inner ? we + static_cast<int64_t>(p.inner + i) * p.ldw13 * ES : nullptr;
+                const uint8_t* we = wb + static_cast<int64_t>(r.act[a]) * p.stride_w13 * ES + ks0 * (kItem * ES) + t * 16;
+                const bool in = i < p.inner;
+                wbytes = in ? 16 : 0;
+                wg = we + (in ? static_cast<int64_t>(i) * p.ldw13 * ES : 0);
+                wu = we + (in ? static_cast<int64_t>(p.inner + i) * p.ldw13 * ES : 0);
+                xbytes = 0;
 #pragma unroll
                 for (int q = 0; q < NT; ++q) {
                     const int j = lg * 8 * NT + q * 8 + g;
-                    xr[q] = j < n ? xb + static_cast<int64_t>(r.list[r.aoff[a] + j] / p.topk) * p.ldx * 2 : nullptr;
+                    xr[q] = xb + ks0 * (kItem * 2) + half_k<W8>(t, 0) * 2;
+                    if (j < n) {
+                        xr[q] += static_cast<int64_t>(r.list[r.aoff[a] + j] / p.topk) * p.ldx * 2;
+                        xbytes |= 1u << q;
+                    }
                 }
-                fresh = false;
             }
             const uint32_t st = ring + lslot * S::BYTES;
-            load_row<W8>(st, wg, wb, lk * kItem, p.hidden, t, p.vec_13);
-            load_row<W8>(st + (W8 ? 1 : 2) * 512, wu, wb, lk * kItem, p.hidden, t, p.vec_13);
+            const bool inside = (lk + 1) * kItem <= p.hidden;
+            const int left = p.hidden - lk * kItem, w0 = (left - half_k<W8>(t, 0)) * ES, w1 = (left - half_k<W8>(t, 1)) * ES;
+            load_chunks<S::PER_ROW, 1, 64, true>(st, wg, wbytes, inside, w0, w1, p.vec_13);
+            load_chunks<S::PER_ROW, 1, 64, true>(st + S::PER_ROW * 512, wu, wbytes, inside, w0, w1, p.vec_13);
 #pragma unroll
-            for (int q = 0; q < NT; ++q)
-                load_token<W8, 2>(st + (S::W_LINES + q * S::B_PER_TOKEN) * 512, xr[q], xb, lk * kItem, p.hidden, t,
-                                  p.vec_x);
+            for (int q = 0; q < NT; ++q) {
+                load_chunks<2, 1, W8 ? 16 : 64, false>(st + (S::W_LINES + q * 2) * 512, xr[q], xbytes >> q & 1 ? 16 : 0,
+                                                       inside, (left - half_k<W8>(t, 0)) * 2,
+                                                       (left - half_k<W8>(t, 1)) * 2, p.vec_x);
+                xr[q] += kItem * 2;
+            }
+            wg += kItem * ES;
+            wu += kItem * ES;
             if (++lk == ks1) {
                 lk = ks0;
-                fresh = true;
                 if (++lg == lgroups) {
                     lg = 0;
                     ++lu;
@@ -514,7 +541,14 @@ __global__ void __launch_bounds__(kThreads, 2) moe_up_kernel(const MoeParams p)
 #pragma unroll 1
     for (int u = u0; u < u1; ++u) {
         const int a = u / tiles, i0 = (u - a * tiles) * 8;
-        const int first = r.aoff[a], n = r.aoff[a + 1] - first, e = r.act[a];
+        const int first = r.aoff[a], n = r.aoff[a + 1] - first;
+        const float *pg = nullptr, *pu = nullptr;  // the lane's rows' scales
+        if (W8) {
+            const int i = min(i0 + g, p.inner - 1);
+            const float* se = p.s13.data + r.act[a] * p.s13.bs;
+            pg = se + static_cast<int64_t>(i >> p.s13.shift) * p.s13.rs;
+            pu = se + static_cast<int64_t>((p.inner + i) >> p.s13.shift) * p.s13.rs;
+        }
 #pragma unroll 1
         for (int g0 = 0; g0 < n; g0 += 8 * NT) {
             const int nt = min(NT, ceil_div(n - g0, 8));
@@ -523,14 +557,14 @@ __global__ void __launch_bounds__(kThreads, 2) moe_up_kernel(const MoeParams p)
             for (int k = ks0; k < ks1; ++k) {
                 float sg = 0.f, su = 0.f;
                 if (W8) {
-                    const int i = min(i0 + g, p.inner - 1), kb = k * kItem / 128;
-                    sg = scale_at(p.s13, e, i, kb);
-                    su = scale_at(p.s13, e, p.inner + i, kb);
+                    const int64_t kb = static_cast<int64_t>(k >> 1) * p.s13.ks;  // an item is half a block of 128
+                    sg = __ldg(pg + kb);
+                    su = __ldg(pu + kb);
                 }
                 cp_async_wait<D - 2>();
                 if constexpr (W8) {
                     float part[1][NT][4] = {};
-                    multiply_item<BF16, W8, 1, NT, 2>(ring + slot * S::BYTES, nt, part);
+                    multiply_item<kPlain, BF16, W8, 1, NT>(ring + slot * S::BYTES, nt, part);
 #pragma unroll
                     for (int q = 0; q < NT; ++q) {
                         c[0][q][0] = fmaf(part[0][q][0], sg, c[0][q][0]);
@@ -539,7 +573,7 @@ __global__ void __launch_bounds__(kThreads, 2) moe_up_kernel(const MoeParams p)
                         c[0][q][3] = fmaf(part[0][q][3], su, c[0][q][3]);
                     }
                 } else {
-                    multiply_item<BF16, W8, 1, NT, 2>(ring + slot * S::BYTES, nt, c);
+                    multiply_item<kPlain, BF16, W8, 1, NT>(ring + slot * S::BYTES, nt, c);
                 }
                 slot = slot + 1 == D ? 0 : slot + 1;
                 load_next();
@@ -564,8 +598,20 @@ __global__ void __launch_bounds__(kThreads, 2) moe_up_kernel(const MoeParams p)
                     up += rd[((w * NT + q) * 4 + 2 + wh) * 32 + l];
                 }
                 const int i = i0 + (l >> 2), j = g0 + q * 8 + 2 * (l & 3) + wh;
-                if (i < p.inner && j < n)
-                    p.h[r.list[first + j] * p.ldh + i] = gate / (1.f + expf(-gate)) * up;
+                if (j < n) {  // columns past inner, to the end of the 8, get zeros
+                    const float h = gate / (1.f + expf(-gate)) * up;
+                    float* row = p.h + r.list[first + j] * p.ldh;
+                    if constexpr (BF16 || W8) {
+                        // groups of 8 columns: their 8 bf16 heads, then their 8 rests
+                        const __nv_bfloat16 head = __float2bfloat16_rn(h);
+                        const float rest = fabsf(h) < INFINITY ? h - __bfloat162float(head) : 0.f;
+                        __nv_bfloat16* o = reinterpret_cast<__nv_bfloat16*>(row + i0) + (l >> 2);
+                        o[0] = head;
+                        o[8] = __float2bfloat16_rn(rest);
+                    } else {
+                        row[i] = h;
+                    }
+                }
             }
         }
     }
@@ -593,7 +639,7 @@ __global__ void __launch_bounds__(kThreads, MT == 1 && NT == 1 ? 2 : 1) moe_down
 {
     using C = DownCfg<W8, NT, MT>;
     using S = typename C::S;
-    constexpr int D = C::D, ROWS = 16 * MT;
+    constexpr int D = C::D, ROWS = 16 * MT, HOW = BF16 || W8 ? kSplit : kTf32;
     extern __shared__ __align__(16) uint8_t smem[];
     float* sums = reinterpret_cast<float*>(smem + C::RING);  // [warp][token][row]
     const Route r = route_carve(smem + C::RING + down_sum_bytes(p.tokens, MT), p);
@@ -616,11 +662,14 @@ __global__ void __launch_bounds__(kThreads, MT == 1 && NT == 1 ? 2 : 1) moe_down
     const uint8_t* wb = static_cast<const uint8_t*>(p.w2);
     const uint8_t* hb = reinterpret_cast<const uint8_t*>(p.h);
 
-    // Loader: per expert of the range, per token group, its K items.
+    // Loader: per expert of the range, per token group, its K items (pointers as in
+    // the up kernel; h's rows are whole groups of 8 columns, zeros past inner).
+    const int kpad = (p.inner + 7) / 8 * 8;
     int lq = q0, lg = 0, lk = 0, lend = 0, lslot = 0, lgroups = 0;
-    bool fresh = true;
     const uint8_t* wr[2 * MT];
     const uint8_t* hr[NT];
+    uint32_t wbytes = 0, hbytes = 0;  // bit m: row m is inside; bit q: token of tile q
+    bool fresh = true;
     auto load_next = [&] {
         if (lq < q1) {
             if (fresh) {
@@ -628,26 +677,44 @@ __global__ void __launch_bounds__(kThreads, MT == 1 && NT == 1 ? 2 : 1) moe_down
                 lk = lq - a * nit;
                 lend = min(nit, lk + q1 - lq);
                 lgroups = ceil_div(n, 8 * NT);
-                const uint8_t* we = wb + static_cast<int64_t>(r.act[a]) * p.stride_w2 * ES;
+                const uint8_t* we = wb + static_cast<int64_t>(r.act[a]) * p.stride_w2 * ES + lk * (kItem * ES) + t * 16;
+                wbytes = hbytes = 0;
 #pragma unroll
                 for (int m = 0; m < 2 * MT; ++m) {
                     const int row = r0 + 8 * m + g;
-                    wr[m] = row < p.hidden ? we + static_cast<int64_t>(row) * p.ldw2 * ES : nullptr;
+                    wr[m] = we;
+                    if (row < p.hidden) {
+                        wr[m] += static_cast<int64_t>(row) * p.ldw2 * ES;
+                        wbytes |= 1u << m;
+                    }
                 }
 #pragma unroll
                 for (int q = 0; q < NT; ++q) {
                     const int j = lg * 8 * NT + q * 8 + g;
-                    hr[q] = j < n ? hb + static_cast<int64_t>(r.list[r.aoff[a] + j]) * p.ldh * 4 : nullptr;
+                    hr[q] = hb + lk * (kItem * 4) + half_k<W8>(t, 0) * 4;
+                    if (j < n) {
+                        hr[q] += static_cast<int64_t>(r.list[r.aoff[a] + j]) * p.ldh * 4;
+                        hbytes |= 1u << q;
+                    }
                 }
                 fresh = false;
             }
             const uint32_t st = ring + lslot * S::BYTES;
+            const bool inside = (lk + 1) * kItem <= p.inner;
+            const int left = p.inner - lk * kItem, w0 = (left - half_k<W8>(t, 0)) * ES, w1 = (left - half_k<W8>(t, 1)) * ES;
+            const int h0 = (kpad - lk * kItem - half_k<W8>(t, 0)) * 4, h1 = (kpad - lk * kItem - half_k<W8>(t, 1)) * 4;
 #pragma unroll
-            for (int m = 0; m < 2 * MT; ++m)
-                load_row<W8>(st + m * (W8 ? 1 : 2) * 512, wr[m], wb, lk * kItem, p.inner, t, p.vec_2);
+            for (int m = 0; m < 2 * MT; ++m) {
+                load_chunks<S::PER_ROW, 1, 64, true>(st + m * S::PER_ROW * 512, wr[m], wbytes >> m & 1 ? 16 : 0, inside, w0,
+                                                     w1, p.vec_2);
+                wr[m] += kItem * ES;
+            }
 #pragma unroll
-            for (int q = 0; q < NT; ++q)
-                load_token<W8, 4>(st + (S::W_LINES + q * S::B_PER_TOKEN) * 512, hr[q], hb, lk * kItem, p.inner, t, true);
+            for (int q = 0; q < NT; ++q) {
+                load_chunks<4, 2, W8 ? 32 : 128, false>(st + (S::W_LINES + q * 4) * 512, hr[q], hbytes >> q & 1 ? 16 : 0,
+                                                        inside, h0, h1, true);
+                hr[q] += kItem * 4;
+            }
             if (++lk == lend) {
                 fresh = true;
                 if (++lg == lgroups) {
@@ -668,7 +735,14 @@ __global__ void __launch_bounds__(kThreads, MT == 1 && NT == 1 ? 2 : 1) moe_down
 #pragma unroll 1
     for (int q = q0; q < q1;) {
         const int a = q / nit, k0 = q - a * nit, k1 = min(nit, k0 + q1 - q);
-        const int first = r.aoff[a], n = r.aoff[a + 1] - first, e = r.act[a];
+        const int first = r.aoff[a], n = r.aoff[a + 1] - first;
+        const float* ps[2 * MT];  // the lane's rows' scales
+        if (W8) {
+#pragma unroll
+            for (int m = 0; m < 2 * MT; ++m)
+                ps[m] = p.s2.data + r.act[a] * p.s2.bs +
+                        static_cast<int64_t>(min(r0 + 8 * m + g, p.hidden - 1) >> p.s2.shift) * p.s2.rs;
+        }
 #pragma unroll 1
         for (int g0 = 0; g0 < n; g0 += 8 * NT) {
             const int nt = min(NT, ceil_div(n - g0, 8));
@@ -677,14 +751,15 @@ __global__ void __launch_bounds__(kThreads, MT == 1 && NT == 1 ? 2 : 1) moe_down
             for (int k = k0; k < k1; ++k) {
                 float s[2 * MT];
                 if (W8) {
+                    const int64_t kb = static_cast<int64_t>(k >> 1) * p.s2.ks;  // an item is half a block of 128
 #pragma unroll
                     for (int m = 0; m < 2 * MT; ++m)
-                        s[m] = scale_at(p.s2, e, min(r0 + 8 * m + g, p.hidden - 1), k * kItem / 128);
+                        s[m] = __ldg(ps[m] + kb);
                 }
                 cp_async_wait<D - 2>();
                 if constexpr (W8) {
                     float part8[MT][NT][4] = {};
-                    multiply_item<BF16, W8, MT, NT, 4>(ring + slot * S::BYTES, nt, part8);
+                    multiply_item<HOW, true, W8, MT, NT>(ring + slot * S::BYTES, nt, part8);
 #pragma unroll
                     for (int m = 0; m < MT; ++m)
 #pragma unroll
@@ -693,7 +768,7 @@ __global__ void __launch_bounds__(kThreads, MT == 1 && NT == 1 ? 2 : 1) moe_down
                             for (int v = 0; v < 4; ++v)
                                 c[m][w][v] = fmaf(part8[m][w][v], s[2 * m + (v >> 1)], c[m][w][v]);
                 } else {
-                    multiply_item<BF16, W8, MT, NT, 4>(ring + slot * S::BYTES, nt, c);
+                    multiply_item<HOW, BF16, W8, MT, NT>(ring + slot * S::BYTES, nt, c);
                 }
                 slot = slot + 1 == D ? 0 : slot + 1;
                 load_next();
@@ -779,13 +854,14 @@ cudaError_t launch_one(const MoeParams& p, int num_sms, cudaStream_t stream)
         if (e != cudaSuccess)
             return e;
     }
-    // Clusters large enough for two CTAs (one, where a CTA takes most of an
-    // SM's shared memory) on every SM, as long as each warp keeps a few items.
+    // The largest clusters whose CTAs are all resident at once, two on an SM (one,
+    // where a CTA takes most of its shared memory), as long as each warp keeps a
+    // few items: a second wave of 512 CTAs after 304 cost one token 9 of 26 us.
     const int tiles = (p.hidden + 16 * MT - 1) / (16 * MT);
     const int64_t items = reach * ((p.inner + kItem - 1) / kItem);
     const int want = num_sms * (MT == 1 && NT == 1 ? 2 : 1);
     int c = 1;
-    while (c < 8 && tiles * c < want && items >= 2 * 2 * c * kWarps)
+    while (c < 8 && 2 * tiles * c <= want && items >= 2 * 2 * c * kWarps)
         c *= 2;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(tiles * c));
