@@ -28,8 +28,8 @@ using tc::BM;
 constexpr int kThreads = 384;   // warps 0-3: producer, MMA, scales, idle; warps 4-11: promotion
 constexpr int kPromoWarps = 8;
 constexpr int kAcc = 4;         // accumulators in Tensor Memory
-constexpr int kScaleRing = 8;
-constexpr int kScaleBatch = 4;
+constexpr int kScaleRing = 4;   // slots of kScaleGroup K blocks
+constexpr int kScaleGroup = 4;
 constexpr int kMaxCluster = 8;
 
 constexpr int max_int(int a, int b) { return a > b ? a : b; }
@@ -39,9 +39,9 @@ template <int BN>
 struct Cfg {
     static constexpr int X_BYTES = BM * kRowBytes, Y_BYTES = BN * kRowBytes;
     static constexpr int STAGE = X_BYTES + Y_BYTES;
-    static constexpr int SCALE_FLOATS = 128 + BN;
+    static constexpr int SCALE_FLOATS = 128 + max_int(32, BN);
     static constexpr int BAR_BYTES = 512;
-    static constexpr int REST = 1024 + kScaleRing * SCALE_FLOATS * 4 + BAR_BYTES;
+    static constexpr int REST = 1024 + kScaleRing * kScaleGroup * SCALE_FLOATS * 4 + BAR_BYTES;
     static constexpr int STAGES = min_int(12, (232448 - REST) / STAGE);
     static constexpr int SMEM = REST + STAGES * STAGE;
     static constexpr int TMEM_COLS = max_int(32, kAcc * BN);
@@ -57,14 +57,22 @@ __device__ __forceinline__ float ld_cluster(uint32_t addr)
     return v;
 }
 
-// Tiles: rows of B first, so that neighbours share A.
-__device__ __forceinline__ void decode(const BlkParams& p, int t, int bn, int& b, int& x0, int& y0)
+// Tiles: rows of B first, so that neighbours share A.  With p.row_share each CTA
+// has one tile, an even share of B's rows (at most 128) that starts anywhere.
+__device__ __forceinline__ void decode(const BlkParams& p, int t, int bn, int& b, int& x0, int& xend, int& y0)
 {
+    if (p.row_share) {
+        b = y0 = 0;
+        x0 = static_cast<int>(static_cast<int64_t>(p.N) * t / p.num_tiles);
+        xend = static_cast<int>(static_cast<int64_t>(p.N) * (t + 1) / p.num_tiles);
+        return;
+    }
     const int per = p.tiles_m * p.tiles_n;
     b = t / per;
     t -= b * per;
     y0 = t / p.tiles_n * bn;
     x0 = t % p.tiles_n * BM;
+    xend = min(x0 + BM, p.N);
 }
 
 template <int BN>
@@ -78,7 +86,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint8_t* xs = smem;
     uint8_t* ys = smem + C::STAGES * C::X_BYTES;
     float* scales = reinterpret_cast<float*>(smem + C::STAGES * C::STAGE);
-    uint64_t* full = reinterpret_cast<uint64_t*>(scales + kScaleRing * C::SCALE_FLOATS);
+    uint64_t* full = reinterpret_cast<uint64_t*>(scales + kScaleRing * kScaleGroup * C::SCALE_FLOATS);
     uint64_t* empty = full + C::STAGES;
     uint64_t* tfull = empty + C::STAGES;
     uint64_t* tempty = tfull + kAcc;
@@ -139,8 +147,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint64_t pol_x = l2_policy_evict_first(), pol_y = l2_policy_evict_last();
             bool ok = true, drop = p.fault == 1 && blockIdx.x == 0;
             for (int t = first; ok && t < p.num_tiles; t += step) {
-                int b, x0, y0;
-                decode(p, t, BN, b, x0, y0);
+                int b, x0, xend, y0;
+                decode(p, t, BN, b, x0, xend, y0);
                 for (int kb = kb0; kb < kb1; ++kb) {
                     if (!wait_bounded(smem_u32(&empty[stage]), phase ^ 1, abort_flag, p.wait_limit)) {
                         raise(p, abort_flag);
@@ -149,7 +157,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     if (!drop) {
                         const uint32_t fb = smem_u32(&full[stage]);
-                        mbar_arrive_expect_tx(fb, C::STAGE);
+                        mbar_arrive_expect_tx(fb, static_cast<uint32_t>(p.x_box * kRowBytes + C::Y_BYTES));
                         filled |= 1u << stage;
                         fill_parity = (fill_parity & ~(1u << stage)) | (phase << stage);
                         tma_load_3d_hint(smem_u32(xs + stage * C::X_BYTES), &tmx, fb, kb * kRowBytes, x0, b * p.b_bmul, pol_x);
@@ -208,103 +216,82 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else if (warp == 2) {
         // ------------------------------------------------------------ scales: 128 rows of B, BN rows of A
-        constexpr int NY = (BN + 31) / 32;
-        int slot = 0;
-        uint32_t phase = 0;
+        const uint32_t ring = smem_u32(scales);
+        int n = 0;  // K blocks so far
         bool ok = true;
         for (int t = first; ok && t < p.num_tiles; t += step) {
-            int b, x0, y0;
-            decode(p, t, BN, b, x0, y0);
-            for (int k0 = kb0; ok && k0 < kb1; k0 += kScaleBatch) {
-                float vx[kScaleBatch][4], vy[kScaleBatch][NY];
-#pragma unroll
-                for (int i = 0; i < kScaleBatch; ++i) {
-                    const int kb = min(k0 + i, kb1 - 1);
-#pragma unroll
-                    for (int r = 0; r < 4; ++r)
-                        vx[i][r] = scale_at(p.sb, b, min(x0 + 32 * r + lane, p.N - 1), kb);
-#pragma unroll
-                    for (int r = 0; r < NY; ++r)
-                        vy[i][r] = scale_at(p.sa, b, min(y0 + 32 * r + lane, p.M - 1), kb);
-                }
-#pragma unroll
-                for (int i = 0; i < kScaleBatch; ++i) {
-                    if (ok && k0 + i < kb1) {
-                        if (!wait_bounded(smem_u32(&sempty[slot]), phase ^ 1, abort_flag, p.wait_limit)) {
-                            raise(p, abort_flag);
-                            ok = false;
-                        } else {
-                            float* s = scales + slot * C::SCALE_FLOATS;
-#pragma unroll
-                            for (int r = 0; r < 4; ++r)
-                                s[32 * r + lane] = vx[i][r];
-#pragma unroll
-                            for (int r = 0; r < NY; ++r)
-                                if (32 * r + lane < BN)
-                                    s[128 + 32 * r + lane] = vy[i][r];
-                            mbar_arrive(smem_u32(&sfull[slot]));
-                            if (++slot == kScaleRing) {
-                                slot = 0;
-                                phase ^= 1;
-                            }
-                        }
-                    }
-                }
-            }
-        }
-    } else if (warp >= 4) {
-        // ------------------------------------------------------------ promotion
-        int slot = 0, buf = 0;
-        uint32_t sphase = 0, tphase = 0;
-        bool ok = true;
-        for (int t = first; ok && t < p.num_tiles; t += step) {
-            for (int kb = kb0; kb < kb1; ++kb) {
-                if (!wait_bounded(smem_u32(&sfull[slot]), sphase, abort_flag, p.wait_limit) ||
-                    !wait_bounded(smem_u32(&tfull[buf]), tphase, abort_flag, p.wait_limit)) {
+            int b, x0, xend, y0;
+            decode(p, t, BN, b, x0, xend, y0);
+            ScaleRun<4> x(p.sb, b, x0, p.N);
+            ScaleRun<(BN + 31) / 32> y(p.sa, b, y0, p.M);
+            x.skip(kb0);
+            y.skip(kb0);
+#pragma unroll 1
+            for (int kb = kb0; kb < kb1; ++kb, ++n) {
+                const int slot = n / kScaleGroup % kScaleRing;
+                if (n % kScaleGroup == 0 && !wait_bounded(smem_u32(&sempty[slot]), (n / (kScaleGroup * kScaleRing) & 1) ^ 1,
+                                                          abort_flag, p.wait_limit)) {
                     raise(p, abort_flag);
                     ok = false;
                     break;
                 }
+                const uint32_t s = ring + n % (kScaleGroup * kScaleRing) * (C::SCALE_FLOATS * 4);
+                x.copy(s);
+                y.copy(s + 128 * 4);
+                if (n % kScaleGroup == kScaleGroup - 1)
+                    cp_async_arrive(smem_u32(&sfull[slot]));
+            }
+        }
+        if (n % kScaleGroup != 0)  // the last group, short
+            cp_async_arrive(smem_u32(&sfull[n / kScaleGroup % kScaleRing]));
+        cp_async_wait_all();
+    } else if (warp >= 4) {
+        // ------------------------------------------------------------ promotion
+        const uint32_t row_scale = smem_u32(scales) + (32 * q + lane) * 4;
+        const uint32_t col_scales = smem_u32(scales) + (128 + C::COLS * ch) * 4;
+        const uint32_t tf0 = smem_u32(tfull), te0 = smem_u32(tempty), sf0 = smem_u32(sfull);
+        const uint32_t ta0 = tmem_base + static_cast<uint32_t>(C::COLS * ch) + (static_cast<uint32_t>(32 * q) << 16);
+        int n = 0;  // K blocks so far: ring positions and phases follow from it
+        bool ok = true;
+        for (int t = first; ok && t < p.num_tiles; t += step) {
+#pragma unroll 1
+            for (int kb = kb0; kb < kb1; ++kb, ++n) {
+                if (n % kScaleGroup == 0)
+                    ok &= wait_bounded(sf0 + n / kScaleGroup % kScaleRing * 8, n / (kScaleGroup * kScaleRing) & 1, abort_flag,
+                                       p.wait_limit);
+                const uint32_t so = n % (kScaleGroup * kScaleRing) * (C::SCALE_FLOATS * 4);
+                const float fx = lds_f32(row_scale + so);
+                ok &= wait_bounded(tf0 + n % kAcc * 8, n / kAcc & 1, abort_flag, p.wait_limit);
+                if (!ok) {
+                    raise(p, abort_flag);
+                    break;
+                }
                 tc_fence_after();
-                const float* s = scales + slot * C::SCALE_FLOATS;
-                const float fx = s[32 * q + lane];
-                const uint64_t sx = pack2(fx, fx);
-                const uint32_t ta = tmem_base + static_cast<uint32_t>(buf * BN + C::COLS * ch) +
-                                    (static_cast<uint32_t>(32 * q) << 16);
                 uint32_t x[C::COLS];
 #pragma unroll
                 for (int c = 0; c < C::COLS; c += 8)
-                    tmem_ld32x8(ta + c, x + c);
+                    tmem_ld32x8(ta0 + n % kAcc * BN + c, x + c);
 #pragma unroll
                 for (int c = 0; c < C::COLS; c += 8)
                     tmem_wait8(x + c);
                 tc_fence_before();
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive(smem_u32(&tempty[buf]));
-                const ulonglong2* sy = reinterpret_cast<const ulonglong2*>(s + 128 + C::COLS * ch);
+                mbar_arrive_if(te0 + n % kAcc * 8, lane == 0);
+                const uint64_t sx = pack2(fx, fx);
 #pragma unroll
                 for (int j = 0; j < C::COLS / 4; ++j) {
-                    const ulonglong2 w = sy[j];
+                    const ulonglong2 w = lds_f32x4(col_scales + so + 16 * j);
                     acc[2 * j] = fma2(mul2(pack2u(x[4 * j], x[4 * j + 1]), w.x), sx, acc[2 * j]);
                     acc[2 * j + 1] = fma2(mul2(pack2u(x[4 * j + 2], x[4 * j + 3]), w.y), sx, acc[2 * j + 1]);
                 }
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive(smem_u32(&sempty[slot]));
-                if (++slot == kScaleRing) {
-                    slot = 0;
-                    sphase ^= 1;
-                }
-                if (++buf == kAcc) {
-                    buf = 0;
-                    tphase ^= 1;
+                if (n % kScaleGroup == kScaleGroup - 1) {
+                    __syncwarp();
+                    mbar_arrive_if(smem_u32(&sempty[n / kScaleGroup % kScaleRing]), lane == 0);
                 }
             }
             if (!ok || cluster > 1)
                 break;  // a cluster has one tile, finished below
-            int b, x0, y0;
-            decode(p, t, BN, b, x0, y0);
+            int b, x0, xend, y0;
+            decode(p, t, BN, b, x0, xend, y0);
             const int x = x0 + 32 * q + lane, y = y0 + C::COLS * ch;
             const auto store = [&](auto ot) {
                 using S = OutStore<decltype(ot)::value>;
@@ -314,7 +301,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     float v0, v1;
                     unpack2(acc[j / 2], v0, v1);
                     acc[j / 2] = 0;
-                    if (x < p.N) {
+                    if (x < xend) {
                         if (y + j < p.M)
                             S::st1(d, v0);
                         if (y + j + 1 < p.M)
@@ -348,8 +335,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     if (cluster > 1) {
         cluster_sync();
-        int b, x0, y0;
-        decode(p, first, BN, b, x0, y0);
+        int b, x0, xend, y0;
+        decode(p, first, BN, b, x0, xend, y0);
         const int n = min(BN, p.M - y0) * BM;
         const int lo = static_cast<int>(static_cast<int64_t>(n) * rank / cluster);
         const int hi = static_cast<int>(static_cast<int64_t>(n) * (rank + 1) / cluster);
@@ -359,7 +346,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int r = 0; r < cluster; ++r)
                 s += ld_cluster(mapa_shared(base + 4 * i, r));
             const int x = x0 + i % BM, y = y0 + i / BM;
-            if (x < p.N) {
+            if (x < xend) {
                 const int64_t o = b * p.stride_o + static_cast<int64_t>(y) * p.ldo + x;
                 if (p.out_type == kOutF16)
                     OutStore<kOutF16>::st1(static_cast<uint16_t*>(p.out) + o, s);
@@ -382,12 +369,17 @@ cudaError_t launch(BlkParams p, int num_sms, cudaStream_t stream)
 {
     CUtensorMap tmx, tmy;
     const int type = p.e5m2 ? 4 : 3;  // gemm_dtype_t
-    if (!operand_map(&tmx, p.B, p.N, p.K, p.ldb, p.batch, p.stride_b, BM, &p.b_bmul, type) ||
+    // One wave of shares of 64 to 128 rows, with boxes just as tall (the MMA's other
+    // rows hold what a slot last held and are not stored): 64 x 16384 x 8192 on all
+    // SMs instead of 128 of them.
+    p.row_share = p.batch == 1 && p.M <= BN && p.N >= 64 * num_sms && p.N <= 128 * num_sms;
+    p.x_box = p.row_share ? std::min(BM, ((p.N + num_sms - 1) / num_sms + 7) / 8 * 8) : BM;
+    if (!operand_map(&tmx, p.B, p.N, p.K, p.ldb, p.batch, p.stride_b, p.x_box, &p.b_bmul, type) ||
         !operand_map(&tmy, p.A, p.M, p.K, p.lda, p.batch, p.stride_a, BN, &p.a_bmul, type))
         return cudaErrorInvalidValue;
     p.tiles_m = (p.M + BN - 1) / BN;
     p.tiles_n = (p.N + BM - 1) / BM;
-    p.num_tiles = p.tiles_m * p.tiles_n * p.batch;
+    p.num_tiles = p.row_share ? num_sms : p.tiles_m * p.tiles_n * p.batch;
     // split K while whole clusters still fit the GPU and a CTA keeps 4 K blocks
     int c = 1;
     while (c < kMaxCluster && p.num_tiles * 2 * c <= num_sms && p.num_kb >= 8 * c)

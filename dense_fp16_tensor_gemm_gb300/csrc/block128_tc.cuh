@@ -236,6 +236,14 @@ struct ScaleRun {
         }
     }
 
+    // Starts at K block kb instead of 0.
+    __device__ __forceinline__ void skip(int kb)
+    {
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+            src[r] += kb * step;
+    }
+
     // The next K block's scales to shared address `dst`.
     __device__ __forceinline__ void copy(uint32_t dst)
     {

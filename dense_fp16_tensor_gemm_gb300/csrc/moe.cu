@@ -28,6 +28,8 @@
 //
 // Routing is recomputed by every CTA from the logits, a few thousand
 // instructions; that spares a kernel and a round trip through memory.
+#include <algorithm>
+
 #include "gemm_nt.h"
 #include "block128.h"
 #include "ptx.cuh"
@@ -127,7 +129,7 @@ struct Route {
     int* nact;
 };
 
-__host__ __device__ inline int route_bytes(int tokens, int experts, int topk)
+__host__ __device__ constexpr int route_bytes(int tokens, int experts, int topk)
 {
     const int words = (tokens + 31) / 32, slots = tokens * topk, act = experts < slots ? experts : slots;
     const int b = 4 * (experts * words + slots + 1) + 2 * (2 * slots + experts + 2 * (act + 1)) + tokens;
@@ -231,6 +233,87 @@ __device__ __forceinline__ void route_token(const MoeParams& p, const Route& r, 
         r.bad[t] = nan;
 }
 
+// One warp, 32 / L tokens at once, L lanes and VPL keys a lane for each: topk
+// rounds of a maximum over a token's keys, the lowest index among equals.  With
+// many tokens few lanes each are best (64 tokens of 64 experts took 9 thousand
+// cycles a token and warp at a time); with few, whole warps.
+template <int VPL, int L>
+__device__ __forceinline__ void route_tokens(const MoeParams& p, const Route& r, int t0, int lane)
+{
+    const int words = (p.tokens + 31) / 32, sub = lane % L, t = t0 + lane / L;
+    const bool live = t < p.tokens;
+    const float* l = p.logits + (live ? t : 0) * p.ldl;
+    uint32_t key[VPL];
+    bool nan = false;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+        const int e = sub + L * i;
+        const float v = live && e < p.experts ? __fadd_rn(l[e], 0.f) : -INFINITY;  // -0 and 0 tie
+        nan |= v != v;
+        key[i] = order_key(v);
+    }
+    uint32_t top = 0;
+    float all = 0.f;  // sum of exponentials over every expert (softmax before the choice)
+    int taken = 0;
+    float* out_p = r.p + t * p.topk;
+    for (int j = 0; j < p.topk; ++j) {
+        uint32_t best = 0, idx = ~0u;
+#pragma unroll
+        for (int i = 0; i < VPL; ++i)
+            if (key[i] > best) {
+                best = key[i];
+                idx = sub + L * i;
+            }
+        uint32_t m = best;
+#pragma unroll
+        for (int s = 1; s < L; s *= 2)
+            m = max(m, __shfl_xor_sync(0xffffffffu, m, s));
+        uint32_t e = best == m ? idx : ~0u;
+#pragma unroll
+        for (int s = 1; s < L; s *= 2)
+            e = min(e, __shfl_xor_sync(0xffffffffu, e, s));
+        if (m >= kAbove) {
+            if (j == 0) {
+                top = m;
+                if (!p.renorm) {
+#pragma unroll
+                    for (int i = 0; i < VPL; ++i)
+                        if (key[i] >= kAbove)
+                            all += expf(key_value(key[i]) - key_value(m));
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < VPL; ++i)
+                if (e == static_cast<uint32_t>(sub + L * i))
+                    key[i] = 0;
+            taken = j + 1;
+        }
+        if (live && sub == 0) {
+            const bool has = m >= kAbove;
+            r.chosen[t * p.topk + j] = has ? static_cast<uint16_t>(e) : uint16_t(0xffff);
+            out_p[j] = key_value(m);
+            if (has)
+                atomicOr(&r.mask[e * words + t / 32], 1u << (t & 31));
+        }
+    }
+    __syncwarp();
+    float sum = all;
+    if (p.renorm)
+        for (int j = sub; live && j < taken; j += L)
+            sum += expf(out_p[j] - key_value(top));
+#pragma unroll
+    for (int s = 1; s < L; s *= 2) {
+        sum += __shfl_xor_sync(0xffffffffu, sum, s);
+        nan |= __shfl_xor_sync(0xffffffffu, static_cast<int>(nan), s) != 0;
+    }
+    if (live) {
+        for (int j = sub; j < taken; j += L)
+            out_p[j] = nan ? NAN : expf(out_p[j] - key_value(top)) / sum;
+        if (sub == 0)
+            r.bad[t] = nan;
+    }
+}
+
 __device__ __forceinline__ void route_all(const MoeParams& p, const Route& r)
 {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -238,13 +321,19 @@ __device__ __forceinline__ void route_all(const MoeParams& p, const Route& r)
     for (int i = threadIdx.x; i < p.experts * words; i += kThreads)
         r.mask[i] = 0;
     __syncthreads();
-    for (int t = warp; t < p.tokens; t += kWarps) {
-        if (p.experts <= 64)
-            route_token<2>(p, r, t, lane);
-        else if (p.experts <= 256)
-            route_token<8>(p, r, t, lane);
-        else
-            route_token<32>(p, r, t, lane);
+    if (p.tokens > kWarps && p.experts <= 64) {
+        for (int t = warp * 8; t < p.tokens; t += kWarps * 8)
+            route_tokens<16, 4>(p, r, t, lane);
+    } else if (p.tokens > kWarps && p.experts <= 256) {
+        for (int t = warp * 2; t < p.tokens; t += kWarps * 2)
+            route_tokens<16, 16>(p, r, t, lane);
+    } else {
+        for (int t = warp; t < p.tokens; t += kWarps) {
+            if (p.experts <= 64)
+                route_token<2>(p, r, t, lane);
+            else
+                route_token<32>(p, r, t, lane);
+        }
     }
     __syncthreads();
     if (warp == 0) {
@@ -437,27 +526,50 @@ __device__ __forceinline__ void multiply_item(uint32_t st, int nt, float (&c)[MT
 __device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; }
 
 // ---------------------------------------------------------------- up
-// A unit is 8 gate rows and the 8 up rows that go with them (one m16 tile: the
-// MMA's lower accumulator rows are the gates, the upper ones their ups), over
-// all of K, for up to 8*NT of the expert's tokens at a time.  CTAs take even
-// ranges of the units of all active experts; the 8 warps split K and meet once
-// per unit in shared memory.
-template <bool W8, int NT>
+// A unit is 8*MT gate rows and the 8*MT up rows that go with them (MT m16 tiles:
+// an accumulator's lower rows are the gates, its upper ones their ups), over all
+// of K, for up to 8*NT of the expert's tokens at a time.  CTAs take even ranges
+// of the units of all active experts.  KS warps share a unit and split its K:
+// one, where there are units enough for every SM (a warp then ends a unit in its
+// own registers; meeting in shared memory after every 4 items of K took half of
+// 64 tokens' time), or all 8, where there are few and a unit's latency counts.
+template <bool W8, int MT, int NT, int KS>
 struct UpCfg {
-    using S = Stage<W8, 1, NT, 2>;
-    // ring stages, and buffers for the warps' sums: what lets two CTAs share an SM
-    static constexpr int D = NT == 1 || W8 ? 4 : 3;
-    static constexpr int RBUF = NT == 1 ? 2 : 1;
+    using S = Stage<W8, MT, NT, 2>;
+    // Ring stages.  A warp alone on 16-bit weights, or on few tokens, is all latency:
+    // one CTA an SM and deep rings; widening E4M3 wants two CTAs' warps.
+    static constexpr int CTAS = KS == 1 && (NT == 1 || !W8) ? 1 : 2;
+    static constexpr int D = KS > 1 ? (NT == 1 || W8 ? 4 : 3) : (NT == 1 ? (W8 ? 7 : 8) : 3);
+    static constexpr int RBUF = KS == 1 ? 0 : (NT == 1 ? 2 : 1);  // buffers for the warps' sums
     static constexpr int RING = kWarps * D * S::BYTES;
     static constexpr int FIXED = RING + RBUF * kWarps * NT * 4 * 32 * 4;
+    static_assert(KS == 1 || (KS == kWarps && MT == 1), "unit shapes");
 };
 
-template <bool BF16, bool W8, int NT>
-__global__ void __launch_bounds__(kThreads, 2) moe_up_kernel(const MoeParams p)
+// h of one element: where it goes in a row's groups of 8 columns (bf16 heads,
+// then their rests; or, for fp16 weights, fp32).
+template <bool SPLIT>
+__device__ __forceinline__ void store_h(float* row, int i0, int j, float gate, float up)
 {
-    using C = UpCfg<W8, NT>;
+    const float h = gate / (1.f + expf(-gate)) * up;
+    if constexpr (SPLIT) {
+        const __nv_bfloat16 head = __float2bfloat16_rn(h);
+        const float rest = fabsf(h) < INFINITY ? h - __bfloat162float(head) : 0.f;
+        __nv_bfloat16* o = reinterpret_cast<__nv_bfloat16*>(row + i0) + j;
+        o[0] = head;
+        o[8] = __float2bfloat16_rn(rest);
+    } else {
+        row[i0 + j] = h;
+    }
+}
+
+template <bool BF16, bool W8, int MT, int NT, int KS>
+__global__ void __launch_bounds__(kThreads, UpCfg<W8, MT, NT, KS>::CTAS) moe_up_kernel(const MoeParams p)
+{
+    using C = UpCfg<W8, MT, NT, KS>;
     using S = typename C::S;
     constexpr int D = C::D;
+    constexpr bool SPLIT = BF16 || W8;
     extern __shared__ __align__(16) uint8_t smem[];
     float* red = reinterpret_cast<float*>(smem + C::RING);
     const Route r = route_carve(smem + C::FIXED, p);
@@ -469,11 +581,13 @@ __global__ void __launch_bounds__(kThreads, 2) moe_up_kernel(const MoeParams p)
     pdl_launch_dependents();
     route_all(p, r);
 
-    const int tiles = ceil_div(p.inner, 8), nit = ceil_div(p.hidden, kItem);
+    const int tiles = ceil_div(p.inner, 8 * MT), nit = ceil_div(p.hidden, kItem);
     const int64_t units = static_cast<int64_t>(*r.nact) * tiles;
-    const int u0 = static_cast<int>(units * blockIdx.x / gridDim.x);
+    // this warp's units: u0, u0 + step, ... < u1, K items [ks0, ks1)
+    constexpr int step = kWarps / KS;
+    const int u0 = static_cast<int>(units * blockIdx.x / gridDim.x) + warp / KS;
     const int u1 = static_cast<int>(units * (blockIdx.x + 1) / gridDim.x);
-    const int ks0 = nit * warp / kWarps, ks1 = nit * (warp + 1) / kWarps;
+    const int ks0 = nit * (warp % KS) / KS, ks1 = nit * (warp % KS + 1) / KS;
     const uint32_t ring = smem_u32(smem) + warp * D * S::BYTES + lane * 16;
     constexpr int ES = W8 ? 1 : 2;
     const uint8_t* xb = static_cast<const uint8_t*>(p.x);
@@ -482,22 +596,28 @@ __global__ void __launch_bounds__(kThreads, 2) moe_up_kernel(const MoeParams p)
     // Loader: the items (unit, token group, K item) of this warp in order, by
     // pointers to the lane's own bytes.  Rows outside the matrix, and tokens past
     // the group, read nothing of row 0.
-    int lu = u0, lg = 0, lk = ks0, lslot = 0, lgroups = 0, wbytes = 0;
-    const uint8_t *wg = wb, *wu = wb;
+    int lu = u0, lg = 0, lk = ks0, lslot = 0, lgroups = 0;
+    const uint8_t* wr[2 * MT];  // gate and up row of each m16 tile
     const uint8_t* xr[NT];
-    uint32_t xbytes = 0;  // bit q: token of tile q
+    uint32_t wbytes = 0, xbytes = 0;  // bit m: tile m's rows are inside; bit q: token of tile q
     auto load_next = [&] {
         if (ks0 < ks1 && lu < u1) {
             if (lk == ks0) {
-                const int a = lu / tiles, i = (lu - a * tiles) * 8 + g;
+                const int a = lu / tiles, i0 = (lu - a * tiles) * (8 * MT) + g;
                 const int n = r.aoff[a + 1] - r.aoff[a];
                 lgroups = ceil_div(n, 8 * NT);
                 const uint8_t* we = wb + static_cast<int64_t>(r.act[a]) * p.stride_w13 * ES + ks0 * (kItem * ES) + t * 16;
-                const bool in = i < p.inner;
-                wbytes = in ? 16 : 0;
-                wg = we + (in ? static_cast<int64_t>(i) * p.ldw13 * ES : 0);
-                wu = we + (in ? static_cast<int64_t>(p.inner + i) * p.ldw13 * ES : 0);
-                xbytes = 0;
+                wbytes = xbytes = 0;
+#pragma unroll
+                for (int m = 0; m < MT; ++m) {
+                    const int i = i0 + 8 * m;
+                    wr[2 * m] = wr[2 * m + 1] = we;
+                    if (i < p.inner) {
+                        wr[2 * m] += static_cast<int64_t>(i) * p.ldw13 * ES;
+                        wr[2 * m + 1] += static_cast<int64_t>(p.inner + i) * p.ldw13 * ES;
+                        wbytes |= 1u << m;
+                    }
+                }
 #pragma unroll
                 for (int q = 0; q < NT; ++q) {
                     const int j = lg * 8 * NT + q * 8 + g;
@@ -511,8 +631,12 @@ __global__ void __launch_bounds__(kThreads, 2) moe_up_kernel(const MoeParams p)
             const uint32_t st = ring + lslot * S::BYTES;
             const bool inside = (lk + 1) * kItem <= p.hidden;
             const int left = p.hidden - lk * kItem, w0 = (left - half_k<W8>(t, 0)) * ES, w1 = (left - half_k<W8>(t, 1)) * ES;
-            load_chunks<S::PER_ROW, 1, 64, true>(st, wg, wbytes, inside, w0, w1, p.vec_13);
-            load_chunks<S::PER_ROW, 1, 64, true>(st + S::PER_ROW * 512, wu, wbytes, inside, w0, w1, p.vec_13);
+#pragma unroll
+            for (int m = 0; m < 2 * MT; ++m) {
+                load_chunks<S::PER_ROW, 1, 64, true>(st + m * S::PER_ROW * 512, wr[m], wbytes >> (m / 2) & 1 ? 16 : 0,
+                                                     inside, w0, w1, p.vec_13);
+                wr[m] += kItem * ES;
+            }
 #pragma unroll
             for (int q = 0; q < NT; ++q) {
                 load_chunks<2, 1, W8 ? 16 : 64, false>(st + (S::W_LINES + q * 2) * 512, xr[q], xbytes >> q & 1 ? 16 : 0,
@@ -520,13 +644,11 @@ __global__ void __launch_bounds__(kThreads, 2) moe_up_kernel(const MoeParams p)
                                                        (left - half_k<W8>(t, 1)) * 2, p.vec_x);
                 xr[q] += kItem * 2;
             }
-            wg += kItem * ES;
-            wu += kItem * ES;
             if (++lk == ks1) {
                 lk = ks0;
                 if (++lg == lgroups) {
                     lg = 0;
-                    ++lu;
+                    lu += step;
                 }
             }
         }
@@ -539,78 +661,87 @@ __global__ void __launch_bounds__(kThreads, 2) moe_up_kernel(const MoeParams p)
 
     int slot = 0, parity = 0;
 #pragma unroll 1
-    for (int u = u0; u < u1; ++u) {
-        const int a = u / tiles, i0 = (u - a * tiles) * 8;
+    for (int u = u0; u < u1; u += step) {
+        const int a = u / tiles, i0 = (u - a * tiles) * (8 * MT);
         const int first = r.aoff[a], n = r.aoff[a + 1] - first;
-        const float *pg = nullptr, *pu = nullptr;  // the lane's rows' scales
+        const float* ps[2 * MT];  // the lane's rows' scales
         if (W8) {
-            const int i = min(i0 + g, p.inner - 1);
             const float* se = p.s13.data + r.act[a] * p.s13.bs;
-            pg = se + static_cast<int64_t>(i >> p.s13.shift) * p.s13.rs;
-            pu = se + static_cast<int64_t>((p.inner + i) >> p.s13.shift) * p.s13.rs;
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+                const int i = min(i0 + 8 * m + g, p.inner - 1);
+                ps[2 * m] = se + static_cast<int64_t>(i >> p.s13.shift) * p.s13.rs;
+                ps[2 * m + 1] = se + static_cast<int64_t>((p.inner + i) >> p.s13.shift) * p.s13.rs;
+            }
         }
 #pragma unroll 1
         for (int g0 = 0; g0 < n; g0 += 8 * NT) {
             const int nt = min(NT, ceil_div(n - g0, 8));
-            float c[1][NT][4] = {};
+            float c[MT][NT][4] = {};
 #pragma unroll 1
             for (int k = ks0; k < ks1; ++k) {
-                float sg = 0.f, su = 0.f;
+                float s[2 * MT];
                 if (W8) {
                     const int64_t kb = static_cast<int64_t>(k >> 1) * p.s13.ks;  // an item is half a block of 128
-                    sg = __ldg(pg + kb);
-                    su = __ldg(pu + kb);
+#pragma unroll
+                    for (int m = 0; m < 2 * MT; ++m)
+                        s[m] = __ldg(ps[m] + kb);
                 }
                 cp_async_wait<D - 2>();
                 if constexpr (W8) {
-                    float part[1][NT][4] = {};
-                    multiply_item<kPlain, BF16, W8, 1, NT>(ring + slot * S::BYTES, nt, part);
+                    float part[MT][NT][4] = {};
+                    multiply_item<kPlain, BF16, W8, MT, NT>(ring + slot * S::BYTES, nt, part);
 #pragma unroll
-                    for (int q = 0; q < NT; ++q) {
-                        c[0][q][0] = fmaf(part[0][q][0], sg, c[0][q][0]);
-                        c[0][q][1] = fmaf(part[0][q][1], sg, c[0][q][1]);
-                        c[0][q][2] = fmaf(part[0][q][2], su, c[0][q][2]);
-                        c[0][q][3] = fmaf(part[0][q][3], su, c[0][q][3]);
-                    }
+                    for (int m = 0; m < MT; ++m)
+#pragma unroll
+                        for (int q = 0; q < NT; ++q)
+#pragma unroll
+                            for (int v = 0; v < 4; ++v)
+                                c[m][q][v] = fmaf(part[m][q][v], s[2 * m + (v >> 1)], c[m][q][v]);
                 } else {
-                    multiply_item<kPlain, BF16, W8, 1, NT>(ring + slot * S::BYTES, nt, c);
+                    multiply_item<kPlain, BF16, W8, MT, NT>(ring + slot * S::BYTES, nt, c);
                 }
                 slot = slot + 1 == D ? 0 : slot + 1;
                 load_next();
             }
-            float* rd = red + parity * (kWarps * NT * 4 * 32);
-            if (C::RBUF == 2)
-                parity ^= 1;  // the other buffer is rewritten only after the next unit's barrier
-            else
-                __syncthreads();
+            // Columns past inner, to the end of their 8, get zeros (their rows were).
+            if constexpr (KS == 1) {
 #pragma unroll
-            for (int q = 0; q < NT; ++q)
+                for (int q = 0; q < NT; ++q)
 #pragma unroll
-                for (int v = 0; v < 4; ++v)
-                    rd[((warp * NT + q) * 4 + v) * 32 + lane] = c[0][q][v];
-            __syncthreads();
-            for (int idx = threadIdx.x; idx < nt * 64; idx += kThreads) {
-                const int l = idx & 31, wh = (idx >> 5) & 1, q = idx >> 6;
-                float gate = 0.f, up = 0.f;
+                    for (int v = 0; v < 2; ++v) {
+                        const int j = g0 + q * 8 + 2 * t + v;
+                        if (j < n) {
+                            float* row = p.h + r.list[first + j] * p.ldh;
 #pragma unroll
-                for (int w = 0; w < kWarps; ++w) {
-                    gate += rd[((w * NT + q) * 4 + wh) * 32 + l];
-                    up += rd[((w * NT + q) * 4 + 2 + wh) * 32 + l];
-                }
-                const int i = i0 + (l >> 2), j = g0 + q * 8 + 2 * (l & 3) + wh;
-                if (j < n) {  // columns past inner, to the end of the 8, get zeros
-                    const float h = gate / (1.f + expf(-gate)) * up;
-                    float* row = p.h + r.list[first + j] * p.ldh;
-                    if constexpr (BF16 || W8) {
-                        // groups of 8 columns: their 8 bf16 heads, then their 8 rests
-                        const __nv_bfloat16 head = __float2bfloat16_rn(h);
-                        const float rest = fabsf(h) < INFINITY ? h - __bfloat162float(head) : 0.f;
-                        __nv_bfloat16* o = reinterpret_cast<__nv_bfloat16*>(row + i0) + (l >> 2);
-                        o[0] = head;
-                        o[8] = __float2bfloat16_rn(rest);
-                    } else {
-                        row[i] = h;
+                            for (int m = 0; m < MT; ++m)
+                                if (i0 + 8 * m < p.inner)
+                                    store_h<SPLIT>(row, i0 + 8 * m, g, c[m][q][v], c[m][q][2 + v]);
+                        }
                     }
+            } else {
+                float* rd = red + parity * (kWarps * NT * 4 * 32);
+                if (C::RBUF == 2)
+                    parity ^= 1;  // the other buffer is rewritten only after the next unit's barrier
+                else
+                    __syncthreads();
+#pragma unroll
+                for (int q = 0; q < NT; ++q)
+#pragma unroll
+                    for (int v = 0; v < 4; ++v)
+                        rd[((warp * NT + q) * 4 + v) * 32 + lane] = c[0][q][v];
+                __syncthreads();
+                for (int idx = threadIdx.x; idx < nt * 64; idx += kThreads) {
+                    const int l = idx & 31, wh = (idx >> 5) & 1, q = idx >> 6;
+                    float gate = 0.f, up = 0.f;
+#pragma unroll
+                    for (int w = 0; w < kWarps; ++w) {
+                        gate += rd[((w * NT + q) * 4 + wh) * 32 + l];
+                        up += rd[((w * NT + q) * 4 + 2 + wh) * 32 + l];
+                    }
+                    const int j = g0 + q * 8 + 2 * (l & 3) + wh;
+                    if (j < n)
+                        store_h<SPLIT>(p.h + r.list[first + j] * p.ldh, i0, l >> 2, gate, up);
                 }
             }
         }
@@ -632,7 +763,7 @@ struct DownCfg {
     static constexpr int RING = kWarps * D * S::BYTES;
 };
 
-__host__ __device__ inline int down_sum_bytes(int tokens, int mt) { return kWarps * tokens * 16 * mt * 4; }
+__host__ __device__ constexpr int down_sum_bytes(int tokens, int mt) { return kWarps * tokens * 16 * mt * 4; }
 
 template <bool BF16, bool W8, int NT, int MT>
 __global__ void __launch_bounds__(kThreads, MT == 1 && NT == 1 ? 2 : 1) moe_down_kernel(const MoeParams p, int cluster)
@@ -827,10 +958,34 @@ constexpr int kMaxSmem = 232448;
 template <bool BF16, bool W8, int NT, int MT>
 cudaError_t configure_one()
 {
-    cudaError_t e = cudaFuncSetAttribute(moe_up_kernel<BF16, W8, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
+    constexpr auto attr = cudaFuncAttributeMaxDynamicSharedMemorySize;
+    cudaError_t e = cudaFuncSetAttribute(moe_up_kernel<BF16, W8, 1, NT, kWarps>, attr, kMaxSmem);
     if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(moe_down_kernel<BF16, W8, NT, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
+        e = cudaFuncSetAttribute(moe_up_kernel<BF16, W8, NT, NT, 1>, attr, kMaxSmem);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(moe_down_kernel<BF16, W8, NT, MT>, attr, kMaxSmem);
     return e;
+}
+
+template <bool BF16, bool W8, int MT, int NT, int KS>
+cudaError_t launch_up(const MoeParams& p, int64_t reach, int num_sms, cudaStream_t stream)
+{
+    using C = UpCfg<W8, MT, NT, KS>;
+    const int64_t units = reach * ((p.inner + 8 * MT - 1) / (8 * MT));
+    const int64_t ctas = KS == 1 ? (units + kWarps - 1) / kWarps : units;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    // one unit a warp and every SM in use before an SM takes more
+    cfg.gridDim = dim3(static_cast<unsigned>(
+        std::min<int64_t>(C::CTAS * num_sms, KS == 1 ? std::max<int64_t>(ctas, std::min<int64_t>(units, num_sms)) : ctas)));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = C::FIXED + route_bytes(p.tokens, p.experts, p.topk);
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, moe_up_kernel<BF16, W8, MT, NT, KS>, p);
 }
 
 template <bool BF16, bool W8, int NT, int MT>
@@ -840,33 +995,27 @@ cudaError_t launch_one(const MoeParams& p, int num_sms, cudaStream_t stream)
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
-    const int64_t reach = p.experts < p.tokens * p.topk ? p.experts : p.tokens * p.topk;  // most experts in use
-    {
-        cudaLaunchConfig_t cfg = {};
-        const int64_t units = reach * ((p.inner + 7) / 8);
-        cfg.gridDim = dim3(static_cast<unsigned>(units < 2 * num_sms ? units : 2 * num_sms));
-        cfg.blockDim = dim3(kThreads);
-        cfg.dynamicSmemBytes = UpCfg<W8, NT>::FIXED + rb;
-        cfg.stream = stream;
-        cfg.attrs = attr;
-        cfg.numAttrs = 1;
-        const cudaError_t e = cudaLaunchKernelEx(&cfg, moe_up_kernel<BF16, W8, NT>, p);
-        if (e != cudaSuccess)
-            return e;
-    }
+    const int64_t reach = std::min<int64_t>(p.experts, int64_t(p.tokens) * p.topk);  // most experts in use
+    // Units of 8*NT columns for a warp alone once there are four for every SM.
+    const bool many = reach * ((p.inner + 8 * NT - 1) / (8 * NT)) >= 4 * num_sms;
+    const cudaError_t e = many ? launch_up<BF16, W8, NT, NT, 1>(p, reach, num_sms, stream)
+                               : launch_up<BF16, W8, 1, NT, kWarps>(p, reach, num_sms, stream);
+    if (e != cudaSuccess)
+        return e;
     // The largest clusters whose CTAs are all resident at once, two on an SM (one,
     // where a CTA takes most of its shared memory), as long as each warp keeps a
     // few items: a second wave of 512 CTAs after 304 cost one token 9 of 26 us.
     const int tiles = (p.hidden + 16 * MT - 1) / (16 * MT);
     const int64_t items = reach * ((p.inner + kItem - 1) / kItem);
-    const int want = num_sms * (MT == 1 && NT == 1 ? 2 : 1);
+    const int smem = DownCfg<W8, NT, MT>::RING + down_sum_bytes(p.tokens, MT) + rb;
+    const int want = num_sms * (MT == 1 && NT == 1 && smem <= kMaxSmem / 2 - 2048 ? 2 : 1);
     int c = 1;
     while (c < 8 && 2 * tiles * c <= want && items >= 2 * 2 * c * kWarps)
         c *= 2;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(tiles * c));
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = DownCfg<W8, NT, MT>::RING + down_sum_bytes(p.tokens, MT) + rb;
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     attr[1].id = cudaLaunchAttributeClusterDimension;
     attr[1].val.clusterDim.x = static_cast<unsigned>(c);
@@ -876,19 +1025,33 @@ cudaError_t launch_one(const MoeParams& p, int num_sms, cudaStream_t stream)
     return cudaLaunchKernelEx(&cfg, moe_down_kernel<BF16, W8, NT, MT>, p, c);
 }
 
-// Up to 8 tokens: one token tile, 16 rows a warp.  More: two token tiles, and 32
-// rows a warp in the down kernel, which halves how often h is read from L2, while
-// the sums of 32 rows fit beside the rings.
+// One token tile and 16 rows a warp where an expert hardly ever has more than 8
+// tokens: up to 8 of them, or up to 4 on average for an expert (16 tokens on 2 of
+// 8 experts); an expert that has more reads its weights again, from L2.  Else two
+// token tiles, and 32 rows a warp, which halves how often x and h are read; in
+// the down kernel only while the sums of 32 rows fit beside the rings.
 template <bool BF16, bool W8>
 cudaError_t launch_typed(const MoeParams& p, int num_sms, cudaStream_t stream)
 {
-    if (p.tokens <= 8)
+    const int rb = route_bytes(p.tokens, p.experts, p.topk);
+    if ((p.tokens <= 8 || p.tokens * p.topk <= 4 * p.experts) && UpCfg<W8, 1, 1, 1>::FIXED + rb <= kMaxSmem &&
+        DownCfg<W8, 1, 1>::RING + down_sum_bytes(p.tokens, 1) + rb <= kMaxSmem)
         return launch_one<BF16, W8, 1, 1>(p, num_sms, stream);
-    if (p.tokens <= 64 && DownCfg<W8, 2, 2>::RING + down_sum_bytes(p.tokens, 2) +
-                                  route_bytes(p.tokens, p.experts, p.topk) <= kMaxSmem)
+    if (p.tokens <= 64 && DownCfg<W8, 2, 2>::RING + down_sum_bytes(p.tokens, 2) + rb <= kMaxSmem)
         return launch_one<BF16, W8, 2, 2>(p, num_sms, stream);
     return launch_one<BF16, W8, 2, 1>(p, num_sms, stream);
 }
+
+// The last form takes anything within the limits.
+static_assert(UpCfg<false, 2, 2, 1>::FIXED + route_bytes(kMoeMaxTokens, kMoeMaxExperts, kMoeMaxTopk) <= kMaxSmem &&
+                  UpCfg<false, 1, 2, kWarps>::FIXED + route_bytes(kMoeMaxTokens, kMoeMaxExperts, kMoeMaxTopk) <= kMaxSmem &&
+                  UpCfg<true, 2, 2, 1>::FIXED + route_bytes(kMoeMaxTokens, kMoeMaxExperts, kMoeMaxTopk) <= kMaxSmem &&
+                  UpCfg<true, 1, 2, kWarps>::FIXED + route_bytes(kMoeMaxTokens, kMoeMaxExperts, kMoeMaxTopk) <= kMaxSmem &&
+                  DownCfg<false, 2, 1>::RING + down_sum_bytes(kMoeMaxTokens, 1) +
+                          route_bytes(kMoeMaxTokens, kMoeMaxExperts, kMoeMaxTopk) <= kMaxSmem &&
+                  DownCfg<true, 2, 1>::RING + down_sum_bytes(kMoeMaxTokens, 1) +
+                          route_bytes(kMoeMaxTokens, kMoeMaxExperts, kMoeMaxTopk) <= kMaxSmem,
+              "shared memory at the limits");
 
 template <bool BF16, bool W8>
 cudaError_t configure_typed()
