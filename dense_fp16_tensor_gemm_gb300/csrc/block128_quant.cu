@@ -183,11 +183,10 @@ __global__ void __launch_bounds__(256, XT == GEMM_DTYPE_F32 ? 2 : (R == 8 ? 3 : 
     static_assert(R == 8 || (!TILE && !T), "column and tile maxima need all 128 rows");
     constexpr float F = E5M2 ? 57344.f : 448.f;
     constexpr float kInvF = 1.f / F;
-    constexpr int kPitchT = 128 + 16;
     using D = Tile<XT, R>;
     constexpr int CW = 16 * D::W;  // words of a warp's column maxima
-    __shared__ __align__(16) uint8_t tq[T ? 128 * kPitchT : 16];
-    __shared__ uint32_t cmax[T || TILE ? 8 : 1][T || TILE ? CW : 1];
+    __shared__ __align__(16) uint8_t tq[T ? 128 * 128 : 16];  // column c's 128 codes, swizzled (below)
+    __shared__ __align__(16) uint32_t cmax[T || TILE ? 8 : 1][T || TILE ? CW : 1];
     __shared__ __align__(16) float cfac[T || TILE ? 128 : 4];  // columns' factors (TILE: their maxima)
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t col0 = static_cast<int64_t>(blockIdx.x) * 128;
@@ -205,8 +204,8 @@ __global__ void __launch_bounds__(256, XT == GEMM_DTYPE_F32 ? 2 : (R == 8 ? 3 : 
             d.col_max(m);
             if (lane < 16) {
 #pragma unroll
-                for (int j = 0; j < D::W; ++j)
-                    cmax[warp][tx * D::W + j] = m[j];
+                for (int j = 0; j < D::W; j += 4)
+                    *reinterpret_cast<uint4*>(&cmax[warp][tx * D::W + j]) = make_uint4(m[j], m[j + 1], m[j + 2], m[j + 3]);
             }
             __syncthreads();
             if (threadIdx.x < CW) {  // a word's columns: their maxima, factors and scales
@@ -287,7 +286,10 @@ __global__ void __launch_bounds__(256, XT == GEMM_DTYPE_F32 ? 2 : (R == 8 ? 3 : 
                 const uint2 w = make_uint2(
                     pack4<E5M2>(d.get(0, j) * r, d.get(1 % R, j) * r, d.get(2 % R, j) * r, d.get(3 % R, j) * r),
                     pack4<E5M2>(d.get(4 % R, j) * r, d.get(5 % R, j) * r, d.get(6 % R, j) * r, d.get(7 % R, j) * r));
-                *reinterpret_cast<uint2*>(tq + (tx * 8 + j) * kPitchT + ty * 8) = w;
+                // 16-byte chunk ty / 2 of column 8 tx + j at chunk ^ (tx % 8), its halves
+                // exchanged for tx >= 8: the 16 lanes of a row of threads fill 128 bytes
+                *reinterpret_cast<uint2*>(tq + (tx * 8 + j) * 128 + (((ty >> 1) ^ (tx & 7)) << 4) +
+                                          (((ty ^ (tx >> 3)) & 1) << 3)) = w;
             }
             __syncthreads();
             const int nrow = static_cast<int>(min(static_cast<int64_t>(128), p.rows - row0));
@@ -295,7 +297,9 @@ __global__ void __launch_bounds__(256, XT == GEMM_DTYPE_F32 ? 2 : (R == 8 ? 3 : 
             for (int e = 0; e < 4; ++e) {
                 const int c = (threadIdx.x >> 3) + 32 * e, r = (threadIdx.x & 7) * 16;
                 if (col0 + c < p.cols && r < nrow) {
-                    const uint4 w = *reinterpret_cast<const uint4*>(tq + c * kPitchT + r);
+                    uint4 w = *reinterpret_cast<const uint4*>(tq + c * 128 + (r ^ ((c >> 3 & 7) << 4)));
+                    if (c >= 64)
+                        w = make_uint4(w.z, w.w, w.x, w.y);
                     uint8_t* o = p.qt + (col0 + c) * p.ldqt + row0 + r;
                     if (p.vec_qt && r + 16 <= nrow) {
                         *reinterpret_cast<uint4*>(o) = w;
