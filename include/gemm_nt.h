@@ -377,10 +377,10 @@ gemm_status_t gemm_nt_block128_quantize(const void *X, gemm_dtype_t x_type, int6
  * ldw13 and ldw2, expert strides strideW13 and strideW2, are of x_type, or
  * E4M3 with scales S13 and S2 (rows 1 or 128, batch_stride the expert stride;
  * null for 16-bit weights).  Only the weights of experts that a token chose are
- * read.  Products run on the warp MMA in tf32, which holds every 16- and 8-bit
- * value exactly, with fp32 accumulation; h stays in fp32 (its products are taken
- * in two tf32 parts), and Out is rounded once to x_type.  Sums over experts
- * follow the expert index, so results do not depend on the run.
+ * read.  x and the weights are multiplied exactly (8-bit weights widened to 16
+ * bits) with fp32 accumulation; h is computed in fp32 and multiplied in two parts
+ * that hold at least 16 significant bits of it; Out is rounded once to x_type.
+ * Sums over experts follow the expert index, so results do not depend on the run.
  *
  * tokens <= 128, experts <= 1024, topk <= min(32, experts): more is
  * GEMM_ERR_NOT_SUPPORTED.  `workspace` (device memory, 16-byte aligned, the
