@@ -13,10 +13,14 @@
 // operation for every two of them (300 cycles; two, where B has a scale for
 // every row).  Two accumulators of 256 columns fill Tensor Memory; what bounds
 // the kernel is the round trip of one: MMA, commit to both CTAs, loads and
-// arithmetic, release to the leader.  Measured per block (4864 x 4096 x 8192):
-// 519 ns, 300 ns with the loads and the arithmetic left out; halves of 128
-// columns, which shorten the trip, take 582 (A is read twice and shared memory
-// fills up); 16 warps with 64 sums each 760.
+// arithmetic, release to the leader.  Measured per block (4864 x 4096, K from
+// 2048 to 8192): 410 ns, 620 where B has a scale for every row; 310 with the
+// arithmetic left out, 345 with the loads left out.  Halves of 128 columns, which
+// shorten the trip, are slower (A is read twice and shared memory fills up), as
+// are 16 warps with 64 sums each, scalar arithmetic (452) and loads of 16 rows x
+// 64 columns, which let a column's scale serve two rows (510 and 655).  A tile's
+// epilogue adds 1.5 us (16-bit Out) to 3 us (fp32): its registers are the sums.
+// 8192 x 8192 x 8192 into bf16: 442 us (2490 TFLOP/s).
 //
 // Roles per CTA (384 threads): warp 0 TMA producer; warps 1 and 3 in the leader
 // MMA issue; warp 2 brings the scales into a ring of their own (any strides);
@@ -52,7 +56,8 @@ constexpr int kOpBytes = BM * kRowBytes;    // one CTA's half of A, and of B
 constexpr int kScaleRing = 4;               // slots of kScaleGroup K blocks
 constexpr int kScaleGroup = 4;
 constexpr int kScaleFloats = 128 + 256;     // rows' scales, then columns' (or the two column blocks')
-constexpr int kStageWords = 32 * 16;        // a promotion warp's staging area: 32 rows of 64 bytes
+constexpr int kStagePitch = 40;             // words of a staging row: 8 of the piece before, then 32
+constexpr int kStageWords = 32 * kStagePitch;  // a promotion warp's staging area
 constexpr int kTmemCols = 512;
 constexpr int kBarBytes = 512;
 constexpr int kSmem = 1024 + kStages * 2 * kOpBytes + kScaleRing * kScaleGroup * kScaleFloats * 4 + kPromoWarps * kStageWords * 4 + kBarBytes;
@@ -77,68 +82,105 @@ __device__ __forceinline__ int blocks_of(const BlkParams& p, int pair, int pairs
     return (p.num_tiles - pair + pairs - 1) / pairs * p.num_kb;
 }
 
+// Word w of row r of a staging area.  16-byte slots change places in pairs in rows
+// 4-7 of every 8, so that the 8 rows a phase of 16-byte stores writes fall on
+// different banks.
+__device__ __forceinline__ int staged(int r, int w) { return r * kStagePitch + (w ^ (r & 4)); }
+
 // Stores a promotion warp's 32 rows x 128 columns, a row per thread, through its
-// staging area: 64 bytes of every row at a time, in 16-byte slots XOR-swizzled
-// by row so that neither side has bank conflicts, leave as whole row segments.
-template <int OT>
+// staging area.  128 bytes of every row at a time leave as whole row segments:
+// 16-byte words where Out's rows lie on 16-byte boundaries; else each row's
+// segments start on its own 32-byte boundary, up to 8 words back in the piece
+// before (which are staged again), so that memory gets whole sectors whatever
+// the pitch, and what is left of a row follows the last piece.  Reads of the
+// staging area go ahead of a batch's stores: one at a time the two latencies add up.
+template <int OT, int C = 0>
 __device__ __forceinline__ void store_tile(const BlkParams& p, const uint64_t (&acc)[kCols / 2], uint32_t* stage, int b,
                                            int row0, int col0, int lane)
 {
     using S = OutStore<OT>;
-    constexpr int PER_WORD = OT == kOutF32 ? 1 : 2, SEG = 16 * PER_WORD;  // elements of a word, of a segment
-    typename S::T* out = static_cast<typename S::T*>(p.out) + b * p.stride_o;
+    using T = typename S::T;
+    constexpr int PER_WORD = OT == kOutF32 ? 1 : 2, SEG = 32 * PER_WORD, BACK = 8 * PER_WORD;  // elements
+    T* out = static_cast<T*>(p.out) + b * p.stride_o + static_cast<int64_t>(row0) * p.ldo + col0;
+    const int rows = min(p.M - row0, 32), cols = min(kCols, p.N - col0);
     const bool wide = p.vec >= 4 * PER_WORD;  // rows on 16-byte boundaries
 #pragma unroll
-    for (int c = 0; c < kCols; c += SEG) {
-        uint32_t w[16];
+    for (int w = C ? 0 : 8; w < kStagePitch; w += 4) {
+        uint32_t v[4];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
+        for (int i = 0; i < 4; ++i) {
+            const int e = C - BACK + (w + i) * PER_WORD;
             if constexpr (OT == kOutF32) {
                 float f[2];
-                unpack2(acc[(c + i) / 2], f[0], f[1]);
-                w[i] = __float_as_uint(f[i & 1]);
+                unpack2(acc[e / 2], f[0], f[1]);
+                v[i] = __float_as_uint(f[i & 1]);
             } else {
                 float f0, f1;
-                unpack2(acc[c / 2 + i], f0, f1);
-                w[i] = S::pack(f0, f1);
+                unpack2(acc[e / 2], f0, f1);
+                v[i] = S::pack(f0, f1);
             }
         }
-        uint4* s4 = reinterpret_cast<uint4*>(stage);
+        *reinterpret_cast<uint4*>(stage + staged(lane, w)) = make_uint4(v[0], v[1], v[2], v[3]);
+    }
+    __syncwarp();
+    if (wide && C + SEG <= cols) {
+        uint4 v[8];
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            s4[lane * 4 + (j ^ ((lane >> 1) & 3))] = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
-        __syncwarp();
-        const int cs = col0 + c;
-        if (wide && cs + SEG <= p.N) {
+        for (int i = 0; i < 8; ++i)
+            v[i] = *reinterpret_cast<const uint4*>(stage + staged(4 * i + (lane >> 3), 8 + 4 * (lane & 7)));
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int r = 8 * i + (lane >> 2), j = lane & 3;
-                if (row0 + r < p.M)
-                    __stcs(reinterpret_cast<uint4*>(out + static_cast<int64_t>(row0 + r) * p.ldo + cs) + j,
-                           s4[r * 4 + (j ^ ((r >> 1) & 3))]);
-            }
-        } else {
-            const int word = lane & 15, col = cs + word * PER_WORD;
-#pragma unroll 8
-            for (int i = 0; i < 16; ++i) {
-                const int r = 2 * i + (lane >> 4);
-                const uint32_t v = stage[r * 16 + (((word >> 2) ^ ((r >> 1) & 3)) << 2) + (word & 3)];
-                if (row0 + r < p.M && col < p.N) {
-                    typename S::T* d = out + static_cast<int64_t>(row0 + r) * p.ldo + col;
-                    if constexpr (OT == kOutF32) {
-                        __stcs(d, __uint_as_float(v));
-                    } else if (p.vec >= 2 && col + 1 < p.N) {
-                        __stcs(reinterpret_cast<uint32_t*>(d), v);
-                    } else {
-                        d[0] = static_cast<uint16_t>(v);
-                        if (col + 1 < p.N)
-                            d[1] = static_cast<uint16_t>(v >> 16);
-                    }
+        for (int i = 0; i < 8; ++i) {
+            const int r = 4 * i + (lane >> 3);
+            if (r < rows)
+                __stcs(reinterpret_cast<uint4*>(out + r * p.ldo + C) + (lane & 7), v[i]);
+        }
+    } else if (C < cols + BACK) {
+        constexpr int FOUR = 4 * PER_WORD, BATCH = 4;
+        // Of rows r0, r0 + step, ... the 16 bytes at column c, less the way back to
+        // the row's boundary: four words off the staging area, one store inside Out.
+        auto batch = [&](int r0, int step, int c) {
+            uint32_t v[BATCH][4];
+            int k[BATCH];
+#pragma unroll
+            for (int i = 0; i < BATCH; ++i) {
+                const int r = r0 + i * step;
+                k[i] = c - (static_cast<int>(reinterpret_cast<uintptr_t>(out + r * p.ldo) / sizeof(T)) & (BACK - 1));
+                const int e = k[i] - (C - BACK), w = e / PER_WORD;
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    v[i][j] = stage[staged(r, min(w + j, kStagePitch - 1))];
+                if (PER_WORD == 2 && (e & 1)) {
+                    const uint32_t next = stage[staged(r, min(w + 4, kStagePitch - 1))];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        v[i][j] = __funnelshift_r(v[i][j], j < 3 ? v[i][(j + 1) & 3] : next, 16);
                 }
             }
-        }
-        __syncwarp();
+#pragma unroll
+            for (int i = 0; i < BATCH; ++i) {
+                const int r = r0 + i * step, lo = max(0, -k[i]), hi = r < rows ? min(FOUR, cols - k[i]) : 0;
+                T* d = out + r * p.ldo + k[i];
+                if (lo == 0 && hi == FOUR) {
+                    // not streamed: a sector shared with the neighbour tile waits for it in L2
+                    *reinterpret_cast<uint4*>(d) = make_uint4(v[i][0], v[i][1], v[i][2], v[i][3]);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < FOUR; ++j)
+                        if (j >= lo && j < hi)
+                            d[j] = OT == kOutF32 ? static_cast<T>(__uint_as_float(v[i][j & 3]))
+                                                 : static_cast<T>(v[i][j / PER_WORD] >> (16 * (j & 1)));
+                }
+            }
+        };
+#pragma unroll 1
+        for (int r = 0; r < rows; r += 4 * BATCH)
+            batch(r + (lane >> 3), 4, C + FOUR * (lane & 7));
+        if (C + SEG == kCols && lane < 16)  // what is left of the rows
+            batch(lane >> 1, 8, kCols + FOUR * (lane & 1));
     }
+    __syncwarp();
+    if constexpr (C + SEG < kCols)
+        store_tile<OT, C + SEG>(p, acc, stage, b, row0, col0, lane);
 }
 
 // The scale warp: for every K block of the pair's tiles, this CTA's 128 row scales

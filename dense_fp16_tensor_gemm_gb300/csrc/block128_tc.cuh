@@ -41,22 +41,9 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b)
     return r;
 }
 
-// 32 lanes x 16 columns with the wait, as tmem_ld32_wait; and that one under the same name.
-__device__ __forceinline__ void tmem_load_wait(uint32_t taddr, uint32_t (&r)[16])
-{
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
-        "tcgen05.wait::ld.sync.aligned;"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-        : "r"(taddr)
-        : "memory");
-}
-__device__ __forceinline__ void tmem_load_wait(uint32_t taddr, uint32_t (&r)[32]) { tmem_ld32_wait(taddr, r); }
-
 // The load alone: r may be used only after tmem_wait(r), which waits for all of this
-// thread's loads and names the registers so that no use of them is scheduled before it.
+// thread's loads and names the registers so that no use of them is scheduled before it.  32 lanes x 16
+// or 32 columns: thread i of the warp receives TMEM lane (lane field) + i.
 __device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[16])
 {
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
@@ -263,20 +250,6 @@ struct ScaleRun {
         }
     }
 };
-
-// True if the phase with the given parity has completed; never suspends.
-__device__ __forceinline__ bool mbar_test_wait(uint32_t bar, uint32_t parity)
-{
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.b32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    return ok != 0;
-}
 
 // Waits (with the limit) without giving up early: for drains before exit.
 __device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity, unsigned long long limit)
