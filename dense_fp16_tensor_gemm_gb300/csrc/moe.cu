@@ -688,6 +688,7 @@ __global__ void __launch_bounds__(kThreads, UpCfg<W8, MT, NT, KS>::CTAS) moe_up_
                         s[m] = __ldg(ps[m] + kb);
                 }
                 cp_async_wait<D - 2>();
+                load_next();  // into the slot of the item before, which is in registers
                 if constexpr (W8) {
                     float part[MT][NT][4] = {};
                     multiply_item<kPlain, BF16, W8, MT, NT>(ring + slot * S::BYTES, nt, part);
@@ -702,7 +703,6 @@ __global__ void __launch_bounds__(kThreads, UpCfg<W8, MT, NT, KS>::CTAS) moe_up_
                     multiply_item<kPlain, BF16, W8, MT, NT>(ring + slot * S::BYTES, nt, c);
                 }
                 slot = slot + 1 == D ? 0 : slot + 1;
-                load_next();
             }
             // Columns past inner, to the end of their 8, get zeros (their rows were).
             if constexpr (KS == 1) {
@@ -888,6 +888,7 @@ __global__ void __launch_bounds__(kThreads, MT == 1 && NT == 1 ? 2 : 1) moe_down
                         s[m] = __ldg(ps[m] + kb);
                 }
                 cp_async_wait<D - 2>();
+                load_next();  // into the slot of the item before, which is in registers
                 if constexpr (W8) {
                     float part8[MT][NT][4] = {};
                     multiply_item<HOW, true, W8, MT, NT>(ring + slot * S::BYTES, nt, part8);
@@ -902,7 +903,6 @@ __global__ void __launch_bounds__(kThreads, MT == 1 && NT == 1 ? 2 : 1) moe_down
                     multiply_item<HOW, BF16, W8, MT, NT>(ring + slot * S::BYTES, nt, c);
                 }
                 slot = slot + 1 == D ? 0 : slot + 1;
-                load_next();
             }
 #pragma unroll
             for (int w = 0; w < NT; ++w)
