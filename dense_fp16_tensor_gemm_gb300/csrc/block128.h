@@ -110,6 +110,8 @@ struct MoeParams {
     int tokens, experts, topk, hidden, inner, renorm;
     int bf16, w8;         // types: x and Out; weights E4M3 (else x's type)
     int vec_x, vec_13, vec_2;  // rows start on 16-byte boundaries
+    uint32_t* status;
+    unsigned long long wait_limit;
 };
 cudaError_t moe_configure();  // one-time per device
 cudaError_t moe_launch(const MoeParams& p, int num_sms, cudaStream_t stream);

@@ -338,6 +338,8 @@ gemm_status_t gemm_nt_moe(const void* X, int64_t ldx, const float* logits, int64
     p.vec_x = aligned(X, 16) && ldx % 8 == 0;
     p.vec_13 = aligned(W13, 16) && ldw13 * wsize % 16 == 0 && strideW13 * wsize % 16 == 0;
     p.vec_2 = aligned(W2, 16) && ldw2 * wsize % 16 == 0 && strideW2 * wsize % 16 == 0;
+    p.status = d.status;
+    p.wait_limit = d.wait_limit;
     return status_of(moe_launch(p, d.num_sms, s));
 }
 

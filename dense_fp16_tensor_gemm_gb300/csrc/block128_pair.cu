@@ -205,6 +205,7 @@ __device__ __forceinline__ void load_scales(const BlkParams& p, int rank, float*
             if (n % kScaleGroup == 0 &&
                 !wait_bounded(smem_u32(&sempty[slot]), (n / (kScaleGroup * kScaleRing) & 1) ^ 1, abort_flag, p.wait_limit)) {
                 raise(p, abort_flag);
+                cp_async_wait_all();
                 return;
             }
             const uint32_t s = ring + n % (kScaleGroup * kScaleRing) * (kScaleFloats * 4);

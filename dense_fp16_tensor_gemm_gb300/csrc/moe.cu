@@ -29,9 +29,11 @@
 // Routing is recomputed by every CTA from the logits, a few thousand
 // instructions; that spares a kernel and a round trip through memory.
 #include <algorithm>
+#include <climits>
 
 #include "gemm_nt.h"
 #include "block128.h"
+#include "internal.h"
 #include "ptx.cuh"
 
 namespace gnt {
@@ -750,44 +752,92 @@ __global__ void __launch_bounds__(kThreads, UpCfg<W8, MT, NT, KS>::CTAS) moe_up_
 }
 
 // ---------------------------------------------------------------- down
-// A cluster of C CTAs owns 16*MT rows of Out; its 8*C warps take even ranges of
-// the items (active expert, K item).  A warp adds each expert's share, times
-// the tokens' weights, to sums of its own in shared memory, so that nothing
-// synchronises until the end, when the warps' and then the CTAs' sums are added
-// in a fixed order.
+// A cluster of C CTAs owns 16*MT rows of Out and shares the experts' K items.
+//
+// One token tile (NT == 1): the cluster's warps take even ranges of the items.  A
+// warp adds each expert's share, times the tokens' weights, to sums of its own in
+// shared memory, so that nothing synchronises until the end, when the warps' and
+// then the CTAs' sums are added in a fixed order.
+//
+// Two token tiles: a warp's own sums would be most of shared memory (64 KB of 211
+// at 64 tokens, one CTA an SM).  There a CTA has one set of sums, its items are cut
+// into units of one expert, warp w takes units w, w + 8, ..., and adds to the
+// sums when the units before have: a fixed order again, and with more units than
+// warps nobody waits long.
 template <bool W8, int NT, int MT>
 struct DownCfg {
     using S = Stage<W8, MT, NT, 4>;
-    // ring stages: NT == 1 lets two CTAs share an SM; else the sums leave this much
-    static constexpr int D = NT == 1 ? (W8 ? 4 : 3) : (MT == 2 && W8 ? 3 : 2);
+    static constexpr bool TURNS = NT > 1;
+    // CTAs an SM, and ring stages within what they leave each other
+    static constexpr int CTAS = TURNS ? (W8 ? 2 : 1) : (MT == 1 ? 2 : 1);
+    static constexpr int D = NT == 1 ? (W8 ? 4 : 3) : (MT == 2 && !W8 ? 3 : 2);
     static constexpr int RING = kWarps * D * S::BYTES;
+    static __host__ __device__ constexpr int sum_bytes(int tokens)
+    {
+        return (TURNS ? 1 : kWarps) * tokens * 16 * MT * 4 + 16;  // 16: whose turn it is
+    }
 };
 
-__host__ __device__ constexpr int down_sum_bytes(int tokens, int mt) { return kWarps * tokens * 16 * mt * 4; }
+// Waits until *turn is at least `unit`; false after `limit` cycles, or once another
+// warp has given up.
+__device__ __forceinline__ bool wait_turn(uint32_t turn, int unit, unsigned long long limit)
+{
+    const long long t0 = clock64();
+    for (;;) {
+        int now;
+        asm volatile("ld.acquire.cta.shared::cta.s32 %0, [%1];" : "=r"(now) : "r"(turn) : "memory");
+        if (__all_sync(0xffffffffu, now >= unit))
+            return now != INT_MAX;
+        if (__any_sync(0xffffffffu, static_cast<unsigned long long>(clock64() - t0) > limit))
+            return false;
+    }
+}
+__device__ __forceinline__ void pass_turn(uint32_t turn, int unit)
+{
+    asm volatile("st.release.cta.shared::cta.s32 [%0], %1;" ::"r"(turn), "r"(unit) : "memory");
+}
 
 template <bool BF16, bool W8, int NT, int MT>
-__global__ void __launch_bounds__(kThreads, MT == 1 && NT == 1 ? 2 : 1) moe_down_kernel(const MoeParams p, int cluster)
+__global__ void __launch_bounds__(kThreads, DownCfg<W8, NT, MT>::CTAS) moe_down_kernel(const MoeParams p, int cluster)
 {
     using C = DownCfg<W8, NT, MT>;
     using S = typename C::S;
     constexpr int D = C::D, ROWS = 16 * MT, HOW = BF16 || W8 ? kSplit : kTf32;
+    constexpr bool TURNS = C::TURNS;
     extern __shared__ __align__(16) uint8_t smem[];
-    float* sums = reinterpret_cast<float*>(smem + C::RING);  // [warp][token][row]
-    const Route r = route_carve(smem + C::RING + down_sum_bytes(p.tokens, MT), p);
+    float* sums = reinterpret_cast<float*>(smem + C::RING);  // [warp][token][row], or [token][row]
+    const uint32_t turn = smem_u32(smem) + C::RING + C::sum_bytes(p.tokens) - 16;
+    const Route r = route_carve(smem + C::RING + C::sum_bytes(p.tokens), p);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const int rank = static_cast<int>(blockIdx.x % cluster);
     const int r0 = static_cast<int>(blockIdx.x / cluster) * ROWS;
 
     const int nout = p.tokens * ROWS;
-    for (int i = threadIdx.x; i < kWarps * nout; i += kThreads)
+    for (int i = threadIdx.x; i < (TURNS ? 1 : kWarps) * nout; i += kThreads)
         sums[i] = 0.f;
+    if (TURNS && threadIdx.x == 0)
+        pass_turn(turn, 0);
     route_all(p, r);  // the logits were complete before the up kernel let this one start
     pdl_wait();       // h
 
     const int nit = ceil_div(p.inner, kItem);
-    const int64_t items = static_cast<int64_t>(*r.nact) * nit;
-    const int part = rank * kWarps + warp, parts = cluster * kWarps;
-    const int q0 = static_cast<int>(items * part / parts), q1 = static_cast<int>(items * (part + 1) / parts);
+    // The warp's positions [q0, q1): K items of all experts, one after the other; or
+    // units of `len` items of an expert, two for every warp where there are enough.
+    int len = nit;
+    if (TURNS)
+        while (len > 4 && *r.nact * ceil_div(nit, len) < 2 * kWarps * cluster)
+            len = (len + 1) / 2;
+    const int per = TURNS ? ceil_div(nit, len) : nit;  // positions of an expert
+    const int64_t all = static_cast<int64_t>(*r.nact) * per;
+    const int share = TURNS ? rank : rank * kWarps + warp, shares = TURNS ? cluster : cluster * kWarps;
+    const int u0 = static_cast<int>(all * share / shares), q1 = static_cast<int>(all * (share + 1) / shares);
+    const int q0 = TURNS ? u0 + warp : u0;
+    // Position q: active expert a, K items [k0, k1).
+    auto segment = [&](int q, int& a, int& k0, int& k1) {
+        a = q / per;
+        k0 = TURNS ? (q - a * per) * len : q - a * per;
+        k1 = min(nit, k0 + (TURNS ? len : q1 - q));
+    };
     const uint32_t ring = smem_u32(smem) + warp * D * S::BYTES + lane * 16;
     constexpr int ES = W8 ? 1 : 2;
     const uint8_t* wb = static_cast<const uint8_t*>(p.w2);
@@ -804,9 +854,9 @@ __global__ void __launch_bounds__(kThreads, MT == 1 && NT == 1 ? 2 : 1) moe_down
     auto load_next = [&] {
         if (lq < q1) {
             if (fresh) {
-                const int a = lq / nit, n = r.aoff[a + 1] - r.aoff[a];
-                lk = lq - a * nit;
-                lend = min(nit, lk + q1 - lq);
+                int a;
+                segment(lq, a, lk, lend);
+                const int n = r.aoff[a + 1] - r.aoff[a];
                 lgroups = ceil_div(n, 8 * NT);
                 const uint8_t* we = wb + static_cast<int64_t>(r.act[a]) * p.stride_w2 * ES + lk * (kItem * ES) + t * 16;
                 wbytes = hbytes = 0;
@@ -850,7 +900,7 @@ __global__ void __launch_bounds__(kThreads, MT == 1 && NT == 1 ? 2 : 1) moe_down
                 fresh = true;
                 if (++lg == lgroups) {
                     lg = 0;
-                    lq += lend - lq % nit;
+                    lq += TURNS ? kWarps : lend - lq % nit;
                 }
             }
         }
@@ -861,11 +911,13 @@ __global__ void __launch_bounds__(kThreads, MT == 1 && NT == 1 ? 2 : 1) moe_down
     for (int i = 0; i < D - 1; ++i)
         load_next();
 
-    float* mine = sums + warp * nout;
+    float* mine = sums + (TURNS ? 0 : warp * nout);
     int slot = 0;
+    bool in_turn = true;
 #pragma unroll 1
     for (int q = q0; q < q1;) {
-        const int a = q / nit, k0 = q - a * nit, k1 = min(nit, k0 + q1 - q);
+        int a, k0, k1;
+        segment(q, a, k0, k1);
         const int first = r.aoff[a], n = r.aoff[a + 1] - first;
         const float* ps[2 * MT];  // the lane's rows' scales
         if (W8) {
@@ -904,6 +956,11 @@ __global__ void __launch_bounds__(kThreads, MT == 1 && NT == 1 ? 2 : 1) moe_down
                 }
                 slot = slot + 1 == D ? 0 : slot + 1;
             }
+            if (TURNS && in_turn && g0 == 0 && !wait_turn(turn, q - u0, p.wait_limit)) {
+                in_turn = false;
+                atomicOr(p.status, kStatusTimeout);
+                pass_turn(turn, INT_MAX);
+            }
 #pragma unroll
             for (int w = 0; w < NT; ++w)
 #pragma unroll
@@ -922,16 +979,20 @@ __global__ void __launch_bounds__(kThreads, MT == 1 && NT == 1 ? 2 : 1) moe_down
                 }
             __syncwarp();
         }
-        q += k1 - k0;
+        if (TURNS && in_turn && lane == 0)
+            pass_turn(turn, q - u0 + 1);
+        q += TURNS ? kWarps : k1 - k0;
     }
     cp_async_wait<0>();
     __syncthreads();
-    for (int i = threadIdx.x; i < nout; i += kThreads) {
-        float s = sums[i];
+    if (!TURNS) {
+        for (int i = threadIdx.x; i < nout; i += kThreads) {
+            float s = sums[i];
 #pragma unroll
-        for (int w = 1; w < kWarps; ++w)
-            s += sums[w * nout + i];
-        sums[i] = s;
+            for (int w = 1; w < kWarps; ++w)
+                s += sums[w * nout + i];
+            sums[i] = s;
+        }
     }
     cluster_sync();
     const int o0 = static_cast<int>(static_cast<int64_t>(nout) * rank / cluster);
@@ -1002,13 +1063,13 @@ cudaError_t launch_one(const MoeParams& p, int num_sms, cudaStream_t stream)
                                : launch_up<BF16, W8, 1, NT, kWarps>(p, reach, num_sms, stream);
     if (e != cudaSuccess)
         return e;
-    // The largest clusters whose CTAs are all resident at once, two on an SM (one,
-    // where a CTA takes most of its shared memory), as long as each warp keeps a
-    // few items: a second wave of 512 CTAs after 304 cost one token 9 of 26 us.
+    // The largest clusters whose CTAs are all resident at once, two on an SM where
+    // two fit, as long as each warp keeps a few items: a second wave of 512 CTAs after 304 cost one token 9 of 26 us.
     const int tiles = (p.hidden + 16 * MT - 1) / (16 * MT);
     const int64_t items = reach * ((p.inner + kItem - 1) / kItem);
-    const int smem = DownCfg<W8, NT, MT>::RING + down_sum_bytes(p.tokens, MT) + rb;
-    const int want = num_sms * (MT == 1 && NT == 1 && smem <= kMaxSmem / 2 - 2048 ? 2 : 1);
+    using Down = DownCfg<W8, NT, MT>;
+    const int smem = Down::RING + Down::sum_bytes(p.tokens) + rb;
+    const int want = num_sms * (Down::CTAS == 2 && smem <= kMaxSmem / 2 - 2048 ? 2 : 1);
     int c = 1;
     while (c < 8 && 2 * tiles * c <= want && items >= 2 * 2 * c * kWarps)
         c *= 2;
@@ -1035,9 +1096,9 @@ cudaError_t launch_typed(const MoeParams& p, int num_sms, cudaStream_t stream)
 {
     const int rb = route_bytes(p.tokens, p.experts, p.topk);
     if ((p.tokens <= 8 || p.tokens * p.topk <= 4 * p.experts) && UpCfg<W8, 1, 1, 1>::FIXED + rb <= kMaxSmem &&
-        DownCfg<W8, 1, 1>::RING + down_sum_bytes(p.tokens, 1) + rb <= kMaxSmem)
+        DownCfg<W8, 1, 1>::RING + DownCfg<W8, 1, 1>::sum_bytes(p.tokens) + rb <= kMaxSmem)
         return launch_one<BF16, W8, 1, 1>(p, num_sms, stream);
-    if (p.tokens <= 64 && DownCfg<W8, 2, 2>::RING + down_sum_bytes(p.tokens, 2) + rb <= kMaxSmem)
+    if (DownCfg<W8, 2, 2>::RING + DownCfg<W8, 2, 2>::sum_bytes(p.tokens) + rb <= kMaxSmem)
         return launch_one<BF16, W8, 2, 2>(p, num_sms, stream);
     return launch_one<BF16, W8, 2, 1>(p, num_sms, stream);
 }
@@ -1047,9 +1108,9 @@ static_assert(UpCfg<false, 2, 2, 1>::FIXED + route_bytes(kMoeMaxTokens, kMoeMaxE
                   UpCfg<false, 1, 2, kWarps>::FIXED + route_bytes(kMoeMaxTokens, kMoeMaxExperts, kMoeMaxTopk) <= kMaxSmem &&
                   UpCfg<true, 2, 2, 1>::FIXED + route_bytes(kMoeMaxTokens, kMoeMaxExperts, kMoeMaxTopk) <= kMaxSmem &&
                   UpCfg<true, 1, 2, kWarps>::FIXED + route_bytes(kMoeMaxTokens, kMoeMaxExperts, kMoeMaxTopk) <= kMaxSmem &&
-                  DownCfg<false, 2, 1>::RING + down_sum_bytes(kMoeMaxTokens, 1) +
+                  DownCfg<false, 2, 1>::RING + DownCfg<false, 2, 1>::sum_bytes(kMoeMaxTokens) +
                           route_bytes(kMoeMaxTokens, kMoeMaxExperts, kMoeMaxTopk) <= kMaxSmem &&
-                  DownCfg<true, 2, 1>::RING + down_sum_bytes(kMoeMaxTokens, 1) +
+                  DownCfg<true, 2, 1>::RING + DownCfg<true, 2, 1>::sum_bytes(kMoeMaxTokens) +
                           route_bytes(kMoeMaxTokens, kMoeMaxExperts, kMoeMaxTopk) <= kMaxSmem,
               "shared memory at the limits");
 
