@@ -20,7 +20,7 @@
 // are 16 warps with 64 sums each, scalar arithmetic (452) and loads of 16 rows x
 // 64 columns, which let a column's scale serve two rows (510 and 655).  A tile's
 // epilogue adds 1.5 us (16-bit Out) to 3 us (fp32): its registers are the sums.
-// 8192 x 8192 x 8192 into bf16: 442 us (2490 TFLOP/s).
+// 8192 x 8192 x 8192 into bf16: 428-446 us (2470-2570 TFLOP/s).
 //
 // Roles per CTA (384 threads): warp 0 TMA producer; warps 1 and 3 in the leader
 // MMA issue; warp 2 brings the scales into a ring of their own (any strides);

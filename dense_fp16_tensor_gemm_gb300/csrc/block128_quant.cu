@@ -18,6 +18,11 @@
 // half as many CTAs again, which is what keeps enough bytes in flight.  A block's factor
 // is computed by one lane and passed on: an fp32 reciprocal costs as much as
 // quantising 8 elements.
+//
+// Measured, bf16: 8192 x 8192 both orders 58 us (4.7 TB/s; 150 with the inputs
+// widened to fp32 in registers, 72 with a padded transposed tile, whose stores met
+// 16 to a bank), rows only 42 us, 64 x 8192 rows only 1.7 us.  A third of the SM's
+// warps fit (80 registers), 56 % of the issue slots are used: latency is what is left.
 #include <cuda_fp8.h>
 
 #include "gemm_nt.h"

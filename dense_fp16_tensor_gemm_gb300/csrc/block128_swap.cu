@@ -14,6 +14,10 @@
 // Tensor Memory) that promotion warps scale and add to sums in registers; here
 // a thread holds one row of B (32x32b loads) and half of the columns, its row's
 // scale in a register and the columns' scales broadcast from shared memory.
+//
+// Measured: 64 x 16384 x 8192 27.6 us (5.0 TB/s; one wave of 152 CTAs with even row
+// shares, 31 us with 128 tiles of 128 rows), 1 x 4096 x 4096 7.5 us, of which the
+// 16.8 MB take 2.5: launch, the first loads and the cluster's exchange are the rest.
 #include <algorithm>
 
 #include "block128_tc.cuh"
