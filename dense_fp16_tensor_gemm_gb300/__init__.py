@@ -434,6 +434,13 @@ def _keep(tensors, stream):
             t.record_stream(s)
 
 
+def _pitch(shape, strides, name):
+    """As _matrix_ld, from a tensor's shape and strides."""
+    if strides[-1] != 1:
+        raise ValueError("%s must have unit stride along its last dimension" % name)
+    return strides[-2] if shape[-2] > 1 else max(shape[-1], 1)
+
+
 def _scale128(S, rows, K, name):
     """A scale tensor (rows or ceil(rows/128), ceil(K/128)), optionally with a
     leading batch dimension, as the C struct."""
@@ -459,9 +466,10 @@ def gemm_nt_block128_tensors(A, SA, B, SB, out=None, path=Path.AUTO, stream=None
     """
     torch = _torch or _init_torch()
     ash, bsh = A.shape, B.shape
-    batched = len(ash) == 3
-    if not (batched or len(ash) == 2) or len(bsh) != len(ash) or ash[-1] != bsh[-1] or SA.dim() != len(ash) \
-            or SB.dim() != len(ash) or batched and not ash[0] == bsh[0] == SA.shape[0] == SB.shape[0]:
+    dims = len(ash)
+    batched = dims == 3
+    if not (batched or dims == 2) or len(bsh) != dims or ash[-1] != bsh[-1] or SA.dim() != dims \
+            or SB.dim() != dims or batched and not ash[0] == bsh[0] == SA.shape[0] == SB.shape[0]:
         raise ValueError("shapes: A (M,K), B (N,K) and their scales, or the same with a leading batch dimension")
     if A.dtype != B.dtype:
         raise TypeError("A and B must have the same type")
@@ -471,14 +479,16 @@ def gemm_nt_block128_tensors(A, SA, B, SB, out=None, path=Path.AUTO, stream=None
     M, K = ash[-2:]
     N = bsh[-2]
     shape = (ash[0], M, N) if batched else (M, N)
+    device = A.device
     if out is None:
-        out = torch.empty(shape, dtype=dt, device=A.device)
+        out = torch.empty(shape, dtype=dt, device=device)
     elif tuple(out.shape) != shape:
         raise ValueError("out must have shape (M,N), with A's batch dimension")
+    ast, bst, ost = A.stride(), B.stride(), out.stride()
     gemm_nt_block128(A.data_ptr(), _scale128(SA, M, K, "SA"), B.data_ptr(), _scale128(SB, N, K, "SB"), out.data_ptr(),
-                     ab, ot, M, N, K, _matrix_ld(A, "A"), _matrix_ld(B, "B"), _matrix_ld(out, "out"),
-                     A.stride(0) if batched else 0, B.stride(0) if batched else 0, out.stride(0) if batched else 0,
-                     ash[0] if batched else 1, path, _stream_of(stream, A.device))
+                     ab, ot, M, N, K, _pitch(ash, ast, "A"), _pitch(bsh, bst, "B"), _pitch(shape, ost, "out"),
+                     ast[0] if batched else 0, bst[0] if batched else 0, ost[0] if batched else 0,
+                     ash[0] if batched else 1, path, _stream_of(stream, device))
     return out
 
 
@@ -508,26 +518,50 @@ def quantize_block128(X, q_dtype=None, block_rows=1, transposed=False, stream=No
     Rows of the codes start on 16-byte boundaries; scales of single rows are
     stored with the rows adjacent.
     """
+    q, s, _, qt, st, _ = _quantize(X, q_dtype, block_rows, transposed, stream)
+    return (q, s, qt, st) if transposed else (q, s)
+
+
+def _quantize(X, q_dtype, block_rows, transposed, stream):
+    """The work of quantize_block128: Q, S and S as the C struct, and the same
+    of X transposed."""
     torch = _torch or _init_torch()
-    if X.dim() != 2:
+    shape = X.shape
+    if len(shape) != 2:
         raise ValueError("X must be a matrix")
     if block_rows not in (1, 128):
         raise ValueError("block_rows must be 1 or 128")
     q_dtype = q_dtype or torch.float8_e4m3fn
     code = _one_of(q_dtype, _IN_F8, "q_dtype")
     xt = _one_of(X.dtype, _OUT, "X")
-    ldx = _matrix_ld(X, "X")
-    rows, cols = X.shape
+    ldx = _pitch(shape, X.stride(), "X")
+    rows, cols = shape
     device = X.device
     q, s, ldq, sq = _quantized(rows, cols, q_dtype, block_rows, device)
-    if not transposed:
-        gemm_nt_block128_quantize(X.data_ptr(), xt, rows, cols, ldx, q.data_ptr(), ldq, sq, 0, 0, None, code,
-                                  _stream_of(stream, device))
-        return q, s
-    qt, st, ldqt, sqt = _quantized(cols, rows, q_dtype, block_rows, device)
-    gemm_nt_block128_quantize(X.data_ptr(), xt, rows, cols, ldx, q.data_ptr(), ldq, sq, qt.data_ptr(), ldqt, sqt, code,
-                              _stream_of(stream, device))
-    return q, s, qt, st
+    qt, st, ldqt, sqt = _quantized(cols, rows, q_dtype, block_rows, device) if transposed else (None, None, 0, None)
+    gemm_nt_block128_quantize(X.data_ptr(), xt, rows, cols, ldx, q.data_ptr(), ldq, sq, qt.data_ptr() if transposed else 0,
+                              ldqt, sqt, code, _stream_of(stream, device))
+    return q, s, sq, qt, st, sqt
+
+
+def _product(A, SA, B, SB, dtype, stream):
+    """A @ B.T of two matrices of codes whose scales are C structs."""
+    (M, K), (N, _) = A.shape, B.shape
+    device = A.device
+    out = _torch.empty((M, N), dtype=dtype, device=device)
+    gemm_nt_block128(A.data_ptr(), SA, B.data_ptr(), SB, out.data_ptr(), _CODES[A.dtype], _CODES[dtype], M, N, K,
+                     _pitch((M, K), A.stride(), "A"), _pitch((N, K), B.stride(), "B"), max(N, 1), 0, 0, 0, 1, 0,
+                     _stream_of(stream, device))
+    return out
+
+
+def _weight(W, SW, width, name):
+    """Checks a matrix of codes against the columns it multiplies; its scales as
+    the C struct."""
+    _torch or _init_torch()
+    if W.dim() != 2 or SW.dim() != 2 or W.shape[1] != width:
+        raise ValueError("%s must be a matrix with %d columns, with its scales" % (name, width))
+    return _scale128(SW, W.shape[0], width, "S" + name)
 
 
 def linear_block128(X, W, SW, stream=None):
@@ -536,8 +570,11 @@ def linear_block128(X, W, SW, stream=None):
     as ``quantize_block128(weight, block_rows=128)`` leaves it.  Returns Y in X's
     type and what :func:`linear_block128_backward` needs (X transposed, in 8
     bits)."""
-    q, s, qt, st = quantize_block128(X, W.dtype, transposed=True, stream=stream)
-    y = gemm_nt_block128_tensors(q, s, W, SW, out_dtype=X.dtype, stream=stream)
+    if X.dim() != 2:
+        raise ValueError("X must be a matrix")
+    sw = _weight(W, SW, X.shape[1], "W")
+    q, s, sq, qt, st, _ = _quantize(X, W.dtype, 1, True, stream)
+    y = _product(q, sq, W, sw, X.dtype, stream)
     _keep((q, s), stream)
     return y, (qt, st)
 
@@ -547,10 +584,16 @@ def linear_block128_backward(dY, saved, WT, SWT, stream=None):
     dY.T @ X in float32, both products in 8 bits.  WT (in, out) and SWT are W's
     codes and scales transposed (the ``transposed`` half of
     ``quantize_block128(weight, block_rows=128, transposed=True)``)."""
+    if dY.dim() != 2:
+        raise ValueError("dY must be a matrix")
     qt_x, st_x = saved
-    q, s, qt, st = quantize_block128(dY, WT.dtype, transposed=True, stream=stream)
-    dx = gemm_nt_block128_tensors(q, s, WT, SWT, out_dtype=dY.dtype, stream=stream)
-    dw = gemm_nt_block128_tensors(qt, st, qt_x, st_x, stream=stream)
+    tokens, width = dY.shape
+    sw, sx = _weight(WT, SWT, width, "WT"), _weight(qt_x, st_x, tokens, "XT")
+    if qt_x.dtype != WT.dtype:
+        raise TypeError("the weights' and the saved codes' types differ")
+    q, s, sq, qt, st, sqt = _quantize(dY, WT.dtype, 1, True, stream)
+    dx = _product(q, sq, WT, sw, dY.dtype, stream)
+    dw = _product(qt, sqt, qt_x, sx, _torch.float32, stream)
     _keep((q, s, qt, st, qt_x, st_x), stream)
     return dx, dw
 
@@ -572,12 +615,14 @@ def moe_few_tokens(X, logits, W13, W2, topk, S13=None, S2=None, renormalize=True
     :func:`gemm_nt_moe_workspace_bytes` bytes, is allocated if not given.
     """
     torch = _torch or _init_torch()
-    if X.dim() != 2 or logits.dim() != 2 or W13.dim() != 3 or W2.dim() != 3:
+    xsh, lsh, s13h, s2h = X.shape, logits.shape, W13.shape, W2.shape
+    if len(xsh) != 2 or len(lsh) != 2 or len(s13h) != 3 or len(s2h) != 3:
         raise ValueError(_MOE_SHAPES)
-    tokens, hidden = X.shape
-    experts, inner = logits.shape[1], W2.shape[2]
-    if logits.shape[0] != tokens or W13.shape != (experts, 2 * inner, hidden) or W2.shape != (experts, hidden, inner):
+    tokens, hidden = xsh
+    experts, inner = lsh[1], s2h[2]
+    if lsh[0] != tokens or s13h != (experts, 2 * inner, hidden) or s2h != (experts, hidden, inner):
         raise ValueError(_MOE_SHAPES)
+    device = X.device
     xt = _one_of(X.dtype, _X16, "X")
     if W13.dtype != W2.dtype:
         raise TypeError("W13 and W2 must have the same type")
@@ -587,7 +632,7 @@ def moe_few_tokens(X, logits, W13, W2, topk, S13=None, S2=None, renormalize=True
     if (wt == 3) != (S13 is not None) or (S13 is None) != (S2 is None):
         raise ValueError("8-bit weights take S13 and S2, 16-bit weights none")
     if out is None:
-        out = torch.empty((tokens, hidden), dtype=X.dtype, device=X.device)
+        out = torch.empty((tokens, hidden), dtype=X.dtype, device=device)
     elif tuple(out.shape) != (tokens, hidden) or out.dtype != X.dtype:
         raise ValueError("out must have X's shape and type")
     s13 = s2 = None
@@ -597,10 +642,11 @@ def moe_few_tokens(X, logits, W13, W2, topk, S13=None, S2=None, renormalize=True
         s13, s2 = _scale128(S13, 2 * inner, hidden, "S13"), _scale128(S2, hidden, inner, "S2")
     if workspace is None:
         need = gemm_nt_moe_workspace_bytes(tokens, topk, inner) if topk > 0 else 0
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=X.device)
+        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=device)
         _keep((workspace,), stream)
-    gemm_nt_moe(X.data_ptr(), _matrix_ld(X, "X"), logits.data_ptr(), _matrix_ld(logits, "logits"), W13.data_ptr(),
-                _matrix_ld(W13, "W13"), W13.stride(0), s13, W2.data_ptr(), _matrix_ld(W2, "W2"), W2.stride(0), s2,
-                out.data_ptr(), _matrix_ld(out, "out"), xt, wt, tokens, experts, topk, hidden, inner, renormalize,
-                workspace.data_ptr(), workspace.numel(), _stream_of(stream, X.device))
+    t13, t2 = W13.stride(), W2.stride()
+    gemm_nt_moe(X.data_ptr(), _pitch(xsh, X.stride(), "X"), logits.data_ptr(), _pitch(lsh, logits.stride(), "logits"),
+                W13.data_ptr(), _pitch(s13h, t13, "W13"), t13[0], s13, W2.data_ptr(), _pitch(s2h, t2, "W2"), t2[0], s2,
+                out.data_ptr(), _pitch(xsh, out.stride(), "out"), xt, wt, tokens, experts, topk, hidden, inner,
+                renormalize, workspace.data_ptr(), workspace.numel(), _stream_of(stream, device))
     return out

@@ -161,3 +161,25 @@ def test_tensor_forms_refuse_shapes_and_types():
         gnt.moe_few_tokens(x, l, w13.half(), w2.half(), 2)
     with pytest.raises(ValueError):
         gnt.moe_few_tokens(x, l, w13, w2, 2, S13=torch.ones(4, 1, 1), S2=torch.ones(4, 1, 1))
+
+
+def test_linear_refuses_what_does_not_fit():
+    torch = pytest.importorskip("torch")
+    f8 = torch.float8_e4m3fn
+    x, w, sw = torch.zeros(4, 256, dtype=torch.bfloat16), torch.zeros(8, 256).to(f8), torch.ones(1, 2)
+    wt, swt = torch.zeros(256, 8).to(f8), torch.ones(2, 1)
+    saved = (torch.zeros(256, 4).to(f8), torch.ones(256, 1))
+    dy = torch.zeros(4, 8, dtype=torch.bfloat16)
+    for bad in (lambda: gnt.linear_block128(x[0], w, sw), lambda: gnt.linear_block128(x[:, :128], w, sw),
+                lambda: gnt.linear_block128(x, w, sw[0]), lambda: gnt.linear_block128(x, w, torch.ones(2, 2)),
+                lambda: gnt.linear_block128_backward(dy[:, :4], saved, wt, swt),
+                lambda: gnt.linear_block128_backward(dy[:3], saved, wt, swt),
+                lambda: gnt.linear_block128_backward(dy, (saved[0], torch.ones(256, 3)), wt, swt),
+                lambda: gnt.linear_block128(x.t(), w[:, :4], torch.ones(1, 1))):
+        with pytest.raises(ValueError):
+            bad()
+    for bad in (lambda: gnt.linear_block128(x.double(), w, sw), lambda: gnt.linear_block128(x, w.float(), sw),
+                lambda: gnt.linear_block128(x, w, sw.double()),
+                lambda: gnt.linear_block128_backward(dy, (saved[0].to(torch.float8_e5m2), saved[1]), wt, swt)):
+        with pytest.raises(TypeError):
+            bad()
