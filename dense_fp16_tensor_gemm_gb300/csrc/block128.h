@@ -87,6 +87,8 @@ struct QuantParams {
     int64_t st_rs, st_ks;
     int e5m2;
     int vec_x, vec_q, vec_qt;  // rows allow 16-byte loads / 8-byte stores / 16-byte stores
+    int num_sms;
+    unsigned ahead;  // set by the launch: CTAs that run at once
 };
 cudaError_t block128_quantize_launch(const QuantParams& p, bool tile, cudaStream_t stream);
 

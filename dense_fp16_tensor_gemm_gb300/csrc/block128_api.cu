@@ -226,6 +226,7 @@ gemm_status_t gemm_nt_block128_quantize(const void* X, gemm_dtype_t x_type, int6
     p.cols = cols;
     p.ldx = ldx;
     p.e5m2 = q_type == GEMM_DTYPE_E5M2;
+    p.num_sms = d.num_sms;
     p.vec_x = aligned(X, 16) && ldx * xsize % 16 == 0;
     if (Q) {
         p.q = static_cast<uint8_t*>(Q);

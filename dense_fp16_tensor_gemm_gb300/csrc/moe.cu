@@ -30,7 +30,7 @@
 //
 // Measured, 64 experts of 2048 x 1024, 8 a token: one token 28 us in bf16 (100 MB,
 // 15 us at the memory's rate; two launches and their first loads take 7.5), 64 tokens
-// 143 us in E4M3 (403 MB, 60 us), 177 in bf16 (805 MB, 119 us).  16 tokens on 8
+// 141 us in E4M3 (403 MB, 60 us), 177 in bf16 (805 MB, 119 us).  16 tokens on 8
 // experts of 4096 x 8192, 2 a token: 265 us (1.6 GB, 235 us).
 //
 // Routing is recomputed by every CTA from the logits, a few thousand
@@ -459,22 +459,34 @@ __device__ __forceinline__ uint4 lds16(uint32_t a)
     return v;
 }
 
-// The 8 weights of a lane's half, as 4 packed pairs of the MMA's type.
-template <bool BF16, bool W8>
-__device__ __forceinline__ void weights8(uint32_t line, int hf, uint32_t (&v)[4])
-{
-    if constexpr (W8) {
-        uint32_t a, b;
-        asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(a), "=r"(b) : "r"(line + 8 * hf) : "memory");
-        v[0] = widen_e4m3<BF16>(a);
-        v[1] = widen_e4m3<BF16>(a >> 16);
-        v[2] = widen_e4m3<BF16>(b);
-        v[3] = widen_e4m3<BF16>(b >> 16);
-    } else {
-        const uint4 w = lds16(line + 512 * hf);
-        v[0] = w.x, v[1] = w.y, v[2] = w.z, v[3] = w.w;
+// The 16 weights of a lane's row, as they lie in shared memory: one 16-byte line
+// (8 bits) or two (16 bits); and those of one half as 4 packed pairs of the MMA's type.
+template <bool W8>
+struct RowWeights {
+    uint4 v[W8 ? 1 : 2];
+
+    __device__ __forceinline__ void read(uint32_t line, int hf)
+    {
+        if (!W8)
+            v[hf] = lds16(line + 512 * hf);
+        else if (hf == 0)
+            v[0] = lds16(line);
     }
-}
+
+    template <bool BF16>
+    __device__ __forceinline__ void half(int hf, uint32_t (&o)[4]) const
+    {
+        if constexpr (W8) {
+            const uint32_t a = hf ? v[0].z : v[0].x, b = hf ? v[0].w : v[0].y;
+            o[0] = widen_e4m3<BF16>(a);
+            o[1] = widen_e4m3<BF16>(a >> 16);
+            o[2] = widen_e4m3<BF16>(b);
+            o[3] = widen_e4m3<BF16>(b >> 16);
+        } else {
+            o[0] = v[hf].x, o[1] = v[hf].y, o[2] = v[hf].z, o[3] = v[hf].w;
+        }
+    }
+};
 
 __device__ __forceinline__ float2 halves(uint32_t w) { return __half22float2(*reinterpret_cast<const __half2*>(&w)); }
 
@@ -488,13 +500,17 @@ template <int HOW, bool BF16, bool W8, int MT, int NT>
 __device__ __forceinline__ void multiply_item(uint32_t st, int nt, float (&c)[MT][NT][4])
 {
     using S = Stage<W8, MT, NT, HOW == kPlain ? 2 : 4>;
+    RowWeights<W8> raw[2 * MT];
 #pragma unroll
     for (int hf = 0; hf < 2; ++hf) {
         uint32_t lo[MT][4], hi[MT][4];
 #pragma unroll
+        for (int m = 0; m < 2 * MT; ++m)
+            raw[m].read(st + m * S::PER_ROW * 512, hf);
+#pragma unroll
         for (int m = 0; m < MT; ++m) {
-            weights8<BF16, W8>(st + m * 2 * S::PER_ROW * 512, hf, lo[m]);
-            weights8<BF16, W8>(st + (m * 2 + 1) * S::PER_ROW * 512, hf, hi[m]);
+            raw[2 * m].template half<BF16>(hf, lo[m]);
+            raw[2 * m + 1].template half<BF16>(hf, hi[m]);
         }
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
