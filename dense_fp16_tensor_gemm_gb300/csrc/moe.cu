@@ -28,7 +28,7 @@
 // and immediate offsets, and the next item's load goes out before the arithmetic.
 // (Widening E4M3 through fp16 costs little: without it 64 tokens take 139 us for 150.)
 //
-// Measured, 64 experts of 2048 x 1024, 8 a token: one token 28 us in bf16 (100 MB,
+// Measured, 64 experts of 2048 x 1024, 8 a token: one token 27 us in bf16 (100 MB,
 // 15 us at the memory's rate; two launches and their first loads take 7.5), 64 tokens
 // 141 us in E4M3 (403 MB, 60 us), 177 in bf16 (805 MB, 119 us).  16 tokens on 8
 // experts of 4096 x 8192, 2 a token: 265 us (1.6 GB, 235 us).
@@ -554,22 +554,33 @@ __device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; 
 // A unit is 8*MT gate rows and the 8*MT up rows that go with them (MT m16 tiles:
 // an accumulator's lower rows are the gates, its upper ones their ups), over all
 // of K, for up to 8*NT of the expert's tokens at a time.  CTAs take even ranges
-// of the units of all active experts.  KS warps share a unit and split its K:
-// one, where there are units enough for every SM (a warp then ends a unit in its
-// own registers; meeting in shared memory after every 4 items of K took half of
-// 64 tokens' time), or all 8, where there are few and a unit's latency counts.
+// of the units of all active experts.  KS warps share a unit and split its K: one,
+// where there are many units for every SM (a warp then ends a unit in its own
+// registers; 8 warps meeting after every 4 items of K took half of 64 tokens'
+// time); two, where a warp each would leave warps without one (one token on 8 of 64
+// experts of 2048 x 1024, 6.7 units an SM: 27.1 us against 27.7 in bf16, 25.2
+// against 27.3 in E4M3; 16 tokens on 8 of 4096 x 8192, 54 units: 285 against 277);
+// or all 8, where there are few and a unit's latency counts.
 template <bool W8, int MT, int NT, int KS>
 struct UpCfg {
     using S = Stage<W8, MT, NT, 2>;
-    // Ring stages.  A warp alone on 16-bit weights, or on few tokens, is all latency:
-    // one CTA an SM and deep rings; widening E4M3 wants two CTAs' warps.
-    static constexpr int CTAS = KS == 1 && (NT == 1 || !W8) ? 1 : 2;
-    static constexpr int D = KS > 1 ? (NT == 1 || W8 ? 4 : 3) : (NT == 1 ? (W8 ? 7 : 8) : 3);
+    // A warp alone on 16-bit weights is all latency: one CTA an SM and deep rings (D
+    // stages).  E4M3's items are half as long and cost a warp as much: two CTAs
+    // (8 tokens on 64 experts 85 us, 97 with one).
+    static constexpr int CTAS = KS == 1 && !W8 ? 1 : 2;
+    static constexpr int D = KS > 1 ? (NT == 1 || W8 ? 4 : 3) : (NT == 1 ? (W8 ? 6 : 8) : 3);
     static constexpr int RBUF = KS == 1 ? 0 : (NT == 1 ? 2 : 1);  // buffers for the warps' sums
     static constexpr int RING = kWarps * D * S::BYTES;
     static constexpr int FIXED = RING + RBUF * kWarps * NT * 4 * 32 * 4;
-    static_assert(KS == 1 || (KS == kWarps && MT == 1), "unit shapes");
+    static_assert(kWarps % KS == 0 && (KS == 1 || MT == 1), "unit shapes");
 };
+
+// Barrier of the KS warps that share a unit.
+template <int KS>
+__device__ __forceinline__ void unit_sync(int group)
+{
+    asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "n"(32 * KS) : "memory");
+}
 
 // h of one element: where it goes in a row's groups of 8 columns (bf16 heads,
 // then their rests; or, for fp16 weights, fp32).
@@ -749,18 +760,19 @@ __global__ void __launch_bounds__(kThreads, UpCfg<W8, MT, NT, KS>::CTAS) moe_up_
                 if (C::RBUF == 2)
                     parity ^= 1;  // the other buffer is rewritten only after the next unit's barrier
                 else
-                    __syncthreads();
+                    unit_sync<KS>(warp / KS);
 #pragma unroll
                 for (int q = 0; q < NT; ++q)
 #pragma unroll
                     for (int v = 0; v < 4; ++v)
                         rd[((warp * NT + q) * 4 + v) * 32 + lane] = c[0][q][v];
-                __syncthreads();
-                for (int idx = threadIdx.x; idx < nt * 64; idx += kThreads) {
+                unit_sync<KS>(warp / KS);
+                const int w0 = warp / KS * KS;
+                for (int idx = threadIdx.x - 32 * w0; idx < nt * 64; idx += 32 * KS) {
                     const int l = idx & 31, wh = (idx >> 5) & 1, q = idx >> 6;
                     float gate = 0.f, up = 0.f;
 #pragma unroll
-                    for (int w = 0; w < kWarps; ++w) {
+                    for (int w = w0; w < w0 + KS; ++w) {
                         gate += rd[((w * NT + q) * 4 + wh) * 32 + l];
                         up += rd[((w * NT + q) * 4 + 2 + wh) * 32 + l];
                     }
@@ -1044,6 +1056,8 @@ cudaError_t configure_one()
 {
     constexpr auto attr = cudaFuncAttributeMaxDynamicSharedMemorySize;
     cudaError_t e = cudaFuncSetAttribute(moe_up_kernel<BF16, W8, 1, NT, kWarps>, attr, kMaxSmem);
+    if (e == cudaSuccess && NT == 1)
+        e = cudaFuncSetAttribute(moe_up_kernel<BF16, W8, 1, 1, 2>, attr, kMaxSmem);
     if (e == cudaSuccess)
         e = cudaFuncSetAttribute(moe_up_kernel<BF16, W8, NT, NT, 1>, attr, kMaxSmem);
     if (e == cudaSuccess)
@@ -1056,14 +1070,15 @@ cudaError_t launch_up(const MoeParams& p, int64_t reach, int num_sms, cudaStream
 {
     using C = UpCfg<W8, MT, NT, KS>;
     const int64_t units = reach * ((p.inner + 8 * MT - 1) / (8 * MT));
-    const int64_t ctas = KS == 1 ? (units + kWarps - 1) / kWarps : units;
+    constexpr int AT_ONCE = kWarps / KS;  // units a CTA works on
+    const int64_t ctas = (units + AT_ONCE - 1) / AT_ONCE;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    // one unit a warp and every SM in use before an SM takes more
+    // every SM in use before a CTA takes as many units as it can
     cfg.gridDim = dim3(static_cast<unsigned>(
-        std::min<int64_t>(C::CTAS * num_sms, KS == 1 ? std::max<int64_t>(ctas, std::min<int64_t>(units, num_sms)) : ctas)));
+        std::min<int64_t>(C::CTAS * num_sms, std::max<int64_t>(ctas, std::min<int64_t>(units, num_sms)))));
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = C::FIXED + route_bytes(p.tokens, p.experts, p.topk);
     cfg.stream = stream;
@@ -1080,10 +1095,14 @@ cudaError_t launch_one(const MoeParams& p, int num_sms, cudaStream_t stream)
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     const int64_t reach = std::min<int64_t>(p.experts, int64_t(p.tokens) * p.topk);  // most experts in use
-    // Units of 8*NT columns for a warp alone once there are four for every SM.
-    const bool many = reach * ((p.inner + 8 * NT - 1) / (8 * NT)) >= 4 * num_sms;
-    const cudaError_t e = many ? launch_up<BF16, W8, NT, NT, 1>(p, reach, num_sms, stream)
-                               : launch_up<BF16, W8, 1, NT, kWarps>(p, reach, num_sms, stream);
+    // Units of 8*NT columns for a warp alone, two warps or all eight of a CTA (above).
+    const int64_t units = reach * ((p.inner + 8 * NT - 1) / (8 * NT));
+    cudaError_t e;
+    if (NT == 1 && units >= 4 * num_sms && units < 16 * num_sms)
+        e = launch_up<BF16, W8, 1, 1, 2>(p, reach, num_sms, stream);
+    else
+        e = units >= 4 * num_sms ? launch_up<BF16, W8, NT, NT, 1>(p, reach, num_sms, stream)
+                                 : launch_up<BF16, W8, 1, NT, kWarps>(p, reach, num_sms, stream);
     if (e != cudaSuccess)
         return e;
     // The largest clusters whose CTAs are all resident at once, two on an SM where
