@@ -17,8 +17,8 @@
 // 2048 to 8192): 410 ns, 620 where B has a scale for every row; 310 with the
 // arithmetic left out, 345 with the loads left out.  Halves of 128 columns, which
 // shorten the trip, are slower (A is read twice and shared memory fills up), as
-// are 16 warps with 64 sums each, scalar arithmetic (452) and loads of 16 rows x
-// 64 columns, which let a column's scale serve two rows (510 and 655).  A tile's
+// are 16 warps with 64 sums each (490 and 670), scalar arithmetic (452) and loads of
+// 16 rows x 64 columns, which let a column's scale serve two rows (510 and 655).  A tile's
 // epilogue adds 1.5 us (16-bit Out) to 3 us (fp32): its registers are the sums.
 // 8192 x 8192 x 8192 into bf16: 428-446 us (2470-2570 TFLOP/s).
 //
