@@ -132,15 +132,21 @@ struct Route {
     uint16_t* chosen;  // [slots] expert, 0xffff: none
     uint16_t* list;    // [slots] slots by expert, then token
     uint16_t* off;     // [experts] start of each expert's part of list
-    uint16_t* act;     // [active + 1] experts with tokens, ascending
+    uint16_t* act;     // [active + 1] experts with tokens, ascending, one entry for every `group` of them
     uint16_t* aoff;    // [active + 1] their starts in list; the last entry closes it
     uint8_t* bad;      // [tokens] the token's logits hold a NaN
     int* nact;
 };
 
+// Most entries of Route::act: a group has 8 tokens at least, but for an expert's last.
+__host__ __device__ constexpr int route_entries(int experts, int slots)
+{
+    return (experts < slots ? experts : slots) + slots / 8;
+}
+
 __host__ __device__ constexpr int route_bytes(int tokens, int experts, int topk)
 {
-    const int words = (tokens + 31) / 32, slots = tokens * topk, act = experts < slots ? experts : slots;
+    const int words = (tokens + 31) / 32, slots = tokens * topk, act = route_entries(experts, slots);
     const int b = 4 * (experts * words + slots + 1) + 2 * (2 * slots + experts + 2 * (act + 1)) + tokens;
     return (b + 15) / 16 * 16;
 }
@@ -148,7 +154,7 @@ __host__ __device__ constexpr int route_bytes(int tokens, int experts, int topk)
 __device__ __forceinline__ Route route_carve(uint8_t* s, const MoeParams& p)
 {
     const int words = (p.tokens + 31) / 32, slots = p.tokens * p.topk;
-    const int act = p.experts < slots ? p.experts : slots;
+    const int act = route_entries(p.experts, slots);
     Route r;
     r.mask = reinterpret_cast<uint32_t*>(s);
     r.p = reinterpret_cast<float*>(r.mask + p.experts * words);
@@ -323,7 +329,7 @@ __device__ __forceinline__ void route_tokens(const MoeParams& p, const Route& r,
     }
 }
 
-__device__ __forceinline__ void route_all(const MoeParams& p, const Route& r)
+__device__ __forceinline__ void route_all(const MoeParams& p, const Route& r, int group)
 {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int words = (p.tokens + 31) / 32, slots = p.tokens * p.topk;
@@ -353,23 +359,24 @@ __device__ __forceinline__ void route_all(const MoeParams& p, const Route& r)
             if (e < p.experts)
                 for (int w = 0; w < words; ++w)
                     n += __popc(r.mask[e * words + w]);
-            int incl = n;
+            const int parts = (n + group - 1) / group;
+            int incl = n | parts << 16;  // tokens and entries so far, summed in one word
 #pragma unroll
             for (int s = 1; s < 32; s *= 2) {
                 const int v = __shfl_up_sync(0xffffffffu, incl, s);
                 if (lane >= s)
                     incl += v;
             }
-            const uint32_t has = __ballot_sync(0xffffffffu, n > 0);
+            const int start = total + (incl & 0xffff) - n, a = nact + (incl >> 16) - parts;
             if (e < p.experts)
-                r.off[e] = static_cast<uint16_t>(total + incl - n);
-            if (n > 0) {
-                const int a = nact + __popc(has & ((1u << lane) - 1));
-                r.act[a] = static_cast<uint16_t>(e);
-                r.aoff[a] = static_cast<uint16_t>(total + incl - n);
+                r.off[e] = static_cast<uint16_t>(start);
+            for (int i = 0; i < parts; ++i) {
+                r.act[a + i] = static_cast<uint16_t>(e);
+                r.aoff[a + i] = static_cast<uint16_t>(start + i * group);
             }
-            nact += __popc(has);
-            total += __shfl_sync(0xffffffffu, incl, 31);
+            const int last = __shfl_sync(0xffffffffu, incl, 31);
+            nact += last >> 16;
+            total += last & 0xffff;
         }
         if (lane == 0) {
             r.aoff[nact] = static_cast<uint16_t>(total);
@@ -553,8 +560,10 @@ __device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; 
 // ---------------------------------------------------------------- up
 // A unit is 8*MT gate rows and the 8*MT up rows that go with them (MT m16 tiles:
 // an accumulator's lower rows are the gates, its upper ones their ups), over all
-// of K, for up to 8*NT of the expert's tokens at a time.  CTAs take even ranges
-// of the units of all active experts.  KS warps share a unit and split its K: one,
+// of K, for up to 8*NT of the expert's tokens; an expert with more has as many
+// entries among the active ones, so that CTAs and warps share out work, not experts
+// (one of 64 with 17 tokens made 143 us 182, now 149; 128 tokens 226, 381 before).
+// CTAs take even ranges of the units of all entries.  KS warps share a unit and split its K: one,
 // where there are many units for every SM (a warp then ends a unit in its own
 // registers; 8 warps meeting after every 4 items of K took half of 64 tokens'
 // time); two, where a warp each would leave warps without one (one token on 8 of 64
@@ -615,7 +624,7 @@ __global__ void __launch_bounds__(kThreads, UpCfg<W8, MT, NT, KS>::CTAS) moe_up_
     // After the wait: the down kernel may start early and read the logits, which
     // are then complete.
     pdl_launch_dependents();
-    route_all(p, r);
+    route_all(p, r, 8 * NT);
 
     const int tiles = ceil_div(p.inner, 8 * MT), nit = ceil_div(p.hidden, kItem);
     const int64_t units = static_cast<int64_t>(*r.nact) * tiles;
@@ -632,7 +641,7 @@ __global__ void __launch_bounds__(kThreads, UpCfg<W8, MT, NT, KS>::CTAS) moe_up_
     // Loader: the items (unit, token group, K item) of this warp in order, by
     // pointers to the lane's own bytes.  Rows outside the matrix, and tokens past
     // the group, read nothing of row 0.
-    int lu = u0, lg = 0, lk = ks0, lslot = 0, lgroups = 0;
+    int lu = u0, lk = ks0, lslot = 0;
     const uint8_t* wr[2 * MT];  // gate and up row of each m16 tile
     const uint8_t* xr[NT];
     uint32_t wbytes = 0, xbytes = 0;  // bit m: tile m's rows are inside; bit q: token of tile q
@@ -641,7 +650,6 @@ __global__ void __launch_bounds__(kThreads, UpCfg<W8, MT, NT, KS>::CTAS) moe_up_
             if (lk == ks0) {
                 const int a = lu / tiles, i0 = (lu - a * tiles) * (8 * MT) + g;
                 const int n = r.aoff[a + 1] - r.aoff[a];
-                lgroups = ceil_div(n, 8 * NT);
                 const uint8_t* we = wb + static_cast<int64_t>(r.act[a]) * p.stride_w13 * ES + ks0 * (kItem * ES) + t * 16;
                 wbytes = xbytes = 0;
 #pragma unroll
@@ -656,7 +664,7 @@ __global__ void __launch_bounds__(kThreads, UpCfg<W8, MT, NT, KS>::CTAS) moe_up_
                 }
 #pragma unroll
                 for (int q = 0; q < NT; ++q) {
-                    const int j = lg * 8 * NT + q * 8 + g;
+                    const int j = q * 8 + g;
                     xr[q] = xb + ks0 * (kItem * 2) + half_k<W8>(t, 0) * 2;
                     if (j < n) {
                         xr[q] += static_cast<int64_t>(r.list[r.aoff[a] + j] / p.topk) * p.ldx * 2;
@@ -682,10 +690,7 @@ __global__ void __launch_bounds__(kThreads, UpCfg<W8, MT, NT, KS>::CTAS) moe_up_
             }
             if (++lk == ks1) {
                 lk = ks0;
-                if (++lg == lgroups) {
-                    lg = 0;
-                    lu += step;
-                }
+                lu += step;
             }
         }
         cp_async_commit();
@@ -710,76 +715,73 @@ __global__ void __launch_bounds__(kThreads, UpCfg<W8, MT, NT, KS>::CTAS) moe_up_
                 ps[2 * m + 1] = se + static_cast<int64_t>((p.inner + i) >> p.s13.shift) * p.s13.rs;
             }
         }
+        const int nt = ceil_div(n, 8);
+        float c[MT][NT][4] = {};
 #pragma unroll 1
-        for (int g0 = 0; g0 < n; g0 += 8 * NT) {
-            const int nt = min(NT, ceil_div(n - g0, 8));
-            float c[MT][NT][4] = {};
-#pragma unroll 1
-            for (int k = ks0; k < ks1; ++k) {
-                float s[2 * MT];
-                if (W8) {
-                    const int64_t kb = static_cast<int64_t>(k >> 1) * p.s13.ks;  // an item is half a block of 128
+        for (int k = ks0; k < ks1; ++k) {
+            float s[2 * MT];
+            if (W8) {
+                const int64_t kb = static_cast<int64_t>(k >> 1) * p.s13.ks;  // an item is half a block of 128
 #pragma unroll
-                    for (int m = 0; m < 2 * MT; ++m)
-                        s[m] = __ldg(ps[m] + kb);
-                }
-                cp_async_wait<D - 2>();
-                load_next();  // into the slot of the item before, which is in registers
-                if constexpr (W8) {
-                    float part[MT][NT][4] = {};
-                    multiply_item<kPlain, BF16, W8, MT, NT>(ring + slot * S::BYTES, nt, part);
-#pragma unroll
-                    for (int m = 0; m < MT; ++m)
-#pragma unroll
-                        for (int q = 0; q < NT; ++q)
-#pragma unroll
-                            for (int v = 0; v < 4; ++v)
-                                c[m][q][v] = fmaf(part[m][q][v], s[2 * m + (v >> 1)], c[m][q][v]);
-                } else {
-                    multiply_item<kPlain, BF16, W8, MT, NT>(ring + slot * S::BYTES, nt, c);
-                }
-                slot = slot + 1 == D ? 0 : slot + 1;
+                for (int m = 0; m < 2 * MT; ++m)
+                    s[m] = __ldg(ps[m] + kb);
             }
-            // Columns past inner, to the end of their 8, get zeros (their rows were).
-            if constexpr (KS == 1) {
+            cp_async_wait<D - 2>();
+            load_next();  // into the slot of the item before, which is in registers
+            if constexpr (W8) {
+                float part[MT][NT][4] = {};
+                multiply_item<kPlain, BF16, W8, MT, NT>(ring + slot * S::BYTES, nt, part);
 #pragma unroll
-                for (int q = 0; q < NT; ++q)
+                for (int m = 0; m < MT; ++m)
 #pragma unroll
-                    for (int v = 0; v < 2; ++v) {
-                        const int j = g0 + q * 8 + 2 * t + v;
-                        if (j < n) {
-                            float* row = p.h + r.list[first + j] * p.ldh;
+                    for (int q = 0; q < NT; ++q)
 #pragma unroll
-                            for (int m = 0; m < MT; ++m)
-                                if (i0 + 8 * m < p.inner)
-                                    store_h<SPLIT>(row, i0 + 8 * m, g, c[m][q][v], c[m][q][2 + v]);
-                        }
-                    }
+                        for (int v = 0; v < 4; ++v)
+                            c[m][q][v] = fmaf(part[m][q][v], s[2 * m + (v >> 1)], c[m][q][v]);
             } else {
-                float* rd = red + parity * (kWarps * NT * 4 * 32);
-                if (C::RBUF == 2)
-                    parity ^= 1;  // the other buffer is rewritten only after the next unit's barrier
-                else
-                    unit_sync<KS>(warp / KS);
+                multiply_item<kPlain, BF16, W8, MT, NT>(ring + slot * S::BYTES, nt, c);
+            }
+            slot = slot + 1 == D ? 0 : slot + 1;
+        }
+        // Columns past inner, to the end of their 8, get zeros (their rows were).
+        if constexpr (KS == 1) {
 #pragma unroll
-                for (int q = 0; q < NT; ++q)
+            for (int q = 0; q < NT; ++q)
 #pragma unroll
-                    for (int v = 0; v < 4; ++v)
-                        rd[((warp * NT + q) * 4 + v) * 32 + lane] = c[0][q][v];
-                unit_sync<KS>(warp / KS);
-                const int w0 = warp / KS * KS;
-                for (int idx = threadIdx.x - 32 * w0; idx < nt * 64; idx += 32 * KS) {
-                    const int l = idx & 31, wh = (idx >> 5) & 1, q = idx >> 6;
-                    float gate = 0.f, up = 0.f;
+                for (int v = 0; v < 2; ++v) {
+                    const int j = q * 8 + 2 * t + v;
+                    if (j < n) {
+                        float* row = p.h + r.list[first + j] * p.ldh;
 #pragma unroll
-                    for (int w = w0; w < w0 + KS; ++w) {
-                        gate += rd[((w * NT + q) * 4 + wh) * 32 + l];
-                        up += rd[((w * NT + q) * 4 + 2 + wh) * 32 + l];
+                        for (int m = 0; m < MT; ++m)
+                            if (i0 + 8 * m < p.inner)
+                                store_h<SPLIT>(row, i0 + 8 * m, g, c[m][q][v], c[m][q][2 + v]);
                     }
-                    const int j = g0 + q * 8 + 2 * (l & 3) + wh;
-                    if (j < n)
-                        store_h<SPLIT>(p.h + r.list[first + j] * p.ldh, i0, l >> 2, gate, up);
                 }
+        } else {
+            float* rd = red + parity * (kWarps * NT * 4 * 32);
+            if (C::RBUF == 2)
+                parity ^= 1;  // the other buffer is rewritten only after the next unit's barrier
+            else
+                unit_sync<KS>(warp / KS);
+#pragma unroll
+            for (int q = 0; q < NT; ++q)
+#pragma unroll
+                for (int v = 0; v < 4; ++v)
+                    rd[((warp * NT + q) * 4 + v) * 32 + lane] = c[0][q][v];
+            unit_sync<KS>(warp / KS);
+            const int w0 = warp / KS * KS;
+            for (int idx = threadIdx.x - 32 * w0; idx < nt * 64; idx += 32 * KS) {
+                const int l = idx & 31, wh = (idx >> 5) & 1, q = idx >> 6;
+                float gate = 0.f, up = 0.f;
+#pragma unroll
+                for (int w = w0; w < w0 + KS; ++w) {
+                    gate += rd[((w * NT + q) * 4 + wh) * 32 + l];
+                    up += rd[((w * NT + q) * 4 + 2 + wh) * 32 + l];
+                }
+                const int j = q * 8 + 2 * (l & 3) + wh;
+                if (j < n)
+                    store_h<SPLIT>(p.h + r.list[first + j] * p.ldh, i0, l >> 2, gate, up);
             }
         }
     }
@@ -852,7 +854,7 @@ __global__ void __launch_bounds__(kThreads, DownCfg<W8, NT, MT>::CTAS) moe_down_
         sums[i] = 0.f;
     if (TURNS && threadIdx.x == 0)
         pass_turn(turn, 0);
-    route_all(p, r);  // the logits were complete before the up kernel let this one start
+    route_all(p, r, 8 * NT);  // the logits were complete before the up kernel let this one start
     pdl_wait();       // h
 
     const int nit = ceil_div(p.inner, kItem);
@@ -881,7 +883,7 @@ __global__ void __launch_bounds__(kThreads, DownCfg<W8, NT, MT>::CTAS) moe_down_
     // Loader: per expert of the range, per token group, its K items (pointers as in
     // the up kernel; h's rows are whole groups of 8 columns, zeros past inner).
     const int kpad = (p.inner + 7) / 8 * 8;
-    int lq = q0, lg = 0, lk = 0, lend = 0, lslot = 0, lgroups = 0;
+    int lq = q0, lk = 0, lend = 0, lslot = 0;
     const uint8_t* wr[2 * MT];
     const uint8_t* hr[NT];
     uint32_t wbytes = 0, hbytes = 0;  // bit m: row m is inside; bit q: token of tile q
@@ -892,7 +894,6 @@ __global__ void __launch_bounds__(kThreads, DownCfg<W8, NT, MT>::CTAS) moe_down_
                 int a;
                 segment(lq, a, lk, lend);
                 const int n = r.aoff[a + 1] - r.aoff[a];
-                lgroups = ceil_div(n, 8 * NT);
                 const uint8_t* we = wb + static_cast<int64_t>(r.act[a]) * p.stride_w2 * ES + lk * (kItem * ES) + t * 16;
                 wbytes = hbytes = 0;
 #pragma unroll
@@ -906,7 +907,7 @@ __global__ void __launch_bounds__(kThreads, DownCfg<W8, NT, MT>::CTAS) moe_down_
                 }
 #pragma unroll
                 for (int q = 0; q < NT; ++q) {
-                    const int j = lg * 8 * NT + q * 8 + g;
+                    const int j = q * 8 + g;
                     hr[q] = hb + lk * (kItem * 4) + half_k<W8>(t, 0) * 4;
                     if (j < n) {
                         hr[q] += static_cast<int64_t>(r.list[r.aoff[a] + j]) * p.ldh * 4;
@@ -933,10 +934,7 @@ __global__ void __launch_bounds__(kThreads, DownCfg<W8, NT, MT>::CTAS) moe_down_
             }
             if (++lk == lend) {
                 fresh = true;
-                if (++lg == lgroups) {
-                    lg = 0;
-                    lq += TURNS ? kWarps : lend - lq % nit;
-                }
+                lq += TURNS ? kWarps : lend - lq % nit;
             }
         }
         cp_async_commit();
@@ -961,59 +959,56 @@ __global__ void __launch_bounds__(kThreads, DownCfg<W8, NT, MT>::CTAS) moe_down_
                 ps[m] = p.s2.data + r.act[a] * p.s2.bs +
                         static_cast<int64_t>(min(r0 + 8 * m + g, p.hidden - 1) >> p.s2.shift) * p.s2.rs;
         }
+        const int nt = ceil_div(n, 8);
+        float c[MT][NT][4] = {};
 #pragma unroll 1
-        for (int g0 = 0; g0 < n; g0 += 8 * NT) {
-            const int nt = min(NT, ceil_div(n - g0, 8));
-            float c[MT][NT][4] = {};
-#pragma unroll 1
-            for (int k = k0; k < k1; ++k) {
-                float s[2 * MT];
-                if (W8) {
-                    const int64_t kb = static_cast<int64_t>(k >> 1) * p.s2.ks;  // an item is half a block of 128
+        for (int k = k0; k < k1; ++k) {
+            float s[2 * MT];
+            if (W8) {
+                const int64_t kb = static_cast<int64_t>(k >> 1) * p.s2.ks;  // an item is half a block of 128
 #pragma unroll
-                    for (int m = 0; m < 2 * MT; ++m)
-                        s[m] = __ldg(ps[m] + kb);
-                }
-                cp_async_wait<D - 2>();
-                load_next();  // into the slot of the item before, which is in registers
-                if constexpr (W8) {
-                    float part8[MT][NT][4] = {};
-                    multiply_item<HOW, true, W8, MT, NT>(ring + slot * S::BYTES, nt, part8);
-#pragma unroll
-                    for (int m = 0; m < MT; ++m)
-#pragma unroll
-                        for (int w = 0; w < NT; ++w)
-#pragma unroll
-                            for (int v = 0; v < 4; ++v)
-                                c[m][w][v] = fmaf(part8[m][w][v], s[2 * m + (v >> 1)], c[m][w][v]);
-                } else {
-                    multiply_item<HOW, BF16, W8, MT, NT>(ring + slot * S::BYTES, nt, c);
-                }
-                slot = slot + 1 == D ? 0 : slot + 1;
+                for (int m = 0; m < 2 * MT; ++m)
+                    s[m] = __ldg(ps[m] + kb);
             }
-            if (TURNS && in_turn && g0 == 0 && !wait_turn(turn, q - u0, p.wait_limit)) {
-                in_turn = false;
-                atomicOr(p.status, kStatusTimeout);
-                pass_turn(turn, INT_MAX);
+            cp_async_wait<D - 2>();
+            load_next();  // into the slot of the item before, which is in registers
+            if constexpr (W8) {
+                float part8[MT][NT][4] = {};
+                multiply_item<HOW, true, W8, MT, NT>(ring + slot * S::BYTES, nt, part8);
+#pragma unroll
+                for (int m = 0; m < MT; ++m)
+#pragma unroll
+                    for (int w = 0; w < NT; ++w)
+#pragma unroll
+                        for (int v = 0; v < 4; ++v)
+                            c[m][w][v] = fmaf(part8[m][w][v], s[2 * m + (v >> 1)], c[m][w][v]);
+            } else {
+                multiply_item<HOW, BF16, W8, MT, NT>(ring + slot * S::BYTES, nt, c);
             }
+            slot = slot + 1 == D ? 0 : slot + 1;
+        }
+        if (TURNS && in_turn && !wait_turn(turn, q - u0, p.wait_limit)) {
+            in_turn = false;
+            atomicOr(p.status, kStatusTimeout);
+            pass_turn(turn, INT_MAX);
+        }
 #pragma unroll
-            for (int w = 0; w < NT; ++w)
+        for (int w = 0; w < NT; ++w)
 #pragma unroll
-                for (int v = 0; v < 2; ++v) {
-                    const int j = g0 + w * 8 + 2 * t + v;
-                    if (w < nt && j < n) {
-                        const int sl = r.list[first + j];
-                        const float pw = r.p[sl];
-                        float* d = mine + (sl / p.topk) * ROWS + g;
+            for (int v = 0; v < 2; ++v) {
+                const int j = w * 8 + 2 * t + v;
+                if (w < nt && j < n) {
+                    const int sl = r.list[first + j];
+                    const float pw = r.p[sl];
+                    float* d = mine + (sl / p.topk) * ROWS + g;
 #pragma unroll
-                        for (int m = 0; m < MT; ++m) {
-                            d[16 * m] = fmaf(pw, c[m][w][v], d[16 * m]);
-                            d[16 * m + 8] = fmaf(pw, c[m][w][2 + v], d[16 * m + 8]);
-                        }
+                    for (int m = 0; m < MT; ++m) {
+                        d[16 * m] = fmaf(pw, c[m][w][v], d[16 * m]);
+                        d[16 * m + 8] = fmaf(pw, c[m][w][2 + v], d[16 * m + 8]);
                     }
                 }
-            __syncwarp();
-        }
+            }
+        __syncwarp();
         if (TURNS && in_turn && lane == 0)
             pass_turn(turn, q - u0 + 1);
         q += TURNS ? kWarps : k1 - k0;
