@@ -15,8 +15,8 @@
 // a thread holds one row of B (32x32b loads) and half of the columns, its row's
 // scale in a register and the columns' scales broadcast from shared memory.
 //
-// Measured: 64 x 16384 x 8192 27.6 us (5.0 TB/s; one wave of 152 CTAs with even row
-// shares, 31 us with 128 tiles of 128 rows), 1 x 4096 x 4096 7.5 us, of which the
+// Measured: 64 x 16384 x 8192 25.0 us (5.5 TB/s; one wave of 152 CTAs with even row
+// shares; 27.5 with one warp issuing the MMAs), 1 x 4096 x 4096 6.8 us, of which the
 // 16.8 MB take 2.5: launch, the first loads and the cluster's exchange are the rest.
 #include <algorithm>
 
@@ -29,7 +29,7 @@ namespace {
 using namespace blk;
 using tc::BM;
 
-constexpr int kThreads = 384;   // warps 0-3: producer, MMA, scales, idle; warps 4-11: promotion
+constexpr int kThreads = 384;   // warps 0-3: producer, MMA, scales, MMA; warps 4-11: promotion
 constexpr int kPromoWarps = 8;
 constexpr int kAcc = 4;         // accumulators in Tensor Memory
 constexpr int kScaleRing = 4;   // slots of kScaleGroup K blocks
@@ -51,7 +51,8 @@ struct Cfg {
     static constexpr int TMEM_COLS = max_int(32, kAcc * BN);
     static constexpr int COLS = BN / 2;  // columns of a promotion thread
     static_assert(BM * BN * 4 <= STAGES * STAGE, "a tile's sums fit in the ring");
-    static_assert((2 * STAGES + 2 * kAcc + 2 * kScaleRing + 1) * 8 + 8 <= BAR_BYTES, "barrier area");
+    static_assert((2 * STAGES + 2 * kAcc + 2 * kScaleRing + 2) * 8 + 8 <= BAR_BYTES, "barrier area");
+    static_assert(STAGES > 2 && kAcc % 2 == 0, "two warps take turns");
 };
 
 __device__ __forceinline__ float ld_cluster(uint32_t addr)
@@ -97,7 +98,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t* sfull = tempty + kAcc;
     uint64_t* sempty = sfull + kScaleRing;
     uint64_t* drain = sempty + kScaleRing;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 2);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -119,7 +120,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(smem_u32(&sfull[r]), 32);
             mbar_init(smem_u32(&sempty[r]), kPromoWarps);
         }
-        mbar_init(smem_u32(drain), 1);
+        mbar_init(smem_u32(&drain[0]), 1);
+        mbar_init(smem_u32(&drain[1]), 1);
         *abort_flag = 0;
         fence_mbar_init();
         tma_prefetch_map(&tmx);
@@ -178,45 +180,54 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (filled & (1u << s))
                     drain_wait(smem_u32(&full[s]), (fill_parity >> s) & 1u, p.wait_limit);
         }
-    } else if (warp == 1) {
-        if (lane == 0) {
-            // -------------------------------------------------------- MMA issue
-            const uint32_t idesc = idesc_f16_f32(BM, BN) | p.idesc_bits;
-            const DescWords dx = desc_words(smem_u32(xs), false), dy = desc_words(smem_u32(ys), false);
-            int stage = 0, buf = 0;
-            uint32_t phase = 0, tphase = 0;
-            bool ok = true, skip_release = p.fault == 2 && blockIdx.x == 0;
-            for (int t = first; ok && t < p.num_tiles; t += step) {
-                for (int kb = kb0; kb < kb1; ++kb) {
-                    if (!wait_bounded(smem_u32(&tempty[buf]), tphase ^ 1, abort_flag, p.wait_limit) ||
-                        !wait_bounded(smem_u32(&full[stage]), phase, abort_flag, p.wait_limit)) {
-                        raise(p, abort_flag);
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    const uint32_t d = tmem_base + static_cast<uint32_t>(buf * BN);
-                    const uint32_t xlo = dx.lo + stage * (C::X_BYTES >> 4), ylo = dy.lo + stage * (C::Y_BYTES >> 4);
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        tc_mma_w<true>(d, xlo + k * dx.kstep, dx.hi, ylo + k * dy.kstep, dy.hi, idesc, k > 0);
-                    if (!skip_release)
-                        tc_commit(smem_u32(&empty[stage]));
-                    skip_release = false;
-                    tc_commit(smem_u32(&tfull[buf]));
-                    if (++stage == C::STAGES) {
-                        stage = 0;
-                        phase ^= 1;
-                    }
-                    if (++buf == kAcc) {
-                        buf = 0;
-                        tphase ^= 1;
-                    }
-                }
+    } else if (warp == 1 || warp == 3) {
+        // ------------------------------------------------------------ MMA issue
+        // As in the pair kernel: one warp for the even K blocks and one for the odd ones,
+        // each paying its waits and commits while the other's MMAs run.
+        const int par = warp >> 1;
+        const uint32_t idesc = idesc_f16_f32(BM, BN) | p.idesc_bits;
+        const DescWords dx = desc_words(smem_u32(xs), false), dy = desc_words(smem_u32(ys), false);
+        const int blocks = (p.num_tiles - first + step - 1) / step * (kb1 - kb0);
+        int stage = par, buf = par;
+        uint32_t phase = 0, tphase = 0;
+        bool skip_release = p.fault == 2 && blockIdx.x == 0 && par == 0;
+        const bool chosen = elect_one();
+#pragma unroll 1
+        for (int n = par; n < blocks; n += 2) {
+            const uint32_t fa = smem_u32(&full[stage]), te = smem_u32(&tempty[buf]);
+            // even lanes: the accumulator is free; odd lanes: the operands are here
+            if (!wait_lanes(lane & 1 ? fa : te, lane & 1 ? phase : tphase ^ 1, abort_flag, p.wait_limit)) {
+                raise(p, abort_flag);
+                break;
             }
-            // no MMA may still be running when Tensor Memory is released
-            tc_commit(smem_u32(drain));
-            drain_wait(smem_u32(drain), 0, p.wait_limit);
+            tc_fence_after();
+            if (chosen) {
+                const uint32_t d = tmem_base + static_cast<uint32_t>(buf * BN);
+                const uint32_t xlo = dx.lo + stage * (C::X_BYTES >> 4), ylo = dy.lo + stage * (C::Y_BYTES >> 4);
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    tc_mma_w<true>(d, xlo + k * dx.kstep, dx.hi, ylo + k * dy.kstep, dy.hi, idesc, k > 0);
+                tc_commit(smem_u32(&tfull[buf]));
+                if (!skip_release)
+                    tc_commit(smem_u32(&empty[stage]));
+            }
+            __syncwarp();
+            skip_release = false;
+            stage += 2;
+            if (stage >= C::STAGES) {
+                stage -= C::STAGES;
+                phase ^= 1;
+            }
+            buf += 2;
+            if (buf >= kAcc) {
+                buf -= kAcc;
+                tphase ^= 1;
+            }
+        }
+        // no MMA may still be running when Tensor Memory is released
+        if (chosen) {
+            tc_commit(smem_u32(&drain[par]));
+            drain_wait(smem_u32(&drain[par]), 0, p.wait_limit);
         }
     } else if (warp == 2) {
         // ------------------------------------------------------------ scales: 128 rows of B, BN rows of A
