@@ -11,7 +11,8 @@
 // and its use.  A warp item is 16 (or 32) weight rows by 64 elements of K; the
 // warps of a CTA split K.
 //
-// Products use mma.sync with fp32 accumulation, weights on the 16-row side and 8
+// Products use mma.sync with fp32 accumulation within an item, items added to
+// nearest in fp32 registers (add_item), weights on the 16-row side and 8
 // tokens on the other.  The up kernel multiplies x as it is, m16n8k16 in x's
 // type, with weights of that type or E4M3 ones widened to it (exact).  h is fp32;
 // for bf16 and E4M3 weights it is stored as the sum of two bf16 values (16
@@ -555,6 +556,22 @@ __device__ __forceinline__ void multiply_item(uint32_t st, int nt, float (&c)[MT
     }
 }
 
+// Adds an item's products to the sums, times the rows' scales (8-bit weights).  Every
+// item starts from zero: an MMA cuts its sums off rather than rounding them, so a
+// chain of them over all of K ends low, by 1e-4 of the result at K = 65536; here 4
+// to 16 MMAs are chained, and the items are added in fp32 to nearest.
+template <bool W8, int MT, int NT>
+__device__ __forceinline__ void add_item(float (&c)[MT][NT][4], const float (&part)[MT][NT][4], const float (&s)[2 * MT])
+{
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int v = 0; v < 4; ++v)
+                c[m][n][v] = W8 ? fmaf(part[m][n][v], s[2 * m + (v >> 1)], c[m][n][v]) : c[m][n][v] + part[m][n][v];
+}
+
 __device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; }
 
 // ---------------------------------------------------------------- up
@@ -719,7 +736,7 @@ __global__ void __launch_bounds__(kThreads, UpCfg<W8, MT, NT, KS>::CTAS) moe_up_
         float c[MT][NT][4] = {};
 #pragma unroll 1
         for (int k = ks0; k < ks1; ++k) {
-            float s[2 * MT];
+            float s[2 * MT] = {};
             if (W8) {
                 const int64_t kb = static_cast<int64_t>(k >> 1) * p.s13.ks;  // an item is half a block of 128
 #pragma unroll
@@ -728,19 +745,9 @@ __global__ void __launch_bounds__(kThreads, UpCfg<W8, MT, NT, KS>::CTAS) moe_up_
             }
             cp_async_wait<D - 2>();
             load_next();  // into the slot of the item before, which is in registers
-            if constexpr (W8) {
-                float part[MT][NT][4] = {};
-                multiply_item<kPlain, BF16, W8, MT, NT>(ring + slot * S::BYTES, nt, part);
-#pragma unroll
-                for (int m = 0; m < MT; ++m)
-#pragma unroll
-                    for (int q = 0; q < NT; ++q)
-#pragma unroll
-                        for (int v = 0; v < 4; ++v)
-                            c[m][q][v] = fmaf(part[m][q][v], s[2 * m + (v >> 1)], c[m][q][v]);
-            } else {
-                multiply_item<kPlain, BF16, W8, MT, NT>(ring + slot * S::BYTES, nt, c);
-            }
+            float part[MT][NT][4] = {};
+            multiply_item<kPlain, BF16, W8, MT, NT>(ring + slot * S::BYTES, nt, part);
+            add_item<W8, MT, NT>(c, part, s);
             slot = slot + 1 == D ? 0 : slot + 1;
         }
         // Columns past inner, to the end of their 8, get zeros (their rows were).
@@ -963,7 +970,7 @@ __global__ void __launch_bounds__(kThreads, DownCfg<W8, NT, MT>::CTAS) moe_down_
         float c[MT][NT][4] = {};
 #pragma unroll 1
         for (int k = k0; k < k1; ++k) {
-            float s[2 * MT];
+            float s[2 * MT] = {};
             if (W8) {
                 const int64_t kb = static_cast<int64_t>(k >> 1) * p.s2.ks;  // an item is half a block of 128
 #pragma unroll
@@ -972,19 +979,9 @@ __global__ void __launch_bounds__(kThreads, DownCfg<W8, NT, MT>::CTAS) moe_down_
             }
             cp_async_wait<D - 2>();
             load_next();  // into the slot of the item before, which is in registers
-            if constexpr (W8) {
-                float part8[MT][NT][4] = {};
-                multiply_item<HOW, true, W8, MT, NT>(ring + slot * S::BYTES, nt, part8);
-#pragma unroll
-                for (int m = 0; m < MT; ++m)
-#pragma unroll
-                    for (int w = 0; w < NT; ++w)
-#pragma unroll
-                        for (int v = 0; v < 4; ++v)
-                            c[m][w][v] = fmaf(part8[m][w][v], s[2 * m + (v >> 1)], c[m][w][v]);
-            } else {
-                multiply_item<HOW, BF16, W8, MT, NT>(ring + slot * S::BYTES, nt, c);
-            }
+            float part[MT][NT][4] = {};
+            multiply_item<HOW, BF16 || W8, W8, MT, NT>(ring + slot * S::BYTES, nt, part);
+            add_item<W8, MT, NT>(c, part, s);
             slot = slot + 1 == D ? 0 : slot + 1;
         }
         if (TURNS && in_turn && !wait_turn(turn, q - u0, p.wait_limit)) {

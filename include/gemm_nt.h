@@ -378,7 +378,8 @@ gemm_status_t gemm_nt_block128_quantize(const void *X, gemm_dtype_t x_type, int6
  * E4M3 with scales S13 and S2 (rows 1 or 128, batch_stride the expert stride;
  * null for 16-bit weights).  Only the weights of experts that a token chose are
  * read.  x and the weights are multiplied exactly (8-bit weights widened to 16
- * bits) with fp32 accumulation; h is computed in fp32 and multiplied in two parts
+ * bits) and accumulated in fp32, by the tensor cores over 64 elements of K at a time and
+ * to nearest over those; h is computed in fp32 and multiplied in two parts
  * that hold at least 16 significant bits of it; Out is rounded once to x_type.
  * Sums over experts follow the expert index, so results do not depend on the run.
  *
