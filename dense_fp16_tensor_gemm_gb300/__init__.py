@@ -391,7 +391,8 @@ def gemm_nt_batched(A, B, out=None, path=Path.AUTO, stream=None, out_dtype=None)
 # ---------------------------------------------------------------- one scale per block of 128
 # These calls serve single tokens, where the host's time per call counts: types
 # are looked up once, the stream handle is read without building a Stream object,
-# and an output is one allocation.
+# and an output is one allocation.  With `stream` they run as under
+# torch.cuda.stream(stream), allocations included.
 _torch = None
 _CODES = {}     # torch dtype -> gemm_dtype_t value
 _IN_F8 = _OUT = _X16 = ()
@@ -415,23 +416,41 @@ def _one_of(dtype, allowed, what):
     return _CODES[dtype]
 
 
-def _stream_of(stream, device):
-    """The handle of `stream`, or of torch's current stream on the device."""
-    if stream is None and device.type == "cuda":
-        return _torch._C._cuda_getCurrentRawStream(device.index)
-    return _stream_handle(stream)
+def _stream_of(device):
+    """The handle of torch's current stream on the device."""
+    return _torch._C._cuda_getCurrentRawStream(device.index)
 
 
-def _keep(tensors, stream):
-    """Temporaries that work on `stream` still reads: torch's allocator must not
-    hand their memory to another stream before that work is done."""
+def _elsewhere(stream):
+    """`stream` as a torch stream if it is another than torch's current one, else None."""
     if stream is None:
-        return
-    handle = _stream_handle(stream)
-    if handle != _torch.cuda.current_stream().cuda_stream:
-        s = stream if isinstance(stream, _torch.cuda.Stream) else _torch.cuda.ExternalStream(handle)
-        for t in tensors:
-            t.record_stream(s)
+        return None
+    cuda, handle = (_torch or _init_torch()).cuda, _stream_handle(stream)
+    if handle == cuda.current_stream().cuda_stream:
+        return None
+    return stream if isinstance(stream, cuda.Stream) else cuda.ExternalStream(handle)
+
+
+def _record(result, stream, given):
+    """Keeps the tensors of a call's result, but for the caller's own `given`, from
+    being handed out again before what `stream` holds when they are freed is done."""
+    if isinstance(result, tuple):
+        for r in result:
+            _record(r, stream, given)
+    elif result is not given:
+        result.record_stream(stream)
+
+
+def _run_on(side, call, *args, given=None):
+    """call(*args) with `side` as torch's current stream, so that its temporaries and
+    results come from side's memory: a block of the caller's current stream may still
+    be in use by work queued there, which side does not wait for.  The results are
+    recorded for the caller's stream, which will read them."""
+    caller = _torch.cuda.current_stream()
+    with _torch.cuda.stream(side):
+        result = call(*args)
+    _record(result, caller, given)
+    return result
 
 
 def _pitch(shape, strides, name):
@@ -464,6 +483,9 @@ def gemm_nt_block128_tensors(A, SA, B, SB, out=None, path=Path.AUTO, stream=None
     (stride 0 shares an operand), a batch of products.  ``out``/``out_dtype`` as
     in :func:`gemm_nt`, float32 by default.
     """
+    side = _elsewhere(stream)
+    if side is not None:
+        return _run_on(side, gemm_nt_block128_tensors, A, SA, B, SB, out, path, None, out_dtype, given=out)
     torch = _torch or _init_torch()
     ash, bsh = A.shape, B.shape
     dims = len(ash)
@@ -488,7 +510,7 @@ def gemm_nt_block128_tensors(A, SA, B, SB, out=None, path=Path.AUTO, stream=None
     gemm_nt_block128(A.data_ptr(), _scale128(SA, M, K, "SA"), B.data_ptr(), _scale128(SB, N, K, "SB"), out.data_ptr(),
                      ab, ot, M, N, K, _pitch(ash, ast, "A"), _pitch(bsh, bst, "B"), _pitch(shape, ost, "out"),
                      ast[0] if batched else 0, bst[0] if batched else 0, ost[0] if batched else 0,
-                     ash[0] if batched else 1, path, _stream_of(stream, device))
+                     ash[0] if batched else 1, path, _stream_of(device))
     return out
 
 
@@ -518,11 +540,14 @@ def quantize_block128(X, q_dtype=None, block_rows=1, transposed=False, stream=No
     Rows of the codes start on 16-byte boundaries; scales of single rows are
     stored with the rows adjacent.
     """
-    q, s, _, qt, st, _ = _quantize(X, q_dtype, block_rows, transposed, stream)
+    side = _elsewhere(stream)
+    if side is not None:
+        return _run_on(side, quantize_block128, X, q_dtype, block_rows, transposed)
+    q, s, _, qt, st, _ = _quantize(X, q_dtype, block_rows, transposed)
     return (q, s, qt, st) if transposed else (q, s)
 
 
-def _quantize(X, q_dtype, block_rows, transposed, stream):
+def _quantize(X, q_dtype, block_rows, transposed):
     """The work of quantize_block128: Q, S and S as the C struct, and the same
     of X transposed."""
     torch = _torch or _init_torch()
@@ -540,18 +565,18 @@ def _quantize(X, q_dtype, block_rows, transposed, stream):
     q, s, ldq, sq = _quantized(rows, cols, q_dtype, block_rows, device)
     qt, st, ldqt, sqt = _quantized(cols, rows, q_dtype, block_rows, device) if transposed else (None, None, 0, None)
     gemm_nt_block128_quantize(X.data_ptr(), xt, rows, cols, ldx, q.data_ptr(), ldq, sq, qt.data_ptr() if transposed else 0,
-                              ldqt, sqt, code, _stream_of(stream, device))
+                              ldqt, sqt, code, _stream_of(device))
     return q, s, sq, qt, st, sqt
 
 
-def _product(A, SA, B, SB, dtype, stream):
+def _product(A, SA, B, SB, dtype):
     """A @ B.T of two matrices of codes whose scales are C structs."""
     (M, K), (N, _) = A.shape, B.shape
     device = A.device
     out = _torch.empty((M, N), dtype=dtype, device=device)
     gemm_nt_block128(A.data_ptr(), SA, B.data_ptr(), SB, out.data_ptr(), _CODES[A.dtype], _CODES[dtype], M, N, K,
                      _pitch((M, K), A.stride(), "A"), _pitch((N, K), B.stride(), "B"), max(N, 1), 0, 0, 0, 1, 0,
-                     _stream_of(stream, device))
+                     _stream_of(device))
     return out
 
 
@@ -570,13 +595,14 @@ def linear_block128(X, W, SW, stream=None):
     as ``quantize_block128(weight, block_rows=128)`` leaves it.  Returns Y in X's
     type and what :func:`linear_block128_backward` needs (X transposed, in 8
     bits)."""
+    side = _elsewhere(stream)
+    if side is not None:
+        return _run_on(side, linear_block128, X, W, SW)
     if X.dim() != 2:
         raise ValueError("X must be a matrix")
     sw = _weight(W, SW, X.shape[1], "W")
-    q, s, sq, qt, st, _ = _quantize(X, W.dtype, 1, True, stream)
-    y = _product(q, sq, W, sw, X.dtype, stream)
-    _keep((q, s), stream)
-    return y, (qt, st)
+    q, s, sq, qt, st, _ = _quantize(X, W.dtype, 1, True)  # s, which sq points into, lives until the product is launched
+    return _product(q, sq, W, sw, X.dtype), (qt, st)
 
 
 def linear_block128_backward(dY, saved, WT, SWT, stream=None):
@@ -584,6 +610,10 @@ def linear_block128_backward(dY, saved, WT, SWT, stream=None):
     dY.T @ X in float32, both products in 8 bits.  WT (in, out) and SWT are W's
     codes and scales transposed (the ``transposed`` half of
     ``quantize_block128(weight, block_rows=128, transposed=True)``)."""
+    side = _elsewhere(stream)
+    if side is not None:
+        _record(tuple(saved), side, None)
+        return _run_on(side, linear_block128_backward, dY, saved, WT, SWT)
     if dY.dim() != 2:
         raise ValueError("dY must be a matrix")
     qt_x, st_x = saved
@@ -591,11 +621,8 @@ def linear_block128_backward(dY, saved, WT, SWT, stream=None):
     sw, sx = _weight(WT, SWT, width, "WT"), _weight(qt_x, st_x, tokens, "XT")
     if qt_x.dtype != WT.dtype:
         raise TypeError("the weights' and the saved codes' types differ")
-    q, s, sq, qt, st, sqt = _quantize(dY, WT.dtype, 1, True, stream)
-    dx = _product(q, sq, WT, sw, dY.dtype, stream)
-    dw = _product(qt, sqt, qt_x, sx, _torch.float32, stream)
-    _keep((q, s, qt, st, qt_x, st_x), stream)
-    return dx, dw
+    q, s, sq, qt, st, sqt = _quantize(dY, WT.dtype, 1, True)
+    return _product(q, sq, WT, sw, dY.dtype), _product(qt, sqt, qt_x, sx, _torch.float32)
 
 
 _MOE_SHAPES = ("shapes: X (tokens, hidden), logits (tokens, experts), W13 (experts, 2*inner, hidden), "
@@ -614,6 +641,9 @@ def moe_few_tokens(X, logits, W13, W2, topk, S13=None, S2=None, renormalize=True
     otherwise over all of its experts.  ``workspace``, a uint8 tensor of
     :func:`gemm_nt_moe_workspace_bytes` bytes, is allocated if not given.
     """
+    side = _elsewhere(stream)
+    if side is not None:
+        return _run_on(side, moe_few_tokens, X, logits, W13, W2, topk, S13, S2, renormalize, out, workspace, given=out)
     torch = _torch or _init_torch()
     xsh, lsh, s13h, s2h = X.shape, logits.shape, W13.shape, W2.shape
     if len(xsh) != 2 or len(lsh) != 2 or len(s13h) != 3 or len(s2h) != 3:
@@ -643,10 +673,9 @@ def moe_few_tokens(X, logits, W13, W2, topk, S13=None, S2=None, renormalize=True
     if workspace is None:
         need = gemm_nt_moe_workspace_bytes(tokens, topk, inner) if topk > 0 else 0
         workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=device)
-        _keep((workspace,), stream)
     t13, t2 = W13.stride(), W2.stride()
     gemm_nt_moe(X.data_ptr(), _pitch(xsh, X.stride(), "X"), logits.data_ptr(), _pitch(lsh, logits.stride(), "logits"),
                 W13.data_ptr(), _pitch(s13h, t13, "W13"), t13[0], s13, W2.data_ptr(), _pitch(s2h, t2, "W2"), t2[0], s2,
                 out.data_ptr(), _pitch(xsh, out.stride(), "out"), xt, wt, tokens, experts, topk, hidden, inner,
-                renormalize, workspace.data_ptr(), workspace.numel(), _stream_of(stream, device))
+                renormalize, workspace.data_ptr(), workspace.numel(), _stream_of(device))
     return out
