@@ -416,6 +416,18 @@ def _one_of(dtype, allowed, what):
     return _CODES[dtype]
 
 
+def _same_device(device, *tensors):
+    """Refuses tensors (None: not given) that are not all on `device`, a CUDA device and
+    torch's current one: the library reads their addresses on that device."""
+    if device.type != "cuda":
+        raise ValueError("tensors must be on a CUDA device, not %s" % device)
+    for t in tensors:
+        if t is not None and t.device != device:
+            raise ValueError("tensors on %s and %s in one call" % (device, t.device))
+    if device.index != _torch.cuda.current_device():
+        raise ValueError("tensors on %s, which is not the current device" % device)
+
+
 def _stream_of(device):
     """The handle of torch's current stream on the device."""
     return _torch._C._cuda_getCurrentRawStream(device.index)
@@ -501,14 +513,16 @@ def gemm_nt_block128_tensors(A, SA, B, SB, out=None, path=Path.AUTO, stream=None
     M, K = ash[-2:]
     N = bsh[-2]
     shape = (ash[0], M, N) if batched else (M, N)
+    sa, sb = _scale128(SA, M, K, "SA"), _scale128(SB, N, K, "SB")
     device = A.device
+    _same_device(device, SA, B, SB, out)
     if out is None:
         out = torch.empty(shape, dtype=dt, device=device)
     elif tuple(out.shape) != shape:
         raise ValueError("out must have shape (M,N), with A's batch dimension")
     ast, bst, ost = A.stride(), B.stride(), out.stride()
-    gemm_nt_block128(A.data_ptr(), _scale128(SA, M, K, "SA"), B.data_ptr(), _scale128(SB, N, K, "SB"), out.data_ptr(),
-                     ab, ot, M, N, K, _pitch(ash, ast, "A"), _pitch(bsh, bst, "B"), _pitch(shape, ost, "out"),
+    gemm_nt_block128(A.data_ptr(), sa, B.data_ptr(), sb, out.data_ptr(), ab, ot, M, N, K,
+                     _pitch(ash, ast, "A"), _pitch(bsh, bst, "B"), _pitch(shape, ost, "out"),
                      ast[0] if batched else 0, bst[0] if batched else 0, ost[0] if batched else 0,
                      ash[0] if batched else 1, path, _stream_of(device))
     return out
@@ -547,9 +561,9 @@ def quantize_block128(X, q_dtype=None, block_rows=1, transposed=False, stream=No
     return (q, s, qt, st) if transposed else (q, s)
 
 
-def _quantize(X, q_dtype, block_rows, transposed):
+def _quantize(X, q_dtype, block_rows, transposed, beside=()):
     """The work of quantize_block128: Q, S and S as the C struct, and the same
-    of X transposed."""
+    of X transposed.  `beside`: what the caller's next calls read on X's device."""
     torch = _torch or _init_torch()
     shape = X.shape
     if len(shape) != 2:
@@ -562,6 +576,7 @@ def _quantize(X, q_dtype, block_rows, transposed):
     ldx = _pitch(shape, X.stride(), "X")
     rows, cols = shape
     device = X.device
+    _same_device(device, *beside)
     q, s, ldq, sq = _quantized(rows, cols, q_dtype, block_rows, device)
     qt, st, ldqt, sqt = _quantized(cols, rows, q_dtype, block_rows, device) if transposed else (None, None, 0, None)
     gemm_nt_block128_quantize(X.data_ptr(), xt, rows, cols, ldx, q.data_ptr(), ldq, sq, qt.data_ptr() if transposed else 0,
@@ -601,7 +616,7 @@ def linear_block128(X, W, SW, stream=None):
     if X.dim() != 2:
         raise ValueError("X must be a matrix")
     sw = _weight(W, SW, X.shape[1], "W")
-    q, s, sq, qt, st, _ = _quantize(X, W.dtype, 1, True)  # s, which sq points into, lives until the product is launched
+    q, s, sq, qt, st, _ = _quantize(X, W.dtype, 1, True, (W, SW))  # s, which sq points into, stays until the product is launched
     return _product(q, sq, W, sw, X.dtype), (qt, st)
 
 
@@ -621,7 +636,7 @@ def linear_block128_backward(dY, saved, WT, SWT, stream=None):
     sw, sx = _weight(WT, SWT, width, "WT"), _weight(qt_x, st_x, tokens, "XT")
     if qt_x.dtype != WT.dtype:
         raise TypeError("the weights' and the saved codes' types differ")
-    q, s, sq, qt, st, sqt = _quantize(dY, WT.dtype, 1, True)
+    q, s, sq, qt, st, sqt = _quantize(dY, WT.dtype, 1, True, (WT, SWT, qt_x, st_x))
     return _product(q, sq, WT, sw, dY.dtype), _product(qt, sqt, qt_x, sx, _torch.float32)
 
 
@@ -638,8 +653,8 @@ def moe_few_tokens(X, logits, W13, W2, topk, S13=None, S2=None, renormalize=True
     in X's type, or float8_e4m3fn with float32 scales S13 and S2 (one for each
     128 elements of a row, or for each 128 x 128 block).  ``renormalize``: the
     weights of a token's ``topk`` experts are normalised over those alone,
-    otherwise over all of its experts.  ``workspace``, a uint8 tensor of
-    :func:`gemm_nt_moe_workspace_bytes` bytes, is allocated if not given.
+    otherwise over all of its experts.  ``workspace``, a contiguous tensor
+    of :func:`gemm_nt_moe_workspace_bytes` bytes, is allocated if not given.
     """
     side = _elsewhere(stream)
     if side is not None:
@@ -661,21 +676,24 @@ def moe_few_tokens(X, logits, W13, W2, topk, S13=None, S2=None, renormalize=True
         raise TypeError("logits must be float32")
     if (wt == 3) != (S13 is not None) or (S13 is None) != (S2 is None):
         raise ValueError("8-bit weights take S13 and S2, 16-bit weights none")
-    if out is None:
-        out = torch.empty((tokens, hidden), dtype=X.dtype, device=device)
-    elif tuple(out.shape) != (tokens, hidden) or out.dtype != X.dtype:
-        raise ValueError("out must have X's shape and type")
     s13 = s2 = None
     if S13 is not None:
         if S13.dim() != 3 or S2.dim() != 3 or S13.shape[0] != experts or S2.shape[0] != experts:
             raise ValueError("S13 and S2 need a leading expert dimension")
         s13, s2 = _scale128(S13, 2 * inner, hidden, "S13"), _scale128(S2, hidden, inner, "S2")
+    _same_device(device, logits, W13, W2, S13, S2, out, workspace)
+    if out is None:
+        out = torch.empty((tokens, hidden), dtype=X.dtype, device=device)
+    elif tuple(out.shape) != (tokens, hidden) or out.dtype != X.dtype:
+        raise ValueError("out must have X's shape and type")
     if workspace is None:
         need = gemm_nt_moe_workspace_bytes(tokens, topk, inner) if topk > 0 else 0
         workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=device)
+    elif not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
     t13, t2 = W13.stride(), W2.stride()
     gemm_nt_moe(X.data_ptr(), _pitch(xsh, X.stride(), "X"), logits.data_ptr(), _pitch(lsh, logits.stride(), "logits"),
                 W13.data_ptr(), _pitch(s13h, t13, "W13"), t13[0], s13, W2.data_ptr(), _pitch(s2h, t2, "W2"), t2[0], s2,
                 out.data_ptr(), _pitch(xsh, out.stride(), "out"), xt, wt, tokens, experts, topk, hidden, inner,
-                renormalize, workspace.data_ptr(), workspace.numel(), _stream_of(device))
+                renormalize, workspace.data_ptr(), workspace.nbytes, _stream_of(device))
     return out
