@@ -23,6 +23,38 @@ __device__ __forceinline__ float scale_at(const ScaleView& s, int b, int row, in
 {
     return __ldg(s.data + b * s.bs + static_cast<int64_t>(row >> s.shift) * s.rs + static_cast<int64_t>(kb) * s.ks);
 }
+
+// A block's sum p times its two scales, which may hold any fp32 values: nothing on
+// the way may leave the normal range while the result is inside.  p is zero or, in
+// E4M3, from 2^-18 to 2^25, in E5M2 from 2^-32 to 2^39: p * s is zero or normal (or
+// has 22 bits left), and the other scale may follow, if |s| lies between 2^-109 or
+// 2^-94 and 2^80; zero, infinity and NaN decide the result alone.  2^-109 takes in
+// what the quantiser gives a block of zeros, 2^-100 / 448.
+__device__ __forceinline__ uint32_t plain_from(int e5m2) { return e5m2 ? (127u - 94) << 23 : (127u - 109) << 23; }
+constexpr uint32_t kPlainTo = (127u + 80) << 23;
+__device__ __forceinline__ bool plain_scale(float s, uint32_t from)
+{
+    const uint32_t u = __float_as_uint(s) & 0x7fffffffu;
+    return u - from <= kPlainTo - from || u == 0 || u >= 0x7f800000u;
+}
+__device__ __forceinline__ bool is_normal(float f)
+{
+    return (__float_as_uint(f) & 0x7fffffffu) - 0x00800000u < 0x7f000000u;
+}
+
+// p * s * w as (p * first) * second.  The scales' product where that is normal or
+// exact; else both scales are below 1, or both above it: the one nearer to 1 first.
+struct Factors {
+    float first, second;
+};
+__device__ __forceinline__ Factors scale_factors(float s, float w)
+{
+    const float f = s * w, as = fabsf(s), aw = fabsf(w);
+    if (is_normal(f) || as == 0.f || aw == 0.f || !(as < INFINITY) || !(aw < INFINITY))
+        return {f, 1.f};
+    const bool swap = (as > aw) == (fabsf(f) < 1.f);
+    return swap ? Factors{s, w} : Factors{w, s};
+}
 #endif
 
 // One block-scaled product, for every kernel.

@@ -110,13 +110,23 @@ __global__ void __launch_bounds__(kThreads) block128_any_kernel(const BlkParams 
 #pragma unroll
             for (int c = 0; c < 8; ++c)
                 fb[c] = scale_at(p.sb, b, min(n0 + wc + 8 * (c >> 1) + 2 * (lane & 3) + (c & 1), p.N - 1), kb);
+            const auto add = [&](auto factors) {
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
+                for (int i = 0; i < 2; ++i)
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
+                    for (int j = 0; j < 4; ++j)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        acc[i][j][e] = fmaf(part[i][j][e] * fb[2 * j + (e & 1)], fa[2 * i + (e >> 1)], acc[i][j][e]);
+                        for (int e = 0; e < 4; ++e) {
+                            const Factors f = factors(fa[2 * i + (e >> 1)], fb[2 * j + (e & 1)]);
+                            acc[i][j][e] = fmaf(part[i][j][e] * f.first, f.second, acc[i][j][e]);
+                        }
+            };
+            const uint32_t from = plain_from(E5M2);
+            if (__all_sync(0xffffffffu, plain_scale(fa[0], from) && plain_scale(fa[1], from) && plain_scale(fa[2], from) &&
+                                            plain_scale(fa[3], from)))
+                add([](float s, float w) { return Factors{s, w}; });
+            else
+                add([](float s, float w) { return scale_factors(s, w); });
         }
         typename S::T* out = static_cast<typename S::T*>(p.out) + b * p.stride_o;
 #pragma unroll

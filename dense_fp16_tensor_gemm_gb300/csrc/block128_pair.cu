@@ -33,6 +33,10 @@
 //   tfull[b], tempty[b]  accumulators: leader's commit to both CTAs / one
 //                        arrival per promotion warp of both, at the leader
 //   sfull[r], sempty[r]  scale ring, within the CTA
+// The scales may hold any fp32 values.  Where their product (by row: a block's sum
+// times the column's scale) may leave the normal range on the way, the scale warp
+// marks the group, and its blocks are scaled in another order, or in two steps inside
+// Tensor Memory: 3-4 % for the check, at 8192 x 8192 x 8192 407 us for 393.
 // Every wait is bounded.
 #include <algorithm>
 
@@ -183,16 +187,61 @@ __device__ __forceinline__ void store_tile(const BlkParams& p, const uint64_t (&
         store_tile<OT, C + SEG>(p, acc, stage, b, row0, col0, lane);
 }
 
+// Whether the scales of a group's K blocks 0 to `last`, landed at shared address `s`,
+// need no care: the smallest and the largest of the rows' times those of the column
+// blocks' are normal, or (BROW) every column's is one to multiply by first.  For the
+// whole warp, four rows or eight columns a lane; few instructions, which promotion
+// warps wait for (200 a group cost 3 % of 8192 x 8192 x 8192).
+template <bool BROW>
+__device__ __forceinline__ bool plain_group(uint32_t s, int last, uint32_t from)
+{
+    const uint32_t lane = threadIdx.x & 31;
+    bool plain;
+    if (BROW) {
+        uint32_t top = 0;
+#pragma unroll
+        for (int i = 0; i < kScaleGroup; ++i) {
+            const uint32_t at = s + min(i, last) * (kScaleFloats * 4) + 512 + 16 * lane;
+            top = max(top, max(beyond(lds_f32x4(at), from), beyond(lds_f32x4(at + 512), from)));
+        }
+        plain = top <= 2u * (kPlainTo - from);
+    } else {
+        float lo = INFINITY, hi = 0.f, blo = INFINITY, bhi = 0.f;
+#pragma unroll
+        for (int i = 0; i < kScaleGroup; ++i) {
+            const uint32_t at = s + min(i, last) * (kScaleFloats * 4);
+            float v[4];
+            const ulonglong2 w = lds_f32x4(at + 16 * lane);
+            unpack2(w.x, v[0], v[1]);
+            unpack2(w.y, v[2], v[3]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                lo = fminf(lo, fabsf(v[e]));
+                hi = fmaxf(hi, fabsf(v[e]));
+            }
+            const float f = fabsf(lds_f32(at + 512 + 4 * (lane & 1)));
+            blo = fminf(blo, f);
+            bhi = fmaxf(bhi, f);
+        }
+        blo = fminf(blo, __shfl_xor_sync(0xffffffffu, blo, 1));
+        bhi = fmaxf(bhi, __shfl_xor_sync(0xffffffffu, bhi, 1));
+        plain = is_normal(lo * blo) && is_normal(hi * bhi);
+    }
+    return __all_sync(0xffffffffu, plain);
+}
+
 // The scale warp: for every K block of the pair's tiles, this CTA's 128 row scales
 // of A and the tile's 256 (BROW) or 2 of B into the scale ring, by asynchronous
-// copies that signal the slot's barrier, so that a ring's worth is in flight.
-// Rows outside Out multiply zeros and are not stored; they take the last row's
-// scale.
+// copies.  A slot is handed on once its copies have landed, with the word that says
+// whether care is needed; the ring keeps the warp three slots ahead.  (One arrival: 32
+// of them, though off the critical path, made 397 us 447 at 8192 x 8192 x 8192.)
+// Rows outside Out multiply zeros and are not stored; they take the last row's scale.
 template <bool BROW>
-__device__ __forceinline__ void load_scales(const BlkParams& p, int rank, float* scales, uint64_t* sfull, uint64_t* sempty,
-                                            volatile int* abort_flag, int pair, int pairs)
+__device__ __forceinline__ void load_scales(const BlkParams& p, int rank, float* scales, uint32_t* careful, uint64_t* sfull,
+                                            uint64_t* sempty, volatile int* abort_flag, int pair, int pairs)
 {
-    const uint32_t ring = smem_u32(scales);
+    const uint32_t ring = smem_u32(scales), from = plain_from(p.e5m2);
+    const int blocks = blocks_of(p, pair, pairs);
     int n = 0;  // K blocks so far
     for (int t = pair; t < p.num_tiles; t += pairs) {
         int b, m0, n0;
@@ -200,24 +249,74 @@ __device__ __forceinline__ void load_scales(const BlkParams& p, int rank, float*
         ScaleRun<4> a(p.sa, b, m0 + rank * BM, p.M);
         ScaleRun<BROW ? 8 : 1> w(p.sb, b, n0, p.N, BROW ? 1 : 128);
 #pragma unroll 1
-        for (int kb = 0; kb < p.num_kb; ++kb, ++n) {
-            const int slot = n / kScaleGroup % kScaleRing;
-            if (n % kScaleGroup == 0 &&
+        for (int kb = 0; kb < p.num_kb; ++kb) {
+            const int slot = n / kScaleGroup % kScaleRing, at = n % kScaleGroup;
+            if (at == 0 &&
                 !wait_bounded(smem_u32(&sempty[slot]), (n / (kScaleGroup * kScaleRing) & 1) ^ 1, abort_flag, p.wait_limit)) {
                 raise(p, abort_flag);
                 cp_async_wait_all();
                 return;
             }
-            const uint32_t s = ring + n % (kScaleGroup * kScaleRing) * (kScaleFloats * 4);
+            const uint32_t first = ring + slot * kScaleGroup * (kScaleFloats * 4), s = first + at * (kScaleFloats * 4);
             a.copy(s);
             w.copy(s + 128 * 4);
-            if (n % kScaleGroup == kScaleGroup - 1)
-                cp_async_arrive(smem_u32(&sfull[slot]));
+            ++n;
+            if (at == kScaleGroup - 1 || n == blocks) {
+                cp_async_wait_all();
+                __syncwarp();  // every lane's copies are here
+                const bool plain = plain_group<BROW>(first, at, from);
+                if ((threadIdx.x & 31) == 0) {
+                    careful[slot] = !plain;
+                    mbar_arrive(smem_u32(&sfull[slot]));
+                }
+                __syncwarp();
+            }
         }
     }
-    if (n % kScaleGroup != 0)  // the last group, short
-        cp_async_arrive(smem_u32(&sfull[n / kScaleGroup % kScaleRing]));
-    cp_async_wait_all();
+}
+
+// Multiplies a warp's 32 rows x 128 columns of the accumulator at `ta` in place by
+// their rows' two factors, where those leave the normal range on the way.
+__device__ __forceinline__ void scale_accumulator(uint32_t ta, Factors f)
+{
+#pragma unroll 1
+    for (int c = 0; c < kCols; c += 16) {
+        uint32_t x[16];
+        tmem_ld(ta + c, x);
+        tmem_wait(x);
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+            x[j] = __float_as_uint(__uint_as_float(x[j]) * f.first * f.second);
+        tmem_st(ta + c, x);
+    }
+    tmem_st_wait();
+}
+
+// By row: one K block, a warp's 32 rows x 128 columns of the accumulator at `ta` times
+// the row's scale fa and the columns' at shared address `cols`, added to its sums; with
+// care where some scales may leave the normal range on the way and there is something
+// to scale (a block of zeros has tiny scales).  16 columns at a time: few registers
+// beside the sums.
+__device__ __forceinline__ void promote_careful(uint64_t (&acc)[kCols / 2], uint32_t ta, float fa, uint32_t cols, bool care)
+{
+    const uint64_t sr = pack2(fa, fa);
+#pragma unroll
+    for (int c = 0; c < kCols; c += 16) {
+        uint32_t x[16];
+        tmem_ld(ta + c, x);
+        tmem_wait(x);
+        uint64_t* d = acc + c / 2;
+        if (care && any_set(x)) {
+            add_careful(d, x, fa, cols + 4 * c);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const ulonglong2 w = lds_f32x4(cols + 4 * c + 16 * j);
+                d[2 * j] = fma2(mul2(pack2u(x[4 * j], x[4 * j + 1]), w.x), sr, d[2 * j]);
+                d[2 * j + 1] = fma2(mul2(pack2u(x[4 * j + 2], x[4 * j + 3]), w.y), sr, d[2 * j + 1]);
+            }
+        }
+    }
 }
 
 // BROW: a scale for each row of B (each column of the tile), else one for each
@@ -242,7 +341,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t* drain = sempty + kScaleRing;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 2);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-    static_assert((2 * kStages + 2 * kAcc + 2 * kScaleRing + 2) * 8 + 8 <= kBarBytes, "barrier area");
+    uint32_t* careful_slot = tmem_slot + 2;  // one word for each slot of the scale ring
+    static_assert((2 * kStages + 2 * kAcc + 2 * kScaleRing + 2) * 8 + 8 + 4 * kScaleRing <= kBarBytes, "barrier area");
 
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const uint32_t rank = cluster_ctarank();
@@ -259,7 +359,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(smem_u32(&tempty[b]), 2 * kPromoWarps);
         }
         for (int r = 0; r < kScaleRing; ++r) {
-            mbar_init(smem_u32(&sfull[r]), 32);
+            mbar_init(smem_u32(&sfull[r]), 1);
             mbar_init(smem_u32(&sempty[r]), kPromoWarps);
         }
         mbar_init(smem_u32(&drain[0]), 1);
@@ -371,7 +471,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 drain_wait(smem_u32(&drain[par]), 0, p.wait_limit);
             }
         } else if (warp == 2) {
-            load_scales<BROW>(p, static_cast<int>(rank), scales, sfull, sempty, abort_flag, pair, pairs);
+            load_scales<BROW>(p, static_cast<int>(rank), scales, careful_slot, sfull, sempty, abort_flag, pair, pairs);
         }
     } else {
         // ------------------------------------------------------------ promotion (both CTAs)
@@ -382,27 +482,42 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t tmem_warp = tmem_base + static_cast<uint32_t>(128 * cq) + (static_cast<uint32_t>(32 * q) << 16);
         const uint32_t my_scales = smem_u32(scales) + (32 * q + lane) * 4;
         const uint32_t col_scales = smem_u32(scales) + (128 + (BROW ? 128 * cq : cq)) * 4;
-        const uint32_t tf0 = smem_u32(tfull), sf0 = smem_u32(sfull);
+        const uint32_t tf0 = smem_u32(tfull), sf0 = smem_u32(sfull), careful0 = smem_u32(careful_slot);
         const uint32_t te0 = mapa_shared(smem_u32(tempty), 0);
         const int blocks = blocks_of(p, pair, pairs);
         int n = 0;  // K blocks so far: ring positions and phases follow from it
-        bool ok = true;
+        bool ok = true, careful = false;  // careful: of the group that block n is in
+        auto enter_group = [&](int at, bool& care) {
+            const int slot = at / kScaleGroup % kScaleRing;
+            const bool here = wait_bounded(sf0 + slot * 8, at / (kScaleGroup * kScaleRing) & 1, abort_flag, p.wait_limit);
+            care = lds_u32(careful0 + slot * 4) != 0;
+            return here;
+        };
         while (ok && n < blocks) {
             uint64_t acc[kCols / 2];
 #pragma unroll
             for (int j = 0; j < kCols / 2; ++j)
                 acc[j] = 0;
             int left = p.num_kb;
+            // Blocks in whose groups all scales are plain; by row, from the first other one
+            // on, the rest of the tile in a loop that can take care.  No way leads back to this loop inside a tile: a
+            // branch around its arithmetic keeps loads from going ahead (490 us for 397 at
+            // 8192 x 8192 x 8192), and so do two bodies in one loop (545).
 #pragma unroll 1
             do {
                 if (n % kScaleGroup == 0)
-                    ok &= wait_bounded(sf0 + n / kScaleGroup % kScaleRing * 8, n / (kScaleGroup * kScaleRing) & 1, abort_flag,
-                                       p.wait_limit);
+                    ok &= enter_group(n, careful);
+                if (BROW && careful)
+                    break;
                 const uint32_t so = n % (kScaleGroup * kScaleRing) * (kScaleFloats * 4);
-                const float fa = lds_f32(my_scales + so), fb = BROW ? 1.f : lds_f32(col_scales + so);
+                float fa = lds_f32(my_scales + so), fb = BROW ? 1.f : lds_f32(col_scales + so);
                 ok &= wait_bounded(tf0 + (n & 1) * 8, n >> 1 & 1, abort_flag, p.wait_limit);
                 tc_fence_after();
                 const uint32_t ta = tmem_warp + (n & 1) * kTile;
+                if (!BROW && careful) {
+                    scale_accumulator(ta, scale_factors(fa, fb));
+                    fa = fb = 1.f;
+                }
                 uint64_t sr = 0;
 #pragma unroll
                 for (int g = 0; g < kCols / kPiece; g += 2) {
@@ -427,14 +542,15 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                         for (int j = 0; j < kPiece / 4; ++j) {
                             uint64_t p0 = pack2u(z[4 * j], z[4 * j + 1]), p1 = pack2u(z[4 * j + 2], z[4 * j + 3]);
+                            uint64_t* d = acc + kPiece / 2 * (g + c) + 2 * j;
                             if (BROW) {
                                 const ulonglong2 w = lds_f32x4(col_scales + so + (kPiece * (g + c) + 4 * j) * 4);
-                                p0 = mul2(p0, w.x);
-                                p1 = mul2(p1, w.y);
+                                d[0] = fma2(mul2(p0, w.x), sr, d[0]);
+                                d[1] = fma2(mul2(p1, w.y), sr, d[1]);
+                            } else {
+                                d[0] = fma2(p0, sr, d[0]);
+                                d[1] = fma2(p1, sr, d[1]);
                             }
-                            uint64_t* d = acc + kPiece / 2 * (g + c) + 2 * j;
-                            d[0] = fma2(p0, sr, d[0]);
-                            d[1] = fma2(p1, sr, d[1]);
                         }
                     }
                 }
@@ -444,6 +560,24 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 ++n;
             } while (--left > 0 && ok);
+            if (BROW && left > 0 && ok) {
+#pragma unroll 1
+                do {
+                    const uint32_t so = n % (kScaleGroup * kScaleRing) * (kScaleFloats * 4);
+                    ok &= wait_bounded(tf0 + (n & 1) * 8, n >> 1 & 1, abort_flag, p.wait_limit);
+                    tc_fence_after();
+                    promote_careful(acc, tmem_warp + (n & 1) * kTile, lds_f32(my_scales + so), col_scales + so, careful);
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive_cluster(te0 + (n & 1) * 8);
+                    if (n % kScaleGroup == kScaleGroup - 1)
+                        mbar_arrive_if(smem_u32(&sempty[n / kScaleGroup % kScaleRing]), lane == 0);
+                    ++n;
+                    if (--left > 0 && n % kScaleGroup == 0)
+                        ok &= enter_group(n, careful);
+                } while (left > 0 && ok);
+            }
             if (!ok) {
                 raise(p, abort_flag);
                 break;

@@ -60,6 +60,16 @@ __device__ __forceinline__ void tmem_wait(uint32_t (&r)[16])
         :
         : "memory");
 }
+// The way back, to be waited for by tmem_st_wait.
+__device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t (&r)[16])
+{
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};"
+        :
+        : "r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+          "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[32])
 {
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
@@ -86,6 +96,12 @@ __device__ __forceinline__ float lds_f32(uint32_t a)
 {
     float v;
     asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint32_t lds_u32(uint32_t a)
+{
+    uint32_t v;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
     return v;
 }
 __device__ __forceinline__ ulonglong2 lds_f32x4(uint32_t a)
@@ -250,6 +266,46 @@ struct ScaleRun {
         }
     }
 };
+
+// Twice how far the largest of four scales' magnitudes lies above `from`, as a word
+// (doubling drops the signs; a smaller one wraps to the top): plain_scale but for zero,
+// infinity and NaN, which may as well be treated with care.
+__device__ __forceinline__ uint32_t beyond(ulonglong2 w, uint32_t from)
+{
+    const uint32_t a = 2u * static_cast<uint32_t>(w.x) - 2u * from, b = 2u * static_cast<uint32_t>(w.x >> 32) - 2u * from;
+    const uint32_t c = 2u * static_cast<uint32_t>(w.y) - 2u * from, d = 2u * static_cast<uint32_t>(w.y >> 32) - 2u * from;
+    return max(max(a, b), max(c, d));
+}
+
+// Whether any of the warp's values is not zero.
+template <int N>
+__device__ __forceinline__ bool any_set(const uint32_t (&x)[N])
+{
+    uint32_t u = 0;
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+        u |= x[j];
+    return __any_sync(0xffffffffu, u != 0);
+}
+
+// acc += x times the thread's scale and the columns' (at shared address `w`), where
+// the thread's leaves the range that needs no care.  Blocks of zeros, whose scales
+// are tiny, do not come here: their products are zero in any order.
+template <int N>
+__device__ __forceinline__ void add_careful(uint64_t* acc, const uint32_t (&x)[N], float s, uint32_t w)
+{
+#pragma unroll
+    for (int j = 0; j < N; j += 2) {
+        float a[2];
+        unpack2(acc[j / 2], a[0], a[1]);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const Factors f = scale_factors(s, lds_f32(w + 4 * (j + e)));
+            a[e] = fmaf(__uint_as_float(x[j + e]) * f.first, f.second, a[e]);
+        }
+        acc[j / 2] = pack2(a[0], a[1]);
+    }
+}
 
 // Waits (with the limit) without giving up early: for drains before exit.
 __device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity, unsigned long long limit)

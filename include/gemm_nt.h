@@ -313,7 +313,10 @@ typedef struct gemm_scale128 {
  * it.  The inner sums are exact products accumulated in fp32 by the tensor
  * cores; they are scaled and summed over c in fp32 registers.  Out is fp32, or
  * that sum rounded once to nearest even into fp16 or bf16.  sa and sb may hold
- * any fp32 values; infinities and NaN follow IEEE arithmetic.
+ * any fp32 values: a block's term is right wherever it lies in fp32's normal range,
+ * whatever sa * sb, or the inner sum times one of them, would be on the way (scales
+ * below 2^-94, E4M3 2^-109, or above 2^80 cost time).  Infinities and NaN follow IEEE
+ * arithmetic.
  *
  * path: GEMM_PATH_AUTO, GEMM_PATH_TC05_PAIR (256 x 256 tiles on CTA pairs),
  * GEMM_PATH_SKINNY (128 rows of B by up to 128 rows of A per CTA, K split over
