@@ -299,7 +299,9 @@ gemm_status_t gemm_nt_moe(const void* X, int64_t ldx, const float* logits, int64
             return GEMM_ERR_SCRATCH_TOO_SMALL;
         const Span ws = span_of(workspace, 1, 1, 0, workspace_bytes, 1);
         if (overlap(ws, out) || overlap(ws, span_of(X, 2, tokens, ldx, hidden, 1)) || overlap(ws, w13) || overlap(ws, w2) ||
-            overlap(ws, span_of(logits, 4, tokens, ldl, experts, 1)))
+            overlap(ws, span_of(logits, 4, tokens, ldl, experts, 1)) ||
+            (w8 && (overlap(ws, scale_span(*S13, 2 * inner, hidden, experts)) ||
+                    overlap(ws, scale_span(*S2, hidden, inner, experts)))))
             return GEMM_ERR_OVERLAP;
     }
     DeviceInfo d;

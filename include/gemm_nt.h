@@ -389,7 +389,8 @@ gemm_status_t gemm_nt_block128_quantize(const void *X, gemm_dtype_t x_type, int6
  * tokens <= 128, experts <= 1024, topk <= min(32, experts): more is
  * GEMM_ERR_NOT_SUPPORTED.  `workspace` (device memory, 16-byte aligned, the
  * caller's, at least gemm_nt_moe_workspace_bytes(tokens, topk, inner) bytes) is
- * overwritten; less is GEMM_ERR_SCRATCH_TOO_SMALL.  Any pitch and alignment is
+ * overwritten; less is GEMM_ERR_SCRATCH_TOO_SMALL.  Out or the workspace overlapping
+ * an operand, its scales or each other: GEMM_ERR_OVERLAP.  Any pitch and alignment is
  * accepted; rows that start on 16-byte boundaries are read fastest.  tokens or
  * hidden 0: nothing to do; inner 0: Out is zero.
  */
