@@ -386,13 +386,15 @@ gemm_status_t gemm_nt_block128_quantize(const void *X, gemm_dtype_t x_type, int6
  * that hold at least 16 significant bits of it; Out is rounded once to x_type.
  * Sums over experts follow the expert index, so results do not depend on the run.
  *
- * tokens <= 128, experts <= 1024, topk <= min(32, experts): more is
- * GEMM_ERR_NOT_SUPPORTED.  `workspace` (device memory, 16-byte aligned, the
+ * topk below 1 or above experts: GEMM_ERR_INVALID_VALUE.  tokens <= 128, experts <=
+ * 1024, topk <= 32, hidden and inner <= 2^20: more is GEMM_ERR_NOT_SUPPORTED.
+ * `workspace` (device memory, 16-byte aligned, the
  * caller's, at least gemm_nt_moe_workspace_bytes(tokens, topk, inner) bytes) is
  * overwritten; less is GEMM_ERR_SCRATCH_TOO_SMALL.  Out or the workspace overlapping
  * an operand, its scales or each other: GEMM_ERR_OVERLAP.  Any pitch and alignment is
  * accepted; rows that start on 16-byte boundaries are read fastest.  tokens or
- * hidden 0: nothing to do; inner 0: Out is zero.
+ * hidden 0: nothing to do.  inner 0: Out is zero whatever the logits, weights and
+ * workspace are not looked at and any number of tokens will do.
  */
 gemm_status_t gemm_nt_moe(const void *X, int64_t ldx, const float *logits, int64_t ldl,
                           const void *W13, int64_t ldw13, int64_t strideW13, const gemm_scale128_t *S13,

@@ -16,3 +16,18 @@ def test_workspace_over_the_scales(lib, ws):  # noqa: F811
     need = gnt.gemm_nt_moe_workspace_bytes(4, 2, 128)
     assert moe(lib, wt=D.E4M3, s13=S13, s2=S2, ws=ws - need + 16, nbytes=need) == Status.OVERLAP
     assert moe(lib, wt=D.E4M3, s13=S13, s2=S2, ws=ws - need, nbytes=need) != Status.OVERLAP
+
+
+@pytest.mark.parametrize("change,status", [
+    (dict(k=17), Status.INVALID_VALUE),
+    (dict(H=2 ** 20 + 1, ldx=2 ** 20 + 1, ldo=2 ** 20 + 1, ldw13=2 ** 20 + 1, sw13=0), Status.NOT_SUPPORTED),
+    (dict(I=2 ** 20 + 1, ldw2=2 ** 20 + 1, sw2=0, w13=1 << 40, w2=1 << 44), Status.NOT_SUPPORTED),
+])
+def test_documented_limits(lib, change, status):  # noqa: F811
+    assert moe(lib, x=1 << 50, l=1 << 51, out=1 << 52, ws=1 << 53, nbytes=1 << 40, **change) == status
+
+
+def test_without_inner_columns_no_limit_applies(lib):  # noqa: F811
+    """Good arguments fail for want of a device only."""
+    never = (Status.OK, Status.INVALID_VALUE, Status.OVERLAP, Status.NOT_SUPPORTED)
+    assert moe(lib, I=0, w13=0, w2=0, ws=0, nbytes=0, T=500, E=2000, ldl=2000, k=40, x=1 << 50, out=1 << 52) not in never
