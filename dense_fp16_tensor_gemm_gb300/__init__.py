@@ -687,7 +687,8 @@ def moe_few_tokens(X, logits, W13, W2, topk, S13=None, S2=None, renormalize=True
     elif tuple(out.shape) != (tokens, hidden) or out.dtype != X.dtype:
         raise ValueError("out must have X's shape and type")
     if workspace is None:
-        need = gemm_nt_moe_workspace_bytes(tokens, topk, inner) if topk > 0 else 0
+        # (what the library is going to refuse needs none)
+        need = gemm_nt_moe_workspace_bytes(tokens, topk, inner) if 0 < topk <= experts and tokens <= 128 else 0
         workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=device)
     elif not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous")

@@ -249,9 +249,11 @@ gemm_status_t gemm_nt_block128_quantize(const void* X, gemm_dtype_t x_type, int6
 
 int64_t gemm_nt_moe_workspace_bytes(int64_t tokens, int64_t topk, int64_t inner)
 {
-    if (tokens < 0 || topk < 0 || inner < 0)
+    int64_t bytes;
+    if (tokens < 0 || topk < 0 || inner < 0 || inner > INT64_MAX - 15 || __builtin_mul_overflow(tokens, topk, &bytes) ||
+        __builtin_mul_overflow(bytes, moe_ldh(inner), &bytes) || __builtin_mul_overflow(bytes, int64_t(4), &bytes))
         return -1;
-    return tokens * topk * moe_ldh(inner) * 4;
+    return bytes;
 }
 
 gemm_status_t gemm_nt_moe(const void* X, int64_t ldx, const float* logits, int64_t ldl, const void* W13, int64_t ldw13,

@@ -403,7 +403,8 @@ gemm_status_t gemm_nt_moe(const void *X, int64_t ldx, const float *logits, int64
                           int64_t tokens, int64_t experts, int64_t topk, int64_t hidden, int64_t inner,
                           int renormalize, void *workspace, int64_t workspace_bytes, gemm_stream_t stream);
 
-/* Bytes of workspace gemm_nt_moe needs (-1 for negative arguments). */
+/* Bytes of workspace gemm_nt_moe needs (-1 for negative arguments, and where the number
+ * would not fit). */
 int64_t gemm_nt_moe_workspace_bytes(int64_t tokens, int64_t topk, int64_t inner);
 
 /*

@@ -31,3 +31,24 @@ def test_without_inner_columns_no_limit_applies(lib):  # noqa: F811
     """Good arguments fail for want of a device only."""
     never = (Status.OK, Status.INVALID_VALUE, Status.OVERLAP, Status.NOT_SUPPORTED)
     assert moe(lib, I=0, w13=0, w2=0, ws=0, nbytes=0, T=500, E=2000, ldl=2000, k=40, x=1 << 50, out=1 << 52) not in never
+
+
+def test_workspace_bytes_that_do_not_fit():
+    """The number of bytes, or -1: never one that wrapped around."""
+    f = gnt.gemm_nt_moe_workspace_bytes
+    assert f(128, 32, 2 ** 20) == 128 * 32 * 2 ** 20 * 4
+    assert f(2 ** 31, 2 ** 31, 1) == -1 and f(2 ** 30, 2 ** 30, 2 ** 30) == -1
+    assert f(1, 1, 2 ** 63 - 1) == -1 and f(2 ** 62, 1, 1) == -1
+    assert f(2 ** 27, 2 ** 27, 1) == 2 ** 60 and f(0, 2 ** 62, 2 ** 62) == 0
+
+
+@pytest.mark.gpu
+def test_nothing_is_allocated_for_what_is_refused():
+    """A workspace for a billion experts a token is not asked of the allocator."""
+    torch = pytest.importorskip("torch")
+    x, logits = torch.zeros(2, 64, dtype=torch.bfloat16, device="cuda"), torch.zeros(2, 4, device="cuda")
+    w13, w2 = (torch.zeros(*s, dtype=torch.bfloat16, device="cuda") for s in ((4, 32, 64), (4, 64, 16)))
+    for topk, status in ((10 ** 9, Status.INVALID_VALUE), (2 ** 62, Status.INVALID_VALUE), (0, Status.INVALID_VALUE)):
+        with pytest.raises(gnt.GemmError) as e:
+            gnt.moe_few_tokens(x, logits, w13, w2, topk)
+        assert e.value.status == status
