@@ -615,8 +615,11 @@ __device__ __forceinline__ void store_h(float* row, int i0, int j, float gate, f
 {
     const float h = gate / (1.f + expf(-gate)) * up;
     if constexpr (SPLIT) {
-        const __nv_bfloat16 head = __float2bfloat16_rn(h);
-        const float rest = fabsf(h) < INFINITY ? h - __bfloat162float(head) : 0.f;
+        // the nearest bf16 value to a finite h may be an infinity: the largest one then
+        const bool finite = fabsf(h) < INFINITY;
+        constexpr float kMax = 3.3895313892515355e38f;
+        const __nv_bfloat16 head = __float2bfloat16_rn(finite ? fminf(fmaxf(h, -kMax), kMax) : h);
+        const float rest = finite ? h - __bfloat162float(head) : 0.f;
         __nv_bfloat16* o = reinterpret_cast<__nv_bfloat16*>(row + i0) + j;
         o[0] = head;
         o[8] = __float2bfloat16_rn(rest);
