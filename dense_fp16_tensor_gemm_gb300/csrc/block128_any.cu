@@ -33,7 +33,7 @@ __device__ __forceinline__ void stage_block(uint16_t* dst, const uint8_t* src, i
             uint32_t w[4] = {0, 0, 0, 0};
             if (row0 + r < nrows && k0 + c < K) {
                 const uint8_t* g = src + static_cast<int64_t>(row0 + r) * ld + k0 + c;
-                if (k0 + c + 16 <= K) {
+                if (K - (k0 + c) >= 16) {
                     const uint4 v = __ldg(reinterpret_cast<const uint4*>(g));
                     w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
                 } else {
@@ -164,8 +164,8 @@ bool rows_on_16(const void* base, int64_t ld, int64_t stride, int batch)
 cudaError_t block128_any_launch(const BlkParams& prm, cudaStream_t stream)
 {
     BlkParams p = prm;
-    p.tiles_m = (p.M + kT - 1) / kT;
-    p.tiles_n = (p.N + kT - 1) / kT;
+    p.tiles_m = (p.M - 1) / kT + 1;
+    p.tiles_n = (p.N - 1) / kT + 1;
     const int64_t tiles = static_cast<int64_t>(p.tiles_m) * p.tiles_n * p.batch;
     const int grid = static_cast<int>(tiles < (1 << 20) ? tiles : (1 << 20));
     const int va = rows_on_16(p.A, p.lda, p.stride_a, p.batch), vb = rows_on_16(p.B, p.ldb, p.stride_b, p.batch);

@@ -655,8 +655,8 @@ cudaError_t block128_pair_launch(const BlkParams& prm, int max_pairs, cudaStream
     if (!operand_map(&tma, p.A, p.M, p.K, p.lda, p.batch, p.stride_a, BM, &p.a_bmul, type) ||
         !operand_map(&tmb, p.B, p.N, p.K, p.ldb, p.batch, p.stride_b, BM, &p.b_bmul, type))
         return cudaErrorInvalidValue;
-    p.tiles_m = (p.M + kTile - 1) / kTile;
-    p.tiles_n = (p.N + kTile - 1) / kTile;
+    p.tiles_m = (p.M - 1) / kTile + 1;
+    p.tiles_n = (p.N - 1) / kTile + 1;
     p.num_tiles = p.tiles_m * p.tiles_n * p.batch;
     p.group_m = 8;
     cudaLaunchAttribute attr[2];

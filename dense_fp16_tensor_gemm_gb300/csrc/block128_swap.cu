@@ -79,7 +79,7 @@ __device__ __forceinline__ void decode(const BlkParams& p, int t, int bn, int& b
     t -= b * per;
     y0 = t / p.tiles_n * bn;
     x0 = t % p.tiles_n * BM;
-    xend = min(x0 + BM, p.N);
+    xend = x0 + min(BM, p.N - x0);
 }
 
 template <int BN>
@@ -399,8 +399,8 @@ cudaError_t launch(BlkParams p, int num_sms, cudaStream_t stream)
     if (!operand_map(&tmx, p.B, p.N, p.K, p.ldb, p.batch, p.stride_b, p.x_box, &p.b_bmul, type) ||
         !operand_map(&tmy, p.A, p.M, p.K, p.lda, p.batch, p.stride_a, BN, &p.a_bmul, type))
         return cudaErrorInvalidValue;
-    p.tiles_m = (p.M + BN - 1) / BN;
-    p.tiles_n = (p.N + BM - 1) / BM;
+    p.tiles_m = (p.M - 1) / BN + 1;
+    p.tiles_n = (p.N - 1) / BM + 1;
     p.num_tiles = p.row_share ? num_sms : p.tiles_m * p.tiles_n * p.batch;
     // split K while whole clusters still fit the GPU and a CTA keeps 4 K blocks
     int c = 1;

@@ -223,7 +223,7 @@ struct ScaleRun {
         const int lane = threadIdx.x & 31;
         const float* base = v.data + b * v.bs;
         step = v.ks;
-        wide = R % 4 == 0 && every == 1 && v.shift == 0 && v.rs == 1 && v.ks % 4 == 0 && first + 32 * R <= rows &&
+        wide = R % 4 == 0 && every == 1 && v.shift == 0 && v.rs == 1 && v.ks % 4 == 0 && rows - first >= 32 * R &&
                (reinterpret_cast<uintptr_t>(base + first) & 15) == 0;
         off = static_cast<uint32_t>(wide ? 16 * lane : 4 * lane);
         if (wide) {
