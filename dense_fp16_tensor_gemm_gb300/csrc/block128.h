@@ -72,7 +72,7 @@ struct BlkParams {
     int tiles_m, tiles_n, num_tiles, group_m;
     int a_bmul, b_bmul;       // 1 if the tensor map has a batch dimension
     int row_share, x_box;     // swapped kernel: an even share of B's rows per CTA; rows of a B box
-    int vec;                  // elements per store that Out's base, pitch and batch stride allow: 8, 4, 2 or 1
+    int vec;                  // elements per store that Out's base, pitch and batch stride allow: 8, 4 or 1
     uint32_t idesc_bits;
     uint32_t* status;
     unsigned long long wait_limit;

@@ -162,11 +162,11 @@ gemm_status_t gemm_nt_block128(const void* A, const gemm_scale128_t* SA, const v
         return GEMM_ERR_NOT_SUPPORTED;
     if (K == 0)  // nothing to multiply: zeros, which the warp kernel stores in any layout
         return status_of(block128_any_launch(p, s));
-    // what Out's rows allow: 16-byte stores of 8 elements, or pairs
+    // what Out's rows allow: stores of 8 or 4 elements, or of single ones
     const auto rows_on = [&](int64_t n) {
         return aligned(Out, static_cast<uintptr_t>(n * osize)) && ldo % n == 0 && (batch == 1 || strideO % n == 0);
     };
-    p.vec = rows_on(8) ? 8 : (rows_on(2) ? 2 : 1);
+    p.vec = rows_on(8) ? 8 : (rows_on(4) ? 4 : 1);
     p.idesc_bits = p.e5m2 ? (1u << 7) | (1u << 10) : 0;
     if (path == GEMM_PATH_TC05_PAIR)
         return status_of(block128_pair_launch(p, d.block_pairs, s));
