@@ -37,7 +37,6 @@
 // Routing is recomputed by every CTA from the logits, a few thousand
 // instructions; that spares a kernel and a round trip through memory.
 #include <algorithm>
-#include <climits>
 
 #include "gemm_nt.h"
 #include "block128.h"
@@ -821,27 +820,29 @@ struct DownCfg {
     static constexpr int RING = kWarps * D * S::BYTES;
     static __host__ __device__ constexpr int sum_bytes(int tokens)
     {
-        return (TURNS ? 1 : kWarps) * tokens * 16 * MT * 4 + 16;  // 16: whose turn it is
+        return (TURNS ? 1 : kWarps) * tokens * 16 * MT * 4 + 16;  // 16: whose turn it is, and whether one gave up
     }
 };
 
-// Waits until *turn is at least `unit`; false after `limit` cycles, or once another
-// warp has given up.
+// Waits until the word at `turn` is at least `unit`; false after `limit` cycles, or
+// once another warp has given up, which the word behind it says and keeps saying.
+__device__ __forceinline__ int turn_word(uint32_t a)
+{
+    int v;
+    asm volatile("ld.acquire.cta.shared::cta.s32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ void set_turn_word(uint32_t a, int v)
+{
+    asm volatile("st.release.cta.shared::cta.s32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
+}
 __device__ __forceinline__ bool wait_turn(uint32_t turn, int unit, unsigned long long limit)
 {
     const long long t0 = clock64();
-    for (;;) {
-        int now;
-        asm volatile("ld.acquire.cta.shared::cta.s32 %0, [%1];" : "=r"(now) : "r"(turn) : "memory");
-        if (__all_sync(0xffffffffu, now >= unit))
-            return now != INT_MAX;
-        if (__any_sync(0xffffffffu, static_cast<unsigned long long>(clock64() - t0) > limit))
+    while (!__all_sync(0xffffffffu, turn_word(turn) >= unit))
+        if (__any_sync(0xffffffffu, turn_word(turn + 4) != 0 || static_cast<unsigned long long>(clock64() - t0) > limit))
             return false;
-    }
-}
-__device__ __forceinline__ void pass_turn(uint32_t turn, int unit)
-{
-    asm volatile("st.release.cta.shared::cta.s32 [%0], %1;" ::"r"(turn), "r"(unit) : "memory");
+    return true;
 }
 
 template <bool BF16, bool W8, int NT, int MT>
@@ -862,8 +863,10 @@ __global__ void __launch_bounds__(kThreads, DownCfg<W8, NT, MT>::CTAS) moe_down_
     const int nout = p.tokens * ROWS;
     for (int i = threadIdx.x; i < (TURNS ? 1 : kWarps) * nout; i += kThreads)
         sums[i] = 0.f;
-    if (TURNS && threadIdx.x == 0)
-        pass_turn(turn, 0);
+    if (TURNS && threadIdx.x == 0) {
+        set_turn_word(turn, 0);
+        set_turn_word(turn + 4, 0);
+    }
     route_all(p, r, 8 * NT);  // the logits were complete before the up kernel let this one start
     pdl_wait();       // h
 
@@ -956,7 +959,6 @@ __global__ void __launch_bounds__(kThreads, DownCfg<W8, NT, MT>::CTAS) moe_down_
 
     float* mine = sums + (TURNS ? 0 : warp * nout);
     int slot = 0;
-    bool in_turn = true;
 #pragma unroll 1
     for (int q = q0; q < q1;) {
         int a, k0, k1;
@@ -987,10 +989,12 @@ __global__ void __launch_bounds__(kThreads, DownCfg<W8, NT, MT>::CTAS) moe_down_
             add_item<W8, MT, NT>(c, part, s);
             slot = slot + 1 == D ? 0 : slot + 1;
         }
-        if (TURNS && in_turn && !wait_turn(turn, q - u0, p.wait_limit)) {
-            in_turn = false;
-            atomicOr(p.status, kStatusTimeout);
-            pass_turn(turn, INT_MAX);
+        if (TURNS && !wait_turn(turn, q - u0, p.wait_limit)) {  // nothing is added out of turn
+            if (lane == 0) {
+                set_turn_word(turn + 4, 1);
+                atomicOr(p.status, kStatusTimeout);
+            }
+            break;
         }
 #pragma unroll
         for (int w = 0; w < NT; ++w)
@@ -1009,8 +1013,8 @@ __global__ void __launch_bounds__(kThreads, DownCfg<W8, NT, MT>::CTAS) moe_down_
                 }
             }
         __syncwarp();
-        if (TURNS && in_turn && lane == 0)
-            pass_turn(turn, q - u0 + 1);
+        if (TURNS && lane == 0)
+            set_turn_word(turn, q - u0 + 1);
         q += TURNS ? kWarps : k1 - k0;
     }
     cp_async_wait<0>();
