@@ -263,8 +263,12 @@ def gemm_nt(A, B, out=None, path=Path.AUTO, stream=None, out_dtype=None):
     Row strides may exceed the row length; the last dimension must be
     contiguous.  ``out`` (M,N) is allocated if not given, as ``out_dtype``
     (default float32; float16 or bfloat16 round to nearest even).  Runs on
-    ``stream`` (default: torch's current stream).
+    ``stream`` (default: torch's current stream) as under ``torch.cuda.stream``,
+    allocations included.
     """
+    side = _elsewhere(stream)
+    if side is not None:
+        return _run_on(side, gemm_nt, A, B, out, path, None, out_dtype, given=out)
     import torch
     if A.dim() != 2 or B.dim() != 2 or A.shape[1] != B.shape[1]:
         raise ValueError("shapes: A (M,K), B (N,K)")
@@ -285,6 +289,9 @@ def pack_mx_scales(S, K, stream=None):
     """Plain block scales -> the packed atom layout, on the device: S a uint8
     CUDA tensor (rows, ceil(K/32)) or (batch, rows, ceil(K/32)) of E8M0
     bytes, last dimension contiguous.  Returns a new uint8 tensor."""
+    side = _elsewhere(stream)
+    if side is not None:
+        return _run_on(side, pack_mx_scales, S, K)
     import torch
     if S.dtype != torch.uint8 or S.dim() not in (2, 3) or S.stride(-1) != 1:
         raise ValueError("S: uint8 (rows, ceil(K/32)) or (batch, rows, ceil(K/32)), last dimension contiguous")
@@ -304,6 +311,9 @@ def gemm_nt_mx_tensors(A, SA, B, SB, out=None, path=Path.AUTO, stream=None, out_
     and SB (N, ceil(K/32)) uint8 E8M0 scales (2^(e-127)), one per 32
     consecutive K elements of a row, in the plain layout (packed here).
     ``out``/``out_dtype`` as in :func:`gemm_nt`."""
+    side = _elsewhere(stream)
+    if side is not None:
+        return _run_on(side, gemm_nt_mx_tensors, A, SA, B, SB, out, path, None, out_dtype, given=out)
     import torch
     if A.dim() != 2 or B.dim() != 2 or A.shape[1] != B.shape[1]:
         raise ValueError("shapes: A (M,K), B (N,K)")
@@ -333,6 +343,9 @@ def gemm_nt_packed(A, B, K, ab_dtype, SA=None, SB=None, out=None, path=Path.AUTO
     multiple of 128, rows start on 32-byte boundaries.  With SA (M, K/32) and
     SB (N, K/32) uint8 E8M0 scales (plain layout) the product is block-scaled
     as in :func:`gemm_nt_mx_tensors`.  ``out``/``out_dtype`` as in :func:`gemm_nt`."""
+    side = _elsewhere(stream)
+    if side is not None:
+        return _run_on(side, gemm_nt_packed, A, B, K, ab_dtype, SA, SB, out, path, None, out_dtype, given=out)
     import torch
     ab = DType(ab_dtype)
     if ab not in PACKED_BITS:
@@ -372,6 +385,9 @@ def gemm_nt_batched(A, B, out=None, path=Path.AUTO, stream=None, out_dtype=None)
     """Out[b] = A[b] @ B[b].T for torch CUDA tensors A (batch,M,K), B (batch,N,K),
     both fp16 or both bf16 (a batch stride of 0, e.g. from ``expand``, shares
     the operand); ``out``/``out_dtype`` as in :func:`gemm_nt`."""
+    side = _elsewhere(stream)
+    if side is not None:
+        return _run_on(side, gemm_nt_batched, A, B, out, path, None, out_dtype, given=out)
     import torch
     if A.dim() != 3 or B.dim() != 3 or A.shape[0] != B.shape[0] or A.shape[2] != B.shape[2]:
         raise ValueError("shapes: A (batch,M,K), B (batch,N,K)")
