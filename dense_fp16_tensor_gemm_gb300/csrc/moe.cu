@@ -576,16 +576,24 @@ __device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; 
 // ---------------------------------------------------------------- up
 // A unit is 8*MT gate rows and the 8*MT up rows that go with them (MT m16 tiles:
 // an accumulator's lower rows are the gates, its upper ones their ups), over all
-// of K, for up to 8*NT of the expert's tokens; an expert with more has as many
-// entries among the active ones, so that CTAs and warps share out work, not experts
-// (one of 64 with 17 tokens made 143 us 182, now 149; 128 tokens 226, 381 before).
-// CTAs take even ranges of the units of all entries.  KS warps share a unit and split its K: one,
-// where there are many units for every SM (a warp then ends a unit in its own
-// registers; 8 warps meeting after every 4 items of K took half of 64 tokens'
-// time); two, where a warp each would leave warps without one (one token on 8 of 64
-// experts of 2048 x 1024, 6.7 units an SM: 27.1 us against 27.7 in bf16, 25.2
-// against 27.3 in E4M3; 16 tokens on 8 of 4096 x 8192, 54 units: 285 against 277);
-// or all 8, where there are few and a unit's latency counts.
+// of K, for up to 8*NT of the expert's tokens.  An expert with more tokens has as many
+// entries among the active ones, so that CTAs and warps share out work, not experts:
+// 64 tokens of which 17 meet on one of 64 experts in E4M3 149 us, 182 with whole
+// experts; 128 tokens 226 and 381.  CTAs take even ranges of the units of all entries.
+//
+// KS warps share a unit and split its K: one, where there are many units for every SM
+// (a warp then ends a unit in its own registers; 8 warps meeting after every 4 items
+// of K took half of 64 tokens' time); two, where a warp each would leave warps
+// without one; all 8, where there are few and a unit's latency counts.  One token on
+// 8 of 64 experts of 2048 x I, layer in us:
+//   units an SM   2     3     4     5     6.7   10    13    16    21
+//   bf16   8     16.3  20.8  22.1  24.9  28.5
+//          2     21.7  23.8  21.9  24.4  28.3  38.9  45.1  50.6  64.9
+//          1                 25.6        30.0  41.7  45.6  50.5  65.0
+//   E4M3   8     15.9  19.4  21.2  23.4  25.5
+//          2     21.9  22.2  21.2  23.4  25.6  34.9  40.3  43.5  55.1
+//          1                 24.2        27.9  34.5  38.8  41.5  55.9
+// hence 8 below 4, 2 up to 16 (E4M3: 8), then 1.
 template <bool W8, int MT, int NT, int KS>
 struct UpCfg {
     using S = Stage<W8, MT, NT, 2>;
@@ -1097,7 +1105,7 @@ cudaError_t launch_one(const MoeParams& p, int num_sms, cudaStream_t stream)
     // Units of 8*NT columns for a warp alone, two warps or all eight of a CTA (above).
     const int64_t units = reach * ((p.inner + 8 * NT - 1) / (8 * NT));
     cudaError_t e;
-    if (NT == 1 && units >= 4 * num_sms && units < 16 * num_sms)
+    if (NT == 1 && units >= 4 * num_sms && units < (W8 ? 8 : 16) * num_sms)
         e = launch_up<BF16, W8, 1, 1, 2>(p, reach, num_sms, stream);
     else
         e = units >= 4 * num_sms ? launch_up<BF16, W8, NT, NT, 1>(p, reach, num_sms, stream)
