@@ -7,7 +7,7 @@
 // x 32; a K block of 128 is staged as fp16 (every E4M3 and E5M2 value is an fp16
 // value), eight m16n8k16 steps give its fp32 partial sums, and the tile's
 // accumulators take them times the two scales.  Bound by the warp MMA and by the
-// staging between barriers (8192 x 8192 x 8192: 9.3 ms, 118 TFLOP/s).  Rows are padded to 272 bytes
+// staging between barriers (8192 x 8192 x 8192: 10.1 ms, 109 TFLOP/s).  Rows are padded to 272 bytes
 // (17 x 16), so the 8 rows an ldmatrix reads fall on different banks.
 #include <cuda_fp8.h>
 

@@ -81,8 +81,8 @@ gemm_path_t select(const BlkParams& p, const DeviceInfo& d, int64_t pair_tiles)
         return GEMM_PATH_MMASYNC;
     // Pairs once their tiles occupy a third of them, half where B has a scale for
     // every row (the pairs' arithmetic is then twice as long).  Measured, pairs
-    // against single CTAs: 512 x 4096 x 4096 (32 tiles) 17.6 and 19.1 us, by row 24.3
-    // and 18.4; 1024 x 4096 x 4096 (64 tiles) 18.4 and 34.8, by row 24.8 and 33.5.
+    // against single CTAs: 512 x 4096 x 4096 (32 tiles) 18.9 and 20.7 us, by row 25.9
+    // and 20.3; 1024 x 4096 x 4096 (64 tiles) 20.0 and 37.4, by row 26.7 and 36.6.
     const int part = p.sb.shift ? 3 : 2;
     return p.M > 128 && d.block_pairs > 0 && part * pair_tiles >= d.block_pairs ? GEMM_PATH_TC05_PAIR : GEMM_PATH_SKINNY;
 }

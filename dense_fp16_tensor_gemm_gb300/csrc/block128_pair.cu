@@ -14,13 +14,15 @@
 // every row).  Two accumulators of 256 columns fill Tensor Memory; what bounds
 // the kernel is the round trip of one: MMA, commit to both CTAs, loads and
 // arithmetic, release to the leader.  Measured per block (4864 x 4096, K from
-// 2048 to 8192): 410 ns, 620 where B has a scale for every row; 310 with the
+// 2048 to 8192): 430 ns, 645 where B has a scale for every row; before the scales were
+// looked at (below) 410 and 620, and against those 310 with the
 // arithmetic left out, 345 with the loads left out.  Halves of 128 columns, which
 // shorten the trip, are slower (A is read twice and shared memory fills up), as
 // are 16 warps with 64 sums each (490 and 670), scalar arithmetic (452) and loads of
 // 16 rows x 64 columns, which let a column's scale serve two rows (510 and 655).  A tile's
 // epilogue adds 1.5 us (16-bit Out) to 3 us (fp32): its registers are the sums.
-// 8192 x 8192 x 8192 into bf16: 428-446 us (2470-2570 TFLOP/s).
+// 8192 x 8192 x 8192 into bf16: 440-452 us among other calls, 407-414 from a graph
+// (2430-2700 TFLOP/s).
 //
 // Roles per CTA (384 threads): warp 0 TMA producer; warps 1 and 3 in the leader
 // MMA issue; warp 2 brings the scales into a ring of their own (any strides);

@@ -17,8 +17,8 @@
 // row's goes first; where it is tiny or huge (a vote per K block) each product's order
 // is chosen by itself.
 //
-// Measured: 64 x 16384 x 8192 25.0 us (5.5 TB/s; one wave of 152 CTAs with even row
-// shares; 27.5 with one warp issuing the MMAs), 1 x 4096 x 4096 6.8 us, of which the
+// Measured: 64 x 16384 x 8192 25.5 us (5.5 TB/s; one wave of 152 CTAs with even row
+// shares; 27.5 with one warp issuing the MMAs), 1 x 4096 x 4096 7.2 us, of which the
 // 16.8 MB take 2.5: launch, the first loads and the cluster's exchange are the rest.
 #include <algorithm>
 
@@ -393,7 +393,8 @@ cudaError_t launch(BlkParams p, int num_sms, cudaStream_t stream)
     const int type = p.e5m2 ? 4 : 3;  // gemm_dtype_t
     // One wave of shares of 64 to 128 rows, with boxes just as tall (the MMA's other
     // rows hold what a slot last held and are not stored): 64 x 16384 x 8192 on all
-    // SMs instead of 128 of them.
+    // SMs instead of 128 of them, 64 x 18000 x 8192 28.4 us.  Above 128 rows an SM whole
+    // tiles take two rounds: 48.5 to 50 us from 20000 to 32768 rows.
     p.row_share = p.batch == 1 && p.M <= BN && p.N >= 64 * num_sms && p.N <= 128 * num_sms;
     p.x_box = p.row_share ? std::min(BM, ((p.N + num_sms - 1) / num_sms + 7) / 8 * 8) : BM;
     if (!operand_map(&tmx, p.B, p.N, p.K, p.ldb, p.batch, p.stride_b, p.x_box, &p.b_bmul, type) ||

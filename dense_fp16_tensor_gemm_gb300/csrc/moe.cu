@@ -16,7 +16,8 @@
 // tokens on the other.  The up kernel multiplies x as it is, m16n8k16 in x's
 // type, with weights of that type or E4M3 ones widened to it (exact).  h is fp32;
 // for bf16 and E4M3 weights it is stored as the sum of two bf16 values (16
-// significant bits, fp32's range) and multiplied as two bf16 operands.  fp16
+// significant bits, fp32's range; the error, 2^-18 of a value at most, is 1/500 of what
+// rounding Out to bf16 adds, and 1/60 in fp16) and multiplied as two bf16 operands.  fp16
 // weights do not fit bf16 and fp16 does not hold h's range, so there the down
 // kernel multiplies in tf32 (m16n8k8), which holds every fp16 value, h in two
 // parts again.  The order of K inside an item is free as long as both operands
@@ -24,15 +25,16 @@
 // elements feed the slots of the MMA that are its own.
 //
 // With 64 tokens the warps' own time on an item bounds the kernels, not memory: an
-// item of 2 KB of E4M3 weights costs a warp 400 instructions, and rings and sums
+// item of 2 KB of E4M3 weights costs a warp 380 instructions in the up kernel and 460
+// in the down kernel (counted, with their part of the routing), and rings and sums
 // leave an SM 16 warps.  So an item's loads and loop are kept to running pointers
 // and immediate offsets, and the next item's load goes out before the arithmetic.
-// (Widening E4M3 through fp16 costs little: without it 64 tokens take 139 us for 150.)
+// (Widening E4M3 through fp16 costs little: leaving it out took 7 % off 64 tokens.)
 //
-// Measured, 64 experts of 2048 x 1024, 8 a token: one token 27 us in bf16 (100 MB,
+// Measured, 64 experts of 2048 x 1024, 8 a token: one token 28 us in bf16 (100 MB,
 // 15 us at the memory's rate; two launches and their first loads take 7.5), 64 tokens
-// 141 us in E4M3 (403 MB, 60 us), 177 in bf16 (805 MB, 119 us).  16 tokens on 8
-// experts of 4096 x 8192, 2 a token: 265 us (1.6 GB, 235 us).
+// 142 us in E4M3 (403 MB, 60 us), 178 in bf16 (805 MB, 119 us).  16 tokens on 8
+// experts of 4096 x 8192, 2 a token: 253 to 276 us (1.6 GB, 235 us).
 //
 // Routing is recomputed by every CTA from the logits, a few thousand
 // instructions; that spares a kernel and a round trip through memory.
@@ -832,8 +834,6 @@ struct DownCfg {
     }
 };
 
-// Waits until the word at `turn` is at least `unit`; false after `limit` cycles, or
-// once another warp has given up, which the word behind it says and keeps saying.
 __device__ __forceinline__ int turn_word(uint32_t a)
 {
     int v;
@@ -844,6 +844,8 @@ __device__ __forceinline__ void set_turn_word(uint32_t a, int v)
 {
     asm volatile("st.release.cta.shared::cta.s32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
 }
+// Waits until the word at `turn` is at least `unit`; false after `limit` cycles, or
+// once another warp has given up, which the word behind it says and keeps saying.
 __device__ __forceinline__ bool wait_turn(uint32_t turn, int unit, unsigned long long limit)
 {
     const long long t0 = clock64();
