@@ -456,7 +456,9 @@ def _elsewhere(stream):
     cuda, handle = (_torch or _init_torch()).cuda, _stream_handle(stream)
     if handle == cuda.current_stream().cuda_stream:
         return None
-    return stream if isinstance(stream, cuda.Stream) else cuda.ExternalStream(handle)
+    if isinstance(stream, cuda.Stream):
+        return stream
+    return cuda.ExternalStream(handle) if handle else cuda.default_stream()
 
 
 def _record(result, stream, given):

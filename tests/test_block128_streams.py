@@ -20,10 +20,16 @@ class Stream:
 
 class Cuda:
     Stream = Stream
-    ExternalStream = Stream
 
     def __init__(self):
         self.now = Stream(1)
+
+    def ExternalStream(self, handle):
+        """As torch's: handle 0 makes a stream of its own, not the default one."""
+        return Stream(handle or 99)
+
+    def default_stream(self, device=None):
+        return Stream(0)
 
     def current_stream(self, device=None):
         return self.now
@@ -136,3 +142,10 @@ def test_given_outputs_and_workspace_are_the_callers(fake):
     out, ws = torch.empty_like(X), torch.empty(4096, dtype=torch.uint8)
     assert gnt.moe_few_tokens(X, LOGITS, W13, W2, 2, out=out, workspace=ws, stream=Stream(7)) is out
     assert not f.pools and not recorded
+
+
+@pytest.mark.parametrize("name", CALLS)
+def test_the_default_stream_by_its_handle(fake, name):
+    f, lib, _ = fake
+    CALLS[name](0)
+    assert set(f.pools) == {0} and set(lib.launched) == {0}

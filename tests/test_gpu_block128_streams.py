@@ -68,3 +68,18 @@ def test_dropped_results_are_not_handed_out_while_they_are_written():
     torch.cuda.synchronize()
     for t in mine:
         assert bool((t == 0x55).all())
+
+
+def test_the_default_stream_by_its_handle():
+    """Handle 0 under another current stream is the default stream: what it wrote is
+    there for work on the default stream without further ado."""
+    call = operands()["forward"]
+    want = bits(call())
+    torch.cuda.synchronize()
+    with torch.cuda.stream(torch.cuda.Stream()):
+        with torch.cuda.stream(torch.cuda.default_stream()):
+            torch.cuda._sleep(50_000_000)
+        got = call(stream=0)
+    got = bits(got)  # copies on the default stream
+    for p, q in zip(got, want):
+        assert torch.equal(p, q)
