@@ -432,21 +432,24 @@ def _one_of(dtype, allowed, what):
     return _CODES[dtype]
 
 
-def _same_device(device, *tensors):
-    """Refuses tensors (None: not given) that are not all on `device`, a CUDA device and
-    torch's current one: the library reads their addresses on that device."""
-    if device.type != "cuda":
-        raise ValueError("tensors must be on a CUDA device, not %s" % device)
-    for t in tensors:
-        if t is not None and t.device != device:
-            raise ValueError("tensors on %s and %s in one call" % (device, t.device))
-    if device.index != _torch.cuda.current_device():
-        raise ValueError("tensors on %s, which is not the current device" % device)
+def _same_device(first, *others):
+    """The index of the CUDA device that all of a call's tensors (None: not given) lie on,
+    torch's current one: the library reads their addresses there.  (Indexes, and torch's
+    own current index: device objects and torch.cuda.current_device() took 4 us a call.)"""
+    index = first.get_device()
+    if index < 0:
+        raise ValueError("tensors must be on a CUDA device, not %s" % first.device)
+    for t in others:
+        if t is not None and t.get_device() != index:
+            raise ValueError("tensors on %s and %s in one call" % (first.device, t.device))
+    if index != _torch._C._cuda_getDevice():
+        raise ValueError("tensors on %s, which is not the current device" % first.device)
+    return index
 
 
-def _stream_of(device):
-    """The handle of torch's current stream on the device."""
-    return _torch._C._cuda_getCurrentRawStream(device.index)
+def _stream_of(index):
+    """The handle of torch's current stream on the device of that index."""
+    return _torch._C._cuda_getCurrentRawStream(index)
 
 
 def _elsewhere(stream):
@@ -532,17 +535,16 @@ def gemm_nt_block128_tensors(A, SA, B, SB, out=None, path=Path.AUTO, stream=None
     N = bsh[-2]
     shape = (ash[0], M, N) if batched else (M, N)
     sa, sb = _scale128(SA, M, K, "SA"), _scale128(SB, N, K, "SB")
-    device = A.device
-    _same_device(device, SA, B, SB, out)
+    index = _same_device(A, SA, B, SB, out)
     if out is None:
-        out = torch.empty(shape, dtype=dt, device=device)
+        out = torch.empty(shape, dtype=dt, device=A.device)
     elif tuple(out.shape) != shape:
         raise ValueError("out must have shape (M,N), with A's batch dimension")
     ast, bst, ost = A.stride(), B.stride(), out.stride()
     gemm_nt_block128(A.data_ptr(), sa, B.data_ptr(), sb, out.data_ptr(), ab, ot, M, N, K,
                      _pitch(ash, ast, "A"), _pitch(bsh, bst, "B"), _pitch(shape, ost, "out"),
                      ast[0] if batched else 0, bst[0] if batched else 0, ost[0] if batched else 0,
-                     ash[0] if batched else 1, path, _stream_of(device))
+                     ash[0] if batched else 1, path, _stream_of(index))
     return out
 
 
@@ -593,23 +595,21 @@ def _quantize(X, q_dtype, block_rows, transposed, beside=()):
     xt = _one_of(X.dtype, _OUT, "X")
     ldx = _pitch(shape, X.stride(), "X")
     rows, cols = shape
-    device = X.device
-    _same_device(device, *beside)
+    index, device = _same_device(X, *beside), X.device
     q, s, ldq, sq = _quantized(rows, cols, q_dtype, block_rows, device)
     qt, st, ldqt, sqt = _quantized(cols, rows, q_dtype, block_rows, device) if transposed else (None, None, 0, None)
     gemm_nt_block128_quantize(X.data_ptr(), xt, rows, cols, ldx, q.data_ptr(), ldq, sq, qt.data_ptr() if transposed else 0,
-                              ldqt, sqt, code, _stream_of(device))
+                              ldqt, sqt, code, _stream_of(index))
     return q, s, sq, qt, st, sqt
 
 
 def _product(A, SA, B, SB, dtype):
     """A @ B.T of two matrices of codes whose scales are C structs."""
     (M, K), (N, _) = A.shape, B.shape
-    device = A.device
-    out = _torch.empty((M, N), dtype=dtype, device=device)
+    out = _torch.empty((M, N), dtype=dtype, device=A.device)
     gemm_nt_block128(A.data_ptr(), SA, B.data_ptr(), SB, out.data_ptr(), _CODES[A.dtype], _CODES[dtype], M, N, K,
                      _pitch((M, K), A.stride(), "A"), _pitch((N, K), B.stride(), "B"), max(N, 1), 0, 0, 0, 1, 0,
-                     _stream_of(device))
+                     _stream_of(A.get_device()))
     return out
 
 
@@ -685,7 +685,6 @@ def moe_few_tokens(X, logits, W13, W2, topk, S13=None, S2=None, renormalize=True
     experts, inner = lsh[1], s2h[2]
     if lsh[0] != tokens or s13h != (experts, 2 * inner, hidden) or s2h != (experts, hidden, inner):
         raise ValueError(_MOE_SHAPES)
-    device = X.device
     xt = _one_of(X.dtype, _X16, "X")
     if W13.dtype != W2.dtype:
         raise TypeError("W13 and W2 must have the same type")
@@ -699,7 +698,7 @@ def moe_few_tokens(X, logits, W13, W2, topk, S13=None, S2=None, renormalize=True
         if S13.dim() != 3 or S2.dim() != 3 or S13.shape[0] != experts or S2.shape[0] != experts:
             raise ValueError("S13 and S2 need a leading expert dimension")
         s13, s2 = _scale128(S13, 2 * inner, hidden, "S13"), _scale128(S2, hidden, inner, "S2")
-    _same_device(device, logits, W13, W2, S13, S2, out, workspace)
+    index, device = _same_device(X, logits, W13, W2, S13, S2, out, workspace), X.device
     if out is None:
         out = torch.empty((tokens, hidden), dtype=X.dtype, device=device)
     elif tuple(out.shape) != (tokens, hidden) or out.dtype != X.dtype:
@@ -714,5 +713,5 @@ def moe_few_tokens(X, logits, W13, W2, topk, S13=None, S2=None, renormalize=True
     gemm_nt_moe(X.data_ptr(), _pitch(xsh, X.stride(), "X"), logits.data_ptr(), _pitch(lsh, logits.stride(), "logits"),
                 W13.data_ptr(), _pitch(s13h, t13, "W13"), t13[0], s13, W2.data_ptr(), _pitch(s2h, t2, "W2"), t2[0], s2,
                 out.data_ptr(), _pitch(xsh, out.stride(), "out"), xt, wt, tokens, experts, topk, hidden, inner,
-                renormalize, workspace.data_ptr(), workspace.nbytes, _stream_of(device))
+                renormalize, workspace.data_ptr(), workspace.nbytes, _stream_of(index))
     return out

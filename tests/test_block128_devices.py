@@ -52,13 +52,12 @@ def test_host_tensors_are_refused(name, no_calls):
 
 def test_mixed_and_other_devices_are_refused(monkeypatch):
     gnt._init_torch()
-    monkeypatch.setattr(gnt, "_torch", types.SimpleNamespace(cuda=types.SimpleNamespace(current_device=lambda: 0)))
-    here, there = torch.device("cuda", 0), torch.device("cuda", 1)
-    on = lambda d: types.SimpleNamespace(device=d)  # noqa: E731
-    gnt._same_device(here, on(here), None, on(here))
-    for device, tensors in ((here, [on(there)]), (here, [on(here), None, on(torch.device("cpu"))]), (there, [on(there)])):
+    monkeypatch.setattr(gnt, "_torch", types.SimpleNamespace(_C=types.SimpleNamespace(_cuda_getDevice=lambda: 0)))
+    on = lambda i: types.SimpleNamespace(get_device=lambda: i, device="device %d" % i)  # noqa: E731
+    assert gnt._same_device(on(0), on(0), None, on(0)) == 0
+    for tensors in ([on(0), on(1)], [on(0), None, on(-1)], [on(-1), on(0)], [on(1), on(1)]):
         with pytest.raises(ValueError):
-            gnt._same_device(device, *tensors)
+            gnt._same_device(*tensors)
 
 
 @pytest.mark.gpu

@@ -80,8 +80,8 @@ def fake(monkeypatch):
     f, lib, recorded = Torch(), Library(), []
     monkeypatch.setattr(gnt, "_torch", f)
     monkeypatch.setattr(gnt, "_lib", lib)
-    monkeypatch.setattr(gnt, "_stream_of", lambda device: f.cuda.now.cuda_stream)
-    monkeypatch.setattr(gnt, "_same_device", lambda *a: None, raising=False)
+    monkeypatch.setattr(gnt, "_stream_of", lambda index: f.cuda.now.cuda_stream)
+    monkeypatch.setattr(gnt, "_same_device", lambda *a: 0)
     monkeypatch.setattr(torch.Tensor, "record_stream",
                         lambda t, s: recorded.append((t.data_ptr(), s.cuda_stream)), raising=False)
     return f, lib, recorded
