@@ -53,6 +53,12 @@ class Path(enum.IntEnum):
     TC05_WS = 6    # 32- or 64-row tiles, weight-stationary MMA
 
 
+class Act(enum.IntEnum):
+    SILU = 0
+    GELU = 1       # with erf
+    GELU_TANH = 2
+
+
 class GemmError(RuntimeError):
     def __init__(self, status):
         self.status = Status(status)
@@ -66,9 +72,17 @@ class Scale128(ctypes.Structure):
                 ("kb_stride", ctypes.c_int64), ("batch_stride", ctypes.c_int64)]
 
 
+class Weights4(ctypes.Structure):
+    """gemm_w4_t: 4-bit weights, two codes to a byte, with one 16-bit scale and
+    (or null) one zero point for each `group` elements of a row."""
+    _fields_ = [("codes", ctypes.c_void_p), ("ldc", ctypes.c_int64), ("scales", ctypes.c_void_p),
+                ("lds", ctypes.c_int64), ("zeros", ctypes.c_void_p), ("ldz", ctypes.c_int64),
+                ("group", ctypes.c_int32)]
+
+
 # name -> (restype, argtypes); mirrors include/gemm_nt.h
 _i64, _vp, _u64 = ctypes.c_int64, ctypes.c_void_p, ctypes.c_uint64
-_sp = ctypes.POINTER(Scale128)
+_sp, _wp = ctypes.POINTER(Scale128), ctypes.POINTER(Weights4)
 _SIGNATURES = {
     "gemm_nt_f16_f32": (ctypes.c_int, [_vp, _vp, _vp] + [_i64] * 6 + [_vp]),
     "gemm_nt_f16_f32_batched": (ctypes.c_int, [_vp, _vp, _vp] + [_i64] * 10 + [_vp]),
@@ -89,6 +103,12 @@ _SIGNATURES = {
     "gemm_nt_moe": (ctypes.c_int, [_vp, _i64, _vp, _i64, _vp, _i64, _i64, _sp, _vp, _i64, _i64, _sp, _vp, _i64,
                                    ctypes.c_int, ctypes.c_int] + [_i64] * 5 + [ctypes.c_int, _vp, _i64, _vp]),
     "gemm_nt_moe_workspace_bytes": (_i64, [_i64, _i64, _i64]),
+    "gemm_nt_gated": (ctypes.c_int, [_vp, _i64] * 4 + [ctypes.c_int, ctypes.c_int] + [_i64] * 3 + [ctypes.c_int, _vp]),
+    "gemm_nt_gated_grad": (ctypes.c_int, [_vp, _i64] * 3 + [ctypes.c_int, ctypes.c_int, _i64, _i64, _vp]),
+    "gemm_nt_w4_quantize": (ctypes.c_int, [_vp, ctypes.c_int, _i64, _i64, _i64, _wp, ctypes.c_int, _vp]),
+    "gemm_nt_w4": (ctypes.c_int, [_vp, _i64, _wp, _vp, _i64, ctypes.c_int] + [_i64] * 3 + [ctypes.c_int, _vp]),
+    "gemm_nt_w4_gated": (ctypes.c_int, [_vp, _i64, _wp, _vp, _i64, ctypes.c_int, ctypes.c_int] + [_i64] * 3
+                         + [ctypes.c_int, _vp]),
     "gemm_nt_select_path": (ctypes.c_int, [_vp, _vp, _vp] + [_i64] * 10),
     "gemm_nt_check": (ctypes.c_int, [_vp]),
     "gemm_nt_error_string": (ctypes.c_char_p, [ctypes.c_int]),
@@ -193,6 +213,30 @@ def gemm_nt_moe(X, ldx, logits, ldl, W13, ldw13, strideW13, S13, W2, ldw2, strid
 
 def gemm_nt_moe_workspace_bytes(tokens, topk, inner):
     return int(load().gemm_nt_moe_workspace_bytes(tokens, topk, inner))
+
+
+def gemm_nt_gated(X, ldx, W13, ldw, H, ldh, GU, ldgu, dtype, act, tokens, hidden, inner, path=0, stream=0):
+    _check(load().gemm_nt_gated(X, ldx, W13, ldw, H, ldh, GU, ldgu, int(dtype), int(act), tokens, hidden, inner,
+                                int(path), stream))
+
+
+def gemm_nt_gated_grad(dH, ldd, GU, ldgu, dGU, ldo, dtype, act, tokens, inner, stream=0):
+    _check(load().gemm_nt_gated_grad(dH, ldd, GU, ldgu, dGU, ldo, int(dtype), int(act), tokens, inner, stream))
+
+
+def gemm_nt_w4_quantize(W, w_type, rows, cols, ldw, Q, s_type, stream=0):
+    """Q is a Weights4, whose arrays are written."""
+    _check(load().gemm_nt_w4_quantize(W, int(w_type), rows, cols, ldw, Q, int(s_type), stream))
+
+
+def gemm_nt_w4(X, ldx, W, Out, ldo, dtype, M, N, K, path=0, stream=0):
+    """W is a Weights4 (or None when K is 0)."""
+    _check(load().gemm_nt_w4(X, ldx, W, Out, ldo, int(dtype), M, N, K, int(path), stream))
+
+
+def gemm_nt_w4_gated(X, ldx, W13, H, ldh, dtype, act, tokens, hidden, inner, path=0, stream=0):
+    _check(load().gemm_nt_w4_gated(X, ldx, W13, H, ldh, int(dtype), int(act), tokens, hidden, inner, int(path),
+                                   stream))
 
 
 def gemm_nt_f16_f32_batched_no_alloc(A, B, Out, M, N, K, lda, ldb, ldo, strideA, strideB, strideO,
@@ -714,4 +758,181 @@ def moe_few_tokens(X, logits, W13, W2, topk, S13=None, S2=None, renormalize=True
                 W13.data_ptr(), _pitch(s13h, t13, "W13"), t13[0], s13, W2.data_ptr(), _pitch(s2h, t2, "W2"), t2[0], s2,
                 out.data_ptr(), _pitch(xsh, out.stride(), "out"), xt, wt, tokens, experts, topk, hidden, inner,
                 renormalize, workspace.data_ptr(), workspace.nbytes, _stream_of(index))
+    return out
+
+
+# ---------------------------------------------------------------- the gated feed-forward block, 4-bit weights
+_ACTS = {"silu": 0, "gelu": 1, "gelu_tanh": 2}
+
+
+def _act(activation):
+    if activation not in _ACTS:
+        raise ValueError("activation must be one of %s" % ", ".join(_ACTS))
+    return _ACTS[activation]
+
+
+def _rows(n, width, dtype, device):
+    """An empty (n, width) matrix of 16-bit elements whose rows start on 16-byte boundaries."""
+    return _torch.empty_strided((n, width), ((width + 7) // 8 * 8, 1), dtype=dtype, device=device)
+
+
+def _out16(out, n, width, like):
+    if out is None:
+        return _rows(n, width, like.dtype, like.device)
+    if tuple(out.shape) != (n, width) or out.dtype != like.dtype:
+        raise ValueError("out must have shape (%d,%d) and X's type" % (n, width))
+    return out
+
+
+def gated_linear(X, W13, activation="silu", keep=False, out=None, path=Path.AUTO, stream=None):
+    """H = act(X @ Wg.T) * (X @ Wu.T) in one kernel: X (tokens, hidden) and W13
+    (2*inner, hidden), Wg's rows then Wu's, both float16 or both bfloat16; H
+    (tokens, inner) in their type.  ``activation``: "silu", "gelu" (with erf) or
+    "gelu_tanh".  With ``keep`` returns ``(H, GU)``: GU (tokens, 2*inner) holds
+    X @ W13.T in X's type, which :func:`gated_linear_backward` takes.  Rows of what is
+    returned start on 16-byte boundaries.
+    """
+    side = _elsewhere(stream)
+    if side is not None:
+        return _run_on(side, gated_linear, X, W13, activation, keep, out, path, given=out)
+    _torch or _init_torch()
+    xsh, wsh = X.shape, W13.shape
+    if len(xsh) != 2 or len(wsh) != 2 or wsh[1] != xsh[1] or wsh[0] % 2:
+        raise ValueError("shapes: X (tokens, hidden), W13 (2*inner, hidden)")
+    if W13.dtype != X.dtype:
+        raise TypeError("X and W13 must have the same type")
+    code, act = _one_of(X.dtype, _X16, "X"), _act(activation)
+    tokens, hidden = xsh
+    inner = wsh[0] // 2
+    index = _same_device(X, W13, out)
+    out = _out16(out, tokens, inner, X)
+    gu = _rows(tokens, 2 * inner, X.dtype, X.device) if keep else None
+    gemm_nt_gated(X.data_ptr(), _pitch(xsh, X.stride(), "X"), W13.data_ptr(), _pitch(wsh, W13.stride(), "W13"),
+                  out.data_ptr(), _pitch(out.shape, out.stride(), "out"), gu.data_ptr() if keep else 0,
+                  gu.stride(0) if keep else 0, code, act, tokens, hidden, inner, path, _stream_of(index))
+    return (out, gu) if keep else out
+
+
+def gated_linear_backward(dH, GU, X, W13, activation="silu", stream=None):
+    """Gradients of :func:`gated_linear`: ``(dX, dW13)`` in X's type from dH
+    (tokens, inner) and the GU it kept.  The gradient at the two projections is
+    rounded to X's type before the products dX = dGU @ W13 and dW13 = dGU.T @ X,
+    which accumulate in float32."""
+    side = _elsewhere(stream)
+    if side is not None:
+        _record(GU, side, None)
+        return _run_on(side, gated_linear_backward, dH, GU, X, W13, activation)
+    _torch or _init_torch()
+    xsh, wsh = X.shape, W13.shape
+    if len(xsh) != 2 or len(wsh) != 2 or wsh[1] != xsh[1] or wsh[0] % 2:
+        raise ValueError("shapes: X (tokens, hidden), W13 (2*inner, hidden)")
+    tokens, hidden = xsh
+    rows = wsh[0]
+    if tuple(dH.shape) != (tokens, rows // 2) or tuple(GU.shape) != (tokens, rows):
+        raise ValueError("shapes: dH (tokens, inner), GU (tokens, 2*inner)")
+    if not X.dtype == W13.dtype == dH.dtype == GU.dtype:
+        raise TypeError("dH, GU, X and W13 must have the same type")
+    code, act = _one_of(X.dtype, _X16, "X"), _act(activation)
+    ldx, ldw = _pitch(xsh, X.stride(), "X"), _pitch(wsh, W13.stride(), "W13")
+    ldd, ldg = _pitch(dH.shape, dH.stride(), "dH"), _pitch(GU.shape, GU.stride(), "GU")
+    index = _same_device(X, W13, dH, GU)
+    stream, device = _stream_of(index), X.device
+    dgu = _rows(tokens, rows, X.dtype, device)
+    ldo = dgu.stride(0)
+    gemm_nt_gated_grad(dH.data_ptr(), ldd, GU.data_ptr(), ldg, dgu.data_ptr(), ldo, code, act, tokens, rows // 2, stream)
+    dx, dw = _rows(tokens, hidden, X.dtype, device), _rows(rows, hidden, X.dtype, device)
+    gemm_nt_batched_major(dgu.data_ptr(), 0, W13.data_ptr(), 1, dx.data_ptr(), code, code, tokens, hidden, rows, ldo, ldw,
+                          dx.stride(0), 0, 0, 0, 1, 0, stream)
+    gemm_nt_batched_major(dgu.data_ptr(), 1, X.data_ptr(), 1, dw.data_ptr(), code, code, rows, hidden, tokens, ldo, ldx,
+                          dw.stride(0), 0, 0, 0, 1, 0, stream)
+    return dx, dw
+
+
+def quantize_w4(W, group=128, zeros=False, scale_dtype=None, stream=None):
+    """4-bit codes and 16-bit scales of W (rows, cols; float32, float16 or
+    bfloat16), one scale for each ``group`` (32, 64 or 128) of a row, and with
+    ``zeros`` one zero point too; see gemm_nt_w4_quantize in include/gemm_nt.h.
+    ``scale_dtype``: float16 or bfloat16, the type of the activations that the weights
+    are multiplied with; W's by default (bfloat16 for float32).
+
+    Returns ``(Q, S)`` or ``(Q, S, Z)``: Q (rows, ceil(cols/2)) uint8, the even
+    column in the low half of a byte, rows on 16-byte boundaries; S (rows,
+    ceil(cols/group)); Z the same, uint8.
+    """
+    side = _elsewhere(stream)
+    if side is not None:
+        return _run_on(side, quantize_w4, W, group, zeros, scale_dtype)
+    torch = _torch or _init_torch()
+    shape = W.shape
+    if len(shape) != 2:
+        raise ValueError("W must be a matrix")
+    wt = _one_of(W.dtype, _OUT, "W")
+    scale_dtype = scale_dtype or (torch.bfloat16 if wt == 2 else W.dtype)
+    st = _one_of(scale_dtype, _X16, "scale_dtype")
+    if group not in (32, 64, 128):
+        raise ValueError("group must be 32, 64 or 128")
+    ldw = _pitch(shape, W.stride(), "W")
+    rows, cols = shape
+    index, device = _same_device(W), W.device
+    width, groups = (cols + 1) // 2, (cols + group - 1) // group
+    pitch = (width + 15) // 16 * 16
+    q = torch.empty_strided((rows, width), (pitch, 1), dtype=torch.uint8, device=device)
+    s = torch.empty((rows, groups), dtype=scale_dtype, device=device)
+    z = torch.empty((rows, groups), dtype=torch.uint8, device=device) if zeros else None
+    gemm_nt_w4_quantize(W.data_ptr(), wt, rows, cols, ldw,
+                        Weights4(q.data_ptr(), pitch, s.data_ptr(), groups, z.data_ptr() if zeros else None, groups, group),
+                        st, _stream_of(index))
+    return (q, s, z) if zeros else (q, s)
+
+
+def _weights4(Q, S, Z, X, group):
+    """4-bit weights for X's columns as the C struct, and their rows."""
+    if group not in (32, 64, 128):
+        raise ValueError("group must be 32, 64 or 128")
+    if X.dim() != 2 or Q.dim() != 2 or S.dim() != 2 or Z is not None and Z.dim() != 2:
+        raise ValueError("X, Q, S and Z must be matrices")
+    if Q.dtype != _torch.uint8 or S.dtype != X.dtype or Z is not None and Z.dtype != _torch.uint8:
+        raise TypeError("Q and Z must be uint8, S of X's type")
+    rows, cols = Q.shape[0], X.shape[1]
+    shape = (rows, (cols + group - 1) // group)
+    if Q.shape[1] != (cols + 1) // 2 or tuple(S.shape) != shape or Z is not None and tuple(Z.shape) != shape:
+        raise ValueError("shapes for %d columns: Q (rows, %d), S and Z (rows, %d)" % (cols, (cols + 1) // 2, shape[1]))
+    return Weights4(Q.data_ptr(), _pitch(Q.shape, Q.stride(), "Q"), S.data_ptr(), _pitch(shape, S.stride(), "S"),
+                    None if Z is None else Z.data_ptr(), 0 if Z is None else _pitch(shape, Z.stride(), "Z"), group), rows
+
+
+def linear_w4(X, Q, S, Z=None, group=128, out=None, path=Path.AUTO, stream=None):
+    """Y = X @ W.T with the 4-bit weights of :func:`quantize_w4`: X (tokens, in)
+    float16 or bfloat16, Q, S and Z of W (out, in), S in X's type.  Sums are
+    float32; Y (tokens, out) has X's type, its rows start on 16-byte boundaries."""
+    side = _elsewhere(stream)
+    if side is not None:
+        return _run_on(side, linear_w4, X, Q, S, Z, group, out, path, given=out)
+    _torch or _init_torch()
+    code = _one_of(X.dtype, _X16, "X")
+    w, rows = _weights4(Q, S, Z, X, group)
+    tokens, cols = X.shape
+    index = _same_device(X, Q, S, Z, out)
+    out = _out16(out, tokens, rows, X)
+    gemm_nt_w4(X.data_ptr(), _pitch(X.shape, X.stride(), "X"), w, out.data_ptr(), _pitch(out.shape, out.stride(), "out"),
+               code, tokens, rows, cols, path, _stream_of(index))
+    return out
+
+
+def gated_linear_w4(X, Q13, S13, Z13=None, group=128, activation="silu", out=None, path=Path.AUTO, stream=None):
+    """:func:`gated_linear` with the 4-bit weights of :func:`quantize_w4` in W13's place."""
+    side = _elsewhere(stream)
+    if side is not None:
+        return _run_on(side, gated_linear_w4, X, Q13, S13, Z13, group, activation, out, path, given=out)
+    _torch or _init_torch()
+    code, act = _one_of(X.dtype, _X16, "X"), _act(activation)
+    w, rows = _weights4(Q13, S13, Z13, X, group)
+    if rows % 2:
+        raise ValueError("Q13 must have 2*inner rows")
+    tokens, hidden = X.shape
+    index = _same_device(X, Q13, S13, Z13, out)
+    out = _out16(out, tokens, rows // 2, X)
+    gemm_nt_w4_gated(X.data_ptr(), _pitch(X.shape, X.stride(), "X"), w, out.data_ptr(),
+                     _pitch(out.shape, out.stride(), "out"), code, act, tokens, hidden, rows // 2, path,
+                     _stream_of(index))
     return out

@@ -4,43 +4,14 @@
 #include <algorithm>
 
 #include "gemm_nt.h"
+#include "api_checks.h"
 #include "block128.h"
 
 namespace gnt {
 
 namespace {
 
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
-
 int64_t kblocks(int64_t K) { return (K + 127) / 128; }
-
-// Bytes [lo, hi) that an array of strided dimensions touches (at least one element each).
-struct Span {
-    uintptr_t lo, hi;
-};
-Span span_of(const void* base, int64_t esize, int64_t n0, int64_t s0, int64_t n1, int64_t s1, int64_t n2 = 1,
-             int64_t s2 = 0)
-{
-    const uintptr_t lo = reinterpret_cast<uintptr_t>(base);
-    return {lo, lo + static_cast<uintptr_t>(((n0 - 1) * s0 + (n1 - 1) * s1 + (n2 - 1) * s2 + 1) * esize)};
-}
-bool overlap(const Span& a, const Span& b) { return a.lo < b.hi && b.lo < a.hi; }
-
-// Whether n0 x n1 x n2 elements with these strides end within 2^62 bytes (sizes are below 2^31).
-bool in_range(int64_t n0, int64_t s0, int64_t n1, int64_t s1, int64_t n2 = 1, int64_t s2 = 0)
-{
-    const double e = static_cast<double>(n0) * static_cast<double>(s0) + static_cast<double>(n1) * static_cast<double>(s1) +
-                     static_cast<double>(n2) * static_cast<double>(s2);
-    return e * 4.0 < 4.0e18;
-}
-
-bool sizes_ok(std::initializer_list<int64_t> v)
-{
-    for (int64_t x : v)
-        if (x < 0 || x > INT32_MAX)
-            return false;
-    return true;
-}
 
 bool scale_ok(const gemm_scale128_t* s, int64_t rows, int64_t K, int64_t batch)
 {
@@ -86,8 +57,6 @@ gemm_path_t select(const BlkParams& p, const DeviceInfo& d, int64_t pair_tiles)
     const int part = p.sb.shift ? 3 : 2;
     return p.M > 128 && d.block_pairs > 0 && part * pair_tiles >= d.block_pairs ? GEMM_PATH_TC05_PAIR : GEMM_PATH_SKINNY;
 }
-
-gemm_status_t status_of(cudaError_t e) { return e == cudaSuccess ? GEMM_OK : GEMM_ERR_LAUNCH; }
 
 }  // namespace
 }  // namespace gnt

@@ -1,0 +1,108 @@
+// ffn.h -- declarations shared by the gated feed-forward product, its backward
+// pass and the products with 4-bit weights.  Not part of the public ABI.
+#pragma once
+#include <cstdint>
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include "internal.h"
+
+namespace gnt {
+
+constexpr int kActSilu = 0, kActGelu = 1, kActGeluTanh = 2;
+
+#ifdef __CUDACC__
+// act(g) = g P(g) and its slope P(g) + g P'(g), with P the logistic function
+// (silu), the normal distribution function (gelu), or the logistic function of
+// 2 sqrt(2/pi) (g + 0.044715 g^3) (gelu_tanh: (1 + tanh v)/2 is the logistic
+// function of 2v, which keeps its relative precision where 1 + tanh v cancels;
+// so does erfc on the normal one's lower tail).
+struct ActP {
+    float p, d;  // P and P'
+};
+__device__ __forceinline__ float logistic(float v) { return __fdividef(1.f, 1.f + __expf(-v)); }
+
+template <bool SLOPE>
+__device__ __forceinline__ ActP act_p(float g, int act)
+{
+    ActP r;
+    r.d = 0.f;
+    if (act == kActGelu) {
+        r.p = 0.5f * erfcf(g * -0.70710678f);
+        if (SLOPE)
+            r.d = 0.39894228f * __expf(-0.5f * g * g);
+    } else {
+        const float v = act == kActSilu ? g : 1.59576912f * (g + 0.044715f * g * g * g);
+        r.p = logistic(v);
+        if (SLOPE) {
+            r.d = r.p - r.p * r.p;
+            // past the ends P' is 0, whatever the polynomial's own slope overflows to
+            if (act == kActGeluTanh && r.d != 0.f)
+                r.d *= 1.59576912f * (1.f + 0.134145f * g * g);
+        }
+    }
+    return r;
+}
+
+__device__ __forceinline__ float act_value(float g, int act) { return g * act_p<false>(g, act).p; }
+#endif
+
+// One product of tokens with weights, plain or gated:
+//   plain  Out[t][j] = sum_k x[t][k] w[j][k]
+//   gated  Out[t][j] = act(g) u, g and u the sums with rows j and n + j of w
+// Weights are 16-bit (x's type), or 4-bit codes (element 2b in the low half of
+// byte b of a row) that stand for (code - zero) * scale, one scale and zero for
+// each `1 << group_shift` elements of a row.
+struct FfnParams {
+    const void* x;
+    int64_t ldx;
+    const void* w;
+    int64_t ldw;           // elements; bytes for 4-bit weights
+    const void* scales;    // x's type; null: 16-bit weights
+    int64_t lds;
+    const uint8_t* zeros;  // null: 8
+    int64_t ldz;
+    int group_shift;
+    void* out;
+    int64_t ldo;
+    void* gu;  // gated, 16-bit weights: [g u] of every token; null: not kept
+    int64_t ldgu;
+    int tokens, n, k;
+    int gated, act, bf16;
+    uint32_t* status;
+    unsigned long long wait_limit;
+    int fault;
+};
+
+// Any layout, on the warp MMA.
+cudaError_t ffn_any_launch(const FfnParams& p, int num_sms, cudaStream_t stream);
+
+// dGU = [dh u act'(g), dh act(g)]
+struct GradParams {
+    const void* dh;
+    int64_t ldd;
+    const void* gu;
+    int64_t ldgu;
+    void* out;
+    int64_t ldo;
+    int64_t tokens, n;
+    int act, bf16;
+};
+cudaError_t gated_grad_launch(const GradParams& p, int num_sms, cudaStream_t stream);
+
+// 4-bit quantiser.
+struct Quant4Params {
+    const void* w;
+    int w_type;  // gemm_dtype_t value
+    int64_t rows, cols, ldw;
+    uint8_t* codes;
+    int64_t ldc;
+    void* scales;
+    int64_t lds;
+    uint8_t* zeros;  // null: symmetric
+    int64_t ldz;
+    int group_shift, s_bf16;
+};
+cudaError_t w4_quantize_launch(const Quant4Params& p, int num_sms, cudaStream_t stream);
+
+}  // namespace gnt

@@ -407,6 +407,98 @@ gemm_status_t gemm_nt_moe(const void *X, int64_t ldx, const float *logits, int64
  * would not fit). */
 int64_t gemm_nt_moe_workspace_bytes(int64_t tokens, int64_t topk, int64_t inner);
 
+/* Activations of the gated product. */
+typedef enum gemm_act {
+    GEMM_ACT_SILU = 0,      /* g / (1 + exp(-g)) */
+    GEMM_ACT_GELU = 1,      /* g (1 + erf(g / sqrt 2)) / 2 */
+    GEMM_ACT_GELU_TANH = 2  /* g (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3))) / 2 */
+} gemm_act_t;
+
+/*
+ * The first half of a gated feed-forward block, in one kernel:
+ *   g = X Wg^T,  u = X Wu^T,  H = act(g) * u
+ * with Wg = W13 rows [0, inner) and Wu = W13 rows [inner, 2*inner).  X (tokens x
+ * hidden, row pitch ldx), W13 (2*inner x hidden, row pitch ldw) and H (tokens x
+ * inner, row pitch ldh) are all fp16 or all bf16 (`type`).  g and u are accumulated and
+ * multiplied in fp32; H is rounded once.  GU (tokens x 2*inner, row pitch ldgu; null to
+ * leave it out) receives g and u, each rounded to `type`, for gemm_nt_gated_grad.
+ *
+ * path: GEMM_PATH_AUTO, or GEMM_PATH_MMASYNC (warp MMA, any layout).  Other paths:
+ * GEMM_ERR_NOT_SUPPORTED.
+ *
+ * tokens or inner 0: nothing to do; hidden 0: zeros.  Any pitch and alignment is
+ * accepted; rows that start on 16-byte boundaries are read fastest.  Outputs that
+ * overlap an operand or each other (the byte spans, counting pitches):
+ * GEMM_ERR_OVERLAP.  Infinities and NaN follow IEEE arithmetic.  Nothing is allocated
+ * and the result does not depend on the run.
+ */
+gemm_status_t gemm_nt_gated(const void *X, int64_t ldx, const void *W13, int64_t ldw, void *H, int64_t ldh,
+                            void *GU, int64_t ldgu, gemm_dtype_t type, gemm_act_t act,
+                            int64_t tokens, int64_t hidden, int64_t inner, gemm_path_t path,
+                            gemm_stream_t stream);
+
+/*
+ * The gradient at the two projections of gemm_nt_gated, from dH (tokens x inner) and the
+ * GU it kept:
+ *   dGU = [dH * u * act'(g),  dH * act(g)]     (tokens x 2*inner)
+ * computed in fp32 and rounded once to `type` (dH's, GU's and dGU's).  The gradients of X
+ * and W13 are two products of gemm_nt_batched_major with the operands as they lie:
+ *   dX   = dGU @ W13    A = dGU K-major, B = W13 MN-major  (tokens, hidden, 2*inner)
+ *   dW13 = dGU^T @ X    A = dGU MN-major, B = X MN-major   (2*inner, hidden, tokens)
+ * Arguments, empty calls and errors as gemm_nt_gated.
+ */
+gemm_status_t gemm_nt_gated_grad(const void *dH, int64_t ldd, const void *GU, int64_t ldgu, void *dGU, int64_t ldo,
+                                 gemm_dtype_t type, gemm_act_t act, int64_t tokens, int64_t inner,
+                                 gemm_stream_t stream);
+
+/*
+ * 4-bit weights (rows x K): element k of row r stands for
+ *   (code - zero) * scale,   code = the low (k even) or high (k odd) half of byte
+ *   codes[r*ldc + k/2],      scale = scales[r*lds + k/group],  zero = zeros[r*ldz + k/group]
+ * codes 0 to 15, scales in 16 bits (the type of the product's X), zeros 0 to 15 or null: 8.
+ * group: 32, 64 or 128; the last group of a row as long as K leaves it.  Pitches in
+ * elements of each array.  The high half of an odd row's last byte and bytes between
+ * rows are not looked at.
+ */
+typedef struct gemm_w4 {
+    const uint8_t *codes;
+    int64_t ldc;
+    const void *scales;
+    int64_t lds;
+    const uint8_t *zeros;
+    int64_t ldz;
+    int32_t group;
+} gemm_w4_t;
+
+/*
+ * Quantises W (rows x cols, fp32, fp16 or bf16, row pitch ldw) into Q, whose arrays are
+ * written although its pointers are const.  For each group of a row, in fp32 with every
+ * step rounded,
+ *   Q->zeros null:  a = max |w|, s = a * (1/7) rounded to s_type (fp16 or bf16),
+ *                   code = clamp(rint(w * (1/s)), -8, 7) + 8
+ *   else            lo = min(w, 0), hi = max(w, 0), s = (hi - lo) * (1/15) rounded to s_type,
+ *                   z = clamp(rint(-lo * (1/s)), 0, 15), code = clamp(rint(w * (1/s)) + z, 0, 15)
+ * A group whose s is below 2^-126 is zero (s = 0); an infinity or NaN makes its group's
+ * scale NaN.  The high half of an odd row's last byte is written as 0, bytes between rows are
+ * left alone.  Empty W: GEMM_OK, nothing launched.  W or an output overlapping an output:
+ * GEMM_ERR_OVERLAP.
+ */
+gemm_status_t gemm_nt_w4_quantize(const void *W, gemm_dtype_t w_type, int64_t rows, int64_t cols, int64_t ldw,
+                                  const gemm_w4_t *Q, gemm_dtype_t s_type, gemm_stream_t stream);
+
+/*
+ * Out = X @ W^T with 4-bit weights: X (M x K) and Out (M x N) both fp16 or both bf16
+ * (`type`, also that of W's scales).  Sums in fp32, Out rounded once.
+ * M or N 0: nothing to do; K 0: zeros.  Paths, errors and the rest as gemm_nt_gated.
+ */
+gemm_status_t gemm_nt_w4(const void *X, int64_t ldx, const gemm_w4_t *W, void *Out, int64_t ldo, gemm_dtype_t type,
+                         int64_t M, int64_t N, int64_t K, gemm_path_t path, gemm_stream_t stream);
+
+/* gemm_nt_gated with 4-bit weights W13 (2*inner rows). */
+gemm_status_t gemm_nt_w4_gated(const void *X, int64_t ldx, const gemm_w4_t *W13, void *H, int64_t ldh,
+                               gemm_dtype_t type, gemm_act_t act, int64_t tokens, int64_t hidden, int64_t inner,
+                               gemm_path_t path, gemm_stream_t stream);
+
 /*
  * Host-side pipeline for callers whose data lives in host memory: copies A and
  * B (packed: lda = ldb = K, strideA = M*K, strideB = N*K) from host to the
