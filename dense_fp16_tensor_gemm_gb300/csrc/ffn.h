@@ -77,6 +77,10 @@ struct FfnParams {
 // Any layout, on the warp MMA.
 cudaError_t ffn_any_launch(const FfnParams& p, int num_sms, cudaStream_t stream);
 
+// The gated product with 16-bit weights on CTA pairs; X and W on the 16-byte grid.
+cudaError_t gated_pair_configure(int* max_pairs);  // one-time per device
+cudaError_t gated_pair_launch(const FfnParams& p, int max_pairs, cudaStream_t stream);
+
 // dGU = [dh u act'(g), dh act(g)]
 struct GradParams {
     const void* dh;

@@ -55,6 +55,22 @@ bool overlaps_any(const Span& a, const Span* b, int n)
 
 int shift_of(int32_t group) { return group == 32 ? 5 : (group == 64 ? 6 : 7); }
 
+// Whether tensor maps can describe X and the 16-bit weights (as two matrices, of the
+// gate and of the up rows): 16-byte aligned bases, pitches of whole 16 bytes below
+// 2^40.
+bool maps_ok(const FfnParams& p)
+{
+    const int64_t lim = int64_t(1) << 39;  // elements
+    return p.k > 0 && !p.scales && aligned(p.x, 16) && aligned(p.w, 16) && p.ldx % 8 == 0 && p.ldw % 8 == 0 &&
+           p.ldx < lim && int64_t(p.n) * p.ldw < lim;
+}
+
+bool pair_ok(const FfnParams& p, const DeviceInfo& d)
+{
+    const int64_t tiles = ((int64_t(p.tokens) + 255) / 256) * ((int64_t(p.n) + 127) / 128);
+    return p.gated && maps_ok(p) && d.gated_pairs > 0 && tiles <= INT32_MAX / 2;
+}
+
 // Selects the kernel and launches the product.
 gemm_status_t run(FfnParams& p, gemm_path_t path, cudaStream_t stream)
 {
@@ -65,8 +81,12 @@ gemm_status_t run(FfnParams& p, gemm_path_t path, cudaStream_t stream)
     p.status = d.status;
     p.wait_limit = d.wait_limit;
     p.fault = d.fault;
+    if (p.tokens == 1)
+        p.ldx = (int64_t(p.k) + 7) / 8 * 8;  // a single row's pitch is never stepped by
     if (path == GEMM_PATH_AUTO)
-        path = GEMM_PATH_MMASYNC;
+        path = pair_ok(p, d) ? GEMM_PATH_TC05_PAIR : GEMM_PATH_MMASYNC;
+    if (path == GEMM_PATH_TC05_PAIR && pair_ok(p, d))
+        return status_of(gated_pair_launch(p, d.gated_pairs, stream));
     if (path == GEMM_PATH_MMASYNC)
         return status_of(ffn_any_launch(p, d.num_sms, stream));
     return GEMM_ERR_NOT_SUPPORTED;

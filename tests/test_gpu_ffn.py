@@ -57,7 +57,7 @@ def test_gated(shape, dtype):
     gnt.gemm_nt_check()
 
 
-@pytest.mark.parametrize("path", [P.MMASYNC])
+@pytest.mark.parametrize("path", [P.MMASYNC, P.TC05_PAIR])
 @pytest.mark.parametrize("offset", [0, 8, 1])
 def test_gated_paths_and_alignments(path, offset):
     for m, k, n, dtype in ((5, 264, 72, BF16), (70, 520, 200, F16), (300, 136, 513, BF16)):
