@@ -81,6 +81,11 @@ cudaError_t ffn_any_launch(const FfnParams& p, int num_sms, cudaStream_t stream)
 cudaError_t gated_pair_configure(int* max_pairs);  // one-time per device
 cudaError_t gated_pair_launch(const FfnParams& p, int max_pairs, cudaStream_t stream);
 
+// Up to 16 tokens, on the warp MMA; rows of the weights on the 16-byte grid.
+constexpr int kFewTokens = 16;
+cudaError_t ffn_few_configure();  // one-time per device
+cudaError_t ffn_few_launch(const FfnParams& p, cudaStream_t stream);
+
 // dGU = [dh u act'(g), dh act(g)]
 struct GradParams {
     const void* dh;

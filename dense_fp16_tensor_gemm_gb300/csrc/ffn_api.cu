@@ -71,6 +71,11 @@ bool pair_ok(const FfnParams& p, const DeviceInfo& d)
     return p.gated && maps_ok(p) && d.gated_pairs > 0 && tiles <= INT32_MAX / 2;
 }
 
+bool few_ok(const FfnParams& p)
+{
+    return p.k > 0 && p.k <= (1 << 29) && p.tokens <= kFewTokens && aligned(p.w, 16) && p.ldw * (p.scales ? 1 : 2) % 16 == 0;
+}
+
 // Selects the kernel and launches the product.
 gemm_status_t run(FfnParams& p, gemm_path_t path, cudaStream_t stream)
 {
@@ -84,7 +89,9 @@ gemm_status_t run(FfnParams& p, gemm_path_t path, cudaStream_t stream)
     if (p.tokens == 1)
         p.ldx = (int64_t(p.k) + 7) / 8 * 8;  // a single row's pitch is never stepped by
     if (path == GEMM_PATH_AUTO)
-        path = pair_ok(p, d) ? GEMM_PATH_TC05_PAIR : GEMM_PATH_MMASYNC;
+        path = few_ok(p) ? GEMM_PATH_SKINNY : (pair_ok(p, d) ? GEMM_PATH_TC05_PAIR : GEMM_PATH_MMASYNC);
+    if (path == GEMM_PATH_SKINNY && few_ok(p))
+        return status_of(ffn_few_launch(p, stream));
     if (path == GEMM_PATH_TC05_PAIR && pair_ok(p, d))
         return status_of(gated_pair_launch(p, d.gated_pairs, stream));
     if (path == GEMM_PATH_MMASYNC)
