@@ -86,6 +86,12 @@ constexpr int kFewTokens = 16;
 cudaError_t ffn_few_configure();  // one-time per device
 cudaError_t ffn_few_launch(const FfnParams& p, cudaStream_t stream);
 
+// The weights as the MMA's rows; X and W on the 16-byte grid.  16-bit weights: up to
+// kSwapTokens tokens.
+constexpr int kSwapTokens = 128;
+cudaError_t ffn_swap_configure();  // one-time per device
+cudaError_t ffn_swap_launch(const FfnParams& p, int num_sms, cudaStream_t stream);
+
 // dGU = [dh u act'(g), dh act(g)]
 struct GradParams {
     const void* dh;

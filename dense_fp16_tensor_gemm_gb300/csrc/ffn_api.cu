@@ -55,25 +55,31 @@ bool overlaps_any(const Span& a, const Span* b, int n)
 
 int shift_of(int32_t group) { return group == 32 ? 5 : (group == 64 ? 6 : 7); }
 
-// Whether tensor maps can describe X and the 16-bit weights (as two matrices, of the
-// gate and of the up rows): 16-byte aligned bases, pitches of whole 16 bytes below
+// Whether tensor maps can describe X and the weights (as two matrices where gated, of
+// the gate and of the up rows): 16-byte aligned bases, pitches of whole 16 bytes below
 // 2^40.
 bool maps_ok(const FfnParams& p)
 {
-    const int64_t lim = int64_t(1) << 39;  // elements
-    return p.k > 0 && !p.scales && aligned(p.x, 16) && aligned(p.w, 16) && p.ldx % 8 == 0 && p.ldw % 8 == 0 &&
-           p.ldx < lim && int64_t(p.n) * p.ldw < lim;
+    const int64_t lim = int64_t(1) << 39;
+    return p.k > 0 && p.k <= (1 << 30) && aligned(p.x, 16) && aligned(p.w, 16) && p.ldx % 8 == 0 && p.ldw % (p.scales ? 16 : 8) == 0 &&
+           p.ldx < lim && p.ldw < lim / p.n;
 }
 
 bool pair_ok(const FfnParams& p, const DeviceInfo& d)
 {
     const int64_t tiles = ((int64_t(p.tokens) + 255) / 256) * ((int64_t(p.n) + 127) / 128);
-    return p.gated && maps_ok(p) && d.gated_pairs > 0 && tiles <= INT32_MAX / 2;
+    return p.gated && !p.scales && maps_ok(p) && d.gated_pairs > 0 && tiles <= INT32_MAX / 2;
 }
 
 bool few_ok(const FfnParams& p)
 {
     return p.k > 0 && p.k <= (1 << 29) && p.tokens <= kFewTokens && aligned(p.w, 16) && p.ldw * (p.scales ? 1 : 2) % 16 == 0;
+}
+
+bool swap_ok(const FfnParams& p)
+{
+    const int64_t tiles = ((int64_t(p.tokens) + 31) / 32) * ((int64_t(p.n) + 63) / 64);
+    return (p.scales || (p.gated && p.tokens <= kSwapTokens)) && maps_ok(p) && tiles <= INT32_MAX / 2;
 }
 
 // Selects the kernel and launches the product.
@@ -89,7 +95,12 @@ gemm_status_t run(FfnParams& p, gemm_path_t path, cudaStream_t stream)
     if (p.tokens == 1)
         p.ldx = (int64_t(p.k) + 7) / 8 * 8;  // a single row's pitch is never stepped by
     if (path == GEMM_PATH_AUTO)
-        path = few_ok(p) ? GEMM_PATH_SKINNY : (pair_ok(p, d) ? GEMM_PATH_TC05_PAIR : GEMM_PATH_MMASYNC);
+        path = few_ok(p)    ? GEMM_PATH_SKINNY
+               : swap_ok(p) ? GEMM_PATH_TC05
+               : pair_ok(p, d) ? GEMM_PATH_TC05_PAIR
+                               : GEMM_PATH_MMASYNC;
+    if (path == GEMM_PATH_TC05 && swap_ok(p))
+        return status_of(ffn_swap_launch(p, d.num_sms, stream));
     if (path == GEMM_PATH_SKINNY && few_ok(p))
         return status_of(ffn_few_launch(p, stream));
     if (path == GEMM_PATH_TC05_PAIR && pair_ok(p, d))

@@ -1,0 +1,604 @@
+// ffn_swap.cu -- gated products, and plain and gated products with 4-bit weights,
+// on tcgen05 with the weights as the MMA's 128 rows and the tokens as its columns.
+//
+// A CTA owns 128 rows of the weights by up to 256 tokens, over all of K or a
+// cluster CTA's share of it.  The accumulator's lane is a row of the weights, so a
+// warp stores neighbouring outputs of one token.  Of a gated product each 32 lanes
+// hold 16 rows of the gate and the same 16 of the up projection: g and u of an
+// output sit 16 lanes apart in one warp, and one exchange per two tokens brings
+// them together.
+//
+// 16-bit weights reach the MMA's shared memory by TMA.  4-bit ones land by TMA as
+// they lie (256 of K, 128 bytes a row, at a stage) and eight warps turn them into
+// 16-bit values (code - zero) * scale, rounded once to the tokens' type, in the
+// swizzled order the MMA reads: 128 x 64 at a time.  A `prmt` puts two neighbours'
+// bytes into the halves of a word, one logical operation turns them into small
+// whole numbers on top of 1024 (fp16) or 128 (bf16), and subtracting that plus the
+// zero is exact.  The rounding is what lets one MMA run over all groups; fewer
+// tokens than the tensor cores need take ffn_few.cu, which has none.
+//
+// Few tokens: bound by the weights' bytes, and with 4-bit weights nearly as much by
+// their conversion (8192 weights in about 150 cycles, the bytes' own time 175).
+// Many: by the tensor cores.
+//
+// Roles (512 threads): warp 0 TMA of the weights, warp 1 MMA issue, warp 2 TMA of
+// the tokens, warp 3 TMEM allocation, warps 4-11 conversion, warps 12-15 epilogue.
+// Every wait is bounded.
+#include <algorithm>
+
+#include "block128.h"
+#include "ffn.h"
+#include "gemm_nt.h"
+#include "ptx.cuh"
+#include "tc05_common.cuh"
+
+namespace gnt {
+
+namespace {
+
+using namespace tc;
+
+constexpr int kThreads = 512;
+constexpr int kRowsW = 128;                  // rows of the weights per tile
+constexpr int kABytes = kRowsW * BK * 2;     // one k-block of 16-bit weights
+constexpr int kRawK = 256;                   // K per stage of codes: 128 bytes a row
+constexpr int kRawBytes = kRowsW * kRawK / 2;
+constexpr int kRawKb = kRawK / BK;
+constexpr int kConvWarps = 8, kEpiWarps = 4;
+
+// NT: tokens per tile.
+template <bool W4, int NT>
+struct Cfg {
+    static constexpr int kXBytes = NT * BK * 2;
+    static constexpr int kStage = kABytes + kXBytes;
+    static constexpr int kRaw = W4 ? (NT == 256 ? 3 : (NT == 128 ? 4 : 6)) : 0;
+    static constexpr int kStages = W4 ? (NT == 256 ? 3 : 4) : (NT == 128 ? 6 : 8);
+    static constexpr int kSmem = 1024 + kStages * kStage + kRaw * kRawBytes + 512;
+    static constexpr int kTmem = 2 * NT;
+    static_assert(kSmem <= 232448, "shared memory budget");
+    static_assert(kStages * kStage >= kRowsW * NT * 4, "a split's sums fit the stages");
+    static_assert((3 * kStages + 2 * kRaw + 5) * 8 + 8 <= 512, "barrier area");
+};
+
+struct SwapParams {
+    FfnParams f;
+    int tiles_w, tiles_t, num_tiles, num_kb, splits;
+    uint32_t idesc;
+};
+
+__device__ __forceinline__ void fence_proxy_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+__device__ __forceinline__ uint4 lds128(uint32_t a)
+{
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ void sts128(uint32_t a, const uint32_t (&v)[4])
+{
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]) : "memory");
+}
+__device__ __forceinline__ float lds_cluster(uint32_t a)
+{
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+    return v;
+}
+
+// 8 codes of a word as 16-bit values, neighbours in one word.
+template <bool BF16>
+__device__ __forceinline__ void convert8(uint32_t word, uint32_t zero2, uint32_t scale2, uint32_t (&out)[4])
+{
+    constexpr uint32_t magic = BF16 ? 0x43004300u : 0x64006400u;
+    const uint32_t high = word >> 4;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        // bytes: word's i-th and high's i-th, each the low byte of a half
+        const uint32_t sel = static_cast<uint32_t>(i) | static_cast<uint32_t>(i) << 4 | static_cast<uint32_t>(4 + i) << 8 |
+                             static_cast<uint32_t>(4 + i) << 12;
+        const uint32_t q = (__byte_perm(word, high, sel) & 0x000f000fu) | magic;
+        if (BF16) {
+            __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&q), *reinterpret_cast<const __nv_bfloat162*>(&zero2));
+            d = __hmul2(d, *reinterpret_cast<const __nv_bfloat162*>(&scale2));
+            out[i] = *reinterpret_cast<const uint32_t*>(&d);
+        } else {
+            __half2 d = __hsub2(*reinterpret_cast<const __half2*>(&q), *reinterpret_cast<const __half2*>(&zero2));
+            d = __hmul2(d, *reinterpret_cast<const __half2*>(&scale2));
+            out[i] = *reinterpret_cast<const uint32_t*>(&d);
+        }
+    }
+}
+
+// Where a CTA's work lies: its tile's first output and first token, and its k-blocks.
+struct Piece {
+    int o0, t0, kb0, kb1;
+};
+// The i-th piece of this CTA; false if there is none.
+__device__ __forceinline__ bool piece_at(const SwapParams& p, int i, int nt, int rank, Piece& c)
+{
+    const int t = static_cast<int>(blockIdx.x) / p.splits + i * (static_cast<int>(gridDim.x) / p.splits);
+    if (t >= p.num_tiles)
+        return false;
+    // neighbouring CTAs take the token tiles of one tile of the weights
+    c.o0 = t / p.tiles_t * (p.f.gated ? kRowsW / 2 : kRowsW);
+    c.t0 = t % p.tiles_t * nt;
+    // shares of whole stages of codes
+    const int groups = (p.num_kb + kRawKb - 1) / kRawKb;
+    c.kb0 = static_cast<int>(static_cast<int64_t>(groups) * rank / p.splits) * kRawKb;
+    c.kb1 = min(p.num_kb, static_cast<int>(static_cast<int64_t>(groups) * (rank + 1) / p.splits) * kRawKb);
+    return true;
+}
+
+// One row's outputs of two tokens (plain), or one output of one token (gated).
+template <int NT>
+__device__ __forceinline__ void store_tokens(const FfnParams& p, int o0, int row, int tok0, const float (&v)[32], int lane)
+{
+    unsigned short* out = static_cast<unsigned short*>(p.out);
+    const auto bits = [&](float f) {
+        return p.bf16 ? __bfloat16_as_ushort(__float2bfloat16_rn(f)) : __half_as_ushort(__float2half_rn(f));
+    };
+    if (!p.gated) {
+        const int o = o0 + row;
+        if (o < p.n) {
+            unsigned short* dst = out + static_cast<int64_t>(tok0) * p.ldo + o;
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+                if (tok0 + j < p.tokens)
+                    *dst = bits(v[j]);
+                dst += p.ldo;
+            }
+        }
+        return;
+    }
+    const int up = lane >> 4;  // lanes 16-31 hold rows of the up projection, and store the odd tokens
+    const int o = o0 + (row >> 5) * 16 + (lane & 15);
+    if (p.gu && o < p.n) {
+        unsigned short* dst = static_cast<unsigned short*>(p.gu) + static_cast<int64_t>(tok0) * p.ldgu + o + (up ? p.n : 0);
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+            if (tok0 + j < p.tokens)
+                *dst = bits(v[j]);
+            dst += p.ldgu;
+        }
+    }
+    unsigned short* dst = out + static_cast<int64_t>(tok0 + up) * p.ldo + o;
+#pragma unroll
+    for (int j = 0; j < 32; j += 2) {
+        const float other = __shfl_xor_sync(0xffffffffu, up ? v[j] : v[j + 1], 16);
+        const float g = up ? other : v[j], u = up ? v[j + 1] : other;
+        if (o < p.n && tok0 + j + up < p.tokens)
+            *dst = bits(act_value(g, p.act) * u);
+        dst += 2 * p.ldo;
+    }
+}
+
+template <bool W4, bool BF16, int NT>
+__global__ void __launch_bounds__(kThreads, 1)
+    ffn_swap_kernel(const __grid_constant__ CUtensorMap tmw, const __grid_constant__ CUtensorMap tmx, const SwapParams p)
+{
+    using C = Cfg<W4, NT>;
+    constexpr int kStages = C::kStages, kRaw = W4 ? C::kRaw : 1;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t* as = smem;
+    uint8_t* xs = smem + kStages * kABytes;
+    uint8_t* raw = smem + kStages * C::kStage;
+    uint64_t* full = reinterpret_cast<uint64_t*>(raw + C::kRaw * kRawBytes);  // tokens (and 16-bit weights) have landed
+    uint64_t* conv = full + kStages;                                          // 4-bit weights: converted
+    uint64_t* empty = conv + kStages;
+    uint64_t* tfull = empty + kStages;
+    uint64_t* tempty = tfull + 2;
+    uint64_t* drain = tempty + 2;
+    uint64_t* raw_full = drain + 1;
+    uint64_t* raw_empty = raw_full + kRaw;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(raw_empty + kRaw);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    const int rank = static_cast<int>(cluster_ctarank());
+    const FfnParams& f = p.f;
+    const unsigned long long limit = f.wait_limit;
+    const auto gave_up = [&] {
+        *abort_flag = 1;
+        atomicOr(f.status, kStatusTimeout);
+    };
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(smem_u32(&full[s]), W4 ? 1 : 2);  // the tokens' copy, and the 16-bit weights'
+            mbar_init(smem_u32(&conv[s]), kConvWarps);
+            mbar_init(smem_u32(&empty[s]), 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(smem_u32(&tfull[b]), 1);
+            mbar_init(smem_u32(&tempty[b]), kEpiWarps);
+        }
+        mbar_init(smem_u32(drain), 1);
+        for (int s = 0; s < kRaw; ++s) {
+            mbar_init(smem_u32(&raw_full[s]), 1);
+            mbar_init(smem_u32(&raw_empty[s]), kConvWarps);
+        }
+        *abort_flag = 0;
+        fence_mbar_init();
+        tma_prefetch_map(&tmw);
+        tma_prefetch_map(&tmx);
+    }
+    if (warp == 3) {
+        tmem_alloc<C::kTmem>(smem_u32(tmem_slot));
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem_base = *tmem_slot;
+    pdl_launch_dependents();
+    pdl_wait();
+
+    // waits (bounded) until the copies last posted on each of n barriers have landed
+    const auto settle = [&](uint64_t* bars, int n, uint32_t filled, uint32_t parity) {
+        for (int s = 0; s < n; ++s) {
+            if (filled & (1u << s)) {
+                const long long t0 = clock64();
+                while (!mbar_try_wait(smem_u32(&bars[s]), (parity >> s) & 1u) &&
+                       static_cast<unsigned long long>(clock64() - t0) <= limit) {
+                }
+            }
+        }
+    };
+
+    if (warp == 0) {
+        // ------------------------------------------------------------ the weights
+        if (lane == 0) {
+            constexpr int ring = W4 ? kRaw : kStages, kbs = W4 ? kRawKb : 1, bytes = W4 ? kRawBytes : kABytes;
+            uint64_t* const fb = W4 ? raw_full : full;
+            uint64_t* const eb = W4 ? raw_empty : empty;
+            uint8_t* const base = W4 ? raw : as;
+            int s = 0;
+            uint32_t phase = 0, filled = 0, parity = 0;
+            bool first = true, ok = true;
+            Piece c;
+            for (int i = 0; ok && piece_at(p, i, NT, rank, c); ++i) {
+                for (int kb = c.kb0; kb < c.kb1; kb += kbs) {
+                    if (!wait_bounded(smem_u32(&eb[s]), phase ^ 1, abort_flag, limit)) {
+                        gave_up();
+                        ok = false;
+                        break;
+                    }
+                    const bool drop = f.fault == 1 && blockIdx.x == 0 && first;
+                    first = false;
+                    if (!drop) {
+                        const uint32_t bar = smem_u32(&fb[s]), dst = smem_u32(base + s * bytes);
+                        mbar_arrive_expect_tx(bar, bytes);
+                        filled |= 1u << s;
+                        parity = (parity & ~(1u << s)) | (phase << s);
+                        const int x = W4 ? kb * (BK / 2) : kb * BK;
+                        if (f.gated) {
+#pragma unroll 1
+                            for (int q = 0; q < 8; ++q)  // 16 rows of the gate, the same of the up projection
+                                tma_load_3d(dst + q * (bytes / 8), &tmw, bar, x, c.o0 + (q >> 1) * 16, q & 1);
+                        } else {
+                            tma_load_3d(dst, &tmw, bar, x, c.o0, 0);
+                        }
+                    }
+                    if (++s == ring) {
+                        s = 0;
+                        phase ^= 1;
+                    }
+                }
+            }
+            settle(fb, ring, filled, parity);
+        }
+    } else if (warp == 2) {
+        // ------------------------------------------------------------ the tokens
+        if (lane == 0) {
+            int s = 0;
+            uint32_t phase = 0, filled = 0, parity = 0;
+            bool ok = true;
+            Piece c;
+            for (int i = 0; ok && piece_at(p, i, NT, rank, c); ++i) {
+                for (int kb = c.kb0; kb < c.kb1; ++kb) {
+                    if (!wait_bounded(smem_u32(&empty[s]), phase ^ 1, abort_flag, limit)) {
+                        gave_up();
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t bar = smem_u32(&full[s]);
+                    mbar_arrive_expect_tx(bar, C::kXBytes);
+                    filled |= 1u << s;
+                    parity = (parity & ~(1u << s)) | (phase << s);
+                    tma_load_3d(smem_u32(xs + s * C::kXBytes), &tmx, bar, kb * BK, c.t0, 0);
+                    if (++s == kStages) {
+                        s = 0;
+                        phase ^= 1;
+                    }
+                }
+            }
+            settle(full, kStages, filled, parity);
+        }
+    } else if (warp == 1) {
+        // ------------------------------------------------------------ MMA issue
+        if (lane == 0) {
+            const DescWords da = desc_words(smem_u32(as), false), dx = desc_words(smem_u32(xs), false);
+            int s = 0;
+            uint32_t phase = 0;
+            bool skip_release = f.fault == 2 && blockIdx.x == 0;  // test hook: lose one stage release
+            bool ok = true;
+            Piece c;
+            for (int i = 0; ok && piece_at(p, i, NT, rank, c); ++i) {
+                const int buf = i & 1;
+                if (!wait_bounded(smem_u32(&tempty[buf]), ((i >> 1) & 1) ^ 1, abort_flag, limit)) {
+                    gave_up();
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t d = tmem_base + static_cast<uint32_t>(buf * NT);
+                for (int kb = c.kb0; kb < c.kb1; ++kb) {
+                    if (!wait_bounded(smem_u32(&full[s]), phase, abort_flag, limit) ||
+                        (W4 && !wait_bounded(smem_u32(&conv[s]), phase, abort_flag, limit))) {
+                        gave_up();
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t alo = da.lo + s * (kABytes >> 4), blo = dx.lo + s * (C::kXBytes >> 4);
+#pragma unroll
+                    for (int k = 0; k < BK / 16; ++k)
+                        tc_mma_w<false>(d, alo + k * da.kstep, da.hi, blo + k * dx.kstep, dx.hi, p.idesc,
+                                        (k > 0 || kb > c.kb0) ? 1u : 0u);
+                    if (!skip_release)
+                        tc_commit(smem_u32(&empty[s]));
+                    skip_release = false;
+                    if (++s == kStages) {
+                        s = 0;
+                        phase ^= 1;
+                    }
+                }
+                if (!ok)
+                    break;
+                tc_commit(smem_u32(&tfull[buf]));
+            }
+            tc_commit(smem_u32(drain));
+            const long long t0 = clock64();
+            while (!mbar_try_wait(smem_u32(drain), 0) && static_cast<unsigned long long>(clock64() - t0) <= limit) {
+            }
+        }
+    } else if (W4 && warp >= 4 && warp < 4 + kConvWarps) {
+        // ------------------------------------------------------------ 4-bit weights to 16 bits
+        // A thread converts 32 of K of one row of each k-block.
+        const int r = (threadIdx.x - 128) & 127, half = (threadIdx.x - 128) >> 7;
+        const uint32_t swz = static_cast<uint32_t>(r & 7);
+        const uint32_t raw0 = smem_u32(raw) + r * 128, a0 = smem_u32(as) + r * 128;
+        int s = 0, rs = 0;
+        uint32_t phase = 0, rphase = 0;
+        bool ok = true;
+        Piece c;
+        for (int i = 0; ok && piece_at(p, i, NT, rank, c); ++i) {
+            const int o = f.gated ? c.o0 + (r >> 5) * 16 + (r & 15) : c.o0 + r;
+            const int64_t row = o + (f.gated && (r & 16) ? static_cast<int64_t>(f.n) : 0);
+            const uint16_t* srow = o < f.n ? static_cast<const uint16_t*>(f.scales) + row * f.lds : nullptr;
+            const uint8_t* zrow = o < f.n && f.zeros ? f.zeros + row * f.ldz : nullptr;
+            // scales and zeros of a stage's four k-blocks, two stages ahead
+            const auto fetch = [&](int kb, uint32_t (&v)[kRawKb]) {
+#pragma unroll
+                for (int j = 0; j < kRawKb; ++j) {
+                    v[j] = 8u << 16;
+                    if (kb + j < c.kb1 && srow) {
+                        const int g = min((kb + j) * BK + half * 32, f.k - 1) >> f.group_shift;
+                        v[j] = __ldg(srow + g) | (zrow ? static_cast<uint32_t>(__ldg(zrow + g)) : 8u) << 16;
+                    }
+                }
+            };
+            uint32_t v0[kRawKb], v1[kRawKb], v2[kRawKb];
+            fetch(c.kb0, v0);
+            fetch(c.kb0 + kRawKb, v1);
+            for (int kb = c.kb0; ok && kb < c.kb1; kb += kRawKb) {
+                fetch(kb + 2 * kRawKb, v2);
+                if (!wait_bounded(smem_u32(&raw_full[rs]), rphase, abort_flag, limit)) {
+                    gave_up();
+                    ok = false;
+                    break;
+                }
+#pragma unroll
+                for (int j = 0; j < kRawKb; ++j) {
+                    if (kb + j >= c.kb1)
+                        break;
+                    const uint4 w = lds128(raw0 + rs * kRawBytes + (((2 * j + half) ^ swz) << 4));
+                    const uint32_t words[4] = {w.x, w.y, w.z, w.w};
+                    const uint32_t scale = __byte_perm(v0[j], 0, 0x1010);
+                    const uint32_t zero = __byte_perm((v0[j] >> 16) | (BF16 ? 0x4300u : 0x6400u), 0, 0x1010);
+                    const int left = f.k - ((kb + j) * BK + half * 32);  // elements inside K
+                    if (!wait_bounded(smem_u32(&empty[s]), phase ^ 1, abort_flag, limit)) {
+                        gave_up();
+                        ok = false;
+                        break;
+                    }
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        uint32_t out[4];
+                        convert8<BF16>(words[e], zero, scale, out);
+                        if (left < 8 * e + 8) {
+                            // past K: zeros, whatever the scale
+#pragma unroll
+                            for (int h = 0; h < 4; ++h) {
+                                const int n = left - 8 * e - 2 * h;
+                                out[h] &= n >= 2 ? 0xffffffffu : (n == 1 ? 0xffffu : 0u);
+                            }
+                        }
+                        sts128(a0 + s * kABytes + (((half * 4 + e) ^ swz) << 4), out);
+                    }
+                    fence_proxy_async();
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(smem_u32(&conv[s]));
+                    if (++s == kStages) {
+                        s = 0;
+                        phase ^= 1;
+                    }
+                }
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(smem_u32(&raw_empty[rs]));
+                if (++rs == kRaw) {
+                    rs = 0;
+                    rphase ^= 1;
+                }
+#pragma unroll
+                for (int j = 0; j < kRawKb; ++j) {
+                    v0[j] = v1[j];
+                    v1[j] = v2[j];
+                }
+            }
+        }
+    } else if (warp >= 12) {
+        // ------------------------------------------------------------ epilogue
+        const int q = warp & 3;
+        Piece c;
+        for (int i = 0; piece_at(p, i, NT, rank, c); ++i) {
+            const int buf = i & 1;
+            if (!wait_bounded(smem_u32(&tfull[buf]), (i >> 1) & 1, abort_flag, limit)) {
+                gave_up();
+                break;
+            }
+            tc_fence_after();
+            const uint32_t tacc = tmem_base + static_cast<uint32_t>(buf * NT) + (static_cast<uint32_t>(q * 32) << 16);
+#pragma unroll 1
+            for (int n = 0; n < NT; n += 32) {
+                if (c.t0 + n >= f.tokens)
+                    break;
+                uint32_t r[32];
+                tmem_ld32_wait(tacc + static_cast<uint32_t>(n), r);
+                float v[32];
+#pragma unroll
+                for (int j = 0; j < 32; ++j)
+                    v[j] = __uint_as_float(r[j]);
+                if (p.splits == 1) {
+                    store_tokens<NT>(f, c.o0, q * 32 + lane, c.t0 + n, v, lane);
+                } else {
+                    // every MMA has read its operands: the stages take the sums, [token][row]
+                    float* sums = reinterpret_cast<float*>(smem) + n * kRowsW + q * 32 + lane;
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        sums[j * kRowsW] = v[j];
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(smem_u32(&tempty[buf]));
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (p.splits > 1) {
+        // A split has one tile per cluster.  Each CTA sums 32 tokens at a time, in the CTAs' order.
+        cluster_sync();
+        Piece c;
+        if (warp >= 12 && piece_at(p, 0, NT, rank, c)) {
+            const int row = (warp & 3) * 32 + lane;
+            for (int n = rank * 32; n < NT && c.t0 + n < f.tokens; n += p.splits * 32) {
+                float v[32] = {};
+                for (int k = 0; k < p.splits; ++k) {
+                    const uint32_t at = mapa_shared(smem_u32(smem), static_cast<uint32_t>(k)) + (n * kRowsW + row) * 4;
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        v[j] += lds_cluster(at + j * (kRowsW * 4));
+                }
+                store_tokens<NT>(f, c.o0, row, c.t0 + n, v, lane);
+            }
+        }
+        cluster_sync();  // nobody leaves while its sums are read
+    }
+    if (warp == 3) {
+        tc_fence_after();
+        tmem_dealloc<C::kTmem>(tmem_base);
+    }
+}
+
+template <bool W4, bool BF16, int NT>
+cudaError_t run(const CUtensorMap* tmw, const CUtensorMap* tmx, const SwapParams* p, int grid, cudaStream_t stream)
+{
+    auto* kernel = ffn_swap_kernel<W4, BF16, NT>;
+    if (!p)
+        return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<W4, NT>::kSmem);
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = static_cast<unsigned>(p->splits);
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(grid));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = Cfg<W4, NT>::kSmem;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kernel, *tmw, *tmx, *p);
+}
+
+template <bool W4, bool BF16>
+cudaError_t by_tokens(int nt, const CUtensorMap* tmw, const CUtensorMap* tmx, const SwapParams* p, int grid,
+                      cudaStream_t stream)
+{
+    switch (nt) {
+    case 32: return run<W4, BF16, 32>(tmw, tmx, p, grid, stream);
+    case 64: return run<W4, BF16, 64>(tmw, tmx, p, grid, stream);
+    case 128: return run<W4, BF16, 128>(tmw, tmx, p, grid, stream);
+    default:
+        if constexpr (W4)
+            return run<W4, BF16, 256>(tmw, tmx, p, grid, stream);
+        else
+            return cudaErrorInvalidValue;
+    }
+}
+
+}  // namespace
+
+cudaError_t ffn_swap_configure()
+{
+    for (int nt : {32, 64, 128, 256}) {
+        cudaError_t e = by_tokens<true, true>(nt, nullptr, nullptr, nullptr, 0, nullptr);
+        if (e == cudaSuccess) e = by_tokens<true, false>(nt, nullptr, nullptr, nullptr, 0, nullptr);
+        if (e == cudaSuccess && nt < 256) e = by_tokens<false, true>(nt, nullptr, nullptr, nullptr, 0, nullptr);
+        if (e != cudaSuccess)
+            return e;
+    }
+    return cudaSuccess;
+}
+
+cudaError_t ffn_swap_launch(const FfnParams& f, int num_sms, cudaStream_t stream)
+{
+    const bool w4 = f.scales != nullptr;
+    const int dtype = f.bf16 ? GEMM_DTYPE_BF16 : GEMM_DTYPE_F16;
+    const int nt = f.tokens <= 32 ? 32 : (f.tokens <= 64 ? 64 : (f.tokens <= 128 ? 128 : 256));
+    SwapParams p{};
+    p.f = f;
+    p.tiles_w = static_cast<int>((int64_t(f.n) + (f.gated ? 63 : 127)) / (f.gated ? 64 : 128));
+    p.tiles_t = static_cast<int>((int64_t(f.tokens) + nt - 1) / nt);
+    p.num_tiles = p.tiles_w * p.tiles_t;  // (the caller's bound)
+    p.num_kb = static_cast<int>((int64_t(f.k) + BK - 1) / BK);
+    p.idesc = idesc_f16_f32(128, nt) | (f.bf16 ? (1u << 7) | (1u << 10) : 0u);
+    // Few tiles: clusters share out K, down to two stages of codes (512 of K) each.
+    p.splits = 1;
+    const int groups = (p.num_kb + kRawKb - 1) / kRawKb;
+    while (p.splits < 8 && p.num_tiles * p.splits * 2 <= num_sms && groups >= 4 * p.splits)
+        p.splits *= 2;
+    CUtensorMap tmw, tmx;
+    int unused;
+    const int box = f.gated ? 16 : 128;
+    const int64_t row_bytes = (int64_t(f.k) + 1) / 2;
+    const bool ok = w4 ? operand_map(&tmw, f.w, f.n, row_bytes, f.ldw, f.gated ? 2 : 1, int64_t(f.n) * f.ldw, box, &unused,
+                                     GEMM_DTYPE_E4M3)  // (bytes)
+                       : operand_map(&tmw, f.w, f.n, f.k, f.ldw, f.gated ? 2 : 1, int64_t(f.n) * f.ldw, box, &unused, dtype);
+    if (!ok || !operand_map(&tmx, f.x, f.tokens, f.k, f.ldx, 1, 0, nt, &unused, dtype))
+        return cudaErrorInvalidValue;
+    const int grid = p.splits > 1 ? p.num_tiles * p.splits : std::min(p.num_tiles, num_sms);
+    if (!w4)  // (the 16-bit forms differ in the instruction descriptor alone)
+        return by_tokens<false, true>(nt, &tmw, &tmx, &p, grid, stream);
+    return f.bf16 ? by_tokens<true, true>(nt, &tmw, &tmx, &p, grid, stream)
+                  : by_tokens<true, false>(nt, &tmw, &tmx, &p, grid, stream);
+}
+
+}  // namespace gnt

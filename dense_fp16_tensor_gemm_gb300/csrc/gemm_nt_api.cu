@@ -107,6 +107,7 @@ gemm_status_t device_state(DeviceState** out)
                 if (e == cudaSuccess) e = moe_configure();
                 if (e == cudaSuccess) e = gated_pair_configure(&gated_pairs);
                 if (e == cudaSuccess) e = ffn_few_configure();
+                if (e == cudaSuccess) e = ffn_swap_configure();
                 if (e != cudaSuccess)
                     return GEMM_ERR_LAUNCH;
                 d.status = static_cast<uint32_t*>(sym);

@@ -57,11 +57,11 @@ def test_gated(shape, dtype):
     gnt.gemm_nt_check()
 
 
-@pytest.mark.parametrize("path", [P.MMASYNC, P.TC05_PAIR, P.SKINNY])
+@pytest.mark.parametrize("path", [P.MMASYNC, P.TC05_PAIR, P.SKINNY, P.TC05])
 @pytest.mark.parametrize("offset", [0, 8, 1])
 def test_gated_paths_and_alignments(path, offset):
     for m, k, n, dtype in ((5, 264, 72, BF16), (70, 520, 200, F16), (300, 136, 513, BF16)):
-        m = min(m, 16) if path == P.SKINNY else m
+        m = min(m, {P.SKINNY: 16, P.TC05: 128}.get(path, m))
         g = gen(m + offset)
         x = normal(g, m, k, dtype=dtype, pitch=k + offset, offset=offset)
         w = normal(g, 2 * n, k, scale=k ** -0.5, dtype=dtype, pitch=k + offset, offset=offset)
@@ -271,8 +271,8 @@ def weights4(g, rows, k, group, zeros, dtype, pitch=0, offset=0):
 
 
 def weight_eps(tokens, dtype):
-    """How far kernels may round a weight's value: not at all for few tokens."""
-    return 0.0
+    """How far kernels may round a weight's value: not at all up to 16 tokens."""
+    return 0.0 if tokens <= 16 else EPS[dtype]
 
 
 @pytest.mark.parametrize("dtype,group,zeros", [(BF16, 128, False), (BF16, 32, True), (F16, 64, True), (F16, 128, False)])
@@ -328,6 +328,28 @@ def test_w4_alignments(offset, pitch, m):
     ref, wide = x.double() @ w.t(), x.double().abs() @ (w.abs() + 31 * s.double()[:, torch.arange(k, device="cuda") // 64]).t()
     check(gnt.linear_w4(x, q, s, z, group=64), ref,
           rounded(sum_error(wide, k) + weight_eps(m, F16) * (x.double().abs() @ w.abs().t()), ref, F16))
+    gnt.gemm_nt_check()
+
+
+@pytest.mark.parametrize("path", [P.SKINNY, P.TC05, P.MMASYNC])
+@pytest.mark.parametrize("m,k,n", [(1, 4096, 64), (4, 8192, 96), (13, 2050, 40), (40, 6000, 200), (64, 4104, 136), (257, 1000, 300),
+                                   (600, 264, 1030), (1, 32, 2000), (130, 8, 16)])
+def test_w4_paths(path, m, k, n):
+    """Every kernel, with and without a split of K."""
+    m = min(m, 16) if path == P.SKINNY else m
+    for dtype, group, zeros in ((BF16, 128, True), (F16, 32, False)):
+        g = gen(m + k)
+        x = normal(g, m, k, dtype=dtype, pitch=(k + 7) // 8 * 8)
+        q, s, z = weights4(g, 2 * n, k, group, zeros, dtype)
+        w = w4_values(q, s, z, group, k)
+        wide = w.abs() + 31 * s.double()[:, torch.arange(k, device="cuda") // group]
+        err = sum_error(x.double().abs() @ wide.t(), k) + EPS[dtype] * (path == P.TC05) * (x.double().abs() @ w.abs().t())
+        y = x.double() @ w.t()
+        check(gnt.linear_w4(x, q, s, z, group=group, path=path), y, rounded(err, y, dtype))
+        gate, up, eg, eu = y[:, :n], y[:, n:], err[:, :n], err[:, n:]
+        a, ea = act64(gate, "silu")[0], 1.13 * eg + 2.0 ** -19 * gate.abs()
+        check(gnt.gated_linear_w4(x, q, s, z, group=group, path=path), a * up,
+              rounded(ea * up.abs() + a.abs() * eu + ea * eu, a * up, dtype))
     gnt.gemm_nt_check()
 
 
