@@ -9,20 +9,24 @@
 // them together.
 //
 // 16-bit weights reach the MMA's shared memory by TMA.  4-bit ones land by TMA as
-// they lie (256 of K, 128 bytes a row, at a stage) and eight warps turn them into
-// 16-bit values (code - zero) * scale, rounded once to the tokens' type, in the
-// swizzled order the MMA reads: 128 x 64 at a time.  A `prmt` puts two neighbours'
-// bytes into the halves of a word, one logical operation turns them into small
-// whole numbers on top of 1024 (fp16) or 128 (bf16), and subtracting that plus the
-// zero is exact.  The rounding is what lets one MMA run over all groups; fewer
-// tokens than the tensor cores need take ffn_few.cu, which has none.
+// they lie (256 of K, 128 bytes a row, at a stage) and sixteen warps turn them into
+// 16-bit values (code - zero) * scale, rounded once to the tokens' type, and write
+// them to Tensor Memory, 128 x 64 at a time, from where the MMA takes its A operand:
+// that needs no shared memory and leaves room for a ring as deep as the round trip
+// conversion - MMA - release is long (from four stages in shared memory the
+// conversion and the MMAs waited for each other's signals: 64 x 16384 x 8192 65 us).
+// A `prmt` puts two neighbours' bytes into the halves of a word, one logical
+// operation turns them into small whole numbers on top of 1024 (fp16) or 128 (bf16),
+// and subtracting that plus the zero is exact.  The rounding is what lets one MMA run
+// over all groups; fewer tokens than the tensor cores need take ffn_few.cu, which has
+// none.
 //
 // Few tokens: bound by the weights' bytes, and with 4-bit weights nearly as much by
 // their conversion (8192 weights in about 150 cycles, the bytes' own time 175).
 // Many: by the tensor cores.
 //
-// Roles (512 threads): warp 0 TMA of the weights, warp 1 MMA issue, warp 2 TMA of
-// the tokens, warp 3 TMEM allocation, warps 4-11 conversion, warps 12-15 epilogue.
+// Roles (768 threads): warp 0 TMA of the weights, warp 1 MMA issue, warp 2 TMA of
+// the tokens, warp 3 TMEM allocation, warps 4-19 conversion, warps 20-23 epilogue.
 // Every wait is bounded.
 #include <algorithm>
 
@@ -38,23 +42,28 @@ namespace {
 
 using namespace tc;
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 768;
 constexpr int kRowsW = 128;                  // rows of the weights per tile
 constexpr int kABytes = kRowsW * BK * 2;     // one k-block of 16-bit weights
 constexpr int kRawK = 256;                   // K per stage of codes: 128 bytes a row
 constexpr int kRawBytes = kRowsW * kRawK / 2;
 constexpr int kRawKb = kRawK / BK;
-constexpr int kConvWarps = 8, kEpiWarps = 4;
+constexpr int kConvWarps = 8, kConvSets = 2, kEpiWarps = 4;
 
 // NT: tokens per tile.
 template <bool W4, int NT>
 struct Cfg {
     static constexpr int kXBytes = NT * BK * 2;
-    static constexpr int kStage = kABytes + kXBytes;
-    static constexpr int kRaw = W4 ? (NT == 256 ? 3 : (NT == 128 ? 4 : 6)) : 0;
-    static constexpr int kStages = W4 ? (NT == 256 ? 3 : 4) : (NT == 128 ? 6 : 8);
+    static constexpr int kStage = (W4 ? 0 : kABytes) + kXBytes;  // of shared memory
+    static constexpr int kRaw = W4 ? (NT == 256 ? 3 : (NT == 128 ? 5 : 6)) : 0;
+    static constexpr int kStages = W4 ? (NT == 256 ? 5 : (NT == 128 ? 8 : 12)) : (NT == 128 ? 6 : 8);
     static constexpr int kSmem = 1024 + kStages * kStage + kRaw * kRawBytes + 512;
-    static constexpr int kTmem = 2 * NT;
+    // Tensor Memory: the accumulators (one of 256 columns, where the converted
+    // weights leave no room for two), then 32 columns of weights a stage
+    static constexpr int kAccs = W4 && NT == 256 ? 1 : 2;
+    static constexpr int kACol = kAccs * NT;
+    static constexpr int kTmem = W4 ? 512 : 2 * NT;
+    static_assert(!W4 || kACol + 32 * kStages <= 512, "weights fit Tensor Memory");
     static_assert(kSmem <= 232448, "shared memory budget");
     static_assert(kStages * kStage >= kRowsW * NT * 4, "a split's sums fit the stages");
     static_assert((3 * kStages + 2 * kRaw + 5) * 8 + 8 <= 512, "barrier area");
@@ -63,19 +72,52 @@ struct Cfg {
 struct SwapParams {
     FfnParams f;
     int tiles_w, tiles_t, num_tiles, num_kb, splits;
+    int whole;  // gated: tiles whose outputs end here are whole boxes of the interleaved map
     uint32_t idesc;
 };
 
-__device__ __forceinline__ void fence_proxy_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.b32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
 __device__ __forceinline__ uint4 lds128(uint32_t a)
 {
     uint4 v;
     asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
     return v;
 }
-__device__ __forceinline__ void sts128(uint32_t a, const uint32_t (&v)[4])
+// 32 lanes x 16 columns of 32 bits, from 16 registers of each thread, and the wait for it.
+__device__ __forceinline__ void tmem_st16_wait(uint32_t taddr, const uint32_t (&r)[16])
 {
-    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]) : "memory");
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};\n\t"
+        "tcgen05.wait::st.sync.aligned;" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+// D[tmem] (+)= A[tmem] * B[smem desc]^T, 16-bit operands: row i of A is lane i, two
+// neighbours of K a column.
+__device__ __forceinline__ void tc_mma_ta(uint32_t d, uint32_t a, uint32_t blo, uint32_t bhi, uint32_t idesc, uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 db;\n\t"
+        "setp.ne.b32 p, %5, 0;\n\t"
+        "mov.b64 db, {%2, %3};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %4, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(blo), "r"(bhi), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int32_t c0, int32_t c1,
+                                            int32_t c2, int32_t c3)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+        : "memory");
 }
 __device__ __forceinline__ float lds_cluster(uint32_t a)
 {
@@ -86,7 +128,7 @@ __device__ __forceinline__ float lds_cluster(uint32_t a)
 
 // 8 codes of a word as 16-bit values, neighbours in one word.
 template <bool BF16>
-__device__ __forceinline__ void convert8(uint32_t word, uint32_t zero2, uint32_t scale2, uint32_t (&out)[4])
+__device__ __forceinline__ void convert8(uint32_t word, uint32_t zero2, uint32_t scale2, uint32_t* out)
 {
     constexpr uint32_t magic = BF16 ? 0x43004300u : 0x64006400u;
     const uint32_t high = word >> 4;
@@ -173,14 +215,15 @@ __device__ __forceinline__ void store_tokens(const FfnParams& p, int o0, int row
 
 template <bool W4, bool BF16, int NT>
 __global__ void __launch_bounds__(kThreads, 1)
-    ffn_swap_kernel(const __grid_constant__ CUtensorMap tmw, const __grid_constant__ CUtensorMap tmx, const SwapParams p)
+    ffn_swap_kernel(const __grid_constant__ CUtensorMap tmw, const __grid_constant__ CUtensorMap tmi,
+                    const __grid_constant__ CUtensorMap tmx, const SwapParams p)
 {
     using C = Cfg<W4, NT>;
     constexpr int kStages = C::kStages, kRaw = W4 ? C::kRaw : 1;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* as = smem;
-    uint8_t* xs = smem + kStages * kABytes;
+    uint8_t* xs = smem + (W4 ? 0 : kStages * kABytes);
     uint8_t* raw = smem + kStages * C::kStage;
     uint64_t* full = reinterpret_cast<uint64_t*>(raw + C::kRaw * kRawBytes);  // tokens (and 16-bit weights) have landed
     uint64_t* conv = full + kStages;                                          // 4-bit weights: converted
@@ -272,7 +315,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                         filled |= 1u << s;
                         parity = (parity & ~(1u << s)) | (phase << s);
                         const int x = W4 ? kb * (BK / 2) : kb * BK;
-                        if (f.gated) {
+                        if (f.gated && c.o0 + kRowsW / 2 <= p.whole) {
+                            // (eight boxes a stage held 64 tokens x 2048 x 8192 to 24.0 us, one 18)
+                            tma_load_4d(dst, &tmi, bar, x, 0, 0, c.o0 / 16);
+                        } else if (f.gated) {
+                            // the last tile, where it ends inside 16 rows
 #pragma unroll 1
                             for (int q = 0; q < 8; ++q)  // 16 rows of the gate, the same of the up projection
                                 tma_load_3d(dst + q * (bytes / 8), &tmw, bar, x, c.o0 + (q >> 1) * 16, q & 1);
@@ -317,7 +364,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMA issue
-        if (lane == 0) {
+        // The whole warp walks the loop and one lane issues: addresses and descriptors
+        // then stay in uniform registers, where the instructions want them.
+        {
+            const bool one = elect_one();
             const DescWords da = desc_words(smem_u32(as), false), dx = desc_words(smem_u32(xs), false);
             int s = 0;
             uint32_t phase = 0;
@@ -325,8 +375,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             bool ok = true;
             Piece c;
             for (int i = 0; ok && piece_at(p, i, NT, rank, c); ++i) {
-                const int buf = i & 1;
-                if (!wait_bounded(smem_u32(&tempty[buf]), ((i >> 1) & 1) ^ 1, abort_flag, limit)) {
+                const int buf = i % C::kAccs;
+                if (!wait_bounded(smem_u32(&tempty[buf]), ((i / C::kAccs) & 1) ^ 1, abort_flag, limit)) {
                     gave_up();
                     break;
                 }
@@ -341,12 +391,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     tc_fence_after();
                     const uint32_t alo = da.lo + s * (kABytes >> 4), blo = dx.lo + s * (C::kXBytes >> 4);
+                    if (one) {
 #pragma unroll
-                    for (int k = 0; k < BK / 16; ++k)
-                        tc_mma_w<false>(d, alo + k * da.kstep, da.hi, blo + k * dx.kstep, dx.hi, p.idesc,
-                                        (k > 0 || kb > c.kb0) ? 1u : 0u);
-                    if (!skip_release)
-                        tc_commit(smem_u32(&empty[s]));
+                        for (int k = 0; k < BK / 16; ++k) {
+                            const uint32_t more = (k > 0 || kb > c.kb0) ? 1u : 0u;
+                            if (W4)
+                                tc_mma_ta(d, tmem_base + C::kACol + 32 * s + 8 * k, blo + k * dx.kstep, dx.hi, p.idesc, more);
+                            else
+                                tc_mma_w<false>(d, alo + k * da.kstep, da.hi, blo + k * dx.kstep, dx.hi, p.idesc, more);
+                        }
+                        if (!skip_release)
+                            tc_commit(smem_u32(&empty[s]));
+                    }
+                    __syncwarp();
                     skip_release = false;
                     if (++s == kStages) {
                         s = 0;
@@ -355,84 +412,106 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 if (!ok)
                     break;
-                tc_commit(smem_u32(&tfull[buf]));
+                if (one)
+                    tc_commit(smem_u32(&tfull[buf]));
+                __syncwarp();
             }
-            tc_commit(smem_u32(drain));
+            if (one)
+                tc_commit(smem_u32(drain));
+            __syncwarp();
             const long long t0 = clock64();
             while (!mbar_try_wait(smem_u32(drain), 0) && static_cast<unsigned long long>(clock64() - t0) <= limit) {
             }
         }
-    } else if (W4 && warp >= 4 && warp < 4 + kConvWarps) {
+    } else if (W4 && warp >= 4 && warp < 4 + kConvSets * kConvWarps) {
         // ------------------------------------------------------------ 4-bit weights to 16 bits
         // A thread converts 32 of K of one row of each k-block.
-        const int r = (threadIdx.x - 128) & 127, half = (threadIdx.x - 128) >> 7;
+        // Two sets of eight warps take the stages in turns.
+        const int r = (threadIdx.x - 128) & 127, half = ((threadIdx.x - 128) >> 7) & 1, set = (threadIdx.x - 128) >> 8;
         const uint32_t swz = static_cast<uint32_t>(r & 7);
-        const uint32_t raw0 = smem_u32(raw) + r * 128, a0 = smem_u32(as) + r * 128;
-        int s = 0, rs = 0;
+        const uint32_t raw0 = smem_u32(raw) + r * 128;
+        const uint32_t a0 = tmem_base + C::kACol + 16 * half + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+        int s = 0, rs = 0, turn = 0;
         uint32_t phase = 0, rphase = 0;
         bool ok = true;
+        // over one stage's k-blocks (n of them)
+        const auto next = [&](int n) {
+            s += n;
+            if (s >= kStages) {
+                s -= kStages;
+                phase ^= 1;
+            }
+        };
         Piece c;
         for (int i = 0; ok && piece_at(p, i, NT, rank, c); ++i) {
             const int o = f.gated ? c.o0 + (r >> 5) * 16 + (r & 15) : c.o0 + r;
             const int64_t row = o + (f.gated && (r & 16) ? static_cast<int64_t>(f.n) : 0);
-            const uint16_t* srow = o < f.n ? static_cast<const uint16_t*>(f.scales) + row * f.lds : nullptr;
-            const uint8_t* zrow = o < f.n && f.zeros ? f.zeros + row * f.ldz : nullptr;
-            // scales and zeros of a stage's four k-blocks, two stages ahead
-            const auto fetch = [&](int kb, uint32_t (&v)[kRawKb]) {
+            // (rows past the weights are converted with the last one's scales and not stored)
+            const int64_t at = o < f.n ? row : static_cast<int64_t>(f.n) - 1;
+            const uint16_t* srow = static_cast<const uint16_t*>(f.scales) + at * f.lds;
+            const uint8_t* zrow = f.zeros ? f.zeros + at * f.ldz : nullptr;
+            // scales and zeros of a stage's four k-blocks, fetched four stages ahead: nothing
+            // is done with them here that would have to wait for them
+            const auto fetch = [&](int kb, uint32_t (&v)[kRawKb], uint32_t (&z)[kRawKb]) {
 #pragma unroll
                 for (int j = 0; j < kRawKb; ++j) {
-                    v[j] = 8u << 16;
-                    if (kb + j < c.kb1 && srow) {
-                        const int g = min((kb + j) * BK + half * 32, f.k - 1) >> f.group_shift;
-                        v[j] = __ldg(srow + g) | (zrow ? static_cast<uint32_t>(__ldg(zrow + g)) : 8u) << 16;
-                    }
+                    const int g = min((kb + j) * BK + half * 32, f.k - 1) >> f.group_shift;
+                    v[j] = __ldg(srow + g);
+                    z[j] = 8;
+                    if (zrow)
+                        z[j] = __ldg(zrow + g);
                 }
             };
-            uint32_t v0[kRawKb], v1[kRawKb], v2[kRawKb];
-            fetch(c.kb0, v0);
-            fetch(c.kb0 + kRawKb, v1);
-            for (int kb = c.kb0; ok && kb < c.kb1; kb += kRawKb) {
-                fetch(kb + 2 * kRawKb, v2);
+            int kb = c.kb0;
+            // one stage, whose scales and zeros are in v and z; false at the piece's end or after a wait that ran out
+            const auto stage = [&](uint32_t (&v)[kRawKb], uint32_t (&z)[kRawKb]) {
+                if (kb < c.kb1 && turn != set) {  // the other set's
+                    next(min(kRawKb, c.kb1 - kb));
+                    if (++rs == kRaw) {
+                        rs = 0;
+                        rphase ^= 1;
+                    }
+                    kb += kRawKb;
+                    turn ^= 1;
+                }
+                if (kb >= c.kb1)
+                    return false;
+                turn ^= 1;
                 if (!wait_bounded(smem_u32(&raw_full[rs]), rphase, abort_flag, limit)) {
                     gave_up();
                     ok = false;
-                    break;
+                    return false;
                 }
 #pragma unroll
                 for (int j = 0; j < kRawKb; ++j) {
-                    if (kb + j >= c.kb1)
-                        break;
-                    const uint4 w = lds128(raw0 + rs * kRawBytes + (((2 * j + half) ^ swz) << 4));
-                    const uint32_t words[4] = {w.x, w.y, w.z, w.w};
-                    const uint32_t scale = __byte_perm(v0[j], 0, 0x1010);
-                    const uint32_t zero = __byte_perm((v0[j] >> 16) | (BF16 ? 0x4300u : 0x6400u), 0, 0x1010);
-                    const int left = f.k - ((kb + j) * BK + half * 32);  // elements inside K
-                    if (!wait_bounded(smem_u32(&empty[s]), phase ^ 1, abort_flag, limit)) {
-                        gave_up();
-                        ok = false;
-                        break;
-                    }
+                    if (kb + j < c.kb1) {
+                        const uint4 w = lds128(raw0 + rs * kRawBytes + (((2 * j + half) ^ swz) << 4));
+                        const uint32_t words[4] = {w.x, w.y, w.z, w.w};
+                        const uint32_t scale = __byte_perm(v[j], 0, 0x1010);
+                        const uint32_t zero = __byte_perm(z[j] | (BF16 ? 0x4300u : 0x6400u), 0, 0x1010);
+                        uint32_t out[16];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        uint32_t out[4];
-                        convert8<BF16>(words[e], zero, scale, out);
-                        if (left < 8 * e + 8) {
+                        for (int e = 0; e < 4; ++e)
+                            convert8<BF16>(words[e], zero, scale, out + 4 * e);
+                        const int left = f.k - ((kb + j) * BK + half * 32);  // elements inside K
+                        if (left < 32) {
                             // past K: zeros, whatever the scale
 #pragma unroll
-                            for (int h = 0; h < 4; ++h) {
-                                const int n = left - 8 * e - 2 * h;
-                                out[h] &= n >= 2 ? 0xffffffffu : (n == 1 ? 0xffffu : 0u);
-                            }
+                            for (int h = 0; h < 16; ++h)
+                                out[h] &= left - 2 * h >= 2 ? 0xffffffffu : (left - 2 * h == 1 ? 0xffffu : 0u);
                         }
-                        sts128(a0 + s * kABytes + (((half * 4 + e) ^ swz) << 4), out);
-                    }
-                    fence_proxy_async();
-                    __syncwarp();
-                    if (lane == 0)
-                        mbar_arrive(smem_u32(&conv[s]));
-                    if (++s == kStages) {
-                        s = 0;
-                        phase ^= 1;
+                        if (!wait_bounded(smem_u32(&empty[s]), phase ^ 1, abort_flag, limit)) {
+                            gave_up();
+                            ok = false;
+                            return false;
+                        }
+                        tc_fence_after();
+                        tmem_st16_wait(a0 + 32 * s, out);
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0)
+                            mbar_arrive(smem_u32(&conv[s]));
+                        next(1);
                     }
                 }
                 __syncwarp();
@@ -442,20 +521,24 @@ __global__ void __launch_bounds__(kThreads, 1)
                     rs = 0;
                     rphase ^= 1;
                 }
+                fetch(kb + 2 * kRawKb * kConvSets, v, z);
+                kb += kRawKb;
+                return true;
+            };
+            uint32_t v[2][kRawKb], z[2][kRawKb];
 #pragma unroll
-                for (int j = 0; j < kRawKb; ++j) {
-                    v0[j] = v1[j];
-                    v1[j] = v2[j];
-                }
+            for (int j = 0; j < 2; ++j)
+                fetch(kb + (j * kConvSets + (turn != set)) * kRawKb, v[j], z[j]);
+            while (stage(v[0], z[0]) && stage(v[1], z[1])) {
             }
         }
-    } else if (warp >= 12) {
+    } else if (warp >= 20) {
         // ------------------------------------------------------------ epilogue
         const int q = warp & 3;
         Piece c;
         for (int i = 0; piece_at(p, i, NT, rank, c); ++i) {
-            const int buf = i & 1;
-            if (!wait_bounded(smem_u32(&tfull[buf]), (i >> 1) & 1, abort_flag, limit)) {
+            const int buf = i % C::kAccs;
+            if (!wait_bounded(smem_u32(&tfull[buf]), (i / C::kAccs) & 1, abort_flag, limit)) {
                 gave_up();
                 break;
             }
@@ -494,7 +577,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // A split has one tile per cluster.  Each CTA sums 32 tokens at a time, in the CTAs' order.
         cluster_sync();
         Piece c;
-        if (warp >= 12 && piece_at(p, 0, NT, rank, c)) {
+        if (warp >= 20 && piece_at(p, 0, NT, rank, c)) {
             const int row = (warp & 3) * 32 + lane;
             for (int n = rank * 32; n < NT && c.t0 + n < f.tokens; n += p.splits * 32) {
                 float v[32] = {};
@@ -516,7 +599,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 template <bool W4, bool BF16, int NT>
-cudaError_t run(const CUtensorMap* tmw, const CUtensorMap* tmx, const SwapParams* p, int grid, cudaStream_t stream)
+cudaError_t run(const CUtensorMap* maps, const SwapParams* p, int grid, cudaStream_t stream)
 {
     auto* kernel = ffn_swap_kernel<W4, BF16, NT>;
     if (!p)
@@ -535,20 +618,19 @@ cudaError_t run(const CUtensorMap* tmw, const CUtensorMap* tmx, const SwapParams
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, kernel, *tmw, *tmx, *p);
+    return cudaLaunchKernelEx(&cfg, kernel, maps[0], maps[1], maps[2], *p);
 }
 
 template <bool W4, bool BF16>
-cudaError_t by_tokens(int nt, const CUtensorMap* tmw, const CUtensorMap* tmx, const SwapParams* p, int grid,
-                      cudaStream_t stream)
+cudaError_t by_tokens(int nt, const CUtensorMap* maps, const SwapParams* p, int grid, cudaStream_t stream)
 {
     switch (nt) {
-    case 32: return run<W4, BF16, 32>(tmw, tmx, p, grid, stream);
-    case 64: return run<W4, BF16, 64>(tmw, tmx, p, grid, stream);
-    case 128: return run<W4, BF16, 128>(tmw, tmx, p, grid, stream);
+    case 32: return run<W4, BF16, 32>(maps, p, grid, stream);
+    case 64: return run<W4, BF16, 64>(maps, p, grid, stream);
+    case 128: return run<W4, BF16, 128>(maps, p, grid, stream);
     default:
         if constexpr (W4)
-            return run<W4, BF16, 256>(tmw, tmx, p, grid, stream);
+            return run<W4, BF16, 256>(maps, p, grid, stream);
         else
             return cudaErrorInvalidValue;
     }
@@ -559,9 +641,9 @@ cudaError_t by_tokens(int nt, const CUtensorMap* tmw, const CUtensorMap* tmx, co
 cudaError_t ffn_swap_configure()
 {
     for (int nt : {32, 64, 128, 256}) {
-        cudaError_t e = by_tokens<true, true>(nt, nullptr, nullptr, nullptr, 0, nullptr);
-        if (e == cudaSuccess) e = by_tokens<true, false>(nt, nullptr, nullptr, nullptr, 0, nullptr);
-        if (e == cudaSuccess && nt < 256) e = by_tokens<false, true>(nt, nullptr, nullptr, nullptr, 0, nullptr);
+        cudaError_t e = by_tokens<true, true>(nt, nullptr, nullptr, 0, nullptr);
+        if (e == cudaSuccess) e = by_tokens<true, false>(nt, nullptr, nullptr, 0, nullptr);
+        if (e == cudaSuccess && nt < 256) e = by_tokens<false, true>(nt, nullptr, nullptr, 0, nullptr);
         if (e != cudaSuccess)
             return e;
     }
@@ -585,20 +667,24 @@ cudaError_t ffn_swap_launch(const FfnParams& f, int num_sms, cudaStream_t stream
     const int groups = (p.num_kb + kRawKb - 1) / kRawKb;
     while (p.splits < 8 && p.num_tiles * p.splits * 2 <= num_sms && groups >= 4 * p.splits)
         p.splits *= 2;
-    CUtensorMap tmw, tmx;
+    // the weights (the gate's and the up rows apart), the same in turns of 16 rows, the tokens
+    CUtensorMap maps[3];
     int unused;
-    const int box = f.gated ? 16 : 128;
-    const int64_t row_bytes = (int64_t(f.k) + 1) / 2;
-    const bool ok = w4 ? operand_map(&tmw, f.w, f.n, row_bytes, f.ldw, f.gated ? 2 : 1, int64_t(f.n) * f.ldw, box, &unused,
-                                     GEMM_DTYPE_E4M3)  // (bytes)
-                       : operand_map(&tmw, f.w, f.n, f.k, f.ldw, f.gated ? 2 : 1, int64_t(f.n) * f.ldw, box, &unused, dtype);
-    if (!ok || !operand_map(&tmx, f.x, f.tokens, f.k, f.ldx, 1, 0, nt, &unused, dtype))
+    const int64_t width = w4 ? (int64_t(f.k) + 1) / 2 : f.k;
+    const int wtype = w4 ? GEMM_DTYPE_E4M3 : dtype;  // (codes: bytes)
+    if (!operand_map(&maps[0], f.w, f.n, width, f.ldw, f.gated ? 2 : 1, int64_t(f.n) * f.ldw, f.gated ? 16 : 128, &unused, wtype) ||
+        !operand_map(&maps[2], f.x, f.tokens, f.k, f.ldx, 1, 0, nt, &unused, dtype))
         return cudaErrorInvalidValue;
+    maps[1] = maps[0];
+    if (f.gated && f.n >= 64) {
+        if (!interleaved_map(&maps[1], f.w, f.n, width, f.ldw, wtype))
+            return cudaErrorInvalidValue;
+        p.whole = f.n % 16 == 0 ? (f.n + 63) / 64 * 64 : f.n;
+    }
     const int grid = p.splits > 1 ? p.num_tiles * p.splits : std::min(p.num_tiles, num_sms);
     if (!w4)  // (the 16-bit forms differ in the instruction descriptor alone)
-        return by_tokens<false, true>(nt, &tmw, &tmx, &p, grid, stream);
-    return f.bf16 ? by_tokens<true, true>(nt, &tmw, &tmx, &p, grid, stream)
-                  : by_tokens<true, false>(nt, &tmw, &tmx, &p, grid, stream);
+        return by_tokens<false, true>(nt, maps, &p, grid, stream);
+    return f.bf16 ? by_tokens<true, true>(nt, maps, &p, grid, stream) : by_tokens<true, false>(nt, maps, &p, grid, stream);
 }
 
 }  // namespace gnt

@@ -1071,6 +1071,29 @@ bool operand_map(CUtensorMap* map, const void* base, int64_t rows, int64_t K, in
     return make_map(map, base, rows, K, ld, batch, stride, box_rows, bmul, dtype);
 }
 
+// Gate and up rows of a gated product's weights in turns of 16, as a 4-D tensor
+// {K, 16 rows, gate or up, block of 16 rows}: a box {128 bytes of K, 16, 2, 4} is 128
+// rows of an operand tile.  Whole blocks only: a box that reaches past them would read
+// the up projection's end.
+bool interleaved_map(CUtensorMap* map, const void* base, int64_t n, int64_t K, int64_t ld, int dtype)
+{
+    auto enc = encode_fn();
+    if (!enc || n < 16)
+        return false;
+    const bool bytes = dtype == GEMM_DTYPE_E4M3;
+    const int64_t esize = bytes ? 1 : 2;
+    cuuint64_t dims[4] = {static_cast<cuuint64_t>(K), 16, 2, static_cast<cuuint64_t>(n / 16)};
+    cuuint64_t strides[3] = {static_cast<cuuint64_t>(ld * esize), static_cast<cuuint64_t>(n * ld * esize),
+                             static_cast<cuuint64_t>(16 * ld * esize)};
+    cuuint32_t box[4] = {static_cast<cuuint32_t>(128 / esize), 16, 2, 4};
+    cuuint32_t estr[4] = {1, 1, 1, 1};
+    return enc(map, bytes ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                          : (dtype == GEMM_DTYPE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16),
+               4, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // The CTA-pair kernel with its split scratch taken from memory the caller of
 // this function owns (no allocation): arguments are checked before any CUDA
 // call, then `scratch` gives the current device's fixed scratch, and the work

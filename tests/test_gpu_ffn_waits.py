@@ -38,8 +38,8 @@ def test_a_lost_stage_is_reported(path, tokens, fault):
 def test_a_lost_stage_of_codes_is_reported(tokens, rows, fault):
     g = torch.Generator(device="cuda")
     g.manual_seed(fault)
-    x = torch.randn(tokens, 4096, generator=g, device="cuda").half()
-    q, s = gnt.quantize_w4(torch.randn(rows, 4096, generator=g, device="cuda") / 64, scale_dtype=torch.half)
+    x = torch.randn(tokens, 16384, generator=g, device="cuda").half()  # an eighth of K is longer than the ring
+    q, s = gnt.quantize_w4(torch.randn(rows, 16384, generator=g, device="cuda") / 128, scale_dtype=torch.half)
     good = gnt.linear_w4(x, q, s, path=gnt.Path.TC05)
     gnt.gemm_nt_check()
     gnt.gemm_nt_debug_set_wait_limit(20_000_000)
