@@ -53,20 +53,26 @@ constexpr int kConvWarps = 8, kConvSets = 2, kEpiWarps = 4;
 // NT: tokens per tile.
 template <bool W4, int NT>
 struct Cfg {
-    static constexpr int kXBytes = NT * BK * 2;
-    static constexpr int kStage = (W4 ? 0 : kABytes) + kXBytes;  // of shared memory
+    // k-blocks per stage.  A wait that finds its barrier done still takes the MMA warp
+    // about 135 cycles and a commit 60, while the four MMAs of a k-block run 127 at 64
+    // tokens, 254 at 128 and 508 at 256: two k-blocks share one wait and one commit,
+    // but for 256 tokens.
+    static constexpr int kKb = NT == 256 ? 1 : 2;
+    static constexpr int kXBytes = NT * BK * 2;                            // of one k-block
+    static constexpr int kStage = kKb * ((W4 ? 0 : kABytes) + kXBytes);  // of shared memory
     static constexpr int kRaw = W4 ? (NT == 256 ? 3 : (NT == 128 ? 5 : 6)) : 0;
-    static constexpr int kStages = W4 ? (NT == 256 ? 5 : (NT == 128 ? 8 : 12)) : (NT == 128 ? 6 : 8);
+    static constexpr int kStages = W4 ? (NT == 256 ? 5 : (NT == 128 ? 4 : 6)) : (NT == 128 ? 3 : 4);
     static constexpr int kSmem = 1024 + kStages * kStage + kRaw * kRawBytes + 512;
     // Tensor Memory: the accumulators (one of 256 columns, where the converted
     // weights leave no room for two), then 32 columns of weights a stage
     static constexpr int kAccs = W4 && NT == 256 ? 1 : 2;
     static constexpr int kACol = kAccs * NT;
     static constexpr int kTmem = W4 ? 512 : 2 * NT;
-    static_assert(!W4 || kACol + 32 * kStages <= 512, "weights fit Tensor Memory");
+    static_assert(!W4 || kACol + 32 * kKb * kStages <= 512, "weights fit Tensor Memory");
     static_assert(kSmem <= 232448, "shared memory budget");
     static_assert(kStages * kStage >= kRowsW * NT * 4, "a split's sums fit the stages");
-    static_assert((3 * kStages + 2 * kRaw + 5) * 8 + 8 <= 512, "barrier area");
+    static_assert((2 * kStages + 2 * kRaw + 5) * 8 + 8 <= 512, "barrier area");
+    static_assert(kRawKb % kKb == 0, "stages of codes are whole stages");
 };
 
 struct SwapParams {
@@ -88,16 +94,17 @@ __device__ __forceinline__ uint4 lds128(uint32_t a)
     asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
     return v;
 }
-// 32 lanes x 16 columns of 32 bits, from 16 registers of each thread, and the wait for it.
-__device__ __forceinline__ void tmem_st16_wait(uint32_t taddr, const uint32_t (&r)[16])
+// 32 lanes x 16 columns of 32 bits, from 16 registers of each thread.
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16])
 {
     asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};\n\t"
-        "tcgen05.wait::st.sync.aligned;" ::"r"(taddr),
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(
+            taddr),
         "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
         "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
         : "memory");
 }
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 // D[tmem] (+)= A[tmem] * B[smem desc]^T, 16-bit operands: row i of A is lane i, two
 // neighbours of K a column.
 __device__ __forceinline__ void tc_mma_ta(uint32_t d, uint32_t a, uint32_t blo, uint32_t bhi, uint32_t idesc, uint32_t accumulate)
@@ -223,11 +230,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* as = smem;
-    uint8_t* xs = smem + (W4 ? 0 : kStages * kABytes);
+    uint8_t* xs = smem + (W4 ? 0 : kStages * C::kKb * kABytes);
     uint8_t* raw = smem + kStages * C::kStage;
-    uint64_t* full = reinterpret_cast<uint64_t*>(raw + C::kRaw * kRawBytes);  // tokens (and 16-bit weights) have landed
-    uint64_t* conv = full + kStages;                                          // 4-bit weights: converted
-    uint64_t* empty = conv + kStages;
+    uint64_t* full = reinterpret_cast<uint64_t*>(raw + C::kRaw * kRawBytes);  // tokens have landed, weights have or are converted
+    uint64_t* empty = full + kStages;
     uint64_t* tfull = empty + kStages;
     uint64_t* tempty = tfull + 2;
     uint64_t* drain = tempty + 2;
@@ -248,8 +254,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
-            mbar_init(smem_u32(&full[s]), W4 ? 1 : 2);  // the tokens' copy, and the 16-bit weights'
-            mbar_init(smem_u32(&conv[s]), kConvWarps);
+            mbar_init(smem_u32(&full[s]), 1 + (W4 ? kConvWarps : 1));  // the tokens' copy, and the weights' or their conversion
             mbar_init(smem_u32(&empty[s]), 1);
         }
         for (int b = 0; b < 2; ++b) {
@@ -292,7 +297,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 0) {
         // ------------------------------------------------------------ the weights
         if (lane == 0) {
-            constexpr int ring = W4 ? kRaw : kStages, kbs = W4 ? kRawKb : 1, bytes = W4 ? kRawBytes : kABytes;
+            constexpr int ring = W4 ? kRaw : kStages, kbs = W4 ? kRawKb : C::kKb, bytes = W4 ? kRawBytes : kABytes;
             uint64_t* const fb = W4 ? raw_full : full;
             uint64_t* const eb = W4 ? raw_empty : empty;
             uint8_t* const base = W4 ? raw : as;
@@ -310,21 +315,25 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const bool drop = f.fault == 1 && blockIdx.x == 0 && first;
                     first = false;
                     if (!drop) {
-                        const uint32_t bar = smem_u32(&fb[s]), dst = smem_u32(base + s * bytes);
-                        mbar_arrive_expect_tx(bar, bytes);
+                        const uint32_t bar = smem_u32(&fb[s]);
+                        const int n = W4 ? 1 : min(kbs, c.kb1 - kb);
+                        mbar_arrive_expect_tx(bar, n * bytes);
                         filled |= 1u << s;
                         parity = (parity & ~(1u << s)) | (phase << s);
-                        const int x = W4 ? kb * (BK / 2) : kb * BK;
-                        if (f.gated && c.o0 + kRowsW / 2 <= p.whole) {
-                            // (eight boxes a stage held 64 tokens x 2048 x 8192 to 24.0 us, one 18)
-                            tma_load_4d(dst, &tmi, bar, x, 0, 0, c.o0 / 16);
-                        } else if (f.gated) {
-                            // the last tile, where it ends inside 16 rows
+                        for (int b = 0; b < n; ++b) {
+                            const uint32_t dst = smem_u32(base) + (W4 ? s : s * kbs + b) * bytes;
+                            const int x = W4 ? kb * (BK / 2) : (kb + b) * BK;
+                            if (f.gated && c.o0 + kRowsW / 2 <= p.whole) {
+                                // (eight boxes a k-block held 64 tokens x 2048 x 8192 to 24.0 us, one 18)
+                                tma_load_4d(dst, &tmi, bar, x, 0, 0, c.o0 / 16);
+                            } else if (f.gated) {
+                                // the last tile, where it ends inside 16 rows
 #pragma unroll 1
-                            for (int q = 0; q < 8; ++q)  // 16 rows of the gate, the same of the up projection
-                                tma_load_3d(dst + q * (bytes / 8), &tmw, bar, x, c.o0 + (q >> 1) * 16, q & 1);
-                        } else {
-                            tma_load_3d(dst, &tmw, bar, x, c.o0, 0);
+                                for (int q = 0; q < 8; ++q)  // 16 rows of the gate, the same of the up projection
+                                    tma_load_3d(dst + q * (bytes / 8), &tmw, bar, x, c.o0 + (q >> 1) * 16, q & 1);
+                            } else {
+                                tma_load_3d(dst, &tmw, bar, x, c.o0, 0);
+                            }
                         }
                     }
                     if (++s == ring) {
@@ -343,17 +352,19 @@ __global__ void __launch_bounds__(kThreads, 1)
             bool ok = true;
             Piece c;
             for (int i = 0; ok && piece_at(p, i, NT, rank, c); ++i) {
-                for (int kb = c.kb0; kb < c.kb1; ++kb) {
+                for (int kb = c.kb0; kb < c.kb1; kb += C::kKb) {
                     if (!wait_bounded(smem_u32(&empty[s]), phase ^ 1, abort_flag, limit)) {
                         gave_up();
                         ok = false;
                         break;
                     }
                     const uint32_t bar = smem_u32(&full[s]);
-                    mbar_arrive_expect_tx(bar, C::kXBytes);
+                    const int n = min(C::kKb, c.kb1 - kb);
+                    mbar_arrive_expect_tx(bar, n * C::kXBytes);
                     filled |= 1u << s;
                     parity = (parity & ~(1u << s)) | (phase << s);
-                    tma_load_3d(smem_u32(xs + s * C::kXBytes), &tmx, bar, kb * BK, c.t0, 0);
+                    for (int b = 0; b < n; ++b)
+                        tma_load_3d(smem_u32(xs + (s * C::kKb + b) * C::kXBytes), &tmx, bar, (kb + b) * BK, c.t0, 0);
                     if (++s == kStages) {
                         s = 0;
                         phase ^= 1;
@@ -365,7 +376,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMA issue
         // The whole warp walks the loop and one lane issues: addresses and descriptors
-        // then stay in uniform registers, where the instructions want them.
+        // then stay in uniform registers, where the instructions want them (a loop of one
+        // thread issues an MMA every 56 cycles, this one every 32 or less).
         {
             const bool one = elect_one();
             const DescWords da = desc_words(smem_u32(as), false), dx = desc_words(smem_u32(xs), false);
@@ -382,23 +394,29 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 tc_fence_after();
                 const uint32_t d = tmem_base + static_cast<uint32_t>(buf * NT);
-                for (int kb = c.kb0; kb < c.kb1; ++kb) {
-                    if (!wait_bounded(smem_u32(&full[s]), phase, abort_flag, limit) ||
-                        (W4 && !wait_bounded(smem_u32(&conv[s]), phase, abort_flag, limit))) {
+                for (int kb = c.kb0; kb < c.kb1; kb += C::kKb) {
+                    if (!wait_bounded(smem_u32(&full[s]), phase, abort_flag, limit)) {
                         gave_up();
                         ok = false;
                         break;
                     }
                     tc_fence_after();
-                    const uint32_t alo = da.lo + s * (kABytes >> 4), blo = dx.lo + s * (C::kXBytes >> 4);
                     if (one) {
 #pragma unroll
-                        for (int k = 0; k < BK / 16; ++k) {
-                            const uint32_t more = (k > 0 || kb > c.kb0) ? 1u : 0u;
-                            if (W4)
-                                tc_mma_ta(d, tmem_base + C::kACol + 32 * s + 8 * k, blo + k * dx.kstep, dx.hi, p.idesc, more);
-                            else
-                                tc_mma_w<false>(d, alo + k * da.kstep, da.hi, blo + k * dx.kstep, dx.hi, p.idesc, more);
+                        for (int b = 0; b < C::kKb; ++b) {
+                            if (b > 0 && kb + b >= c.kb1)
+                                break;
+                            const int slot = s * C::kKb + b;
+                            const uint32_t alo = da.lo + slot * (kABytes >> 4), blo = dx.lo + slot * (C::kXBytes >> 4);
+#pragma unroll
+                            for (int k = 0; k < BK / 16; ++k) {
+                                const uint32_t more = (k > 0 || b > 0 || kb > c.kb0) ? 1u : 0u;
+                                if (W4)
+                                    tc_mma_ta(d, tmem_base + C::kACol + 32 * slot + 8 * k, blo + k * dx.kstep, dx.hi, p.idesc,
+                                              more);
+                                else
+                                    tc_mma_w<false>(d, alo + k * da.kstep, da.hi, blo + k * dx.kstep, dx.hi, p.idesc, more);
+                            }
                         }
                         if (!skip_release)
                             tc_commit(smem_u32(&empty[s]));
@@ -425,8 +443,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else if (W4 && warp >= 4 && warp < 4 + kConvSets * kConvWarps) {
         // ------------------------------------------------------------ 4-bit weights to 16 bits
-        // A thread converts 32 of K of one row of each k-block.
-        // Two sets of eight warps take the stages in turns.
+        // A thread converts 32 of K of one row of each k-block.  Two sets of eight warps
+        // take the stages of codes in turns.
         const int r = (threadIdx.x - 128) & 127, half = ((threadIdx.x - 128) >> 7) & 1, set = (threadIdx.x - 128) >> 8;
         const uint32_t swz = static_cast<uint32_t>(r & 7);
         const uint32_t raw0 = smem_u32(raw) + r * 128;
@@ -434,14 +452,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         int s = 0, rs = 0, turn = 0;
         uint32_t phase = 0, rphase = 0;
         bool ok = true;
-        // over one stage's k-blocks (n of them)
-        const auto next = [&](int n) {
-            s += n;
-            if (s >= kStages) {
-                s -= kStages;
-                phase ^= 1;
-            }
-        };
         Piece c;
         for (int i = 0; ok && piece_at(p, i, NT, rank, c); ++i) {
             const int o = f.gated ? c.o0 + (r >> 5) * 16 + (r & 15) : c.o0 + r;
@@ -450,86 +460,92 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int64_t at = o < f.n ? row : static_cast<int64_t>(f.n) - 1;
             const uint16_t* srow = static_cast<const uint16_t*>(f.scales) + at * f.lds;
             const uint8_t* zrow = f.zeros ? f.zeros + at * f.ldz : nullptr;
-            // scales and zeros of a stage's four k-blocks, fetched four stages ahead: nothing
-            // is done with them here that would have to wait for them
-            const auto fetch = [&](int kb, uint32_t (&v)[kRawKb], uint32_t (&z)[kRawKb]) {
+            // the scales and zeros of a stage's k-blocks, fetched a stage ahead; what lies
+            // four stages of codes ahead is brought near
+            uint32_t scale[C::kKb], zero[C::kKb];
+            const auto fetch = [&](int kb) {
 #pragma unroll
-                for (int j = 0; j < kRawKb; ++j) {
-                    const int g = min((kb + j) * BK + half * 32, f.k - 1) >> f.group_shift;
-                    v[j] = __ldg(srow + g);
-                    z[j] = 8;
+                for (int b = 0; b < C::kKb; ++b) {
+                    const int g = min((kb + b) * BK + half * 32, f.k - 1) >> f.group_shift;
+                    scale[b] = __ldg(srow + g);
+                    zero[b] = 8;
                     if (zrow)
-                        z[j] = __ldg(zrow + g);
+                        zero[b] = __ldg(zrow + g);
                 }
             };
-            int kb = c.kb0;
-            // one stage, whose scales and zeros are in v and z; false at the piece's end or after a wait that ran out
-            const auto stage = [&](uint32_t (&v)[kRawKb], uint32_t (&z)[kRawKb]) {
-                if (kb < c.kb1 && turn != set) {  // the other set's
-                    next(min(kRawKb, c.kb1 - kb));
-                    if (++rs == kRaw) {
-                        rs = 0;
-                        rphase ^= 1;
+            fetch(c.kb0 + (turn != set ? kRawKb : 0));
+            for (int kb = c.kb0; ok && kb < c.kb1; kb += kRawKb) {
+                const int n = min(kRawKb, c.kb1 - kb);
+                if (turn == set) {
+                    if (!wait_bounded(smem_u32(&raw_full[rs]), rphase, abort_flag, limit)) {
+                        gave_up();
+                        ok = false;
+                        break;
                     }
-                    kb += kRawKb;
-                    turn ^= 1;
-                }
-                if (kb >= c.kb1)
-                    return false;
-                turn ^= 1;
-                if (!wait_bounded(smem_u32(&raw_full[rs]), rphase, abort_flag, limit)) {
-                    gave_up();
-                    ok = false;
-                    return false;
-                }
+                    {
+                        const int g = min((kb + 4 * kRawKb) * BK, f.k - 1) >> f.group_shift;
+                        asm volatile("prefetch.global.L1 [%0];" ::"l"(srow + g));
+                    }
+#pragma unroll 1
+                    for (int j = 0; j < n; j += C::kKb) {
+                        uint32_t out[C::kKb][16];
 #pragma unroll
-                for (int j = 0; j < kRawKb; ++j) {
-                    if (kb + j < c.kb1) {
-                        const uint4 w = lds128(raw0 + rs * kRawBytes + (((2 * j + half) ^ swz) << 4));
-                        const uint32_t words[4] = {w.x, w.y, w.z, w.w};
-                        const uint32_t scale = __byte_perm(v[j], 0, 0x1010);
-                        const uint32_t zero = __byte_perm(z[j] | (BF16 ? 0x4300u : 0x6400u), 0, 0x1010);
-                        uint32_t out[16];
+                        for (int b = 0; b < C::kKb; ++b) {
+                            // (of a k-block past the last, whatever the stage holds)
+                            const uint4 w = lds128(raw0 + rs * kRawBytes + (((2 * (j + b) + half) ^ swz) << 4));
+                            const uint32_t words[4] = {w.x, w.y, w.z, w.w};
+                            const uint32_t scale2 = __byte_perm(scale[b], 0, 0x1010);
+                            const uint32_t zero2 = __byte_perm(zero[b] | (BF16 ? 0x4300u : 0x6400u), 0, 0x1010);
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            convert8<BF16>(words[e], zero, scale, out + 4 * e);
+                            for (int e = 0; e < 4; ++e)
+                                convert8<BF16>(words[e], zero2, scale2, out[b] + 4 * e);
+                        }
+                        fetch(j + C::kKb < n ? kb + j + C::kKb : kb + kConvSets * kRawKb);
                         const int left = f.k - ((kb + j) * BK + half * 32);  // elements inside K
-                        if (left < 32) {
+                        if (left < 32 + (C::kKb - 1) * BK) {
                             // past K: zeros, whatever the scale
 #pragma unroll
-                            for (int h = 0; h < 16; ++h)
-                                out[h] &= left - 2 * h >= 2 ? 0xffffffffu : (left - 2 * h == 1 ? 0xffffu : 0u);
+                            for (int b = 0; b < C::kKb; ++b)
+#pragma unroll
+                                for (int h = 0; h < 16; ++h) {
+                                    const int l = left - b * BK - 2 * h;
+                                    out[b][h] &= l >= 2 ? 0xffffffffu : (l == 1 ? 0xffffu : 0u);
+                                }
                         }
                         if (!wait_bounded(smem_u32(&empty[s]), phase ^ 1, abort_flag, limit)) {
                             gave_up();
                             ok = false;
-                            return false;
+                            break;
                         }
                         tc_fence_after();
-                        tmem_st16_wait(a0 + 32 * s, out);
+#pragma unroll
+                        for (int b = 0; b < C::kKb; ++b)
+                            tmem_st16(a0 + 32 * (s * C::kKb + b), out[b]);
+                        tmem_st_wait();
                         tc_fence_before();
                         __syncwarp();
                         if (lane == 0)
-                            mbar_arrive(smem_u32(&conv[s]));
-                        next(1);
+                            mbar_arrive(smem_u32(&full[s]));
+                        if (++s == kStages) {
+                            s = 0;
+                            phase ^= 1;
+                        }
+                    }
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(smem_u32(&raw_empty[rs]));
+                } else {  // the other set's
+                    s += (n + C::kKb - 1) / C::kKb;
+                    if (s >= kStages) {
+                        s -= kStages;
+                        phase ^= 1;
                     }
                 }
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive(smem_u32(&raw_empty[rs]));
                 if (++rs == kRaw) {
                     rs = 0;
                     rphase ^= 1;
                 }
-                fetch(kb + 2 * kRawKb * kConvSets, v, z);
-                kb += kRawKb;
-                return true;
-            };
-            uint32_t v[2][kRawKb], z[2][kRawKb];
-#pragma unroll
-            for (int j = 0; j < 2; ++j)
-                fetch(kb + (j * kConvSets + (turn != set)) * kRawKb, v[j], z[j]);
-            while (stage(v[0], z[0]) && stage(v[1], z[1])) {
+                turn ^= 1;
             }
         }
     } else if (warp >= 20) {
