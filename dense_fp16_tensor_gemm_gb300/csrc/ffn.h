@@ -84,7 +84,8 @@ cudaError_t gated_pair_launch(const FfnParams& p, int max_pairs, cudaStream_t st
 // Up to 16 tokens, on the warp MMA; rows of the weights on the 16-byte grid.
 constexpr int kFewTokens = 16;
 cudaError_t ffn_few_configure();  // one-time per device
-cudaError_t ffn_few_launch(const FfnParams& p, cudaStream_t stream);
+bool ffn_few_fits(const FfnParams& p);  // tokens up to kFewTokens, and no more than shared memory takes
+cudaError_t ffn_few_launch(const FfnParams& p, int num_sms, cudaStream_t stream);
 
 // The weights as the MMA's rows; X and W on the 16-byte grid.  16-bit weights: up to
 // kSwapTokens tokens.

@@ -73,7 +73,7 @@ bool pair_ok(const FfnParams& p, const DeviceInfo& d)
 
 bool few_ok(const FfnParams& p)
 {
-    return p.k > 0 && p.k <= (1 << 29) && p.tokens <= kFewTokens && aligned(p.w, 16) && p.ldw * (p.scales ? 1 : 2) % 16 == 0;
+    return p.k > 0 && p.k <= (1 << 29) && ffn_few_fits(p) && aligned(p.w, 16) && p.ldw * (p.scales ? 1 : 2) % 16 == 0;
 }
 
 bool swap_ok(const FfnParams& p)
@@ -102,7 +102,7 @@ gemm_status_t run(FfnParams& p, gemm_path_t path, cudaStream_t stream)
     if (path == GEMM_PATH_TC05 && swap_ok(p))
         return status_of(ffn_swap_launch(p, d.num_sms, stream));
     if (path == GEMM_PATH_SKINNY && few_ok(p))
-        return status_of(ffn_few_launch(p, stream));
+        return status_of(ffn_few_launch(p, d.num_sms, stream));
     if (path == GEMM_PATH_TC05_PAIR && pair_ok(p, d))
         return status_of(gated_pair_launch(p, d.gated_pairs, stream));
     if (path == GEMM_PATH_MMASYNC)
