@@ -35,6 +35,10 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int by
 {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void cp_async_wait()
@@ -96,7 +100,9 @@ template <bool BF16>
 __device__ __forceinline__ uint32_t codes_at(uint32_t word, int i, uint32_t magic_zero)
 {
     constexpr uint32_t magic = BF16 ? 0x43004300u : 0x64006400u;
-    const uint32_t v = ((word >> (4 * i)) & 0x000f000fu) | magic;
+    // (word >> 4 i) & 0x000f000f | magic: one logical operation after the shift
+    uint32_t v;
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(v) : "r"(word >> (4 * i)), "r"(0x000f000fu), "r"(magic));
     if (BF16) {
         const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&v), *reinterpret_cast<const __nv_bfloat162*>(&magic_zero));
         return *reinterpret_cast<const uint32_t*>(&d);
@@ -135,12 +141,14 @@ struct Cfg {
     static constexpr int kRed = 2 * WARPS * NT * 512;
 };
 
-// NT: sets of 8 tokens.  G128: groups of 128.
-template <bool BF16, bool W4, bool GATED, int NT, int WARPS, bool G128>
+// NT: sets of 8 tokens; 0: a single token.  G128: groups of 128.
+template <bool BF16, bool W4, bool GATED, int NTOK, int WARPS, bool G128>
 __global__ void __launch_bounds__(32 * WARPS, WARPS == 8 ? 3 : 1) ffn_few_kernel(const FfnParams p, int vec_x, int vec_s, int tiles)
 {
     using S = OutStore<BF16 ? kOutBF16 : kOutF16>;
+    constexpr int NT = NTOK ? NTOK : 1;
     using C = Cfg<NT, WARPS>;
+    const int tokens = NTOK ? p.tokens : 1;
     constexpr int kDepth = C::kDepth;
     constexpr int kRows = GATED ? 8 : 16;  // outputs per tile
     constexpr int kStepK = W4 ? 256 : 64;
@@ -152,8 +160,6 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS == 8 ? 3 : 1) ffn_few_kernel
     uint4* const xs = reinterpret_cast<uint4*>(smem + C::kRing + C::kRed);
 
     pdl_launch_dependents();
-    pdl_wait();
-
     const int row_bytes = W4 ? (p.k >> 1) + (p.k & 1) : 2 * p.k;
     const int steps = (row_bytes + 127) >> 7;
     const int count = steps > warp ? (steps - warp + WARPS - 1) / WARPS : 0;  // of this warp, per tile
@@ -162,13 +168,15 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS == 8 ? 3 : 1) ffn_few_kernel
     // lane / 8 + 4 i, and fetches scales and zeros of rows g and g + 8: those of the step's
     // two groups, or, in shorter groups, those at 64 t and 64 t + 32 of it.
     int ft = blockIdx.x, fi = 0;
-    const uint8_t* src[2];  // rows i = 0 and 2
+    const uint8_t* src[2];  // rows i = 0 and 2, of step fi
     const uint16_t* srow[2];
     const uint8_t* zrow[2];
     int valid = 0;
+    bool full = false;  // a tile of 16 rows
     const int64_t four = p.ldw * (W4 ? 4 : 8);  // bytes from a row to the fourth after it
     const auto open = [&] {
         valid = 0;
+        full = static_cast<int64_t>(ft + 1) * kRows <= p.n;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int r = (lane >> 3) + 4 * i, o = ft * kRows + (GATED ? r & 7 : r);
@@ -197,12 +205,20 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS == 8 ? 3 : 1) ffn_few_kernel
     const auto fetch = [&](int slot, uint32_t (&sc)[2], uint32_t (&ze)[2]) {
         if (ft < tiles) {
             const int step = warp + fi * WARPS;
-            const int left = max(0, min(16, row_bytes - step * 128 - (lane & 7) * 16));
+            if (full && (step + 1) * 128 <= row_bytes) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                // (nothing is read where 0 bytes are copied)
-                cp_async16(dst[i & 1] + slot * kStep + 1024 * (i >> 1), src[i >> 1] + (i & 1 ? four : 0) + fi * (WARPS * 128),
-                           valid & (1 << i) ? left : 0);
+                for (int i = 0; i < 4; ++i)
+                    cp_async16(dst[i & 1] + slot * kStep + 1024 * (i >> 1), src[i >> 1] + (i & 1 ? four : 0));
+            } else {
+                const int left = max(0, min(16, row_bytes - step * 128 - (lane & 7) * 16));
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    // (nothing is read where 0 bytes are copied)
+                    cp_async16(dst[i & 1] + slot * kStep + 1024 * (i >> 1), src[i >> 1] + (i & 1 ? four : 0),
+                               valid & (1 << i) ? left : 0);
+            }
+            src[0] += WARPS * 128;
+            src[1] += WARPS * 128;
             if (W4) {
                 const int k = step * kStepK + (G128 ? 0 : 64 * t);
                 const int g0 = k >> p.group_shift, g1 = (k + (G128 ? 128 : 32)) >> p.group_shift;
@@ -247,13 +263,27 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS == 8 ? 3 : 1) ffn_few_kernel
         }
     if (count > 0) {
         open();
+        // The first steps' weights come into L2 while the preceding grids finish: a prefetch
+        // reads no value, so it may run ahead of the wait for them.
+        if (lane % 8 == 0) {
+#pragma unroll
+            for (int i = 0; i < kDepth; ++i)
+                if (i < count && (warp + i * WARPS) * 128 < row_bytes)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        if (valid & (1 << r))
+                            asm volatile("prefetch.global.L2 [%0];" ::"l"(src[r >> 1] + (r & 1 ? four : 0) + i * (WARPS * 128)));
+        }
+        pdl_wait();
 #pragma unroll
         for (int i = 0; i < kDepth; ++i)
             fetch(i, sc[i], ze[i]);
+    } else {
+        pdl_wait();
     }
 
     // the tokens: [step][piece][token][t], 8 elements each, paired as the codes are
-    for (int e = threadIdx.x; e < steps * XV * p.tokens * 4; e += C::kThreads) {
+    for (int e = threadIdx.x; e < steps * XV * tokens * 4; e += C::kThreads) {
         // consecutive threads on consecutive elements of a token
         const int tok = e / (steps * XV * 4), r = e - tok * (steps * XV * 4);
         const int k = r * 8, step = r / (XV * 4), in = r % (XV * 4);
@@ -264,15 +294,15 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS == 8 ? 3 : 1) ffn_few_kernel
         if (W4)
             v = make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632), __byte_perm(v.y, v.w, 0x5410),
                            __byte_perm(v.y, v.w, 0x7632));
-        xs[((step * XV + j) * p.tokens + tok) * 4 + tt] = v;
+        xs[((step * XV + j) * tokens + tok) * 4 + tt] = v;
     }
     __syncthreads();
-    const uint32_t xpiece = p.tokens * 64;  // bytes
+    const uint32_t xpiece = tokens * 64;  // bytes
     uint32_t xat[NT];
 #pragma unroll
     for (int n = 0; n < NT; ++n)
         // (lanes of tokens that are not there read the last one: their columns are not stored)
-        xat[n] = smem_u32(xs) + min(8 * n + g, p.tokens - 1) * 64 + t * 16 + warp * XV * xpiece;
+        xat[n] = smem_u32(xs) + min(8 * n + g, tokens - 1) * 64 + t * 16 + warp * XV * xpiece;
     const uint32_t swz = (g & 1) << 2 | ((g >> 1) & 3);  // of rows g and g + 8
     // 16-byte piece c of row g of a step
     const auto piece = [&](int c) { return ring + g * 128 + ((static_cast<uint32_t>(c) ^ swz) << 4); };
@@ -391,7 +421,7 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS == 8 ? 3 : 1) ffn_few_kernel
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const int tok = 8 * n + 2 * t + e;
-                if (tok >= p.tokens)
+                if (tok >= tokens)
                     continue;
                 const int o = tile * kRows + g;
                 if (GATED) {
@@ -415,11 +445,11 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS == 8 ? 3 : 1) ffn_few_kernel
     cp_async_wait<0>();
 }
 
-template <bool BF16, bool W4, bool GATED, int NT, int WARPS, bool G128>
+template <bool BF16, bool W4, bool GATED, int NTOK, int WARPS, bool G128>
 cudaError_t run(const FfnParams& p, int num_sms, cudaStream_t stream, bool configure)
 {
-    using C = Cfg<NT, WARPS>;
-    auto* kernel = ffn_few_kernel<BF16, W4, GATED, NT, WARPS, G128>;
+    using C = Cfg<NTOK ? NTOK : 1, WARPS>;
+    auto* kernel = ffn_few_kernel<BF16, W4, GATED, NTOK, WARPS, G128>;
     if (configure)
         return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
     const int vec_x = reinterpret_cast<uintptr_t>(p.x) % 16 == 0 && p.ldx % 8 == 0;
@@ -445,7 +475,8 @@ template <bool BF16, bool W4, bool GATED, bool G128>
 cudaError_t by_tokens(const FfnParams& p, int num_sms, cudaStream_t stream, bool configure)
 {
     if (configure) {
-        cudaError_t e = run<BF16, W4, GATED, 1, 8, G128>(p, num_sms, stream, true);
+        cudaError_t e = run<BF16, W4, GATED, 0, 8, G128>(p, num_sms, stream, true);
+        if (e == cudaSuccess) e = run<BF16, W4, GATED, 1, 8, G128>(p, num_sms, stream, true);
         if (e == cudaSuccess) e = run<BF16, W4, GATED, 1, 16, G128>(p, num_sms, stream, true);
         if (e == cudaSuccess) e = run<BF16, W4, GATED, 2, 16, G128>(p, num_sms, stream, true);
         return e;
@@ -454,7 +485,8 @@ cudaError_t by_tokens(const FfnParams& p, int num_sms, cudaStream_t stream, bool
         return run<BF16, W4, GATED, 2, 16, G128>(p, num_sms, stream, false);
     // two CTAs of 8 warps have to fit
     if (2 * (Cfg<1, 8>::kRing + Cfg<1, 8>::kRed + x_bytes(p) + 1024) <= kMaxSmem + 1024)
-        return run<BF16, W4, GATED, 1, 8, G128>(p, num_sms, stream, false);
+        return p.tokens == 1 ? run<BF16, W4, GATED, 0, 8, G128>(p, num_sms, stream, false)
+                             : run<BF16, W4, GATED, 1, 8, G128>(p, num_sms, stream, false);
     return run<BF16, W4, GATED, 1, 16, G128>(p, num_sms, stream, false);
 }
 
