@@ -6,10 +6,12 @@
 //               z = clamp(rint(-lo * (1/s)), 0, 15), code = clamp(rint(w * (1/s)) + z, 0, 15)
 //
 // in fp32, each step rounded, with the rounded s, so that codes and scales
-// together stand for the weights as nearly as they can.  A thread holds 8
-// consecutive elements (one 16-byte load of 16-bit weights, one 4-byte store of
-// codes); a group's 4, 8 or 16 threads share its extremes by shuffles.  Bound by
-// memory: one read of the weights.
+// together stand for the weights as nearly as they can.  A thread holds 16
+// consecutive elements (two 16-byte loads of 16-bit weights, one 8-byte store of
+// codes); a group's 2, 4 or 8 threads share its extremes by shuffles.  Bound by
+// memory, one read of the weights, as long as the instructions stay below it: w * (1/s)
+// is rounded to a whole number by adding 1.5 * 2^23, whose low bits then hold it
+// (|w / s| stays below 32), and a saturating pack clamps and joins two codes.
 #include <algorithm>
 #include <cfloat>
 
@@ -21,24 +23,29 @@ namespace gnt {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kPer = 16;  // elements per thread
 
 // WT: 0 fp16, 1 bf16, 2 fp32.  VEC: 16-byte aligned rows of weights.
 template <int WT, bool VEC>
-__device__ __forceinline__ void load8(const Quant4Params& p, int64_t row, int64_t col, float (&v)[8])
+__device__ __forceinline__ void load16(const Quant4Params& p, int64_t row, int64_t col, float (&v)[kPer])
 {
-    if (VEC && col + 8 <= p.cols) {
+    if (VEC && col + kPer <= p.cols) {
         if constexpr (WT == 2) {
             const float4* g = reinterpret_cast<const float4*>(static_cast<const float*>(p.w) + row * p.ldw + col);
-            const float4 a = __ldcs(g), b = __ldcs(g + 1);
-            v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-        } else {
-            const uint4 a = __ldcs(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.w) + row * p.ldw + col));
-            const uint32_t w[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
+                const float4 a = __ldcs(g + i);
+                v[4 * i] = a.x, v[4 * i + 1] = a.y, v[4 * i + 2] = a.z, v[4 * i + 3] = a.w;
+            }
+        } else {
+            const uint4* g = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.w) + row * p.ldw + col);
+            const uint4 a = __ldcs(g), b = __ldcs(g + 1);
+            const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
                 float2 f;
                 if constexpr (WT == 1)
-                    f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w[i]));
+                    f = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
                 else
                     f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
                 v[2 * i] = f.x;
@@ -48,7 +55,7 @@ __device__ __forceinline__ void load8(const Quant4Params& p, int64_t row, int64_
         return;
     }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < kPer; ++i) {
         v[i] = 0.f;
         if (col + i < p.cols) {
             if constexpr (WT == 2)
@@ -61,31 +68,56 @@ __device__ __forceinline__ void load8(const Quant4Params& p, int64_t row, int64_
     }
 }
 
-template <int WT, bool VEC>
-__global__ void __launch_bounds__(kThreads) w4_quantize_kernel(const Quant4Params p, int64_t per_row, int64_t total)
+// max, a NaN if either is one
+__device__ __forceinline__ float max_nan(float a, float b)
 {
-    const int lane = threadIdx.x & 31;
-    const int lanes = 1 << (p.group_shift - 3);  // threads of a group
-    // 32 threads take 256 consecutive elements of a row
-    for (int64_t i = (blockIdx.x * static_cast<int64_t>(kThreads) + threadIdx.x) >> 5; i < total;
-         i += static_cast<int64_t>(gridDim.x) * (kThreads / 32)) {
-        const int64_t row = i / per_row, col = (i - row * per_row) * 256 + lane * 8;
-        float v[8];
-        load8<WT, VEC>(p, row, col, v);
-        float lo = 0.f, hi = 0.f;
-        int bad = 0;  // an infinity or NaN
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
+// {hi, lo} as two 4-bit numbers, clamped to 0..15, below c's bits
+__device__ __forceinline__ uint32_t pack_u4(int hi, int lo, uint32_t c)
+{
+    uint32_t d;
+    asm("cvt.pack.sat.u4.s32.b32 %0, %1, %2, %3;" : "=r"(d) : "r"(hi), "r"(lo), "r"(c));
+    return d;
+}
+
+template <int WT, bool VEC, bool ZEROS>
+__global__ void __launch_bounds__(kThreads) w4_quantize_kernel(const Quant4Params p, int per_row, int64_t total, int step_rows,
+                                                               int step_pieces)
+{
+    const int lanes = 1 << (p.group_shift - 4);  // threads of a group
+    int64_t i = blockIdx.x * static_cast<int64_t>(kThreads) + threadIdx.x;
+    int64_t row = i / per_row;
+    int piece = static_cast<int>(i - row * per_row);
+    // (a warp goes on as a whole: its groups share by shuffles)
+    for (; (i & ~31ll) < total; i += static_cast<int64_t>(gridDim.x) * kThreads) {
+        const int64_t col = static_cast<int64_t>(piece) * kPer;
+        float v[kPer];
+        if (i < total) {
+            load16<WT, VEC>(p, row, col, v);
+        } else {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            lo = fminf(lo, v[k]);
-            hi = fmaxf(hi, v[k]);
-            bad |= (__float_as_uint(v[k]) & 0x7f800000u) == 0x7f800000u;
+            for (int k = 0; k < kPer; ++k)
+                v[k] = 0.f;
+        }
+        // the largest of w and of -w, or of |w|
+        float hi = 0.f, low = 0.f;
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) {
+            hi = max_nan(hi, ZEROS ? v[k] : fabsf(v[k]));
+            if (ZEROS)
+                low = max_nan(low, -v[k]);
         }
         for (int o = 1; o < lanes; o <<= 1) {
-            lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-            hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
-            bad |= __shfl_xor_sync(0xffffffffu, bad, o);
+            hi = max_nan(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+            if (ZEROS)
+                low = max_nan(low, __shfl_xor_sync(0xffffffffu, low, o));
         }
-        float s = p.zeros ? __fmul_rn(__fsub_rn(hi, lo), 1.f / 15.f) : __fmul_rn(fmaxf(hi, -lo), 1.f / 7.f);
+        float s = ZEROS ? __fmul_rn(__fadd_rn(hi, low), 1.f / 15.f) : __fmul_rn(hi, 1.f / 7.f);
+        const bool bad = !(hi < INFINITY) || !(low < INFINITY);  // an infinity or NaN
         if (bad)
             s = __uint_as_float(0x7fc00000u);
         uint16_t s16;
@@ -96,46 +128,75 @@ __global__ void __launch_bounds__(kThreads) w4_quantize_kernel(const Quant4Param
             s16 = __half_as_ushort(__float2half_rn(s));
             s = __half2float(__ushort_as_half(s16));
         }
-        float inv = 0.f;  // also of a NaN: the group's codes are its zero's
+        float inv = 0.f;
         if (s >= FLT_MIN)
             inv = __frcp_rn(s);
         else if (s > 0.f)
             s16 = 0;  // 1/s could be infinite: such a group is zero
-        const float z = !p.zeros ? 8.f : (bad ? 0.f : fminf(fmaxf(rintf(__fmul_rn(-lo, inv)), 0.f), 15.f));
-        uint32_t word = 0;
+        int z = 8;
+        if (ZEROS)
+            z = bad ? 0 : static_cast<int>(fminf(rintf(__fmul_rn(low, inv)), 15.f));
+        uint32_t word[2];
+        if (bad) {
+            word[0] = word[1] = 0x11111111u * static_cast<uint32_t>(z);
+        } else {
+            const int bias = z - 0x4b400000;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            const float q = bad ? 0.f : rintf(__fmul_rn(v[k], inv));
-            word |= static_cast<uint32_t>(static_cast<int>(fminf(fmaxf(q + z, 0.f), 15.f))) << (4 * k);
+            for (int h = 0; h < 2; ++h) {
+                int q[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    q[k] = __float_as_int(__fadd_rn(__fmul_rn(v[8 * h + k], inv), 12582912.f)) + bias;
+                word[h] = pack_u4(q[1], q[0], pack_u4(q[3], q[2], pack_u4(q[5], q[4], pack_u4(q[7], q[6], 0u))));
+            }
         }
-        if (col < p.cols) {
-            const int64_t group = col >> p.group_shift;
-            if ((lane & (lanes - 1)) == 0) {
+        if (i < total && col < p.cols) {
+            if ((threadIdx.x & (lanes - 1)) == 0) {
+                const int64_t group = col >> p.group_shift;
                 static_cast<uint16_t*>(p.scales)[row * p.lds + group] = s16;
-                if (p.zeros)
+                if (ZEROS)
                     p.zeros[row * p.ldz + group] = static_cast<uint8_t>(z);
             }
             uint8_t* dst = p.codes + row * p.ldc + (col >> 1);
-            const int64_t left = (p.cols - col + 1) >> 1;  // bytes
-            if ((p.cols & 1) && left <= 4)
-                word &= (1u << (4 * (p.cols - col))) - 1;  // an odd row's last high half is zero
-            if (left >= 4 && (reinterpret_cast<uintptr_t>(dst) & 3) == 0) {
-                *reinterpret_cast<uint32_t*>(dst) = word;
+            if (col + kPer <= p.cols && (reinterpret_cast<uintptr_t>(dst) & 7) == 0) {
+                *reinterpret_cast<uint2*>(dst) = make_uint2(word[0], word[1]);
             } else {
-                for (int k = 0; k < 4 && k < left; ++k)
-                    dst[k] = static_cast<uint8_t>(word >> (8 * k));
+#pragma unroll
+                for (int k = 0; k < kPer / 2; ++k) {
+                    const int64_t left = p.cols - col - 2 * k;  // elements from this byte on
+                    const uint32_t byte = word[k >> 2] >> (8 * (k & 3)) & 0xffu;
+                    if (left > 0)
+                        dst[k] = static_cast<uint8_t>(left == 1 ? byte & 15u : byte);  // an odd row's last high half is zero
+                }
             }
+        }
+        row += step_rows;
+        piece += step_pieces;
+        if (piece >= per_row) {
+            piece -= per_row;
+            ++row;
         }
     }
 }
 
+template <int WT, bool VEC>
+void launch(const Quant4Params& p, unsigned grid, int per_row, int64_t total, cudaStream_t stream)
+{
+    const int64_t step = static_cast<int64_t>(grid) * kThreads;
+    const int rows = static_cast<int>(step / per_row), pieces = static_cast<int>(step % per_row);
+    if (p.zeros)
+        w4_quantize_kernel<WT, VEC, true><<<grid, kThreads, 0, stream>>>(p, per_row, total, rows, pieces);
+    else
+        w4_quantize_kernel<WT, VEC, false><<<grid, kThreads, 0, stream>>>(p, per_row, total, rows, pieces);
+}
+
 template <int WT>
-void launch(const Quant4Params& p, bool vec, unsigned grid, int64_t per_row, int64_t total, cudaStream_t stream)
+void launch(const Quant4Params& p, bool vec, unsigned grid, int per_row, int64_t total, cudaStream_t stream)
 {
     if (vec)
-        w4_quantize_kernel<WT, true><<<grid, kThreads, 0, stream>>>(p, per_row, total);
+        launch<WT, true>(p, grid, per_row, total, stream);
     else
-        w4_quantize_kernel<WT, false><<<grid, kThreads, 0, stream>>>(p, per_row, total);
+        launch<WT, false>(p, grid, per_row, total, stream);
 }
 
 }  // namespace
@@ -143,10 +204,12 @@ void launch(const Quant4Params& p, bool vec, unsigned grid, int64_t per_row, int
 cudaError_t w4_quantize_launch(const Quant4Params& p, int num_sms, cudaStream_t stream)
 {
     const int esize = p.w_type == GEMM_DTYPE_F32 ? 4 : 2;
-    const bool vec = reinterpret_cast<uintptr_t>(p.w) % 16 == 0 && p.ldw * esize % 16 == 0;
-    const int64_t per_row = (p.cols + 255) / 256, total = per_row * p.rows;
-    const unsigned grid =
-        static_cast<unsigned>(std::min<int64_t>((total + kThreads / 32 - 1) / (kThreads / 32), int64_t(num_sms) * 64));
+    const bool vec = reinterpret_cast<uintptr_t>(p.w) % 16 == 0 && (p.rows == 1 || p.ldw * esize % 16 == 0);
+    // pieces of 16 elements, whole groups of them: a group's threads are neighbours
+    const int64_t groups = (p.cols + (int64_t(1) << p.group_shift) - 1) >> p.group_shift;
+    const int per_row = static_cast<int>(groups << (p.group_shift - 4));
+    const int64_t total = per_row * p.rows;
+    const unsigned grid = static_cast<unsigned>(std::min<int64_t>((total + kThreads - 1) / kThreads, int64_t(num_sms) * 32));
     if (p.w_type == GEMM_DTYPE_F32)
         launch<2>(p, vec, grid, per_row, total, stream);
     else if (p.w_type == GEMM_DTYPE_BF16)
