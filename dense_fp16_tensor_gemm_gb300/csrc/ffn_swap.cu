@@ -126,6 +126,12 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map
         "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
         : "memory");
 }
+__device__ __forceinline__ void tma_prefetch_l2_4d(const CUtensorMap* map, int32_t c0, int32_t c1, int32_t c2, int32_t c3)
+{
+    asm volatile("cp.async.bulk.prefetch.tensor.4d.L2.global.tile [%0, {%1, %2, %3, %4}];" ::"l"(reinterpret_cast<uint64_t>(map)),
+                 "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+                 : "memory");
+}
 __device__ __forceinline__ float lds_cluster(uint32_t a)
 {
     float v;
@@ -144,7 +150,8 @@ __device__ __forceinline__ void convert8(uint32_t word, uint32_t zero2, uint32_t
         // bytes: word's i-th and high's i-th, each the low byte of a half
         const uint32_t sel = static_cast<uint32_t>(i) | static_cast<uint32_t>(i) << 4 | static_cast<uint32_t>(4 + i) << 8 |
                              static_cast<uint32_t>(4 + i) << 12;
-        const uint32_t q = (__byte_perm(word, high, sel) & 0x000f000fu) | magic;
+        uint32_t q;  // bytes & 0x000f000f | magic, in one logical operation
+        asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(q) : "r"(__byte_perm(word, high, sel)), "r"(0x000f000fu), "r"(magic));
         if (BF16) {
             __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&q), *reinterpret_cast<const __nv_bfloat162*>(&zero2));
             d = __hmul2(d, *reinterpret_cast<const __nv_bfloat162*>(&scale2));
@@ -280,6 +287,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
     pdl_launch_dependents();
+    if (warp == 0 && lane == 0) {
+        // the first ring of weights comes into L2 while the preceding grids finish
+        Piece c;
+        if (piece_at(p, 0, NT, rank, c)) {
+            constexpr int step = W4 ? kRawKb : 1;
+            for (int i = 0, kb = c.kb0; i < (W4 ? C::kRaw : C::kKb * kStages) && kb < c.kb1; ++i, kb += step) {
+                const int x = W4 ? kb * (BK / 2) : kb * BK;
+                if (f.gated && c.o0 + kRowsW / 2 <= p.whole)
+                    tma_prefetch_l2_4d(&tmi, x, 0, 0, c.o0 / 16);
+                else if (!f.gated)
+                    tma_prefetch_l2_3d(&tmw, x, c.o0, 0);
+            }
+        }
+    }
     pdl_wait();
 
     // waits (bounded) until the copies last posted on each of n barriers have landed
