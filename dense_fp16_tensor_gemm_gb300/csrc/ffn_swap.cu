@@ -53,15 +53,14 @@ constexpr int kConvWarps = 8, kConvSets = 2, kEpiWarps = 4;
 // NT: tokens per tile.
 template <bool W4, int NT>
 struct Cfg {
-    // k-blocks per stage.  A wait that finds its barrier done still takes the MMA warp
-    // about 135 cycles and a commit 60, while the four MMAs of a k-block run 127 at 64
-    // tokens, 254 at 128 and 508 at 256: two k-blocks share one wait and one commit,
-    // but for 256 tokens.
-    static constexpr int kKb = NT == 256 ? 1 : 2;
+    // k-blocks per stage.  A wait that finds its barrier done still takes a warp about
+    // 135 cycles and a commit 60, while the four MMAs of a k-block run 127 at 64 tokens, 254
+    // at 128 and 508 at 256: k-blocks share them, as many as leave room for a ring.
+    static constexpr int kKb = NT == 256 ? 1 : (W4 && NT <= 64 ? 4 : 2);
     static constexpr int kXBytes = NT * BK * 2;                            // of one k-block
     static constexpr int kStage = kKb * ((W4 ? 0 : kABytes) + kXBytes);  // of shared memory
     static constexpr int kRaw = W4 ? (NT == 256 ? 3 : (NT == 128 ? 5 : 6)) : 0;
-    static constexpr int kStages = W4 ? (NT == 256 ? 5 : (NT == 128 ? 4 : 6)) : (NT == 128 ? 3 : 4);
+    static constexpr int kStages = W4 ? (NT == 256 ? 5 : (NT == 128 ? 4 : 3)) : (NT == 128 ? 3 : 4);
     static constexpr int kSmem = 1024 + kStages * kStage + kRaw * kRawBytes + 512;
     // Tensor Memory: the accumulators (one of 256 columns, where the converted
     // weights leave no room for two), then 32 columns of weights a stage
@@ -227,7 +226,8 @@ __device__ __forceinline__ void store_tokens(const FfnParams& p, int o0, int row
     }
 }
 
-template <bool W4, bool BF16, int NT>
+// G128: groups of 128.
+template <bool W4, bool BF16, int NT, bool G128>
 __global__ void __launch_bounds__(kThreads, 1)
     ffn_swap_kernel(const __grid_constant__ CUtensorMap tmw, const __grid_constant__ CUtensorMap tmi,
                     const __grid_constant__ CUtensorMap tmx, const SwapParams p)
@@ -481,58 +481,39 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int64_t at = o < f.n ? row : static_cast<int64_t>(f.n) - 1;
             const uint16_t* srow = static_cast<const uint16_t*>(f.scales) + at * f.lds;
             const uint8_t* zrow = f.zeros ? f.zeros + at * f.ldz : nullptr;
-            // the scales and zeros of a stage's k-blocks, fetched a stage ahead; what lies
-            // four stages of codes ahead is brought near
-            uint32_t scale[C::kKb], zero[C::kKb];
-            const auto fetch = [&](int kb) {
+            // the scales and zeros of a stage of codes, two of groups of 128 and else one for
+            // every k-block, fetched a turn ahead; what lies four stages ahead is brought near
+            constexpr int NS = G128 ? 2 : kRawKb;
+            uint32_t scale[NS], zero[NS], scale1[NS], zero1[NS];
+            const auto fetch = [&](int kb, uint32_t (&sc)[NS], uint32_t (&ze)[NS]) {
 #pragma unroll
-                for (int b = 0; b < C::kKb; ++b) {
-                    const int g = min((kb + b) * BK + half * 32, f.k - 1) >> f.group_shift;
-                    scale[b] = __ldg(srow + g);
-                    zero[b] = 8;
+                for (int b = 0; b < NS; ++b) {
+                    const int g = min((kb + b * (kRawKb / NS)) * BK + (G128 ? 0 : half * 32), f.k - 1) >> f.group_shift;
+                    sc[b] = __ldg(srow + g);
+                    ze[b] = 8;
                     if (zrow)
-                        zero[b] = __ldg(zrow + g);
+                        ze[b] = __ldg(zrow + g);
                 }
             };
-            fetch(c.kb0 + (turn != set ? kRawKb : 0));
+            fetch(c.kb0 + (turn != set ? kRawKb : 0), scale, zero);
             for (int kb = c.kb0; ok && kb < c.kb1; kb += kRawKb) {
                 const int n = min(kRawKb, c.kb1 - kb);
                 if (turn == set) {
+                    fetch(kb + kConvSets * kRawKb, scale1, zero1);
+                    {
+                        const int g = min((kb + 4 * kRawKb) * BK, f.k - 1) >> f.group_shift;
+                        asm volatile("prefetch.global.L1 [%0];" ::"l"(srow + g));
+                    }
                     if (!wait_bounded(smem_u32(&raw_full[rs]), rphase, abort_flag, limit)) {
                         gave_up();
                         ok = false;
                         break;
                     }
-                    {
-                        const int g = min((kb + 4 * kRawKb) * BK, f.k - 1) >> f.group_shift;
-                        asm volatile("prefetch.global.L1 [%0];" ::"l"(srow + g));
-                    }
-#pragma unroll 1
-                    for (int j = 0; j < n; j += C::kKb) {
-                        uint32_t out[C::kKb][16];
+                    const int left = f.k - (kb * BK + half * 32);  // elements inside K
 #pragma unroll
-                        for (int b = 0; b < C::kKb; ++b) {
-                            // (of a k-block past the last, whatever the stage holds)
-                            const uint4 w = lds128(raw0 + rs * kRawBytes + (((2 * (j + b) + half) ^ swz) << 4));
-                            const uint32_t words[4] = {w.x, w.y, w.z, w.w};
-                            const uint32_t scale2 = __byte_perm(scale[b], 0, 0x1010);
-                            const uint32_t zero2 = __byte_perm(zero[b] | (BF16 ? 0x4300u : 0x6400u), 0, 0x1010);
-#pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                convert8<BF16>(words[e], zero2, scale2, out[b] + 4 * e);
-                        }
-                        fetch(j + C::kKb < n ? kb + j + C::kKb : kb + kConvSets * kRawKb);
-                        const int left = f.k - ((kb + j) * BK + half * 32);  // elements inside K
-                        if (left < 32 + (C::kKb - 1) * BK) {
-                            // past K: zeros, whatever the scale
-#pragma unroll
-                            for (int b = 0; b < C::kKb; ++b)
-#pragma unroll
-                                for (int h = 0; h < 16; ++h) {
-                                    const int l = left - b * BK - 2 * h;
-                                    out[b][h] &= l >= 2 ? 0xffffffffu : (l == 1 ? 0xffffu : 0u);
-                                }
-                        }
+                    for (int j = 0; j < kRawKb; j += C::kKb) {
+                        if (j >= n)
+                            break;
                         if (!wait_bounded(smem_u32(&empty[s]), phase ^ 1, abort_flag, limit)) {
                             gave_up();
                             ok = false;
@@ -540,8 +521,27 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                         tc_fence_after();
 #pragma unroll
-                        for (int b = 0; b < C::kKb; ++b)
-                            tmem_st16(a0 + 32 * (s * C::kKb + b), out[b]);
+                        for (int b = 0; b < C::kKb; ++b) {
+                            // (of a k-block past the last, whatever the stage holds)
+                            const int jb = j + b;
+                            const uint4 w = lds128(raw0 + rs * kRawBytes + (((2 * jb + half) ^ swz) << 4));
+                            const uint32_t words[4] = {w.x, w.y, w.z, w.w};
+                            const uint32_t scale2 = __byte_perm(scale[jb * NS / kRawKb], 0, 0x1010);
+                            const uint32_t zero2 = __byte_perm(zero[jb * NS / kRawKb], BF16 ? 0x43 : 0x64, 0x4040);
+                            uint32_t out[16];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                convert8<BF16>(words[e], zero2, scale2, out + 4 * e);
+                            if (left < 32 + jb * BK) {
+                                // past K: zeros, whatever the scale
+#pragma unroll
+                                for (int h = 0; h < 16; ++h) {
+                                    const int l = left - jb * BK - 2 * h;
+                                    out[h] &= l >= 2 ? 0xffffffffu : (l == 1 ? 0xffffu : 0u);
+                                }
+                            }
+                            tmem_st16(a0 + 32 * (s * C::kKb + b), out);
+                        }
                         tmem_st_wait();
                         tc_fence_before();
                         __syncwarp();
@@ -555,6 +555,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                     __syncwarp();
                     if (lane == 0)
                         mbar_arrive(smem_u32(&raw_empty[rs]));
+#pragma unroll
+                    for (int b = 0; b < NS; ++b) {
+                        scale[b] = scale1[b];
+                        zero[b] = zero1[b];
+                    }
                 } else {  // the other set's
                     s += (n + C::kKb - 1) / C::kKb;
                     if (s >= kStages) {
@@ -635,10 +640,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-template <bool W4, bool BF16, int NT>
+template <bool W4, bool BF16, int NT, bool G128>
 cudaError_t run(const CUtensorMap* maps, const SwapParams* p, int grid, cudaStream_t stream)
 {
-    auto* kernel = ffn_swap_kernel<W4, BF16, NT>;
+    auto* kernel = ffn_swap_kernel<W4, BF16, NT, G128>;
     if (!p)
         return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<W4, NT>::kSmem);
     cudaLaunchAttribute attr[2];
@@ -658,32 +663,41 @@ cudaError_t run(const CUtensorMap* maps, const SwapParams* p, int grid, cudaStre
     return cudaLaunchKernelEx(&cfg, kernel, maps[0], maps[1], maps[2], *p);
 }
 
-template <bool W4, bool BF16>
+template <bool W4, bool BF16, bool G128>
 cudaError_t by_tokens(int nt, const CUtensorMap* maps, const SwapParams* p, int grid, cudaStream_t stream)
 {
     switch (nt) {
-    case 32: return run<W4, BF16, 32>(maps, p, grid, stream);
-    case 64: return run<W4, BF16, 64>(maps, p, grid, stream);
-    case 128: return run<W4, BF16, 128>(maps, p, grid, stream);
+    case 32: return run<W4, BF16, 32, G128>(maps, p, grid, stream);
+    case 64: return run<W4, BF16, 64, G128>(maps, p, grid, stream);
+    case 128: return run<W4, BF16, 128, G128>(maps, p, grid, stream);
     default:
         if constexpr (W4)
-            return run<W4, BF16, 256>(maps, p, grid, stream);
+            return run<W4, BF16, 256, G128>(maps, p, grid, stream);
         else
             return cudaErrorInvalidValue;
     }
+}
+
+cudaError_t by_kind(bool w4, bool bf16, bool g128, int nt, const CUtensorMap* maps, const SwapParams* p, int grid,
+                    cudaStream_t stream)
+{
+    if (!w4)  // (the 16-bit types differ in the instruction descriptor alone)
+        return by_tokens<false, true, false>(nt, maps, p, grid, stream);
+    if (bf16)
+        return g128 ? by_tokens<true, true, true>(nt, maps, p, grid, stream) : by_tokens<true, true, false>(nt, maps, p, grid, stream);
+    return g128 ? by_tokens<true, false, true>(nt, maps, p, grid, stream) : by_tokens<true, false, false>(nt, maps, p, grid, stream);
 }
 
 }  // namespace
 
 cudaError_t ffn_swap_configure()
 {
-    for (int nt : {32, 64, 128, 256}) {
-        cudaError_t e = by_tokens<true, true>(nt, nullptr, nullptr, 0, nullptr);
-        if (e == cudaSuccess) e = by_tokens<true, false>(nt, nullptr, nullptr, 0, nullptr);
-        if (e == cudaSuccess && nt < 256) e = by_tokens<false, true>(nt, nullptr, nullptr, 0, nullptr);
-        if (e != cudaSuccess)
-            return e;
-    }
+    for (int nt : {32, 64, 128, 256})
+        for (int kind = nt == 256 ? 1 : 0; kind < 5; ++kind) {
+            const cudaError_t e = by_kind(kind > 0, kind & 1, kind > 2, nt, nullptr, nullptr, 0, nullptr);
+            if (e != cudaSuccess)
+                return e;
+        }
     return cudaSuccess;
 }
 
@@ -719,9 +733,7 @@ cudaError_t ffn_swap_launch(const FfnParams& f, int num_sms, cudaStream_t stream
         p.whole = f.n % 16 == 0 ? (f.n + 63) / 64 * 64 : f.n;
     }
     const int grid = p.splits > 1 ? p.num_tiles * p.splits : std::min(p.num_tiles, num_sms);
-    if (!w4)  // (the 16-bit forms differ in the instruction descriptor alone)
-        return by_tokens<false, true>(nt, maps, &p, grid, stream);
-    return f.bf16 ? by_tokens<true, true>(nt, maps, &p, grid, stream) : by_tokens<true, false>(nt, maps, &p, grid, stream);
+    return by_kind(w4, f.bf16, f.group_shift == 7, nt, maps, &p, grid, stream);
 }
 
 }  // namespace gnt
