@@ -77,6 +77,7 @@ struct Cfg {
 struct SwapParams {
     FfnParams f;
     int tiles_w, tiles_t, num_tiles, num_kb, splits;
+    int vec_s, vec_z;  // rows of scales and zeros on 16- and 8-byte boundaries
     int whole;  // gated: tiles whose outputs end here are whole boxes of the interleaved map
     uint32_t idesc;
 };
@@ -226,8 +227,8 @@ __device__ __forceinline__ void store_tokens(const FfnParams& p, int o0, int row
     }
 }
 
-// G128: groups of 128.
-template <bool W4, bool BF16, int NT, bool G128>
+// GS: the group's length, as a shift.
+template <bool W4, bool BF16, int NT, int GS>
 __global__ void __launch_bounds__(kThreads, 1)
     ffn_swap_kernel(const __grid_constant__ CUtensorMap tmw, const __grid_constant__ CUtensorMap tmi,
                     const __grid_constant__ CUtensorMap tmx, const SwapParams p)
@@ -481,28 +482,56 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int64_t at = o < f.n ? row : static_cast<int64_t>(f.n) - 1;
             const uint16_t* srow = static_cast<const uint16_t*>(f.scales) + at * f.lds;
             const uint8_t* zrow = f.zeros ? f.zeros + at * f.ldz : nullptr;
-            // the scales and zeros of a stage of codes, two of groups of 128 and else one for
-            // every k-block, fetched a turn ahead; what lies four stages ahead is brought near
-            constexpr int NS = G128 ? 2 : kRawKb;
-            uint32_t scale[NS], zero[NS], scale1[NS], zero1[NS];
-            const auto fetch = [&](int kb, uint32_t (&sc)[NS], uint32_t (&ze)[NS]) {
+            // Scales and zeros come eight groups at a time, those of one, two or four stages of
+            // codes, in one 16-byte and one 8-byte load a thread, a turn of this set ahead of
+            // their use: each load of a warp touches 32 rows, and two of single scales a stage
+            // cost 64 x 16384 x 8192 5 us.
+            const int chunks = ((f.k - 1) >> (GS + 3)) + 1, last = (f.k - 1) >> GS;
+            const auto fetch = [&](int kb, uint4& sc, uint2& ze) {
+                const int ch = min(kb * BK >> (GS + 3), chunks - 1);
+                const bool whole = 8 * ch + 8 <= last + 1;  // (no element past a row's last is read)
+                if (whole && p.vec_s) {
+                    sc = __ldg(reinterpret_cast<const uint4*>(srow) + ch);
+                } else {
+                    uint32_t v[8];
 #pragma unroll
-                for (int b = 0; b < NS; ++b) {
-                    const int g = min((kb + b * (kRawKb / NS)) * BK + (G128 ? 0 : half * 32), f.k - 1) >> f.group_shift;
-                    sc[b] = __ldg(srow + g);
-                    ze[b] = 8;
-                    if (zrow)
-                        ze[b] = __ldg(zrow + g);
+                    for (int b = 0; b < 8; ++b)
+                        v[b] = __ldg(srow + min(8 * ch + b, last));
+                    sc = make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16);
+                }
+                ze = make_uint2(0x08080808u, 0x08080808u);
+                if (zrow && whole && p.vec_z) {
+                    ze = __ldg(reinterpret_cast<const uint2*>(zrow) + ch);
+                } else if (zrow) {
+                    uint32_t v[8];
+#pragma unroll
+                    for (int b = 0; b < 8; ++b)
+                        v[b] = __ldg(zrow + min(8 * ch + b, last));
+                    ze = make_uint2(v[0] | v[1] << 8 | v[2] << 16 | v[3] << 24, v[4] | v[5] << 8 | v[6] << 16 | v[7] << 24);
                 }
             };
-            fetch(c.kb0 + (turn != set ? kRawKb : 0), scale, zero);
+            uint4 scales, scales1;
+            uint2 zeros, zeros1;
+            fetch(c.kb0 + (turn != set ? kRawKb : 0), scales, zeros);
             for (int kb = c.kb0; ok && kb < c.kb1; kb += kRawKb) {
                 const int n = min(kRawKb, c.kb1 - kb);
                 if (turn == set) {
-                    fetch(kb + kConvSets * kRawKb, scale1, zero1);
-                    {
-                        const int g = min((kb + 4 * kRawKb) * BK, f.k - 1) >> f.group_shift;
-                        asm volatile("prefetch.global.L1 [%0];" ::"l"(srow + g));
+                    fetch(kb + kConvSets * kRawKb, scales1, zeros1);
+                    // the groups of this stage's k-blocks, first of them `first` of the eight
+                    const int first = kb * BK >> GS & 7;
+                    uint32_t sw[2], zw;  // scales 0-3 and zeros 0-3 of the stage (of shorter groups: this half's)
+                    if (GS == 7) {
+                        sw[0] = first & 4 ? (first & 2 ? scales.w : scales.z) : (first & 2 ? scales.y : scales.x);
+                        sw[1] = 0;
+                        zw = (first & 4 ? zeros.y : zeros.x) >> (first & 2 ? 16 : 0);
+                    } else if (GS == 6) {
+                        sw[0] = first & 4 ? scales.z : scales.x;
+                        sw[1] = first & 4 ? scales.w : scales.y;
+                        zw = first & 4 ? zeros.y : zeros.x;
+                    } else {
+                        sw[0] = __byte_perm(scales.x, scales.y, half ? 0x7632 : 0x5410);
+                        sw[1] = __byte_perm(scales.z, scales.w, half ? 0x7632 : 0x5410);
+                        zw = __byte_perm(zeros.x, zeros.y, half ? 0x7531 : 0x6420);
                     }
                     if (!wait_bounded(smem_u32(&raw_full[rs]), rphase, abort_flag, limit)) {
                         gave_up();
@@ -526,8 +555,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                             const int jb = j + b;
                             const uint4 w = lds128(raw0 + rs * kRawBytes + (((2 * jb + half) ^ swz) << 4));
                             const uint32_t words[4] = {w.x, w.y, w.z, w.w};
-                            const uint32_t scale2 = __byte_perm(scale[jb * NS / kRawKb], 0, 0x1010);
-                            const uint32_t zero2 = __byte_perm(zero[jb * NS / kRawKb], BF16 ? 0x43 : 0x64, 0x4040);
+                            const int at = GS == 7 ? jb >> 1 : jb;
+                            const uint32_t scale2 = __byte_perm(sw[at >> 1], 0, at & 1 ? 0x3232 : 0x1010);
+                            const uint32_t zero2 = __byte_perm(zw, BF16 ? 0x43 : 0x64, 0x4040 | at | at << 8);
                             uint32_t out[16];
 #pragma unroll
                             for (int e = 0; e < 4; ++e)
@@ -555,11 +585,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     __syncwarp();
                     if (lane == 0)
                         mbar_arrive(smem_u32(&raw_empty[rs]));
-#pragma unroll
-                    for (int b = 0; b < NS; ++b) {
-                        scale[b] = scale1[b];
-                        zero[b] = zero1[b];
-                    }
+                    scales = scales1;
+                    zeros = zeros1;
                 } else {  // the other set's
                     s += (n + C::kKb - 1) / C::kKb;
                     if (s >= kStages) {
@@ -640,10 +667,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-template <bool W4, bool BF16, int NT, bool G128>
+template <bool W4, bool BF16, int NT, int GS>
 cudaError_t run(const CUtensorMap* maps, const SwapParams* p, int grid, cudaStream_t stream)
 {
-    auto* kernel = ffn_swap_kernel<W4, BF16, NT, G128>;
+    auto* kernel = ffn_swap_kernel<W4, BF16, NT, GS>;
     if (!p)
         return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<W4, NT>::kSmem);
     cudaLaunchAttribute attr[2];
@@ -663,29 +690,37 @@ cudaError_t run(const CUtensorMap* maps, const SwapParams* p, int grid, cudaStre
     return cudaLaunchKernelEx(&cfg, kernel, maps[0], maps[1], maps[2], *p);
 }
 
-template <bool W4, bool BF16, bool G128>
+template <bool W4, bool BF16, int GS>
 cudaError_t by_tokens(int nt, const CUtensorMap* maps, const SwapParams* p, int grid, cudaStream_t stream)
 {
     switch (nt) {
-    case 32: return run<W4, BF16, 32, G128>(maps, p, grid, stream);
-    case 64: return run<W4, BF16, 64, G128>(maps, p, grid, stream);
-    case 128: return run<W4, BF16, 128, G128>(maps, p, grid, stream);
+    case 32: return run<W4, BF16, 32, GS>(maps, p, grid, stream);
+    case 64: return run<W4, BF16, 64, GS>(maps, p, grid, stream);
+    case 128: return run<W4, BF16, 128, GS>(maps, p, grid, stream);
     default:
         if constexpr (W4)
-            return run<W4, BF16, 256, G128>(maps, p, grid, stream);
+            return run<W4, BF16, 256, GS>(maps, p, grid, stream);
         else
             return cudaErrorInvalidValue;
     }
 }
 
-cudaError_t by_kind(bool w4, bool bf16, bool g128, int nt, const CUtensorMap* maps, const SwapParams* p, int grid,
-                    cudaStream_t stream)
+template <bool BF16>
+cudaError_t by_group(int shift, int nt, const CUtensorMap* maps, const SwapParams* p, int grid, cudaStream_t stream)
 {
-    if (!w4)  // (the 16-bit types differ in the instruction descriptor alone)
-        return by_tokens<false, true, false>(nt, maps, p, grid, stream);
-    if (bf16)
-        return g128 ? by_tokens<true, true, true>(nt, maps, p, grid, stream) : by_tokens<true, true, false>(nt, maps, p, grid, stream);
-    return g128 ? by_tokens<true, false, true>(nt, maps, p, grid, stream) : by_tokens<true, false, false>(nt, maps, p, grid, stream);
+    switch (shift) {
+    case 5: return by_tokens<true, BF16, 5>(nt, maps, p, grid, stream);
+    case 6: return by_tokens<true, BF16, 6>(nt, maps, p, grid, stream);
+    default: return by_tokens<true, BF16, 7>(nt, maps, p, grid, stream);
+    }
+}
+
+// shift 0: 16-bit weights (whose types differ in the instruction descriptor alone).
+cudaError_t by_kind(int shift, bool bf16, int nt, const CUtensorMap* maps, const SwapParams* p, int grid, cudaStream_t stream)
+{
+    if (shift == 0)
+        return by_tokens<false, true, 0>(nt, maps, p, grid, stream);
+    return bf16 ? by_group<true>(shift, nt, maps, p, grid, stream) : by_group<false>(shift, nt, maps, p, grid, stream);
 }
 
 }  // namespace
@@ -693,11 +728,14 @@ cudaError_t by_kind(bool w4, bool bf16, bool g128, int nt, const CUtensorMap* ma
 cudaError_t ffn_swap_configure()
 {
     for (int nt : {32, 64, 128, 256})
-        for (int kind = nt == 256 ? 1 : 0; kind < 5; ++kind) {
-            const cudaError_t e = by_kind(kind > 0, kind & 1, kind > 2, nt, nullptr, nullptr, 0, nullptr);
-            if (e != cudaSuccess)
-                return e;
-        }
+        for (int shift : {0, 5, 6, 7})
+            for (bool bf16 : {true, false}) {
+                if (shift == 0 && (!bf16 || nt == 256))
+                    continue;
+                const cudaError_t e = by_kind(shift, bf16, nt, nullptr, nullptr, 0, nullptr);
+                if (e != cudaSuccess)
+                    return e;
+            }
     return cudaSuccess;
 }
 
@@ -713,6 +751,9 @@ cudaError_t ffn_swap_launch(const FfnParams& f, int num_sms, cudaStream_t stream
     p.num_tiles = p.tiles_w * p.tiles_t;  // (the caller's bound)
     p.num_kb = static_cast<int>((int64_t(f.k) + BK - 1) / BK);
     p.idesc = idesc_f16_f32(128, nt) | (f.bf16 ? (1u << 7) | (1u << 10) : 0u);
+    const auto on = [](const void* q, uintptr_t a, int64_t bytes) { return reinterpret_cast<uintptr_t>(q) % a == 0 && bytes % a == 0; };
+    p.vec_s = on(f.scales, 16, 2 * f.lds);
+    p.vec_z = on(f.zeros, 8, f.ldz);
     // Few tiles: clusters share out K, down to two stages of codes (512 of K) each.
     p.splits = 1;
     const int groups = (p.num_kb + kRawKb - 1) / kRawKb;
@@ -733,7 +774,7 @@ cudaError_t ffn_swap_launch(const FfnParams& f, int num_sms, cudaStream_t stream
         p.whole = f.n % 16 == 0 ? (f.n + 63) / 64 * 64 : f.n;
     }
     const int grid = p.splits > 1 ? p.num_tiles * p.splits : std::min(p.num_tiles, num_sms);
-    return by_kind(w4, f.bf16, f.group_shift == 7, nt, maps, &p, grid, stream);
+    return by_kind(f.group_shift, f.bf16, nt, maps, &p, grid, stream);
 }
 
 }  // namespace gnt
