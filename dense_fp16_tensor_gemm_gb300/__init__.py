@@ -762,26 +762,30 @@ def moe_few_tokens(X, logits, W13, W2, topk, S13=None, S2=None, renormalize=True
 
 
 # ---------------------------------------------------------------- the gated feed-forward block, 4-bit weights
+# (As above, written for the host's time per call: on a Grace core a helper's call or an
+# attribute of a tensor costs 0.1-0.3 us of the 8 that a launch with one allocation takes.)
 _ACTS = {"silu": 0, "gelu": 1, "gelu_tanh": 2}
+_GROUPS = (32, 64, 128)
+_FFN_SHAPES = "shapes: X (tokens, hidden), W13 (2*inner, hidden)"
 
 
 def _act(activation):
-    if activation not in _ACTS:
+    act = _ACTS.get(activation)
+    if act is None:
         raise ValueError("activation must be one of %s" % ", ".join(_ACTS))
-    return _ACTS[activation]
+    return act
 
 
-def _rows(n, width, dtype, device):
-    """An empty (n, width) matrix of 16-bit elements whose rows start on 16-byte boundaries."""
-    return _torch.empty_strided((n, width), ((width + 7) // 8 * 8, 1), dtype=dtype, device=device)
+def _rows(n, width, like):
+    """An empty (n, width) matrix of `like`'s type whose rows start on 16-byte boundaries."""
+    return _torch.empty_strided((n, width), ((width + 7) // 8 * 8, 1), dtype=like.dtype, device=like.device)
 
 
-def _out16(out, n, width, like):
-    if out is None:
-        return _rows(n, width, like.dtype, like.device)
-    if tuple(out.shape) != (n, width) or out.dtype != like.dtype:
+def _given(out, n, width, like):
+    """Checks the caller's own output; its pitch."""
+    if out.shape != (n, width) or out.dtype != like.dtype:
         raise ValueError("out must have shape (%d,%d) and X's type" % (n, width))
-    return out
+    return _pitch(out.shape, out.stride(), "out")
 
 
 def gated_linear(X, W13, activation="silu", keep=False, out=None, path=Path.AUTO, stream=None):
@@ -792,24 +796,31 @@ def gated_linear(X, W13, activation="silu", keep=False, out=None, path=Path.AUTO
     X @ W13.T in X's type, which :func:`gated_linear_backward` takes.  Rows of what is
     returned start on 16-byte boundaries.
     """
-    side = _elsewhere(stream)
-    if side is not None:
-        return _run_on(side, gated_linear, X, W13, activation, keep, out, path, given=out)
+    if stream is not None:
+        side = _elsewhere(stream)
+        if side is not None:
+            return _run_on(side, gated_linear, X, W13, activation, keep, out, path, given=out)
     _torch or _init_torch()
     xsh, wsh = X.shape, W13.shape
     if len(xsh) != 2 or len(wsh) != 2 or wsh[1] != xsh[1] or wsh[0] % 2:
-        raise ValueError("shapes: X (tokens, hidden), W13 (2*inner, hidden)")
+        raise ValueError(_FFN_SHAPES)
     if W13.dtype != X.dtype:
         raise TypeError("X and W13 must have the same type")
     code, act = _one_of(X.dtype, _X16, "X"), _act(activation)
     tokens, hidden = xsh
     inner = wsh[0] // 2
+    ldx, ldw = _pitch(xsh, X.stride(), "X"), _pitch(wsh, W13.stride(), "W13")
     index = _same_device(X, W13, out)
-    out = _out16(out, tokens, inner, X)
-    gu = _rows(tokens, 2 * inner, X.dtype, X.device) if keep else None
-    gemm_nt_gated(X.data_ptr(), _pitch(xsh, X.stride(), "X"), W13.data_ptr(), _pitch(wsh, W13.stride(), "W13"),
-                  out.data_ptr(), _pitch(out.shape, out.stride(), "out"), gu.data_ptr() if keep else 0,
-                  gu.stride(0) if keep else 0, code, act, tokens, hidden, inner, path, _stream_of(index))
+    if out is None:
+        out, ldh = _rows(tokens, inner, X), (inner + 7) // 8 * 8
+    else:
+        ldh = _given(out, tokens, inner, X)
+    gu = _rows(tokens, 2 * inner, X) if keep else None
+    status = (_lib or load()).gemm_nt_gated(X.data_ptr(), ldx, W13.data_ptr(), ldw, out.data_ptr(), ldh,
+                                            gu.data_ptr() if keep else None, (inner + 3) // 4 * 8, code, act, tokens,
+                                            hidden, inner, path, _stream_of(index))
+    if status:
+        raise GemmError(status)
     return (out, gu) if keep else out
 
 
@@ -825,26 +836,24 @@ def gated_linear_backward(dH, GU, X, W13, activation="silu", stream=None):
     _torch or _init_torch()
     xsh, wsh = X.shape, W13.shape
     if len(xsh) != 2 or len(wsh) != 2 or wsh[1] != xsh[1] or wsh[0] % 2:
-        raise ValueError("shapes: X (tokens, hidden), W13 (2*inner, hidden)")
+        raise ValueError(_FFN_SHAPES)
     tokens, hidden = xsh
     rows = wsh[0]
-    if tuple(dH.shape) != (tokens, rows // 2) or tuple(GU.shape) != (tokens, rows):
+    if dH.shape != (tokens, rows // 2) or GU.shape != (tokens, rows):
         raise ValueError("shapes: dH (tokens, inner), GU (tokens, 2*inner)")
     if not X.dtype == W13.dtype == dH.dtype == GU.dtype:
         raise TypeError("dH, GU, X and W13 must have the same type")
     code, act = _one_of(X.dtype, _X16, "X"), _act(activation)
     ldx, ldw = _pitch(xsh, X.stride(), "X"), _pitch(wsh, W13.stride(), "W13")
     ldd, ldg = _pitch(dH.shape, dH.stride(), "dH"), _pitch(GU.shape, GU.stride(), "GU")
-    index = _same_device(X, W13, dH, GU)
-    stream, device = _stream_of(index), X.device
-    dgu = _rows(tokens, rows, X.dtype, device)
-    ldo = dgu.stride(0)
-    gemm_nt_gated_grad(dH.data_ptr(), ldd, GU.data_ptr(), ldg, dgu.data_ptr(), ldo, code, act, tokens, rows // 2, stream)
-    dx, dw = _rows(tokens, hidden, X.dtype, device), _rows(rows, hidden, X.dtype, device)
-    gemm_nt_batched_major(dgu.data_ptr(), 0, W13.data_ptr(), 1, dx.data_ptr(), code, code, tokens, hidden, rows, ldo, ldw,
-                          dx.stride(0), 0, 0, 0, 1, 0, stream)
-    gemm_nt_batched_major(dgu.data_ptr(), 1, X.data_ptr(), 1, dw.data_ptr(), code, code, rows, hidden, tokens, ldo, ldx,
-                          dw.stride(0), 0, 0, 0, 1, 0, stream)
+    stream = _stream_of(_same_device(X, W13, dH, GU))
+    dgu, dx, dw = _rows(tokens, rows, X), _rows(tokens, hidden, X), _rows(rows, hidden, X)
+    at, ldo, ldout = dgu.data_ptr(), (rows + 7) // 8 * 8, (hidden + 7) // 8 * 8
+    gemm_nt_gated_grad(dH.data_ptr(), ldd, GU.data_ptr(), ldg, at, ldo, code, act, tokens, rows // 2, stream)
+    gemm_nt_batched_major(at, 0, W13.data_ptr(), 1, dx.data_ptr(), code, code, tokens, hidden, rows, ldo, ldw, ldout,
+                          0, 0, 0, 1, 0, stream)
+    gemm_nt_batched_major(at, 1, X.data_ptr(), 1, dw.data_ptr(), code, code, rows, hidden, tokens, ldo, ldx, ldout,
+                          0, 0, 0, 1, 0, stream)
     return dx, dw
 
 
@@ -859,9 +868,10 @@ def quantize_w4(W, group=128, zeros=False, scale_dtype=None, stream=None):
     column in the low half of a byte, rows on 16-byte boundaries; S (rows,
     ceil(cols/group)); Z the same, uint8.
     """
-    side = _elsewhere(stream)
-    if side is not None:
-        return _run_on(side, quantize_w4, W, group, zeros, scale_dtype)
+    if stream is not None:
+        side = _elsewhere(stream)
+        if side is not None:
+            return _run_on(side, quantize_w4, W, group, zeros, scale_dtype)
     torch = _torch or _init_torch()
     shape = W.shape
     if len(shape) != 2:
@@ -869,7 +879,7 @@ def quantize_w4(W, group=128, zeros=False, scale_dtype=None, stream=None):
     wt = _one_of(W.dtype, _OUT, "W")
     scale_dtype = scale_dtype or (torch.bfloat16 if wt == 2 else W.dtype)
     st = _one_of(scale_dtype, _X16, "scale_dtype")
-    if group not in (32, 64, 128):
+    if group not in _GROUPS:
         raise ValueError("group must be 32, 64 or 128")
     ldw = _pitch(shape, W.stride(), "W")
     rows, cols = shape
@@ -879,60 +889,69 @@ def quantize_w4(W, group=128, zeros=False, scale_dtype=None, stream=None):
     q = torch.empty_strided((rows, width), (pitch, 1), dtype=torch.uint8, device=device)
     s = torch.empty((rows, groups), dtype=scale_dtype, device=device)
     z = torch.empty((rows, groups), dtype=torch.uint8, device=device) if zeros else None
-    gemm_nt_w4_quantize(W.data_ptr(), wt, rows, cols, ldw,
-                        Weights4(q.data_ptr(), pitch, s.data_ptr(), groups, z.data_ptr() if zeros else None, groups, group),
-                        st, _stream_of(index))
+    into = Weights4(q.data_ptr(), pitch, s.data_ptr(), groups, z.data_ptr() if zeros else None, groups, group)
+    status = (_lib or load()).gemm_nt_w4_quantize(W.data_ptr(), wt, rows, cols, ldw, into, st, _stream_of(index))
+    if status:
+        raise GemmError(status)
     return (q, s, z) if zeros else (q, s)
 
 
-def _weights4(Q, S, Z, X, group):
-    """4-bit weights for X's columns as the C struct, and their rows."""
-    if group not in (32, 64, 128):
+def _w4_product(X, Q, S, Z, group, act, out, path):
+    """The plain product with 4-bit weights, or (act not None) the gated one."""
+    torch = _torch or _init_torch()
+    dtype, xsh, qsh, ssh = X.dtype, X.shape, Q.shape, S.shape
+    code = _one_of(dtype, _X16, "X")
+    if group not in _GROUPS:
         raise ValueError("group must be 32, 64 or 128")
-    if X.dim() != 2 or Q.dim() != 2 or S.dim() != 2 or Z is not None and Z.dim() != 2:
-        raise ValueError("X, Q, S and Z must be matrices")
-    if Q.dtype != _torch.uint8 or S.dtype != X.dtype or Z is not None and Z.dtype != _torch.uint8:
+    if len(xsh) != 2 or len(qsh) != 2:
+        raise ValueError("X and Q must be matrices")
+    if Q.dtype != torch.uint8 or S.dtype != dtype or Z is not None and Z.dtype != torch.uint8:
         raise TypeError("Q and Z must be uint8, S of X's type")
-    rows, cols = Q.shape[0], X.shape[1]
-    shape = (rows, (cols + group - 1) // group)
-    if Q.shape[1] != (cols + 1) // 2 or tuple(S.shape) != shape or Z is not None and tuple(Z.shape) != shape:
-        raise ValueError("shapes for %d columns: Q (rows, %d), S and Z (rows, %d)" % (cols, (cols + 1) // 2, shape[1]))
-    return Weights4(Q.data_ptr(), _pitch(Q.shape, Q.stride(), "Q"), S.data_ptr(), _pitch(shape, S.stride(), "S"),
-                    None if Z is None else Z.data_ptr(), 0 if Z is None else _pitch(shape, Z.stride(), "Z"), group), rows
+    tokens, cols = xsh
+    rows, width = qsh
+    groups = (cols + group - 1) // group
+    if width != (cols + 1) // 2 or ssh != (rows, groups) or Z is not None and Z.shape != ssh:
+        raise ValueError("shapes for %d columns: Q (rows, %d), S and Z (rows, %d)" % (cols, (cols + 1) // 2, groups))
+    if act is not None and rows % 2:
+        raise ValueError("Q13 must have 2*inner rows")
+    ldx = _pitch(xsh, X.stride(), "X")
+    weights = Weights4(Q.data_ptr(), _pitch(qsh, Q.stride(), "Q"), S.data_ptr(), _pitch(ssh, S.stride(), "S"),
+                       None if Z is None else Z.data_ptr(), 0 if Z is None else _pitch(ssh, Z.stride(), "Z"), group)
+    index = _same_device(X, Q, S, Z, out)
+    n = rows if act is None else rows // 2
+    if out is None:
+        ldo = (n + 7) // 8 * 8
+        out = torch.empty_strided((tokens, n), (ldo, 1), dtype=dtype, device=X.device)
+    else:
+        ldo = _given(out, tokens, n, X)
+    lib = _lib or load()
+    if act is None:
+        status = lib.gemm_nt_w4(X.data_ptr(), ldx, weights, out.data_ptr(), ldo, code, tokens, n, cols, path,
+                                _stream_of(index))
+    else:
+        status = lib.gemm_nt_w4_gated(X.data_ptr(), ldx, weights, out.data_ptr(), ldo, code, act, tokens, cols, n, path,
+                                      _stream_of(index))
+    if status:
+        raise GemmError(status)
+    return out
 
 
 def linear_w4(X, Q, S, Z=None, group=128, out=None, path=Path.AUTO, stream=None):
     """Y = X @ W.T with the 4-bit weights of :func:`quantize_w4`: X (tokens, in)
     float16 or bfloat16, Q, S and Z of W (out, in), S in X's type.  Sums are
     float32; Y (tokens, out) has X's type, its rows start on 16-byte boundaries."""
-    side = _elsewhere(stream)
-    if side is not None:
-        return _run_on(side, linear_w4, X, Q, S, Z, group, out, path, given=out)
-    _torch or _init_torch()
-    code = _one_of(X.dtype, _X16, "X")
-    w, rows = _weights4(Q, S, Z, X, group)
-    tokens, cols = X.shape
-    index = _same_device(X, Q, S, Z, out)
-    out = _out16(out, tokens, rows, X)
-    gemm_nt_w4(X.data_ptr(), _pitch(X.shape, X.stride(), "X"), w, out.data_ptr(), _pitch(out.shape, out.stride(), "out"),
-               code, tokens, rows, cols, path, _stream_of(index))
-    return out
+    if stream is not None:
+        side = _elsewhere(stream)
+        if side is not None:
+            return _run_on(side, _w4_product, X, Q, S, Z, group, None, out, path, given=out)
+    return _w4_product(X, Q, S, Z, group, None, out, path)
 
 
 def gated_linear_w4(X, Q13, S13, Z13=None, group=128, activation="silu", out=None, path=Path.AUTO, stream=None):
     """:func:`gated_linear` with the 4-bit weights of :func:`quantize_w4` in W13's place."""
-    side = _elsewhere(stream)
-    if side is not None:
-        return _run_on(side, gated_linear_w4, X, Q13, S13, Z13, group, activation, out, path, given=out)
-    _torch or _init_torch()
-    code, act = _one_of(X.dtype, _X16, "X"), _act(activation)
-    w, rows = _weights4(Q13, S13, Z13, X, group)
-    if rows % 2:
-        raise ValueError("Q13 must have 2*inner rows")
-    tokens, hidden = X.shape
-    index = _same_device(X, Q13, S13, Z13, out)
-    out = _out16(out, tokens, rows // 2, X)
-    gemm_nt_w4_gated(X.data_ptr(), _pitch(X.shape, X.stride(), "X"), w, out.data_ptr(),
-                     _pitch(out.shape, out.stride(), "out"), code, act, tokens, hidden, rows // 2, path,
-                     _stream_of(index))
-    return out
+    act = _act(activation)
+    if stream is not None:
+        side = _elsewhere(stream)
+        if side is not None:
+            return _run_on(side, _w4_product, X, Q13, S13, Z13, group, act, out, path, given=out)
+    return _w4_product(X, Q13, S13, Z13, group, act, out, path)
