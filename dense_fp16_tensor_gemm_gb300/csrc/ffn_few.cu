@@ -143,7 +143,7 @@ struct Cfg {
 
 // NT: sets of 8 tokens; 0: a single token.  G128: groups of 128.
 template <bool BF16, bool W4, bool GATED, int NTOK, int WARPS, bool G128>
-__global__ void __launch_bounds__(32 * WARPS, WARPS == 8 ? 3 : 1) ffn_few_kernel(const FfnParams p, int vec_x, int vec_s, int tiles)
+__global__ void __launch_bounds__(32 * WARPS, WARPS == 8 ? 3 : 1) ffn_few_kernel(const FfnParams p, int vec_x, int vec_s, int vec_z, int tiles)
 {
     using S = OutStore<BF16 ? kOutBF16 : kOutF16>;
     constexpr int NT = NTOK ? NTOK : 1;
@@ -222,27 +222,32 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS == 8 ? 3 : 1) ffn_few_kernel
             if (W4) {
                 const int k = step * kStepK + (G128 ? 0 : 64 * t);
                 const int g0 = k >> p.group_shift, g1 = (k + (G128 ? 128 : 32)) >> p.group_shift;
-                if ((step + 1) * kStepK <= p.k && vec_s) {
+                // Nothing is done here with what is loaded that would have to wait for it: a
+                // pair comes in one load, and of groups of 64, both elements 64 t and 64 t + 32
+                // of which are in one, the lower half alone is looked at.
+                const bool single = !G128 && p.group_shift == 6;
+                const bool inside = (step + 1) * kStepK <= p.k;
+                // past K: the last group's, whose end may lie there
+                const int last = (p.k - 1) >> p.group_shift;
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        // (one group of 64 is both of the pair)
-                        if (G128 || p.group_shift == 5)
-                            sc[h] = __ldg(reinterpret_cast<const uint32_t*>(srow[h] + g0));
-                        else
-                            sc[h] = __ldg(srow[h] + g0) * 0x10001u;
-                    }
-                } else {
-                    // past K: the last group's, whose end may lie there
-                    const int last = (p.k - 1) >> p.group_shift;
-#pragma unroll
-                    for (int h = 0; h < 2; ++h)
+                for (int h = 0; h < 2; ++h) {
+                    if (inside && !single && vec_s)
+                        sc[h] = __ldg(reinterpret_cast<const uint32_t*>(srow[h] + g0));
+                    else if (inside && single)
+                        sc[h] = __ldg(srow[h] + g0);
+                    else
                         sc[h] = __ldg(srow[h] + min(g0, last)) | static_cast<uint32_t>(__ldg(srow[h] + min(g1, last))) << 16;
                 }
                 if (p.zeros) {
-                    const int last = (p.k - 1) >> p.group_shift;
 #pragma unroll
-                    for (int h = 0; h < 2; ++h)
-                        ze[h] = __ldg(zrow[h] + min(g0, last)) | static_cast<uint32_t>(__ldg(zrow[h] + min(g1, last))) << 8;
+                    for (int h = 0; h < 2; ++h) {
+                        if (inside && !single && vec_z)
+                            ze[h] = __ldg(reinterpret_cast<const uint16_t*>(zrow[h] + g0));
+                        else if (inside && single)
+                            ze[h] = __ldg(zrow[h] + g0);
+                        else
+                            ze[h] = __ldg(zrow[h] + min(g0, last)) | static_cast<uint32_t>(__ldg(zrow[h] + min(g1, last))) << 8;
+                    }
                 }
             }
             if (++fi == count) {
@@ -335,8 +340,11 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS == 8 ? 3 : 1) ffn_few_kernel
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         if (!G128) {
-                            f[h] = scale_of<BF16>(__shfl_sync(0xffffffffu, s[h], (lane & ~3) | (j >> 1)), j & 1);
-                            zero[h] = zero_of<BF16>(__shfl_sync(0xffffffffu, z[h], (lane & ~3) | (j >> 1)), j & 1);
+                            const uint32_t sv = __shfl_sync(0xffffffffu, s[h], (lane & ~3) | (j >> 1));
+                            const uint32_t zv = __shfl_sync(0xffffffffu, z[h], (lane & ~3) | (j >> 1));
+                            const bool high = j & 1 && p.group_shift == 5;
+                            f[h] = high ? scale_of<BF16>(sv, 1) : scale_of<BF16>(sv, 0);
+                            zero[h] = high ? zero_of<BF16>(zv, 1) : zero_of<BF16>(zv, 0);
                             words[h][j & 3] = lds32(piece(j) + slot * kStep + 1024 * h + t * 4);
                         }
 #pragma unroll
@@ -454,6 +462,7 @@ cudaError_t run(const FfnParams& p, int num_sms, cudaStream_t stream, bool confi
         return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
     const int vec_x = reinterpret_cast<uintptr_t>(p.x) % 16 == 0 && p.ldx % 8 == 0;
     const int vec_s = reinterpret_cast<uintptr_t>(p.scales) % 4 == 0 && p.lds % 2 == 0;  // pairs of scales
+    const int vec_z = reinterpret_cast<uintptr_t>(p.zeros) % 2 == 0 && p.ldz % 2 == 0;
     const int smem = C::kRing + C::kRed + static_cast<int>(x_bytes(p));
     constexpr int per = GATED ? 8 : 16;
     const int tiles = static_cast<int>((int64_t(p.n) + per - 1) / per);
@@ -468,7 +477,7 @@ cudaError_t run(const FfnParams& p, int num_sms, cudaStream_t stream, bool confi
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, p, vec_x, vec_s, tiles);
+    return cudaLaunchKernelEx(&cfg, kernel, p, vec_x, vec_s, vec_z, tiles);
 }
 
 template <bool BF16, bool W4, bool GATED, bool G128>
