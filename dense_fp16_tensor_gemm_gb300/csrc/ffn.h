@@ -89,7 +89,7 @@ cudaError_t ffn_few_launch(const FfnParams& p, int num_sms, cudaStream_t stream)
 
 // The weights as the MMA's rows; X and W on the 16-byte grid.  16-bit weights: up to
 // kSwapTokens tokens.
-constexpr int kSwapTokens = 128;
+constexpr int kSwapTokens = 64;
 bool interleaved_map(CUtensorMap* map, const void* base, int64_t n, int64_t K, int64_t ld, int dtype);
 cudaError_t ffn_swap_configure();  // one-time per device
 cudaError_t ffn_swap_launch(const FfnParams& p, int num_sms, cudaStream_t stream);

@@ -71,15 +71,34 @@ bool pair_ok(const FfnParams& p, const DeviceInfo& d)
     return p.gated && !p.scales && maps_ok(p) && d.gated_pairs > 0 && tiles <= INT32_MAX / 2;
 }
 
+// The warp MMA's kernel, which streams the weights for up to 16 tokens.
 bool few_ok(const FfnParams& p)
 {
     return p.k > 0 && p.k <= (1 << 29) && ffn_few_fits(p) && aligned(p.w, 16) && p.ldw * (p.scales ? 1 : 2) % 16 == 0;
 }
 
+// tcgen05 with the weights as rows, on single CTAs.
 bool swap_ok(const FfnParams& p)
 {
     const int64_t tiles = ((int64_t(p.tokens) + 31) / 32) * ((int64_t(p.n) + 63) / 64);
     return (p.scales || (p.gated && p.tokens <= kSwapTokens)) && maps_ok(p) && tiles <= INT32_MAX / 2;
+}
+
+// Whether the stream of the warp MMA is the faster of the two.  It starts 4 us sooner, but
+// its time grows with the tokens while the tensor cores' does not, so it has the smaller
+// weights.  Measured (us, stream and tcgen05), gated 16-bit: 1 token x 4096 x 8192 (134 MB)
+// 23.5 and 25.3; 8 tokens x 4096 x 4096 (67 MB) 17.0 and 17.6, x 8192 26.4 and 24.7; 16 tokens
+// x 2048 x 1024 (8 MB) 7.4 and 9.0, x 4096 x 2048 (34 MB) 15.9 and 12.9.  4-bit: 1 token x
+// 8192 x 16384 (67 MB) 22.0 and 29.4; 2 tokens x 4096 x 16384 (34 MB) 14.0 and 17.4; 4 tokens
+// 17.8 and 17.3; 8 tokens x 4096 x 8192 (17 MB) 13.6 and 13.3; 16 tokens x 2048 x 4096 (4 MB)
+// 7.9 and 9.1, x 4096 x 4096 (8 MB) 13.8 and 10.9.
+bool few_first(const FfnParams& p)
+{
+    const int64_t rows = p.gated ? 2 * int64_t(p.n) : p.n;
+    const int64_t mb = rows * p.k * (p.scales ? 1 : 4) / 2 >> 20;
+    if (p.scales)
+        return p.tokens == 1 || mb < (p.tokens == 2 ? 64 : p.tokens <= 4 ? 32 : p.tokens <= 8 ? 16 : 5);
+    return mb < (p.tokens == 1 ? 192 : p.tokens <= 8 ? 80 : 16);
 }
 
 // Selects the kernel and launches the product.
@@ -94,16 +113,18 @@ gemm_status_t run(FfnParams& p, gemm_path_t path, cudaStream_t stream)
     p.fault = d.fault;
     if (p.tokens == 1)
         p.ldx = (int64_t(p.k) + 7) / 8 * 8;  // a single row's pitch is never stepped by
-    if (path == GEMM_PATH_AUTO)
-        path = few_ok(p)    ? GEMM_PATH_SKINNY
-               : swap_ok(p) ? GEMM_PATH_TC05
-               : pair_ok(p, d) ? GEMM_PATH_TC05_PAIR
-                               : GEMM_PATH_MMASYNC;
-    if (path == GEMM_PATH_TC05 && swap_ok(p))
-        return status_of(ffn_swap_launch(p, d.num_sms, stream));
-    if (path == GEMM_PATH_SKINNY && few_ok(p))
+    const bool few = few_ok(p), swap = swap_ok(p), pair = pair_ok(p, d);
+    if (path == GEMM_PATH_AUTO) {
+        if (few && (!swap || few_first(p)))
+            path = GEMM_PATH_SKINNY;
+        else
+            path = swap ? GEMM_PATH_TC05 : (pair ? GEMM_PATH_TC05_PAIR : GEMM_PATH_MMASYNC);
+    }
+    if (path == GEMM_PATH_SKINNY && few)
         return status_of(ffn_few_launch(p, d.num_sms, stream));
-    if (path == GEMM_PATH_TC05_PAIR && pair_ok(p, d))
+    if (path == GEMM_PATH_TC05 && swap)
+        return status_of(ffn_swap_launch(p, d.num_sms, stream));
+    if (path == GEMM_PATH_TC05_PAIR && pair)
         return status_of(gated_pair_launch(p, d.gated_pairs, stream));
     if (path == GEMM_PATH_MMASYNC)
         return status_of(ffn_any_launch(p, d.num_sms, stream));

@@ -18,11 +18,9 @@
 // wait is bounded.
 #include <algorithm>
 
-#include "block128.h"
+#include "block128_tc.cuh"
 #include "ffn.h"
 #include "gemm_nt.h"
-#include "ptx.cuh"
-#include "tc05_common.cuh"
 
 namespace gnt {
 
@@ -208,7 +206,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMA issuer (leader)
-        if (lane == 0 && leader) {
+        // The whole warp walks the loop and one lane issues, so that descriptors stay in
+        // uniform registers.
+        if (leader) {
+            const bool one = blk::elect_one();
             const DescWords da = desc_words(smem_u32(as), false), db = desc_words(smem_u32(bs), false);
             int stage = 0, local = 0;
             uint32_t phase = 0;
@@ -216,7 +217,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             bool ok = true;
             for (int t = pair; ok && t < p.num_tiles; t += pairs, ++local) {
                 const int buf = local & 1;
-                if (!wait_bounded(smem_u32(&tempty[buf]), ((local >> 1) & 1) ^ 1, abort_flag, p.wait_limit)) {
+                if (!blk::wait_lanes(smem_u32(&tempty[buf]), ((local >> 1) & 1) ^ 1, abort_flag, p.wait_limit)) {
                     *abort_flag = 1;
                     atomicOr(p.status, kStatusTimeout);
                     break;
@@ -224,7 +225,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc_fence_after();
                 const uint32_t d = tmem_base + static_cast<uint32_t>(buf * 256);
                 for (int kb = 0; kb < p.num_kb; ++kb) {
-                    if (!wait_bounded(smem_u32(&full[stage]), phase, abort_flag, p.wait_limit)) {
+                    if (!blk::wait_lanes(smem_u32(&full[stage]), phase, abort_flag, p.wait_limit)) {
                         *abort_flag = 1;
                         atomicOr(p.status, kStatusTimeout);
                         ok = false;
@@ -232,12 +233,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     tc_fence_after();
                     const uint32_t alo = da.lo + stage * (kOpBytes >> 4), blo = db.lo + stage * (kOpBytes >> 4);
+                    if (one) {
 #pragma unroll
-                    for (int k = 0; k < BK / 16; ++k)
-                        tc_mma_pair_w<false>(d, alo + k * da.kstep, da.hi, blo + k * db.kstep, db.hi, p.idesc,
-                                             (k > 0 || kb > 0) ? 1u : 0u);
-                    if (!skip_release)
-                        tc_commit_pair_mc(smem_u32(&empty[stage]), 0x3);
+                        for (int k = 0; k < BK / 16; ++k)
+                            tc_mma_pair_w<false>(d, alo + k * da.kstep, da.hi, blo + k * db.kstep, db.hi, p.idesc,
+                                                 (k > 0 || kb > 0) ? 1u : 0u);
+                        if (!skip_release)
+                            tc_commit_pair_mc(smem_u32(&empty[stage]), 0x3);
+                    }
+                    __syncwarp();
                     skip_release = false;
                     if (++stage == kStages) {
                         stage = 0;
@@ -246,9 +250,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 if (!ok)
                     break;
-                tc_commit_pair_mc(smem_u32(&tfull[buf]), 0x3);
+                if (one)
+                    tc_commit_pair_mc(smem_u32(&tfull[buf]), 0x3);
+                __syncwarp();
             }
-            tc_commit_pair(smem_u32(drain));
+            if (one)
+                tc_commit_pair(smem_u32(drain));
+            __syncwarp();
             const long long t0 = clock64();
             while (!mbar_try_wait(smem_u32(drain), 0) && static_cast<unsigned long long>(clock64() - t0) <= p.wait_limit) {
             }
@@ -264,7 +272,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             int tx, ty;
             tile_at(p, t, tx, ty);
             const int buf = local & 1;
-            if (!wait_bounded(smem_u32(&tfull[buf]), (local >> 1) & 1, abort_flag, p.wait_limit)) {
+            if (!blk::wait_lanes(smem_u32(&tfull[buf]), (local >> 1) & 1, abort_flag, p.wait_limit)) {
                 *abort_flag = 1;
                 atomicOr(p.status, kStatusTimeout);
                 break;

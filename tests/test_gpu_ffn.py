@@ -61,7 +61,7 @@ def test_gated(shape, dtype):
 @pytest.mark.parametrize("offset", [0, 8, 1])
 def test_gated_paths_and_alignments(path, offset):
     for m, k, n, dtype in ((5, 264, 72, BF16), (70, 520, 200, F16), (300, 136, 513, BF16)):
-        m = min(m, {P.SKINNY: 16, P.TC05: 128}.get(path, m))
+        m = min(m, {P.SKINNY: 16, P.TC05: 64}.get(path, m))
         g = gen(m + offset)
         x = normal(g, m, k, dtype=dtype, pitch=k + offset, offset=offset)
         w = normal(g, 2 * n, k, scale=k ** -0.5, dtype=dtype, pitch=k + offset, offset=offset)
