@@ -939,7 +939,9 @@ def _w4_product(X, Q, S, Z, group, act, out, path):
 def linear_w4(X, Q, S, Z=None, group=128, out=None, path=Path.AUTO, stream=None):
     """Y = X @ W.T with the 4-bit weights of :func:`quantize_w4`: X (tokens, in)
     float16 or bfloat16, Q, S and Z of W (out, in), S in X's type.  Sums are
-    float32; Y (tokens, out) has X's type, its rows start on 16-byte boundaries."""
+    float32 (for more than a few tokens of weights rounded to X's type: see gemm_nt_w4 in
+    include/gemm_nt.h); Y (tokens, out) has X's type, its rows start on 16-byte
+    boundaries."""
     if stream is not None:
         side = _elsewhere(stream)
         if side is not None:

@@ -423,14 +423,22 @@ typedef enum gemm_act {
  * multiplied in fp32; H is rounded once.  GU (tokens x 2*inner, row pitch ldgu; null to
  * leave it out) receives g and u, each rounded to `type`, for gemm_nt_gated_grad.
  *
- * path: GEMM_PATH_AUTO, or GEMM_PATH_MMASYNC (warp MMA, any layout).  Other paths:
- * GEMM_ERR_NOT_SUPPORTED.
+ * path: GEMM_PATH_AUTO, or one of
+ *   GEMM_PATH_SKINNY     a stream of the weights on the warp MMA: up to 16 tokens, and
+ *                        tokens * hidden (rounded up to 64) <= 65536
+ *   GEMM_PATH_TC05       tcgen05 with the weights as rows: up to 64 tokens
+ *   GEMM_PATH_TC05_PAIR  tcgen05 on CTA pairs, 256 tokens x 128 columns of H
+ *   GEMM_PATH_MMASYNC    warp MMA, any layout
+ * SKINNY needs W13 on 16-byte boundaries (base and ldw), TC05 and TC05_PAIR X (base and
+ * ldx) too; a path that cannot take the arguments, and the other paths, are
+ * GEMM_ERR_NOT_SUPPORTED.  AUTO takes one that can, by the tokens and the weights' bytes;
+ * paths differ in the order of their sums.
  *
  * tokens or inner 0: nothing to do; hidden 0: zeros.  Any pitch and alignment is
  * accepted; rows that start on 16-byte boundaries are read fastest.  Outputs that
  * overlap an operand or each other (the byte spans, counting pitches):
- * GEMM_ERR_OVERLAP.  Infinities and NaN follow IEEE arithmetic.  Nothing is allocated
- * and the result does not depend on the run.
+ * GEMM_ERR_OVERLAP.  Infinities and NaN follow IEEE arithmetic.  Nothing is allocated,
+ * no two calls share memory of the library's, and the result does not depend on the run.
  */
 gemm_status_t gemm_nt_gated(const void *X, int64_t ldx, const void *W13, int64_t ldw, void *H, int64_t ldh,
                             void *GU, int64_t ldgu, gemm_dtype_t type, gemm_act_t act,
@@ -489,12 +497,22 @@ gemm_status_t gemm_nt_w4_quantize(const void *W, gemm_dtype_t w_type, int64_t ro
 /*
  * Out = X @ W^T with 4-bit weights: X (M x K) and Out (M x N) both fp16 or both bf16
  * (`type`, also that of W's scales).  Sums in fp32, Out rounded once.
- * M or N 0: nothing to do; K 0: zeros.  Paths, errors and the rest as gemm_nt_gated.
+ *
+ * path: as gemm_nt_gated, without TC05_PAIR.  SKINNY (up to 16 rows of X, and M * K
+ * (rounded up to 256) <= 65536) and MMASYNC multiply whole numbers code - zero, exactly, and scale
+ * each group's sum in fp32.  TC05 takes any M; it multiplies (code - zero) * scale rounded
+ * to nearest in `type`, so that one sum runs over all groups: each weight is off by at most
+ * half a step (bf16 2^-8 of it, fp16 2^-11), and one beyond fp16's largest value is
+ * infinite.  AUTO takes SKINNY for few rows and small weights, else TC05, and MMASYNC where
+ * alignment leaves nothing else: SKINNY needs the codes on 16-byte boundaries (base and
+ * ldc), TC05 X as well.  A group whose scale is infinite or NaN makes its row's sums NaN or
+ * infinite, however it is reached.
+ * M or N 0: nothing to do; K 0: zeros.  The rest as gemm_nt_gated.
  */
 gemm_status_t gemm_nt_w4(const void *X, int64_t ldx, const gemm_w4_t *W, void *Out, int64_t ldo, gemm_dtype_t type,
                          int64_t M, int64_t N, int64_t K, gemm_path_t path, gemm_stream_t stream);
 
-/* gemm_nt_gated with 4-bit weights W13 (2*inner rows). */
+/* gemm_nt_gated with 4-bit weights W13 (2*inner rows), its paths those of gemm_nt_w4. */
 gemm_status_t gemm_nt_w4_gated(const void *X, int64_t ldx, const gemm_w4_t *W13, void *H, int64_t ldh,
                                gemm_dtype_t type, gemm_act_t act, int64_t tokens, int64_t hidden, int64_t inner,
                                gemm_path_t path, gemm_stream_t stream);
