@@ -105,6 +105,7 @@ _SIGNATURES = {
     "gemm_nt_moe_workspace_bytes": (_i64, [_i64, _i64, _i64]),
     "gemm_nt_gated": (ctypes.c_int, [_vp, _i64] * 4 + [ctypes.c_int, ctypes.c_int] + [_i64] * 3 + [ctypes.c_int, _vp]),
     "gemm_nt_gated_grad": (ctypes.c_int, [_vp, _i64] * 3 + [ctypes.c_int, ctypes.c_int, _i64, _i64, _vp]),
+    "gemm_nt_copy_rows": (ctypes.c_int, [_vp] + [_i64, _vp] + [_i64] * 3 + [_vp]),
     "gemm_nt_w4_quantize": (ctypes.c_int, [_vp, ctypes.c_int, _i64, _i64, _i64, _wp, ctypes.c_int, _vp]),
     "gemm_nt_w4": (ctypes.c_int, [_vp, _i64, _wp, _vp, _i64, ctypes.c_int] + [_i64] * 3 + [ctypes.c_int, _vp]),
     "gemm_nt_w4_gated": (ctypes.c_int, [_vp, _i64, _wp, _vp, _i64, ctypes.c_int, ctypes.c_int] + [_i64] * 3
@@ -222,6 +223,10 @@ def gemm_nt_gated(X, ldx, W13, ldw, H, ldh, GU, ldgu, dtype, act, tokens, hidden
 
 def gemm_nt_gated_grad(dH, ldd, GU, ldgu, dGU, ldo, dtype, act, tokens, inner, stream=0):
     _check(load().gemm_nt_gated_grad(dH, ldd, GU, ldgu, dGU, ldo, int(dtype), int(act), tokens, inner, stream))
+
+
+def gemm_nt_copy_rows(src, lds, dst, ldd, rows, nbytes, stream=0):
+    _check(load().gemm_nt_copy_rows(src, lds, dst, ldd, rows, nbytes, stream))
 
 
 def gemm_nt_w4_quantize(W, w_type, rows, cols, ldw, Q, s_type, stream=0):
@@ -788,13 +793,27 @@ def _given(out, n, width, like):
     return _pitch(out.shape, out.stride(), "out")
 
 
+def _on_grid(t, at, ld):
+    """Whether rows of 16-bit elements at that address and pitch start on 16-byte boundaries."""
+    return at % 16 == 0 and (ld % 8 == 0 or t.shape[0] < 2)
+
+
+def _to_grid(t, ld, index):
+    """A copy of a matrix of 16-bit elements with its rows on 16-byte boundaries; its pitch."""
+    rows, width = t.shape
+    copy, pitch = _rows(rows, width, t), (width + 7) // 8 * 8
+    gemm_nt_copy_rows(t.data_ptr(), 2 * ld, copy.data_ptr(), 2 * pitch, rows, 2 * width, _stream_of(index))
+    return copy, pitch
+
+
 def gated_linear(X, W13, activation="silu", keep=False, out=None, path=Path.AUTO, stream=None):
     """H = act(X @ Wg.T) * (X @ Wu.T) in one kernel: X (tokens, hidden) and W13
     (2*inner, hidden), Wg's rows then Wu's, both float16 or both bfloat16; H
     (tokens, inner) in their type.  ``activation``: "silu", "gelu" (with erf) or
     "gelu_tanh".  With ``keep`` returns ``(H, GU)``: GU (tokens, 2*inner) holds
     X @ W13.T in X's type, which :func:`gated_linear_backward` takes.  Rows of what is
-    returned start on 16-byte boundaries.
+    returned start on 16-byte boundaries; operands whose rows do not (an odd ``hidden``) are
+    copied there first, unless a ``path`` is given.
     """
     if stream is not None:
         side = _elsewhere(stream)
@@ -811,6 +830,11 @@ def gated_linear(X, W13, activation="silu", keep=False, out=None, path=Path.AUTO
     inner = wsh[0] // 2
     ldx, ldw = _pitch(xsh, X.stride(), "X"), _pitch(wsh, W13.stride(), "W13")
     index = _same_device(X, W13, out)
+    if path == 0:
+        if not _on_grid(W13, W13.data_ptr(), ldw):
+            W13, ldw = _to_grid(W13, ldw, index)
+        if tokens > 16 and not _on_grid(X, X.data_ptr(), ldx):
+            X, ldx = _to_grid(X, ldx, index)
     if out is None:
         out, ldh = _rows(tokens, inner, X), (inner + 7) // 8 * 8
     else:
@@ -828,7 +852,8 @@ def gated_linear_backward(dH, GU, X, W13, activation="silu", stream=None):
     """Gradients of :func:`gated_linear`: ``(dX, dW13)`` in X's type from dH
     (tokens, inner) and the GU it kept.  The gradient at the two projections is
     rounded to X's type before the products dX = dGU @ W13 and dW13 = dGU.T @ X,
-    which accumulate in float32."""
+    which accumulate in float32.  Operands off 16-byte boundaries as in
+    :func:`gated_linear`."""
     side = _elsewhere(stream)
     if side is not None:
         _record(GU, side, None)
@@ -846,7 +871,12 @@ def gated_linear_backward(dH, GU, X, W13, activation="silu", stream=None):
     code, act = _one_of(X.dtype, _X16, "X"), _act(activation)
     ldx, ldw = _pitch(xsh, X.stride(), "X"), _pitch(wsh, W13.stride(), "W13")
     ldd, ldg = _pitch(dH.shape, dH.stride(), "dH"), _pitch(GU.shape, GU.stride(), "GU")
-    stream = _stream_of(_same_device(X, W13, dH, GU))
+    index = _same_device(X, W13, dH, GU)
+    if not _on_grid(W13, W13.data_ptr(), ldw):
+        W13, ldw = _to_grid(W13, ldw, index)
+    if not _on_grid(X, X.data_ptr(), ldx):
+        X, ldx = _to_grid(X, ldx, index)
+    stream = _stream_of(index)
     dgu, dx, dw = _rows(tokens, rows, X), _rows(tokens, hidden, X), _rows(rows, hidden, X)
     at, ldo, ldout = dgu.data_ptr(), (rows + 7) // 8 * 8, (hidden + 7) // 8 * 8
     gemm_nt_gated_grad(dH.data_ptr(), ldd, GU.data_ptr(), ldg, at, ldo, code, act, tokens, rows // 2, stream)
@@ -915,9 +945,11 @@ def _w4_product(X, Q, S, Z, group, act, out, path):
     if act is not None and rows % 2:
         raise ValueError("Q13 must have 2*inner rows")
     ldx = _pitch(xsh, X.stride(), "X")
+    index = _same_device(X, Q, S, Z, out)
+    if path == 0 and tokens > 16 and not _on_grid(X, X.data_ptr(), ldx):
+        X, ldx = _to_grid(X, ldx, index)
     weights = Weights4(Q.data_ptr(), _pitch(qsh, Q.stride(), "Q"), S.data_ptr(), _pitch(ssh, S.stride(), "S"),
                        None if Z is None else Z.data_ptr(), 0 if Z is None else _pitch(ssh, Z.stride(), "Z"), group)
-    index = _same_device(X, Q, S, Z, out)
     n = rows if act is None else rows // 2
     if out is None:
         ldo = (n + 7) // 8 * 8

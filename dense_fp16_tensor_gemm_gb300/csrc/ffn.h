@@ -122,4 +122,7 @@ struct Quant4Params {
 };
 cudaError_t w4_quantize_launch(const Quant4Params& p, int num_sms, cudaStream_t stream);
 
+// Rows of `bytes` bytes onto 16-byte boundaries (dst and ldd; pitches in bytes).
+cudaError_t copy_rows_launch(const void* src, int64_t lds, void* dst, int64_t ldd, int64_t rows, int64_t bytes, cudaStream_t stream);
+
 }  // namespace gnt

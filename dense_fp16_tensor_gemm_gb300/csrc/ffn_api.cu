@@ -250,6 +250,25 @@ gemm_status_t gemm_nt_gated_grad(const void* dH, int64_t ldd, const void* GU, in
     return status_of(gated_grad_launch(p, d.num_sms, reinterpret_cast<cudaStream_t>(stream)));
 }
 
+gemm_status_t gemm_nt_copy_rows(const void* src, int64_t lds, void* dst, int64_t ldd, int64_t rows, int64_t bytes,
+                                gemm_stream_t stream)
+{
+    if (!sizes_ok({rows}) || bytes < 0 || bytes > (int64_t(1) << 40))
+        return GEMM_ERR_INVALID_VALUE;
+    if (rows == 0 || bytes == 0)
+        return GEMM_OK;
+    if (!matrix_ok(src, 1, rows, bytes, lds) || !matrix_ok(dst, 1, rows, bytes, ldd) || !aligned(dst, 16) ||
+        (rows > 1 && ldd % 16 != 0))
+        return GEMM_ERR_INVALID_VALUE;
+    if (overlap(matrix_span(dst, 1, rows, bytes, ldd), matrix_span(src, 1, rows, bytes, lds)))
+        return GEMM_ERR_OVERLAP;
+    DeviceInfo d;
+    gemm_status_t st = static_cast<gemm_status_t>(device_info(&d));
+    if (st != GEMM_OK)
+        return st;
+    return status_of(copy_rows_launch(src, lds, dst, ldd, rows, bytes, reinterpret_cast<cudaStream_t>(stream)));
+}
+
 gemm_status_t gemm_nt_w4_quantize(const void* W, gemm_dtype_t w_type, int64_t rows, int64_t cols, int64_t ldw,
                                   const gemm_w4_t* Q, gemm_dtype_t s_type, gemm_stream_t stream)
 {

@@ -460,6 +460,17 @@ gemm_status_t gemm_nt_gated_grad(const void *dH, int64_t ldd, const void *GU, in
                                  gemm_stream_t stream);
 
 /*
+ * Copies a matrix of `rows` rows of `bytes` bytes, row pitch lds, to dst, whose base and
+ * row pitch ldd lie on 16-byte boundaries (pitches in bytes): the layout that the
+ * tensor-core kernels read.  Worth its time before gemm_nt_gated, its backward products and
+ * gemm_nt_w4 whenever an operand's rows lie off that grid, as those of an odd number of
+ * elements do.  Bytes between dst's rows are left alone.  dst off the grid, pitches below
+ * `bytes`, null: GEMM_ERR_INVALID_VALUE; dst overlapping src: GEMM_ERR_OVERLAP.
+ */
+gemm_status_t gemm_nt_copy_rows(const void *src, int64_t lds, void *dst, int64_t ldd, int64_t rows, int64_t bytes,
+                                gemm_stream_t stream);
+
+/*
  * 4-bit weights (rows x K): element k of row r stands for
  *   (code - zero) * scale,   code = the low (k even) or high (k odd) half of byte
  *   codes[r*ldc + k/2],      scale = scales[r*lds + k/group],  zero = zeros[r*ldz + k/group]

@@ -133,6 +133,24 @@ def test_quantize_valid_arguments_reach_the_device(lib):
     assert quantize(lib, q=w4(zeros=Z)) not in NEVER
 
 
+def copy_rows(lib, src=X + 2, lds=500, dst=H, ldd=512, rows=100, nbytes=498):
+    return lib.gemm_nt_copy_rows(src, lds, dst, ldd, rows, nbytes, None)
+
+
+@pytest.mark.parametrize("change,status", [
+    (dict(rows=-1), INVALID), (dict(nbytes=-1), INVALID), (dict(nbytes=HUGE), INVALID), (dict(src=0), INVALID),
+    (dict(dst=0), INVALID), (dict(dst=H + 8), INVALID), (dict(ldd=504), INVALID), (dict(ldd=496), INVALID),
+    (dict(lds=497), INVALID), (dict(dst=X + 16), OVERLAP), (dict(rows=0, src=0), OK), (dict(nbytes=0), OK),
+])
+def test_copy_rows_refusals(lib, change, status):
+    assert copy_rows(lib, **change) == status
+
+
+def test_copy_rows_valid_arguments_reach_the_device(lib):
+    assert copy_rows(lib) not in NEVER
+    assert copy_rows(lib, rows=1, ldd=499) not in NEVER
+
+
 def test_tensor_forms_refuse():
     """What the tensor forms refuse before they look at a device."""
     x, w = torch.zeros(4, 64, dtype=torch.float16), torch.zeros(32, 64, dtype=torch.float16)

@@ -373,3 +373,39 @@ def test_empty_sums():
     x, (q, s, z) = torch.zeros(0, 64, dtype=BF16, device="cuda"), weights4(gen(1), 6, 64, 32, False, BF16)
     assert gnt.linear_w4(x, q, s, group=32).shape == (0, 6)
     assert gnt.linear_w4(torch.zeros(3, 64, dtype=BF16, device="cuda"), q[:0], s[:0], group=32).shape == (3, 0)
+
+
+@pytest.mark.parametrize("offset", [0, 1, 2, 4, 16, 30])
+def test_copy_rows(offset):
+    """Every unit that a source's alignment allows, and bytes between the rows left alone."""
+    for rows, width, pitch in ((1, 1, 1), (3, 15, 16), (7, 16, 17), (70, 1001, 1002), (40, 4096, 4100), (2, 70000, 70016)):
+        src = torch.randint(0, 256, (offset + rows * pitch,), dtype=torch.uint8, device="cuda")
+        ldd = (width + 15) // 16 * 16 + 16
+        dst = torch.full((rows, ldd), 0xA5, dtype=torch.uint8, device="cuda")
+        gnt.gemm_nt_copy_rows(src.data_ptr() + offset, pitch, dst.data_ptr(), ldd, rows, width,
+                              torch.cuda.current_stream().cuda_stream)
+        assert torch.equal(dst[:, :width], src[offset:].view(rows, pitch)[:, :width])
+        assert (dst[:, width:] == 0xA5).all()
+
+
+@pytest.mark.parametrize("m", [1, 16, 17, 70, 300])
+@pytest.mark.parametrize("k,offset", [(1001, 0), (1002, 3), (1000, 1), (1004, 4)])
+def test_rows_off_the_grid(k, offset, m):
+    """Operands that are copied first, and the same calls on the warp kernel."""
+    n = 300
+    g = gen(k + m)
+    x = normal(g, m, k, dtype=F16, pitch=k + offset, offset=offset)
+    w = normal(g, 2 * n, k, scale=k ** -0.5, dtype=F16, pitch=k + offset, offset=offset)
+    h, y, eh, ey = gated_bound(x, w, "gelu")
+    for path in (P.AUTO, P.MMASYNC):
+        out, gu = gnt.gated_linear(x, w, "gelu", keep=True, path=path)
+        check(out, h, rounded(eh, h, F16))
+        check(gu, y, rounded(ey, y, F16))
+    dh = normal(g, m, n, scale=0.1, dtype=F16)
+    check_backward(x, w, gu, dh, "gelu", *gnt.gated_linear_backward(dh, gu, x, w, "gelu"))
+    q, s, z = weights4(g, n, k, 32, True, F16)
+    v = w4_values(q, s, z, 32, k)
+    wide = x.double().abs() @ (v.abs() + 31 * s.double()[:, torch.arange(k, device="cuda") // 32]).t()
+    ref, mag = x.double() @ v.t(), x.double().abs() @ v.abs().t()
+    check(gnt.linear_w4(x, q, s, z, group=32), ref, rounded(sum_error(wide, k) + weight_eps(m, F16) * mag, ref, F16))
+    gnt.gemm_nt_check()
