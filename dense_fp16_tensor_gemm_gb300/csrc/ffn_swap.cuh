@@ -71,6 +71,16 @@ struct Cfg {
     static_assert(kStages * kStage >= kRowsW * NT * 4, "a split's sums fit the stages");
     static_assert((2 * kStages + 2 * kRaw + 5) * 8 + 8 <= 512, "barrier area");
     static_assert(kRawKb % kKb == 0, "stages of codes are whole stages");
+    // A wait tells a phase from the next, not from the one after that, so no set may come
+    // two turns of a ring ahead of the slowest.  From one stage that a set writes to its
+    // next one lie at most 1 + (kConvSets - 1) * kPer others.  When it wrote the former, the
+    // stage kStages before that had been multiplied, and with it everything before: the
+    // latter's last use but one is among that if the gap is at most kStages.  In the ring of
+    // codes the fill before last of a set's next stage has to have landed: it has if a
+    // stage of its has been multiplied.
+    static constexpr int kPer = kRawKb / kKb;
+    static_assert(!W4 || 1 + (kConvSets - 1) * kPer <= kStages, "conversion stays within one turn of the ring");
+    static_assert(!W4 || (kRaw - kConvSets + 1) * kPer >= kStages + 1, "and of the ring of codes");
 };
 
 struct SwapParams {
@@ -160,8 +170,12 @@ __device__ __forceinline__ void convert8(uint32_t word, uint32_t zero2, uint32_t
 // Where a CTA's work lies: its tile's first output and first token, and its k-blocks.
 struct Piece {
     int o0, t0, kb0, kb1;
+    int end;  // kb1, or with 4-bit weights the end of its last stage of codes: the ring's
+              // stages up to there are passed on too, without k-blocks, so that every stage
+              // of codes is as many of the ring's (what keeps the conversion's sets together)
 };
 // The i-th piece of this CTA; false if there is none.
+template <bool W4>
 __device__ __forceinline__ bool piece_at(const SwapParams& p, int i, int nt, int rank, Piece& c)
 {
     const int t = static_cast<int>(blockIdx.x) / p.splits + i * (static_cast<int>(gridDim.x) / p.splits);
@@ -173,7 +187,10 @@ __device__ __forceinline__ bool piece_at(const SwapParams& p, int i, int nt, int
     // shares of whole stages of codes
     const int groups = (p.num_kb + kRawKb - 1) / kRawKb;
     c.kb0 = static_cast<int>(static_cast<int64_t>(groups) * rank / p.splits) * kRawKb;
-    c.kb1 = min(p.num_kb, static_cast<int>(static_cast<int64_t>(groups) * (rank + 1) / p.splits) * kRawKb);
+    c.end = static_cast<int>(static_cast<int64_t>(groups) * (rank + 1) / p.splits) * kRawKb;
+    c.kb1 = min(p.num_kb, c.end);
+    if (!W4)
+        c.end = c.kb1;
     return true;
 }
 
@@ -284,7 +301,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 0 && lane == 0) {
         // the first ring of weights comes into L2 while the preceding grids finish
         Piece c;
-        if (piece_at(p, 0, NT, rank, c)) {
+        if (piece_at<W4>(p, 0, NT, rank, c)) {
             constexpr int step = W4 ? kRawKb : 1;
             for (int i = 0, kb = c.kb0; i < (W4 ? C::kRaw : C::kKb * kStages) && kb < c.kb1; ++i, kb += step) {
                 const int x = W4 ? kb * (BK / 2) : kb * BK;
@@ -320,7 +337,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t phase = 0, filled = 0, parity = 0;
             bool first = true, ok = true;
             Piece c;
-            for (int i = 0; ok && piece_at(p, i, NT, rank, c); ++i) {
+            for (int i = 0; ok && piece_at<W4>(p, i, NT, rank, c); ++i) {
                 for (int kb = c.kb0; kb < c.kb1; kb += kbs) {
                     if (!wait_bounded(smem_u32(&eb[s]), phase ^ 1, abort_flag, limit)) {
                         gave_up();
@@ -366,15 +383,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t phase = 0, filled = 0, parity = 0;
             bool ok = true;
             Piece c;
-            for (int i = 0; ok && piece_at(p, i, NT, rank, c); ++i) {
-                for (int kb = c.kb0; kb < c.kb1; kb += C::kKb) {
+            for (int i = 0; ok && piece_at<W4>(p, i, NT, rank, c); ++i) {
+                for (int kb = c.kb0; kb < c.end; kb += C::kKb) {
                     if (!wait_bounded(smem_u32(&empty[s]), phase ^ 1, abort_flag, limit)) {
                         gave_up();
                         ok = false;
                         break;
                     }
                     const uint32_t bar = smem_u32(&full[s]);
-                    const int n = min(C::kKb, c.kb1 - kb);
+                    const int n = max(0, min(C::kKb, c.kb1 - kb));
                     mbar_arrive_expect_tx(bar, n * C::kXBytes);
                     filled |= 1u << s;
                     parity = (parity & ~(1u << s)) | (phase << s);
@@ -401,7 +418,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             bool skip_release = f.fault == 2 && blockIdx.x == 0;  // test hook: lose one stage release
             bool ok = true;
             Piece c;
-            for (int i = 0; ok && piece_at(p, i, NT, rank, c); ++i) {
+            for (int i = 0; ok && piece_at<W4>(p, i, NT, rank, c); ++i) {
                 const int buf = i % C::kAccs;
                 if (!blk::wait_lanes(smem_u32(&tempty[buf]), ((i / C::kAccs) & 1) ^ 1, abort_flag, limit)) {
                     gave_up();
@@ -409,7 +426,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 tc_fence_after();
                 const uint32_t d = tmem_base + static_cast<uint32_t>(buf * NT);
-                for (int kb = c.kb0; kb < c.kb1; kb += C::kKb) {
+                for (int kb = c.kb0; kb < c.end; kb += C::kKb) {
                     if (!blk::wait_lanes(smem_u32(&full[s]), phase, abort_flag, limit)) {
                         gave_up();
                         ok = false;
@@ -419,7 +436,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (one) {
 #pragma unroll
                         for (int b = 0; b < C::kKb; ++b) {
-                            if (b > 0 && kb + b >= c.kb1)
+                            if (kb + b >= c.kb1)
                                 break;
                             const int slot = s * C::kKb + b;
                             const uint32_t alo = da.lo + slot * (kABytes >> 4), blo = dx.lo + slot * (C::kXBytes >> 4);
@@ -468,7 +485,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t phase = 0, rphase = 0;
         bool ok = true;
         Piece c;
-        for (int i = 0; ok && piece_at(p, i, NT, rank, c); ++i) {
+        for (int i = 0; ok && piece_at<W4>(p, i, NT, rank, c); ++i) {
             const int o = f.gated ? c.o0 + (r >> 5) * 16 + (r & 15) : c.o0 + r;
             const int64_t row = o + (f.gated && (r & 16) ? static_cast<int64_t>(f.n) : 0);
             // (rows past the weights are converted with the last one's scales and not stored)
@@ -505,9 +522,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             };
             uint4 scales, scales1;
             uint2 zeros, zeros1;
-            fetch(c.kb0 + (turn != set ? kRawKb : 0), scales, zeros);
+            fetch(c.kb0 + (set + kConvSets - turn) % kConvSets * kRawKb, scales, zeros);
             for (int kb = c.kb0; ok && kb < c.kb1; kb += kRawKb) {
-                const int n = min(kRawKb, c.kb1 - kb);
                 if (turn == set) {
                     fetch(kb + kConvSets * kRawKb, scales1, zeros1);
                     // the groups of this stage's k-blocks, first of them `first` of the eight
@@ -534,8 +550,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int left = f.k - (kb * BK + half * 32);  // elements inside K
 #pragma unroll
                     for (int j = 0; j < kRawKb; j += C::kKb) {
-                        if (j >= n)
-                            break;
                         if (!blk::wait_lanes(smem_u32(&empty[s]), phase ^ 1, abort_flag, limit)) {
                             gave_up();
                             ok = false;
@@ -544,8 +558,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         tc_fence_after();
 #pragma unroll
                         for (int b = 0; b < C::kKb; ++b) {
-                            // (of a k-block past the last, whatever the stage holds)
-                            const int jb = j + b;
+                            const int jb = j + b;  // (past the last k-block: zeros, which nothing reads)
                             const uint4 w = lds128(raw0 + rs * kRawBytes + (((2 * jb + half) ^ swz) << 4));
                             const uint32_t words[4] = {w.x, w.y, w.z, w.w};
                             const int at = GS == 7 ? jb >> 1 : jb;
@@ -581,7 +594,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     scales = scales1;
                     zeros = zeros1;
                 } else {  // the other set's
-                    s += (n + C::kKb - 1) / C::kKb;
+                    s += C::kPer;
                     if (s >= kStages) {
                         s -= kStages;
                         phase ^= 1;
@@ -591,14 +604,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                     rs = 0;
                     rphase ^= 1;
                 }
-                turn ^= 1;
+                turn = turn + 1 == kConvSets ? 0 : turn + 1;
             }
         }
     } else if (warp >= 20) {
         // ------------------------------------------------------------ epilogue
         const int q = warp & 3;
         Piece c;
-        for (int i = 0; piece_at(p, i, NT, rank, c); ++i) {
+        for (int i = 0; piece_at<W4>(p, i, NT, rank, c); ++i) {
             const int buf = i % C::kAccs;
             if (!blk::wait_lanes(smem_u32(&tfull[buf]), (i / C::kAccs) & 1, abort_flag, limit)) {
                 gave_up();
@@ -639,7 +652,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // A split has one tile per cluster.  Each CTA sums 32 tokens at a time, in the CTAs' order.
         cluster_sync();
         Piece c;
-        if (warp >= 20 && piece_at(p, 0, NT, rank, c)) {
+        if (warp >= 20 && piece_at<W4>(p, 0, NT, rank, c)) {
             const int row = (warp & 3) * 32 + lane;
             for (int n = rank * 32; n < NT && c.t0 + n < f.tokens; n += p.splits * 32) {
                 float v[32] = {};
