@@ -192,7 +192,7 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS == 8 ? 3 : 1) ffn_few_kernel
                 // (rows past the weights: the last one's scales, and zeros for codes)
                 const int64_t row = min(ft * kRows + (GATED ? g : g + 8 * h), p.n - 1) + up;
                 srow[h] = static_cast<const uint16_t*>(p.scales) + row * p.lds;
-                zrow[h] = p.zeros + row * p.ldz;
+                zrow[h] = p.zeros ? p.zeros + row * p.ldz : nullptr;
             }
         }
     };

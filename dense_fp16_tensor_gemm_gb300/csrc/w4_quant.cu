@@ -6,9 +6,9 @@
 //               z = clamp(rint(-lo * (1/s)), 0, 15), code = clamp(rint(w * (1/s)) + z, 0, 15)
 //
 // in fp32, each step rounded, with the rounded s, so that codes and scales
-// together stand for the weights as nearly as they can.  A thread holds 16
-// consecutive elements (two 16-byte loads of 16-bit weights, one 8-byte store of
-// codes); a group's 2, 4 or 8 threads share its extremes by shuffles.  Bound by
+// together stand for the weights as nearly as they can.  A thread holds 32
+// consecutive elements (four 16-byte loads of 16-bit weights, one 16-byte store of
+// codes); a group's 1, 2 or 4 threads share its extremes by shuffles.  Bound by
 // memory, one read of the weights, as long as the instructions stay below it: w * (1/s)
 // is rounded to a whole number by adding 1.5 * 2^23, whose low bits then hold it
 // (|w / s| stays below 32), and a saturating pack clamps and joins two codes.
@@ -23,26 +23,30 @@ namespace gnt {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kPer = 16;  // elements per thread
+constexpr int kPer = 32;  // elements per thread
 
 // WT: 0 fp16, 1 bf16, 2 fp32.  VEC: 16-byte aligned rows of weights.
 template <int WT, bool VEC>
-__device__ __forceinline__ void load16(const Quant4Params& p, int64_t row, int64_t col, float (&v)[kPer])
+__device__ __forceinline__ void load_piece(const Quant4Params& p, int64_t row, int64_t col, float (&v)[kPer])
 {
     if (VEC && col + kPer <= p.cols) {
         if constexpr (WT == 2) {
             const float4* g = reinterpret_cast<const float4*>(static_cast<const float*>(p.w) + row * p.ldw + col);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < kPer / 4; ++i) {
                 const float4 a = __ldcs(g + i);
                 v[4 * i] = a.x, v[4 * i + 1] = a.y, v[4 * i + 2] = a.z, v[4 * i + 3] = a.w;
             }
         } else {
             const uint4* g = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.w) + row * p.ldw + col);
-            const uint4 a = __ldcs(g), b = __ldcs(g + 1);
-            const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+            uint32_t w[kPer / 2];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
+            for (int i = 0; i < kPer / 8; ++i) {
+                const uint4 a = __ldcs(g + i);
+                w[4 * i] = a.x, w[4 * i + 1] = a.y, w[4 * i + 2] = a.z, w[4 * i + 3] = a.w;
+            }
+#pragma unroll
+            for (int i = 0; i < kPer / 2; ++i) {
                 float2 f;
                 if constexpr (WT == 1)
                     f = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
@@ -88,7 +92,7 @@ template <int WT, bool VEC, bool ZEROS>
 __global__ void __launch_bounds__(kThreads) w4_quantize_kernel(const Quant4Params p, int per_row, int64_t total, int step_rows,
                                                                int step_pieces)
 {
-    const int lanes = 1 << (p.group_shift - 4);  // threads of a group
+    const int lanes = 1 << (p.group_shift - 5);  // threads of a group
     int64_t i = blockIdx.x * static_cast<int64_t>(kThreads) + threadIdx.x;
     int64_t row = i / per_row;
     int piece = static_cast<int>(i - row * per_row);
@@ -97,7 +101,7 @@ __global__ void __launch_bounds__(kThreads) w4_quantize_kernel(const Quant4Param
         const int64_t col = static_cast<int64_t>(piece) * kPer;
         float v[kPer];
         if (i < total) {
-            load16<WT, VEC>(p, row, col, v);
+            load_piece<WT, VEC>(p, row, col, v);
         } else {
 #pragma unroll
             for (int k = 0; k < kPer; ++k)
@@ -136,13 +140,15 @@ __global__ void __launch_bounds__(kThreads) w4_quantize_kernel(const Quant4Param
         int z = 8;
         if (ZEROS)
             z = bad ? 0 : static_cast<int>(fminf(rintf(__fmul_rn(low, inv)), 15.f));
-        uint32_t word[2];
+        uint32_t word[kPer / 8];
         if (bad) {
-            word[0] = word[1] = 0x11111111u * static_cast<uint32_t>(z);
+#pragma unroll
+            for (int h = 0; h < kPer / 8; ++h)
+                word[h] = 0x11111111u * static_cast<uint32_t>(z);
         } else {
             const int bias = z - 0x4b400000;
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
+            for (int h = 0; h < kPer / 8; ++h) {
                 int q[8];
 #pragma unroll
                 for (int k = 0; k < 8; ++k)
@@ -158,8 +164,8 @@ __global__ void __launch_bounds__(kThreads) w4_quantize_kernel(const Quant4Param
                     p.zeros[row * p.ldz + group] = static_cast<uint8_t>(z);
             }
             uint8_t* dst = p.codes + row * p.ldc + (col >> 1);
-            if (col + kPer <= p.cols && (reinterpret_cast<uintptr_t>(dst) & 7) == 0) {
-                *reinterpret_cast<uint2*>(dst) = make_uint2(word[0], word[1]);
+            if (col + kPer <= p.cols && (reinterpret_cast<uintptr_t>(dst) & 15) == 0) {
+                *reinterpret_cast<uint4*>(dst) = make_uint4(word[0], word[1], word[2], word[3]);
             } else {
 #pragma unroll
                 for (int k = 0; k < kPer / 2; ++k) {
@@ -205,9 +211,9 @@ cudaError_t w4_quantize_launch(const Quant4Params& p, int num_sms, cudaStream_t 
 {
     const int esize = p.w_type == GEMM_DTYPE_F32 ? 4 : 2;
     const bool vec = reinterpret_cast<uintptr_t>(p.w) % 16 == 0 && (p.rows == 1 || p.ldw * esize % 16 == 0);
-    // pieces of 16 elements, whole groups of them: a group's threads are neighbours
+    // pieces of 32 elements, whole groups of them: a group's threads are neighbours
     const int64_t groups = (p.cols + (int64_t(1) << p.group_shift) - 1) >> p.group_shift;
-    const int per_row = static_cast<int>(groups << (p.group_shift - 4));
+    const int per_row = static_cast<int>(groups << (p.group_shift - 5));
     const int64_t total = per_row * p.rows;
     const unsigned grid = static_cast<unsigned>(std::min<int64_t>((total + kThreads - 1) / kThreads, int64_t(num_sms) * 32));
     if (p.w_type == GEMM_DTYPE_F32)
