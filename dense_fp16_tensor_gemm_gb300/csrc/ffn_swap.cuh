@@ -497,8 +497,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             // their use: each load of a warp touches 32 rows, and two of single scales a stage
             // cost 64 x 16384 x 8192 5 us.
             const int chunks = ((f.k - 1) >> (GS + 3)) + 1, last = (f.k - 1) >> GS;
-            const auto fetch = [&](int kb, uint4& sc, uint2& ze) {
-                const int ch = min(kb * BK >> (GS + 3), chunks - 1);
+            const auto chunk_of = [&](int kb) { return min(kb * BK >> (GS + 3), chunks - 1); };
+            const auto fetch = [&](int ch, uint4& sc, uint2& ze) {
                 const bool whole = 8 * ch + 8 <= last + 1;  // (no element past a row's last is read)
                 if (whole && p.vec_s) {
                     sc = __ldg(reinterpret_cast<const uint4*>(srow) + ch);
@@ -520,12 +520,24 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ze = make_uint2(v[0] | v[1] << 8 | v[2] << 16 | v[3] << 24, v[4] | v[5] << 8 | v[6] << 16 | v[7] << 24);
                 }
             };
+            // (the whole piece's come into L2 first: a turn is shorter than a load from memory)
+            if (set == 0 && half == 0) {
+                const int g1 = min(c.end * BK >> GS, last + 1);
+                for (int g = c.kb0 * BK >> GS; g < g1; g += 64)
+                    asm volatile("prefetch.global.L2 [%0];" ::"l"(srow + g));
+                if (zrow)
+                    for (int g = c.kb0 * BK >> GS; g < g1; g += 128)
+                        asm volatile("prefetch.global.L2 [%0];" ::"l"(zrow + g));
+            }
             uint4 scales, scales1;
             uint2 zeros, zeros1;
-            fetch(c.kb0 + (set + kConvSets - turn) % kConvSets * kRawKb, scales, zeros);
+            int chunk = chunk_of(c.kb0 + (set + kConvSets - turn) % kConvSets * kRawKb);
+            fetch(chunk, scales, zeros);
             for (int kb = c.kb0; ok && kb < c.kb1; kb += kRawKb) {
                 if (turn == set) {
-                    fetch(kb + kConvSets * kRawKb, scales1, zeros1);
+                    const int chunk1 = chunk_of(kb + kConvSets * kRawKb);
+                    if (chunk1 != chunk)
+                        fetch(chunk1, scales1, zeros1);
                     // the groups of this stage's k-blocks, first of them `first` of the eight
                     const int first = kb * BK >> GS & 7;
                     uint32_t sw[2], zw;  // scales 0-3 and zeros 0-3 of the stage (of shorter groups: this half's)
@@ -591,8 +603,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                     __syncwarp();
                     if (lane == 0)
                         mbar_arrive(smem_u32(&raw_empty[rs]));
-                    scales = scales1;
-                    zeros = zeros1;
+                    if (chunk1 != chunk) {
+                        scales = scales1;
+                        zeros = zeros1;
+                        chunk = chunk1;
+                    }
                 } else {  // the other set's
                     s += C::kPer;
                     if (s >= kStages) {
