@@ -472,7 +472,38 @@ def _init_torch():
     _OUT = (torch.float32, torch.float16, torch.bfloat16)
     _X16 = (torch.float16, torch.bfloat16)
     _torch = torch
+    _bind_calls()
     return torch
+
+
+# The feed-forward forms' common case as an extension (csrc/tensor_calls.cpp): its
+# functions make the whole call, or return None and leave it to the Python forms below.
+# None before the first call, and where the extension has not been built.
+_calls = None
+
+
+def _bind_calls():
+    global _calls
+    path = os.path.join(_HERE, "_build", "_tensor_calls.so")
+    if not os.path.exists(path):
+        return
+    import importlib.machinery
+    import importlib.util
+    loader = importlib.machinery.ExtensionFileLoader("_tensor_calls", path)
+    module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_tensor_calls", loader))
+    loader.exec_module(module)
+    lib = load()
+    module.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
+        lib.gemm_nt_gated, lib.gemm_nt_gated_grad, lib.gemm_nt_batched_major, lib.gemm_nt_w4_quantize, lib.gemm_nt_w4,
+        lib.gemm_nt_w4_gated)))
+    _calls = module
+
+
+def _made(result):
+    """What an extension call returned, or its refusal as the exception it stands for."""
+    if result.__class__ is int:
+        raise GemmError(result)
+    return result
 
 
 def _one_of(dtype, allowed, what):
@@ -768,7 +799,9 @@ def moe_few_tokens(X, logits, W13, W2, topk, S13=None, S2=None, renormalize=True
 
 # ---------------------------------------------------------------- the gated feed-forward block, 4-bit weights
 # (As above, written for the host's time per call: on a Grace core a helper's call or an
-# attribute of a tensor costs 0.1-0.3 us of the 8 that a launch with one allocation takes.)
+# attribute of a tensor costs 0.1-0.3 us.  Where the extension is built it takes every call
+# that needs no copy, no other stream and no error message; what it leaves, and all of it
+# where it is not, is done here.)
 _ACTS = {"silu": 0, "gelu": 1, "gelu_tanh": 2}
 _GROUPS = (32, 64, 128)
 _FFN_SHAPES = "shapes: X (tokens, hidden), W13 (2*inner, hidden)"
@@ -815,6 +848,10 @@ def gated_linear(X, W13, activation="silu", keep=False, out=None, path=Path.AUTO
     returned start on 16-byte boundaries; operands whose rows do not (an odd ``hidden``) are
     copied there first, unless a ``path`` is given.
     """
+    if stream is None and _calls is not None:
+        made = _calls.gated(X, W13, _ACTS.get(activation), keep, out, path)
+        if made is not None:
+            return _made(made)
     if stream is not None:
         side = _elsewhere(stream)
         if side is not None:
@@ -854,6 +891,10 @@ def gated_linear_backward(dH, GU, X, W13, activation="silu", stream=None):
     rounded to X's type before the products dX = dGU @ W13 and dW13 = dGU.T @ X,
     which accumulate in float32.  Operands off 16-byte boundaries as in
     :func:`gated_linear`."""
+    if stream is None and _calls is not None:
+        made = _calls.backward(dH, GU, X, W13, _ACTS.get(activation))
+        if made is not None:
+            return _made(made)
     side = _elsewhere(stream)
     if side is not None:
         _record(GU, side, None)
@@ -898,6 +939,10 @@ def quantize_w4(W, group=128, zeros=False, scale_dtype=None, stream=None):
     column in the low half of a byte, rows on 16-byte boundaries; S (rows,
     ceil(cols/group)); Z the same, uint8.
     """
+    if stream is None and _calls is not None:
+        made = _calls.quantize(W, group, zeros, scale_dtype)
+        if made is not None:
+            return _made(made)
     if stream is not None:
         side = _elsewhere(stream)
         if side is not None:
@@ -928,6 +973,10 @@ def quantize_w4(W, group=128, zeros=False, scale_dtype=None, stream=None):
 
 def _w4_product(X, Q, S, Z, group, act, out, path):
     """The plain product with 4-bit weights, or (act not None) the gated one."""
+    if _calls is not None:
+        made = _calls.w4(X, Q, S, Z, group, act, out, path)
+        if made is not None:
+            return _made(made)
     torch = _torch or _init_torch()
     dtype, xsh, qsh, ssh = X.dtype, X.shape, Q.shape, S.shape
     code = _one_of(dtype, _X16, "X")

@@ -5,13 +5,17 @@
 Each CUDA translation unit is compiled in parallel with nvcc, then linked into
 dense_fp16_tensor_gemm_gb300/_build/libgemm_nt.so with the static CUDA runtime
 (no libcuda link: the driver's tensor-map encoder is fetched at run time), so
-the library loads on machines without a GPU driver.
+the library loads on machines without a GPU driver.  Beside it, with g++,
+_build/_tensor_calls.so: the common case of the feed-forward tensor forms as a
+Python extension (csrc/tensor_calls.cpp).
 """
 import concurrent.futures as cf
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(PKG, "csrc")
@@ -19,6 +23,7 @@ ROOT = os.path.dirname(PKG)
 INCLUDE = os.path.join(ROOT, "include")
 OUT_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(OUT_DIR, "libgemm_nt.so")
+CALLS = os.path.join(OUT_DIR, "_tensor_calls.so")
 
 SOURCES = ["gemm_nt_api.cu", "tc05_gemm.cu", "tc05_small.cu", "tc05_pair.cu", "mmasync_gemm.cu", "gemm_nt_no_alloc.cu", "mx_scales.cu",
            "block128_api.cu", "block128_any.cu", "block128_pair.cu", "block128_swap.cu",
@@ -47,8 +52,24 @@ def _deps():
     return files
 
 
+def _calls_command(out):
+    """The g++ command of the Python extension; None where it cannot be built (no
+    torch, no Python headers): the tensor forms are then marshalled in Python alone."""
+    spec = importlib.util.find_spec("torch")
+    include = sysconfig.get_paths()["include"]
+    if spec is None or not os.path.exists(os.path.join(include, "Python.h")):
+        return None
+    torch = list(spec.submodule_search_locations)[0]
+    lib = os.path.join(torch, "lib")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")
+    return ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-I", INCLUDE, "-isystem", os.path.join(torch, "include"),
+            "-isystem", os.path.join(torch, "include", "torch", "csrc", "api", "include"), "-isystem", include,
+            "-isystem", cuda, os.path.join(CSRC, "tensor_calls.cpp"), "-o", out, "-L", lib, "-ltorch_python", "-ltorch_cpu",
+            "-lc10", "-lc10_cuda", "-Wl,-rpath," + lib]
+
+
 def _stale():
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(CALLS) and _calls_command(CALLS):
         return True
     t = os.path.getmtime(LIB)
     return any(os.path.getmtime(f) > t for f in _deps())
@@ -74,8 +95,20 @@ def build(force=False, verbose=False, extra_flags=()):
             print(r.stdout + r.stderr, flush=True)
         return obj
 
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    def compile_calls():
+        tmp = CALLS + ".tmp.%d" % os.getpid()
+        cmd = _calls_command(tmp)
+        if cmd is None:
+            return
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError("g++ failed on tensor_calls.cpp:\n%s%s" % (r.stdout, r.stderr))
+        os.replace(tmp, CALLS)
+
+    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        calls = ex.submit(compile_calls)
         objs = list(ex.map(compile_one, SOURCES))
+        calls.result()
     tmp = LIB + ".tmp.%d" % os.getpid()
     cmd = [cc, *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)

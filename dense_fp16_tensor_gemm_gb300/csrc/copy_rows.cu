@@ -1,7 +1,8 @@
 // copy_rows.cu -- a matrix's rows onto 16-byte boundaries, for kernels that read by TMA
 // or 16 bytes at a time.  A thread writes 16 bytes, gathered in the widest units that the
 // source's base and pitch allow (neighbouring threads share their lines in L1).  Bound by
-// memory: one read and one write.
+// memory, one read and one write, and at 2-byte units by the loads' lines in L1 (4000 x
+// 4097 16-bit elements 16 us).
 #include <algorithm>
 
 #include "ffn.h"

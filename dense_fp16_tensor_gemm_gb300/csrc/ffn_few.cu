@@ -20,6 +20,13 @@
 // i + 4 as small whole numbers in the low bits of 1024 + code (fp16) or 128 + code
 // (bf16), from which 1024 + zero or 128 + zero is subtracted: exact, so the MMA sums
 // (code - zero) x, and a group's sum is scaled in fp32.
+//
+// One token x 4096 x 8192 gated: 23.7 us in bf16 (134 MB, 5.7 TB/s), 13.4 in 4 bits (35 MB);
+// x 4096 x 4096 in 4 bits 6.4, x 8192 x 16384 22.0.  About 4 us of each are launch, first loads
+// and the last sums.  In 4 bits a step of 4096 codes takes some 400 instructions, 112 of them the
+// codes' shifts and logical operations, on the pipe that is busiest.  Rings of two steps
+// (4-bit 12.8 and 21.6, but 4 tokens 9.0 for 8.3) and two CTAs an SM (5.4 for 4096 x 4096, 25 for
+// 8192 x 16384) were measured beside three and three.
 #include <algorithm>
 
 #include "ffn.h"

@@ -21,9 +21,13 @@
 // over all groups; fewer tokens than the tensor cores need take ffn_few.cu, which has
 // none.
 //
-// Few tokens: bound by the weights' bytes, and with 4-bit weights nearly as much by
-// their conversion (8192 weights in about 150 cycles, the bytes' own time 175).
-// Many: by the tensor cores.
+// 16-bit weights: bound by their bytes (64 tokens x 4096 x 8192 gated 27.6 us, x 2048 x 8192
+// 17.5, 6 TB/s between the two and 7 us that every call takes).  4-bit ones, up to 128
+// tokens: by their conversion, 350 cycles for 128 x 64 of them where the bytes take 175 (64 x
+// 16384 x 8192 28.8 us, x 4096 x 4096 12.0; 25.4 without the conversion's arithmetic, 20.5 without
+// the scales either; half the tokens' loads change nothing, so pairs of CTAs would not
+// either).  More tokens: by the tensor cores and the last round of tiles (2048 x 8192 x 4096
+// 89 us, four rounds of 152 tiles for 3.4).
 //
 // Roles (768 threads): warp 0 TMA of the weights, warp 1 MMA issue, warp 2 TMA of
 // the tokens, warp 3 TMEM allocation, warps 4-19 conversion, warps 20-23 epilogue.

@@ -11,7 +11,9 @@
 // codes); a group's 1, 2 or 4 threads share its extremes by shuffles.  Bound by
 // memory, one read of the weights, as long as the instructions stay below it: w * (1/s)
 // is rounded to a whole number by adding 1.5 * 2^23, whose low bits then hold it
-// (|w / s| stays below 32), and a saturating pack clamps and joins two codes.
+// (|w / s| stays below 32), and a saturating pack clamps and joins two codes.  8192 x 8192
+// bf16 in 28.8 us, 5.9 TB/s (16 elements a thread 33.6: the scale's arithmetic is per thread;
+// 8 elements, comparisons and shifts in the place of the pack 80).
 #include <algorithm>
 #include <cfloat>
 
