@@ -12,6 +12,9 @@ namespace gnt {
 
 namespace {
 
+// The longest sum: the kernels step along K in 32 bits.
+constexpr int64_t kMaxK = int64_t(1) << 30;
+
 bool real16(gemm_dtype_t t) { return t == GEMM_DTYPE_F16 || t == GEMM_DTYPE_BF16; }
 bool act_ok(gemm_act_t a) { return a == GEMM_ACT_SILU || a == GEMM_ACT_GELU || a == GEMM_ACT_GELU_TANH; }
 
@@ -61,7 +64,7 @@ int shift_of(int32_t group) { return group == 32 ? 5 : (group == 64 ? 6 : 7); }
 bool maps_ok(const FfnParams& p)
 {
     const int64_t lim = int64_t(1) << 39;
-    return p.k > 0 && p.k <= (1 << 30) && aligned(p.x, 16) && aligned(p.w, 16) && p.ldx % 8 == 0 && p.ldw % (p.scales ? 16 : 8) == 0 &&
+    return p.k > 0 && aligned(p.x, 16) && aligned(p.w, 16) && p.ldx % 8 == 0 && p.ldw % (p.scales ? 16 : 8) == 0 &&
            p.ldx < lim && p.ldw < lim / p.n;
 }
 
@@ -136,7 +139,7 @@ gemm_status_t w4_product(const void* X, int64_t ldx, const gemm_w4_t* W, void* O
                          int gated, int act, int64_t tokens, int64_t n, int64_t K, gemm_path_t path,
                          gemm_stream_t stream)
 {
-    if (path < GEMM_PATH_AUTO || path > GEMM_PATH_TC05_WS)
+    if (K > kMaxK || path < GEMM_PATH_AUTO || path > GEMM_PATH_TC05_WS)
         return GEMM_ERR_INVALID_VALUE;
     if (tokens == 0 || n == 0)
         return GEMM_OK;
@@ -182,7 +185,8 @@ gemm_status_t gemm_nt_gated(const void* X, int64_t ldx, const void* W13, int64_t
                             int64_t ldgu, gemm_dtype_t type, gemm_act_t act, int64_t tokens, int64_t hidden,
                             int64_t inner, gemm_path_t path, gemm_stream_t stream)
 {
-    if (!sizes_ok({tokens, hidden, inner}) || inner > INT32_MAX / 2 || path < GEMM_PATH_AUTO || path > GEMM_PATH_TC05_WS)
+    if (!sizes_ok({tokens, hidden, inner}) || inner > INT32_MAX / 2 || hidden > kMaxK || path < GEMM_PATH_AUTO ||
+        path > GEMM_PATH_TC05_WS)
         return GEMM_ERR_INVALID_VALUE;
     if (tokens == 0 || inner == 0)
         return GEMM_OK;

@@ -434,7 +434,8 @@ typedef enum gemm_act {
  * GEMM_ERR_NOT_SUPPORTED.  AUTO takes one that can, by the tokens and the weights' bytes;
  * paths differ in the order of their sums.
  *
- * tokens or inner 0: nothing to do; hidden 0: zeros.  Any pitch and alignment is
+ * tokens or inner 0: nothing to do; hidden 0: zeros; hidden above 2^30 or inner above
+ * 2^30 - 1: GEMM_ERR_INVALID_VALUE.  Any pitch and alignment is
  * accepted; rows that start on 16-byte boundaries are read fastest.  Outputs that
  * overlap an operand or each other (the byte spans, counting pitches):
  * GEMM_ERR_OVERLAP.  Infinities and NaN follow IEEE arithmetic.  Nothing is allocated,
@@ -518,7 +519,8 @@ gemm_status_t gemm_nt_w4_quantize(const void *W, gemm_dtype_t w_type, int64_t ro
  * alignment leaves nothing else: SKINNY needs the codes on 16-byte boundaries (base and
  * ldc), TC05 X as well.  A group whose scale is infinite or NaN makes its row's sums NaN or
  * infinite, however it is reached.
- * M or N 0: nothing to do; K 0: zeros.  The rest as gemm_nt_gated.
+ * M or N 0: nothing to do; K 0: zeros; K above 2^30: GEMM_ERR_INVALID_VALUE.  The rest as
+ * gemm_nt_gated.
  */
 gemm_status_t gemm_nt_w4(const void *X, int64_t ldx, const gemm_w4_t *W, void *Out, int64_t ldo, gemm_dtype_t type,
                          int64_t M, int64_t N, int64_t K, gemm_path_t path, gemm_stream_t stream);

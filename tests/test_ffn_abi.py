@@ -176,3 +176,15 @@ def test_tensor_forms_refuse():
     ):
         with pytest.raises(TypeError):
             call()
+
+
+def test_sums_longer_than_the_kernels_step(lib):
+    """K is walked in 32 bits: 2^30 is taken, one more is refused before any device call."""
+    x, w, h, s = (i << 40 for i in range(1, 5))
+    for k, refused in ((2 ** 30, False), (2 ** 30 + 1, True), (2 ** 31 - 1, True)):
+        ld = 2 ** 31
+        four = w4(codes=w, ldc=ld, scales=s, lds=2 ** 24)
+        for status in (gated(lib, x=x, ldx=ld, w=w, ldw=ld, h=h, ldh=8, tokens=1, hidden=k, inner=8),
+                       lib.gemm_nt_w4(x, ld, four, h, 8, D.F16, 1, 8, k, 0, None),
+                       lib.gemm_nt_w4_gated(x, ld, four, h, 8, D.F16, 0, 1, k, 8, 0, None)):
+            assert status == INVALID if refused else status not in NEVER
