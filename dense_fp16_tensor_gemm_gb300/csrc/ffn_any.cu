@@ -185,8 +185,8 @@ __global__ void __launch_bounds__(kThreads) ffn_any_kernel(const FfnParams p, in
 cudaError_t ffn_any_launch(const FfnParams& p, int num_sms, cudaStream_t stream)
 {
     const int per = p.gated ? kT / 2 : kT;
-    const int tiles_t = (p.tokens + kT - 1) / kT;
-    const int64_t tiles = static_cast<int64_t>(tiles_t) * ((p.n + per - 1) / per);
+    const int tiles_t = static_cast<int>((int64_t(p.tokens) + kT - 1) / kT);
+    const int64_t tiles = tiles_t * ((int64_t(p.n) + per - 1) / per);
     const unsigned grid = static_cast<unsigned>(std::min<int64_t>(tiles, static_cast<int64_t>(num_sms) * 8));
     if (p.scales) {
         if (p.bf16)

@@ -76,3 +76,28 @@ def test_more_than_2_to_the_31_outputs(op):
         err = 2.0 ** -19 * torch.cat(((t * up).abs() * (1 + gate.abs()), (t * gate).abs()), 1)
         check(d[rows], ref, rounded(err, ref, BF16))
     gnt.gemm_nt_check()
+
+
+@pytest.mark.parametrize("op", ["tokens", "outputs"])
+def test_as_many_rows_as_an_int_counts(op):
+    """2^31 - 1 tokens, and 2^31 - 1 rows of 4-bit weights, with sums of one element."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(2)
+    many = 2 ** 31 - 1
+    rows = torch.tensor([0, 1, 63, 64, 2 ** 30, many - 65, many - 64, many - 63, many - 1], device="cuda")
+    if op == "tokens":
+        x = torch.empty(many, 1, dtype=BF16, device="cuda").normal_(generator=g)
+        w = torch.randn(2, 1, generator=g, device="cuda").to(BF16)
+        out = torch.empty(many, 1, dtype=BF16, device="cuda")
+        gnt.gated_linear(x, w, out=out, path=P.MMASYNC)
+        h, _, eh, _ = gated_bound(x[rows], w, "silu")
+        check(out[rows], h, rounded(eh, h, BF16))
+    else:
+        x = torch.randn(1, 1, generator=g, device="cuda").to(BF16)
+        q = torch.empty(many, 1, dtype=torch.uint8, device="cuda").random_(0, 256, generator=g)
+        s = torch.empty(many, 1, dtype=BF16, device="cuda").uniform_(0.01, 1, generator=g)
+        out = gnt.linear_w4(x, q, s, path=P.MMASYNC)[:, rows]
+        v = w4_values(q[rows], s[rows], None, 128, 1)
+        ref, mag = x.double() @ v.t(), x.double().abs() @ v.abs().t()
+        check(out, ref, rounded(sum_error(mag, 1), ref, BF16))
+    gnt.gemm_nt_check()
