@@ -56,11 +56,10 @@ cudaError_t ffn_swap_launch(const FfnParams& f, int num_sms, cudaStream_t stream
         p.splits *= 2;
     // the weights (the gate's and the up rows apart), the same in turns of 16 rows, the tokens
     CUtensorMap maps[3];
-    int unused;
     const int64_t width = w4 ? (int64_t(f.k) + 1) / 2 : f.k;
     const int wtype = w4 ? GEMM_DTYPE_E4M3 : dtype;  // (codes: bytes)
-    if (!operand_map(&maps[0], f.w, f.n, width, f.ldw, f.gated ? 2 : 1, int64_t(f.n) * f.ldw, f.gated ? 16 : 128, &unused, wtype) ||
-        !operand_map(&maps[2], f.x, f.tokens, f.k, f.ldx, 1, 0, nt, &unused, dtype))
+    if (!call_map(&maps[0], f.w, f.n, width, f.ldw, f.gated ? 2 : 1, int64_t(f.n) * f.ldw, f.gated ? 16 : 128, wtype) ||
+        !call_map(&maps[2], f.x, f.tokens, f.k, f.ldx, 1, 0, nt, dtype))
         return cudaErrorInvalidValue;
     maps[1] = maps[0];
     if (f.gated && f.n >= 64) {

@@ -376,9 +376,8 @@ cudaError_t gated_pair_launch(const FfnParams& f, int max_pairs, cudaStream_t st
     PairParams p{};
     const int dtype = f.bf16 ? GEMM_DTYPE_BF16 : GEMM_DTYPE_F16;
     CUtensorMap tmx, tmw;
-    int unused;
-    if (!operand_map(&tmx, f.x, f.tokens, f.k, f.ldx, 1, 0, 128, &unused, dtype) ||
-        !operand_map(&tmw, f.w, f.n, f.k, f.ldw, 2, int64_t(f.n) * f.ldw, kCols, &unused, dtype))
+    if (!call_map(&tmx, f.x, f.tokens, f.k, f.ldx, 1, 0, 128, dtype) ||
+        !call_map(&tmw, f.w, f.n, f.k, f.ldw, 2, int64_t(f.n) * f.ldw, kCols, dtype))
         return cudaErrorInvalidValue;
     p.out = f.out;
     p.ldo = f.ldo;

@@ -484,18 +484,6 @@ bool encode_scale_rep_map(CUtensorMap* map, const void* base, int64_t rows, int6
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-void remember_map(const MapKey& key, const CUtensorMap& map, int bmul)
-{
-    MapCache& c = t_maps;
-    const int slot = c.next;
-    c.key[slot] = key;
-    c.map[slot] = map;
-    c.bmul[slot] = bmul;
-    c.next = (slot + 1) % MapCache::kEntries;
-    if (c.count < MapCache::kEntries)
-        ++c.count;
-}
-
 bool make_map(CUtensorMap* map, const void* base, int64_t rows, int64_t K, int64_t ld, int64_t batch,
               int64_t stride, int box_rows, int* bmul, int dtype = GEMM_DTYPE_F16, bool mn = false)
 {
@@ -510,7 +498,13 @@ bool make_map(CUtensorMap* map, const void* base, int64_t rows, int64_t K, int64
     }
     if (!encode_map(map, base, rows, K, ld, batch, stride, box_rows, bmul, dtype, mn))
         return false;
-    remember_map(k, *map, *bmul);
+    const int slot = c.next;
+    c.key[slot] = k;
+    c.map[slot] = *map;
+    c.bmul[slot] = *bmul;
+    c.next = (slot + 1) % MapCache::kEntries;
+    if (c.count < MapCache::kEntries)
+        ++c.count;
     return true;
 }
 
@@ -1077,20 +1071,19 @@ bool operand_map(CUtensorMap* map, const void* base, int64_t rows, int64_t K, in
     return make_map(map, base, rows, K, ld, batch, stride, box_rows, bmul, dtype);
 }
 
+bool call_map(CUtensorMap* map, const void* base, int64_t rows, int64_t K, int64_t ld, int64_t batch, int64_t stride,
+              int box_rows, int dtype)
+{
+    int bmul;
+    return encode_map(map, base, rows, K, ld, batch, stride, box_rows, &bmul, dtype, false);
+}
+
 // Gate and up rows of a gated product's weights in turns of 16, as a 4-D tensor
 // {K, 16 rows, gate or up, block of 16 rows}: a box {128 bytes of K, 16, 2, 4} is 128
 // rows of an operand tile.  Whole blocks only: a box that reaches past them would read
 // the up projection's end.
 bool interleaved_map(CUtensorMap* map, const void* base, int64_t n, int64_t K, int64_t ld, int dtype)
 {
-    // (a box height of its own tells these maps from the other ones of the same operand)
-    const MapKey key{base, n, K, ld, 2, n * ld, -16, dtype, false};
-    MapCache& c = t_maps;
-    for (int i = 0; i < c.count; ++i)
-        if (c.key[i] == key) {
-            *map = c.map[i];
-            return true;
-        }
     auto enc = encode_fn();
     if (!enc || n < 16)
         return false;
@@ -1101,14 +1094,11 @@ bool interleaved_map(CUtensorMap* map, const void* base, int64_t n, int64_t K, i
                              static_cast<cuuint64_t>(16 * ld * esize)};
     cuuint32_t box[4] = {static_cast<cuuint32_t>(128 / esize), 16, 2, 4};
     cuuint32_t estr[4] = {1, 1, 1, 1};
-    if (enc(map, bytes ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+    return enc(map, bytes ? CU_TENSOR_MAP_DATA_TYPE_UINT8
                        : (dtype == GEMM_DTYPE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16),
             4, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-        return false;
-    remember_map(key, *map, 1);
-    return true;
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // The CTA-pair kernel with its split scratch taken from memory the caller of
