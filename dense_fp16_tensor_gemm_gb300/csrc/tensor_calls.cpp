@@ -69,7 +69,7 @@ gemm_dtype_t code(at::ScalarType t)
     return t == at::kHalf ? GEMM_DTYPE_F16 : (t == at::kBFloat16 ? GEMM_DTYPE_BF16 : GEMM_DTYPE_F32);
 }
 
-// A small int argument; false if it is none.
+// An int argument; false if it is none, or none of 32 bits.
 bool number(PyObject* o, long& v)
 {
     if (!PyLong_Check(o))
@@ -79,7 +79,17 @@ bool number(PyObject* o, long& v)
         PyErr_Clear();
         return false;
     }
-    return true;
+    return v >= INT32_MIN && v <= INT32_MAX;
+}
+
+// The truth of a flag; false if it has none (what that raises is left to the Python form).
+bool flag(PyObject* o, bool& v)
+{
+    const int t = PyObject_IsTrue(o);
+    if (t < 0)
+        PyErr_Clear();
+    v = t == 1;
+    return t >= 0;
 }
 
 int64_t pitch(int64_t cols, int64_t unit) { return (cols + unit - 1) / unit * unit; }
@@ -128,12 +138,12 @@ PyObject* gated(PyObject*, PyObject* const* a, Py_ssize_t n)
     int index = -1;
     Matrix x, w, h, gu;
     long act, path;
-    if (n != 6 || !matrix(a[0], index, x) || !matrix(a[1], index, w) || !number(a[2], act) || !number(a[5], path) ||
+    bool keep;
+    if (n != 6 || !flag(a[3], keep) || !matrix(a[0], index, x) || !matrix(a[1], index, w) || !number(a[2], act) || !number(a[5], path) ||
         !real16(x.t) || w.t.scalar_type() != x.t.scalar_type() || w.cols != x.cols || w.rows % 2 ||
         index != c10::cuda::current_device() || (path == 0 && (!w.on_grid() || (x.rows > 16 && !x.on_grid()))))
         Py_RETURN_NONE;
     const int64_t inner = w.rows / 2;
-    const bool keep = PyObject_IsTrue(a[3]) == 1;
     if (!output(a[4], x.rows, inner, x.t, index, h))
         Py_RETURN_NONE;
     if (keep) {
@@ -203,7 +213,8 @@ PyObject* quantize(PyObject*, PyObject* const* a, Py_ssize_t n)
     int index = -1;
     Matrix w;
     long group;
-    if (n != 4 || !matrix(a[0], index, w) || !number(a[1], group) || (group != 32 && group != 64 && group != 128) ||
+    bool zeros;
+    if (n != 4 || !flag(a[2], zeros) || !matrix(a[0], index, w) || !number(a[1], group) || (group != 32 && group != 64 && group != 128) ||
         (!real16(w.t) && w.t.scalar_type() != at::kFloat) || index != c10::cuda::current_device())
         Py_RETURN_NONE;
     at::ScalarType st = real16(w.t) ? w.t.scalar_type() : at::kBFloat16;
@@ -214,7 +225,6 @@ PyObject* quantize(PyObject*, PyObject* const* a, Py_ssize_t n)
         if (st != at::kHalf && st != at::kBFloat16)
             Py_RETURN_NONE;
     }
-    const bool zeros = PyObject_IsTrue(a[2]) == 1;
     const int64_t width = (w.cols + 1) / 2, groups = (w.cols + group - 1) / group, ldc = pitch(width, 16);
     const int64_t lds = std::max<int64_t>(groups, 1);
     const at::Tensor q = rows_of(w.rows, width, ldc, w.t, at::kByte), s = rows_of(w.rows, groups, lds, w.t, st);
