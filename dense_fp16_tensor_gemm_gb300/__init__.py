@@ -135,6 +135,8 @@ def load(path=LIB_PATH):
             fn.restype = res
             fn.argtypes = args
         _lib = lib
+        if _torch is not None:
+            _bind_calls()
     return _lib
 
 
@@ -472,13 +474,16 @@ def _init_torch():
     _OUT = (torch.float32, torch.float16, torch.bfloat16)
     _X16 = (torch.float16, torch.bfloat16)
     _torch = torch
-    _bind_calls()
+    if isinstance(_lib, ctypes.CDLL):
+        _bind_calls()
     return torch
 
 
 # The feed-forward forms' common case as an extension (csrc/tensor_calls.cpp): its
 # functions make the whole call, or return None and leave it to the Python forms below.
-# None before the first call, and where the extension has not been built.
+# Bound once both torch and the library are there, as nothing asks for the library before a
+# call's arguments have been checked.  None until then, and where the extension has not been
+# built, or for another torch than the one that is loaded.
 _calls = None
 
 
@@ -489,9 +494,12 @@ def _bind_calls():
         return
     import importlib.machinery
     import importlib.util
-    loader = importlib.machinery.ExtensionFileLoader("_tensor_calls", path)
-    module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_tensor_calls", loader))
-    loader.exec_module(module)
+    try:
+        loader = importlib.machinery.ExtensionFileLoader("_tensor_calls", path)
+        module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_tensor_calls", loader))
+        loader.exec_module(module)
+    except ImportError:
+        return
     lib = load()
     module.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
         lib.gemm_nt_gated, lib.gemm_nt_gated_grad, lib.gemm_nt_batched_major, lib.gemm_nt_w4_quantize, lib.gemm_nt_w4,

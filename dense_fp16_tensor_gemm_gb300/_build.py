@@ -61,6 +61,8 @@ def _calls_command(out):
         return None
     torch = list(spec.submodule_search_locations)[0]
     lib = os.path.join(torch, "lib")
+    if not os.path.exists(os.path.join(lib, "libc10_cuda.so")):  # a torch without CUDA
+        return None
     cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")
     return ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-I", INCLUDE, "-isystem", os.path.join(torch, "include"),
             "-isystem", os.path.join(torch, "include", "torch", "csrc", "api", "include"), "-isystem", include,

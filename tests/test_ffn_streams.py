@@ -84,3 +84,41 @@ def test_one_operand_on_the_host_is_refused(monkeypatch):
         for one in tensors:
             with pytest.raises(ValueError):
                 call(**{k: v if k == one else v.cuda() for k, v in tensors.items()})
+
+
+@pytest.mark.parametrize("name", CALLS)
+def test_host_tensors_are_refused_by_the_first_call_of_all(name, monkeypatch):
+    """Before torch has been looked at, too, nothing asks the library for anything."""
+    class Library:
+        def __getattr__(self, name):
+            raise AssertionError("%s was called" % name)
+    monkeypatch.setattr(gnt, "_torch", None)
+    monkeypatch.setattr(gnt, "_calls", None)
+    monkeypatch.setattr(gnt, "_lib", Library())
+    with pytest.raises(ValueError, match="CUDA device"):
+        CALLS[name]()
+    assert gnt._calls is None
+
+
+def test_the_extension_is_bound_once_torch_and_the_library_are_there(monkeypatch):
+    from dense_fp16_tensor_gemm_gb300 import _build
+    _build.build()
+    for first, second in ((gnt._init_torch, gnt.load), (gnt.load, gnt._init_torch)):
+        monkeypatch.setattr(gnt, "_torch", None)
+        monkeypatch.setattr(gnt, "_calls", None)
+        monkeypatch.setattr(gnt, "_lib", None)
+        first()
+        assert gnt._calls is None
+        second()
+        assert gnt._calls is not None
+
+
+def test_an_extension_that_does_not_load_leaves_the_python_forms(monkeypatch):
+    def refuse(*a):
+        raise ImportError("built for another torch")
+    import importlib.machinery
+    lib = gnt.load()
+    monkeypatch.setattr(importlib.machinery, "ExtensionFileLoader", refuse)
+    monkeypatch.setattr(gnt, "_calls", None)
+    gnt._bind_calls()
+    assert gnt._calls is None and gnt.load() is lib
