@@ -28,7 +28,8 @@ CALLS = os.path.join(OUT_DIR, "_tensor_calls.so")
 SOURCES = ["gemm_nt_api.cu", "tc05_gemm.cu", "tc05_small.cu", "tc05_pair.cu", "mmasync_gemm.cu", "gemm_nt_no_alloc.cu", "mx_scales.cu",
            "block128_api.cu", "block128_any.cu", "block128_pair.cu", "block128_swap.cu",
            "block128_quant.cu", "moe.cu",
-           "ffn_api.cu", "ffn_any.cu", "ffn_few.cu", "ffn_swap.cu", "ffn_swap_f16.cu", "gated_pair.cu", "gated_grad.cu", "w4_quant.cu",
+           "ffn_api.cu", "ffn_any.cu", "ffn_few.cu", "ffn_swap.cu", "ffn_swap_f16.cu", "ffn_swap_plain.cu",
+           "ffn_swap_plain_f16.cu", "gated_pair.cu", "gated_grad.cu", "w4_quant.cu",
            "copy_rows.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-std=c++17", "-O3", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",

@@ -1,5 +1,5 @@
-// ffn_swap.cu -- the products of ffn_swap.cuh: set-up, launch, and the forms for bf16
-// and for 16-bit weights (fp16's 4-bit ones are compiled apart, beside these).
+// ffn_swap.cu -- the products of ffn_swap.cuh: set-up, launch, and the gated forms for bf16
+// and for 16-bit weights (the others are compiled apart, beside these).
 #include "ffn_swap.cuh"
 
 namespace gnt {
@@ -7,15 +7,19 @@ namespace gnt {
 using namespace swp;
 
 cudaError_t ffn_swap_f16(int shift, int nt, const CUtensorMap* maps, const SwapParams* p, int grid, cudaStream_t stream);
+cudaError_t ffn_swap_plain(int shift, int nt, const CUtensorMap* maps, const SwapParams* p, int grid, cudaStream_t stream);
+cudaError_t ffn_swap_plain_f16(int shift, int nt, const CUtensorMap* maps, const SwapParams* p, int grid, cudaStream_t stream);
 
 namespace {
 
 // shift 0: 16-bit weights (whose types differ in the instruction descriptor alone).
-cudaError_t by_kind(int shift, bool bf16, int nt, const CUtensorMap* maps, const SwapParams* p, int grid, cudaStream_t stream)
+cudaError_t by_kind(bool gated, int shift, bool bf16, int nt, const CUtensorMap* maps, const SwapParams* p, int grid, cudaStream_t stream)
 {
     if (shift == 0)
-        return by_tokens<false, true, 0>(nt, maps, p, grid, stream);
-    return bf16 ? by_group<true>(shift, nt, maps, p, grid, stream) : ffn_swap_f16(shift, nt, maps, p, grid, stream);
+        return by_tokens<false, true, true, 0>(nt, maps, p, grid, stream);
+    if (!gated)
+        return bf16 ? ffn_swap_plain(shift, nt, maps, p, grid, stream) : ffn_swap_plain_f16(shift, nt, maps, p, grid, stream);
+    return bf16 ? by_group<true, true>(shift, nt, maps, p, grid, stream) : ffn_swap_f16(shift, nt, maps, p, grid, stream);
 }
 
 }  // namespace
@@ -27,9 +31,11 @@ cudaError_t ffn_swap_configure()
             for (bool bf16 : {true, false}) {
                 if (shift == 0 && (!bf16 || nt > kSwapTokens))
                     continue;
-                const cudaError_t e = by_kind(shift, bf16, nt, nullptr, nullptr, 0, nullptr);
-                if (e != cudaSuccess)
-                    return e;
+                for (bool gated : {true, false}) {
+                    const cudaError_t e = by_kind(gated, shift, bf16, nt, nullptr, nullptr, 0, nullptr);
+                    if (e != cudaSuccess)
+                        return e;
+                }
             }
     return cudaSuccess;
 }
@@ -68,7 +74,7 @@ cudaError_t ffn_swap_launch(const FfnParams& f, int num_sms, cudaStream_t stream
         p.whole = f.n % 16 == 0 ? (f.n + 63) / 64 * 64 : f.n;
     }
     const int grid = p.splits > 1 ? p.num_tiles * p.splits : std::min(p.num_tiles, num_sms);
-    return by_kind(f.group_shift, f.bf16, nt, maps, &p, grid, stream);
+    return by_kind(f.gated, f.group_shift, f.bf16, nt, maps, &p, grid, stream);
 }
 
 }  // namespace gnt

@@ -22,12 +22,12 @@
 // none.
 //
 // 16-bit weights: bound by their bytes (64 tokens x 4096 x 8192 gated 27.6 us, x 2048 x 8192
-// 17.5, 6 TB/s between the two and 7 us that every call takes).  4-bit ones, up to 128
+// 15.3, 6 TB/s between the two and 7 us that every call takes).  4-bit ones, up to 128
 // tokens: by their conversion, 350 cycles for 128 x 64 of them where the bytes take 175 (64 x
-// 16384 x 8192 28.8 us, x 4096 x 4096 12.0; 25.4 without the conversion's arithmetic, 20.5 without
+// 16384 x 8192 27.9 us, x 4096 x 4096 12.0; 25.4 without the conversion's arithmetic, 20.5 without
 // the scales either; half the tokens' loads change nothing, so pairs of CTAs would not
 // either).  More tokens: by the tensor cores and the last round of tiles (2048 x 8192 x 4096
-// 89 us, four rounds of 152 tiles for 3.4).
+// 87 us, four rounds of 152 tiles for 3.4).
 //
 // Roles (768 threads): warp 0 TMA of the weights, warp 1 MMA issue, warp 2 TMA of
 // the tokens, warp 3 TMEM allocation, warps 4-19 conversion, warps 20-23 epilogue.
@@ -179,14 +179,14 @@ struct Piece {
               // of codes is as many of the ring's (what keeps the conversion's sets together)
 };
 // The i-th piece of this CTA; false if there is none.
-template <bool W4>
+template <bool W4, bool GATED>
 __device__ __forceinline__ bool piece_at(const SwapParams& p, int i, int nt, int rank, Piece& c)
 {
     const int t = static_cast<int>(blockIdx.x) / p.splits + i * (static_cast<int>(gridDim.x) / p.splits);
     if (t >= p.num_tiles)
         return false;
     // neighbouring CTAs take the token tiles of one tile of the weights
-    c.o0 = t / p.tiles_t * (p.f.gated ? kRowsW / 2 : kRowsW);
+    c.o0 = t / p.tiles_t * (GATED ? kRowsW / 2 : kRowsW);
     c.t0 = t % p.tiles_t * nt;
     // shares of whole stages of codes
     const int groups = (p.num_kb + kRawKb - 1) / kRawKb;
@@ -198,18 +198,40 @@ __device__ __forceinline__ bool piece_at(const SwapParams& p, int i, int nt, int
     return true;
 }
 
+// The outputs of 32 tokens in a lane pair of a gated product: lanes 16-31 (`up`) hold rows of the
+// up projection, and store the odd tokens.
+template <int ACT>
+__device__ __forceinline__ void store_gated(const FfnParams& p, int o, int up, int tok0, const float (&v)[32])
+{
+    float h[16];
+#pragma unroll
+    for (int j = 0; j < 32; j += 2) {
+        const float other = __shfl_xor_sync(0xffffffffu, up ? v[j] : v[j + 1], 16);
+        const float g = up ? other : v[j], u = up ? v[j + 1] : other;
+        h[j / 2] = act_value(g, ACT) * u;
+    }
+    unsigned short* dst = static_cast<unsigned short*>(p.out) + static_cast<int64_t>(tok0 + up) * p.ldo + o;
+    const int left = o < p.n ? p.tokens - tok0 - up : 0;
+#pragma unroll
+    for (int j = 0; j < 32; j += 2) {
+        if (j < left)
+            *dst = p.bf16 ? __bfloat16_as_ushort(__float2bfloat16_rn(h[j / 2])) : __half_as_ushort(__float2half_rn(h[j / 2]));
+        dst += 2 * p.ldo;
+    }
+}
+
 // This lane's row of the weights, 32 tokens: its outputs (plain), or with the lane that
 // holds the other projection's row the outputs of half the tokens each (gated).
+template <bool GATED>
 __device__ __forceinline__ void store_tokens(const FfnParams& p, int o0, int row, int tok0, const float (&v)[32], int lane)
 {
-    unsigned short* out = static_cast<unsigned short*>(p.out);
     const auto bits = [&](float f) {
         return p.bf16 ? __bfloat16_as_ushort(__float2bfloat16_rn(f)) : __half_as_ushort(__float2half_rn(f));
     };
-    if (!p.gated) {
+    if constexpr (!GATED) {
         const int o = o0 + row;
         if (o < p.n) {
-            unsigned short* dst = out + static_cast<int64_t>(tok0) * p.ldo + o;
+            unsigned short* dst = static_cast<unsigned short*>(p.out) + static_cast<int64_t>(tok0) * p.ldo + o;
 #pragma unroll
             for (int j = 0; j < 32; ++j) {
                 if (tok0 + j < p.tokens)
@@ -217,32 +239,31 @@ __device__ __forceinline__ void store_tokens(const FfnParams& p, int o0, int row
                 dst += p.ldo;
             }
         }
-        return;
-    }
-    const int up = lane >> 4;  // lanes 16-31 hold rows of the up projection, and store the odd tokens
-    const int o = o0 + (row >> 5) * 16 + (lane & 15);
-    if (p.gu && o < p.n) {
-        unsigned short* dst = static_cast<unsigned short*>(p.gu) + static_cast<int64_t>(tok0) * p.ldgu + o + (up ? p.n : 0);
+    } else {
+        const int up = lane >> 4;
+        const int o = o0 + (row >> 5) * 16 + (lane & 15);
+        if (p.gu && o < p.n) {
+            unsigned short* dst = static_cast<unsigned short*>(p.gu) + static_cast<int64_t>(tok0) * p.ldgu + o + (up ? p.n : 0);
 #pragma unroll
-        for (int j = 0; j < 32; ++j) {
-            if (tok0 + j < p.tokens)
-                *dst = bits(v[j]);
-            dst += p.ldgu;
+            for (int j = 0; j < 32; ++j) {
+                if (tok0 + j < p.tokens)
+                    *dst = bits(v[j]);
+                dst += p.ldgu;
+            }
         }
-    }
-    unsigned short* dst = out + static_cast<int64_t>(tok0 + up) * p.ldo + o;
-#pragma unroll
-    for (int j = 0; j < 32; j += 2) {
-        const float other = __shfl_xor_sync(0xffffffffu, up ? v[j] : v[j + 1], 16);
-        const float g = up ? other : v[j], u = up ? v[j + 1] : other;
-        if (o < p.n && tok0 + j + up < p.tokens)
-            *dst = bits(act_value(g, p.act) * u);
-        dst += 2 * p.ldo;
+        // (the activation is chosen once: a choice per output is a branch behind which the next
+        // output's arithmetic waits: 2048 tokens x 2048 x 8192 in 4 bits 171 us, 98 so; 8 outputs
+        // at a time 113)
+        switch (p.act) {
+        case kActSilu: store_gated<kActSilu>(p, o, up, tok0, v); break;
+        case kActGelu: store_gated<kActGelu>(p, o, up, tok0, v); break;
+        default: store_gated<kActGeluTanh>(p, o, up, tok0, v);
+        }
     }
 }
 
 // GS: the group's length, as a shift.
-template <bool W4, bool BF16, int NT, int GS>
+template <bool W4, bool BF16, bool GATED, int NT, int GS>
 __global__ void __launch_bounds__(kThreads, 1)
     ffn_swap_kernel(const __grid_constant__ CUtensorMap tmw, const __grid_constant__ CUtensorMap tmi,
                     const __grid_constant__ CUtensorMap tmx, const SwapParams p)
@@ -305,13 +326,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 0 && lane == 0) {
         // the first ring of weights comes into L2 while the preceding grids finish
         Piece c;
-        if (piece_at<W4>(p, 0, NT, rank, c)) {
+        if (piece_at<W4, GATED>(p, 0, NT, rank, c)) {
             constexpr int step = W4 ? kRawKb : 1;
             for (int i = 0, kb = c.kb0; i < (W4 ? C::kRaw : C::kKb * kStages) && kb < c.kb1; ++i, kb += step) {
                 const int x = W4 ? kb * (BK / 2) : kb * BK;
-                if (f.gated && c.o0 + kRowsW / 2 <= p.whole)
+                if (GATED && c.o0 + kRowsW / 2 <= p.whole)
                     tma_prefetch_l2_4d(&tmi, x, 0, 0, c.o0 / 16);
-                else if (!f.gated)
+                else if (!GATED)
                     tma_prefetch_l2_3d(&tmw, x, c.o0, 0);
             }
         }
@@ -341,7 +362,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t phase = 0, filled = 0, parity = 0;
             bool first = true, ok = true;
             Piece c;
-            for (int i = 0; ok && piece_at<W4>(p, i, NT, rank, c); ++i) {
+            for (int i = 0; ok && piece_at<W4, GATED>(p, i, NT, rank, c); ++i) {
                 for (int kb = c.kb0; kb < c.kb1; kb += kbs) {
                     if (!wait_bounded(smem_u32(&eb[s]), phase ^ 1, abort_flag, limit)) {
                         gave_up();
@@ -359,10 +380,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int b = 0; b < n; ++b) {
                             const uint32_t dst = smem_u32(base) + (W4 ? s : s * kbs + b) * bytes;
                             const int x = W4 ? kb * (BK / 2) : (kb + b) * BK;
-                            if (f.gated && c.o0 + kRowsW / 2 <= p.whole) {
+                            if (GATED && c.o0 + kRowsW / 2 <= p.whole) {
                                 // (eight boxes a k-block held 64 tokens x 2048 x 8192 to 24.0 us, one 18)
                                 tma_load_4d(dst, &tmi, bar, x, 0, 0, c.o0 / 16);
-                            } else if (f.gated) {
+                            } else if (GATED) {
                                 // the last tile, where it ends inside 16 rows
 #pragma unroll 1
                                 for (int q = 0; q < 8; ++q)  // 16 rows of the gate, the same of the up projection
@@ -387,7 +408,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t phase = 0, filled = 0, parity = 0;
             bool ok = true;
             Piece c;
-            for (int i = 0; ok && piece_at<W4>(p, i, NT, rank, c); ++i) {
+            for (int i = 0; ok && piece_at<W4, GATED>(p, i, NT, rank, c); ++i) {
                 for (int kb = c.kb0; kb < c.end; kb += C::kKb) {
                     if (!wait_bounded(smem_u32(&empty[s]), phase ^ 1, abort_flag, limit)) {
                         gave_up();
@@ -422,7 +443,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             bool skip_release = f.fault == 2 && blockIdx.x == 0;  // test hook: lose one stage release
             bool ok = true;
             Piece c;
-            for (int i = 0; ok && piece_at<W4>(p, i, NT, rank, c); ++i) {
+            for (int i = 0; ok && piece_at<W4, GATED>(p, i, NT, rank, c); ++i) {
                 const int buf = i % C::kAccs;
                 if (!blk::wait_lanes(smem_u32(&tempty[buf]), ((i / C::kAccs) & 1) ^ 1, abort_flag, limit)) {
                     gave_up();
@@ -489,9 +510,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t phase = 0, rphase = 0;
         bool ok = true;
         Piece c;
-        for (int i = 0; ok && piece_at<W4>(p, i, NT, rank, c); ++i) {
-            const int o = f.gated ? c.o0 + (r >> 5) * 16 + (r & 15) : c.o0 + r;
-            const int64_t row = o + (f.gated && (r & 16) ? static_cast<int64_t>(f.n) : 0);
+        for (int i = 0; ok && piece_at<W4, GATED>(p, i, NT, rank, c); ++i) {
+            const int o = GATED ? c.o0 + (r >> 5) * 16 + (r & 15) : c.o0 + r;
+            const int64_t row = o + (GATED && (r & 16) ? static_cast<int64_t>(f.n) : 0);
             // (rows past the weights are converted with the last one's scales and not stored)
             const int64_t at = o < f.n ? row : static_cast<int64_t>(f.n) - 1;
             const uint16_t* srow = static_cast<const uint16_t*>(f.scales) + at * f.lds;
@@ -630,7 +651,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ------------------------------------------------------------ epilogue
         const int q = warp & 3;
         Piece c;
-        for (int i = 0; piece_at<W4>(p, i, NT, rank, c); ++i) {
+        for (int i = 0; piece_at<W4, GATED>(p, i, NT, rank, c); ++i) {
             const int buf = i % C::kAccs;
             if (!blk::wait_lanes(smem_u32(&tfull[buf]), (i / C::kAccs) & 1, abort_flag, limit)) {
                 gave_up();
@@ -649,7 +670,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int j = 0; j < 32; ++j)
                     v[j] = __uint_as_float(r[j]);
                 if (p.splits == 1) {
-                    store_tokens(f, c.o0, q * 32 + lane, c.t0 + n, v, lane);
+                    store_tokens<GATED>(f, c.o0, q * 32 + lane, c.t0 + n, v, lane);
                 } else {
                     // every MMA has read its operands: the stages take the sums, [token][row]
                     float* sums = reinterpret_cast<float*>(smem) + n * kRowsW + q * 32 + lane;
@@ -671,7 +692,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // A split has one tile per cluster.  Each CTA sums 32 tokens at a time, in the CTAs' order.
         cluster_sync();
         Piece c;
-        if (warp >= 20 && piece_at<W4>(p, 0, NT, rank, c)) {
+        if (warp >= 20 && piece_at<W4, GATED>(p, 0, NT, rank, c)) {
             const int row = (warp & 3) * 32 + lane;
             for (int n = rank * 32; n < NT && c.t0 + n < f.tokens; n += p.splits * 32) {
                 float v[32] = {};
@@ -681,7 +702,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int j = 0; j < 32; ++j)
                         v[j] += lds_cluster(at + j * (kRowsW * 4));
                 }
-                store_tokens(f, c.o0, row, c.t0 + n, v, lane);
+                store_tokens<GATED>(f, c.o0, row, c.t0 + n, v, lane);
             }
         }
         cluster_sync();  // nobody leaves while its sums are read
@@ -692,10 +713,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-template <bool W4, bool BF16, int NT, int GS>
+template <bool W4, bool BF16, bool GATED, int NT, int GS>
 cudaError_t run(const CUtensorMap* maps, const SwapParams* p, int grid, cudaStream_t stream)
 {
-    auto* kernel = ffn_swap_kernel<W4, BF16, NT, GS>;
+    auto* kernel = ffn_swap_kernel<W4, BF16, GATED, NT, GS>;
     if (!p)
         return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<W4, NT>::kSmem);
     cudaLaunchAttribute attr[2];
@@ -715,27 +736,27 @@ cudaError_t run(const CUtensorMap* maps, const SwapParams* p, int grid, cudaStre
     return cudaLaunchKernelEx(&cfg, kernel, maps[0], maps[1], maps[2], *p);
 }
 
-template <bool W4, bool BF16, int GS>
+template <bool W4, bool BF16, bool GATED, int GS>
 cudaError_t by_tokens(int nt, const CUtensorMap* maps, const SwapParams* p, int grid, cudaStream_t stream)
 {
     if (nt == 32)
-        return run<W4, BF16, 32, GS>(maps, p, grid, stream);
+        return run<W4, BF16, GATED, 32, GS>(maps, p, grid, stream);
     if constexpr (W4) {
         if (nt == 256)
-            return run<W4, BF16, 256, GS>(maps, p, grid, stream);
+            return run<W4, BF16, GATED, 256, GS>(maps, p, grid, stream);
         if (nt == 128)
-            return run<W4, BF16, 128, GS>(maps, p, grid, stream);
+            return run<W4, BF16, GATED, 128, GS>(maps, p, grid, stream);
     }
-    return run<W4, BF16, 64, GS>(maps, p, grid, stream);
+    return run<W4, BF16, GATED, 64, GS>(maps, p, grid, stream);
 }
 
-template <bool BF16>
+template <bool BF16, bool GATED>
 cudaError_t by_group(int shift, int nt, const CUtensorMap* maps, const SwapParams* p, int grid, cudaStream_t stream)
 {
     switch (shift) {
-    case 5: return by_tokens<true, BF16, 5>(nt, maps, p, grid, stream);
-    case 6: return by_tokens<true, BF16, 6>(nt, maps, p, grid, stream);
-    default: return by_tokens<true, BF16, 7>(nt, maps, p, grid, stream);
+    case 5: return by_tokens<true, BF16, GATED, 5>(nt, maps, p, grid, stream);
+    case 6: return by_tokens<true, BF16, GATED, 6>(nt, maps, p, grid, stream);
+    default: return by_tokens<true, BF16, GATED, 7>(nt, maps, p, grid, stream);
     }
 }
 

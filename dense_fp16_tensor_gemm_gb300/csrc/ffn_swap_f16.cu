@@ -1,11 +1,11 @@
-// ffn_swap_f16.cu -- the products of ffn_swap.cuh with 4-bit weights for fp16 tokens.
+// ffn_swap_f16.cu -- the gated products of ffn_swap.cuh with 4-bit weights for fp16 tokens.
 #include "ffn_swap.cuh"
 
 namespace gnt {
 
 cudaError_t ffn_swap_f16(int shift, int nt, const CUtensorMap* maps, const swp::SwapParams* p, int grid, cudaStream_t stream)
 {
-    return swp::by_group<false>(shift, nt, maps, p, grid, stream);
+    return swp::by_group<false, true>(shift, nt, maps, p, grid, stream);
 }
 
 }  // namespace gnt

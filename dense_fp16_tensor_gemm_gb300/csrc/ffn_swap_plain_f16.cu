@@ -1,0 +1,11 @@
+// ffn_swap_plain_f16.cu -- the plain products of ffn_swap.cuh with 4-bit weights for fp16 tokens.
+#include "ffn_swap.cuh"
+
+namespace gnt {
+
+cudaError_t ffn_swap_plain_f16(int shift, int nt, const CUtensorMap* maps, const swp::SwapParams* p, int grid, cudaStream_t stream)
+{
+    return swp::by_group<false, false>(shift, nt, maps, p, grid, stream);
+}
+
+}  // namespace gnt
