@@ -503,7 +503,7 @@ def _bind_calls():
     lib = load()
     module.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
         lib.gemm_nt_gated, lib.gemm_nt_gated_grad, lib.gemm_nt_batched_major, lib.gemm_nt_w4_quantize, lib.gemm_nt_w4,
-        lib.gemm_nt_w4_gated)))
+        lib.gemm_nt_w4_gated, lib.gemm_nt_copy_rows)))
     _calls = module
 
 
@@ -808,7 +808,7 @@ def moe_few_tokens(X, logits, W13, W2, topk, S13=None, S2=None, renormalize=True
 # ---------------------------------------------------------------- the gated feed-forward block, 4-bit weights
 # (As above, written for the host's time per call: on a Grace core a helper's call or an
 # attribute of a tensor costs 0.1-0.3 us.  Where the extension is built it takes every call
-# that needs no copy, no other stream and no error message; what it leaves, and all of it
+# that needs no other stream and no error message; what it leaves, and all of it
 # where it is not, is done here.)
 _ACTS = {"silu": 0, "gelu": 1, "gelu_tanh": 2}
 _GROUPS = (32, 64, 128)

@@ -1,5 +1,5 @@
 // tensor_calls.cpp -- the common case of the feed-forward tensor forms in one call from
-// Python: tensors that need no copy, no other stream and no error message.
+// Python: tensors that need no other stream and no error message.
 //
 // A decoded token's product takes the GPU 4 to 6 us and took Python 11, half of it in looking
 // up shapes, strides, types and addresses one by one.  Each function here looks at all of
@@ -7,7 +7,7 @@
 //   the result    when the call was made,
 //   an int        when the library refused it (the status),
 //   None          when anything is out of the ordinary: the Python form then does the whole
-//                 call, with its checks, messages, copies and streams.
+//                 call, with its checks, messages and streams.
 // So what is checked here decides only which of the two runs; nothing is refused here.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
@@ -33,6 +33,7 @@ decltype(&gemm_nt_batched_major) p_major;
 decltype(&gemm_nt_w4_quantize) p_quantize;
 decltype(&gemm_nt_w4) p_w4;
 decltype(&gemm_nt_w4_gated) p_w4_gated;
+decltype(&gemm_nt_copy_rows) p_copy;
 
 struct Matrix {
     at::Tensor t;
@@ -108,6 +109,20 @@ gemm_stream_t stream_of(int index)
     return reinterpret_cast<gemm_stream_t>(c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(index)).stream());
 }
 
+// Copies a matrix of 16-bit elements onto 16-byte boundaries, if it lies off them.
+gemm_status_t to_grid(Matrix& m, gemm_stream_t stream)
+{
+    if (m.on_grid())
+        return GEMM_OK;
+    const at::Tensor copy = rows_of(m.rows, m.cols, m.t);
+    const int64_t ld = pitch(m.cols, 8);
+    const gemm_status_t st = p_copy(m.at, 2 * m.ld, copy.data_ptr(), 2 * ld, m.rows, 2 * m.cols, stream);
+    m.t = copy;
+    m.ld = ld;
+    m.at = copy.data_ptr();
+    return st;
+}
+
 // The caller's own output, or a new one.
 bool output(PyObject* o, int64_t rows, int64_t cols, const at::Tensor& like, int index, Matrix& m)
 {
@@ -141,7 +156,7 @@ PyObject* gated(PyObject*, PyObject* const* a, Py_ssize_t n)
     bool keep;
     if (n != 6 || !flag(a[3], keep) || !matrix(a[0], index, x) || !matrix(a[1], index, w) || !number(a[2], act) || !number(a[5], path) ||
         !real16(x.t) || w.t.scalar_type() != x.t.scalar_type() || w.cols != x.cols || w.rows % 2 ||
-        index != c10::cuda::current_device() || (path == 0 && (!w.on_grid() || (x.rows > 16 && !x.on_grid()))))
+        index != c10::cuda::current_device())
         Py_RETURN_NONE;
     const int64_t inner = w.rows / 2;
     if (!output(a[4], x.rows, inner, x.t, index, h))
@@ -151,9 +166,15 @@ PyObject* gated(PyObject*, PyObject* const* a, Py_ssize_t n)
         gu.at = gu.t.data_ptr();
         gu.ld = pitch(2 * inner, 8);
     }
+    const gemm_stream_t stream = stream_of(index);
     const gemm_status_t st = unlocked([&] {
+        gemm_status_t s = path == 0 ? to_grid(w, stream) : GEMM_OK;
+        if (s == GEMM_OK && path == 0 && x.rows > 16)
+            s = to_grid(x, stream);
+        if (s != GEMM_OK)
+            return s;
         return p_gated(x.at, x.ld, w.at, w.ld, h.at, h.ld, gu.at, gu.ld, code(x.t.scalar_type()), static_cast<gemm_act_t>(act),
-                       x.rows, x.cols, inner, static_cast<gemm_path_t>(path), stream_of(index));
+                       x.rows, x.cols, inner, static_cast<gemm_path_t>(path), stream);
     });
     if (st != GEMM_OK)
         return PyLong_FromLong(st);
@@ -179,7 +200,7 @@ PyObject* backward(PyObject*, PyObject* const* a, Py_ssize_t n)
         !number(a[4], act) || !real16(x.t) || w.t.scalar_type() != x.t.scalar_type() ||
         d.t.scalar_type() != x.t.scalar_type() || gu.t.scalar_type() != x.t.scalar_type() || w.cols != x.cols || w.rows % 2 ||
         d.rows != x.rows || 2 * d.cols != w.rows || gu.rows != x.rows || gu.cols != w.rows ||
-        index != c10::cuda::current_device() || !w.on_grid() || !x.on_grid())
+        index != c10::cuda::current_device())
         Py_RETURN_NONE;
     const at::Tensor dgu = rows_of(x.rows, w.rows, x.t), dx = rows_of(x.rows, x.cols, x.t), dw = rows_of(w.rows, x.cols, x.t);
     const gemm_dtype_t t = code(x.t.scalar_type());
@@ -187,7 +208,11 @@ PyObject* backward(PyObject*, PyObject* const* a, Py_ssize_t n)
     const gemm_stream_t stream = stream_of(index);
     void *pg = dgu.data_ptr(), *px = dx.data_ptr(), *pw = dw.data_ptr();
     const gemm_status_t st = unlocked([&] {
-        gemm_status_t s = p_grad(d.at, d.ld, gu.at, gu.ld, pg, ldg, t, static_cast<gemm_act_t>(act), x.rows, d.cols, stream);
+        gemm_status_t s = to_grid(w, stream);
+        if (s == GEMM_OK)
+            s = to_grid(x, stream);
+        if (s == GEMM_OK)
+            s = p_grad(d.at, d.ld, gu.at, gu.ld, pg, ldg, t, static_cast<gemm_act_t>(act), x.rows, d.cols, stream);
         if (s == GEMM_OK)
             s = p_major(pg, GEMM_MAJOR_K, w.at, GEMM_MAJOR_MN, px, t, t, x.rows, x.cols, w.rows, ldg, w.ld, ldo, 0, 0, 0, 1,
                         GEMM_PATH_AUTO, stream);
@@ -267,8 +292,6 @@ PyObject* w4(PyObject*, PyObject* const* a, Py_ssize_t n)
     if (a[3] != Py_None &&
         (!matrix(a[3], index, z) || z.t.scalar_type() != at::kByte || z.rows != q.rows || z.cols != groups))
         Py_RETURN_NONE;
-    if (path == 0 && x.rows > 16 && !x.on_grid())
-        Py_RETURN_NONE;
     const int64_t width = is_gated ? q.rows / 2 : q.rows;
     if (!output(a[6], x.rows, width, x.t, index, out))
         Py_RETURN_NONE;
@@ -276,24 +299,28 @@ PyObject* w4(PyObject*, PyObject* const* a, Py_ssize_t n)
                          static_cast<int32_t>(group)};
     const gemm_dtype_t t = code(x.t.scalar_type());
     const gemm_path_t way = static_cast<gemm_path_t>(path);
+    const gemm_stream_t stream = stream_of(index);
     const gemm_status_t st = unlocked([&] {
+        const gemm_status_t s = path == 0 && x.rows > 16 ? to_grid(x, stream) : GEMM_OK;
+        if (s != GEMM_OK)
+            return s;
         return is_gated ? p_w4_gated(x.at, x.ld, &w, out.at, out.ld, t, static_cast<gemm_act_t>(act), x.rows, x.cols, width,
-                                     way, stream_of(index))
-                        : p_w4(x.at, x.ld, &w, out.at, out.ld, t, x.rows, width, x.cols, way, stream_of(index));
+                                     way, stream)
+                        : p_w4(x.at, x.ld, &w, out.at, out.ld, t, x.rows, width, x.cols, way, stream);
     });
     return st == GEMM_OK ? given_or(a[6], out) : PyLong_FromLong(st);
     END_HANDLE_TH_ERRORS
 }
 
-// bind(addresses of the six entry points, in the order above)
+// bind(addresses of the seven entry points, in the order above)
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n)
 {
-    void* at[6];
-    if (n != 6) {
-        PyErr_SetString(PyExc_TypeError, "six addresses");
+    void* at[7];
+    if (n != 7) {
+        PyErr_SetString(PyExc_TypeError, "seven addresses");
         return nullptr;
     }
-    for (int i = 0; i < 6; ++i) {
+    for (int i = 0; i < 7; ++i) {
         at[i] = PyLong_AsVoidPtr(a[i]);
         if (PyErr_Occurred())
             return nullptr;
@@ -304,6 +331,7 @@ PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n)
     p_quantize = reinterpret_cast<decltype(p_quantize)>(at[3]);
     p_w4 = reinterpret_cast<decltype(p_w4)>(at[4]);
     p_w4_gated = reinterpret_cast<decltype(p_w4_gated)>(at[5]);
+    p_copy = reinterpret_cast<decltype(p_copy)>(at[6]);
     Py_RETURN_NONE;
 }
 
