@@ -2,8 +2,10 @@
 //   dg = dh u act'(g),  du = dh act(g)
 // from dh and the g and u that the forward pass kept.  Each of dg and du is
 // rounded once to 16 bits, the operands' type of the two products that follow.
-// Bound by memory: 6 bytes read and 4 written per element (4096 x 8192 in 56 us, 6.0 TB/s;
-// at an odd width, where nothing but single elements can be read, 3001 x 2047 in 16 us).
+// Bound by memory: 6 bytes read and 4 written per element (4096 x 8192 silu in 50 us, 6.7 TB/s;
+// 55 where the activation was chosen per element), with gelu by erfc's and exp's instructions
+// (81 us).  At an odd width, where nothing but single elements can be read, 3001 x 2047 silu
+// in 16 us.
 #include <algorithm>
 
 #include "ffn.h"
@@ -22,17 +24,17 @@ __device__ __forceinline__ float2 unpack(uint32_t v)
     return __half22float2(*reinterpret_cast<const __half2*>(&v));
 }
 
-template <bool BF16>
-__device__ __forceinline__ void grad(float dh, float g, float u, int act, float& dg, float& du)
+template <int ACT>
+__device__ __forceinline__ void grad(float dh, float g, float u, float& dg, float& du)
 {
-    const ActP a = act_p<true>(g, act);
+    const ActP a = act_p<true>(g, ACT);
     // (where P' is 0 the slope is P, also for an infinite g)
     dg = dh * u * (a.d == 0.f ? a.p : fmaf(g, a.d, a.p));
     du = dh * (g * a.p);
 }
 
 // 8 elements per thread and operand, rows that allow 16-byte loads and stores.
-template <bool BF16>
+template <bool BF16, int ACT>
 __global__ void __launch_bounds__(kThreads) gated_grad_kernel(const GradParams p, int64_t per_row, int64_t total)
 {
     using S = OutStore<BF16 ? kOutBF16 : kOutF16>;
@@ -51,8 +53,8 @@ __global__ void __launch_bounds__(kThreads) gated_grad_kernel(const GradParams p
         for (int k = 0; k < 4; ++k) {
             const float2 fd = unpack<BF16>(dw[k]), fg = unpack<BF16>(gw[k]), fu = unpack<BF16>(uw[k]);
             float2 a, b;
-            grad<BF16>(fd.x, fg.x, fu.x, p.act, a.x, b.x);
-            grad<BF16>(fd.y, fg.y, fu.y, p.act, a.y, b.y);
+            grad<ACT>(fd.x, fg.x, fu.x, a.x, b.x);
+            grad<ACT>(fd.y, fg.y, fu.y, a.y, b.y);
             og[k] = S::pack(a.x, a.y);
             ou[k] = S::pack(b.x, b.y);
         }
@@ -64,7 +66,7 @@ __global__ void __launch_bounds__(kThreads) gated_grad_kernel(const GradParams p
 
 // Any layout (an odd number of columns puts u's and du's rows off every boundary): single
 // elements, four of a row in flight per thread, blockDim.y rows to a CTA.
-template <bool BF16>
+template <bool BF16, int ACT>
 __global__ void __launch_bounds__(kThreads) gated_grad_any_kernel(const GradParams p)
 {
     using S = OutStore<BF16 ? kOutBF16 : kOutF16>;
@@ -92,7 +94,7 @@ __global__ void __launch_bounds__(kThreads) gated_grad_any_kernel(const GradPara
                 const int64_t col = c + k * blockDim.x;
                 if (col < p.n) {
                     float a, b;
-                    grad<BF16>(at(d[k]), at(g[k]), at(u[k]), p.act, a, b);
+                    grad<ACT>(at(d[k]), at(g[k]), at(u[k]), a, b);
                     out[col] = S::pack(a, 0.f) & 0xffffu;
                     out[p.n + col] = S::pack(b, 0.f) & 0xffffu;
                 }
@@ -101,30 +103,42 @@ __global__ void __launch_bounds__(kThreads) gated_grad_any_kernel(const GradPara
     }
 }
 
-}  // namespace
-
-cudaError_t gated_grad_launch(const GradParams& p, int num_sms, cudaStream_t stream)
+template <bool BF16, int ACT>
+void launch(const GradParams& p, int num_sms, cudaStream_t stream)
 {
     const auto on16 = [](const void* q, int64_t ld) { return reinterpret_cast<uintptr_t>(q) % 16 == 0 && ld % 8 == 0; };
-    const bool vec = p.n % 8 == 0 && on16(p.dh, p.ldd) && on16(p.gu, p.ldgu) && on16(p.out, p.ldo);
-    if (vec) {
+    if (p.n % 8 == 0 && on16(p.dh, p.ldd) && on16(p.gu, p.ldgu) && on16(p.out, p.ldo)) {
         const int64_t per_row = p.n / 8, total = per_row * p.tokens;
         const unsigned grid = static_cast<unsigned>(std::min<int64_t>((total + kThreads - 1) / kThreads, int64_t(num_sms) * 64));
-        if (p.bf16)
-            gated_grad_kernel<true><<<grid, kThreads, 0, stream>>>(p, per_row, total);
-        else
-            gated_grad_kernel<false><<<grid, kThreads, 0, stream>>>(p, per_row, total);
-        return cudaGetLastError();
+        gated_grad_kernel<BF16, ACT><<<grid, kThreads, 0, stream>>>(p, per_row, total);
+        return;
     }
     unsigned x = 32;
     while (x < kThreads && x * 4 < p.n)
         x *= 2;
     const dim3 block(x, kThreads / x);
     const unsigned grid = static_cast<unsigned>(std::min<int64_t>((p.tokens + block.y - 1) / block.y, int64_t(num_sms) * 64));
+    gated_grad_any_kernel<BF16, ACT><<<grid, block, 0, stream>>>(p);
+}
+
+template <bool BF16>
+void by_act(const GradParams& p, int num_sms, cudaStream_t stream)
+{
+    switch (p.act) {
+    case kActSilu: return launch<BF16, kActSilu>(p, num_sms, stream);
+    case kActGelu: return launch<BF16, kActGelu>(p, num_sms, stream);
+    default: return launch<BF16, kActGeluTanh>(p, num_sms, stream);
+    }
+}
+
+}  // namespace
+
+cudaError_t gated_grad_launch(const GradParams& p, int num_sms, cudaStream_t stream)
+{
     if (p.bf16)
-        gated_grad_any_kernel<true><<<grid, block, 0, stream>>>(p);
+        by_act<true>(p, num_sms, stream);
     else
-        gated_grad_any_kernel<false><<<grid, block, 0, stream>>>(p);
+        by_act<false>(p, num_sms, stream);
     return cudaGetLastError();
 }
 
