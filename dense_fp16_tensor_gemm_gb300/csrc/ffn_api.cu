@@ -87,21 +87,25 @@ bool swap_ok(const FfnParams& p)
     return (p.scales || (p.gated && p.tokens <= kSwapTokens)) && maps_ok(p) && tiles <= INT32_MAX / 2;
 }
 
-// Whether the stream of the warp MMA is the faster of the two.  It starts 4 us sooner, but
-// its time grows with the tokens while the tensor cores' does not, so it has the smaller
-// weights.  Measured (us, stream and tcgen05), gated 16-bit: 1 token x 4096 x 8192 (134 MB)
-// 23.5 and 25.3; 8 tokens x 4096 x 4096 (67 MB) 17.0 and 17.6, x 8192 26.4 and 24.7; 16 tokens
-// x 2048 x 1024 (8 MB) 7.4 and 9.0, x 4096 x 2048 (34 MB) 15.9 and 12.9.  4-bit: 1 token x
-// 8192 x 16384 (67 MB) 22.0 and 29.4; 2 tokens x 4096 x 16384 (34 MB) 14.0 and 17.4; 4 tokens
-// 17.8 and 17.3; 8 tokens x 4096 x 8192 (17 MB) 13.6 and 13.3; 16 tokens x 2048 x 4096 (4 MB)
-// 7.9 and 9.1, x 4096 x 4096 (8 MB) 13.8 and 10.9.
+// Whether the stream of the warp MMA is the faster of the two.  It starts sooner, but its time
+// grows with the tokens while the tensor cores' does not, so it has one token, and of more the
+// smaller weights.  Measured (us, stream and tcgen05), tokens x hidden x inner, gated 16-bit: 1 x
+// 4096 x 8192 (134 MB) 23.8 and 24.9, x 32768 (537 MB) 78.9 and 87.3; 2 x 4096 x 4096 (67 MB) 16.1
+// and 17.3; 8 x 2048 x 4096 (34 MB) 11.1 and 11.4, x 4096 x 4096 16.9 and 16.7, x 8192 26.5 and
+// 24.9; 16 x 1024 x 2048 (8 MB) 5.9 and 7.2, x 2048 x 4096 (34 MB) 12.2 and 11.1.  4-bit, tokens x
+// K x N: 1 x 16384 x 8192 (67 MB) 27.2 and 29.8; 2 x 16384 x 4096 (34 MB) 18.9 and 19.1, x 8192
+// 30.9 and 29.9; 4 x 8192 x 4096 (17 MB) 12.8 and 13.2, x 16384 x 4096 23.0 and 18.9; 8 x 4096 x
+// 4096 (8 MB) 8.8 and 10.2, x 8192 x 4096 16.9 and 13.1; 16 x 2048 x 4096 (4 MB) 8.2 and 8.5, x
+// 4096 x 4096 13.7 and 9.9.
 bool few_first(const FfnParams& p)
 {
     const int64_t rows = p.gated ? 2 * int64_t(p.n) : p.n;
     const int64_t mb = rows * p.k * (p.scales ? 1 : 4) / 2 >> 20;
+    if (p.tokens == 1)
+        return true;
     if (p.scales)
-        return p.tokens == 1 || mb < (p.tokens == 2 ? 64 : p.tokens <= 4 ? 32 : p.tokens <= 8 ? 16 : 5);
-    return mb < (p.tokens == 1 ? 192 : p.tokens <= 8 ? 80 : 16);
+        return mb < (p.tokens == 2 ? 64 : p.tokens <= 4 ? 32 : p.tokens <= 8 ? 16 : 5);
+    return mb < (p.tokens <= 8 ? 80 : 16);
 }
 
 // Selects the kernel and launches the product.

@@ -21,8 +21,8 @@
 // over all groups; fewer tokens than the tensor cores need take ffn_few.cu, which has
 // none.
 //
-// 16-bit weights: bound by their bytes (64 tokens x 4096 x 8192 gated 27.6 us, x 2048 x 8192
-// 15.3, 6 TB/s between the two and 7 us that every call takes).  4-bit ones, up to 128
+// 16-bit weights: bound by their bytes (64 tokens x 4096 x 8192 gated 26.0 us, x 2048 x 8192
+// 15.0, 6 TB/s between the two and 4 us that every call takes).  4-bit ones, up to 128
 // tokens: by their conversion, 350 cycles for 128 x 64 of them where the bytes take 175 (64 x
 // 16384 x 8192 27.9 us, x 4096 x 4096 12.0; 25.4 without the conversion's arithmetic, 20.5 without
 // the scales either; half the tokens' loads change nothing, so pairs of CTAs would not
