@@ -233,6 +233,20 @@ def test_quantize(wt, st, group, zeros):
             assert (got[0][:, -1] >> 4 == 0).all()
     assert gnt.quantize_w4(w[:0])[0].shape == (0, 128) and gnt.quantize_w4(w[:, :0])[1].shape == (300, 0)
 
+@pytest.mark.parametrize("zeros", [False, True])
+@pytest.mark.parametrize("wt", [torch.float32, BF16, F16])
+@pytest.mark.parametrize("pitch,offset", [(1000, 0), (1004, 0), (1004, 4), (1002, 0), (1002, 2), (1001, 0), (1000, 1), (1008, 12)])
+def test_quantize_alignments(pitch, offset, wt, zeros):
+    """Rows on boundaries of 16, 8, 4 and 2 bytes, and columns that end inside a thread's 32."""
+    for cols in (32, 96, 999, 1000):
+        w = normal(gen(cols + pitch), 37, cols, dtype=wt, pitch=pitch, offset=offset)
+        out = gnt.quantize_w4(w, 64, zeros, BF16)
+        ref = quantize_ref(w, 64, zeros, BF16)
+        assert torch.equal(unpack(out[0], cols).cpu(), ref[0]) and torch.equal(out[1].cpu(), ref[1])
+        assert not zeros or torch.equal(out[2].cpu(), ref[2])
+    gnt.gemm_nt_check()
+
+
 
 def test_quantize_of_infinities():
     w = torch.ones(4, 128, device="cuda")
