@@ -135,15 +135,17 @@ bool output(PyObject* o, int64_t rows, int64_t cols, const at::Tensor& like, int
 }
 PyObject* given_or(PyObject* o, const Matrix& m) { return o != Py_None ? Py_NewRef(o) : THPVariable_Wrap(m.t); }
 
-// Calls without the interpreter's lock, as ctypes does.
+// Calls without the interpreter's lock, as ctypes does; a call that throws (an operand's
+// copy that finds no memory) takes the lock again on its way out.
+struct Unlock {
+    PyThreadState* state = PyEval_SaveThread();
+    ~Unlock() { PyEval_RestoreThread(state); }
+};
 template <typename F>
 gemm_status_t unlocked(F&& call)
 {
-    gemm_status_t st;
-    Py_BEGIN_ALLOW_THREADS
-    st = call();
-    Py_END_ALLOW_THREADS
-    return st;
+    const Unlock hold;
+    return call();
 }
 
 // gated(X, W13, act, keep, out, path)

@@ -115,3 +115,21 @@ def test_refusals(both):
                          (dict(Z=s), TypeError), (dict(group=64), ValueError), (dict(out=rand(4, 63)), ValueError),
                          (dict(path=P.TC05_PAIR), gnt.GemmError), (dict(path=-1), gnt.GemmError), (dict(Q=q.cpu()), ValueError)):
         refused(both(gnt.linear_w4, **{**dict(X=x, Q=q, S=s), **change}), kind)
+
+
+def test_an_operand_copy_without_memory_is_an_exception(both):
+    """The copy onto 16-byte boundaries is allocated inside the call: an allocator that refuses
+    it raises, from the extension as from Python, and the next call works."""
+    torch.cuda.empty_cache()
+    x, w = rand(2, 4095), torch.zeros(32768, 4095, dtype=BF16, device="cuda")   # a copy of 268 MB
+    gnt.gated_linear(x, w[:8])
+    dh, gu = rand(2, 16384), rand(2, 32768)
+    torch.cuda.empty_cache()
+    total = torch.cuda.get_device_properties(0).total_memory
+    try:
+        torch.cuda.set_per_process_memory_fraction((torch.cuda.memory_reserved() + (128 << 20)) / total)
+        refused_by = [type(v) for v in both(gnt.gated_linear, x, w) + both(gnt.gated_linear_backward, dh, gu, x, w)]
+    finally:
+        torch.cuda.set_per_process_memory_fraction(1.0)
+    assert refused_by == [torch.cuda.OutOfMemoryError] * 4
+    same(both(gnt.gated_linear, x, w))
