@@ -10,6 +10,7 @@ fails, an exception is raised.
 import ctypes
 import enum
 import os
+import re
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "_build", "libgemm_nt.so")
@@ -499,6 +500,8 @@ def _bind_calls():
         module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_tensor_calls", loader))
         loader.exec_module(module)
     except ImportError:
+        return
+    if tuple(int(n) for n in re.findall(r"\d+", _torch.__version__)[:3]) != module.torch_release:
         return
     lib = load()
     module.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (

@@ -21,6 +21,7 @@
 #include <torch/csrc/Dtype.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
+#include <torch/version.h>
 
 #include "gemm_nt.h"
 
@@ -349,4 +350,13 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_tensor_calls", nullptr, -1, metho
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__tensor_calls() { return PyModule_Create(&module); }
+PyMODINIT_FUNC PyInit__tensor_calls()
+{
+    PyObject* m = PyModule_Create(&module);
+    // a tensor's layout in memory is this release's: the Python side binds under no other
+    PyObject* v = m ? Py_BuildValue("(iii)", TORCH_VERSION_MAJOR, TORCH_VERSION_MINOR, TORCH_VERSION_PATCH) : nullptr;
+    if (m && (!v || PyModule_AddObjectRef(m, "torch_release", v) < 0))
+        Py_CLEAR(m);
+    Py_XDECREF(v);
+    return m;
+}

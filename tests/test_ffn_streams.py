@@ -122,3 +122,19 @@ def test_an_extension_that_does_not_load_leaves_the_python_forms(monkeypatch):
     monkeypatch.setattr(gnt, "_calls", None)
     gnt._bind_calls()
     assert gnt._calls is None and gnt.load() is lib
+
+
+def test_an_extension_of_another_torch_stays_unbound(monkeypatch):
+    """Where it has been built: under its own release it is bound, under another one not."""
+    from dense_fp16_tensor_gemm_gb300 import _build
+    if _build._calls_command("") is None:
+        pytest.skip("no extension here")
+    _build.build()
+    gnt.load()
+    torch = gnt._init_torch()
+    release = torch.__version__
+    for version, bound in ((release, True), ("2.0.1+cu118", False), (release, True)):
+        monkeypatch.setattr(gnt, "_calls", None)
+        monkeypatch.setattr(torch, "__version__", version)
+        gnt._bind_calls()
+        assert (gnt._calls is not None) == bound
