@@ -842,6 +842,20 @@ def _on_grid(t, at, ld):
     return at % 16 == 0 and (ld % 8 == 0 or t.shape[0] < 2)
 
 
+def _span(t, ld):
+    """The bytes [from, to) that a matrix of that pitch touches, pitches counted."""
+    (rows, width), at = t.shape, t.data_ptr()
+    return (at, at + ((rows - 1) * ld + width) * t.element_size()) if rows and width else (0, 0)
+
+
+def _refuse_overlap(out, ldo, t, ld):
+    """The library looks whether an output overlaps what it reads; of an operand that is
+    copied onto the grid first that is the copy, so the operand itself is looked at here."""
+    (lo, hi), (olo, ohi) = _span(t, ld), _span(out, ldo)
+    if lo < ohi and olo < hi:
+        raise GemmError(Status.OVERLAP)
+
+
 def _to_grid(t, ld, index):
     """A copy of a matrix of 16-bit elements with its rows on 16-byte boundaries; its pitch."""
     rows, width = t.shape
@@ -878,15 +892,20 @@ def gated_linear(X, W13, activation="silu", keep=False, out=None, path=Path.AUTO
     inner = wsh[0] // 2
     ldx, ldw = _pitch(xsh, X.stride(), "X"), _pitch(wsh, W13.stride(), "W13")
     index = _same_device(X, W13, out)
-    if path == 0:
-        if not _on_grid(W13, W13.data_ptr(), ldw):
-            W13, ldw = _to_grid(W13, ldw, index)
-        if tokens > 16 and not _on_grid(X, X.data_ptr(), ldx):
-            X, ldx = _to_grid(X, ldx, index)
     if out is None:
         out, ldh = _rows(tokens, inner, X), (inner + 7) // 8 * 8
     else:
         ldh = _given(out, tokens, inner, X)
+    if path == 0:
+        copy_w = not _on_grid(W13, W13.data_ptr(), ldw)
+        copy_x = tokens > 16 and not _on_grid(X, X.data_ptr(), ldx)
+        if copy_w:
+            _refuse_overlap(out, ldh, W13, ldw)
+        if copy_x:
+            _refuse_overlap(out, ldh, X, ldx)
+            X, ldx = _to_grid(X, ldx, index)
+        if copy_w:
+            W13, ldw = _to_grid(W13, ldw, index)
     gu = _rows(tokens, 2 * inner, X) if keep else None
     status = (_lib or load()).gemm_nt_gated(X.data_ptr(), ldx, W13.data_ptr(), ldw, out.data_ptr(), ldh,
                                             gu.data_ptr() if keep else None, (inner + 3) // 4 * 8, code, act, tokens,
@@ -1006,8 +1025,6 @@ def _w4_product(X, Q, S, Z, group, act, out, path):
         raise ValueError("Q13 must have 2*inner rows")
     ldx = _pitch(xsh, X.stride(), "X")
     index = _same_device(X, Q, S, Z, out)
-    if path == 0 and tokens > 16 and not _on_grid(X, X.data_ptr(), ldx):
-        X, ldx = _to_grid(X, ldx, index)
     weights = Weights4(Q.data_ptr(), _pitch(qsh, Q.stride(), "Q"), S.data_ptr(), _pitch(ssh, S.stride(), "S"),
                        None if Z is None else Z.data_ptr(), 0 if Z is None else _pitch(ssh, Z.stride(), "Z"), group)
     n = rows if act is None else rows // 2
@@ -1016,6 +1033,9 @@ def _w4_product(X, Q, S, Z, group, act, out, path):
         out = torch.empty_strided((tokens, n), (ldo, 1), dtype=dtype, device=X.device)
     else:
         ldo = _given(out, tokens, n, X)
+    if path == 0 and tokens > 16 and not _on_grid(X, X.data_ptr(), ldx):
+        _refuse_overlap(out, ldo, X, ldx)
+        X, ldx = _to_grid(X, ldx, index)
     lib = _lib or load()
     if act is None:
         status = lib.gemm_nt_w4(X.data_ptr(), ldx, weights, out.data_ptr(), ldo, code, tokens, n, cols, path,

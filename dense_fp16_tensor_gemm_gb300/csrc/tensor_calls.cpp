@@ -42,6 +42,11 @@ struct Matrix {
     void* at = nullptr;
     // rows of 16-bit elements that start on 16-byte boundaries
     bool on_grid() const { return reinterpret_cast<uintptr_t>(at) % 16 == 0 && (ld % 8 == 0 || rows < 2); }
+    uintptr_t begin() const { return reinterpret_cast<uintptr_t>(at); }
+    // of the bytes that the matrix touches, pitches counted
+    uintptr_t end() const { return begin() + static_cast<uintptr_t>(((rows - 1) * ld + cols) * t.element_size()); }
+    bool empty() const { return rows == 0 || cols == 0; }
+    bool overlaps(const Matrix& o) const { return !empty() && !o.empty() && begin() < o.end() && o.begin() < end(); }
 };
 
 // Whether o is a matrix on the device `index` (taken from it if negative) with rows of
@@ -130,6 +135,8 @@ bool output(PyObject* o, int64_t rows, int64_t cols, const at::Tensor& like, int
     if (o != Py_None)
         return matrix(o, index, m) && m.rows == rows && m.cols == cols && m.t.scalar_type() == like.scalar_type();
     m.t = rows_of(rows, cols, like);
+    m.rows = rows;
+    m.cols = cols;
     m.ld = pitch(cols, 8);
     m.at = m.t.data_ptr();
     return true;
@@ -169,10 +176,14 @@ PyObject* gated(PyObject*, PyObject* const* a, Py_ssize_t n)
         gu.at = gu.t.data_ptr();
         gu.ld = pitch(2 * inner, 8);
     }
+    // (the library would see whether the output overlaps the copies, not the operands)
+    const bool copy_w = path == 0 && !w.on_grid(), copy_x = path == 0 && x.rows > 16 && !x.on_grid();
+    if ((copy_w && h.overlaps(w)) || (copy_x && h.overlaps(x)))
+        return PyLong_FromLong(GEMM_ERR_OVERLAP);
     const gemm_stream_t stream = stream_of(index);
     const gemm_status_t st = unlocked([&] {
-        gemm_status_t s = path == 0 ? to_grid(w, stream) : GEMM_OK;
-        if (s == GEMM_OK && path == 0 && x.rows > 16)
+        gemm_status_t s = copy_w ? to_grid(w, stream) : GEMM_OK;
+        if (s == GEMM_OK && copy_x)
             s = to_grid(x, stream);
         if (s != GEMM_OK)
             return s;
@@ -302,9 +313,12 @@ PyObject* w4(PyObject*, PyObject* const* a, Py_ssize_t n)
                          static_cast<int32_t>(group)};
     const gemm_dtype_t t = code(x.t.scalar_type());
     const gemm_path_t way = static_cast<gemm_path_t>(path);
+    const bool copy_x = path == 0 && x.rows > 16 && !x.on_grid();
+    if (copy_x && out.overlaps(x))  // (the library would see the copy)
+        return PyLong_FromLong(GEMM_ERR_OVERLAP);
     const gemm_stream_t stream = stream_of(index);
     const gemm_status_t st = unlocked([&] {
-        const gemm_status_t s = path == 0 && x.rows > 16 ? to_grid(x, stream) : GEMM_OK;
+        const gemm_status_t s = copy_x ? to_grid(x, stream) : GEMM_OK;
         if (s != GEMM_OK)
             return s;
         return is_gated ? p_w4_gated(x.at, x.ld, &w, out.at, out.ld, t, static_cast<gemm_act_t>(act), x.rows, x.cols, width,
