@@ -842,6 +842,13 @@ def _on_grid(t, at, ld):
     return at % 16 == 0 and (ld % 8 == 0 or t.shape[0] < 2)
 
 
+def _stream_takes(tokens, cols, step):
+    """Whether the kernel that streams the weights takes that many tokens (GEMM_PATH_SKINNY
+    in include/gemm_nt.h), their rows in steps of 64, or of 256 with 4-bit weights.  It reads
+    them off the grid, and is then faster than a copy and another kernel."""
+    return tokens <= 16 and tokens * ((cols + step - 1) // step * step) <= 65536
+
+
 def _span(t, ld):
     """The bytes [from, to) that a matrix of that pitch touches, pitches counted."""
     (rows, width), at = t.shape, t.data_ptr()
@@ -898,7 +905,7 @@ def gated_linear(X, W13, activation="silu", keep=False, out=None, path=Path.AUTO
         ldh = _given(out, tokens, inner, X)
     if path == 0:
         copy_w = not _on_grid(W13, W13.data_ptr(), ldw)
-        copy_x = tokens > 16 and not _on_grid(X, X.data_ptr(), ldx)
+        copy_x = not _on_grid(X, X.data_ptr(), ldx) and not _stream_takes(tokens, hidden, 64)
         if copy_w:
             _refuse_overlap(out, ldh, W13, ldw)
         if copy_x:
@@ -1033,7 +1040,7 @@ def _w4_product(X, Q, S, Z, group, act, out, path):
         out = torch.empty_strided((tokens, n), (ldo, 1), dtype=dtype, device=X.device)
     else:
         ldo = _given(out, tokens, n, X)
-    if path == 0 and tokens > 16 and not _on_grid(X, X.data_ptr(), ldx):
+    if path == 0 and not _on_grid(X, X.data_ptr(), ldx) and not _stream_takes(tokens, cols, 256):
         _refuse_overlap(out, ldo, X, ldx)
         X, ldx = _to_grid(X, ldx, index)
     lib = _lib or load()

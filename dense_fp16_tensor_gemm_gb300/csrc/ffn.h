@@ -5,6 +5,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include "few_tokens.h"
 #include "internal.h"
 
 namespace gnt {
@@ -81,10 +82,9 @@ cudaError_t ffn_any_launch(const FfnParams& p, int num_sms, cudaStream_t stream)
 cudaError_t gated_pair_configure(int* max_pairs);  // one-time per device
 cudaError_t gated_pair_launch(const FfnParams& p, int max_pairs, cudaStream_t stream);
 
-// Up to 16 tokens, on the warp MMA; rows of the weights on the 16-byte grid.
-constexpr int kFewTokens = 16;
+// Up to 16 tokens that fit (few_tokens_fit), on the warp MMA; rows of the weights on the
+// 16-byte grid.
 cudaError_t ffn_few_configure();  // one-time per device
-bool ffn_few_fits(const FfnParams& p);  // tokens up to kFewTokens, and no more than shared memory takes
 cudaError_t ffn_few_launch(const FfnParams& p, int num_sms, cudaStream_t stream);
 
 // The weights as the MMA's rows; X and W on the 16-byte grid.  16-bit weights: up to

@@ -77,7 +77,8 @@ bool pair_ok(const FfnParams& p, const DeviceInfo& d)
 // The warp MMA's kernel, which streams the weights for up to 16 tokens.
 bool few_ok(const FfnParams& p)
 {
-    return p.k > 0 && p.k <= (1 << 29) && ffn_few_fits(p) && aligned(p.w, 16) && p.ldw * (p.scales ? 1 : 2) % 16 == 0;
+    return p.k > 0 && few_tokens_fit(p.tokens, p.k, p.scales != nullptr) && aligned(p.w, 16) &&
+           p.ldw * (p.scales ? 1 : 2) % 16 == 0;
 }
 
 // tcgen05 with the weights as rows, on single CTAs.

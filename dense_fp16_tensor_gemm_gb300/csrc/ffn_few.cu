@@ -131,12 +131,7 @@ __device__ __forceinline__ uint4 load_x(const uint16_t* row, int k, int K, bool 
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// Bytes of the tokens in shared memory.
-int64_t x_bytes(const FfnParams& p)
-{
-    const int step = p.scales ? 256 : 64;
-    return (int64_t(p.k) + step - 1) / step * step * 2 * p.tokens;
-}
+int64_t x_bytes(const FfnParams& p) { return few_token_bytes(p.tokens, p.k, p.scales != nullptr); }
 constexpr int kMaxSmem = 227 * 1024;
 
 // What the tokens' memory leaves: CTAs of 8 warps, three or two to an SM, or one of 16.
@@ -527,11 +522,6 @@ cudaError_t by_kind(const FfnParams& p, int num_sms, cudaStream_t stream, bool c
 }
 
 }  // namespace
-
-bool ffn_few_fits(const FfnParams& p)
-{
-    return p.tokens <= kFewTokens && x_bytes(p) <= 128 * 1024;
-}
 
 cudaError_t ffn_few_configure()
 {

@@ -23,6 +23,7 @@
 #include <torch/csrc/autograd/python_variable.h>
 #include <torch/version.h>
 
+#include "few_tokens.h"
 #include "gemm_nt.h"
 
 namespace {
@@ -129,6 +130,13 @@ gemm_status_t to_grid(Matrix& m, gemm_stream_t stream)
     return st;
 }
 
+// Whether tokens are to be copied: off 16-byte boundaries, where the stream of the weights,
+// which reads them anywhere, does not take them.  (Where it takes them it is faster than a
+// copy and the kernels that need one: 16 tokens x 2047 x 4096 gated 11.9 us and 15.7, x 4095 x 4096
+// in 4 bits 13.7 and 16.4; the any-layout kernel, which is what is left for the others, takes
+// 226 for 16 x 4097 x 8192 gated and 31 is the copied form's.)
+bool copied(const Matrix& x, bool codes) { return !x.on_grid() && !gnt::few_tokens_fit(x.rows, x.cols, codes); }
+
 // The caller's own output, or a new one.
 bool output(PyObject* o, int64_t rows, int64_t cols, const at::Tensor& like, int index, Matrix& m)
 {
@@ -177,7 +185,7 @@ PyObject* gated(PyObject*, PyObject* const* a, Py_ssize_t n)
         gu.ld = pitch(2 * inner, 8);
     }
     // (the library would see whether the output overlaps the copies, not the operands)
-    const bool copy_w = path == 0 && !w.on_grid(), copy_x = path == 0 && x.rows > 16 && !x.on_grid();
+    const bool copy_w = path == 0 && !w.on_grid(), copy_x = path == 0 && copied(x, false);
     if ((copy_w && h.overlaps(w)) || (copy_x && h.overlaps(x)))
         return PyLong_FromLong(GEMM_ERR_OVERLAP);
     const gemm_stream_t stream = stream_of(index);
@@ -313,7 +321,7 @@ PyObject* w4(PyObject*, PyObject* const* a, Py_ssize_t n)
                          static_cast<int32_t>(group)};
     const gemm_dtype_t t = code(x.t.scalar_type());
     const gemm_path_t way = static_cast<gemm_path_t>(path);
-    const bool copy_x = path == 0 && x.rows > 16 && !x.on_grid();
+    const bool copy_x = path == 0 && copied(x, true);
     if (copy_x && out.overlaps(x))  // (the library would see the copy)
         return PyLong_FromLong(GEMM_ERR_OVERLAP);
     const gemm_stream_t stream = stream_of(index);
