@@ -838,8 +838,8 @@ def _given(out, n, width, like):
 
 
 def _on_grid(t, at, ld):
-    """Whether rows of 16-bit elements at that address and pitch start on 16-byte boundaries."""
-    return at % 16 == 0 and (ld % 8 == 0 or t.shape[0] < 2)
+    """Whether a matrix's rows at that address and pitch start on 16-byte boundaries."""
+    return at % 16 == 0 and (ld * t.element_size() % 16 == 0 or t.shape[0] < 2)
 
 
 def _stream_takes(tokens, cols, step):
@@ -864,10 +864,11 @@ def _refuse_overlap(out, ldo, t, ld):
 
 
 def _to_grid(t, ld, index):
-    """A copy of a matrix of 16-bit elements with its rows on 16-byte boundaries; its pitch."""
-    rows, width = t.shape
-    copy, pitch = _rows(rows, width, t), (width + 7) // 8 * 8
-    gemm_nt_copy_rows(t.data_ptr(), 2 * ld, copy.data_ptr(), 2 * pitch, rows, 2 * width, _stream_of(index))
+    """A copy of a matrix with its rows on 16-byte boundaries; its pitch."""
+    (rows, width), size = t.shape, t.element_size()
+    pitch = (width * size + 15) // 16 * 16 // size
+    copy = _torch.empty_strided((rows, width), (pitch, 1), dtype=t.dtype, device=t.device)
+    gemm_nt_copy_rows(t.data_ptr(), size * ld, copy.data_ptr(), size * pitch, rows, size * width, _stream_of(index))
     return copy, pitch
 
 
@@ -1032,17 +1033,25 @@ def _w4_product(X, Q, S, Z, group, act, out, path):
         raise ValueError("Q13 must have 2*inner rows")
     ldx = _pitch(xsh, X.stride(), "X")
     index = _same_device(X, Q, S, Z, out)
-    weights = Weights4(Q.data_ptr(), _pitch(qsh, Q.stride(), "Q"), S.data_ptr(), _pitch(ssh, S.stride(), "S"),
-                       None if Z is None else Z.data_ptr(), 0 if Z is None else _pitch(ssh, Z.stride(), "Z"), group)
+    ldq, lds = _pitch(qsh, Q.stride(), "Q"), _pitch(ssh, S.stride(), "S")
+    ldz = 0 if Z is None else _pitch(ssh, Z.stride(), "Z")
     n = rows if act is None else rows // 2
     if out is None:
         ldo = (n + 7) // 8 * 8
         out = torch.empty_strided((tokens, n), (ldo, 1), dtype=dtype, device=X.device)
     else:
         ldo = _given(out, tokens, n, X)
-    if path == 0 and not _on_grid(X, X.data_ptr(), ldx) and not _stream_takes(tokens, cols, 256):
-        _refuse_overlap(out, ldo, X, ldx)
-        X, ldx = _to_grid(X, ldx, index)
+    if path == 0:
+        copy_q = not _on_grid(Q, Q.data_ptr(), ldq)
+        copy_x = not _on_grid(X, X.data_ptr(), ldx) and not _stream_takes(tokens, cols, 256)
+        if copy_q:
+            _refuse_overlap(out, ldo, Q, ldq)
+        if copy_x:
+            _refuse_overlap(out, ldo, X, ldx)
+            X, ldx = _to_grid(X, ldx, index)
+        if copy_q:
+            Q, ldq = _to_grid(Q, ldq, index)
+    weights = Weights4(Q.data_ptr(), ldq, S.data_ptr(), lds, None if Z is None else Z.data_ptr(), ldz, group)
     lib = _lib or load()
     if act is None:
         status = lib.gemm_nt_w4(X.data_ptr(), ldx, weights, out.data_ptr(), ldo, code, tokens, n, cols, path,
@@ -1060,7 +1069,9 @@ def linear_w4(X, Q, S, Z=None, group=128, out=None, path=Path.AUTO, stream=None)
     float16 or bfloat16, Q, S and Z of W (out, in), S in X's type.  Sums are
     float32 (for more than a few tokens of weights rounded to X's type: see gemm_nt_w4 in
     include/gemm_nt.h); Y (tokens, out) has X's type, its rows start on 16-byte
-    boundaries."""
+    boundaries.  Rows of Q that do not (a contiguous Q whose width is no multiple of 16) are
+    copied there by every call, unless a ``path`` is given: keep the Q that the quantiser
+    returns, whose rows do."""
     if stream is not None:
         side = _elsewhere(stream)
         if side is not None:

@@ -121,6 +121,8 @@ gemm_status_t run(FfnParams& p, gemm_path_t path, cudaStream_t stream)
     p.fault = d.fault;
     if (p.tokens == 1)
         p.ldx = (int64_t(p.k) + 7) / 8 * 8;  // a single row's pitch is never stepped by
+    if (p.n == 1 && !p.gated)
+        p.ldw = ((int64_t(p.k) + 1) / 2 + 15) / 16 * 16;  // (plain: codes)
     const bool few = few_ok(p), swap = swap_ok(p), pair = pair_ok(p, d);
     if (path == GEMM_PATH_AUTO) {
         if (few && (!swap || few_first(p)))

@@ -41,8 +41,8 @@ struct Matrix {
     at::Tensor t;
     int64_t rows = 0, cols = 0, ld = 0;
     void* at = nullptr;
-    // rows of 16-bit elements that start on 16-byte boundaries
-    bool on_grid() const { return reinterpret_cast<uintptr_t>(at) % 16 == 0 && (ld % 8 == 0 || rows < 2); }
+    // rows that start on 16-byte boundaries
+    bool on_grid() const { return begin() % 16 == 0 && (ld * t.element_size() % 16 == 0 || rows < 2); }
     uintptr_t begin() const { return reinterpret_cast<uintptr_t>(at); }
     // of the bytes that the matrix touches, pitches counted
     uintptr_t end() const { return begin() + static_cast<uintptr_t>(((rows - 1) * ld + cols) * t.element_size()); }
@@ -116,14 +116,14 @@ gemm_stream_t stream_of(int index)
     return reinterpret_cast<gemm_stream_t>(c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(index)).stream());
 }
 
-// Copies a matrix of 16-bit elements onto 16-byte boundaries, if it lies off them.
+// Copies a matrix onto 16-byte boundaries, if it lies off them.
 gemm_status_t to_grid(Matrix& m, gemm_stream_t stream)
 {
     if (m.on_grid())
         return GEMM_OK;
-    const at::Tensor copy = rows_of(m.rows, m.cols, m.t);
-    const int64_t ld = pitch(m.cols, 8);
-    const gemm_status_t st = p_copy(m.at, 2 * m.ld, copy.data_ptr(), 2 * ld, m.rows, 2 * m.cols, stream);
+    const int64_t size = m.t.element_size(), ld = pitch(m.cols, 16 / size);
+    const at::Tensor copy = rows_of(m.rows, m.cols, ld, m.t, m.t.scalar_type());
+    const gemm_status_t st = p_copy(m.at, size * m.ld, copy.data_ptr(), size * ld, m.rows, size * m.cols, stream);
     m.t = copy;
     m.ld = ld;
     m.at = copy.data_ptr();
@@ -317,18 +317,21 @@ PyObject* w4(PyObject*, PyObject* const* a, Py_ssize_t n)
     const int64_t width = is_gated ? q.rows / 2 : q.rows;
     if (!output(a[6], x.rows, width, x.t, index, out))
         Py_RETURN_NONE;
-    const gemm_w4_t w = {static_cast<const uint8_t*>(q.at), q.ld, s.at, s.ld, static_cast<const uint8_t*>(z.at), z.ld,
-                         static_cast<int32_t>(group)};
     const gemm_dtype_t t = code(x.t.scalar_type());
     const gemm_path_t way = static_cast<gemm_path_t>(path);
-    const bool copy_x = path == 0 && copied(x, true);
-    if (copy_x && out.overlaps(x))  // (the library would see the copy)
+    // (as in `gated`)
+    const bool copy_q = path == 0 && !q.on_grid(), copy_x = path == 0 && copied(x, true);
+    if ((copy_q && out.overlaps(q)) || (copy_x && out.overlaps(x)))
         return PyLong_FromLong(GEMM_ERR_OVERLAP);
     const gemm_stream_t stream = stream_of(index);
     const gemm_status_t st = unlocked([&] {
-        const gemm_status_t s = copy_x ? to_grid(x, stream) : GEMM_OK;
-        if (s != GEMM_OK)
-            return s;
+        gemm_status_t status = copy_q ? to_grid(q, stream) : GEMM_OK;
+        if (status == GEMM_OK && copy_x)
+            status = to_grid(x, stream);
+        if (status != GEMM_OK)
+            return status;
+        const gemm_w4_t w = {static_cast<const uint8_t*>(q.at), q.ld, s.at, s.ld, static_cast<const uint8_t*>(z.at), z.ld,
+                             static_cast<int32_t>(group)};
         return is_gated ? p_w4_gated(x.at, x.ld, &w, out.at, out.ld, t, static_cast<gemm_act_t>(act), x.rows, x.cols, width,
                                      way, stream)
                         : p_w4(x.at, x.ld, &w, out.at, out.ld, t, x.rows, width, x.cols, way, stream);

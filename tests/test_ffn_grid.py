@@ -110,3 +110,70 @@ def test_calls_off_the_grid_take_the_kernels_of_those_on_it(forms, tokens, cols,
             with pytest.raises(gnt.GemmError):
                 call()
     gnt.gemm_nt_check()
+
+
+# columns of 4-bit weights, bytes between the rows' starts, of what the storage starts with
+CODES = [(1000, 500, 0), (1000, 512, 1), (999, 500, 16), (4100, 2050, 0), (256, 130, 2)]
+
+
+def codes_off(cols, pitch, offset, rows, device):
+    width = (cols + 1) // 2
+    store = torch.zeros(offset + rows * pitch + 16, dtype=torch.uint8, device=device)
+    return store[offset:offset + rows * pitch].view(rows, pitch)[:, :width]
+
+
+@pytest.mark.parametrize("cols,pitch,offset", CODES)
+def test_codes_off_the_grid_are_copied(fake, monkeypatch, cols, pitch, offset):  # noqa: F811
+    for tokens, rows in ((1, 6), (40, 6)):
+        x = torch.zeros(tokens, (cols + 7) // 8 * 8, dtype=BF16)[:, :cols]
+        q, s = codes_off(cols, pitch, offset, rows, "cpu"), torch.zeros(rows, (cols + 127) // 128, dtype=BF16)
+        for call in (gnt.linear_w4, gnt.gated_linear_w4):
+            for path, copies in ((P.AUTO, [(rows, (cols + 1) // 2)]), (P.MMASYNC, [])):
+                lib = Library()
+                monkeypatch.setattr(gnt, "_lib", lib)
+                call(x, q, s, path=path)
+                assert lib.copied == copies
+    # an output that lies on them is refused before that, whatever the library sees
+    lib = Library()
+    monkeypatch.setattr(gnt, "_lib", lib)
+    monkeypatch.setattr(gnt, "error_string", lambda status: "overlap")
+    store = torch.zeros(4096, dtype=torch.uint8)
+    q, out = store[1:1 + 6 * 500].view(6, 500), store[3000:3012].view(BF16).view(1, 6)
+    for at, refused in ((out, True), (store[3002:3014].view(BF16).view(1, 6), False)):
+        x, s = torch.zeros(1, 1000, dtype=BF16), torch.zeros(6, 8, dtype=BF16)
+        if refused:
+            with pytest.raises(gnt.GemmError) as e:
+                gnt.linear_w4(x, q, s, out=at)
+            assert e.value.status == gnt.Status.OVERLAP and not lib.copied
+        else:
+            assert gnt.linear_w4(x, q, s, out=at) is at
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("cols,pitch,offset", CODES)
+def test_codes_off_the_grid_take_the_kernels_of_those_on_it(forms, cols, pitch, offset):
+    g = torch.Generator("cuda").manual_seed(cols + pitch)
+    for tokens in (1, 7, 40, 200):
+        x = on_grid(normal(g, tokens, cols))
+        for zeros in (False, True):
+            q, s, *z = gnt.quantize_w4(normal(g, 320, cols) / 32, 64, zeros)
+            off = codes_off(cols, pitch, offset, 320, "cuda")
+            off.copy_(q)
+            for call in (gnt.linear_w4, gnt.gated_linear_w4):
+                want = call(x, q, s, *z, group=64)
+                for out in forms(lambda: call(x, off, s, *z, group=64)):
+                    assert torch.equal(out, want)
+    gnt.gemm_nt_check()
+
+
+@pytest.mark.gpu
+def test_a_single_row_of_codes_takes_the_same_kernels(forms):
+    """Its pitch is never stepped by, so any will do."""
+    g = torch.Generator("cuda").manual_seed(1)
+    for tokens in (1, 40):
+        for cols in (1001, 1000):
+            x = on_grid(normal(g, tokens, cols))
+            q, s = gnt.quantize_w4(normal(g, 1, cols) / 32)
+            for out in forms(lambda: gnt.linear_w4(x, q, s)):
+                assert torch.equal(out, gnt.linear_w4(x, q, s, path=P.SKINNY if tokens == 1 else P.TC05))
+    gnt.gemm_nt_check()
