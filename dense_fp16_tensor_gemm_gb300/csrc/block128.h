@@ -83,7 +83,7 @@ struct BlkParams {
 struct DeviceInfo {
     int num_sms;
     int block_pairs;  // CTA pairs of block128_pair resident at once
-    int gated_pairs;  // and of gated_pair
+    int device;       // its index, below 64
     uint32_t* status;
     unsigned long long wait_limit;
     int fault;

@@ -1,6 +1,7 @@
 // ffn.h -- declarations shared by the gated feed-forward product, its backward
 // pass and the products with 4-bit weights.  Not part of the public ABI.
 #pragma once
+#include <atomic>
 #include <cstdint>
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -75,17 +76,38 @@ struct FfnParams {
     int fault;
 };
 
+// A kernel's limit of dynamic shared memory, set by its first launch on a device.  (The 93
+// kernels here and their device memory, 6 MB, are not brought in by the first product of a
+// program that launches none of them: 19.8 ms of host time where they were, 13.4 without.)
+class SmemLimit {
+public:
+    template <typename K>
+    cudaError_t allow(K* kernel, int bytes, int device)
+    {
+        const uint64_t bit = uint64_t(1) << device;
+        if (done_.load(std::memory_order_acquire) & bit)
+            return cudaSuccess;
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        if (e == cudaSuccess)
+            done_.fetch_or(bit, std::memory_order_release);
+        return e;
+    }
+
+private:
+    std::atomic<uint64_t> done_{0};  // a bit per device
+};
+
+// Launches take the current device's index and SMs.
 // Any layout, on the warp MMA.
 cudaError_t ffn_any_launch(const FfnParams& p, int num_sms, cudaStream_t stream);
 
 // The gated product with 16-bit weights on CTA pairs; X and W on the 16-byte grid.
-cudaError_t gated_pair_configure(int* max_pairs);  // one-time per device
-cudaError_t gated_pair_launch(const FfnParams& p, int max_pairs, cudaStream_t stream);
+cudaError_t gated_pairs(int act, int device, int* pairs);  // pairs that can be resident at once
+cudaError_t gated_pair_launch(const FfnParams& p, int pairs, cudaStream_t stream);
 
 // Up to 16 tokens that fit (few_tokens_fit), on the warp MMA; rows of the weights on the
 // 16-byte grid.
-cudaError_t ffn_few_configure();  // one-time per device
-cudaError_t ffn_few_launch(const FfnParams& p, int num_sms, cudaStream_t stream);
+cudaError_t ffn_few_launch(const FfnParams& p, int device, int num_sms, cudaStream_t stream);
 
 // The weights as the MMA's rows; X and W on the 16-byte grid.  16-bit weights: up to
 // kSwapTokens tokens.
@@ -96,8 +118,7 @@ constexpr int kSwapTokens = 64;
 bool call_map(CUtensorMap* map, const void* base, int64_t rows, int64_t K, int64_t ld, int64_t batch, int64_t stride,
               int box_rows, int dtype);
 bool interleaved_map(CUtensorMap* map, const void* base, int64_t n, int64_t K, int64_t ld, int dtype);
-cudaError_t ffn_swap_configure();  // one-time per device
-cudaError_t ffn_swap_launch(const FfnParams& p, int num_sms, cudaStream_t stream);
+cudaError_t ffn_swap_launch(const FfnParams& p, int device, int num_sms, cudaStream_t stream);
 
 // dGU = [dh u act'(g), dh act(g)]
 struct GradParams {

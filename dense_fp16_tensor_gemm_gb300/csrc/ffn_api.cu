@@ -68,10 +68,10 @@ bool maps_ok(const FfnParams& p)
            p.ldx < lim && p.ldw < lim / p.n;
 }
 
-bool pair_ok(const FfnParams& p, const DeviceInfo& d)
+bool pair_ok(const FfnParams& p)
 {
     const int64_t tiles = ((int64_t(p.tokens) + 255) / 256) * ((int64_t(p.n) + 127) / 128);
-    return p.gated && !p.scales && maps_ok(p) && d.gated_pairs > 0 && tiles <= INT32_MAX / 2;
+    return p.gated && !p.scales && maps_ok(p) && tiles <= INT32_MAX / 2;
 }
 
 // The warp MMA's kernel, which streams the weights for up to 16 tokens.
@@ -123,19 +123,24 @@ gemm_status_t run(FfnParams& p, gemm_path_t path, cudaStream_t stream)
         p.ldx = (int64_t(p.k) + 7) / 8 * 8;  // a single row's pitch is never stepped by
     if (p.n == 1 && !p.gated)
         p.ldw = ((int64_t(p.k) + 1) / 2 + 15) / 16 * 16;  // (plain: codes)
-    const bool few = few_ok(p), swap = swap_ok(p), pair = pair_ok(p, d);
-    if (path == GEMM_PATH_AUTO) {
-        if (few && (!swap || few_first(p)))
-            path = GEMM_PATH_SKINNY;
-        else
-            path = swap ? GEMM_PATH_TC05 : (pair ? GEMM_PATH_TC05_PAIR : GEMM_PATH_MMASYNC);
-    }
+    const bool few = few_ok(p), swap = swap_ok(p), any = path == GEMM_PATH_AUTO;
+    if (any && few && (!swap || few_first(p)))
+        path = GEMM_PATH_SKINNY;
+    else if (any)
+        path = swap ? GEMM_PATH_TC05 : GEMM_PATH_TC05_PAIR;
     if (path == GEMM_PATH_SKINNY && few)
-        return status_of(ffn_few_launch(p, d.num_sms, stream));
+        return status_of(ffn_few_launch(p, d.device, d.num_sms, stream));
     if (path == GEMM_PATH_TC05 && swap)
-        return status_of(ffn_swap_launch(p, d.num_sms, stream));
-    if (path == GEMM_PATH_TC05_PAIR && pair)
-        return status_of(gated_pair_launch(p, d.gated_pairs, stream));
+        return status_of(ffn_swap_launch(p, d.device, d.num_sms, stream));
+    if (path == GEMM_PATH_TC05_PAIR) {
+        int pairs = 0;
+        if (pair_ok(p) && gated_pairs(p.act, d.device, &pairs) != cudaSuccess)
+            return GEMM_ERR_LAUNCH;
+        if (pairs > 0)
+            return status_of(gated_pair_launch(p, pairs, stream));
+        if (any)
+            path = GEMM_PATH_MMASYNC;
+    }
     if (path == GEMM_PATH_MMASYNC)
         return status_of(ffn_any_launch(p, d.num_sms, stream));
     return GEMM_ERR_NOT_SUPPORTED;

@@ -456,12 +456,14 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS == 8 ? 3 : 1) ffn_few_kernel
 }
 
 template <bool BF16, bool W4, bool GATED, int NTOK, int WARPS, bool G128>
-cudaError_t run(const FfnParams& p, int num_sms, cudaStream_t stream, bool configure)
+cudaError_t run(const FfnParams& p, int device, int num_sms, cudaStream_t stream)
 {
     using C = Cfg<NTOK ? NTOK : 1, WARPS>;
     auto* kernel = ffn_few_kernel<BF16, W4, GATED, NTOK, WARPS, G128>;
-    if (configure)
-        return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
+    static SmemLimit limit;
+    const cudaError_t e = limit.allow(kernel, kMaxSmem, device);
+    if (e != cudaSuccess)
+        return e;
     const int vec_x = reinterpret_cast<uintptr_t>(p.x) % 16 == 0 && p.ldx % 8 == 0;
     const int vec_s = reinterpret_cast<uintptr_t>(p.scales) % 4 == 0 && p.lds % 2 == 0;  // pairs of scales
     const int vec_z = reinterpret_cast<uintptr_t>(p.zeros) % 2 == 0 && p.ldz % 2 == 0;
@@ -483,56 +485,40 @@ cudaError_t run(const FfnParams& p, int num_sms, cudaStream_t stream, bool confi
 }
 
 template <bool BF16, bool W4, bool GATED, bool G128>
-cudaError_t by_tokens(const FfnParams& p, int num_sms, cudaStream_t stream, bool configure)
+cudaError_t by_tokens(const FfnParams& p, int device, int num_sms, cudaStream_t stream)
 {
-    if (configure) {
-        cudaError_t e = run<BF16, W4, GATED, 0, 8, G128>(p, num_sms, stream, true);
-        if (e == cudaSuccess) e = run<BF16, W4, GATED, 1, 8, G128>(p, num_sms, stream, true);
-        if (e == cudaSuccess) e = run<BF16, W4, GATED, 1, 16, G128>(p, num_sms, stream, true);
-        if (e == cudaSuccess) e = run<BF16, W4, GATED, 2, 16, G128>(p, num_sms, stream, true);
-        return e;
-    }
     if (p.tokens > 8)
-        return run<BF16, W4, GATED, 2, 16, G128>(p, num_sms, stream, false);
+        return run<BF16, W4, GATED, 2, 16, G128>(p, device, num_sms, stream);
     // two CTAs of 8 warps have to fit
     if (2 * (Cfg<1, 8>::kRing + Cfg<1, 8>::kRed + x_bytes(p) + 1024) <= kMaxSmem + 1024)
-        return p.tokens == 1 ? run<BF16, W4, GATED, 0, 8, G128>(p, num_sms, stream, false)
-                             : run<BF16, W4, GATED, 1, 8, G128>(p, num_sms, stream, false);
-    return run<BF16, W4, GATED, 1, 16, G128>(p, num_sms, stream, false);
+        return p.tokens == 1 ? run<BF16, W4, GATED, 0, 8, G128>(p, device, num_sms, stream)
+                             : run<BF16, W4, GATED, 1, 8, G128>(p, device, num_sms, stream);
+    return run<BF16, W4, GATED, 1, 16, G128>(p, device, num_sms, stream);
 }
 
 template <bool BF16, bool W4, bool GATED>
-cudaError_t by_group(const FfnParams& p, int num_sms, cudaStream_t stream, bool configure)
+cudaError_t by_group(const FfnParams& p, int device, int num_sms, cudaStream_t stream)
 {
-    cudaError_t e = cudaSuccess;
     if constexpr (W4)
-        if (configure || p.group_shift == 7) e = by_tokens<BF16, W4, GATED, true>(p, num_sms, stream, configure);
-    if (e == cudaSuccess && (configure || p.group_shift != 7)) e = by_tokens<BF16, W4, GATED, false>(p, num_sms, stream, configure);
-    return e;
+        if (p.group_shift == 7)
+            return by_tokens<BF16, W4, GATED, true>(p, device, num_sms, stream);
+    return by_tokens<BF16, W4, GATED, false>(p, device, num_sms, stream);
 }
 
 template <bool BF16>
-cudaError_t by_kind(const FfnParams& p, int num_sms, cudaStream_t stream, bool configure)
+cudaError_t by_kind(const FfnParams& p, int device, int num_sms, cudaStream_t stream)
 {
-    cudaError_t e = cudaSuccess;
-    if (configure || (p.scales && !p.gated)) e = by_group<BF16, true, false>(p, num_sms, stream, configure);
-    if (e == cudaSuccess && (configure || (p.scales && p.gated))) e = by_group<BF16, true, true>(p, num_sms, stream, configure);
-    if (e == cudaSuccess && (configure || !p.scales)) e = by_group<BF16, false, true>(p, num_sms, stream, configure);
-    return e;
+    if (!p.scales)
+        return by_group<BF16, false, true>(p, device, num_sms, stream);
+    return p.gated ? by_group<BF16, true, true>(p, device, num_sms, stream)
+                   : by_group<BF16, true, false>(p, device, num_sms, stream);
 }
 
 }  // namespace
 
-cudaError_t ffn_few_configure()
+cudaError_t ffn_few_launch(const FfnParams& p, int device, int num_sms, cudaStream_t stream)
 {
-    const FfnParams p{};
-    const cudaError_t e = by_kind<true>(p, 0, nullptr, true);
-    return e == cudaSuccess ? by_kind<false>(p, 0, nullptr, true) : e;
-}
-
-cudaError_t ffn_few_launch(const FfnParams& p, int num_sms, cudaStream_t stream)
-{
-    return p.bf16 ? by_kind<true>(p, num_sms, stream, false) : by_kind<false>(p, num_sms, stream, false);
+    return p.bf16 ? by_kind<true>(p, device, num_sms, stream) : by_kind<false>(p, device, num_sms, stream);
 }
 
 }  // namespace gnt

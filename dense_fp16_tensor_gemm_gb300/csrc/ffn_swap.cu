@@ -1,4 +1,4 @@
-// ffn_swap.cu -- the products of ffn_swap.cuh: set-up, launch, and the gated forms for bf16
+// ffn_swap.cu -- the products of ffn_swap.cuh: launch, and the gated forms for bf16
 // and for 16-bit weights (the others are compiled apart, beside these).
 #include "ffn_swap.cuh"
 
@@ -6,41 +6,25 @@ namespace gnt {
 
 using namespace swp;
 
-cudaError_t ffn_swap_f16(int shift, int nt, const CUtensorMap* maps, const SwapParams* p, int grid, cudaStream_t stream);
-cudaError_t ffn_swap_plain(int shift, int nt, const CUtensorMap* maps, const SwapParams* p, int grid, cudaStream_t stream);
-cudaError_t ffn_swap_plain_f16(int shift, int nt, const CUtensorMap* maps, const SwapParams* p, int grid, cudaStream_t stream);
+cudaError_t ffn_swap_f16(int shift, int nt, const CUtensorMap* maps, const SwapParams& p, const Launch& l);
+cudaError_t ffn_swap_plain(int shift, int nt, const CUtensorMap* maps, const SwapParams& p, const Launch& l);
+cudaError_t ffn_swap_plain_f16(int shift, int nt, const CUtensorMap* maps, const SwapParams& p, const Launch& l);
 
 namespace {
 
 // shift 0: 16-bit weights (whose types differ in the instruction descriptor alone).
-cudaError_t by_kind(bool gated, int shift, bool bf16, int nt, const CUtensorMap* maps, const SwapParams* p, int grid, cudaStream_t stream)
+cudaError_t by_kind(bool gated, int shift, bool bf16, int nt, const CUtensorMap* maps, const SwapParams& p, const Launch& l)
 {
     if (shift == 0)
-        return by_tokens<false, true, true, 0>(nt, maps, p, grid, stream);
+        return by_tokens<false, true, true, 0>(nt, maps, p, l);
     if (!gated)
-        return bf16 ? ffn_swap_plain(shift, nt, maps, p, grid, stream) : ffn_swap_plain_f16(shift, nt, maps, p, grid, stream);
-    return bf16 ? by_group<true, true>(shift, nt, maps, p, grid, stream) : ffn_swap_f16(shift, nt, maps, p, grid, stream);
+        return bf16 ? ffn_swap_plain(shift, nt, maps, p, l) : ffn_swap_plain_f16(shift, nt, maps, p, l);
+    return bf16 ? by_group<true, true>(shift, nt, maps, p, l) : ffn_swap_f16(shift, nt, maps, p, l);
 }
 
 }  // namespace
 
-cudaError_t ffn_swap_configure()
-{
-    for (int nt : {32, 64, 128, 256})
-        for (int shift : {0, 5, 6, 7})
-            for (bool bf16 : {true, false}) {
-                if (shift == 0 && (!bf16 || nt > kSwapTokens))
-                    continue;
-                for (bool gated : {true, false}) {
-                    const cudaError_t e = by_kind(gated, shift, bf16, nt, nullptr, nullptr, 0, nullptr);
-                    if (e != cudaSuccess)
-                        return e;
-                }
-            }
-    return cudaSuccess;
-}
-
-cudaError_t ffn_swap_launch(const FfnParams& f, int num_sms, cudaStream_t stream)
+cudaError_t ffn_swap_launch(const FfnParams& f, int device, int num_sms, cudaStream_t stream)
 {
     const bool w4 = f.scales != nullptr;
     const int dtype = f.bf16 ? GEMM_DTYPE_BF16 : GEMM_DTYPE_F16;
@@ -74,7 +58,7 @@ cudaError_t ffn_swap_launch(const FfnParams& f, int num_sms, cudaStream_t stream
         p.whole = f.n % 16 == 0 ? (f.n + 63) / 64 * 64 : f.n;
     }
     const int grid = p.splits > 1 ? p.num_tiles * p.splits : std::min(p.num_tiles, num_sms);
-    return by_kind(f.gated, f.group_shift, f.bf16, nt, maps, &p, grid, stream);
+    return by_kind(f.gated, f.group_shift, f.bf16, nt, maps, p, Launch{device, grid, stream});
 }
 
 }  // namespace gnt

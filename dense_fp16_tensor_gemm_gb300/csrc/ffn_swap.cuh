@@ -713,50 +713,57 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
+struct Launch {
+    int device, grid;
+    cudaStream_t stream;
+};
+
 template <bool W4, bool BF16, bool GATED, int NT, int GS>
-cudaError_t run(const CUtensorMap* maps, const SwapParams* p, int grid, cudaStream_t stream)
+cudaError_t run(const CUtensorMap* maps, const SwapParams& p, const Launch& l)
 {
     auto* kernel = ffn_swap_kernel<W4, BF16, GATED, NT, GS>;
-    if (!p)
-        return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<W4, NT>::kSmem);
+    static SmemLimit limit;
+    const cudaError_t e = limit.allow(kernel, Cfg<W4, NT>::kSmem, l.device);
+    if (e != cudaSuccess)
+        return e;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = static_cast<unsigned>(p->splits);
+    attr[1].val.clusterDim.x = static_cast<unsigned>(p.splits);
     attr[1].val.clusterDim.y = 1;
     attr[1].val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(grid));
+    cfg.gridDim = dim3(static_cast<unsigned>(l.grid));
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = Cfg<W4, NT>::kSmem;
-    cfg.stream = stream;
+    cfg.stream = l.stream;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, kernel, maps[0], maps[1], maps[2], *p);
+    return cudaLaunchKernelEx(&cfg, kernel, maps[0], maps[1], maps[2], p);
 }
 
 template <bool W4, bool BF16, bool GATED, int GS>
-cudaError_t by_tokens(int nt, const CUtensorMap* maps, const SwapParams* p, int grid, cudaStream_t stream)
+cudaError_t by_tokens(int nt, const CUtensorMap* maps, const SwapParams& p, const Launch& l)
 {
     if (nt == 32)
-        return run<W4, BF16, GATED, 32, GS>(maps, p, grid, stream);
+        return run<W4, BF16, GATED, 32, GS>(maps, p, l);
     if constexpr (W4) {
         if (nt == 256)
-            return run<W4, BF16, GATED, 256, GS>(maps, p, grid, stream);
+            return run<W4, BF16, GATED, 256, GS>(maps, p, l);
         if (nt == 128)
-            return run<W4, BF16, GATED, 128, GS>(maps, p, grid, stream);
+            return run<W4, BF16, GATED, 128, GS>(maps, p, l);
     }
-    return run<W4, BF16, GATED, 64, GS>(maps, p, grid, stream);
+    return run<W4, BF16, GATED, 64, GS>(maps, p, l);
 }
 
 template <bool BF16, bool GATED>
-cudaError_t by_group(int shift, int nt, const CUtensorMap* maps, const SwapParams* p, int grid, cudaStream_t stream)
+cudaError_t by_group(int shift, int nt, const CUtensorMap* maps, const SwapParams& p, const Launch& l)
 {
     switch (shift) {
-    case 5: return by_tokens<true, BF16, GATED, 5>(nt, maps, p, grid, stream);
-    case 6: return by_tokens<true, BF16, GATED, 6>(nt, maps, p, grid, stream);
-    default: return by_tokens<true, BF16, GATED, 7>(nt, maps, p, grid, stream);
+    case 5: return by_tokens<true, BF16, GATED, 5>(nt, maps, p, l);
+    case 6: return by_tokens<true, BF16, GATED, 6>(nt, maps, p, l);
+    default: return by_tokens<true, BF16, GATED, 7>(nt, maps, p, l);
     }
 }
 

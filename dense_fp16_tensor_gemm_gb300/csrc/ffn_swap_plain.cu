@@ -3,9 +3,9 @@
 
 namespace gnt {
 
-cudaError_t ffn_swap_plain(int shift, int nt, const CUtensorMap* maps, const swp::SwapParams* p, int grid, cudaStream_t stream)
+cudaError_t ffn_swap_plain(int shift, int nt, const CUtensorMap* maps, const swp::SwapParams& p, const swp::Launch& l)
 {
-    return swp::by_group<true, false>(shift, nt, maps, p, grid, stream);
+    return swp::by_group<true, false>(shift, nt, maps, p, l);
 }
 
 }  // namespace gnt

@@ -346,32 +346,38 @@ cudaLaunchConfig_t config(int grid, cudaStream_t stream, cudaLaunchAttribute* at
     return cfg;
 }
 
+// Asked once per device, by the kernel's first launch there.
 template <int ACT>
-cudaError_t configure_act(int* max_pairs)
+cudaError_t resident(int device, int* pairs)
 {
-    cudaError_t e = cudaFuncSetAttribute(gated_pair_kernel<ACT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-    if (e != cudaSuccess)
-        return e;
-    cudaLaunchAttribute attr[2];
-    cudaLaunchConfig_t cfg = config(2, nullptr, attr);
-    int n = 0;
-    e = cudaOccupancyMaxActiveClusters(&n, gated_pair_kernel<ACT>, &cfg);
-    *max_pairs = std::min(*max_pairs, n);
-    return e;
+    static SmemLimit limit;
+    static std::atomic<int> known[64];  // 1 + their number
+    int n = known[device].load(std::memory_order_relaxed);
+    if (n == 0) {
+        cudaError_t e = limit.allow(gated_pair_kernel<ACT>, kSmem, device);
+        cudaLaunchAttribute attr[2];
+        cudaLaunchConfig_t cfg = config(2, nullptr, attr);
+        if (e == cudaSuccess) e = cudaOccupancyMaxActiveClusters(&n, gated_pair_kernel<ACT>, &cfg);
+        if (e != cudaSuccess)
+            return e;
+        known[device].store(++n, std::memory_order_relaxed);
+    }
+    *pairs = n - 1;
+    return cudaSuccess;
 }
 
 }  // namespace
 
-cudaError_t gated_pair_configure(int* max_pairs)
+cudaError_t gated_pairs(int act, int device, int* pairs)
 {
-    *max_pairs = 1 << 30;
-    cudaError_t e = configure_act<kActSilu>(max_pairs);
-    if (e == cudaSuccess) e = configure_act<kActGelu>(max_pairs);
-    if (e == cudaSuccess) e = configure_act<kActGeluTanh>(max_pairs);
-    return e;
+    switch (act) {
+    case kActSilu: return resident<kActSilu>(device, pairs);
+    case kActGelu: return resident<kActGelu>(device, pairs);
+    default: return resident<kActGeluTanh>(device, pairs);
+    }
 }
 
-cudaError_t gated_pair_launch(const FfnParams& f, int max_pairs, cudaStream_t stream)
+cudaError_t gated_pair_launch(const FfnParams& f, int pairs, cudaStream_t stream)
 {
     PairParams p{};
     const int dtype = f.bf16 ? GEMM_DTYPE_BF16 : GEMM_DTYPE_F16;
@@ -403,7 +409,7 @@ cudaError_t gated_pair_launch(const FfnParams& f, int max_pairs, cudaStream_t st
     p.wait_limit = f.wait_limit;
     p.fault = f.fault;
     cudaLaunchAttribute attr[2];
-    cudaLaunchConfig_t cfg = config(2 * std::min(p.num_tiles, max_pairs), stream, attr);
+    cudaLaunchConfig_t cfg = config(2 * std::min(p.num_tiles, pairs), stream, attr);
     switch (f.act) {
     case kActSilu: return cudaLaunchKernelEx(&cfg, gated_pair_kernel<kActSilu>, tmx, tmw, p);
     case kActGelu: return cudaLaunchKernelEx(&cfg, gated_pair_kernel<kActGelu>, tmx, tmw, p);
