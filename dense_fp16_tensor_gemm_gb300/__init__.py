@@ -1071,7 +1071,8 @@ def linear_w4(X, Q, S, Z=None, group=128, out=None, path=Path.AUTO, stream=None)
     include/gemm_nt.h); Y (tokens, out) has X's type, its rows start on 16-byte
     boundaries.  Rows of Q that do not (a contiguous Q whose width is no multiple of 16) are
     copied there by every call, unless a ``path`` is given: keep the Q that the quantiser
-    returns, whose rows do."""
+    returns, whose rows do.  ``path=Path.MMASYNC`` multiplies unrounded weights for any number
+    of tokens, slowly; ``Path.SKINNY`` for few."""
     if stream is not None:
         side = _elsewhere(stream)
         if side is not None:
@@ -1080,7 +1081,8 @@ def linear_w4(X, Q, S, Z=None, group=128, out=None, path=Path.AUTO, stream=None)
 
 
 def gated_linear_w4(X, Q13, S13, Z13=None, group=128, activation="silu", out=None, path=Path.AUTO, stream=None):
-    """:func:`gated_linear` with the 4-bit weights of :func:`quantize_w4` in W13's place."""
+    """:func:`gated_linear` with the 4-bit weights of :func:`quantize_w4` in W13's place;
+    roundings, copies and paths as in :func:`linear_w4`."""
     act = _act(activation)
     if stream is not None:
         side = _elsewhere(stream)

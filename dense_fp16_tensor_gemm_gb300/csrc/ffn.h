@@ -18,7 +18,8 @@ constexpr int kActSilu = 0, kActGelu = 1, kActGeluTanh = 2;
 // (silu), the normal distribution function (gelu), or the logistic function of
 // 2 sqrt(2/pi) (g + 0.044715 g^3) (gelu_tanh: (1 + tanh v)/2 is the logistic
 // function of 2v, which keeps its relative precision where 1 + tanh v cancels;
-// so does erfc on the normal one's lower tail).
+// so does erfc on the normal one's lower tail).  A quotient below 2^-126 is 0: silu of -88 is
+// -0, not -5e-37.
 struct ActP {
     float p, d;  // P and P'
 };

@@ -1,8 +1,8 @@
 // ffn_few.cu -- gated products, and plain and gated products with 4-bit weights,
 // for up to 16 tokens on the warp MMA: a stream of the weights.
 //
-// Bound by memory, and with 4-bit weights by the instructions that turn codes into
-// operands: every weight is read once and meets at most 16 tokens.  The weights are
+// Bound by memory, and with 4-bit weights by the latency of its loads: every weight is read once
+// and meets at most 16 tokens.  The weights are
 // the MMA's A operand (16 rows by 16 of K), the tokens its 8 columns.  A CTA walks
 // over tiles of 16 rows (of a gated product 8 of the gate and the same 8 of the up
 // projection, so that a thread ends with g and u of its outputs); its warps take turns
@@ -24,7 +24,9 @@
 // One token x 4096 x 8192 gated: 23.7 us in bf16 (134 MB, 5.7 TB/s), 13.4 in 4 bits (35 MB);
 // x 4096 x 4096 in 4 bits 6.4, x 8192 x 16384 22.0.  About 4 us of each are launch, first loads
 // and the last sums.  In 4 bits a step of 4096 codes takes some 400 instructions, 112 of them the
-// codes' shifts and logical operations, on the pipe that is busiest.  Rings of two steps
+// codes' shifts and logical operations, on the ALU, the busiest pipe at 45 to 49 % of active cycles
+// (issue slots 54 to 57 %); of the 10 cycles between two instructions of a warp 3 to 4 go to waiting
+// for loads.  Rings of two steps
 // (4-bit 12.8 and 21.6, but 4 tokens 9.0 for 8.3) and two CTAs an SM (5.4 for 4096 x 4096, 25 for
 // 8192 x 16384) were measured beside three and three.
 #include <algorithm>

@@ -23,11 +23,13 @@
 //
 // 16-bit weights: bound by their bytes (64 tokens x 4096 x 8192 gated 26.0 us, x 2048 x 8192
 // 15.0, 6 TB/s between the two and 4 us that every call takes).  4-bit ones, up to 128
-// tokens: by their conversion, 350 cycles for 128 x 64 of them where the bytes take 175 (64 x
-// 16384 x 8192 27.9 us, x 4096 x 4096 12.0; 25.4 without the conversion's arithmetic, 20.5 without
-// the scales either; half the tokens' loads change nothing, so pairs of CTAs would not
+// tokens: by no one thing (64 x 16384 x 8192 27.9 us, x 4096 x 4096 12.0; 25.4 without the
+// conversion's arithmetic, 20.5 without the scales either, of which 6.6 are launch and ends and
+// 13.9 the codes, 5.0 TB/s on 128 of 152 SMs; there the ALU is busy 71 % of the time, issue
+// slots 78 %.  Half the tokens' loads change nothing, so pairs of CTAs would not
 // either).  More tokens: by the tensor cores and the last round of tiles (2048 x 8192 x 4096
-// 87 us, four rounds of 152 tiles for 3.4).
+// in bf16, groups of 128, no zero points, 87 us, four rounds of 152 tiles for 3.4; in fp16, groups
+// of 64 and zero points, 102).
 //
 // Roles (768 threads): warp 0 TMA of the weights, warp 1 MMA issue, warp 2 TMA of
 // the tokens, warp 3 TMEM allocation, warps 4-19 conversion, warps 20-23 epilogue.
