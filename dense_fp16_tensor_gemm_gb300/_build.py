@@ -96,8 +96,9 @@ def _calls_key():
 
 def _calls_stale():
     """Whether the extension is missing or for another torch or Python than this one's.  One
-    that did not compile is not tried again until those or the sources change."""
-    if _calls_command(CALLS) is None:
+    that did not compile is not tried again until those or the sources change; nothing is
+    where the folder cannot be written."""
+    if _calls_command(CALLS) is None or not os.access(OUT_DIR, os.W_OK):
         return False
     try:
         with open(CALLS_FOR) as f:

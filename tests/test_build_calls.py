@@ -65,6 +65,13 @@ def test_a_machine_without_what_it_needs_builds_nothing(place):
     assert not made[1:] and not os.path.exists(_build.CALLS_FOR)
 
 
+def test_a_folder_that_cannot_be_written_is_left_alone(place, monkeypatch):
+    use, made = place
+    use("cp", os.devnull, "OUT")
+    monkeypatch.setattr(_build.os, "access", lambda path, mode: path != _build.OUT_DIR)
+    assert _build.build() == _build.LIB and not made
+
+
 def test_no_toolkit_no_extension(monkeypatch):
     def missing():
         raise RuntimeError("nvcc not found")
