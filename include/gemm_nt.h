@@ -430,9 +430,9 @@ typedef enum gemm_act {
  *   GEMM_PATH_TC05_PAIR  tcgen05 on CTA pairs, 256 tokens x 128 columns of H
  *   GEMM_PATH_MMASYNC    warp MMA, any layout
  * SKINNY needs W13 on 16-byte boundaries (base and ldw), TC05 and TC05_PAIR X (base and
- * ldx) too; a path that cannot take the arguments, and the other paths, are
- * GEMM_ERR_NOT_SUPPORTED.  AUTO takes one that can, by the tokens and the weights' bytes;
- * paths differ in the order of their sums.
+ * ldx) too, a matrix of a single row its base alone; a path that cannot take the
+ * arguments, and the other paths, are GEMM_ERR_NOT_SUPPORTED.  AUTO takes one that can, by
+ * the tokens and the weights' bytes; paths differ in the order of their sums.
  *
  * tokens or inner 0: nothing to do; hidden 0: zeros; hidden above 2^30 or inner above
  * 2^30 - 1: GEMM_ERR_INVALID_VALUE.  Any pitch and alignment is

@@ -51,7 +51,8 @@ print("same")
 
 
 def child(code, *args):
-    r = subprocess.run([sys.executable, "-c", code, *args], cwd=ROOT, capture_output=True, text=True, timeout=300)
+    r = subprocess.run([sys.executable, "-c", code, *args], cwd=ROOT, capture_output=True, text=True, timeout=300,
+                       env={**os.environ, "CUDA_MODULE_LOADING": "LAZY"})
     assert r.returncode == 0, r.stderr[-2000:]
     return r.stdout.split()[-1]
 
